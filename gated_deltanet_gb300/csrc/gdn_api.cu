@@ -8,7 +8,7 @@
 #include <utility>
 #include <vector>
 
-#include "gdn_internal.cuh"
+#include "gdn_layer.cuh"
 
 using namespace gdn;
 
@@ -436,6 +436,22 @@ gdn_status managed_ws(size_t need, cudaStream_t stream, void **out, size_t *out_
 }
 
 }  // namespace
+
+gdn_status gdn::managed_workspace(size_t need, cudaStream_t stream, void **out, size_t *out_bytes)
+{
+    return managed_ws(need, stream, out, out_bytes);
+}
+
+bool gdn::managed_workspace_holds(size_t need, cudaStream_t stream)
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    std::lock_guard<std::mutex> lock(g_mu);
+    const auto it = g_ws.find({dev, stream});
+    return it != g_ws.end() && it->second.ptr && it->second.bytes >= need;
+}
+
+int gdn::device_sm_count() { return current_sm_count(); }
 
 gdn_status gdn::check_call(const gdn_shape *s, const void *q, const void *k, const void *v, const float *g,
                            const float *beta, float scale, const int64_t *cu, int chunk_size, const void *o,

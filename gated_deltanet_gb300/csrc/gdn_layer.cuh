@@ -1,0 +1,162 @@
+// Internal declarations of the decoder-block operators (norm, linear, gated linear unit): the
+// argument blocks of their kernels and the arithmetic that every engine's epilogue shares.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "gdn_internal.cuh"
+
+namespace gdn {
+
+// Activations.  `PRECISE` (fp32 outputs) takes the full-accuracy exponential and division; otherwise the
+// result is rounded to bf16 (relative step 2^-8) and the fast ones (relative error below 2^-20 for the
+// arguments where the result is not itself lost in that rounding) are enough.
+template <bool PRECISE>
+__device__ __forceinline__ float logistic(float z)
+{
+    if (PRECISE) return 1.f / (1.f + expf(-z));
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-z)));
+    return r;
+}
+constexpr float kGeluA = 1.5957691216057308f;            // 2 sqrt(2 / pi): 0.5 (1 + tanh u) = logistic(2 u)
+constexpr float kGeluB = 1.5957691216057308f * 0.044715f;
+
+template <bool PRECISE>
+__device__ __forceinline__ float act_value(int act, float z)
+{
+    switch (act) {
+    case GDN_ACT_SILU: return z * logistic<PRECISE>(z);
+    case GDN_ACT_GELU: return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+    case GDN_ACT_GELU_TANH: return z * logistic<PRECISE>(z * (kGeluA + kGeluB * z * z));
+    case GDN_ACT_RELU: return z < 0.f ? 0.f : z;  // (keeps a NaN)
+    case GDN_ACT_SIGMOID: return logistic<PRECISE>(z);
+    default: return z;
+    }
+}
+// value and derivative
+template <bool PRECISE>
+__device__ __forceinline__ void act_both(int act, float z, float &v, float &d)
+{
+    switch (act) {
+    case GDN_ACT_SILU: {
+        const float p = logistic<PRECISE>(z);
+        v = z * p;
+        d = p * (1.f + z * (1.f - p));
+        return;
+    }
+    case GDN_ACT_GELU: {
+        const float c = 0.5f * (1.f + erff(z * 0.70710678118654752f));
+        const float e = PRECISE ? expf(-0.5f * z * z) : __expf(-0.5f * z * z);
+        v = z * c;
+        d = c + z * e * 0.3989422804014327f;  // 1 / sqrt(2 pi)
+        return;
+    }
+    case GDN_ACT_GELU_TANH: {
+        const float z2 = z * z, p = logistic<PRECISE>(z * (kGeluA + kGeluB * z2));
+        v = z * p;
+        d = p + v * (1.f - p) * (kGeluA + 3.f * kGeluB * z2);
+        return;
+    }
+    case GDN_ACT_RELU:
+        v = z < 0.f ? 0.f : z;
+        d = z > 0.f ? 1.f : 0.f;
+        return;
+    case GDN_ACT_SIGMOID: {
+        const float p = logistic<PRECISE>(z);
+        v = p;
+        d = p * (1.f - p);
+        return;
+    }
+    default: v = z; d = 1.f;
+    }
+}
+
+// What a product's epilogue does with z = sum_k A(m, k) B(n, k).
+enum Epi : int {
+    kEpiLinear = 0,    // out = act(sx_m sw_n z + bias_n) + extra_mn
+    kEpiGated = 1,     // out = act(gate) up, gate / up from rows n and F + n of B
+    kEpiDact = 2,      // out = extra_mn act'(z + bias_n); column sums of it per 32 rows into colpart
+    kEpiGatedBwd = 3,  // out[m, n] = extra up act'(gate), out[m, F + n] = extra act(gate); out2 = act(gate) up
+};
+
+// One product with its epilogue.  A(m, k) is at a[m lda + k], or a[k lda + m] when a_t; B(n, k) at
+// b[n ldb + k], or b[k ldb + n] when b_t.  Gated modes: B has 2 N rows, gate rows first.
+struct GemmArgs {
+    int64_t M, N, K;
+    gdn_dtype in, out_dt;
+    const void *a, *b;
+    int64_t lda, ldb;
+    int a_t, b_t;
+    const float *x_scale, *w_scale;  // per row of A and of B, nullable (1)
+    const float *bias;               // per column, nullable
+    gdn_activation act;
+    const void *extra;               // residual (nullable), dy or dh: [M][ld_extra], the output's type
+    int64_t ld_extra;
+    void *out;
+    int64_t ldo;
+    void *out2;                      // kEpiGatedBwd: the recomputed output [M][ldo2], nullable
+    int64_t ldo2;
+    float *colpart;                  // kEpiDact: [ceil(M / 32)][N], nullable
+};
+
+cudaError_t launch_gemm_simt(const GemmArgs &g, Epi epi, cudaStream_t st);
+
+// out[n] = sum over `parts` rows of part[.][N] (a fixed order: the same sum every time)
+cudaError_t launch_colsum_finish(const float *part, int64_t parts, int64_t N, float *out, cudaStream_t st);
+// part[i][n] = sum of rows 32 i .. 32 i + 31 of x (M x N): `parts` of them must be ceil(M / 32)
+cudaError_t launch_colsum_rows(const void *x, gdn_dtype dt, int64_t M, int64_t N, int64_t ld, float *part, cudaStream_t st);
+
+struct NormArgs {
+    int64_t M;
+    int D;
+    gdn_dtype dt, w_dt, out_dt;
+    const void *x, *r;       // r nullable
+    int64_t ldx, ldr;
+    const void *w;           // [D], nullable (1)
+    float eps;
+    void *y;                 // [M][D], out_dt
+    float *scale;            // e4m3: [M]
+    void *h;                 // [M][D], nullable
+    int normalise;           // 0: y = x (the quantiser alone)
+};
+cudaError_t launch_norm(const NormArgs &a, cudaStream_t st);
+
+struct NormBwdArgs {
+    int64_t M;
+    int D;
+    gdn_dtype dt, w_dt;
+    const void *dy, *h, *dh;  // dh nullable
+    int64_t ld_dy, ld_h, ld_dh;
+    const void *w;            // nullable
+    float eps;
+    void *dx;                 // [M][D]
+    float *dw;                // [D], nullable
+    float *part;              // workspace, norm_bwd_parts() rows of D
+    float *rstd;              // workspace [M] (wide rows only)
+};
+int norm_bwd_parts(int64_t M, int D, gdn_dtype dt, int num_sms);  // rows of partial sums the launch writes
+bool norm_bwd_wide(int D);  // rows too wide for one block's registers: the two-kernel form
+cudaError_t launch_norm_bwd(const NormBwdArgs &a, int num_sms, cudaStream_t st);
+
+// The library-managed workspace of (device, stream), grown to `need` bytes; and whether it holds them already.
+gdn_status managed_workspace(size_t need, cudaStream_t stream, void **out, size_t *out_bytes);
+bool managed_workspace_holds(size_t need, cudaStream_t stream);
+int device_sm_count();
+
+// typed loads and stores
+template <typename T> __device__ __forceinline__ float to_f(T v);
+template <> __device__ __forceinline__ float to_f<float>(float v) { return v; }
+template <> __device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <> __device__ __forceinline__ float to_f<__nv_fp8_e4m3>(__nv_fp8_e4m3 v) { return (float)v; }
+template <typename T> __device__ __forceinline__ T from_f(float v);
+template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <> __device__ __forceinline__ __nv_fp8_e4m3 from_f<__nv_fp8_e4m3>(float v)
+{
+    __nv_fp8_e4m3 q;
+    q.__x = __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
+    return q;
+}
+
+}  // namespace gdn

@@ -1,0 +1,320 @@
+// C-ABI layer of the decoder-block operators: argument checks, workspace layout and the launches of
+// each call.
+#include <cmath>
+
+#include "gdn_layer.cuh"
+
+using namespace gdn;
+
+namespace {
+
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+size_t esize(gdn_dtype t) { return t == GDN_F32 ? 4 : t == GDN_BF16 ? 2 : 1; }
+
+// caller's workspace, or the library's where none is given
+gdn_status take_workspace(size_t need, void *ws, size_t bytes, cudaStream_t st, char **out)
+{
+    *out = nullptr;
+    if (need == 0) return GDN_OK;
+    if (ws) {
+        if (bytes < need) return GDN_ERR_WORKSPACE;
+        if ((uintptr_t)ws & 255) return GDN_ERR_INVALID;
+        *out = (char *)ws;
+        return GDN_OK;
+    }
+    need += 256;  // past the status word of the library-managed workspace
+    if (!managed_workspace_holds(need, st)) {
+        cudaStreamCaptureStatus cs;
+        if (cudaStreamIsCapturing(st, &cs) != cudaSuccess) return GDN_ERR_CUDA;
+        if (cs != cudaStreamCaptureStatusNone) return GDN_ERR_NOMEM;
+    }
+    void *p = nullptr;
+    size_t got = 0;
+    const gdn_status s = managed_workspace(need, st, &p, &got);
+    if (s == GDN_OK) *out = (char *)p + 256;
+    return s;
+}
+
+bool real(gdn_dtype t) { return t == GDN_F32 || t == GDN_BF16; }
+bool on_element(const void *p, gdn_dtype t) { return ((uintptr_t)p & (esize(t) - 1)) == 0; }
+
+// ---------------------------------------------------------------- norm
+gdn_status check_norm(const gdn_norm_args *a)
+{
+    if (!a || a->rows < 0 || a->width < 1) return GDN_ERR_INVALID;
+    if (!real(a->dtype) || !real(a->w_dtype)) return GDN_ERR_INVALID;
+    if (!(a->eps >= 0.f) || std::isinf(a->eps)) return GDN_ERR_INVALID;
+    if (a->rows > 0 && !a->x) return GDN_ERR_INVALID;
+    if (a->rows > 1 && a->ldx < a->width) return GDN_ERR_INVALID;
+    if (!on_element(a->x, a->dtype) || !on_element(a->weight, a->w_dtype)) return GDN_ERR_INVALID;
+    return GDN_OK;
+}
+
+gdn_status run_norm(const gdn_norm_args *a, bool normalise, cudaStream_t st)
+{
+    gdn_status s = check_norm(a);
+    if (s != GDN_OK) return s;
+    if (a->out_dtype != a->dtype && a->out_dtype != GDN_E4M3) return GDN_ERR_INVALID;
+    if (a->rows == 0) return GDN_OK;
+    if (!a->y || (a->out_dtype == GDN_E4M3 && !a->scale)) return GDN_ERR_INVALID;
+    if (!on_element(a->residual, a->dtype) || !on_element(a->y, a->out_dtype) || !on_element(a->h, a->dtype) ||
+        ((uintptr_t)a->scale & 3))
+        return GDN_ERR_INVALID;
+    NormArgs n{};
+    n.M = a->rows; n.D = a->width;
+    n.dt = a->dtype; n.w_dt = a->w_dtype; n.out_dt = a->out_dtype;
+    n.x = a->x; n.ldx = a->ldx; n.eps = a->eps;
+    n.y = a->y; n.scale = a->scale;
+    n.normalise = normalise;
+    if (normalise) {
+        if (a->residual && a->rows > 1 && a->ld_residual < a->width) return GDN_ERR_INVALID;
+        n.r = a->residual; n.ldr = a->ld_residual;
+        n.w = a->weight;
+        n.h = a->h;
+    }
+    return launch_norm(n, st) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------- products
+struct Carve {  // offsets into a workspace
+    size_t at = 0;
+    size_t take(size_t bytes)
+    {
+        const size_t o = at;
+        at = up256(at + bytes);
+        return o;
+    }
+};
+
+// A product as it will be launched: its workspace follows `base`
+cudaError_t launch_product(const GemmArgs &g, Epi epi, cudaStream_t st) { return launch_gemm_simt(g, epi, st); }
+
+gdn_status check_linear(const gdn_linear_args *a, bool gated, bool backward)
+{
+    if (!a || a->rows < 0 || a->out_features < 1 || a->in_features < 1) return GDN_ERR_INVALID;
+    if (gated && a->out_features > (1 << 30)) return GDN_ERR_INVALID;
+    if (a->dtype != GDN_F32 && a->dtype != GDN_BF16 && a->dtype != GDN_E4M3) return GDN_ERR_INVALID;
+    if (a->act < GDN_ACT_NONE || a->act > GDN_ACT_SIGMOID) return GDN_ERR_INVALID;
+    if (backward && a->dtype == GDN_E4M3) return GDN_ERR_UNSUPPORTED;
+    const gdn_dtype plain_out = a->dtype == GDN_F32 ? GDN_F32 : GDN_BF16;
+    if (!real(a->out_dtype)) return GDN_ERR_INVALID;
+    if (a->out_dtype != plain_out && (gated || backward || a->dtype == GDN_F32)) return GDN_ERR_UNSUPPORTED;
+    if ((a->x_scale != nullptr) != (a->w_scale != nullptr)) return GDN_ERR_INVALID;
+    if (a->x_scale && a->dtype != GDN_E4M3) return GDN_ERR_INVALID;
+    if (gated && (a->bias || a->residual || a->dbias)) return GDN_ERR_INVALID;
+    const int64_t K = a->in_features, N = a->out_features;
+    if ((a->rows > 1 && a->ldx < K) || a->ldw < K) return GDN_ERR_INVALID;
+    if (!a->w || (a->rows > 0 && !a->x)) return GDN_ERR_INVALID;
+    if (!on_element(a->x, a->dtype) || !on_element(a->w, a->dtype) || ((uintptr_t)a->bias & 3) ||
+        ((uintptr_t)a->x_scale & 3) || ((uintptr_t)a->w_scale & 3))
+        return GDN_ERR_INVALID;
+    if (backward) {
+        if (a->rows > 0 && !a->dy) return GDN_ERR_INVALID;
+        if (a->rows > 1 && a->ld_dy < N) return GDN_ERR_INVALID;
+        if (!on_element(a->dy, a->dtype) || !on_element(a->dx, a->dtype) || !on_element(a->dw, a->dtype) ||
+            ((uintptr_t)a->dbias & 3))
+            return GDN_ERR_INVALID;
+        if (gated && a->y && (!on_element(a->y, a->dtype) || (a->rows > 1 && a->ldy < N))) return GDN_ERR_INVALID;
+    } else {
+        if (a->rows > 0 && !a->y) return GDN_ERR_INVALID;
+        if (a->rows > 1 && a->ldy < N) return GDN_ERR_INVALID;
+        if (a->residual && a->rows > 1 && a->ld_residual < N) return GDN_ERR_INVALID;
+        if (!on_element(a->y, a->out_dtype) || !on_element(a->residual, a->out_dtype)) return GDN_ERR_INVALID;
+    }
+    return GDN_OK;
+}
+
+GemmArgs forward_product(const gdn_linear_args *a)
+{
+    GemmArgs g{};
+    g.M = a->rows; g.N = a->out_features; g.K = a->in_features;
+    g.in = a->dtype; g.out_dt = a->out_dtype;
+    g.a = a->x; g.lda = a->ldx;
+    g.b = a->w; g.ldb = a->ldw;
+    g.x_scale = a->x_scale; g.w_scale = a->w_scale;
+    g.bias = a->bias;
+    g.act = a->act;
+    return g;
+}
+
+// The backward calls' own workspace: dz (rows padded to 16 bytes) and the column sums of groups of 32 rows
+struct BwdPlan {
+    int64_t dz_cols, dz_ld, parts;
+    size_t off_dz, off_part, bytes;
+    bool own_dz;
+};
+BwdPlan plan_bwd(const gdn_linear_args *a, bool gated)
+{
+    BwdPlan p{};
+    p.dz_cols = gated ? 2 * (int64_t)a->out_features : a->out_features;
+    const int64_t q = 16 / (int64_t)esize(a->dtype);
+    p.own_dz = gated || a->act != GDN_ACT_NONE;
+    p.dz_ld = p.own_dz ? (p.dz_cols + q - 1) / q * q : a->ld_dy;
+    p.parts = (a->rows + 31) / 32;
+    Carve c;
+    p.off_dz = c.take(p.own_dz ? (size_t)a->rows * p.dz_ld * esize(a->dtype) : 0);
+    p.off_part = c.take(a->dbias ? (size_t)p.parts * a->out_features * sizeof(float) : 0);
+    p.bytes = c.at;
+    return p;
+}
+
+gdn_status run_bwd(const gdn_linear_args *a, bool gated, void *ws, size_t ws_bytes, cudaStream_t st)
+{
+    gdn_status s = check_linear(a, gated, true);
+    if (s != GDN_OK) return s;
+    const int64_t M = a->rows, N = a->out_features, K = a->in_features;
+    const BwdPlan p = plan_bwd(a, gated);
+    if (M == 0) {
+        if (a->dw && cudaMemsetAsync(a->dw, 0, (size_t)p.dz_cols * K * esize(a->dtype), st) != cudaSuccess)
+            return GDN_ERR_CUDA;
+        if (a->dbias && cudaMemsetAsync(a->dbias, 0, (size_t)N * sizeof(float), st) != cudaSuccess) return GDN_ERR_CUDA;
+        return GDN_OK;
+    }
+    char *base = nullptr;
+    if ((s = take_workspace(p.bytes, ws, ws_bytes, st, &base)) != GDN_OK) return s;
+    const void *dz = a->dy;
+    float *part = a->dbias ? (float *)(base + p.off_part) : nullptr;
+    if (p.own_dz) {
+        GemmArgs g = forward_product(a);
+        g.extra = a->dy; g.ld_extra = a->ld_dy;
+        g.out = base + p.off_dz; g.ldo = p.dz_ld;
+        g.out2 = gated ? a->y : nullptr;
+        g.ldo2 = a->ldy;
+        g.colpart = part;
+        dz = g.out;
+        if (launch_product(g, gated ? kEpiGatedBwd : kEpiDact, st) != cudaSuccess) return GDN_ERR_CUDA;
+    } else if (part && launch_colsum_rows(a->dy, a->dtype, M, N, a->ld_dy, part, st) != cudaSuccess) {
+        return GDN_ERR_CUDA;
+    }
+    if (part && launch_colsum_finish(part, p.parts, N, a->dbias, st) != cudaSuccess) return GDN_ERR_CUDA;
+    GemmArgs g{};
+    g.in = a->dtype; g.out_dt = a->dtype;
+    g.a = dz; g.lda = p.dz_ld;
+    g.act = GDN_ACT_NONE;
+    g.b_t = 1;
+    if (a->dx) {  // dx[m][k] = sum_n dz[m][n] w[n][k]
+        GemmArgs d = g;
+        d.M = M; d.N = K; d.K = p.dz_cols;
+        d.b = a->w; d.ldb = a->ldw;
+        d.out = a->dx; d.ldo = K;
+        if (launch_product(d, kEpiLinear, st) != cudaSuccess) return GDN_ERR_CUDA;
+    }
+    if (a->dw) {  // dw[n][k] = sum_m dz[m][n] x[m][k]
+        GemmArgs d = g;
+        d.M = p.dz_cols; d.N = K; d.K = M;
+        d.a_t = 1;
+        d.b = a->x; d.ldb = a->ldx;
+        d.out = a->dw; d.ldo = K;
+        if (launch_product(d, kEpiLinear, st) != cudaSuccess) return GDN_ERR_CUDA;
+    }
+    return GDN_OK;
+}
+
+gdn_status run_fwd(const gdn_linear_args *a, bool gated, void *ws, size_t ws_bytes, cudaStream_t st)
+{
+    gdn_status s = check_linear(a, gated, false);
+    if (s != GDN_OK) return s;
+    if (a->rows == 0) return GDN_OK;
+    GemmArgs g = forward_product(a);
+    g.extra = a->residual; g.ld_extra = a->ld_residual;
+    g.out = a->y; g.ldo = a->ldy;
+    (void)ws; (void)ws_bytes;
+    return launch_product(g, gated ? kEpiGated : kEpiLinear, st) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+gdn_status gdn_rms_norm(const gdn_norm_args *a, gdn_stream_t stream) { return run_norm(a, true, (cudaStream_t)stream); }
+
+gdn_status gdn_quantize_rows(const gdn_norm_args *a, gdn_stream_t stream)
+{
+    if (!a || a->out_dtype != GDN_E4M3) return GDN_ERR_INVALID;
+    return run_norm(a, false, (cudaStream_t)stream);
+}
+
+size_t gdn_rms_norm_bwd_workspace_size(const gdn_norm_args *a)
+{
+    if (check_norm(a) != GDN_OK || a->rows == 0 || !a->dweight) return 0;
+    Carve c;
+    c.take((size_t)norm_bwd_parts(a->rows, a->width, a->dtype, device_sm_count()) * a->width * sizeof(float));
+    if (norm_bwd_wide(a->width)) c.take((size_t)a->rows * sizeof(float));
+    return c.at;
+}
+
+gdn_status gdn_rms_norm_bwd(const gdn_norm_args *a, void *workspace, size_t ws_bytes, gdn_stream_t stream)
+{
+    cudaStream_t st = (cudaStream_t)stream;
+    gdn_status s = check_norm(a);
+    if (s != GDN_OK) return s;
+    if (a->rows > 0 && (!a->dy || !a->dx)) return GDN_ERR_INVALID;
+    if (a->rows > 1 && (a->ld_dy < a->width || (a->dh && a->ld_dh < a->width))) return GDN_ERR_INVALID;
+    if (!on_element(a->dy, a->dtype) || !on_element(a->dh, a->dtype) || !on_element(a->dx, a->dtype) ||
+        ((uintptr_t)a->dweight & 3))
+        return GDN_ERR_INVALID;
+    char *base = nullptr;
+    if ((s = take_workspace(gdn_rms_norm_bwd_workspace_size(a), workspace, ws_bytes, st, &base)) != GDN_OK) return s;
+    const int sms = device_sm_count();
+    NormBwdArgs n{};
+    n.M = a->rows; n.D = a->width;
+    n.dt = a->dtype; n.w_dt = a->w_dtype;
+    n.dy = a->dy; n.ld_dy = a->ld_dy;
+    n.h = a->x; n.ld_h = a->ldx;
+    n.dh = a->dh; n.ld_dh = a->ld_dh;
+    n.w = a->weight; n.eps = a->eps;
+    n.dx = a->dx; n.dw = a->dweight;
+    if (base) {
+        n.part = (float *)base;
+        if (norm_bwd_wide(a->width))
+            n.rstd = (float *)(base + up256((size_t)norm_bwd_parts(a->rows, a->width, a->dtype, sms) * a->width * sizeof(float)));
+    }
+    return launch_norm_bwd(n, sms, st) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+size_t gdn_linear_workspace_size(const gdn_linear_args *a)
+{
+    return check_linear(a, false, false) == GDN_OK ? 0 : 0;
+}
+
+gdn_status gdn_linear(const gdn_linear_args *a, void *workspace, size_t ws_bytes, gdn_stream_t stream)
+{
+    return run_fwd(a, false, workspace, ws_bytes, (cudaStream_t)stream);
+}
+
+size_t gdn_linear_bwd_workspace_size(const gdn_linear_args *a)
+{
+    return check_linear(a, false, true) == GDN_OK ? plan_bwd(a, false).bytes : 0;
+}
+
+gdn_status gdn_linear_bwd(const gdn_linear_args *a, void *workspace, size_t ws_bytes, gdn_stream_t stream)
+{
+    return run_bwd(a, false, workspace, ws_bytes, (cudaStream_t)stream);
+}
+
+size_t gdn_gated_linear_workspace_size(const gdn_linear_args *a)
+{
+    return check_linear(a, true, false) == GDN_OK ? 0 : 0;
+}
+
+gdn_status gdn_gated_linear(const gdn_linear_args *a, void *workspace, size_t ws_bytes, gdn_stream_t stream)
+{
+    return run_fwd(a, true, workspace, ws_bytes, (cudaStream_t)stream);
+}
+
+size_t gdn_gated_linear_bwd_workspace_size(const gdn_linear_args *a)
+{
+    return check_linear(a, true, true) == GDN_OK ? plan_bwd(a, true).bytes : 0;
+}
+
+gdn_status gdn_gated_linear_bwd(const gdn_linear_args *a, void *workspace, size_t ws_bytes, gdn_stream_t stream)
+{
+    return run_bwd(a, true, workspace, ws_bytes, (cudaStream_t)stream);
+}
+
+gdn_status gdn_read_layer_status(gdn_stream_t stream)
+{
+    return cudaStreamSynchronize((cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,496 @@
+// Root-mean-square norm of rows with the residual's addition, in bf16 / fp32 or e4m3 with a scale per
+// row, and its gradients:
+//
+//   h = x + r;   n = sqrt(mean(h^2) + eps);   y = w h / n
+//   e4m3:  s = max(max|y| / 448, 2^-126),  q = y / s
+//   dx = dh + (w dy - h mean(w dy h) / n^2) / n,   dw = sum over rows of dy h / n
+//
+// Bound: HBM.  Each input is read once and each output written once: a row stays in the registers of the
+// threads that share it (at most 16 elements a thread) while its sums meet, by shuffles and, for rows
+// shared by several warps, one exchange through shared memory.  max|y| is taken as max|w h| / n, so that
+// both statistics of a quantised row meet in the same exchange.  A block walks rows a grid apart and
+// loads its next row before it works on this one; the weights stay in registers.
+#include "gdn_layer.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kRowElems = 16;        // elements of a row per thread, at most
+constexpr int kRowThreads = 512;     // threads of a block, at most
+constexpr int kWide = kRowElems * kRowThreads;  // wider rows take the looping kernels
+constexpr float kE4m3Max = 448.f, kScaleMin = 1.17549435e-38f;  // 2^-126: the smallest normal scale
+
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// VEC elements (16 bytes, or one element) as they are in memory
+template <typename T, int VEC> struct Raw;
+template <> struct Raw<__nv_bfloat16, 8> {
+    uint4 v;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { v = *(const uint4 *)p; }
+    __device__ __forceinline__ void to(float *f) const
+    {
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(u[i] << 16);
+            f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        }
+    }
+};
+template <> struct Raw<float, 4> {
+    float4 v;
+    __device__ __forceinline__ void load(const float *p) { v = *(const float4 *)p; }
+    __device__ __forceinline__ void to(float *f) const { f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w; }
+};
+template <typename T> struct Raw<T, 1> {
+    T v;
+    __device__ __forceinline__ void load(const T *p) { v = *p; }
+    __device__ __forceinline__ void to(float *f) const { f[0] = to_f(v); }
+};
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *(const uint32_t *)&p;
+}
+__device__ __forceinline__ uint32_t pack4_e4m3(const float *f)
+{
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[0], f[1]), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[2], f[3]), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+}
+template <int VEC> __device__ __forceinline__ void put(__nv_bfloat16 *p, const float *f)
+{
+    if constexpr (VEC == 8) *(uint4 *)p = make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+    else *p = __float2bfloat16_rn(f[0]);
+}
+template <int VEC> __device__ __forceinline__ void put(float *p, const float *f)
+{
+    if constexpr (VEC == 4) *(float4 *)p = make_float4(f[0], f[1], f[2], f[3]);
+    else *p = f[0];
+}
+template <int VEC> __device__ __forceinline__ void put(__nv_fp8_e4m3 *p, const float *f)
+{
+    if constexpr (VEC == 8) *(uint2 *)p = make_uint2(pack4_e4m3(f), pack4_e4m3(f + 4));
+    else if constexpr (VEC == 4) *(uint32_t *)p = pack4_e4m3(f);
+    else *p = from_f<__nv_fp8_e4m3>(f[0]);
+}
+
+__device__ __forceinline__ float weight_at(const void *w, gdn_dtype dt, int64_t i)
+{
+    if (!w) return 1.f;
+    return dt == GDN_F32 ? ((const float *)w)[i] : __bfloat162float(((const __nv_bfloat16 *)w)[i]);
+}
+
+// (sum of a, sum or maximum of b) over the tpr threads of a row; every one of them gets both.  `buf` is this
+// row's half of a double buffer, so one barrier per row is enough.
+template <bool MAX>
+__device__ __forceinline__ float2 row_reduce(float a, float b, int tpr, float2 *buf)
+{
+#pragma unroll
+    for (int off = 16; off; off >>= 1) {
+        if (off < tpr) {
+            a += __shfl_xor_sync(0xffffffffu, a, off);
+            const float o = __shfl_xor_sync(0xffffffffu, b, off);
+            b = MAX ? max_nan(b, o) : b + o;
+        }
+    }
+    if (tpr > 32) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = tpr >> 5, w0 = warp / nw * nw;
+        if (lane == 0) buf[warp] = make_float2(a, b);
+        __syncthreads();
+        const float2 v = lane < nw ? buf[w0 + lane] : make_float2(0.f, 0.f);
+        a = v.x;
+        b = v.y;
+#pragma unroll
+        for (int off = 8; off; off >>= 1) {
+            a += __shfl_xor_sync(0xffffffffu, a, off);
+            const float o = __shfl_xor_sync(0xffffffffu, b, off);
+            b = MAX ? max_nan(b, o) : b + o;
+        }
+        a = __shfl_sync(0xffffffffu, a, 0);
+        b = __shfl_sync(0xffffffffu, b, 0);
+    }
+    return make_float2(a, b);
+}
+
+// tpr threads (a power of two) per row, VPT groups of VEC elements each
+template <typename T, typename TO, int VEC, int VPT>
+__global__ void __launch_bounds__(kRowThreads) norm_kernel(NormArgs a, int tpr)
+{
+    __shared__ float2 red[2][kRowThreads / 32];
+    const int t = threadIdx.x & (tpr - 1), rpb = blockDim.x / tpr, nv = a.D / VEC;
+    const int64_t step = (int64_t)gridDim.x * rpb;
+    const T *x = (const T *)a.x, *r = (const T *)a.r;
+    float w[VPT][VEC];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            const int c = (t + i * tpr) * VEC + j;
+            w[i][j] = c < a.D ? weight_at(a.w, a.w_dt, c) : 0.f;
+        }
+    Raw<T, VEC> xr[VPT], rr[VPT];
+    auto fetch = [&](int64_t row) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = t + i * tpr;
+            if (v < nv && row < a.M) {
+                xr[i].load(x + row * a.ldx + (int64_t)v * VEC);
+                if (r) rr[i].load(r + row * a.ldr + (int64_t)v * VEC);
+            }
+        }
+    };
+    int64_t row = (int64_t)blockIdx.x * rpb + threadIdx.x / tpr;
+    fetch(row);
+    // every thread of a block runs the same number of rounds (they meet in the reduction)
+    const int64_t rounds = (a.M - (int64_t)blockIdx.x * rpb + step - 1) / step;
+    for (int64_t it = 0; it < rounds; ++it, row += step) {
+        float h[VPT][VEC];
+        float ss = 0.f, mx = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const bool in = t + i * tpr < nv && row < a.M;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) h[i][j] = 0.f;
+            if (in) {
+                xr[i].to(h[i]);
+                if (r) {
+                    float q[VEC];
+                    rr[i].to(q);
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) h[i][j] += q[j];
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                ss = fmaf(h[i][j], h[i][j], ss);
+                mx = max_nan(mx, fabsf(h[i][j] * w[i][j]));
+            }
+        }
+        const int64_t cur = row;
+        fetch(row + step);
+        const float2 s = row_reduce<true>(ss, mx, tpr, red[it & 1]);
+        const float rn = a.normalise ? 1.f / sqrtf(s.x / (float)a.D + a.eps) : 1.f;
+        float inv = 1.f;
+        if (sizeof(TO) == 1) {
+            const float sc = max_nan(s.y * rn / kE4m3Max, kScaleMin);
+            inv = 1.f / sc;
+            if (t == 0 && cur < a.M) a.scale[cur] = sc;
+        }
+        if (cur >= a.M) continue;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = t + i * tpr;
+            if (v >= nv) continue;
+            if (a.h) put<VEC>((T *)a.h + cur * a.D + (int64_t)v * VEC, h[i]);
+            float y[VEC];
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                y[j] = h[i][j] * rn * w[i][j];
+                if (sizeof(TO) == 1) y[j] *= inv;
+            }
+            put<VEC>((TO *)a.y + cur * a.D + (int64_t)v * VEC, y);
+        }
+    }
+}
+
+// Rows of any width: one block per row, read twice (the second time from the caches)
+template <typename T, typename TO>
+__global__ void __launch_bounds__(kRowThreads) norm_wide_kernel(NormArgs a)
+{
+    __shared__ float2 red[2][kRowThreads / 32];
+    const T *x = (const T *)a.x, *r = (const T *)a.r;
+    int it = 0;
+    for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, ++it) {
+        auto at = [&](int c) {
+            const float v = to_f(x[row * a.ldx + c]);
+            return r ? v + to_f(r[row * a.ldr + c]) : v;
+        };
+        float ss = 0.f, mx = 0.f;
+        for (int c = threadIdx.x; c < a.D; c += blockDim.x) {
+            const float h = at(c);
+            ss = fmaf(h, h, ss);
+            mx = max_nan(mx, fabsf(h * weight_at(a.w, a.w_dt, c)));
+        }
+        const float2 s = row_reduce<true>(ss, mx, blockDim.x, red[it & 1]);
+        const float rn = a.normalise ? 1.f / sqrtf(s.x / (float)a.D + a.eps) : 1.f;
+        float inv = 1.f;
+        if (sizeof(TO) == 1) {
+            const float sc = max_nan(s.y * rn / kE4m3Max, kScaleMin);
+            inv = 1.f / sc;
+            if (threadIdx.x == 0) a.scale[row] = sc;
+        }
+        // (h may be r itself: it is written only here, by the thread that reads the same element)
+        for (int c = threadIdx.x; c < a.D; c += blockDim.x) {
+            const float h = at(c);
+            if (a.h) ((T *)a.h)[row * a.D + c] = from_f<T>(h);
+            float y = h * rn * weight_at(a.w, a.w_dt, c);
+            if (sizeof(TO) == 1) y *= inv;
+            ((TO *)a.y)[row * a.D + c] = from_f<TO>(y);
+        }
+    }
+}
+
+// The gradients of one row from (sum h^2, sum w dy h):  n = sqrt(mean h^2 + eps),
+// dx = dh + (w dy - h mean(w dy h) / n^2) / n; the block's rows add dy h / n to dw in registers
+template <typename T, int VEC, int VPT>
+__global__ void __launch_bounds__(kRowThreads) norm_bwd_kernel(NormBwdArgs a, int tpr)
+{
+    __shared__ float2 red[2][kRowThreads / 32];
+    extern __shared__ float dws[];  // [rows per block][D], where a block holds several rows
+    const int t = threadIdx.x & (tpr - 1), rpb = blockDim.x / tpr, nv = a.D / VEC;
+    const int64_t step = (int64_t)gridDim.x * rpb;
+    const T *gy = (const T *)a.dy, *gh = (const T *)a.h, *gd = (const T *)a.dh;
+    float w[VPT][VEC], dw[VPT][VEC];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            const int c = (t + i * tpr) * VEC + j;
+            w[i][j] = c < a.D ? weight_at(a.w, a.w_dt, c) : 0.f;
+            dw[i][j] = 0.f;
+        }
+    Raw<T, VEC> yr[VPT], hr[VPT], dr[VPT];
+    auto fetch = [&](int64_t row) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = t + i * tpr;
+            if (v < nv && row < a.M) {
+                yr[i].load(gy + row * a.ld_dy + (int64_t)v * VEC);
+                hr[i].load(gh + row * a.ld_h + (int64_t)v * VEC);
+                if (gd) dr[i].load(gd + row * a.ld_dh + (int64_t)v * VEC);
+            }
+        }
+    };
+    int64_t row = (int64_t)blockIdx.x * rpb + threadIdx.x / tpr;
+    fetch(row);
+    const int64_t rounds = (a.M - (int64_t)blockIdx.x * rpb + step - 1) / step;
+    for (int64_t it = 0; it < rounds; ++it, row += step) {
+        float h[VPT][VEC], dy[VPT][VEC], dh[VPT][VEC];
+        float ss = 0.f, sd = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const bool in = t + i * tpr < nv && row < a.M;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) h[i][j] = dy[i][j] = dh[i][j] = 0.f;
+            if (in) {
+                hr[i].to(h[i]);
+                yr[i].to(dy[i]);
+                if (gd) dr[i].to(dh[i]);
+            }
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                ss = fmaf(h[i][j], h[i][j], ss);
+                sd = fmaf(w[i][j] * dy[i][j], h[i][j], sd);
+            }
+        }
+        const int64_t cur = row;
+        fetch(row + step);
+        const float2 s = row_reduce<false>(ss, sd, tpr, red[it & 1]);
+        const float rn = 1.f / sqrtf(s.x / (float)a.D + a.eps);
+        const float c = s.y / (float)a.D * rn * rn;
+        if (cur >= a.M) continue;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = t + i * tpr;
+            if (v >= nv) continue;
+            float dx[VEC];
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                dx[j] = dh[i][j] + (w[i][j] * dy[i][j] - h[i][j] * c) * rn;
+                dw[i][j] = fmaf(dy[i][j], h[i][j] * rn, dw[i][j]);
+            }
+            put<VEC>((T *)a.dx + cur * a.D + (int64_t)v * VEC, dx);
+        }
+    }
+    if (!a.dw) return;
+    if (rpb == 1) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+            if (t + i * tpr < nv)
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) a.part[(int64_t)blockIdx.x * a.D + (t + i * tpr) * VEC + j] = dw[i][j];
+        return;
+    }
+    const int grp = threadIdx.x / tpr;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+        if (t + i * tpr < nv)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) dws[grp * a.D + (t + i * tpr) * VEC + j] = dw[i][j];
+    __syncthreads();
+    for (int cidx = threadIdx.x; cidx < a.D; cidx += blockDim.x) {
+        float s = 0.f;
+        for (int q = 0; q < rpb; ++q) s += dws[q * a.D + cidx];
+        a.part[(int64_t)blockIdx.x * a.D + cidx] = s;
+    }
+}
+
+// Wide rows: dx (and 1 / n of every row), then dw by columns
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads) norm_bwd_wide_kernel(NormBwdArgs a)
+{
+    __shared__ float2 red[2][kRowThreads / 32];
+    const T *gy = (const T *)a.dy, *gh = (const T *)a.h, *gd = (const T *)a.dh;
+    int it = 0;
+    for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, ++it) {
+        float ss = 0.f, sd = 0.f;
+        for (int c = threadIdx.x; c < a.D; c += blockDim.x) {
+            const float h = to_f(gh[row * a.ld_h + c]);
+            ss = fmaf(h, h, ss);
+            sd = fmaf(weight_at(a.w, a.w_dt, c) * to_f(gy[row * a.ld_dy + c]), h, sd);
+        }
+        const float2 s = row_reduce<false>(ss, sd, blockDim.x, red[it & 1]);
+        const float rn = 1.f / sqrtf(s.x / (float)a.D + a.eps);
+        const float k = s.y / (float)a.D * rn * rn;
+        if (threadIdx.x == 0 && a.rstd) a.rstd[row] = rn;  // (only dw needs it)
+        for (int c = threadIdx.x; c < a.D; c += blockDim.x) {
+            const float h = to_f(gh[row * a.ld_h + c]);
+            float dx = (weight_at(a.w, a.w_dt, c) * to_f(gy[row * a.ld_dy + c]) - h * k) * rn;
+            if (gd) dx += to_f(gd[row * a.ld_dh + c]);
+            ((T *)a.dx)[row * a.D + c] = from_f<T>(dx);
+        }
+    }
+}
+template <typename T>
+__global__ void __launch_bounds__(256) norm_dw_wide_kernel(NormBwdArgs a)
+{
+    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (c >= a.D) return;
+    const T *gy = (const T *)a.dy, *gh = (const T *)a.h;
+    float s = 0.f;
+    for (int64_t row = blockIdx.y; row < a.M; row += gridDim.y)
+        s = fmaf(to_f(gy[row * a.ld_dy + c]), to_f(gh[row * a.ld_h + c]) * a.rstd[row], s);
+    a.part[(int64_t)blockIdx.y * a.D + c] = s;
+}
+
+bool aligned16(const void *p, int64_t ld, int esz) { return ((uintptr_t)p & 15) == 0 && (ld * esz) % 16 == 0; }
+
+// Threads of a row, elements of a thread and the block: one group of VEC elements a thread while the row
+// fits a block of 512 so, else two, else four (or 16 single elements).
+struct RowPlan {
+    int vec, vpt, tpr, threads;
+};
+RowPlan plan_rows(int D, int esz, bool vec_ok)
+{
+    RowPlan p;
+    p.vec = vec_ok ? 16 / esz : 1;
+    const int nv = (D + p.vec - 1) / p.vec;
+    p.vpt = p.vec == 1 ? 4 : 1;
+    while (nv > kRowThreads * p.vpt) p.vpt *= p.vec == 1 ? 4 : 2;
+    p.tpr = 1;
+    while (p.tpr * p.vpt < nv) p.tpr *= 2;
+    p.threads = p.tpr < 128 ? 128 : p.tpr;
+    return p;
+}
+
+int64_t norm_blocks(int64_t M, const RowPlan &p, int num_sms)
+{
+    const int64_t need = (M + p.threads / p.tpr - 1) / (p.threads / p.tpr);
+    const int64_t most = (int64_t)num_sms * (1024 / p.threads);
+    return need < most ? need : most;
+}
+
+template <typename T, typename TO>
+cudaError_t norm_go(const NormArgs &a, cudaStream_t st)
+{
+    constexpr int V = 16 / (int)sizeof(T);
+    const int sms = device_sm_count();
+    if (a.D > kWide) {
+        const int64_t most = (int64_t)sms * 4;
+        norm_wide_kernel<T, TO><<<(unsigned)(a.M < most ? a.M : most), kRowThreads, 0, st>>>(a);
+        return cudaGetLastError();
+    }
+    const bool ok = a.D % V == 0 && aligned16(a.x, a.ldx, sizeof(T)) && (!a.r || aligned16(a.r, a.ldr, sizeof(T))) &&
+                    ((uintptr_t)a.y & 15) == 0 && ((uintptr_t)a.h & 15) == 0;
+    const RowPlan p = plan_rows(a.D, sizeof(T), ok);
+    const unsigned grid = (unsigned)norm_blocks(a.M, p, sms);
+    if (p.vec == 1) {
+        if (p.vpt == 4) norm_kernel<T, TO, 1, 4><<<grid, p.threads, 0, st>>>(a, p.tpr);
+        else norm_kernel<T, TO, 1, 16><<<grid, p.threads, 0, st>>>(a, p.tpr);
+    } else if (p.vpt == 1) {
+        norm_kernel<T, TO, V, 1><<<grid, p.threads, 0, st>>>(a, p.tpr);
+    } else if (p.vpt == 2) {
+        norm_kernel<T, TO, V, 2><<<grid, p.threads, 0, st>>>(a, p.tpr);
+    } else {
+        norm_kernel<T, TO, V, kRowElems / V><<<grid, p.threads, 0, st>>>(a, p.tpr);
+    }
+    return cudaGetLastError();
+}
+
+bool bwd_vec(const NormBwdArgs &a, int esz)
+{
+    return a.D % (16 / esz) == 0 && aligned16(a.dy, a.ld_dy, esz) && aligned16(a.h, a.ld_h, esz) &&
+           (!a.dh || aligned16(a.dh, a.ld_dh, esz)) && ((uintptr_t)a.dx & 15) == 0;
+}
+
+constexpr int kWideParts = 64;
+
+template <typename T>
+cudaError_t norm_bwd_go(const NormBwdArgs &a, int sms, cudaStream_t st)
+{
+    constexpr int V = 16 / (int)sizeof(T);
+    int64_t parts;
+    if (norm_bwd_wide(a.D)) {
+        const int64_t most = (int64_t)sms * 4;
+        norm_bwd_wide_kernel<T><<<(unsigned)(a.M < most ? a.M : most), kRowThreads, 0, st>>>(a);
+        parts = a.M < kWideParts ? a.M : kWideParts;
+        if (a.dw) norm_dw_wide_kernel<T><<<dim3((unsigned)((a.D + 255) / 256), (unsigned)parts), 256, 0, st>>>(a);
+    } else {
+        const RowPlan p = plan_rows(a.D, sizeof(T), bwd_vec(a, sizeof(T)));
+        const unsigned grid = (unsigned)norm_blocks(a.M, p, sms);
+        parts = grid;
+        const size_t sm = p.threads > p.tpr ? (size_t)(p.threads / p.tpr) * a.D * sizeof(float) : 0;
+        if (p.vec == 1) {
+            if (p.vpt == 4) norm_bwd_kernel<T, 1, 4><<<grid, p.threads, sm, st>>>(a, p.tpr);
+            else norm_bwd_kernel<T, 1, 16><<<grid, p.threads, sm, st>>>(a, p.tpr);
+        } else if (p.vpt == 1) {
+            norm_bwd_kernel<T, V, 1><<<grid, p.threads, sm, st>>>(a, p.tpr);
+        } else if (p.vpt == 2) {
+            norm_bwd_kernel<T, V, 2><<<grid, p.threads, sm, st>>>(a, p.tpr);
+        } else {
+            norm_bwd_kernel<T, V, kRowElems / V><<<grid, p.threads, sm, st>>>(a, p.tpr);
+        }
+    }
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || !a.dw) return e;
+    return launch_colsum_finish(a.part, parts, a.D, a.dw, st);
+}
+
+}  // namespace
+
+bool norm_bwd_wide(int D) { return D > kWide; }
+
+int norm_bwd_parts(int64_t M, int D, gdn_dtype dt, int num_sms)
+{
+    if (norm_bwd_wide(D)) return (int)(M < kWideParts ? M : kWideParts);
+    // the larger of the vector and the single-element form (alignment is not known here)
+    const int esz = dt == GDN_F32 ? 4 : 2;
+    int64_t parts = norm_blocks(M, plan_rows(D, esz, false), num_sms);
+    if (D % (16 / esz) == 0) {
+        const int64_t q = norm_blocks(M, plan_rows(D, esz, true), num_sms);
+        parts = q > parts ? q : parts;
+    }
+    return (int)parts;
+}
+
+cudaError_t launch_norm(const NormArgs &a, cudaStream_t st)
+{
+    if (a.M <= 0) return cudaSuccess;
+    if (a.dt == GDN_F32) return a.out_dt == GDN_E4M3 ? norm_go<float, __nv_fp8_e4m3>(a, st) : norm_go<float, float>(a, st);
+    return a.out_dt == GDN_E4M3 ? norm_go<__nv_bfloat16, __nv_fp8_e4m3>(a, st) : norm_go<__nv_bfloat16, __nv_bfloat16>(a, st);
+}
+
+cudaError_t launch_norm_bwd(const NormBwdArgs &a, int num_sms, cudaStream_t st)
+{
+    if (a.M <= 0) return a.dw ? cudaMemsetAsync(a.dw, 0, a.D * sizeof(float), st) : cudaSuccess;
+    return a.dt == GDN_F32 ? norm_bwd_go<float>(a, num_sms, st) : norm_bwd_go<__nv_bfloat16>(a, num_sms, st);
+}
+
+}  // namespace gdn

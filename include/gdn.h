@@ -56,7 +56,12 @@ extern "C" {
 
 typedef struct CUstream_st *gdn_stream_t; /* identical to cudaStream_t */
 
-typedef enum { GDN_F32 = 0, GDN_BF16 = 1 } gdn_dtype;
+typedef enum {
+    GDN_F32 = 0,
+    GDN_BF16 = 1,
+    GDN_E4M3 = 2 /* 8-bit floating point, 4 exponent and 3 mantissa bits (the decoder-block
+                    operators only: gdn_rms_norm, gdn_linear, gdn_gated_linear)           */
+} gdn_dtype;
 
 typedef enum { GDN_GATE_SCALAR = 0, GDN_GATE_CHANNEL = 1 } gdn_gate_kind;
 
@@ -354,6 +359,153 @@ gdn_status gdn_chunk_summary(const gdn_shape *s,
  */
 gdn_status gdn_chain_states(int ranks, int pairs, int K, int V, const float *summaries,
                             const float *h0, float *starts, gdn_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The operators that stand around the gated delta rule in a decoder block:
+ * the norm before it, the projections into and out of it, the feed-forward
+ * block after it.  (No counterpart in the pages; their conventions are those
+ * above: device pointers, work enqueued on `stream`, argument errors before
+ * anything is enqueued.)
+ *
+ *  - Matrices are row-major with consecutive elements in a row; inputs take a
+ *    row stride in elements (at least the row's length), outputs are
+ *    contiguous unless they have a stride.  Any length, any alignment to the
+ *    element: operands whose rows do not start on 16-byte boundaries are
+ *    copied once into the workspace in a padded layout.
+ *  - `workspace`: device memory of at least the size that the operator's
+ *    _workspace_size call gives for the same arguments, 256-byte aligned, not
+ *    used by another call that can run concurrently.  NULL: the
+ *    library-managed workspace of (device, stream), which is not allowed to
+ *    grow while the stream is being captured (GDN_ERR_NOMEM then).  A size of
+ *    0 needs none.
+ *  - A device-side wait that ran out (2 s) is recorded per device; the next
+ *    gdn_read_layer_status reads and clears it.
+ *  - Zero rows are allowed: outputs without rows are left alone, the
+ *    gradients of weights and biases are then zero.
+ */
+typedef struct {
+    int64_t rows;         /* M */
+    int width;            /* D >= 1 */
+    gdn_dtype dtype;      /* x, residual, h, dy, dh, dx: GDN_F32 or GDN_BF16           */
+    gdn_dtype w_dtype;    /* weight: GDN_F32 or GDN_BF16                               */
+    gdn_dtype out_dtype;  /* y: `dtype`, or GDN_E4M3 with one scale per row            */
+    float eps;            /* >= 0 */
+    const void *x;        /* [M][D], row stride ldx (backward: h)                      */
+    int64_t ldx;
+    const void *residual; /* [M][D], row stride ld_residual; nullable                  */
+    int64_t ld_residual;
+    const void *weight;   /* [D]; nullable (all one)                                   */
+    void *y;              /* [M][D]                                                    */
+    float *scale;         /* [M], out_dtype GDN_E4M3: y stands for scale[m] * y[m][d]  */
+    void *h;              /* [M][D], x + residual rounded to dtype; may be residual or
+                             x itself (same rows); nullable                            */
+    const void *dy;       /* backward: [M][D], row stride ld_dy                        */
+    int64_t ld_dy;
+    const void *dh;       /* backward: the gradient that reaches h past the norm,
+                             [M][D], row stride ld_dh; nullable (zero)                 */
+    int64_t ld_dh;
+    void *dx;             /* backward: [M][D], may be dy or dh itself (same rows)      */
+    float *dweight;       /* backward: [D]; nullable                                   */
+} gdn_norm_args;
+
+/*
+ * Root-mean-square norm of rows with the residual's addition in front:
+ *     h = x + residual,  n = sqrt(mean(h^2) + eps),  y = weight h / n
+ * in fp32 from the unrounded h, rounded once.  With out_dtype GDN_E4M3:
+ *     scale = max(max|y| / 448, 2^-126),  y = e4m3(y / scale), saturating
+ * (a row that holds a NaN or an infinity gets a NaN scale).
+ */
+gdn_status gdn_rms_norm(const gdn_norm_args *a, gdn_stream_t stream);
+
+/* One scale per row and e4m3 values of x as it stands: gdn_rms_norm without
+ * the norm, residual and weight (x, y, scale of `a`). */
+gdn_status gdn_quantize_rows(const gdn_norm_args *a, gdn_stream_t stream);
+
+/*
+ * Gradients of gdn_rms_norm (bf16 / fp32 output) from h = x + residual:
+ *     dx = dh + (weight dy - h mean(weight dy h) / n^2) / n
+ * (the gradient of x and of residual), dweight = sum over rows of dy h / n,
+ * summed in a fixed order.
+ */
+size_t gdn_rms_norm_bwd_workspace_size(const gdn_norm_args *a);
+gdn_status gdn_rms_norm_bwd(const gdn_norm_args *a, void *workspace, size_t ws_bytes, gdn_stream_t stream);
+
+typedef enum {
+    GDN_ACT_NONE = 0,
+    GDN_ACT_SILU = 1,      /* z / (1 + exp(-z))                                        */
+    GDN_ACT_GELU = 2,      /* z (1 + erf(z / sqrt 2)) / 2                              */
+    GDN_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2        */
+    GDN_ACT_RELU = 4,
+    GDN_ACT_SIGMOID = 5
+} gdn_activation;
+
+typedef struct {
+    int64_t rows;         /* M */
+    int out_features;     /* N (gated linear unit: F, the width of one half)           */
+    int in_features;      /* K >= 1 */
+    gdn_dtype dtype;      /* x and w: GDN_F32, GDN_BF16 or (forward only) GDN_E4M3     */
+    gdn_dtype out_dtype;  /* y and residual: GDN_F32 or GDN_BF16 (fp32 inputs: GDN_F32;
+                             gated and backward: `dtype`, GDN_BF16 for GDN_E4M3)       */
+    gdn_activation act;
+    const void *x;        /* [M][K], row stride ldx                                    */
+    int64_t ldx;
+    const void *w;        /* [N][K] (gated: [2F][K], the gate's rows first), stride ldw */
+    int64_t ldw;
+    const float *x_scale; /* [M] and [N] (gated: [2F]): the scales of GDN_E4M3 inputs  */
+    const float *w_scale; /*   (both or none; none: 1)                                 */
+    const float *bias;    /* [N], nullable (gated: none)                               */
+    const void *residual; /* [M][N], row stride ld_residual; nullable                  */
+    int64_t ld_residual;
+    void *y;              /* [M][N] (gated: [M][F]), row stride ldy; may be residual
+                             itself.  Gated backward: the recomputed output, nullable  */
+    int64_t ldy;
+    const void *dy;       /* backward: [M][N] (gated: [M][F]), row stride ld_dy        */
+    int64_t ld_dy;
+    void *dx;             /* backward: [M][K], nullable                                */
+    void *dw;             /* backward: as w, contiguous, nullable                      */
+    float *dbias;         /* backward: [N], nullable                                   */
+} gdn_linear_args;
+
+/*
+ * Linear layer with its epilogue:
+ *     y = act(x_scale_m w_scale_n (x w^T) + bias) + residual
+ * Products are summed in fp32 and the epilogue runs on those sums; y is
+ * rounded once.  bf16 and e4m3 inputs run on the tensor cores.
+ */
+size_t gdn_linear_workspace_size(const gdn_linear_args *a);
+gdn_status gdn_linear(const gdn_linear_args *a, void *workspace, size_t ws_bytes, gdn_stream_t stream);
+
+/*
+ * Gradients of gdn_linear (F32 or BF16; the residual's is dy): with
+ * z = x w^T + bias recomputed where there is an activation,
+ *     dz = dy act'(z),  dx = dz w,  dw = dz^T x,  dbias = sum over rows of dz
+ * dz is rounded to `dtype` between the products (an operand of the tensor
+ * cores); dbias is summed from the unrounded values, in a fixed order.
+ */
+size_t gdn_linear_bwd_workspace_size(const gdn_linear_args *a);
+gdn_status gdn_linear_bwd(const gdn_linear_args *a, void *workspace, size_t ws_bytes, gdn_stream_t stream);
+
+/*
+ * Gated linear unit, both projections and their product in one kernel:
+ *     y = act(x w_gate^T) * (x w_up^T),   w = [w_gate; w_up]
+ */
+size_t gdn_gated_linear_workspace_size(const gdn_linear_args *a);
+gdn_status gdn_gated_linear(const gdn_linear_args *a, void *workspace, size_t ws_bytes, gdn_stream_t stream);
+
+/*
+ * Gradients of gdn_gated_linear (F32 or BF16) from x, w and dy alone: the
+ * projections are recomputed (nothing of the forward is kept), with
+ *     dgate = dy up act'(gate),  dup = dy act(gate)
+ * rounded to `dtype` between the products, dx = dgate w_gate + dup w_up and
+ * dw = [dgate dup]^T x.  `y`, when given, receives the recomputed output.
+ */
+size_t gdn_gated_linear_bwd_workspace_size(const gdn_linear_args *a);
+gdn_status gdn_gated_linear_bwd(const gdn_linear_args *a, void *workspace, size_t ws_bytes, gdn_stream_t stream);
+
+/* Synchronise `stream`, return what device-side waits of the operators above
+ * recorded on the current device since the last read (GDN_OK or
+ * GDN_ERR_TIMEOUT) and clear it. */
+gdn_status gdn_read_layer_status(gdn_stream_t stream);
 
 /* Plan summary (host only, no GPU needed) -- what a call would launch: the
  * engine and the in-GPU split (FlashQLA blog, "A balanced solution", the CP
