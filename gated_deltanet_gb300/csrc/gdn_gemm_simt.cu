@@ -9,30 +9,30 @@ namespace {
 
 constexpr int kT = 64, kKt = 16;
 
-template <typename T, typename TO, int EPI>
+template <int EPI>
 __global__ void __launch_bounds__(256) gemm_simt_kernel(GemmArgs g)
 {
     constexpr bool kTwo = EPI == kEpiGated || EPI == kEpiGatedBwd;
     constexpr int kB = kTwo ? 2 : 1;
-    constexpr bool kPrecise = sizeof(TO) == 4;
+    constexpr bool kPrecise = true;
     __shared__ float sa[kKt][kT + 4], sb[kB][kKt][kT + 4];
     __shared__ float cs[16][kT];
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int64_t m0 = (int64_t)blockIdx.x * kT, n0 = (int64_t)blockIdx.y * kT;  // (x has the larger limit)
-    const T *A = (const T *)g.a, *B = (const T *)g.b;
+    const float *A = (const float *)g.a, *B = (const float *)g.b;
     float acc[kB][4][4] = {};
     for (int64_t k0 = 0; k0 < g.K; k0 += kKt) {
         // consecutive threads along the operand's contiguous index
         for (int i = tid; i < kT * kKt; i += 256) {
             const int mi = g.a_t ? i & (kT - 1) : i / kKt, ki = g.a_t ? i / kT : i & (kKt - 1);
             const int64_t m = m0 + mi, k = k0 + ki;
-            sa[ki][mi] = m < g.M && k < g.K ? to_f(A[g.a_t ? k * g.lda + m : m * g.lda + k]) : 0.f;
+            sa[ki][mi] = m < g.M && k < g.K ? A[g.a_t ? k * g.lda + m : m * g.lda + k] : 0.f;
             const int ni = g.b_t ? i & (kT - 1) : i / kKt, kj = g.b_t ? i / kT : i & (kKt - 1);
             const int64_t n = n0 + ni, kk = k0 + kj;
 #pragma unroll
             for (int h = 0; h < kB; ++h) {
                 const int64_t row = n + h * g.N;
-                sb[h][kj][ni] = n < g.N && kk < g.K ? to_f(B[g.b_t ? kk * g.ldb + row : row * g.ldb + kk]) : 0.f;
+                sb[h][kj][ni] = n < g.N && kk < g.K ? B[g.b_t ? kk * g.ldb + row : row * g.ldb + kk] : 0.f;
             }
         }
         __syncthreads();
@@ -52,44 +52,41 @@ __global__ void __launch_bounds__(256) gemm_simt_kernel(GemmArgs g)
         }
         __syncthreads();
     }
-    TO *out = (TO *)g.out;
-    const TO *extra = (const TO *)g.extra;
+    float *out = (float *)g.out;
+    const float *extra = (const float *)g.extra;
     float col[4] = {};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int64_t m = m0 + 4 * ty + i;
         if (m >= g.M) continue;
-        const float sx = g.x_scale ? g.x_scale[m] : 1.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int64_t n = n0 + 4 * tx + j;
             if (n >= g.N) continue;
             float z = acc[0][i][j];
-            if (g.x_scale) z *= sx * g.w_scale[n];
             if (EPI == kEpiLinear) {
                 if (g.bias) z += g.bias[n];
                 z = act_value<kPrecise>(g.act, z);
-                if (extra) z += to_f(extra[m * g.ld_extra + n]);
-                out[m * g.ldo + n] = from_f<TO>(z);
+                if (extra) z += extra[m * g.ld_extra + n];
+                out[m * g.ldo + n] = z;
             } else if (EPI == kEpiDact) {
                 if (g.bias) z += g.bias[n];
                 float v, d;
                 act_both<kPrecise>(g.act, z, v, d);
-                const float dz = to_f(extra[m * g.ld_extra + n]) * d;
-                out[m * g.ldo + n] = from_f<TO>(dz);
+                const float dz = extra[m * g.ld_extra + n] * d;
+                out[m * g.ldo + n] = dz;
                 col[j] += dz;
             } else {
-                float u = acc[kB - 1][i][j];
-                if (g.x_scale) u *= sx * g.w_scale[g.N + n];
+                const float u = acc[kB - 1][i][j];
                 if (EPI == kEpiGated) {
-                    out[m * g.ldo + n] = from_f<TO>(act_value<kPrecise>(g.act, z) * u);
+                    out[m * g.ldo + n] = act_value<kPrecise>(g.act, z) * u;
                 } else {
                     float v, d;
                     act_both<kPrecise>(g.act, z, v, d);
-                    const float dh = to_f(extra[m * g.ld_extra + n]);
-                    out[m * g.ldo + n] = from_f<TO>(dh * u * d);
-                    out[m * g.ldo + g.N + n] = from_f<TO>(dh * v);
-                    if (g.out2) ((TO *)g.out2)[m * g.ldo2 + n] = from_f<TO>(v * u);
+                    const float dh = extra[m * g.ld_extra + n];
+                    out[m * g.ldo + n] = dh * u * d;
+                    out[m * g.ldo + g.N + n] = dh * v;
+                    if (g.out2) ((float *)g.out2)[m * g.ldo2 + n] = v * u;
                 }
             }
         }
@@ -107,19 +104,6 @@ __global__ void __launch_bounds__(256) gemm_simt_kernel(GemmArgs g)
             if (n < g.N && p * 32 < g.M) g.colpart[p * g.N + n] = s;
         }
     }
-}
-
-template <typename T, typename TO>
-cudaError_t go(const GemmArgs &g, Epi epi, cudaStream_t st)
-{
-    const dim3 grid((unsigned)((g.M + kT - 1) / kT), (unsigned)((g.N + kT - 1) / kT));
-    switch (epi) {
-    case kEpiLinear: gemm_simt_kernel<T, TO, kEpiLinear><<<grid, 256, 0, st>>>(g); break;
-    case kEpiGated: gemm_simt_kernel<T, TO, kEpiGated><<<grid, 256, 0, st>>>(g); break;
-    case kEpiDact: gemm_simt_kernel<T, TO, kEpiDact><<<grid, 256, 0, st>>>(g); break;
-    case kEpiGatedBwd: gemm_simt_kernel<T, TO, kEpiGatedBwd><<<grid, 256, 0, st>>>(g); break;
-    }
-    return cudaGetLastError();
 }
 
 // 32 columns per CTA, the parts dealt to 32 warps, whose sums meet in a fixed order
@@ -157,9 +141,14 @@ __global__ void __launch_bounds__(128) colsum_rows_kernel(const T *x, int64_t M,
 cudaError_t launch_gemm_simt(const GemmArgs &g, Epi epi, cudaStream_t st)
 {
     if (g.M <= 0 || g.N <= 0) return cudaSuccess;
-    if (g.in == GDN_F32) return go<float, float>(g, epi, st);
-    if (g.in == GDN_BF16) return g.out_dt == GDN_F32 ? go<__nv_bfloat16, float>(g, epi, st) : go<__nv_bfloat16, __nv_bfloat16>(g, epi, st);
-    return g.out_dt == GDN_F32 ? go<__nv_fp8_e4m3, float>(g, epi, st) : go<__nv_fp8_e4m3, __nv_bfloat16>(g, epi, st);
+    const dim3 grid((unsigned)((g.M + kT - 1) / kT), (unsigned)((g.N + kT - 1) / kT));
+    switch (epi) {
+    case kEpiLinear: gemm_simt_kernel<kEpiLinear><<<grid, 256, 0, st>>>(g); break;
+    case kEpiGated: gemm_simt_kernel<kEpiGated><<<grid, 256, 0, st>>>(g); break;
+    case kEpiDact: gemm_simt_kernel<kEpiDact><<<grid, 256, 0, st>>>(g); break;
+    case kEpiGatedBwd: gemm_simt_kernel<kEpiGatedBwd><<<grid, 256, 0, st>>>(g); break;
+    }
+    return cudaGetLastError();
 }
 
 cudaError_t launch_colsum_finish(const float *part, int64_t parts, int64_t N, float *out, cudaStream_t st)

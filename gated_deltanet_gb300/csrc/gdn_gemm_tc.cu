@@ -1,0 +1,661 @@
+// Products of bf16 and e4m3 operands on the tensor cores, with the epilogues of the decoder-block
+// operators.
+//
+// A pair of CTAs (a cluster of two, one per SM) owns a 256 x BN tile of accumulators: each CTA holds
+// 128 rows of A and half of B's rows in its shared memory and one M = 256 tcgen05.mma reads both halves,
+// so that every byte staged serves twice the products of a single CTA's tile (a single CTA's 128 x 256
+// instruction with both operands in shared memory takes 161 cycles here for 128 cycles of work; the pair's
+// reads half of B per SM).  Roles per CTA: eight epilogue warps, one thread that issues the TMA loads, one
+// that issues the products (in the pair's first CTA only).  The accumulators are double-buffered in tensor
+// memory, so a tile's epilogue runs under the next tile's products; a persistent grid walks the tiles in
+// groups of eight row tiles, which keeps one group's operands in L2.
+//
+// Operands are loaded as 128-byte-swizzled boxes, either along k (K-major) or, for the products of the
+// backward passes, along m / n as they lie in memory (MN-major): nothing is transposed.
+#include <cstring>
+#include <atomic>
+#include <mutex>
+
+#include <cudaTypedefs.h>
+
+#include "gdn_layer.cuh"
+#include "gdn_ptx.cuh"
+
+namespace gdn {
+namespace {
+
+using namespace ptx;
+
+__device__ unsigned g_tc_status;  // kStatusTimeout once a wait ran out
+constexpr unsigned long long kLimitNs = 2000000000ull;
+
+constexpr int kEpiWarps = 8, kThreads = 32 * (kEpiWarps + 2);
+constexpr int kABytes = 128 * 128;       // a CTA's rows of A, 128 bytes of k (or 64 k rows of 2 x 64 m)
+constexpr int kStageBuf = 32 * 128;      // one epilogue box: 32 rows of 128 bytes
+
+template <int BN> struct Geo {
+    static constexpr int kB = BN / 2 * 128;
+    static constexpr int kStage = kABytes + kB;
+    static constexpr int kStages = BN == 256 ? 5 : 6;
+    static constexpr int kTmem = 2 * BN;  // two accumulators
+    static constexpr int kBars = 2 * kStages + 4 + 2 * kEpiWarps;
+    static constexpr int kSmem = 1024 + kStages * kStage + kEpiWarps * 2 * kStageBuf + kBars * 8 + 16;
+};
+static_assert(Geo<256>::kSmem <= 227 * 1024 && Geo<128>::kSmem <= 227 * 1024, "shared memory budget");
+
+struct TcMaps {
+    CUtensorMap a, b, out, up, extra, out2;
+};
+struct TcParams {
+    int64_t M, N;            // output rows; output columns (gated: F)
+    int kblocks;             // blocks of 128 bytes of k
+    int mt, nt;              // tiles of 256 rows, of BN accumulator columns
+    int tma_out, tma_extra, tma_out2;
+    const float *x_scale, *w_scale, *bias;
+    int act;
+    const void *extra;
+    int64_t ld_extra;
+    void *out;
+    int64_t ldo;
+    void *out2;
+    int64_t ldo2;
+    float *colpart;
+};
+
+// ------------------------------------------------------------------ pair primitives
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
+}
+// the address, in the first CTA of the pair, of a barrier at the same place
+__device__ __forceinline__ uint32_t leader_addr(const void *p)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
+    return r;
+}
+__device__ __forceinline__ void remote_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// a wait for arrivals of both CTAs
+__device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity)
+{
+    uint64_t t0 = 0;
+    for (;;) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        const uint64_t t = globaltimer();
+        if (!t0) t0 = t;
+        if (t - t0 > kLimitNs) {
+            atomicOr(&g_tc_status, kStatusTimeout);
+            return false;
+        }
+    }
+}
+__device__ __forceinline__ bool wait_cta(uint64_t *bar, uint32_t parity)
+{
+    return mbar_wait(bar, parity, &g_tc_status, kStatusTimeout, kLimitNs);
+}
+__device__ __forceinline__ void pair_load(void *dst, const CUtensorMap *map, int c0, int c1, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+template <bool FP8>
+__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    if (FP8)
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(acc));
+    else
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+// arrives on the barrier at the same place in both CTAs once every product issued so far is done
+__device__ __forceinline__ void pair_commit(uint64_t *bar)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+// ------------------------------------------------------------------ epilogue boxes
+template <typename TO> struct Box {
+    static constexpr int kCols = 128 / (int)sizeof(TO);
+    // byte offset of (row, column) in a 128-byte-swizzled box
+    static __device__ __forceinline__ uint32_t at(int r, int c)
+    {
+        const int b = c * (int)sizeof(TO);
+        return (uint32_t)(r * 128 + ((((b >> 4) ^ (r & 7)) << 4) | (b & 15)));
+    }
+};
+// Rows that TMA cannot address (a pitch or a base off 16 bytes): element by element, 32 columns at a time
+template <typename TO>
+__device__ __forceinline__ void box_in(uint8_t *buf, const void *src, int64_t ld, int64_t row0, int64_t col0, int64_t M, int64_t N, int lane)
+{
+    for (int r = 0; r < 32; ++r)
+        for (int c = lane; c < Box<TO>::kCols; c += 32) {
+            const bool in = row0 + r < M && col0 + c < N;
+            *(TO *)(buf + Box<TO>::at(r, c)) = in ? ((const TO *)src)[(row0 + r) * ld + col0 + c] : from_f<TO>(0.f);
+        }
+    __syncwarp();
+}
+template <typename TO>
+__device__ __forceinline__ void box_out(const uint8_t *buf, void *dst, int64_t ld, int64_t row0, int64_t col0, int64_t M, int64_t N, int lane)
+{
+    __syncwarp();
+    for (int r = 0; r < 32; ++r)
+        for (int c = lane; c < Box<TO>::kCols; c += 32)
+            if (row0 + r < M && col0 + c < N) ((TO *)dst)[(row0 + r) * ld + col0 + c] = *(const TO *)(buf + Box<TO>::at(r, c));
+    __syncwarp();
+}
+__device__ __forceinline__ float lo_bf16(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float hi_bf16(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+// 32 values of a box row, 16 bytes at a time; `part`: which 32 columns
+template <typename TO> __device__ __forceinline__ void row_get(const uint8_t *buf, int r, int part, float *v);
+template <> __device__ __forceinline__ void row_get<__nv_bfloat16>(const uint8_t *buf, int r, int part, float *v)
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint4 u = *(const uint4 *)(buf + r * 128 + (((4 * part + j) ^ (r & 7)) << 4));
+        v[8 * j] = lo_bf16(u.x); v[8 * j + 1] = hi_bf16(u.x);
+        v[8 * j + 2] = lo_bf16(u.y); v[8 * j + 3] = hi_bf16(u.y);
+        v[8 * j + 4] = lo_bf16(u.z); v[8 * j + 5] = hi_bf16(u.z);
+        v[8 * j + 6] = lo_bf16(u.w); v[8 * j + 7] = hi_bf16(u.w);
+    }
+}
+template <> __device__ __forceinline__ void row_get<float>(const uint8_t *buf, int r, int, float *v)
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j) *(float4 *)(v + 4 * j) = *(const float4 *)(buf + r * 128 + ((j ^ (r & 7)) << 4));
+}
+template <typename TO> __device__ __forceinline__ void row_put(uint8_t *buf, int r, int part, const float *v);
+template <> __device__ __forceinline__ void row_put<__nv_bfloat16>(uint8_t *buf, int r, int part, const float *v)
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) *(uint4 *)(buf + r * 128 + (((4 * part + j) ^ (r & 7)) << 4)) = pack8(v + 8 * j);
+}
+template <> __device__ __forceinline__ void row_put<float>(uint8_t *buf, int r, int, const float *v)
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j) *(float4 *)(buf + r * 128 + ((j ^ (r & 7)) << 4)) = *(const float4 *)(v + 4 * j);
+}
+
+// keeps the uses of freshly loaded accumulators behind the wait for them
+__device__ __forceinline__ void pin32(float *v)
+{
+#pragma unroll
+    for (int j = 0; j < 32; ++j) asm volatile("" : "+f"(v[j]));
+}
+
+// Sum over the warp's 32 rows of each of 32 columns (one per register): halves of the columns change hands
+// at every step, 31 shuffles in all; lane l ends with the sum of column l.
+__device__ __forceinline__ float column_sums(float *v, int lane)
+{
+#pragma unroll
+    for (int w = 16; w; w >>= 1) {
+        const bool high = lane & w;
+#pragma unroll
+        for (int j = 0; j < w; ++j) {
+            const float give = high ? v[j] : v[j + w], keep = high ? v[j + w] : v[j];
+            v[j] = keep + __shfl_xor_sync(0xffffffffu, give, w);
+        }
+    }
+    return v[0];
+}
+
+// LAYOUT 0: A and B K-major; 1: B MN-major; 2: both MN-major
+template <bool FP8, int LAYOUT, int EPI, int BN, typename TO>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
+{
+    using G = Geo<BN>;
+    constexpr bool kGated = EPI == kEpiGated || EPI == kEpiGatedBwd;
+    constexpr bool kExtra = EPI != kEpiGated;
+    constexpr bool kPrecise = sizeof(TO) == 4;
+    constexpr int kOutN = kGated ? BN / 2 : BN;  // output columns of a tile
+    static_assert(!kGated || BN == 256, "a gated tile is 128 gate and 128 up columns");
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t *boxes = sm + G::kStages * G::kStage;
+    uint64_t *full = (uint64_t *)(boxes + kEpiWarps * 2 * kStageBuf);
+    uint64_t *empty = full + G::kStages, *tfull = empty + G::kStages, *tempty = tfull + 2, *ebar = tempty + 2;
+    uint32_t *tslot = (uint32_t *)(ebar + 2 * kEpiWarps);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_rank();
+    const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
+    const int tiles = p.mt * p.nt;
+
+    if (tid == 0) {
+        for (int s = 0; s < G::kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&tfull[i], 1);
+            mbar_init(&tempty[i], 2 * kEpiWarps);
+        }
+        for (int i = 0; i < 2 * kEpiWarps; ++i) mbar_init(&ebar[i], 1);
+        fence_mbar_init();
+    }
+    if (warp == kEpiWarps + 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tslot)), "r"(G::kTmem));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = *tslot;
+
+    // tile -> (row tile, column tile): groups of eight row tiles, column tiles within a group one after another
+    auto place = [&](int t, int &m, int &n) {
+        const int per = 8 * p.nt, g = t / per, w = t - g * per, rows = min(8, p.mt - 8 * g);
+        m = 8 * g + w % rows;
+        n = w / rows;
+    };
+    bool ok = true;
+
+    if (warp == kEpiWarps) {
+        // ---------------------------------------------------------------- loads
+        if (lane == 0) {
+            uint32_t it = 0;
+            for (int t = pair; t < tiles && ok; t += pairs) {
+                int mi, ni;
+                place(t, mi, ni);
+                const int m0 = mi * 256 + (int)rank * 128;
+                const int n0 = kGated ? (rank ? (int)p.N : 0) + ni * kOutN : ni * BN + (int)rank * (BN / 2);
+                for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
+                    const int s = it % G::kStages;
+                    if (!(ok = wait_cta(&empty[s], ((it / G::kStages) & 1) ^ 1))) break;
+                    uint8_t *sa = sm + s * G::kStage, *sb = sa + kABytes;
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * G::kStage);
+                    const uint32_t bar = leader_addr(&full[s]);
+                    const int k0 = kb * (FP8 ? 128 : 64);
+                    if (LAYOUT == 2) {
+                        pair_load(sa, &maps.a, m0, k0, bar);
+                        pair_load(sa + 8192, &maps.a, m0 + 64, k0, bar);
+                    } else {
+                        pair_load(sa, &maps.a, k0, m0, bar);
+                    }
+                    if (LAYOUT >= 1) {
+#pragma unroll
+                        for (int j = 0; j < BN / 128; ++j) pair_load(sb + 8192 * j, &maps.b, n0 + 64 * j, k0, bar);
+                    } else {
+                        pair_load(sb, &maps.b, k0, n0, bar);
+                    }
+                }
+            }
+            // the last products have read every stage before the CTAs of the pair may leave
+            for (int i = 0; i < G::kStages && ok; ++i, ++it) ok = wait_cta(&empty[it % G::kStages], ((it / G::kStages) & 1) ^ 1);
+        }
+    } else if (warp == kEpiWarps + 1) {
+        // ---------------------------------------------------------------- products
+        if (rank == 0 && lane == 0) {
+            constexpr uint32_t id = FP8 ? (1u << 4) | ((uint32_t)(BN >> 3) << 17) | (16u << 24)
+                                        : idesc_bf16_f32(256, BN, LAYOUT == 2, LAYOUT >= 1);
+            constexpr uint32_t sa_step = LAYOUT == 2 ? 128 : 2, sb_step = LAYOUT >= 1 ? 128 : 2;
+            uint32_t it = 0, n = 0;
+            for (int t = pair; t < tiles && ok; t += pairs, ++n) {
+                const uint32_t acc = n & 1;
+                if (!(ok = wait_cluster(&tempty[acc], ((n >> 1) & 1) ^ 1))) break;
+                tc_fence_after();
+                for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
+                    const int s = it % G::kStages;
+                    if (!(ok = wait_cluster(&full[s], (it / G::kStages) & 1))) break;
+                    tc_fence_after();
+                    const uint32_t a = smem_u32(sm + s * G::kStage);
+                    const uint64_t da = sdesc_sw128(a, LAYOUT == 2 ? 8192 : 16, 1024);
+                    const uint64_t db = sdesc_sw128(a + kABytes, LAYOUT >= 1 ? 8192 : 16, 1024);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        pair_mma<FP8>(tmem + acc * BN, da + j * sa_step, db + j * sb_step, id, (kb | j) != 0);
+                    pair_commit(&empty[s]);
+                }
+                if (ok) pair_commit(&tfull[acc]);
+            }
+        }
+    } else {
+        // ---------------------------------------------------------------- epilogue
+        constexpr int kCols = Box<TO>::kCols;
+        const int q = warp & 3, half = warp >> 2;
+        constexpr int kChunks = kOutN / kCols / 2;  // boxes of this warp (its half of the columns)
+        uint8_t *buf[2] = {boxes + warp * 2 * kStageBuf, boxes + warp * 2 * kStageBuf + kStageBuf};
+        uint64_t *eb = ebar + 2 * warp;
+        uint32_t n = 0, eph[2] = {0, 0};
+        for (int t = pair; t < tiles && ok; t += pairs, ++n) {
+            int mi, ni;
+            place(t, mi, ni);
+            const int64_t row0 = (int64_t)mi * 256 + rank * 128 + q * 32, row = row0 + lane;
+            const uint32_t acc = n & 1;
+            const uint32_t tl = tmem + acc * BN + ((uint32_t)(q * 32) << 16);
+            auto col_of = [&](int c) { return (int64_t)ni * kOutN + (half * kChunks + c) * kCols; };
+            auto live = [&](int c) { return col_of(c) < p.N && row0 < p.M; };
+            // the box of extra (residual, dy, dh) of chunk c
+            auto fetch = [&](int c) {
+                if (!kExtra || !p.extra || !live(c)) return;
+                if (p.tma_extra) {
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&eb[c & 1], kStageBuf);
+                        tma_load_2d(buf[c & 1], &maps.extra, (int)col_of(c), (int)row0, &eb[c & 1]);
+                    }
+                } else {
+                    box_in<TO>(buf[c & 1], p.extra, p.ld_extra, row0, col_of(c), p.M, p.N, lane);
+                }
+            };
+            // both buffers free again, for copies by either path
+            fence_proxy_async();
+            if (lane == 0) tma_store_wait_read0();
+            __syncwarp();
+            fetch(0);
+            if (kChunks > 1 && EPI != kEpiGatedBwd) fetch(1);
+            const float sx = FP8 && p.x_scale && row < p.M ? p.x_scale[row] : 1.f;
+            ok = wait_cluster(&tfull[acc], (n >> 1) & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                const int64_t col0 = col_of(c);
+                uint8_t *b = buf[c & 1];
+                if (c >= 2) {  // (four boxes of fp32: the buffer's previous store has to be read first)
+                    fence_proxy_async();
+                    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                    __syncwarp();
+                    fetch(c);
+                }
+                if (live(c)) {
+                    if (kExtra && p.extra && p.tma_extra) {
+                        ok = wait_cta(&eb[c & 1], eph[c & 1]);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        eph[c & 1] ^= 1;
+                    }
+                    uint32_t hp[EPI == kEpiGatedBwd ? 32 : 1];
+#pragma unroll
+                    for (int part = 0; part < kCols / 32; ++part) {
+                        const int64_t cp = col0 + 32 * part;
+                        const int tc = (half * kChunks + c) * kCols + 32 * part;  // accumulator column
+                        float v[32];
+                        tmem_ld32(tl + tc, (uint32_t *)v);
+                        if constexpr (!kGated) {
+                            tmem_ld_wait();
+                            pin32(v);
+                            const float ws = FP8 && p.w_scale && cp + lane < p.N ? p.w_scale[cp + lane] : 1.f;
+                            const float bs = p.bias && cp + lane < p.N ? p.bias[cp + lane] : 0.f;
+                            if (FP8 && p.w_scale) {
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) v[j] *= sx * __shfl_sync(0xffffffffu, ws, j);
+                            }
+                            if (p.bias) {
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) v[j] += __shfl_sync(0xffffffffu, bs, j);
+                            }
+                            if constexpr (EPI == kEpiLinear) {
+                                if (p.act != GDN_ACT_NONE) {
+#pragma unroll
+                                    for (int j = 0; j < 32; ++j) v[j] = act_value<kPrecise>(p.act, v[j]);
+                                }
+                                if (p.extra) {
+                                    float e[32];
+                                    row_get<TO>(b, lane, part, e);
+#pragma unroll
+                                    for (int j = 0; j < 32; ++j) v[j] += e[j];
+                                }
+                                row_put<TO>(b, lane, part, v);
+                            } else {
+                                float e[32];
+                                row_get<TO>(b, lane, part, e);
+                                const bool in = row < p.M;
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) {
+                                    float a, d;
+                                    act_both<kPrecise>(p.act, v[j], a, d);
+                                    v[j] = in ? e[j] * d : 0.f;
+                                }
+                                row_put<TO>(b, lane, part, v);
+                                if (p.colpart) {
+                                    const float s = column_sums(v, lane);
+                                    if (cp + lane < p.N) p.colpart[(row0 >> 5) * p.N + cp + lane] = s;
+                                }
+                            }
+                        } else {
+                            float u[32];
+                            tmem_ld32(tl + BN / 2 + tc, (uint32_t *)u);
+                            tmem_ld_wait();
+                            pin32(v);
+                            pin32(u);
+                            if (FP8 && p.w_scale) {
+                                const bool in = cp + lane < p.N;
+                                const float wg = in ? p.w_scale[cp + lane] : 1.f, wu = in ? p.w_scale[p.N + cp + lane] : 1.f;
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) {
+                                    v[j] *= sx * __shfl_sync(0xffffffffu, wg, j);
+                                    u[j] *= sx * __shfl_sync(0xffffffffu, wu, j);
+                                }
+                            }
+                            if constexpr (EPI == kEpiGated) {
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) v[j] = act_value<kPrecise>(p.act, v[j]) * u[j];
+                                row_put<TO>(b, lane, part, v);
+                            } else {
+                                float e[32];
+                                row_get<TO>(b, lane, part, e);
+#pragma unroll
+                                for (int j = 0; j < 32; j += 2) {
+                                    float a0, d0, a1, d1;
+                                    act_both<kPrecise>(p.act, v[j], a0, d0);
+                                    act_both<kPrecise>(p.act, v[j + 1], a1, d1);
+                                    hp[16 * part + j / 2] = pack_bf16(a0 * u[j], a1 * u[j + 1]);
+                                    v[j] = e[j] * u[j] * d0;
+                                    v[j + 1] = e[j + 1] * u[j + 1] * d1;
+                                    u[j] = e[j] * a0;
+                                    u[j + 1] = e[j + 1] * a1;
+                                }
+                                row_put<TO>(b, lane, part, v);
+                                row_put<TO>(buf[1], lane, part, u);
+                            }
+                        }
+                    }
+                    if (p.tma_out) {
+                        fence_proxy_async();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_2d(&maps.out, b, (int)col0, (int)row0);
+                            if (EPI == kEpiGatedBwd) tma_store_2d(&maps.up, buf[1], (int)col0, (int)row0);
+                            tma_store_commit();
+                        }
+                    } else {
+                        box_out<TO>(b, p.out, p.ldo, row0, col0, p.M, p.N, lane);
+                        if (EPI == kEpiGatedBwd) box_out<TO>(buf[1], (TO *)p.out + p.N, p.ldo, row0, col0, p.M, p.N, lane);
+                    }
+                    if (EPI == kEpiGatedBwd && p.out2) {
+                        if (lane == 0) tma_store_wait_read0();
+                        __syncwarp();
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            *(uint4 *)(b + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_uint4(hp[4 * j], hp[4 * j + 1], hp[4 * j + 2], hp[4 * j + 3]);
+                        if (p.tma_out2) {
+                            fence_proxy_async();
+                            __syncwarp();
+                            if (lane == 0) {
+                                tma_store_2d(&maps.out2, b, (int)col0, (int)row0);
+                                tma_store_commit();
+                            }
+                        } else {
+                            box_out<TO>(b, p.out2, p.ldo2, row0, col0, p.M, p.N, lane);
+                        }
+                    }
+                }
+            }
+            if (!ok) break;
+            // the accumulators are read: hand them back to the issuer
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) remote_arrive(leader_addr(&tempty[acc]));
+        }
+        if (lane == 0) tma_store_wait0();
+    }
+    if (!ok) {
+        // a wait ran out: give whatever is still in flight a millisecond to land before the memory is let go
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < 1000000) {}
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    if (warp == kEpiWarps + 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(G::kTmem));
+}
+
+// ------------------------------------------------------------------ host side
+PFN_cuTensorMapEncodeTiled_v12000 encoder()
+{
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        cudaDriverEntryPointQueryResult q;
+        void *p = nullptr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = (PFN_cuTensorMapEncodeTiled_v12000)p;
+    });
+    return fn;
+}
+
+size_t esz(gdn_dtype t) { return t == GDN_F32 ? 4 : t == GDN_BF16 ? 2 : 1; }
+
+// a map over `rows` rows of `cols` elements, boxes of 128 bytes x box_rows, 128-byte swizzle
+bool make_map(CUtensorMap *m, gdn_dtype t, const void *base, int64_t cols, int64_t rows, int64_t ld, int box_rows)
+{
+    const auto enc = encoder();
+    if (!enc) return false;
+    const size_t e = esz(t);
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {rows > 1 ? (cuuint64_t)ld * e : ((cuuint64_t)cols * e + 15) / 16 * 16};
+    cuuint32_t box[2] = {(cuuint32_t)(128 / e), (cuuint32_t)box_rows}, es[2] = {1, 1};
+    const CUtensorMapDataType dt = t == GDN_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : t == GDN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                   : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    return enc(m, dt, 2, const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool FP8, int LAYOUT, int EPI, int BN, typename TO>
+cudaError_t go(const GemmArgs &g, cudaStream_t st)
+{
+    constexpr bool gated = EPI == kEpiGated || EPI == kEpiGatedBwd;
+    TcMaps maps;
+    std::memset(&maps, 0, sizeof(maps));
+    const int64_t brows = gated ? 2 * g.N : g.N;
+    const bool a_ok = LAYOUT == 2 ? make_map(&maps.a, g.in, g.a, g.M, g.K, g.lda, 64) : make_map(&maps.a, g.in, g.a, g.K, g.M, g.lda, 128);
+    const bool b_ok = LAYOUT >= 1 ? make_map(&maps.b, g.in, g.b, brows, g.K, g.ldb, 64) : make_map(&maps.b, g.in, g.b, g.K, brows, g.ldb, BN / 2);
+    if (!a_ok || !b_ok) return cudaErrorInvalidValue;
+    TcParams p{};
+    p.M = g.M; p.N = g.N;
+    const int per = FP8 ? 128 : 64;
+    p.kblocks = (int)((g.K + per - 1) / per);
+    p.mt = (int)((g.M + 255) / 256);
+    p.nt = (int)((g.N + (gated ? BN / 2 : BN) - 1) / (gated ? BN / 2 : BN));
+    p.x_scale = g.x_scale; p.w_scale = g.w_scale; p.bias = g.bias; p.act = g.act;
+    p.extra = g.extra; p.ld_extra = g.ld_extra;
+    p.out = g.out; p.ldo = g.ldo; p.out2 = g.out2; p.ldo2 = g.ldo2;
+    p.colpart = g.colpart;
+    const size_t eo = sizeof(TO);
+    p.tma_out = tma_ok(g.out, g.ldo, g.M, eo) && (EPI != kEpiGatedBwd || (g.N * eo) % 16 == 0);
+    if (p.tma_out && !make_map(&maps.out, g.out_dt, g.out, g.N, g.M, g.ldo, 32)) return cudaErrorInvalidValue;
+    if (p.tma_out && EPI == kEpiGatedBwd && !make_map(&maps.up, g.out_dt, (const TO *)g.out + g.N, g.N, g.M, g.ldo, 32))
+        return cudaErrorInvalidValue;
+    p.tma_extra = g.extra && tma_ok(g.extra, g.ld_extra, g.M, eo);
+    if (p.tma_extra && !make_map(&maps.extra, g.out_dt, g.extra, g.N, g.M, g.ld_extra, 32)) return cudaErrorInvalidValue;
+    p.tma_out2 = g.out2 && tma_ok(g.out2, g.ldo2, g.M, eo);
+    if (p.tma_out2 && !make_map(&maps.out2, g.out_dt, g.out2, g.N, g.M, g.ldo2, 32)) return cudaErrorInvalidValue;
+
+    auto *kern = gemm_tc_kernel<FP8, LAYOUT, EPI, BN, TO>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<BN>::kSmem);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = (int64_t)p.mt * p.nt;
+    const int pairs = (int)(tiles < device_sm_count() / 2 ? tiles : device_sm_count() / 2);
+    kern<<<2 * pairs, kThreads, Geo<BN>::kSmem, st>>>(maps, p);
+    return cudaGetLastError();
+}
+
+template <bool FP8, int LAYOUT, int EPI, typename TO>
+cudaError_t pick(const GemmArgs &g, cudaStream_t st)
+{
+    return go<FP8, LAYOUT, EPI, 256, TO>(g, st);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) repack_kernel(const T *src, int64_t ld, int64_t rows, int64_t cols, T *dst, int64_t pitch)
+{
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+        for (int64_t c = threadIdx.x; c < cols; c += 256) dst[r * pitch + c] = src[r * ld + c];
+}
+
+}  // namespace
+
+bool tma_ok(const void *p, int64_t ld, int64_t rows, size_t e)
+{
+    return ((uintptr_t)p & 15) == 0 && (rows <= 1 || (size_t)ld * e % 16 == 0);
+}
+
+cudaError_t launch_repack(const void *src, gdn_dtype t, int64_t ld, int64_t rows, int64_t cols, void *dst, int64_t pitch, cudaStream_t st)
+{
+    const unsigned grid = (unsigned)(rows < 4096 ? rows : 4096);
+    if (t == GDN_BF16) repack_kernel<<<grid, 256, 0, st>>>((const uint16_t *)src, ld, rows, cols, (uint16_t *)dst, pitch);
+    else repack_kernel<<<grid, 256, 0, st>>>((const uint8_t *)src, ld, rows, cols, (uint8_t *)dst, pitch);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_gemm_tc(const GemmArgs &g, Epi epi, cudaStream_t st)
+{
+    if (g.M <= 0 || g.N <= 0) return cudaSuccess;
+    const bool f32 = g.out_dt == GDN_F32;
+    if (g.in == GDN_E4M3) {
+        if (epi == kEpiGated) return pick<true, 0, kEpiGated, __nv_bfloat16>(g, st);
+        return f32 ? pick<true, 0, kEpiLinear, float>(g, st) : pick<true, 0, kEpiLinear, __nv_bfloat16>(g, st);
+    }
+    switch (epi) {
+    case kEpiGated: return pick<false, 0, kEpiGated, __nv_bfloat16>(g, st);
+    case kEpiGatedBwd: return pick<false, 0, kEpiGatedBwd, __nv_bfloat16>(g, st);
+    case kEpiDact: return pick<false, 0, kEpiDact, __nv_bfloat16>(g, st);
+    default: break;
+    }
+    if (g.a_t) return pick<false, 2, kEpiLinear, __nv_bfloat16>(g, st);
+    if (g.b_t) return pick<false, 1, kEpiLinear, __nv_bfloat16>(g, st);
+    return f32 ? pick<false, 0, kEpiLinear, float>(g, st) : pick<false, 0, kEpiLinear, __nv_bfloat16>(g, st);
+}
+
+gdn_status read_tc_status(cudaStream_t st)
+{
+    unsigned word = 0, zero = 0;
+    if (cudaMemcpyFromSymbolAsync(&word, g_tc_status, sizeof(word), 0, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+        cudaMemcpyToSymbolAsync(g_tc_status, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, st) != cudaSuccess ||
+        cudaStreamSynchronize(st) != cudaSuccess)
+        return GDN_ERR_CUDA;
+    return word & kStatusTimeout ? GDN_ERR_TIMEOUT : GDN_OK;
+}
+
+}  // namespace gdn

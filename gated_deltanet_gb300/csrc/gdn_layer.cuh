@@ -100,6 +100,13 @@ struct GemmArgs {
     float *colpart;                  // kEpiDact: [ceil(M / 32)][N], nullable
 };
 
+// bf16 and e4m3 operands whose rows start on 16-byte boundaries (tma_ok); output types as gdn_linear allows
+cudaError_t launch_gemm_tc(const GemmArgs &g, Epi epi, cudaStream_t st);
+bool tma_ok(const void *p, int64_t ld, int64_t rows, size_t esz);
+// copies rows into a layout of `pitch` elements per row
+cudaError_t launch_repack(const void *src, gdn_dtype t, int64_t ld, int64_t rows, int64_t cols, void *dst, int64_t pitch, cudaStream_t st);
+gdn_status read_tc_status(cudaStream_t st);  // synchronises; clears
+
 cudaError_t launch_gemm_simt(const GemmArgs &g, Epi epi, cudaStream_t st);
 
 // out[n] = sum over `parts` rows of part[.][N] (a fixed order: the same sum every time)

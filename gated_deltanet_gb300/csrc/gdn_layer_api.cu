@@ -86,8 +86,38 @@ struct Carve {  // offsets into a workspace
     }
 };
 
-// A product as it will be launched: its workspace follows `base`
-cudaError_t launch_product(const GemmArgs &g, Epi epi, cudaStream_t st) { return launch_gemm_simt(g, epi, st); }
+// fp32 on the CUDA cores, bf16 and e4m3 on the tensor cores
+cudaError_t launch_product(const GemmArgs &g, Epi epi, cudaStream_t st)
+{
+    return g.in == GDN_F32 ? launch_gemm_simt(g, epi, st) : launch_gemm_tc(g, epi, st);
+}
+
+// An operand of the tensor cores: as it is, or, where its rows do not start on 16-byte boundaries, as a padded
+// copy in the workspace (one more read and write of it; its odd rows could only be loaded element by element)
+struct Operand {
+    const void *p;
+    int64_t ld, rows, cols;
+    bool copy;
+    size_t off;
+    void plan(const void *ptr, int64_t stride, int64_t r, int64_t c, gdn_dtype t, Carve &ws)
+    {
+        p = ptr; ld = stride; rows = r; cols = c;
+        copy = t != GDN_F32 && r > 0 && !tma_ok(ptr, stride, r, esize(t));
+        off = 0;
+        if (copy) {
+            const int64_t q = 16 / (int64_t)esize(t);
+            ld = (c + q - 1) / q * q;
+            off = ws.take((size_t)r * ld * esize(t));
+        }
+    }
+    cudaError_t make(int64_t stride, gdn_dtype t, char *base, cudaStream_t st)
+    {
+        if (!copy) return cudaSuccess;
+        const void *src = p;
+        p = base + off;
+        return launch_repack(src, t, stride, rows, cols, base + off, ld, st);
+    }
+};
 
 gdn_status check_linear(const gdn_linear_args *a, bool gated, bool backward)
 {
@@ -137,25 +167,50 @@ GemmArgs forward_product(const gdn_linear_args *a)
     return g;
 }
 
-// The backward calls' own workspace: dz (rows padded to 16 bytes) and the column sums of groups of 32 rows
-struct BwdPlan {
+// A call's workspace: padded copies of operands; backward: dz (its rows padded to 16 bytes) and the column sums
+// of groups of 32 rows
+struct LinearPlan {
+    Operand x, w, dy;
     int64_t dz_cols, dz_ld, parts;
     size_t off_dz, off_part, bytes;
     bool own_dz;
 };
-BwdPlan plan_bwd(const gdn_linear_args *a, bool gated)
+LinearPlan plan_linear(const gdn_linear_args *a, bool gated, bool backward)
 {
-    BwdPlan p{};
-    p.dz_cols = gated ? 2 * (int64_t)a->out_features : a->out_features;
-    const int64_t q = 16 / (int64_t)esize(a->dtype);
-    p.own_dz = gated || a->act != GDN_ACT_NONE;
-    p.dz_ld = p.own_dz ? (p.dz_cols + q - 1) / q * q : a->ld_dy;
-    p.parts = (a->rows + 31) / 32;
+    LinearPlan p{};
     Carve c;
-    p.off_dz = c.take(p.own_dz ? (size_t)a->rows * p.dz_ld * esize(a->dtype) : 0);
-    p.off_part = c.take(a->dbias ? (size_t)p.parts * a->out_features * sizeof(float) : 0);
+    const int64_t wrows = (gated ? 2 : 1) * (int64_t)a->out_features;
+    p.x.plan(a->x, a->ldx, a->rows, a->in_features, a->dtype, c);
+    p.w.plan(a->w, a->ldw, a->rows > 0 ? wrows : 0, a->in_features, a->dtype, c);
+    if (backward) {
+        const int64_t q = 16 / (int64_t)esize(a->dtype);
+        p.dz_cols = wrows;
+        p.own_dz = gated || a->act != GDN_ACT_NONE;
+        p.parts = (a->rows + 31) / 32;
+        if (p.own_dz) {
+            p.dz_ld = (p.dz_cols + q - 1) / q * q;
+            p.off_dz = c.take((size_t)a->rows * p.dz_ld * esize(a->dtype));
+        } else {
+            p.dy.plan(a->dy, a->ld_dy, a->rows, a->out_features, a->dtype, c);
+            p.dz_ld = p.dy.ld;
+        }
+        p.off_part = c.take(a->dbias ? (size_t)p.parts * a->out_features * sizeof(float) : 0);
+    }
     p.bytes = c.at;
     return p;
+}
+
+GemmArgs forward_product(const gdn_linear_args *a, const LinearPlan &p)
+{
+    GemmArgs g{};
+    g.M = a->rows; g.N = a->out_features; g.K = a->in_features;
+    g.in = a->dtype; g.out_dt = a->out_dtype;
+    g.a = p.x.p; g.lda = p.x.ld;
+    g.b = p.w.p; g.ldb = p.w.ld;
+    g.x_scale = a->x_scale; g.w_scale = a->w_scale;
+    g.bias = a->bias;
+    g.act = a->act;
+    return g;
 }
 
 gdn_status run_bwd(const gdn_linear_args *a, bool gated, void *ws, size_t ws_bytes, cudaStream_t st)
@@ -163,7 +218,7 @@ gdn_status run_bwd(const gdn_linear_args *a, bool gated, void *ws, size_t ws_byt
     gdn_status s = check_linear(a, gated, true);
     if (s != GDN_OK) return s;
     const int64_t M = a->rows, N = a->out_features, K = a->in_features;
-    const BwdPlan p = plan_bwd(a, gated);
+    LinearPlan p = plan_linear(a, gated, true);
     if (M == 0) {
         if (a->dw && cudaMemsetAsync(a->dw, 0, (size_t)p.dz_cols * K * esize(a->dtype), st) != cudaSuccess)
             return GDN_ERR_CUDA;
@@ -172,10 +227,12 @@ gdn_status run_bwd(const gdn_linear_args *a, bool gated, void *ws, size_t ws_byt
     }
     char *base = nullptr;
     if ((s = take_workspace(p.bytes, ws, ws_bytes, st, &base)) != GDN_OK) return s;
-    const void *dz = a->dy;
+    if (p.x.make(a->ldx, a->dtype, base, st) != cudaSuccess || p.w.make(a->ldw, a->dtype, base, st) != cudaSuccess)
+        return GDN_ERR_CUDA;
     float *part = a->dbias ? (float *)(base + p.off_part) : nullptr;
+    const void *dz;
     if (p.own_dz) {
-        GemmArgs g = forward_product(a);
+        GemmArgs g = forward_product(a, p);
         g.extra = a->dy; g.ld_extra = a->ld_dy;
         g.out = base + p.off_dz; g.ldo = p.dz_ld;
         g.out2 = gated ? a->y : nullptr;
@@ -183,8 +240,10 @@ gdn_status run_bwd(const gdn_linear_args *a, bool gated, void *ws, size_t ws_byt
         g.colpart = part;
         dz = g.out;
         if (launch_product(g, gated ? kEpiGatedBwd : kEpiDact, st) != cudaSuccess) return GDN_ERR_CUDA;
-    } else if (part && launch_colsum_rows(a->dy, a->dtype, M, N, a->ld_dy, part, st) != cudaSuccess) {
-        return GDN_ERR_CUDA;
+    } else {
+        if (p.dy.make(a->ld_dy, a->dtype, base, st) != cudaSuccess) return GDN_ERR_CUDA;
+        dz = p.dy.p;
+        if (part && launch_colsum_rows(dz, a->dtype, M, N, p.dz_ld, part, st) != cudaSuccess) return GDN_ERR_CUDA;
     }
     if (part && launch_colsum_finish(part, p.parts, N, a->dbias, st) != cudaSuccess) return GDN_ERR_CUDA;
     GemmArgs g{};
@@ -195,7 +254,7 @@ gdn_status run_bwd(const gdn_linear_args *a, bool gated, void *ws, size_t ws_byt
     if (a->dx) {  // dx[m][k] = sum_n dz[m][n] w[n][k]
         GemmArgs d = g;
         d.M = M; d.N = K; d.K = p.dz_cols;
-        d.b = a->w; d.ldb = a->ldw;
+        d.b = p.w.p; d.ldb = p.w.ld;
         d.out = a->dx; d.ldo = K;
         if (launch_product(d, kEpiLinear, st) != cudaSuccess) return GDN_ERR_CUDA;
     }
@@ -203,7 +262,7 @@ gdn_status run_bwd(const gdn_linear_args *a, bool gated, void *ws, size_t ws_byt
         GemmArgs d = g;
         d.M = p.dz_cols; d.N = K; d.K = M;
         d.a_t = 1;
-        d.b = a->x; d.ldb = a->ldx;
+        d.b = p.x.p; d.ldb = p.x.ld;
         d.out = a->dw; d.ldo = K;
         if (launch_product(d, kEpiLinear, st) != cudaSuccess) return GDN_ERR_CUDA;
     }
@@ -215,11 +274,20 @@ gdn_status run_fwd(const gdn_linear_args *a, bool gated, void *ws, size_t ws_byt
     gdn_status s = check_linear(a, gated, false);
     if (s != GDN_OK) return s;
     if (a->rows == 0) return GDN_OK;
-    GemmArgs g = forward_product(a);
+    LinearPlan p = plan_linear(a, gated, false);
+    char *base = nullptr;
+    if ((s = take_workspace(p.bytes, ws, ws_bytes, st, &base)) != GDN_OK) return s;
+    if (p.x.make(a->ldx, a->dtype, base, st) != cudaSuccess || p.w.make(a->ldw, a->dtype, base, st) != cudaSuccess)
+        return GDN_ERR_CUDA;
+    GemmArgs g = forward_product(a, p);
     g.extra = a->residual; g.ld_extra = a->ld_residual;
     g.out = a->y; g.ldo = a->ldy;
-    (void)ws; (void)ws_bytes;
     return launch_product(g, gated ? kEpiGated : kEpiLinear, st) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+size_t linear_workspace(const gdn_linear_args *a, bool gated, bool backward)
+{
+    return check_linear(a, gated, backward) == GDN_OK ? plan_linear(a, gated, backward).bytes : 0;
 }
 
 }  // namespace
@@ -274,7 +342,7 @@ gdn_status gdn_rms_norm_bwd(const gdn_norm_args *a, void *workspace, size_t ws_b
 
 size_t gdn_linear_workspace_size(const gdn_linear_args *a)
 {
-    return check_linear(a, false, false) == GDN_OK ? 0 : 0;
+    return linear_workspace(a, false, false);
 }
 
 gdn_status gdn_linear(const gdn_linear_args *a, void *workspace, size_t ws_bytes, gdn_stream_t stream)
@@ -284,7 +352,7 @@ gdn_status gdn_linear(const gdn_linear_args *a, void *workspace, size_t ws_bytes
 
 size_t gdn_linear_bwd_workspace_size(const gdn_linear_args *a)
 {
-    return check_linear(a, false, true) == GDN_OK ? plan_bwd(a, false).bytes : 0;
+    return linear_workspace(a, false, true);
 }
 
 gdn_status gdn_linear_bwd(const gdn_linear_args *a, void *workspace, size_t ws_bytes, gdn_stream_t stream)
@@ -294,7 +362,7 @@ gdn_status gdn_linear_bwd(const gdn_linear_args *a, void *workspace, size_t ws_b
 
 size_t gdn_gated_linear_workspace_size(const gdn_linear_args *a)
 {
-    return check_linear(a, true, false) == GDN_OK ? 0 : 0;
+    return linear_workspace(a, true, false);
 }
 
 gdn_status gdn_gated_linear(const gdn_linear_args *a, void *workspace, size_t ws_bytes, gdn_stream_t stream)
@@ -304,7 +372,7 @@ gdn_status gdn_gated_linear(const gdn_linear_args *a, void *workspace, size_t ws
 
 size_t gdn_gated_linear_bwd_workspace_size(const gdn_linear_args *a)
 {
-    return check_linear(a, true, true) == GDN_OK ? plan_bwd(a, true).bytes : 0;
+    return linear_workspace(a, true, true);
 }
 
 gdn_status gdn_gated_linear_bwd(const gdn_linear_args *a, void *workspace, size_t ws_bytes, gdn_stream_t stream)
@@ -314,7 +382,7 @@ gdn_status gdn_gated_linear_bwd(const gdn_linear_args *a, void *workspace, size_
 
 gdn_status gdn_read_layer_status(gdn_stream_t stream)
 {
-    return cudaStreamSynchronize((cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    return read_tc_status((cudaStream_t)stream);
 }
 
 }  // extern "C"
