@@ -14,7 +14,6 @@ __global__ void __launch_bounds__(256) gemm_simt_kernel(GemmArgs g)
 {
     constexpr bool kTwo = EPI == kEpiGated || EPI == kEpiGatedBwd;
     constexpr int kB = kTwo ? 2 : 1;
-    constexpr bool kPrecise = true;
     __shared__ float sa[kKt][kT + 4], sb[kB][kKt][kT + 4];
     __shared__ float cs[16][kT];
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
@@ -55,42 +54,45 @@ __global__ void __launch_bounds__(256) gemm_simt_kernel(GemmArgs g)
     float *out = (float *)g.out;
     const float *extra = (const float *)g.extra;
     float col[4] = {};
+    with_act(g.act, [&](auto tag) {
+        constexpr int ACT = decltype(tag)::value;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t m = m0 + 4 * ty + i;
-        if (m >= g.M) continue;
+        for (int i = 0; i < 4; ++i) {
+            const int64_t m = m0 + 4 * ty + i;
+            if (m >= g.M) continue;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t n = n0 + 4 * tx + j;
-            if (n >= g.N) continue;
-            float z = acc[0][i][j];
-            if (EPI == kEpiLinear) {
-                if (g.bias) z += g.bias[n];
-                z = act_value<kPrecise>(g.act, z);
-                if (extra) z += extra[m * g.ld_extra + n];
-                out[m * g.ldo + n] = z;
-            } else if (EPI == kEpiDact) {
-                if (g.bias) z += g.bias[n];
-                float v, d;
-                act_both<kPrecise>(g.act, z, v, d);
-                const float dz = extra[m * g.ld_extra + n] * d;
-                out[m * g.ldo + n] = dz;
-                col[j] += dz;
-            } else {
-                const float u = acc[kB - 1][i][j];
-                if (EPI == kEpiGated) {
-                    out[m * g.ldo + n] = act_value<kPrecise>(g.act, z) * u;
-                } else {
+            for (int j = 0; j < 4; ++j) {
+                const int64_t n = n0 + 4 * tx + j;
+                if (n >= g.N) continue;
+                float z = acc[0][i][j];
+                if (EPI == kEpiLinear) {
+                    if (g.bias) z += g.bias[n];
+                    z = act_value<true, ACT>(z);
+                    if (extra) z += extra[m * g.ld_extra + n];
+                    out[m * g.ldo + n] = z;
+                } else if (EPI == kEpiDact) {
+                    if (g.bias) z += g.bias[n];
                     float v, d;
-                    act_both<kPrecise>(g.act, z, v, d);
-                    const float dh = extra[m * g.ld_extra + n];
-                    out[m * g.ldo + n] = dh * u * d;
-                    out[m * g.ldo + g.N + n] = dh * v;
-                    if (g.out2) ((float *)g.out2)[m * g.ldo2 + n] = v * u;
+                    act_both<true, ACT>(z, v, d);
+                    const float dz = extra[m * g.ld_extra + n] * d;
+                    out[m * g.ldo + n] = dz;
+                    col[j] += dz;
+                } else {
+                    const float u = acc[kB - 1][i][j];
+                    if (EPI == kEpiGated) {
+                        out[m * g.ldo + n] = act_value<true, ACT>(z) * u;
+                    } else {
+                        float v, d;
+                        act_both<true, ACT>(z, v, d);
+                        const float dh = extra[m * g.ld_extra + n];
+                        out[m * g.ldo + n] = dh * u * d;
+                        out[m * g.ldo + g.N + n] = dh * v;
+                        if (g.out2) ((float *)g.out2)[m * g.ldo2 + n] = v * u;
+                    }
                 }
             }
         }
-    }
+    });
     if (EPI == kEpiDact && g.colpart) {
         // this tile's column sums over its two groups of 32 rows
 #pragma unroll

@@ -36,10 +36,10 @@ constexpr int kStageBuf = 32 * 128;      // one epilogue box: 32 rows of 128 byt
 template <int BN> struct Geo {
     static constexpr int kB = BN / 2 * 128;
     static constexpr int kStage = kABytes + kB;
-    static constexpr int kStages = BN == 256 ? 5 : 6;
+    static constexpr int kStages = BN == 256 ? 6 : 8;
     static constexpr int kTmem = 2 * BN;  // two accumulators
-    static constexpr int kBars = 2 * kStages + 4 + 2 * kEpiWarps;
-    static constexpr int kSmem = 1024 + kStages * kStage + kEpiWarps * 2 * kStageBuf + kBars * 8 + 16;
+    static constexpr int kBars = 2 * kStages + 4 + kEpiWarps;
+    static constexpr int kSmem = 1024 + kStages * kStage + kEpiWarps * kStageBuf + kBars * 8 + 16;
 };
 static_assert(Geo<256>::kSmem <= 227 * 1024 && Geo<128>::kSmem <= 227 * 1024, "shared memory budget");
 
@@ -237,9 +237,9 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *boxes = sm + G::kStages * G::kStage;
-    uint64_t *full = (uint64_t *)(boxes + kEpiWarps * 2 * kStageBuf);
+    uint64_t *full = (uint64_t *)(boxes + kEpiWarps * kStageBuf);
     uint64_t *empty = full + G::kStages, *tfull = empty + G::kStages, *tempty = tfull + 2, *ebar = tempty + 2;
-    uint32_t *tslot = (uint32_t *)(ebar + 2 * kEpiWarps);
+    uint32_t *tslot = (uint32_t *)(ebar + kEpiWarps);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_rank();
     const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
@@ -254,7 +254,7 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
             mbar_init(&tfull[i], 1);
             mbar_init(&tempty[i], 2 * kEpiWarps);
         }
-        for (int i = 0; i < 2 * kEpiWarps; ++i) mbar_init(&ebar[i], 1);
+        for (int i = 0; i < kEpiWarps; ++i) mbar_init(&ebar[i], 1);
         fence_mbar_init();
     }
     if (warp == kEpiWarps + 1) {
@@ -277,16 +277,15 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
 
     if (warp == kEpiWarps) {
         // ---------------------------------------------------------------- loads
-        if (lane == 0) {
-            uint32_t it = 0;
-            for (int t = pair; t < tiles && ok; t += pairs) {
-                int mi, ni;
-                place(t, mi, ni);
-                const int m0 = mi * 256 + (int)rank * 128;
-                const int n0 = kGated ? (rank ? (int)p.N : 0) + ni * kOutN : ni * BN + (int)rank * (BN / 2);
-                for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
-                    const int s = it % G::kStages;
-                    if (!(ok = wait_cta(&empty[s], ((it / G::kStages) & 1) ^ 1))) break;
+        uint32_t s = 0, ph = 1;
+        for (int t = pair; t < tiles && ok; t += pairs) {
+            int mi, ni;
+            place(t, mi, ni);
+            const int m0 = mi * 256 + (int)rank * 128;
+            const int n0 = kGated ? (rank ? (int)p.N : 0) + ni * kOutN : ni * BN + (int)rank * (BN / 2);
+            for (int kb = 0; kb < p.kblocks; ++kb) {
+                if (!(ok = __all_sync(0xffffffffu, wait_cta(&empty[s], ph)))) break;
+                if (elect_one_sync()) {
                     uint8_t *sa = sm + s * G::kStage, *sb = sa + kABytes;
                     if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * G::kStage);
                     const uint32_t bar = leader_addr(&full[s]);
@@ -304,44 +303,61 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
                         pair_load(sb, &maps.b, k0, n0, bar);
                     }
                 }
+                __syncwarp();
+                if (++s == G::kStages) { s = 0; ph ^= 1; }
             }
-            // the last products have read every stage before the CTAs of the pair may leave
-            for (int i = 0; i < G::kStages && ok; ++i, ++it) ok = wait_cta(&empty[it % G::kStages], ((it / G::kStages) & 1) ^ 1);
+        }
+        // the last products have read every stage before the CTAs of the pair may leave
+        for (int i = 0; i < G::kStages && ok; ++i) {
+            ok = __all_sync(0xffffffffu, wait_cta(&empty[s], ph));
+            if (++s == G::kStages) { s = 0; ph ^= 1; }
         }
     } else if (warp == kEpiWarps + 1) {
         // ---------------------------------------------------------------- products
-        if (rank == 0 && lane == 0) {
+        if (rank == 0) {
+            // (the whole warp follows the loop, so that its bookkeeping stays uniform; one elected lane issues)
             constexpr uint32_t id = FP8 ? (1u << 4) | ((uint32_t)(BN >> 3) << 17) | (16u << 24)
                                         : idesc_bf16_f32(256, BN, LAYOUT == 2, LAYOUT >= 1);
             constexpr uint32_t sa_step = LAYOUT == 2 ? 128 : 2, sb_step = LAYOUT >= 1 ? 128 : 2;
-            uint32_t it = 0, n = 0;
+            const uint32_t base = smem_u32(sm);
+            const uint64_t da0 = sdesc_sw128(base, LAYOUT == 2 ? 8192 : 16, 1024);
+            const uint64_t db0 = sdesc_sw128(base + kABytes, LAYOUT >= 1 ? 8192 : 16, 1024);
+            uint32_t s = 0, ph = 0, n = 0;
             for (int t = pair; t < tiles && ok; t += pairs, ++n) {
                 const uint32_t acc = n & 1;
-                if (!(ok = wait_cluster(&tempty[acc], ((n >> 1) & 1) ^ 1))) break;
+                if (!(ok = __all_sync(0xffffffffu, wait_cluster(&tempty[acc], ((n >> 1) & 1) ^ 1)))) break;
                 tc_fence_after();
-                for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
-                    const int s = it % G::kStages;
-                    if (!(ok = wait_cluster(&full[s], (it / G::kStages) & 1))) break;
+                for (int kb = 0; kb < p.kblocks; ++kb) {
+                    if (!(ok = __all_sync(0xffffffffu, wait_cluster(&full[s], ph)))) break;
                     tc_fence_after();
-                    const uint32_t a = smem_u32(sm + s * G::kStage);
-                    const uint64_t da = sdesc_sw128(a, LAYOUT == 2 ? 8192 : 16, 1024);
-                    const uint64_t db = sdesc_sw128(a + kABytes, LAYOUT >= 1 ? 8192 : 16, 1024);
+                    const uint64_t da = da0 + s * (G::kStage >> 4), db = db0 + s * (G::kStage >> 4);
+                    uint64_t *const rel = &empty[s];
+                    if (++s == G::kStages) { s = 0; ph ^= 1; }
+                    if (elect_one_sync()) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        pair_mma<FP8>(tmem + acc * BN, da + j * sa_step, db + j * sb_step, id, (kb | j) != 0);
-                    pair_commit(&empty[s]);
+                        for (int j = 0; j < 4; ++j)
+                            pair_mma<FP8>(tmem + acc * BN, da + j * sa_step, db + j * sb_step, id, (kb | j) != 0);
+                        pair_commit(rel);
+                        if (kb + 1 == p.kblocks) pair_commit(&tfull[acc]);
+                    }
+                    __syncwarp();
                 }
-                if (ok) pair_commit(&tfull[acc]);
             }
         }
     } else {
         // ---------------------------------------------------------------- epilogue
         constexpr int kCols = Box<TO>::kCols;
         const int q = warp & 3, half = warp >> 2;
-        constexpr int kChunks = kOutN / kCols / 2;  // boxes of this warp (its half of the columns)
-        uint8_t *buf[2] = {boxes + warp * 2 * kStageBuf, boxes + warp * 2 * kStageBuf + kStageBuf};
-        uint64_t *eb = ebar + 2 * warp;
-        uint32_t n = 0, eph[2] = {0, 0};
+        constexpr int kChunks = kOutN / kCols / 2;  // boxes of this warp (its half of the columns), one at a time
+        uint8_t *buf = boxes + warp * kStageBuf;
+        uint64_t *eb = ebar + warp;
+        uint32_t n = 0, eph = 0;
+        // the box is free again, for copies by either path
+        auto box_free = [&] {
+            fence_proxy_async();
+            if (lane == 0) tma_store_wait_read0();
+            __syncwarp();
+        };
         for (int t = pair; t < tiles && ok; t += pairs, ++n) {
             int mi, ni;
             place(t, mi, ni);
@@ -355,19 +371,28 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
                 if (!kExtra || !p.extra || !live(c)) return;
                 if (p.tma_extra) {
                     if (lane == 0) {
-                        mbar_arrive_expect_tx(&eb[c & 1], kStageBuf);
-                        tma_load_2d(buf[c & 1], &maps.extra, (int)col_of(c), (int)row0, &eb[c & 1]);
+                        mbar_arrive_expect_tx(eb, kStageBuf);
+                        tma_load_2d(buf, &maps.extra, (int)col_of(c), (int)row0, eb);
                     }
                 } else {
-                    box_in<TO>(buf[c & 1], p.extra, p.ld_extra, row0, col_of(c), p.M, p.N, lane);
+                    box_in<TO>(buf, p.extra, p.ld_extra, row0, col_of(c), p.M, p.N, lane);
                 }
             };
-            // both buffers free again, for copies by either path
-            fence_proxy_async();
-            if (lane == 0) tma_store_wait_read0();
-            __syncwarp();
-            fetch(0);
-            if (kChunks > 1 && EPI != kEpiGatedBwd) fetch(1);
+            // the finished box to its place: columns col0 ..., of an output with its own map
+            auto store = [&](const CUtensorMap *map, int tma, void *dst, int64_t ld, int64_t col0) {
+                if (tma) {
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_2d(map, buf, (int)col0, (int)row0);
+                        tma_store_commit();
+                    }
+                } else {
+                    box_out<TO>(buf, dst, ld, row0, col0, p.M, p.N, lane);
+                }
+            };
+            box_free();
+            fetch(0);  // under the tile's products
             const float sx = FP8 && p.x_scale && row < p.M ? p.x_scale[row] : 1.f;
             ok = wait_cluster(&tfull[acc], (n >> 1) & 1);
             ok = __all_sync(0xffffffffu, ok);
@@ -376,135 +401,119 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) {
                 const int64_t col0 = col_of(c);
-                uint8_t *b = buf[c & 1];
-                if (c >= 2) {  // (four boxes of fp32: the buffer's previous store has to be read first)
-                    fence_proxy_async();
-                    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-                    __syncwarp();
+                if (c > 0) {
+                    box_free();
                     fetch(c);
                 }
-                if (live(c)) {
-                    if (kExtra && p.extra && p.tma_extra) {
-                        ok = wait_cta(&eb[c & 1], eph[c & 1]);
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (!ok) break;
-                        eph[c & 1] ^= 1;
-                    }
-                    uint32_t hp[EPI == kEpiGatedBwd ? 32 : 1];
+                if (!live(c)) continue;
+                if (kExtra && p.extra && p.tma_extra) {
+                    ok = wait_cta(eb, eph);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    eph ^= 1;
+                }
+                uint32_t up[EPI == kEpiGatedBwd ? 32 : 1], hp[EPI == kEpiGatedBwd ? 32 : 1];
 #pragma unroll
-                    for (int part = 0; part < kCols / 32; ++part) {
-                        const int64_t cp = col0 + 32 * part;
-                        const int tc = (half * kChunks + c) * kCols + 32 * part;  // accumulator column
-                        float v[32];
-                        tmem_ld32(tl + tc, (uint32_t *)v);
-                        if constexpr (!kGated) {
-                            tmem_ld_wait();
-                            pin32(v);
-                            const float ws = FP8 && p.w_scale && cp + lane < p.N ? p.w_scale[cp + lane] : 1.f;
-                            const float bs = p.bias && cp + lane < p.N ? p.bias[cp + lane] : 0.f;
-                            if (FP8 && p.w_scale) {
+                for (int part = 0; part < kCols / 32; ++part) {
+                    const int64_t cp = col0 + 32 * part;
+                    const int tc = (half * kChunks + c) * kCols + 32 * part;  // accumulator column
+                    float v[32];
+                    tmem_ld32(tl + tc, (uint32_t *)v);
+                    if constexpr (!kGated) {
+                        tmem_ld_wait();
+                        pin32(v);
+                        if (FP8 && p.w_scale) {
+                            const float ws = cp + lane < p.N ? p.w_scale[cp + lane] : 1.f;
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) v[j] *= sx * __shfl_sync(0xffffffffu, ws, j);
-                            }
-                            if (p.bias) {
+                            for (int j = 0; j < 32; ++j) v[j] *= sx * __shfl_sync(0xffffffffu, ws, j);
+                        }
+                        if (p.bias) {
+                            const float bs = cp + lane < p.N ? p.bias[cp + lane] : 0.f;
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) v[j] += __shfl_sync(0xffffffffu, bs, j);
-                            }
-                            if constexpr (EPI == kEpiLinear) {
-                                if (p.act != GDN_ACT_NONE) {
+                            for (int j = 0; j < 32; ++j) v[j] += __shfl_sync(0xffffffffu, bs, j);
+                        }
+                        if constexpr (EPI == kEpiLinear) {
+                            if (p.act != GDN_ACT_NONE)
+                                with_act(p.act, [&](auto tag) {
 #pragma unroll
-                                    for (int j = 0; j < 32; ++j) v[j] = act_value<kPrecise>(p.act, v[j]);
-                                }
-                                if (p.extra) {
-                                    float e[32];
-                                    row_get<TO>(b, lane, part, e);
-#pragma unroll
-                                    for (int j = 0; j < 32; ++j) v[j] += e[j];
-                                }
-                                row_put<TO>(b, lane, part, v);
-                            } else {
+                                    for (int j = 0; j < 32; ++j) v[j] = act_value<kPrecise, decltype(tag)::value>(v[j]);
+                                });
+                            if (p.extra) {
                                 float e[32];
-                                row_get<TO>(b, lane, part, e);
-                                const bool in = row < p.M;
+                                row_get<TO>(buf, lane, part, e);
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) v[j] += e[j];
+                            }
+                            row_put<TO>(buf, lane, part, v);
+                        } else {
+                            float e[32];
+                            row_get<TO>(buf, lane, part, e);
+                            const bool in = row < p.M;
+                            with_act(p.act, [&](auto tag) {
 #pragma unroll
                                 for (int j = 0; j < 32; ++j) {
                                     float a, d;
-                                    act_both<kPrecise>(p.act, v[j], a, d);
+                                    act_both<kPrecise, decltype(tag)::value>(v[j], a, d);
                                     v[j] = in ? e[j] * d : 0.f;
                                 }
-                                row_put<TO>(b, lane, part, v);
-                                if (p.colpart) {
-                                    const float s = column_sums(v, lane);
-                                    if (cp + lane < p.N) p.colpart[(row0 >> 5) * p.N + cp + lane] = s;
-                                }
+                            });
+                            row_put<TO>(buf, lane, part, v);
+                            if (p.colpart) {
+                                const float s = column_sums(v, lane);
+                                if (cp + lane < p.N) p.colpart[(row0 >> 5) * p.N + cp + lane] = s;
                             }
+                        }
+                    } else {
+                        float u[32];
+                        tmem_ld32(tl + BN / 2 + tc, (uint32_t *)u);
+                        tmem_ld_wait();
+                        pin32(v);
+                        pin32(u);
+                        if (FP8 && p.w_scale) {
+                            const bool in = cp + lane < p.N;
+                            const float wg = in ? p.w_scale[cp + lane] : 1.f, wu = in ? p.w_scale[p.N + cp + lane] : 1.f;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) {
+                                v[j] *= sx * __shfl_sync(0xffffffffu, wg, j);
+                                u[j] *= sx * __shfl_sync(0xffffffffu, wu, j);
+                            }
+                        }
+                        if constexpr (EPI == kEpiGated) {
+                            with_act(p.act, [&](auto tag) {
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) v[j] = act_value<kPrecise, decltype(tag)::value>(v[j]) * u[j];
+                            });
+                            row_put<TO>(buf, lane, part, v);
                         } else {
-                            float u[32];
-                            tmem_ld32(tl + BN / 2 + tc, (uint32_t *)u);
-                            tmem_ld_wait();
-                            pin32(v);
-                            pin32(u);
-                            if (FP8 && p.w_scale) {
-                                const bool in = cp + lane < p.N;
-                                const float wg = in ? p.w_scale[cp + lane] : 1.f, wu = in ? p.w_scale[p.N + cp + lane] : 1.f;
-#pragma unroll
-                                for (int j = 0; j < 32; ++j) {
-                                    v[j] *= sx * __shfl_sync(0xffffffffu, wg, j);
-                                    u[j] *= sx * __shfl_sync(0xffffffffu, wu, j);
-                                }
-                            }
-                            if constexpr (EPI == kEpiGated) {
-#pragma unroll
-                                for (int j = 0; j < 32; ++j) v[j] = act_value<kPrecise>(p.act, v[j]) * u[j];
-                                row_put<TO>(b, lane, part, v);
-                            } else {
-                                float e[32];
-                                row_get<TO>(b, lane, part, e);
+                            float e[32];
+                            row_get<TO>(buf, lane, part, e);
+                            with_act(p.act, [&](auto tag) {
 #pragma unroll
                                 for (int j = 0; j < 32; j += 2) {
                                     float a0, d0, a1, d1;
-                                    act_both<kPrecise>(p.act, v[j], a0, d0);
-                                    act_both<kPrecise>(p.act, v[j + 1], a1, d1);
+                                    act_both<kPrecise, decltype(tag)::value>(v[j], a0, d0);
+                                    act_both<kPrecise, decltype(tag)::value>(v[j + 1], a1, d1);
                                     hp[16 * part + j / 2] = pack_bf16(a0 * u[j], a1 * u[j + 1]);
+                                    up[16 * part + j / 2] = pack_bf16(e[j] * a0, e[j + 1] * a1);
                                     v[j] = e[j] * u[j] * d0;
                                     v[j + 1] = e[j + 1] * u[j + 1] * d1;
-                                    u[j] = e[j] * a0;
-                                    u[j + 1] = e[j + 1] * a1;
                                 }
-                                row_put<TO>(b, lane, part, v);
-                                row_put<TO>(buf[1], lane, part, u);
-                            }
+                            });
+                            row_put<TO>(buf, lane, part, v);
                         }
                     }
-                    if (p.tma_out) {
-                        fence_proxy_async();
-                        __syncwarp();
-                        if (lane == 0) {
-                            tma_store_2d(&maps.out, b, (int)col0, (int)row0);
-                            if (EPI == kEpiGatedBwd) tma_store_2d(&maps.up, buf[1], (int)col0, (int)row0);
-                            tma_store_commit();
-                        }
-                    } else {
-                        box_out<TO>(b, p.out, p.ldo, row0, col0, p.M, p.N, lane);
-                        if (EPI == kEpiGatedBwd) box_out<TO>(buf[1], (TO *)p.out + p.N, p.ldo, row0, col0, p.M, p.N, lane);
-                    }
-                    if (EPI == kEpiGatedBwd && p.out2) {
-                        if (lane == 0) tma_store_wait_read0();
-                        __syncwarp();
+                }
+                store(&maps.out, p.tma_out, p.out, p.ldo, col0);
+                if constexpr (EPI == kEpiGatedBwd) {
+                    auto second = [&](const uint32_t *w, const CUtensorMap *map, int tma, void *dst, int64_t ld) {
+                        box_free();
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            *(uint4 *)(b + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_uint4(hp[4 * j], hp[4 * j + 1], hp[4 * j + 2], hp[4 * j + 3]);
-                        if (p.tma_out2) {
-                            fence_proxy_async();
-                            __syncwarp();
-                            if (lane == 0) {
-                                tma_store_2d(&maps.out2, b, (int)col0, (int)row0);
-                                tma_store_commit();
-                            }
-                        } else {
-                            box_out<TO>(b, p.out2, p.ldo2, row0, col0, p.M, p.N, lane);
-                        }
-                    }
+                            *(uint4 *)(buf + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+                        store(map, tma, dst, ld, col0);
+                    };
+                    second(up, &maps.up, p.tma_out, (TO *)p.out + p.N, p.ldo);
+                    if (p.out2) second(hp, &maps.out2, p.tma_out2, p.out2, p.ldo2);
                 }
             }
             if (!ok) break;
@@ -545,8 +554,73 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder()
 
 size_t esz(gdn_dtype t) { return t == GDN_F32 ? 4 : t == GDN_BF16 ? 2 : 1; }
 
-// a map over `rows` rows of `cols` elements, boxes of 128 bytes x box_rows, 128-byte swizzle
-bool make_map(CUtensorMap *m, gdn_dtype t, const void *base, int64_t cols, int64_t rows, int64_t ld, int box_rows)
+template <bool FP8, int LAYOUT, int EPI, int BN, typename TO>
+cudaError_t go(const GemmArgs &g, cudaStream_t st)
+{
+    constexpr bool gated = EPI == kEpiGated || EPI == kEpiGatedBwd;
+    TcMaps maps;
+    std::memset(&maps, 0, sizeof(maps));
+    const int64_t brows = gated ? 2 * g.N : g.N;
+    const bool a_ok = LAYOUT == 2 ? make_operand_map(&maps.a, g.in, g.a, g.M, g.K, g.lda, 64) : make_operand_map(&maps.a, g.in, g.a, g.K, g.M, g.lda, 128);
+    const bool b_ok = LAYOUT >= 1 ? make_operand_map(&maps.b, g.in, g.b, brows, g.K, g.ldb, 64) : make_operand_map(&maps.b, g.in, g.b, g.K, brows, g.ldb, BN / 2);
+    if (!a_ok || !b_ok) return cudaErrorInvalidValue;
+    TcParams p{};
+    p.M = g.M; p.N = g.N;
+    const int per = FP8 ? 128 : 64;
+    p.kblocks = (int)((g.K + per - 1) / per);
+    p.mt = (int)((g.M + 255) / 256);
+    p.nt = (int)((g.N + (gated ? BN / 2 : BN) - 1) / (gated ? BN / 2 : BN));
+    p.x_scale = g.x_scale; p.w_scale = g.w_scale; p.bias = g.bias; p.act = g.act;
+    p.extra = g.extra; p.ld_extra = g.ld_extra;
+    p.out = g.out; p.ldo = g.ldo; p.out2 = g.out2; p.ldo2 = g.ldo2;
+    p.colpart = g.colpart;
+    const size_t eo = sizeof(TO);
+    p.tma_out = tma_ok(g.out, g.ldo, g.M, eo) && (EPI != kEpiGatedBwd || (g.N * eo) % 16 == 0);
+    if (p.tma_out && !make_operand_map(&maps.out, g.out_dt, g.out, g.N, g.M, g.ldo, 32)) return cudaErrorInvalidValue;
+    if (p.tma_out && EPI == kEpiGatedBwd && !make_operand_map(&maps.up, g.out_dt, (const TO *)g.out + g.N, g.N, g.M, g.ldo, 32))
+        return cudaErrorInvalidValue;
+    p.tma_extra = g.extra && tma_ok(g.extra, g.ld_extra, g.M, eo);
+    if (p.tma_extra && !make_operand_map(&maps.extra, g.out_dt, g.extra, g.N, g.M, g.ld_extra, 32)) return cudaErrorInvalidValue;
+    p.tma_out2 = g.out2 && tma_ok(g.out2, g.ldo2, g.M, eo);
+    if (p.tma_out2 && !make_operand_map(&maps.out2, g.out_dt, g.out2, g.N, g.M, g.ldo2, 32)) return cudaErrorInvalidValue;
+
+    auto *kern = gemm_tc_kernel<FP8, LAYOUT, EPI, BN, TO>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<BN>::kSmem);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = (int64_t)p.mt * p.nt;
+    const int pairs = (int)(tiles < device_sm_count() / 2 ? tiles : device_sm_count() / 2);
+    kern<<<2 * pairs, kThreads, Geo<BN>::kSmem, st>>>(maps, p);
+    return cudaGetLastError();
+}
+
+template <bool FP8, int LAYOUT, int EPI, typename TO>
+cudaError_t pick(const GemmArgs &g, cudaStream_t st)
+{
+    if constexpr (EPI == kEpiGated || EPI == kEpiGatedBwd) {
+        return go<FP8, LAYOUT, EPI, 256, TO>(g, st);
+    } else {
+        // Whole rounds of tiles over the pairs of SMs decide: a round of 128-column tiles costs a little over half
+        // of one of 256 columns (its products re-read A), but fills a ragged last round better.
+        const int64_t pairs = device_sm_count() / 2, mt = (g.M + 255) / 256;
+        const auto rounds = [&](int bn) { return (mt * ((g.N + bn - 1) / bn) + pairs - 1) / pairs; };
+        return 0.56 * rounds(128) < rounds(256) ? go<FP8, LAYOUT, EPI, 128, TO>(g, st) : go<FP8, LAYOUT, EPI, 256, TO>(g, st);
+    }
+}
+
+// Few rows: the weights' reading is the cost, and the pair's tiles would be padding.  (A weight gradient's rows are
+// the weight's, and its contraction the batch.)
+bool use_small(const GemmArgs &g) { return !g.a_t && g.M <= 128; }
+
+template <typename T>
+__global__ void __launch_bounds__(256) repack_kernel(const T *src, int64_t ld, int64_t rows, int64_t cols, T *dst, int64_t pitch)
+{
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+        for (int64_t c = threadIdx.x; c < cols; c += 256) dst[r * pitch + c] = src[r * ld + c];
+}
+
+}  // namespace
+
+bool make_operand_map(CUtensorMap *m, gdn_dtype t, const void *base, int64_t cols, int64_t rows, int64_t ld, int box_rows)
 {
     const auto enc = encoder();
     if (!enc) return false;
@@ -562,60 +636,6 @@ bool make_map(CUtensorMap *m, gdn_dtype t, const void *base, int64_t cols, int64
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool FP8, int LAYOUT, int EPI, int BN, typename TO>
-cudaError_t go(const GemmArgs &g, cudaStream_t st)
-{
-    constexpr bool gated = EPI == kEpiGated || EPI == kEpiGatedBwd;
-    TcMaps maps;
-    std::memset(&maps, 0, sizeof(maps));
-    const int64_t brows = gated ? 2 * g.N : g.N;
-    const bool a_ok = LAYOUT == 2 ? make_map(&maps.a, g.in, g.a, g.M, g.K, g.lda, 64) : make_map(&maps.a, g.in, g.a, g.K, g.M, g.lda, 128);
-    const bool b_ok = LAYOUT >= 1 ? make_map(&maps.b, g.in, g.b, brows, g.K, g.ldb, 64) : make_map(&maps.b, g.in, g.b, g.K, brows, g.ldb, BN / 2);
-    if (!a_ok || !b_ok) return cudaErrorInvalidValue;
-    TcParams p{};
-    p.M = g.M; p.N = g.N;
-    const int per = FP8 ? 128 : 64;
-    p.kblocks = (int)((g.K + per - 1) / per);
-    p.mt = (int)((g.M + 255) / 256);
-    p.nt = (int)((g.N + (gated ? BN / 2 : BN) - 1) / (gated ? BN / 2 : BN));
-    p.x_scale = g.x_scale; p.w_scale = g.w_scale; p.bias = g.bias; p.act = g.act;
-    p.extra = g.extra; p.ld_extra = g.ld_extra;
-    p.out = g.out; p.ldo = g.ldo; p.out2 = g.out2; p.ldo2 = g.ldo2;
-    p.colpart = g.colpart;
-    const size_t eo = sizeof(TO);
-    p.tma_out = tma_ok(g.out, g.ldo, g.M, eo) && (EPI != kEpiGatedBwd || (g.N * eo) % 16 == 0);
-    if (p.tma_out && !make_map(&maps.out, g.out_dt, g.out, g.N, g.M, g.ldo, 32)) return cudaErrorInvalidValue;
-    if (p.tma_out && EPI == kEpiGatedBwd && !make_map(&maps.up, g.out_dt, (const TO *)g.out + g.N, g.N, g.M, g.ldo, 32))
-        return cudaErrorInvalidValue;
-    p.tma_extra = g.extra && tma_ok(g.extra, g.ld_extra, g.M, eo);
-    if (p.tma_extra && !make_map(&maps.extra, g.out_dt, g.extra, g.N, g.M, g.ld_extra, 32)) return cudaErrorInvalidValue;
-    p.tma_out2 = g.out2 && tma_ok(g.out2, g.ldo2, g.M, eo);
-    if (p.tma_out2 && !make_map(&maps.out2, g.out_dt, g.out2, g.N, g.M, g.ldo2, 32)) return cudaErrorInvalidValue;
-
-    auto *kern = gemm_tc_kernel<FP8, LAYOUT, EPI, BN, TO>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<BN>::kSmem);
-    if (e != cudaSuccess) return e;
-    const int64_t tiles = (int64_t)p.mt * p.nt;
-    const int pairs = (int)(tiles < device_sm_count() / 2 ? tiles : device_sm_count() / 2);
-    kern<<<2 * pairs, kThreads, Geo<BN>::kSmem, st>>>(maps, p);
-    return cudaGetLastError();
-}
-
-template <bool FP8, int LAYOUT, int EPI, typename TO>
-cudaError_t pick(const GemmArgs &g, cudaStream_t st)
-{
-    return go<FP8, LAYOUT, EPI, 256, TO>(g, st);
-}
-
-template <typename T>
-__global__ void __launch_bounds__(256) repack_kernel(const T *src, int64_t ld, int64_t rows, int64_t cols, T *dst, int64_t pitch)
-{
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-        for (int64_t c = threadIdx.x; c < cols; c += 256) dst[r * pitch + c] = src[r * ld + c];
-}
-
-}  // namespace
-
 bool tma_ok(const void *p, int64_t ld, int64_t rows, size_t e)
 {
     return ((uintptr_t)p & 15) == 0 && (rows <= 1 || (size_t)ld * e % 16 == 0);
@@ -629,9 +649,15 @@ cudaError_t launch_repack(const void *src, gdn_dtype t, int64_t ld, int64_t rows
     return cudaGetLastError();
 }
 
+int64_t gemm_colparts(const GemmArgs &g, Epi epi)
+{
+    return g.in != GDN_F32 && use_small(g) ? gemm_small_colparts(g, epi) : (g.M + 31) / 32;
+}
+
 cudaError_t launch_gemm_tc(const GemmArgs &g, Epi epi, cudaStream_t st)
 {
     if (g.M <= 0 || g.N <= 0) return cudaSuccess;
+    if (use_small(g)) return launch_gemm_small(g, epi, st);
     const bool f32 = g.out_dt == GDN_F32;
     if (g.in == GDN_E4M3) {
         if (epi == kEpiGated) return pick<true, 0, kEpiGated, __nv_bfloat16>(g, st);
@@ -655,7 +681,7 @@ gdn_status read_tc_status(cudaStream_t st)
         cudaMemcpyToSymbolAsync(g_tc_status, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, st) != cudaSuccess ||
         cudaStreamSynchronize(st) != cudaSuccess)
         return GDN_ERR_CUDA;
-    return word & kStatusTimeout ? GDN_ERR_TIMEOUT : GDN_OK;
+    return word & kStatusTimeout ? GDN_ERR_TIMEOUT : read_small_status(st);
 }
 
 }  // namespace gdn

@@ -22,53 +22,57 @@ __device__ __forceinline__ float logistic(float z)
 constexpr float kGeluA = 1.5957691216057308f;            // 2 sqrt(2 / pi): 0.5 (1 + tanh u) = logistic(2 u)
 constexpr float kGeluB = 1.5957691216057308f * 0.044715f;
 
-template <bool PRECISE>
-__device__ __forceinline__ float act_value(int act, float z)
+template <bool PRECISE, int ACT>
+__device__ __forceinline__ float act_value(float z)
 {
-    switch (act) {
-    case GDN_ACT_SILU: return z * logistic<PRECISE>(z);
-    case GDN_ACT_GELU: return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
-    case GDN_ACT_GELU_TANH: return z * logistic<PRECISE>(z * (kGeluA + kGeluB * z * z));
-    case GDN_ACT_RELU: return z < 0.f ? 0.f : z;  // (keeps a NaN)
-    case GDN_ACT_SIGMOID: return logistic<PRECISE>(z);
-    default: return z;
-    }
+    if (ACT == GDN_ACT_SILU) return z * logistic<PRECISE>(z);
+    if (ACT == GDN_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+    if (ACT == GDN_ACT_GELU_TANH) return z * logistic<PRECISE>(z * (kGeluA + kGeluB * z * z));
+    if (ACT == GDN_ACT_RELU) return z < 0.f ? 0.f : z;  // (keeps a NaN)
+    if (ACT == GDN_ACT_SIGMOID) return logistic<PRECISE>(z);
+    return z;
 }
 // value and derivative
-template <bool PRECISE>
-__device__ __forceinline__ void act_both(int act, float z, float &v, float &d)
+template <bool PRECISE, int ACT>
+__device__ __forceinline__ void act_both(float z, float &v, float &d)
 {
-    switch (act) {
-    case GDN_ACT_SILU: {
+    if (ACT == GDN_ACT_SILU) {
         const float p = logistic<PRECISE>(z);
         v = z * p;
         d = p * (1.f + z * (1.f - p));
-        return;
-    }
-    case GDN_ACT_GELU: {
+    } else if (ACT == GDN_ACT_GELU) {
         const float c = 0.5f * (1.f + erff(z * 0.70710678118654752f));
         const float e = PRECISE ? expf(-0.5f * z * z) : __expf(-0.5f * z * z);
         v = z * c;
         d = c + z * e * 0.3989422804014327f;  // 1 / sqrt(2 pi)
-        return;
-    }
-    case GDN_ACT_GELU_TANH: {
+    } else if (ACT == GDN_ACT_GELU_TANH) {
         const float z2 = z * z, p = logistic<PRECISE>(z * (kGeluA + kGeluB * z2));
         v = z * p;
         d = p + v * (1.f - p) * (kGeluA + 3.f * kGeluB * z2);
-        return;
-    }
-    case GDN_ACT_RELU:
+    } else if (ACT == GDN_ACT_RELU) {
         v = z < 0.f ? 0.f : z;
         d = z > 0.f ? 1.f : 0.f;
-        return;
-    case GDN_ACT_SIGMOID: {
+    } else if (ACT == GDN_ACT_SIGMOID) {
         const float p = logistic<PRECISE>(z);
         v = p;
         d = p * (1.f - p);
-        return;
+    } else {
+        v = z;
+        d = 1.f;
     }
-    default: v = z; d = 1.f;
+}
+// f(an integral constant of the activation): the choice is made once, outside f's loops
+template <int A> struct ActTag { static constexpr int value = A; };
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F f)
+{
+    switch (act) {
+    case GDN_ACT_SILU: f(ActTag<GDN_ACT_SILU>()); break;
+    case GDN_ACT_GELU: f(ActTag<GDN_ACT_GELU>()); break;
+    case GDN_ACT_GELU_TANH: f(ActTag<GDN_ACT_GELU_TANH>()); break;
+    case GDN_ACT_RELU: f(ActTag<GDN_ACT_RELU>()); break;
+    case GDN_ACT_SIGMOID: f(ActTag<GDN_ACT_SIGMOID>()); break;
+    default: f(ActTag<GDN_ACT_NONE>());
     }
 }
 
@@ -76,7 +80,7 @@ __device__ __forceinline__ void act_both(int act, float z, float &v, float &d)
 enum Epi : int {
     kEpiLinear = 0,    // out = act(sx_m sw_n z + bias_n) + extra_mn
     kEpiGated = 1,     // out = act(gate) up, gate / up from rows n and F + n of B
-    kEpiDact = 2,      // out = extra_mn act'(z + bias_n); column sums of it per 32 rows into colpart
+    kEpiDact = 2,      // out = extra_mn act'(z + bias_n); column sums of it over groups of rows into colpart
     kEpiGatedBwd = 3,  // out[m, n] = extra up act'(gate), out[m, F + n] = extra act(gate); out2 = act(gate) up
 };
 
@@ -97,7 +101,7 @@ struct GemmArgs {
     int64_t ldo;
     void *out2;                      // kEpiGatedBwd: the recomputed output [M][ldo2], nullable
     int64_t ldo2;
-    float *colpart;                  // kEpiDact: [ceil(M / 32)][N], nullable
+    float *colpart;                  // kEpiDact: column sums of groups of rows, [gemm_colparts][N], nullable
 };
 
 // bf16 and e4m3 operands whose rows start on 16-byte boundaries (tma_ok); output types as gdn_linear allows
@@ -106,6 +110,14 @@ bool tma_ok(const void *p, int64_t ld, int64_t rows, size_t esz);
 // copies rows into a layout of `pitch` elements per row
 cudaError_t launch_repack(const void *src, gdn_dtype t, int64_t ld, int64_t rows, int64_t cols, void *dst, int64_t pitch, cudaStream_t st);
 gdn_status read_tc_status(cudaStream_t st);  // synchronises; clears
+// the form for few rows (launch_gemm_tc chooses), its status word
+cudaError_t launch_gemm_small(const GemmArgs &g, Epi epi, cudaStream_t st);
+gdn_status read_small_status(cudaStream_t st);
+// rows of partial column sums that a kEpiDact product writes
+int64_t gemm_colparts(const GemmArgs &g, Epi epi);
+int64_t gemm_small_colparts(const GemmArgs &g, Epi epi);
+// a TMA map over `rows` rows of `cols` elements, boxes of 128 bytes x box_rows, 128-byte swizzle
+bool make_operand_map(CUtensorMap *m, gdn_dtype t, const void *base, int64_t cols, int64_t rows, int64_t ld, int box_rows);
 
 cudaError_t launch_gemm_simt(const GemmArgs &g, Epi epi, cudaStream_t st);
 

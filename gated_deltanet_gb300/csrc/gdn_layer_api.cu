@@ -154,19 +154,6 @@ gdn_status check_linear(const gdn_linear_args *a, bool gated, bool backward)
     return GDN_OK;
 }
 
-GemmArgs forward_product(const gdn_linear_args *a)
-{
-    GemmArgs g{};
-    g.M = a->rows; g.N = a->out_features; g.K = a->in_features;
-    g.in = a->dtype; g.out_dt = a->out_dtype;
-    g.a = a->x; g.lda = a->ldx;
-    g.b = a->w; g.ldb = a->ldw;
-    g.x_scale = a->x_scale; g.w_scale = a->w_scale;
-    g.bias = a->bias;
-    g.act = a->act;
-    return g;
-}
-
 // A call's workspace: padded copies of operands; backward: dz (its rows padded to 16 bytes) and the column sums
 // of groups of 32 rows
 struct LinearPlan {
@@ -175,6 +162,19 @@ struct LinearPlan {
     size_t off_dz, off_part, bytes;
     bool own_dz;
 };
+GemmArgs forward_product(const gdn_linear_args *a, const LinearPlan &p)
+{
+    GemmArgs g{};
+    g.M = a->rows; g.N = a->out_features; g.K = a->in_features;
+    g.in = a->dtype; g.out_dt = a->out_dtype;
+    g.a = p.x.p; g.lda = p.x.ld;
+    g.b = p.w.p; g.ldb = p.w.ld;
+    g.x_scale = a->x_scale; g.w_scale = a->w_scale;
+    g.bias = a->bias;
+    g.act = a->act;
+    return g;
+}
+
 LinearPlan plan_linear(const gdn_linear_args *a, bool gated, bool backward)
 {
     LinearPlan p{};
@@ -188,6 +188,7 @@ LinearPlan plan_linear(const gdn_linear_args *a, bool gated, bool backward)
         p.own_dz = gated || a->act != GDN_ACT_NONE;
         p.parts = (a->rows + 31) / 32;
         if (p.own_dz) {
+            if (a->dbias && a->rows > 0) p.parts = gemm_colparts(forward_product(a, p), kEpiDact);
             p.dz_ld = (p.dz_cols + q - 1) / q * q;
             p.off_dz = c.take((size_t)a->rows * p.dz_ld * esize(a->dtype));
         } else {
@@ -198,19 +199,6 @@ LinearPlan plan_linear(const gdn_linear_args *a, bool gated, bool backward)
     }
     p.bytes = c.at;
     return p;
-}
-
-GemmArgs forward_product(const gdn_linear_args *a, const LinearPlan &p)
-{
-    GemmArgs g{};
-    g.M = a->rows; g.N = a->out_features; g.K = a->in_features;
-    g.in = a->dtype; g.out_dt = a->out_dtype;
-    g.a = p.x.p; g.lda = p.x.ld;
-    g.b = p.w.p; g.ldb = p.w.ld;
-    g.x_scale = a->x_scale; g.w_scale = a->w_scale;
-    g.bias = a->bias;
-    g.act = a->act;
-    return g;
 }
 
 gdn_status run_bwd(const gdn_linear_args *a, bool gated, void *ws, size_t ws_bytes, cudaStream_t st)
