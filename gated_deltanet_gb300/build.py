@@ -2,7 +2,9 @@
 
 Each ``csrc/*.cu`` file is compiled to an object in parallel (one -gencode,
 sm_103a only) and linked into ``gated_deltanet_gb300/_lib/libgdn.so``.
-A rebuild happens only when a source or header is newer than the library.
+Beside it, ``csrc/layer_binding.cpp`` (the compiled part of the Python binding) becomes ``_lib/_layer.so``
+with the host compiler, against the installed PyTorch's headers.  A rebuild happens only when a source or
+header is newer than what was built.
 """
 from __future__ import annotations
 
@@ -18,6 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libgdn.so")
+BINDING_SRC = os.path.join(CSRC, "layer_binding.cpp")
+BINDING = os.path.join(LIBDIR, "_layer.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -32,18 +36,53 @@ def _sources():
 
 def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [
-        os.path.join(ROOT, "include", "gdn.h"), os.path.abspath(__file__)]
+        os.path.join(ROOT, "include", "gdn.h"), os.path.abspath(__file__), BINDING_SRC]
 
 
 def lib_path() -> str:
     return LIB
 
 
+def binding_path() -> str:
+    return BINDING
+
+
 def needs_build() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return any(os.path.getmtime(p) > t for p in _deps())
+
+
+def _compile_binding() -> str:
+    """The binding's object file (its library is linked once ``libgdn.so`` exists)."""
+    import sysconfig
+
+    import torch
+
+    t = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    obj = os.path.join(OBJ, "layer_binding.o")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", t, "-isystem", os.path.join(t, "torch", "csrc", "api", "include"), "-isystem", cuda,
+           "-isystem", sysconfig.get_paths()["include"], "-I", os.path.join(ROOT, "include"), "-c", BINDING_SRC, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+
+    t = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, LIB, "-Wl,-rpath,$ORIGIN", "-L" + t, "-ltorch_python", "-ltorch_cpu",
+           "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of {BINDING} failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
 
 
 def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -> str:
@@ -65,18 +104,21 @@ def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -
         return obj, r.stderr
 
     srcs = _sources()
-    with ThreadPoolExecutor(max_workers=jobs or min(8, len(srcs))) as ex:
+    with ThreadPoolExecutor(max_workers=jobs or min(12, len(srcs) + 1)) as ex:
+        binding = ex.submit(_compile_binding)
         results = list(ex.map(compile_one, srcs))
+        binding_obj = binding.result()
     if verbose:
         for _, err in results:
             if err:
                 print(err)
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + [o for o, _ in results] + ["-lcudart_static"]
+    cmd = [nvcc()] + ARCH + ["-shared", "-Xlinker", "-soname=libgdn.so", "-o", tmp] + [o for o, _ in results] + ["-lcudart_static"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding_obj)
     return LIB
 
 

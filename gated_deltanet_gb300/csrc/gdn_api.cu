@@ -451,7 +451,15 @@ bool gdn::managed_workspace_holds(size_t need, cudaStream_t stream)
     return it != g_ws.end() && it->second.ptr && it->second.bytes >= need;
 }
 
-int gdn::device_sm_count() { return current_sm_count(); }
+int gdn::device_sm_count()
+{
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return current_sm_count();
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (!n) known[dev].store(n = current_sm_count(), std::memory_order_relaxed);
+    return n;
+}
 
 gdn_status gdn::check_call(const gdn_shape *s, const void *q, const void *k, const void *v, const float *g,
                            const float *beta, float scale, const int64_t *cu, int chunk_size, const void *o,

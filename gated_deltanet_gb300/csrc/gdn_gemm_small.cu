@@ -3,9 +3,12 @@
 // The roles of the operands are swapped: 128 rows of the weight are the M side of the instruction and up to
 // NT rows of x its N side, so that one token costs an N = 16 instruction and not a padded 128 x 256 tile.  The
 // contraction is split over a cluster of up to eight CTAs, which makes enough CTAs to keep every SM's
-// loads in flight (N = 2048 alone is 16 tiles); their fp32 partial sums meet through distributed shared memory,
-// each CTA of the cluster finishing its share of the rows of x, in a fixed order.  A CTA's shared memory is
-// one long queue of 128-byte-wide weight boxes: most of what a CTA reads is requested at once.
+// loads in flight (N = 2048 alone is 16 tiles).  Each CTA sends its fp32 partial sums to the CTAs of the cluster
+// that finish the rows of x in turn (row t: CTA t mod split), which add them in the order of the
+// contraction; sums are sent and not fetched, so that one meeting of the cluster is enough.  A CTA's shared
+// memory is one queue of 128-byte-wide weight boxes, and two CTAs share an SM: most of what they read is
+// requested at once.
+#include <atomic>
 #include <cstring>
 
 #include <cudaTypedefs.h>
@@ -40,24 +43,25 @@ struct SmallParams {
     void *out2;
     int64_t ldo2;
     float *colpart;
+    int vec_out, vec_extra;  // rows of out (and out2), of extra allow groups of four elements
 };
 
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity)
 {
     return mbar_wait(bar, parity, &g_small_status, kStatusTimeout, kLimitNs);
 }
-// a float at the same place in CTA `cta` of the cluster
-__device__ __forceinline__ float peer_float(const float *p, uint32_t cta)
+// the shared memory of CTA `cta` of the cluster, at the place of p
+__device__ __forceinline__ uint32_t peer_addr(const float *p, uint32_t cta)
 {
     uint32_t a;
-    float v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(cta));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-    return v;
+    return a;
+}
+__device__ __forceinline__ void peer_store(uint32_t addr, float v)
+{
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 template <bool FP8>
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
@@ -91,8 +95,10 @@ gemm_small_kernel(const __grid_constant__ SmallMaps maps, const SmallParams p)
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages], done;
     __shared__ uint32_t tslot;
+    __shared__ float cols[EPI == kEpiDact ? kThreads / 32 : 1][128];
     uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    float *red = (float *)sm;  // [NT][128], once every stage is dead
+    float *red = (float *)(sm + p.stages * kStage);  // [split][slots][128]: partial sums of the rows finished here
+    const int slots = (NT + p.split - 1) / p.split;
     const int tid = threadIdx.x, warp = tid >> 5;
     const int rank = blockIdx.x % p.split, tile = blockIdx.x / p.split;
     const int mi = tile % p.mtiles, ni = tile / p.mtiles;
@@ -110,6 +116,7 @@ gemm_small_kernel(const __grid_constant__ SmallMaps maps, const SmallParams p)
     if (warp == 5) tmem_alloc(&tslot, kCols);
     tc_fence_before();
     __syncthreads();
+    cluster_arrive();  // (waited for before the first store into another CTA)
     tc_fence_after();
     const uint32_t tmem = tslot;
     bool ok = true;
@@ -141,39 +148,27 @@ gemm_small_kernel(const __grid_constant__ SmallMaps maps, const SmallParams p)
         constexpr uint32_t id = FP8 ? (1u << 4) | ((uint32_t)(NT >> 3) << 17) | (8u << 24) : idesc_bf16_f32(128, NT, WT, 0);
         int s = 0;
         uint32_t ph = 0;
+        bool ready = false;
         for (int kb = kb0; kb < kb1; ++kb) {
-            if (!(ok = __all_sync(0xffffffffu, wait(&full[s], ph)))) break;
+            if (!ready && !(ok = __all_sync(0xffffffffu, wait(&full[s], ph)))) break;
             tc_fence_after();
+            uint64_t *const rel = &empty[s];
             const uint32_t a = smem_u32(sm + s * kStage);
             const uint64_t da = sdesc_sw128(a, WT ? 8192 : 16, 1024), db = sdesc_sw128(a + kWBytes, 16, 1024);
+            if (++s == p.stages) { s = 0; ph ^= 1; }
+            // the next block's state, asked for before this block's products are issued
+            ready = __all_sync(0xffffffffu, mbar_test_wait(&full[s], ph));
             if (elect_one_sync()) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) mma<FP8>(tmem, da + j * (WT ? 128 : 2), db + j * 2, id, kb > kb0 || j);
-                mma_commit(&empty[s]);
+                mma_commit(rel);
                 if (kb + 1 == kb1) mma_commit(&done);
             }
             __syncwarp();
-            if (++s == p.stages) { s = 0; ph ^= 1; }
         }
     } else {
-        // this CTA's partial sums, [row of x][feature]
         ok = __all_sync(0xffffffffu, wait(&done, 0));
-        if (ok) {
-            tc_fence_after();
-            const uint32_t tl = tmem + ((uint32_t)(warp * 32) << 16);
-#pragma unroll
-            for (int c = 0; c < NT; c += 16) {
-                if (m0 + c >= p.M) break;
-                float v[16];
-                tmem_ld16(tl + c, v);
-                tmem_ld_wait();
-#pragma unroll
-                for (int j = 0; j < 16; ++j) asm volatile("" : "+f"(v[j]));
-#pragma unroll
-                for (int j = 0; j < 16; ++j) red[(c + j) * 128 + tid] = v[j];
-            }
-            tc_fence_before();
-        }
+        tc_fence_after();
     }
     if (!ok) {
         // a wait ran out: give whatever is still in flight a millisecond to land before the memory is let go
@@ -181,73 +176,139 @@ gemm_small_kernel(const __grid_constant__ SmallMaps maps, const SmallParams p)
         while (globaltimer() - t0 < 1000000) {}
     }
     __syncwarp();
-    cluster_sync();
+    cluster_wait();  // every CTA of the cluster runs
     if (warp < 4 && ok) {
-        // rows rank, rank + split, ... of the tile: the partial sums in the order of the contraction, then the epilogue
+        // partial sums to the CTAs that finish their rows: lane = feature, so 32 lanes store 128 bytes
+        const uint32_t tl = tmem + ((uint32_t)(warp * 32) << 16);
+        int owner = 0, slot = 0;
+#pragma unroll
+        for (int c = 0; c < NT; c += 16) {
+            if (m0 + c >= p.M) break;
+            float v[16];
+            tmem_ld16(tl + c, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) asm volatile("" : "+f"(v[j]));
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                if (m0 + c + j < p.M) peer_store(peer_addr(red + (rank * slots + slot) * 128 + tid, owner), v[j]);
+                if (++owner == p.split) { owner = 0; ++slot; }
+            }
+        }
+        tc_fence_before();
+    }
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+    if (ok) {
+        // rows rank, rank + split, ... of the tile: the partial sums in the order of the contraction, then the
+        // epilogue; four features a thread, a row per 32 (gated: 16) threads
+        constexpr int kPer = kOut / 4, kGroups = kThreads / kPer, kElem = (int)sizeof(TO);
         TO *out = (TO *)p.out;
         const TO *extra = (const TO *)p.extra;
-        const int f = kGated ? tid & 63 : tid;
+        const int f = tid % kPer * 4, grp = tid / kPer;
         const int64_t n = n0 + f;
-        const int first = kGated ? rank + (tid >> 6) * p.split : rank, step = kGated ? 2 * p.split : p.split;
         const int rows = (int)(p.M - m0 < NT ? p.M - m0 : NT);
-        const bool in = n < p.N;
-        const float bias = !kGated && p.bias && in ? p.bias[n] : 0.f;
-        const float wg = FP8 && p.w_scale && in ? p.w_scale[n] : 1.f;
-        const float wu = FP8 && kGated && p.w_scale && in ? p.w_scale[p.N + n] : 1.f;
-        float col = 0.f;
+        const int mine = rows > rank ? (rows - rank + p.split - 1) / p.split : 0;  // rows finished here
+        const int have = p.N - n >= 4 ? 4 : p.N > n ? (int)(p.N - n) : 0;          // features that exist
+        // whole groups of four by one load or store, where every row allows it
+        const bool vec_out = have == 4 && p.vec_out, vec_extra = have == 4 && p.vec_extra;
+        float bias[4], wg[4], wu[4], col[4] = {};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            bias[j] = !kGated && p.bias && j < have ? p.bias[n + j] : 0.f;
+            wg[j] = FP8 && p.w_scale && j < have ? p.w_scale[n + j] : 1.f;
+            wu[j] = FP8 && kGated && p.w_scale && j < have ? p.w_scale[p.N + n + j] : 1.f;
+        }
+        auto put = [&](TO *dst, const float *v) {
+            if (vec_out) {
+                if constexpr (kElem == 2) *(uint2 *)dst = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+                else *(float4 *)dst = make_float4(v[0], v[1], v[2], v[3]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j < have) dst[j] = from_f<TO>(v[j]);
+            }
+        };
         with_act(p.act, [&](auto tag) {
             constexpr int ACT = decltype(tag)::value;
-            constexpr int U = 4;  // rows at a time, for loads in flight
-            for (int t0 = first; t0 < rows; t0 += U * step) {
-                float z[U] = {}, u[U] = {}, e[U] = {}, sx[U];
+            for (int sl = grp; sl < mine; sl += kGroups) {
+                const int64_t m = m0 + rank + (int64_t)sl * p.split;
+                float e[4] = {};
+                if (EPI != kEpiGated && extra) {
+                    const TO *src = extra + m * p.ld_extra + n;
+                    if (vec_extra) {
+                        if constexpr (kElem == 2) {
+                            const uint2 u = *(const uint2 *)src;
+                            e[0] = __uint_as_float(u.x << 16); e[1] = __uint_as_float(u.x & 0xffff0000u);
+                            e[2] = __uint_as_float(u.y << 16); e[3] = __uint_as_float(u.y & 0xffff0000u);
+                        } else {
+                            const float4 u = *(const float4 *)src;
+                            e[0] = u.x; e[1] = u.y; e[2] = u.z; e[3] = u.w;
+                        }
+                    } else {
 #pragma unroll
-                for (int i = 0; i < U; ++i) {
-                    const int t = t0 + i * step;
-                    sx[i] = 1.f;
-                    if (t >= rows) continue;
-                    const int64_t m = m0 + t;
-                    if (EPI != kEpiGated && extra && in) e[i] = to_f(extra[m * p.ld_extra + n]);
-                    if (FP8 && p.x_scale) sx[i] = p.x_scale[m];
-                    for (int c = 0; c < p.split; ++c) {
-                        z[i] += peer_float(red + t * 128 + f, c);
-                        if (kGated) u[i] += peer_float(red + t * 128 + 64 + f, c);
+                        for (int j = 0; j < 4; ++j)
+                            if (j < have) e[j] = to_f(src[j]);
                     }
                 }
+                const float sx = FP8 && p.x_scale ? p.x_scale[m] : 1.f;
+                float z[4] = {}, u[4] = {};
+                for (int c = 0; c < p.split; ++c) {
+                    const float *r = red + (c * slots + sl) * 128 + f;
+                    const float4 a = *(const float4 *)r;
+                    z[0] += a.x; z[1] += a.y; z[2] += a.z; z[3] += a.w;
+                    if (kGated) {
+                        const float4 b = *(const float4 *)(r + 64);
+                        u[0] += b.x; u[1] += b.y; u[2] += b.z; u[3] += b.w;
+                    }
+                }
+                float y[4], y2[4];
 #pragma unroll
-                for (int i = 0; i < U; ++i) {
-                    const int t = t0 + i * step;
-                    if (t >= rows || !in) continue;
-                    const int64_t m = m0 + t;
+                for (int j = 0; j < 4; ++j) {
                     if (FP8 && p.w_scale) {
-                        z[i] *= sx[i] * wg;
-                        u[i] *= sx[i] * wu;
+                        z[j] *= sx * wg[j];
+                        u[j] *= sx * wu[j];
                     }
                     if (EPI == kEpiLinear) {
-                        float y = act_value<kPrecise, ACT>(z[i] + bias);
-                        out[m * p.ldo + n] = from_f<TO>(y + e[i]);
+                        y[j] = act_value<kPrecise, ACT>(z[j] + bias[j]) + e[j];
                     } else if (EPI == kEpiGated) {
-                        out[m * p.ldo + n] = from_f<TO>(act_value<kPrecise, ACT>(z[i]) * u[i]);
+                        y[j] = act_value<kPrecise, ACT>(z[j]) * u[j];
                     } else if (EPI == kEpiDact) {
                         float v, d;
-                        act_both<kPrecise, ACT>(z[i] + bias, v, d);
-                        const float dz = e[i] * d;
-                        out[m * p.ldo + n] = from_f<TO>(dz);
-                        col += dz;
+                        act_both<kPrecise, ACT>(z[j] + bias[j], v, d);
+                        y[j] = e[j] * d;
+                        col[j] += y[j];
                     } else {
                         float v, d;
-                        act_both<kPrecise, ACT>(z[i], v, d);
-                        out[m * p.ldo + n] = from_f<TO>(e[i] * u[i] * d);
-                        out[m * p.ldo + p.N + n] = from_f<TO>(e[i] * v);
-                        if (p.out2) ((TO *)p.out2)[m * p.ldo2 + n] = from_f<TO>(v * u[i]);
+                        act_both<kPrecise, ACT>(z[j], v, d);
+                        y[j] = e[j] * u[j] * d;
+                        y2[j] = e[j] * v;
+                        z[j] = v * u[j];
                     }
+                }
+                put(out + m * p.ldo + n, y);
+                if (EPI == kEpiGatedBwd) {
+                    put(out + m * p.ldo + p.N + n, y2);
+                    if (p.out2) put((TO *)p.out2 + m * p.ldo2 + n, z);
                 }
             }
         });
-        if (EPI == kEpiDact && p.colpart && in) p.colpart[((int64_t)mi * p.split + rank) * p.N + n] = col;
+        if (EPI == kEpiDact && p.colpart) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) cols[grp][f + j] = col[j];
+        }
     }
-    __syncwarp();
-    cluster_sync();  // no CTA leaves while another reads its sums
-    if (warp == 5) {
+    if (EPI == kEpiDact && p.colpart) {
+        __syncthreads();
+        if (tid < 128 && n0 + tid < p.N) {
+            float sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < kThreads / 32; ++w) sum += cols[w][tid];
+            p.colpart[((int64_t)mi * p.split + rank) * p.N + n0 + tid] = sum;
+        }
+    }
+    if (warp == 5) {  // (the accumulators were read before the cluster met)
         tc_fence_after();
         tmem_dealloc(tmem, kCols);
     }
@@ -255,34 +316,75 @@ gemm_small_kernel(const __grid_constant__ SmallMaps maps, const SmallParams p)
 
 size_t esz(gdn_dtype t) { return t == GDN_F32 ? 4 : t == GDN_BF16 ? 2 : 1; }
 
-// How a product is cut: rows of x per tile, CTAs per contraction, CTAs resident per SM
+constexpr size_t kRoom = 110 * 1024;  // a CTA's shared memory: two on an SM
+
+// How a product is cut: rows of x per tile, CTAs per contraction
 struct SmallPlan {
     int nt, split, mtiles, stages;
     int64_t tiles;
     size_t smem;
 };
+
+// two CTAs of this size on an SM (without the carve-out the driver leaves room for one)
+template <typename F>
+cudaError_t allow_two(F *kern)
+{
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRoom);
+    return e != cudaSuccess ? e : cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+}
+
+// A kernel of the same block and shared memory that holds no tensor memory: the runtime answers one block per SM
+// for every kernel that allocates tensor memory, whatever it holds, while the SM runs two of them.
+__global__ void __launch_bounds__(kThreads) place_kernel() {}
+
+// clusters of `split` CTAs of this size that the device runs at once (asked once per device)
+int64_t clusters_at_once(int split)
+{
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices][kMaxSplit + 1];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) dev = 0;
+    int n = known[dev][split].load(std::memory_order_relaxed);
+    if (n) return n;
+    auto *kern = place_kernel;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)split;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)split);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kRoom;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (allow_two(kern) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        n = 2 * device_sm_count() / (split + 1);
+    }
+    known[dev][split].store(n, std::memory_order_relaxed);
+    return n;
+}
+
 SmallPlan plan_small(const GemmArgs &g, Epi epi)
 {
     SmallPlan p{};
     const bool gated = epi == kEpiGated || epi == kEpiGatedBwd;
-    p.nt = g.M <= 16 ? 16 : g.M <= 32 ? 32 : g.M <= 64 ? 64 : 128;
+    p.nt = g.M <= 16 ? 16 : g.M <= 32 ? 32 : 64;
     p.mtiles = (int)((g.M + p.nt - 1) / p.nt);
     const int kb = (int)((g.K * (int64_t)esz(g.in) + 127) / 128);
     p.tiles = (g.N + (gated ? 63 : 127)) / (gated ? 64 : 128) * p.mtiles;
-    // as many CTAs as two per SM hold; every CTA keeps at least two blocks of the contraction
-    const int64_t slots = 2 * device_sm_count();
-    int64_t split = slots / p.tiles;
-    split = split > kMaxSplit ? kMaxSplit : split;
-    split = split > kb / 2 ? kb / 2 : split;
-    p.split = (int)(split < 1 ? 1 : split);
-    const bool two = p.tiles * p.split > device_sm_count();
-    const size_t stage = kWBytes + p.nt * 128, room = (two ? 110 : 222) * 1024;
-    p.stages = (int)(room / stage);
+    // The largest split whose clusters all run at once (a cluster that has to wait for a free place doubles the
+    // time: N = 2048, K = 5504 took 13.7 us with the sixteenth cluster of eight left over, on one CTA per SM);
+    // every CTA keeps at least two blocks of the contraction.
+    p.split = kMaxSplit;
+    while (p.split > 1 && (p.split > kb / 2 || clusters_at_once(p.split) < p.tiles)) --p.split;
+    const size_t stage = kWBytes + p.nt * 128, red = (size_t)(p.nt + kMaxSplit) * 512;
+    p.stages = (int)((kRoom - 1024 - red) / stage);
     const int need = (kb + p.split - 1) / p.split;
     p.stages = p.stages > kMaxStages ? kMaxStages : p.stages;
     p.stages = p.stages > need ? need : p.stages;
-    const size_t bytes = p.stages * stage, redb = (size_t)p.nt * 512;
-    p.smem = 1024 + (bytes > redb ? bytes : redb);
+    p.smem = 1024 + p.stages * stage + red;
     return p;
 }
 
@@ -304,9 +406,16 @@ cudaError_t go(const GemmArgs &g, const SmallPlan &pl, cudaStream_t st)
     p.extra = g.extra; p.ld_extra = g.ld_extra;
     p.out = g.out; p.ldo = g.ldo; p.out2 = g.out2; p.ldo2 = g.ldo2;
     p.colpart = g.colpart;
+    auto four = [](const void *q, int64_t ld) { return ((uintptr_t)q & (4 * sizeof(TO) - 1)) == 0 && ld % 4 == 0; };
+    p.vec_out = four(g.out, g.ldo) && (EPI != kEpiGatedBwd || (g.N % 4 == 0 && four(g.out2, g.ldo2)));
+    p.vec_extra = four(g.extra, g.ld_extra);
     auto *kern = gemm_small_kernel<FP8, WT, EPI, NT, TO>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024);
-    if (e != cudaSuccess) return e;
+    static std::atomic<uint64_t> seen;
+    if (first_on_device(seen)) {
+        const cudaError_t e = allow_two(kern);
+        if (e != cudaSuccess) return e;
+        done_on_device(seen);
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(pl.tiles * pl.split));
     cfg.blockDim = dim3(kThreads);
@@ -328,8 +437,7 @@ cudaError_t pick(const GemmArgs &g, cudaStream_t st)
     switch (p.nt) {
     case 16: return go<FP8, WT, EPI, 16, TO>(g, p, st);
     case 32: return go<FP8, WT, EPI, 32, TO>(g, p, st);
-    case 64: return go<FP8, WT, EPI, 64, TO>(g, p, st);
-    default: return go<FP8, WT, EPI, 128, TO>(g, p, st);
+    default: return go<FP8, WT, EPI, 64, TO>(g, p, st);
     }
 }
 

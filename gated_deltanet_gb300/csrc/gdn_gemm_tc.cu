@@ -585,8 +585,12 @@ cudaError_t go(const GemmArgs &g, cudaStream_t st)
     if (p.tma_out2 && !make_operand_map(&maps.out2, g.out_dt, g.out2, g.N, g.M, g.ldo2, 32)) return cudaErrorInvalidValue;
 
     auto *kern = gemm_tc_kernel<FP8, LAYOUT, EPI, BN, TO>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<BN>::kSmem);
-    if (e != cudaSuccess) return e;
+    static std::atomic<uint64_t> seen;
+    if (first_on_device(seen)) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<BN>::kSmem);
+        if (e != cudaSuccess) return e;
+        done_on_device(seen);
+    }
     const int64_t tiles = (int64_t)p.mt * p.nt;
     const int pairs = (int)(tiles < device_sm_count() / 2 ? tiles : device_sm_count() / 2);
     kern<<<2 * pairs, kThreads, Geo<BN>::kSmem, st>>>(maps, p);

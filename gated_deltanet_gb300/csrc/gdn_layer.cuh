@@ -2,6 +2,8 @@
 // argument blocks of their kernels and the arithmetic that every engine's epilogue shares.
 #pragma once
 
+#include <atomic>
+
 #include <cuda_fp8.h>
 
 #include "gdn_internal.cuh"
@@ -161,7 +163,20 @@ cudaError_t launch_norm_bwd(const NormBwdArgs &a, int num_sms, cudaStream_t st);
 // The library-managed workspace of (device, stream), grown to `need` bytes; and whether it holds them already.
 gdn_status managed_workspace(size_t need, cudaStream_t stream, void **out, size_t *out_bytes);
 bool managed_workspace_holds(size_t need, cudaStream_t stream);
-int device_sm_count();
+int device_sm_count();  // of the current device (asked once per device)
+// Whether this is the first call with `seen` on the current device; then the caller sets the kernel's attributes.
+// (Two threads may both see a first call: setting an attribute twice is harmless.)
+inline bool first_on_device(std::atomic<uint64_t> &seen)
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev > 63) return true;
+    return !(seen.load(std::memory_order_relaxed) >> dev & 1);
+}
+inline void done_on_device(std::atomic<uint64_t> &seen)
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev <= 63) seen.fetch_or(1ull << dev, std::memory_order_relaxed);
+}
 
 // typed loads and stores
 template <typename T> __device__ __forceinline__ float to_f(T v);
