@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(1024) colsum_finish_kernel(const float *part, 
     const int64_t n = (int64_t)blockIdx.x * 32 + lane;
     float acc = 0.f;
     if (n < N) {
-#pragma unroll 4
+#pragma unroll 8
         for (int64_t p = w; p < parts; p += 32) acc += part[p * N + n];
     }
     s[w][lane] = acc;

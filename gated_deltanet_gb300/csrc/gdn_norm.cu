@@ -6,18 +6,19 @@
 //   dx = dh + (w dy - h mean(w dy h) / n^2) / n,   dw = sum over rows of dy h / n
 //
 // Bound: HBM.  Each input is read once and each output written once: a row stays in the registers of the
-// threads that share it (at most 16 elements a thread) while its sums meet, by shuffles and, for rows
+// threads that share it while its sums meet, by shuffles and, for rows
 // shared by several warps, one exchange through shared memory.  max|y| is taken as max|w h| / n, so that
-// both statistics of a quantised row meet in the same exchange.  A block walks rows a grid apart and
-// loads its next row before it works on this one; the weights stay in registers.
+// both statistics of a quantised row meet in the same exchange.  A block walks rows a grid apart with the
+// next rows already on their way; the weights stay in registers.
 #include "gdn_layer.cuh"
 
 namespace gdn {
 namespace {
 
-constexpr int kRowElems = 16;        // elements of a row per thread, at most
 constexpr int kRowThreads = 512;     // threads of a block, at most
-constexpr int kWide = kRowElems * kRowThreads;  // wider rows take the looping kernels
+constexpr int kMaxGroups = 4;        // groups of 16 bytes of a row per thread, at most
+constexpr int kMaxSingles = 16;      // single elements of a row per thread, at most
+constexpr int kWide = 8192;          // wider rows take the looping kernels (512 threads hold this much either way)
 constexpr float kE4m3Max = 448.f, kScaleMin = 1.17549435e-38f;  // 2^-126: the smallest normal scale
 
 __device__ __forceinline__ float max_nan(float a, float b)
@@ -87,17 +88,19 @@ __device__ __forceinline__ float weight_at(const void *w, gdn_dtype dt, int64_t 
     return dt == GDN_F32 ? ((const float *)w)[i] : __bfloat162float(((const __nv_bfloat16 *)w)[i]);
 }
 
+// What meets beside a row's sum of squares: nothing, another sum, or a maximum
+enum Second : int { kNone, kSum, kMax };
 // (sum of a, sum or maximum of b) over the tpr threads of a row; every one of them gets both.  `buf` is this
 // row's half of a double buffer, so one barrier per row is enough.
-template <bool MAX>
+template <int SECOND>
 __device__ __forceinline__ float2 row_reduce(float a, float b, int tpr, float2 *buf)
 {
+    auto meet = [&](float o) { return SECOND == kMax ? max_nan(b, o) : b + o; };
 #pragma unroll
     for (int off = 16; off; off >>= 1) {
         if (off < tpr) {
             a += __shfl_xor_sync(0xffffffffu, a, off);
-            const float o = __shfl_xor_sync(0xffffffffu, b, off);
-            b = MAX ? max_nan(b, o) : b + o;
+            if (SECOND != kNone) b = meet(__shfl_xor_sync(0xffffffffu, b, off));
         }
     }
     if (tpr > 32) {
@@ -109,15 +112,87 @@ __device__ __forceinline__ float2 row_reduce(float a, float b, int tpr, float2 *
         b = v.y;
 #pragma unroll
         for (int off = 8; off; off >>= 1) {
-            a += __shfl_xor_sync(0xffffffffu, a, off);
-            const float o = __shfl_xor_sync(0xffffffffu, b, off);
-            b = MAX ? max_nan(b, o) : b + o;
+            if (off < nw) {
+                a += __shfl_xor_sync(0xffffffffu, a, off);
+                if (SECOND != kNone) b = meet(__shfl_xor_sync(0xffffffffu, b, off));
+            }
         }
         a = __shfl_sync(0xffffffffu, a, 0);
-        b = __shfl_sync(0xffffffffu, b, 0);
+        if (SECOND != kNone) b = __shfl_sync(0xffffffffu, b, 0);
     }
     return make_float2(a, b);
 }
+
+__device__ __forceinline__ void copy16(void *smem, const void *g)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(g) : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// The rows ahead of the one a thread works on.  16-byte groups come by asynchronous copies into slots of the
+// thread's own (no other thread reads them, so a thread only waits for its own copies), kAhead rows deep: the
+// copies in flight, not registers or resident blocks, cover the memory's latency.  Single elements (rows off 16
+// bytes) are loaded into registers, one row ahead.
+template <typename T, int VEC, int VPT, int TENSORS>
+struct RowsAhead {
+    static constexpr bool kAsync = VEC > 1;
+    static constexpr int kAhead = !kAsync ? 1 : VPT == 1 ? 4 : VPT == 2 ? 3 : 2;
+    static size_t bytes(int threads) { return kAsync ? (size_t)kAhead * TENSORS * VPT * threads * 16 : 0; }
+
+    uint4 *slots;  // [kAhead][TENSORS][VPT][threads]
+    const T *src[TENSORS];
+    int64_t ld[TENSORS];
+    int64_t step, M;
+    int t, tpr, nv;
+    Raw<T, VEC> held[kAsync ? 1 : TENSORS][kAsync ? 1 : VPT];
+
+    __device__ __forceinline__ uint4 *slot(int stage, int k, int i) const
+    {
+        return slots + ((stage * TENSORS + k) * VPT + i) * blockDim.x + threadIdx.x;
+    }
+    __device__ __forceinline__ void fetch(int64_t row, int stage)
+    {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = t + i * tpr;
+            if (v < nv && row < M)
+#pragma unroll
+                for (int k = 0; k < TENSORS; ++k) {
+                    if (!src[k]) continue;
+                    const T *p = src[k] + row * ld[k] + (int64_t)v * VEC;
+                    if constexpr (kAsync) copy16(slot(stage, k, i), p);
+                    else held[k][i].load(p);
+                }
+        }
+        if constexpr (kAsync) copies_done();
+    }
+    __device__ __forceinline__ void start(int64_t row)
+    {
+        for (int s = 0; s < (kAsync ? kAhead - 1 : 1); ++s) fetch(row + s * step, s);
+    }
+    // this thread's elements of tensor k of the row of round `it` (they are there: call after ready())
+    __device__ __forceinline__ void ready()
+    {
+        if constexpr (kAsync) copies_wait<kAhead - 2>();
+    }
+    __device__ __forceinline__ void get(int it, int k, int i, float *f) const
+    {
+        if constexpr (kAsync) {
+            Raw<T, VEC> r;
+            r.v = *(const decltype(r.v) *)slot(it % kAhead, k, i);
+            r.to(f);
+        } else {
+            held[k][i].to(f);
+        }
+    }
+    // ask for the row that comes kAhead - 1 rounds later (single elements: the next one)
+    __device__ __forceinline__ void next(int64_t row, int it)
+    {
+        if constexpr (kAsync) fetch(row + (kAhead - 1) * step, (it + kAhead - 1) % kAhead);
+        else fetch(row + step, 0);
+    }
+};
 
 // tpr threads (a power of two) per row, VPT groups of VEC elements each
 template <typename T, typename TO, int VEC, int VPT>
@@ -127,6 +202,14 @@ __global__ void __launch_bounds__(kRowThreads) norm_kernel(NormArgs a, int tpr)
     const int t = threadIdx.x & (tpr - 1), rpb = blockDim.x / tpr, nv = a.D / VEC;
     const int64_t step = (int64_t)gridDim.x * rpb;
     const T *x = (const T *)a.x, *r = (const T *)a.r;
+    extern __shared__ uint4 ahead_slots[];
+    RowsAhead<T, VEC, VPT, 2> in;
+    in.slots = ahead_slots;
+    in.src[0] = x; in.src[1] = r;
+    in.ld[0] = a.ldx; in.ld[1] = a.ldr;
+    in.step = step; in.M = a.M; in.t = t; in.tpr = tpr; in.nv = nv;
+    int64_t row = (int64_t)blockIdx.x * rpb + threadIdx.x / tpr;
+    in.start(row);
     float w[VPT][VEC];
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
@@ -135,34 +218,21 @@ __global__ void __launch_bounds__(kRowThreads) norm_kernel(NormArgs a, int tpr)
             const int c = (t + i * tpr) * VEC + j;
             w[i][j] = c < a.D ? weight_at(a.w, a.w_dt, c) : 0.f;
         }
-    Raw<T, VEC> xr[VPT], rr[VPT];
-    auto fetch = [&](int64_t row) {
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int v = t + i * tpr;
-            if (v < nv && row < a.M) {
-                xr[i].load(x + row * a.ldx + (int64_t)v * VEC);
-                if (r) rr[i].load(r + row * a.ldr + (int64_t)v * VEC);
-            }
-        }
-    };
-    int64_t row = (int64_t)blockIdx.x * rpb + threadIdx.x / tpr;
-    fetch(row);
     // every thread of a block runs the same number of rounds (they meet in the reduction)
-    const int64_t rounds = (a.M - (int64_t)blockIdx.x * rpb + step - 1) / step;
-    for (int64_t it = 0; it < rounds; ++it, row += step) {
+    const int rounds = (int)((a.M - (int64_t)blockIdx.x * rpb + step - 1) / step);
+    for (int it = 0; it < rounds; ++it, row += step) {
         float h[VPT][VEC];
         float ss = 0.f, mx = 0.f;
+        in.ready();
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const bool in = t + i * tpr < nv && row < a.M;
 #pragma unroll
             for (int j = 0; j < VEC; ++j) h[i][j] = 0.f;
-            if (in) {
-                xr[i].to(h[i]);
+            if (t + i * tpr < nv && row < a.M) {
+                in.get(it, 0, i, h[i]);
                 if (r) {
                     float q[VEC];
-                    rr[i].to(q);
+                    in.get(it, 1, i, q);
 #pragma unroll
                     for (int j = 0; j < VEC; ++j) h[i][j] += q[j];
                 }
@@ -170,12 +240,12 @@ __global__ void __launch_bounds__(kRowThreads) norm_kernel(NormArgs a, int tpr)
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
                 ss = fmaf(h[i][j], h[i][j], ss);
-                mx = max_nan(mx, fabsf(h[i][j] * w[i][j]));
+                if (sizeof(TO) == 1) mx = max_nan(mx, fabsf(h[i][j] * w[i][j]));
             }
         }
         const int64_t cur = row;
-        fetch(row + step);
-        const float2 s = row_reduce<true>(ss, mx, tpr, red[it & 1]);
+        in.next(row, it);
+        const float2 s = row_reduce<sizeof(TO) == 1 ? kMax : kNone>(ss, mx, tpr, red[it & 1]);
         const float rn = a.normalise ? 1.f / sqrtf(s.x / (float)a.D + a.eps) : 1.f;
         float inv = 1.f;
         if (sizeof(TO) == 1) {
@@ -216,9 +286,9 @@ __global__ void __launch_bounds__(kRowThreads) norm_wide_kernel(NormArgs a)
         for (int c = threadIdx.x; c < a.D; c += blockDim.x) {
             const float h = at(c);
             ss = fmaf(h, h, ss);
-            mx = max_nan(mx, fabsf(h * weight_at(a.w, a.w_dt, c)));
+            if (sizeof(TO) == 1) mx = max_nan(mx, fabsf(h * weight_at(a.w, a.w_dt, c)));
         }
-        const float2 s = row_reduce<true>(ss, mx, blockDim.x, red[it & 1]);
+        const float2 s = row_reduce<sizeof(TO) == 1 ? kMax : kNone>(ss, mx, blockDim.x, red[it & 1]);
         const float rn = a.normalise ? 1.f / sqrtf(s.x / (float)a.D + a.eps) : 1.f;
         float inv = 1.f;
         if (sizeof(TO) == 1) {
@@ -243,10 +313,17 @@ template <typename T, int VEC, int VPT>
 __global__ void __launch_bounds__(kRowThreads) norm_bwd_kernel(NormBwdArgs a, int tpr)
 {
     __shared__ float2 red[2][kRowThreads / 32];
-    extern __shared__ float dws[];  // [rows per block][D], where a block holds several rows
+    extern __shared__ uint4 ahead_slots[];
     const int t = threadIdx.x & (tpr - 1), rpb = blockDim.x / tpr, nv = a.D / VEC;
     const int64_t step = (int64_t)gridDim.x * rpb;
     const T *gy = (const T *)a.dy, *gh = (const T *)a.h, *gd = (const T *)a.dh;
+    RowsAhead<T, VEC, VPT, 3> in;
+    in.slots = ahead_slots;
+    in.src[0] = gy; in.src[1] = gh; in.src[2] = gd;
+    in.ld[0] = a.ld_dy; in.ld[1] = a.ld_h; in.ld[2] = a.ld_dh;
+    in.step = step; in.M = a.M; in.t = t; in.tpr = tpr; in.nv = nv;
+    int64_t row = (int64_t)blockIdx.x * rpb + threadIdx.x / tpr;
+    in.start(row);
     float w[VPT][VEC], dw[VPT][VEC];
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
@@ -256,58 +333,65 @@ __global__ void __launch_bounds__(kRowThreads) norm_bwd_kernel(NormBwdArgs a, in
             w[i][j] = c < a.D ? weight_at(a.w, a.w_dt, c) : 0.f;
             dw[i][j] = 0.f;
         }
-    Raw<T, VEC> yr[VPT], hr[VPT], dr[VPT];
-    auto fetch = [&](int64_t row) {
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int v = t + i * tpr;
-            if (v < nv && row < a.M) {
-                yr[i].load(gy + row * a.ld_dy + (int64_t)v * VEC);
-                hr[i].load(gh + row * a.ld_h + (int64_t)v * VEC);
-                if (gd) dr[i].load(gd + row * a.ld_dh + (int64_t)v * VEC);
-            }
-        }
-    };
-    int64_t row = (int64_t)blockIdx.x * rpb + threadIdx.x / tpr;
-    fetch(row);
-    const int64_t rounds = (a.M - (int64_t)blockIdx.x * rpb + step - 1) / step;
-    for (int64_t it = 0; it < rounds; ++it, row += step) {
-        float h[VPT][VEC], dy[VPT][VEC], dh[VPT][VEC];
+    const int rounds = (int)((a.M - (int64_t)blockIdx.x * rpb + step - 1) / step);
+    for (int it = 0; it < rounds; ++it, row += step) {
+        // (the row's elements are read from their slots twice: held in registers they would cost occupancy)
+        constexpr bool kTwice = RowsAhead<T, VEC, VPT, 3>::kAsync;
+        float hk[kTwice ? 1 : VPT][VEC], dyk[kTwice ? 1 : VPT][VEC], dhk[kTwice ? 1 : VPT][VEC];
         float ss = 0.f, sd = 0.f;
+        in.ready();
+        const bool live = row < a.M;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const bool in = t + i * tpr < nv && row < a.M;
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) h[i][j] = dy[i][j] = dh[i][j] = 0.f;
-            if (in) {
-                hr[i].to(h[i]);
-                yr[i].to(dy[i]);
-                if (gd) dr[i].to(dh[i]);
-            }
+            if (!(t + i * tpr < nv && live)) continue;
+            float h[VEC], dy[VEC];
+            in.get(it, 0, i, dy);
+            in.get(it, 1, i, h);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
-                ss = fmaf(h[i][j], h[i][j], ss);
-                sd = fmaf(w[i][j] * dy[i][j], h[i][j], sd);
+                ss = fmaf(h[j], h[j], ss);
+                sd = fmaf(w[i][j] * dy[j], h[j], sd);
+            }
+            if constexpr (!kTwice) {
+                hk[i][0] = h[0];
+                dyk[i][0] = dy[0];
+                dhk[i][0] = 0.f;
+                if (gd) in.get(it, 2, i, dhk[i]);
             }
         }
         const int64_t cur = row;
-        fetch(row + step);
-        const float2 s = row_reduce<false>(ss, sd, tpr, red[it & 1]);
+        if constexpr (!kTwice) in.next(row, it);
+        const float2 s = row_reduce<kSum>(ss, sd, tpr, red[it & 1]);
         const float rn = 1.f / sqrtf(s.x / (float)a.D + a.eps);
-        const float c = s.y / (float)a.D * rn * rn;
-        if (cur >= a.M) continue;
+        const float c = s.y / (float)a.D * rn * rn * rn;  // dx = dh + w dy / n - h c
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int v = t + i * tpr;
-            if (v >= nv) continue;
-            float dx[VEC];
+            if (!(v < nv && live)) continue;
+            float h[VEC], dy[VEC], dx[VEC];
+            if constexpr (kTwice) {
+                in.get(it, 0, i, dy);
+                in.get(it, 1, i, h);
+                if (gd) {
+                    in.get(it, 2, i, dx);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) dx[j] = 0.f;
+                }
+            } else {
+                dy[0] = dyk[i][0];
+                h[0] = hk[i][0];
+                dx[0] = dhk[i][0];
+            }
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
-                dx[j] = dh[i][j] + (w[i][j] * dy[i][j] - h[i][j] * c) * rn;
-                dw[i][j] = fmaf(dy[i][j], h[i][j] * rn, dw[i][j]);
+                const float g = dy[j] * rn;
+                dx[j] = fmaf(-h[j], c, fmaf(w[i][j], g, dx[j]));
+                dw[i][j] = fmaf(g, h[j], dw[i][j]);
             }
             put<VEC>((T *)a.dx + cur * a.D + (int64_t)v * VEC, dx);
         }
+        if constexpr (kTwice) in.next(row, it);
     }
     if (!a.dw) return;
     if (rpb == 1) {
@@ -318,7 +402,11 @@ __global__ void __launch_bounds__(kRowThreads) norm_bwd_kernel(NormBwdArgs a, in
                 for (int j = 0; j < VEC; ++j) a.part[(int64_t)blockIdx.x * a.D + (t + i * tpr) * VEC + j] = dw[i][j];
         return;
     }
+    // several rows per block: their sums meet in the slots, [rows per block][D]
+    float *dws = (float *)ahead_slots;
     const int grp = threadIdx.x / tpr;
+    if constexpr (RowsAhead<T, VEC, VPT, 3>::kAsync) copies_wait<0>();
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
         if (t + i * tpr < nv)
@@ -346,7 +434,7 @@ __global__ void __launch_bounds__(kRowThreads) norm_bwd_wide_kernel(NormBwdArgs 
             ss = fmaf(h, h, ss);
             sd = fmaf(weight_at(a.w, a.w_dt, c) * to_f(gy[row * a.ld_dy + c]), h, sd);
         }
-        const float2 s = row_reduce<false>(ss, sd, blockDim.x, red[it & 1]);
+        const float2 s = row_reduce<kSum>(ss, sd, blockDim.x, red[it & 1]);
         const float rn = 1.f / sqrtf(s.x / (float)a.D + a.eps);
         const float k = s.y / (float)a.D * rn * rn;
         if (threadIdx.x == 0 && a.rstd) a.rstd[row] = rn;  // (only dw needs it)
@@ -372,29 +460,71 @@ __global__ void __launch_bounds__(256) norm_dw_wide_kernel(NormBwdArgs a)
 
 bool aligned16(const void *p, int64_t ld, int esz) { return ((uintptr_t)p & 15) == 0 && (ld * esz) % 16 == 0; }
 
-// Threads of a row, elements of a thread and the block: one group of VEC elements a thread while the row
-// fits a block of 512 so, else two, else four (or 16 single elements).
+// Groups (16 bytes, or single elements) of a row per thread, threads per row, the block.  The statistics' exchange
+// costs a thread about as many instructions as twenty elements do, and with one group a thread the kernels are
+// bound by instructions before they are by memory (16384 rows of 2048 in bf16: norm 33.0 us at 75 % of all issue
+// slots, 28.4 with four groups; backward 67.5 us, 59.0 with four and 53.9 with two, whose weight sums leave registers
+// for more threads), so a thread takes up to four (backward: two) as long as every SM has a thousand threads; few
+// rows are spread over as many threads as they have groups.
 struct RowPlan {
     int vec, vpt, tpr, threads;
 };
-RowPlan plan_rows(int D, int esz, bool vec_ok)
+RowPlan plan_rows(int64_t M, int D, int esz, bool vec_ok, bool backward, int num_sms)
 {
     RowPlan p;
     p.vec = vec_ok ? 16 / esz : 1;
-    const int nv = (D + p.vec - 1) / p.vec;
-    p.vpt = p.vec == 1 ? 4 : 1;
-    while (nv > kRowThreads * p.vpt) p.vpt *= p.vec == 1 ? 4 : 2;
-    p.tpr = 1;
-    while (p.tpr * p.vpt < nv) p.tpr *= 2;
-    p.threads = p.tpr < 128 ? 128 : p.tpr;
+    const int nv = (D + p.vec - 1) / p.vec, least = vec_ok ? 1 : 4;
+    const int most = vec_ok ? (backward ? 2 : kMaxGroups) : backward ? least : kMaxSingles;
+    auto threads_of = [&](int vpt) {
+        int t = 1;
+        while (t * vpt < nv) t *= 2;
+        return t;
+    };
+    p.vpt = most;
+    while (threads_of(p.vpt) > kRowThreads) p.vpt *= vec_ok ? 2 : 4;  // (the backward's most, where it does not hold a row)
+    while (p.vpt > least && threads_of(p.vpt / (vec_ok ? 2 : 4)) <= kRowThreads && M * threads_of(p.vpt) < (int64_t)num_sms * 1024)
+        p.vpt /= vec_ok ? 2 : 4;
+    p.tpr = threads_of(p.vpt);
+    // (backward: two rows of 2048 a block, whose dw meet before they are written)
+    const int block = backward ? 256 : 128;
+    p.threads = p.tpr < block ? block : p.tpr;
     return p;
 }
 
 int64_t norm_blocks(int64_t M, const RowPlan &p, int num_sms)
 {
     const int64_t need = (M + p.threads / p.tpr - 1) / (p.threads / p.tpr);
-    const int64_t most = (int64_t)num_sms * (1024 / p.threads);
+    // what the registers (and the rows ahead in shared memory) leave room for
+    const int room = p.vec > 1 ? (p.vpt == 1 ? 1024 : p.vpt == 2 ? 768 : 512) : p.vpt == 4 ? 768 : 512;
+    const int64_t most = (int64_t)num_sms * (room > p.threads ? room / p.threads : 1);
     return need < most ? need : most;
+}
+
+// launches with the dynamic shared memory allowed once per device
+template <typename F, typename A>
+cudaError_t launch_rows(F *kern, std::atomic<uint64_t> &seen, const A &a, unsigned grid, const RowPlan &p, size_t bytes, cudaStream_t st)
+{
+    if (bytes > 40 * 1024 && first_on_device(seen)) {  // (beside the static 256 bytes)
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+        if (e != cudaSuccess) return e;
+        done_on_device(seen);
+    }
+    kern<<<grid, p.threads, bytes, st>>>(a, p.tpr);
+    return cudaGetLastError();
+}
+template <typename T, typename TO, int VEC, int VPT>
+cudaError_t norm_rows(const NormArgs &a, const RowPlan &p, unsigned grid, cudaStream_t st)
+{
+    static std::atomic<uint64_t> seen;
+    return launch_rows(norm_kernel<T, TO, VEC, VPT>, seen, a, grid, p, RowsAhead<T, VEC, VPT, 2>::bytes(p.threads), st);
+}
+template <typename T, int VEC, int VPT>
+cudaError_t norm_bwd_rows(const NormBwdArgs &a, const RowPlan &p, unsigned grid, cudaStream_t st)
+{
+    static std::atomic<uint64_t> seen;
+    const size_t ring = RowsAhead<T, VEC, VPT, 3>::bytes(p.threads);
+    const size_t sums = p.threads > p.tpr ? (size_t)(p.threads / p.tpr) * a.D * sizeof(float) : 0;
+    return launch_rows(norm_bwd_kernel<T, VEC, VPT>, seen, a, grid, p, ring > sums ? ring : sums, st);
 }
 
 template <typename T, typename TO>
@@ -409,19 +539,12 @@ cudaError_t norm_go(const NormArgs &a, cudaStream_t st)
     }
     const bool ok = a.D % V == 0 && aligned16(a.x, a.ldx, sizeof(T)) && (!a.r || aligned16(a.r, a.ldr, sizeof(T))) &&
                     ((uintptr_t)a.y & 15) == 0 && ((uintptr_t)a.h & 15) == 0;
-    const RowPlan p = plan_rows(a.D, sizeof(T), ok);
+    const RowPlan p = plan_rows(a.M, a.D, sizeof(T), ok, false, sms);
     const unsigned grid = (unsigned)norm_blocks(a.M, p, sms);
-    if (p.vec == 1) {
-        if (p.vpt == 4) norm_kernel<T, TO, 1, 4><<<grid, p.threads, 0, st>>>(a, p.tpr);
-        else norm_kernel<T, TO, 1, 16><<<grid, p.threads, 0, st>>>(a, p.tpr);
-    } else if (p.vpt == 1) {
-        norm_kernel<T, TO, V, 1><<<grid, p.threads, 0, st>>>(a, p.tpr);
-    } else if (p.vpt == 2) {
-        norm_kernel<T, TO, V, 2><<<grid, p.threads, 0, st>>>(a, p.tpr);
-    } else {
-        norm_kernel<T, TO, V, kRowElems / V><<<grid, p.threads, 0, st>>>(a, p.tpr);
-    }
-    return cudaGetLastError();
+    if (p.vec == 1) return p.vpt == 4 ? norm_rows<T, TO, 1, 4>(a, p, grid, st) : norm_rows<T, TO, 1, kMaxSingles>(a, p, grid, st);
+    if (p.vpt == 1) return norm_rows<T, TO, V, 1>(a, p, grid, st);
+    if (p.vpt == 2) return norm_rows<T, TO, V, 2>(a, p, grid, st);
+    return norm_rows<T, TO, V, kMaxGroups>(a, p, grid, st);
 }
 
 bool bwd_vec(const NormBwdArgs &a, int esz)
@@ -437,28 +560,28 @@ cudaError_t norm_bwd_go(const NormBwdArgs &a, int sms, cudaStream_t st)
 {
     constexpr int V = 16 / (int)sizeof(T);
     int64_t parts;
+    cudaError_t e = cudaSuccess;
     if (norm_bwd_wide(a.D)) {
         const int64_t most = (int64_t)sms * 4;
         norm_bwd_wide_kernel<T><<<(unsigned)(a.M < most ? a.M : most), kRowThreads, 0, st>>>(a);
         parts = a.M < kWideParts ? a.M : kWideParts;
         if (a.dw) norm_dw_wide_kernel<T><<<dim3((unsigned)((a.D + 255) / 256), (unsigned)parts), 256, 0, st>>>(a);
     } else {
-        const RowPlan p = plan_rows(a.D, sizeof(T), bwd_vec(a, sizeof(T)));
+        const RowPlan p = plan_rows(a.M, a.D, sizeof(T), bwd_vec(a, sizeof(T)), true, sms);
         const unsigned grid = (unsigned)norm_blocks(a.M, p, sms);
         parts = grid;
-        const size_t sm = p.threads > p.tpr ? (size_t)(p.threads / p.tpr) * a.D * sizeof(float) : 0;
         if (p.vec == 1) {
-            if (p.vpt == 4) norm_bwd_kernel<T, 1, 4><<<grid, p.threads, sm, st>>>(a, p.tpr);
-            else norm_bwd_kernel<T, 1, 16><<<grid, p.threads, sm, st>>>(a, p.tpr);
+            if (p.vpt == 4) e = norm_bwd_rows<T, 1, 4>(a, p, grid, st);
+            else e = norm_bwd_rows<T, 1, kMaxSingles>(a, p, grid, st);
         } else if (p.vpt == 1) {
-            norm_bwd_kernel<T, V, 1><<<grid, p.threads, sm, st>>>(a, p.tpr);
+            e = norm_bwd_rows<T, V, 1>(a, p, grid, st);
         } else if (p.vpt == 2) {
-            norm_bwd_kernel<T, V, 2><<<grid, p.threads, sm, st>>>(a, p.tpr);
+            e = norm_bwd_rows<T, V, 2>(a, p, grid, st);
         } else {
-            norm_bwd_kernel<T, V, kRowElems / V><<<grid, p.threads, sm, st>>>(a, p.tpr);
+            e = norm_bwd_rows<T, V, kMaxGroups>(a, p, grid, st);
         }
     }
-    const cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess || !a.dw) return e;
     return launch_colsum_finish(a.part, parts, a.D, a.dw, st);
 }
@@ -472,9 +595,9 @@ int norm_bwd_parts(int64_t M, int D, gdn_dtype dt, int num_sms)
     if (norm_bwd_wide(D)) return (int)(M < kWideParts ? M : kWideParts);
     // the larger of the vector and the single-element form (alignment is not known here)
     const int esz = dt == GDN_F32 ? 4 : 2;
-    int64_t parts = norm_blocks(M, plan_rows(D, esz, false), num_sms);
+    int64_t parts = norm_blocks(M, plan_rows(M, D, esz, false, true, num_sms), num_sms);
     if (D % (16 / esz) == 0) {
-        const int64_t q = norm_blocks(M, plan_rows(D, esz, true), num_sms);
+        const int64_t q = norm_blocks(M, plan_rows(M, D, esz, true, true, num_sms), num_sms);
         parts = q > parts ? q : parts;
     }
     return (int)parts;
