@@ -33,24 +33,34 @@ constexpr int kEpiWarps = 8, kThreads = 32 * (kEpiWarps + 2);
 constexpr int kABytes = 128 * 128;       // a CTA's rows of A, 128 bytes of k (or 64 k rows of 2 x 64 m)
 constexpr int kStageBuf = 32 * 128;      // one epilogue box: 32 rows of 128 bytes
 
-template <int BN> struct Geo {
+// Shared memory of a CTA.  BN = 128: two 128-byte-wide blocks of k per stage, so that eight products and not four
+// follow each wait (16384 x 2048 x 2048: 112 -> 87 us; with BN = 256, whose products take twice as long, it is flat).
+// BOXES: epilogue boxes per warp; with two, the second box of extra values loads, and the first box of results
+// leaves, beside the arithmetic.
+template <int BN, int BOXES> struct Geo {
+    static constexpr int kAtoms = BN == 256 ? 1 : 2;
     static constexpr int kB = BN / 2 * 128;
-    static constexpr int kStage = kABytes + kB;
-    static constexpr int kStages = BN == 256 ? 6 : 8;
+    static constexpr int kAtom = kABytes + kB;  // 128 bytes of k
+    static constexpr int kStage = kAtoms * kAtom;
+    static constexpr int kBoxBytes = kEpiWarps * BOXES * kStageBuf;
+    static constexpr int kBars(int stages) { return 2 * stages + 4 + 2 * kEpiWarps; }
+    static constexpr int kStages = (227 * 1024 - 1024 - kBoxBytes - 512) / kStage;
     static constexpr int kTmem = 2 * BN;  // two accumulators
-    static constexpr int kBars = 2 * kStages + 4 + kEpiWarps;
-    static constexpr int kSmem = 1024 + kStages * kStage + kEpiWarps * kStageBuf + kBars * 8 + 16;
+    static constexpr int kSmem = 1024 + kStages * kStage + kBoxBytes + kBars(kStages) * 8 + 16;
 };
-static_assert(Geo<256>::kSmem <= 227 * 1024 && Geo<128>::kSmem <= 227 * 1024, "shared memory budget");
+static_assert(Geo<256, 1>::kStages == 6 && Geo<256, 2>::kStages == 5 && Geo<128, 1>::kStages == 4, "stages");
+static_assert(Geo<256, 1>::kSmem <= 227 * 1024 && Geo<256, 2>::kSmem <= 227 * 1024 && Geo<128, 1>::kSmem <= 227 * 1024,
+              "shared memory budget");
 
 struct TcMaps {
-    CUtensorMap a, b, out, up, extra, out2;
+    CUtensorMap a, b, out, up, extra;
 };
 struct TcParams {
     int64_t M, N;            // output rows; output columns (gated: F)
-    int kblocks;             // blocks of 128 bytes of k
+    int kblocks;             // stages of k
     int mt, nt;              // tiles of 256 rows, of BN accumulator columns
-    int tma_out, tma_extra, tma_out2;
+    int tma_out, tma_extra;                   // boxes of them by TMA (else element by element)
+    int vec_w, vec_up, vec_bias, vec_out2;    // 16-byte accesses of them
     const float *x_scale, *w_scale, *bias;
     int act;
     const void *extra;
@@ -170,65 +180,97 @@ __device__ __forceinline__ void box_out(const uint8_t *buf, void *dst, int64_t l
 }
 __device__ __forceinline__ float lo_bf16(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float hi_bf16(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
-// 32 values of a box row, 16 bytes at a time; `part`: which 32 columns
-template <typename TO> __device__ __forceinline__ void row_get(const uint8_t *buf, int r, int part, float *v);
-template <> __device__ __forceinline__ void row_get<__nv_bfloat16>(const uint8_t *buf, int r, int part, float *v)
+// 16 columns of a box row (group g of them), 16 bytes at a time
+__device__ __forceinline__ void row_get(const uint8_t *buf, int r, int g, float *v, __nv_bfloat16)
 {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const uint4 u = *(const uint4 *)(buf + r * 128 + (((4 * part + j) ^ (r & 7)) << 4));
+    for (int j = 0; j < 2; ++j) {
+        const uint4 u = *(const uint4 *)(buf + r * 128 + (((2 * g + j) ^ (r & 7)) << 4));
         v[8 * j] = lo_bf16(u.x); v[8 * j + 1] = hi_bf16(u.x);
         v[8 * j + 2] = lo_bf16(u.y); v[8 * j + 3] = hi_bf16(u.y);
         v[8 * j + 4] = lo_bf16(u.z); v[8 * j + 5] = hi_bf16(u.z);
         v[8 * j + 6] = lo_bf16(u.w); v[8 * j + 7] = hi_bf16(u.w);
     }
 }
-template <> __device__ __forceinline__ void row_get<float>(const uint8_t *buf, int r, int, float *v)
+__device__ __forceinline__ void row_get(const uint8_t *buf, int r, int g, float *v, float)
 {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) *(float4 *)(v + 4 * j) = *(const float4 *)(buf + r * 128 + ((j ^ (r & 7)) << 4));
+    for (int j = 0; j < 4; ++j) *(float4 *)(v + 4 * j) = *(const float4 *)(buf + r * 128 + (((4 * g + j) ^ (r & 7)) << 4));
 }
-template <typename TO> __device__ __forceinline__ void row_put(uint8_t *buf, int r, int part, const float *v);
-template <> __device__ __forceinline__ void row_put<__nv_bfloat16>(uint8_t *buf, int r, int part, const float *v)
+__device__ __forceinline__ void row_put(uint8_t *buf, int r, int g, const float *v, __nv_bfloat16)
 {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) *(uint4 *)(buf + r * 128 + (((4 * part + j) ^ (r & 7)) << 4)) = pack8(v + 8 * j);
+    for (int j = 0; j < 2; ++j) *(uint4 *)(buf + r * 128 + (((2 * g + j) ^ (r & 7)) << 4)) = pack8(v + 8 * j);
 }
-template <> __device__ __forceinline__ void row_put<float>(uint8_t *buf, int r, int, const float *v)
+__device__ __forceinline__ void row_put(uint8_t *buf, int r, int g, const float *v, float)
 {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) *(float4 *)(buf + r * 128 + ((j ^ (r & 7)) << 4)) = *(const float4 *)(v + 4 * j);
+    for (int j = 0; j < 4; ++j) *(float4 *)(buf + r * 128 + (((4 * g + j) ^ (r & 7)) << 4)) = *(const float4 *)(v + 4 * j);
 }
-
+// 16 values of a row of global memory from column c on (an output without a box of its own)
+__device__ __forceinline__ void line_out(__nv_bfloat16 *dst, int64_t c, int64_t N, int vec, const float *v)
+{
+    if (vec && c + 16 <= N) {
+        *(uint4 *)dst = pack8(v);
+        *(uint4 *)(dst + 8) = pack8(v + 8);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (c + j < N) dst[j] = __float2bfloat16_rn(v[j]);
+    }
+}
+// 16 per-column values (the same for every row): by 16-byte loads where `vec` and all exist; 0 past the end
+__device__ __forceinline__ void columns(const float *src, int64_t c, int64_t N, int vec, float *v)
+{
+    if (vec && c + 16 <= N) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) *(float4 *)(v + 4 * j) = __ldg((const float4 *)(src + c) + j);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = c + j < N ? __ldg(src + c + j) : 0.f;
+    }
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float *r)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+        : "r"(taddr));
+}
 // keeps the uses of freshly loaded accumulators behind the wait for them
-__device__ __forceinline__ void pin32(float *v)
+__device__ __forceinline__ void pin16(float *v)
 {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) asm volatile("" : "+f"(v[j]));
+    for (int j = 0; j < 16; ++j) asm volatile("" : "+f"(v[j]));
 }
 
-// Sum over the warp's 32 rows of each of 32 columns (one per register): halves of the columns change hands
-// at every step, 31 shuffles in all; lane l ends with the sum of column l.
+// Sum over the warp's 32 rows of each of 16 columns (one per register): halves of the columns change hands at every
+// step, 16 shuffles in all; lanes 2 c and 2 c + 1 end with the sum of column c.
 __device__ __forceinline__ float column_sums(float *v, int lane)
 {
 #pragma unroll
-    for (int w = 16; w; w >>= 1) {
-        const bool high = lane & w;
+    for (int w = 8; w; w >>= 1) {
+        const bool high = lane & (2 * w);
 #pragma unroll
         for (int j = 0; j < w; ++j) {
             const float give = high ? v[j] : v[j + w], keep = high ? v[j + w] : v[j];
-            v[j] = keep + __shfl_xor_sync(0xffffffffu, give, w);
+            v[j] = keep + __shfl_xor_sync(0xffffffffu, give, 2 * w);
         }
     }
-    return v[0];
+    return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
 }
 
+constexpr int kLinearBoxes = 1;
+template <int N> struct Count { static constexpr int value = N; };
+
 // LAYOUT 0: A and B K-major; 1: B MN-major; 2: both MN-major
-template <bool FP8, int LAYOUT, int EPI, int BN, typename TO>
+template <bool FP8, int LAYOUT, int EPI, int BN, int BOXES, typename TO>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
 {
-    using G = Geo<BN>;
+    using G = Geo<BN, BOXES>;
+    constexpr int kAtoms = G::kAtoms;
     constexpr bool kGated = EPI == kEpiGated || EPI == kEpiGatedBwd;
     constexpr bool kExtra = EPI != kEpiGated;
     constexpr bool kPrecise = sizeof(TO) == 4;
@@ -237,9 +279,9 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *boxes = sm + G::kStages * G::kStage;
-    uint64_t *full = (uint64_t *)(boxes + kEpiWarps * kStageBuf);
+    uint64_t *full = (uint64_t *)(boxes + G::kBoxBytes);
     uint64_t *empty = full + G::kStages, *tfull = empty + G::kStages, *tempty = tfull + 2, *ebar = tempty + 2;
-    uint32_t *tslot = (uint32_t *)(ebar + kEpiWarps);
+    uint32_t *tslot = (uint32_t *)(ebar + 2 * kEpiWarps);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_rank();
     const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
@@ -254,7 +296,7 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
             mbar_init(&tfull[i], 1);
             mbar_init(&tempty[i], 2 * kEpiWarps);
         }
-        for (int i = 0; i < kEpiWarps; ++i) mbar_init(&ebar[i], 1);
+        for (int i = 0; i < 2 * kEpiWarps; ++i) mbar_init(&ebar[i], 1);
         fence_mbar_init();
     }
     if (warp == kEpiWarps + 1) {
@@ -286,21 +328,24 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
             for (int kb = 0; kb < p.kblocks; ++kb) {
                 if (!(ok = __all_sync(0xffffffffu, wait_cta(&empty[s], ph)))) break;
                 if (elect_one_sync()) {
-                    uint8_t *sa = sm + s * G::kStage, *sb = sa + kABytes;
                     if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * G::kStage);
                     const uint32_t bar = leader_addr(&full[s]);
-                    const int k0 = kb * (FP8 ? 128 : 64);
-                    if (LAYOUT == 2) {
-                        pair_load(sa, &maps.a, m0, k0, bar);
-                        pair_load(sa + 8192, &maps.a, m0 + 64, k0, bar);
-                    } else {
-                        pair_load(sa, &maps.a, k0, m0, bar);
-                    }
-                    if (LAYOUT >= 1) {
 #pragma unroll
-                        for (int j = 0; j < BN / 128; ++j) pair_load(sb + 8192 * j, &maps.b, n0 + 64 * j, k0, bar);
-                    } else {
-                        pair_load(sb, &maps.b, k0, n0, bar);
+                    for (int at = 0; at < kAtoms; ++at) {
+                        uint8_t *sa = sm + s * G::kStage + at * G::kAtom, *sb = sa + kABytes;
+                        const int k0 = (kb * kAtoms + at) * (FP8 ? 128 : 64);  // (past the end: zeros)
+                        if (LAYOUT == 2) {
+                            pair_load(sa, &maps.a, m0, k0, bar);
+                            pair_load(sa + 8192, &maps.a, m0 + 64, k0, bar);
+                        } else {
+                            pair_load(sa, &maps.a, k0, m0, bar);
+                        }
+                        if (LAYOUT >= 1) {
+#pragma unroll
+                            for (int j = 0; j < BN / 128; ++j) pair_load(sb + 8192 * j, &maps.b, n0 + 64 * j, k0, bar);
+                        } else {
+                            pair_load(sb, &maps.b, k0, n0, bar);
+                        }
                     }
                 }
                 __syncwarp();
@@ -335,8 +380,9 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
                     if (++s == G::kStages) { s = 0; ph ^= 1; }
                     if (elect_one_sync()) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            pair_mma<FP8>(tmem + acc * BN, da + j * sa_step, db + j * sb_step, id, (kb | j) != 0);
+                        for (int j = 0; j < 4 * kAtoms; ++j)
+                            pair_mma<FP8>(tmem + acc * BN, da + (j >> 2) * (G::kAtom >> 4) + (j & 3) * sa_step,
+                                          db + (j >> 2) * (G::kAtom >> 4) + (j & 3) * sb_step, id, (kb | j) != 0);
                         pair_commit(rel);
                         if (kb + 1 == p.kblocks) pair_commit(&tfull[acc]);
                     }
@@ -348,14 +394,14 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
         // ---------------------------------------------------------------- epilogue
         constexpr int kCols = Box<TO>::kCols;
         const int q = warp & 3, half = warp >> 2;
-        constexpr int kChunks = kOutN / kCols / 2;  // boxes of this warp (its half of the columns), one at a time
-        uint8_t *buf = boxes + warp * kStageBuf;
-        uint64_t *eb = ebar + warp;
-        uint32_t n = 0, eph = 0;
-        // the box is free again, for copies by either path
-        auto box_free = [&] {
+        constexpr int kChunks = kOutN / kCols / 2;  // boxes' worth of columns of this warp
+        uint8_t *const boxes0 = boxes + warp * BOXES * kStageBuf;
+        uint64_t *const eb = ebar + 2 * warp;
+        uint32_t n = 0, eph = 0;  // (a phase bit per box)
+        // every box but the `pending` latest is free again, for copies by either path
+        auto boxes_free = [&](auto pending) {
             fence_proxy_async();
-            if (lane == 0) tma_store_wait_read0();
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(decltype(pending)::value) : "memory");
             __syncwarp();
         };
         for (int t = pair; t < tiles && ok; t += pairs, ++n) {
@@ -366,20 +412,21 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
             const uint32_t tl = tmem + acc * BN + ((uint32_t)(q * 32) << 16);
             auto col_of = [&](int c) { return (int64_t)ni * kOutN + (half * kChunks + c) * kCols; };
             auto live = [&](int c) { return col_of(c) < p.N && row0 < p.M; };
-            // the box of extra (residual, dy, dh) of chunk c
+            auto box_of = [&](int c) { return boxes0 + (c % BOXES) * kStageBuf; };
+            // extra values (residual, dy, dh) of chunk c into its box
             auto fetch = [&](int c) {
                 if (!kExtra || !p.extra || !live(c)) return;
                 if (p.tma_extra) {
                     if (lane == 0) {
-                        mbar_arrive_expect_tx(eb, kStageBuf);
-                        tma_load_2d(buf, &maps.extra, (int)col_of(c), (int)row0, eb);
+                        mbar_arrive_expect_tx(&eb[c % BOXES], kStageBuf);
+                        tma_load_2d(box_of(c), &maps.extra, (int)col_of(c), (int)row0, &eb[c % BOXES]);
                     }
                 } else {
-                    box_in<TO>(buf, p.extra, p.ld_extra, row0, col_of(c), p.M, p.N, lane);
+                    box_in<TO>(box_of(c), p.extra, p.ld_extra, row0, col_of(c), p.M, p.N, lane);
                 }
             };
-            // the finished box to its place: columns col0 ..., of an output with its own map
-            auto store = [&](const CUtensorMap *map, int tma, void *dst, int64_t ld, int64_t col0) {
+            // a finished box to its place: columns col0 ..., of an output with its own map
+            auto store = [&](uint8_t *buf, const CUtensorMap *map, int tma, void *dst, int64_t ld, int64_t col0) {
                 if (tma) {
                     fence_proxy_async();
                     __syncwarp();
@@ -391,129 +438,122 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
                     box_out<TO>(buf, dst, ld, row0, col0, p.M, p.N, lane);
                 }
             };
-            box_free();
-            fetch(0);  // under the tile's products
+            boxes_free(Count<0>());
+            for (int c = 0; c < BOXES && c < kChunks; ++c) fetch(c);  // under the tile's products
             const float sx = FP8 && p.x_scale && row < p.M ? p.x_scale[row] : 1.f;
             ok = wait_cluster(&tfull[acc], (n >> 1) & 1);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < kChunks; ++c) {
                 const int64_t col0 = col_of(c);
-                if (c > 0) {
-                    box_free();
+                uint8_t *const buf = box_of(c);
+                if (c >= BOXES) {
+                    boxes_free(Count<BOXES - 1>());
                     fetch(c);
                 }
                 if (!live(c)) continue;
                 if (kExtra && p.extra && p.tma_extra) {
-                    ok = wait_cta(eb, eph);
+                    ok = wait_cta(&eb[c % BOXES], (eph >> (c % BOXES)) & 1);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
-                    eph ^= 1;
+                    eph ^= 1u << (c % BOXES);
                 }
-                uint32_t up[EPI == kEpiGatedBwd ? 32 : 1], hp[EPI == kEpiGatedBwd ? 32 : 1];
+                // 16 columns at a time, in a loop that stays rolled: unrolled over a box, an activation's code left the
+                // instruction cache at every pass (erf's gradient took 19 K cycles a tile, 2.5 times its arithmetic).
+                // The next accumulators load under this group's arithmetic.
+                constexpr int kGroups = kCols / 16;
+                const int tc = (half * kChunks + c) * kCols;  // accumulator column
+                float nv[16], nu[kGated ? 16 : 1];
+                tmem_ld16(tl + tc, nv);
+                if constexpr (kGated) tmem_ld16(tl + BN / 2 + tc, nu);
+#pragma unroll 1
+                for (int g = 0; g < kGroups; ++g) {
+                    const int64_t cg = col0 + 16 * g;
+                    float v[16], u[16], e[16];
+                    if (kExtra && p.extra) row_get(buf, lane, g, e, TO());
+                    tmem_ld_wait();
+                    pin16(nv);
 #pragma unroll
-                for (int part = 0; part < kCols / 32; ++part) {
-                    const int64_t cp = col0 + 32 * part;
-                    const int tc = (half * kChunks + c) * kCols + 32 * part;  // accumulator column
-                    float v[32];
-                    tmem_ld32(tl + tc, (uint32_t *)v);
-                    if constexpr (!kGated) {
-                        tmem_ld_wait();
-                        pin32(v);
-                        if (FP8 && p.w_scale) {
-                            const float ws = cp + lane < p.N ? p.w_scale[cp + lane] : 1.f;
+                    for (int j = 0; j < 16; ++j) v[j] = nv[j];
+                    if constexpr (kGated) {
+                        pin16(nu);
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) v[j] *= sx * __shfl_sync(0xffffffffu, ws, j);
-                        }
-                        if (p.bias) {
-                            const float bs = cp + lane < p.N ? p.bias[cp + lane] : 0.f;
+                        for (int j = 0; j < 16; ++j) u[j] = nu[j];
+                    }
+                    if (g + 1 < kGroups) {
+                        tmem_ld16(tl + tc + 16 * (g + 1), nv);
+                        if constexpr (kGated) tmem_ld16(tl + BN / 2 + tc + 16 * (g + 1), nu);
+                    }
+                    if (FP8 && p.w_scale) {
+                        float ws[16];
+                        columns(p.w_scale, cg, p.N, p.vec_w, ws);
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) v[j] += __shfl_sync(0xffffffffu, bs, j);
-                        }
-                        if constexpr (EPI == kEpiLinear) {
-                            if (p.act != GDN_ACT_NONE)
-                                with_act(p.act, [&](auto tag) {
+                        for (int j = 0; j < 16; ++j) v[j] *= sx * ws[j];
+                        if constexpr (kGated) {
+                            columns(p.w_scale + p.N, cg, p.N, p.vec_up, ws);
 #pragma unroll
-                                    for (int j = 0; j < 32; ++j) v[j] = act_value<kPrecise, decltype(tag)::value>(v[j]);
-                                });
-                            if (p.extra) {
-                                float e[32];
-                                row_get<TO>(buf, lane, part, e);
-#pragma unroll
-                                for (int j = 0; j < 32; ++j) v[j] += e[j];
-                            }
-                            row_put<TO>(buf, lane, part, v);
-                        } else {
-                            float e[32];
-                            row_get<TO>(buf, lane, part, e);
-                            const bool in = row < p.M;
-                            with_act(p.act, [&](auto tag) {
-#pragma unroll
-                                for (int j = 0; j < 32; ++j) {
-                                    float a, d;
-                                    act_both<kPrecise, decltype(tag)::value>(v[j], a, d);
-                                    v[j] = in ? e[j] * d : 0.f;
-                                }
-                            });
-                            row_put<TO>(buf, lane, part, v);
-                            if (p.colpart) {
-                                const float s = column_sums(v, lane);
-                                if (cp + lane < p.N) p.colpart[(row0 >> 5) * p.N + cp + lane] = s;
-                            }
-                        }
-                    } else {
-                        float u[32];
-                        tmem_ld32(tl + BN / 2 + tc, (uint32_t *)u);
-                        tmem_ld_wait();
-                        pin32(v);
-                        pin32(u);
-                        if (FP8 && p.w_scale) {
-                            const bool in = cp + lane < p.N;
-                            const float wg = in ? p.w_scale[cp + lane] : 1.f, wu = in ? p.w_scale[p.N + cp + lane] : 1.f;
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) {
-                                v[j] *= sx * __shfl_sync(0xffffffffu, wg, j);
-                                u[j] *= sx * __shfl_sync(0xffffffffu, wu, j);
-                            }
-                        }
-                        if constexpr (EPI == kEpiGated) {
-                            with_act(p.act, [&](auto tag) {
-#pragma unroll
-                                for (int j = 0; j < 32; ++j) v[j] = act_value<kPrecise, decltype(tag)::value>(v[j]) * u[j];
-                            });
-                            row_put<TO>(buf, lane, part, v);
-                        } else {
-                            float e[32];
-                            row_get<TO>(buf, lane, part, e);
-                            with_act(p.act, [&](auto tag) {
-#pragma unroll
-                                for (int j = 0; j < 32; j += 2) {
-                                    float a0, d0, a1, d1;
-                                    act_both<kPrecise, decltype(tag)::value>(v[j], a0, d0);
-                                    act_both<kPrecise, decltype(tag)::value>(v[j + 1], a1, d1);
-                                    hp[16 * part + j / 2] = pack_bf16(a0 * u[j], a1 * u[j + 1]);
-                                    up[16 * part + j / 2] = pack_bf16(e[j] * a0, e[j + 1] * a1);
-                                    v[j] = e[j] * u[j] * d0;
-                                    v[j + 1] = e[j + 1] * u[j + 1] * d1;
-                                }
-                            });
-                            row_put<TO>(buf, lane, part, v);
+                            for (int j = 0; j < 16; ++j) u[j] *= sx * ws[j];
                         }
                     }
-                }
-                store(&maps.out, p.tma_out, p.out, p.ldo, col0);
-                if constexpr (EPI == kEpiGatedBwd) {
-                    auto second = [&](const uint32_t *w, const CUtensorMap *map, int tma, void *dst, int64_t ld) {
-                        box_free();
+                    if (!kGated && p.bias) {
+                        float bs[16];
+                        columns(p.bias, cg, p.N, p.vec_bias, bs);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            *(uint4 *)(buf + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-                        store(map, tma, dst, ld, col0);
-                    };
-                    second(up, &maps.up, p.tma_out, (TO *)p.out + p.N, p.ldo);
-                    if (p.out2) second(hp, &maps.out2, p.tma_out2, p.out2, p.ldo2);
+                        for (int j = 0; j < 16; ++j) v[j] += bs[j];
+                    }
+                    if constexpr (EPI == kEpiLinear) {
+                        if (p.act != GDN_ACT_NONE)
+                            with_act(p.act, [&](auto tag) {
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) v[j] = act_value<kPrecise, decltype(tag)::value>(v[j]);
+                            });
+                        if (p.extra) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) v[j] += e[j];
+                        }
+                    } else if constexpr (EPI == kEpiDact) {
+                        const bool in = row < p.M;
+                        with_act(p.act, [&](auto tag) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                float a, d;
+                                act_both<kPrecise, decltype(tag)::value>(v[j], a, d);
+                                v[j] = in ? e[j] * d : 0.f;
+                            }
+                        });
+                    } else if constexpr (EPI == kEpiGated) {
+                        with_act(p.act, [&](auto tag) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) v[j] = act_value<kPrecise, decltype(tag)::value>(v[j]) * u[j];
+                        });
+                    } else {
+                        float h[16];
+                        with_act(p.act, [&](auto tag) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                float a, d;
+                                act_both<kPrecise, decltype(tag)::value>(v[j], a, d);
+                                h[j] = a * u[j];
+                                v[j] = e[j] * u[j] * d;
+                                u[j] = e[j] * a;
+                            }
+                        });
+                        row_put(boxes0 + kStageBuf, lane, g, u, TO());  // (one chunk a tile: the second box is free)
+                        if (p.out2 && row < p.M) line_out((__nv_bfloat16 *)p.out2 + row * p.ldo2 + cg, cg, p.N, p.vec_out2, h);
+                    }
+                    row_put(buf, lane, g, v, TO());
+                    if (EPI == kEpiDact && p.colpart) {
+                        const float sum = column_sums(v, lane);
+                        const int64_t cc = cg + (lane >> 1);
+                        if (!(lane & 1) && cc < p.N) p.colpart[(row0 >> 5) * p.N + cc] = sum;
+                    }
+                }
+                store(buf, &maps.out, p.tma_out, p.out, p.ldo, col0);
+                if constexpr (EPI == kEpiGatedBwd) {
+                    static_assert(kChunks == 1 && BOXES == 2, "boxes of the two halves");
+                    store(boxes0 + kStageBuf, &maps.up, p.tma_out, (TO *)p.out + p.N, p.ldo, col0);
                 }
             }
             if (!ok) break;
@@ -554,7 +594,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder()
 
 size_t esz(gdn_dtype t) { return t == GDN_F32 ? 4 : t == GDN_BF16 ? 2 : 1; }
 
-template <bool FP8, int LAYOUT, int EPI, int BN, typename TO>
+template <bool FP8, int LAYOUT, int EPI, int BN, int BOXES, typename TO>
 cudaError_t go(const GemmArgs &g, cudaStream_t st)
 {
     constexpr bool gated = EPI == kEpiGated || EPI == kEpiGatedBwd;
@@ -566,7 +606,7 @@ cudaError_t go(const GemmArgs &g, cudaStream_t st)
     if (!a_ok || !b_ok) return cudaErrorInvalidValue;
     TcParams p{};
     p.M = g.M; p.N = g.N;
-    const int per = FP8 ? 128 : 64;
+    const int per = Geo<BN, BOXES>::kAtoms * (FP8 ? 128 : 64);
     p.kblocks = (int)((g.K + per - 1) / per);
     p.mt = (int)((g.M + 255) / 256);
     p.nt = (int)((g.N + (gated ? BN / 2 : BN) - 1) / (gated ? BN / 2 : BN));
@@ -581,19 +621,22 @@ cudaError_t go(const GemmArgs &g, cudaStream_t st)
         return cudaErrorInvalidValue;
     p.tma_extra = g.extra && tma_ok(g.extra, g.ld_extra, g.M, eo);
     if (p.tma_extra && !make_operand_map(&maps.extra, g.out_dt, g.extra, g.N, g.M, g.ld_extra, 32)) return cudaErrorInvalidValue;
-    p.tma_out2 = g.out2 && tma_ok(g.out2, g.ldo2, g.M, eo);
-    if (p.tma_out2 && !make_operand_map(&maps.out2, g.out_dt, g.out2, g.N, g.M, g.ldo2, 32)) return cudaErrorInvalidValue;
+    auto on16 = [](const void *q) { return ((uintptr_t)q & 15) == 0; };
+    p.vec_w = on16(g.w_scale);
+    p.vec_up = g.w_scale && on16(g.w_scale + g.N);
+    p.vec_bias = on16(g.bias);
+    p.vec_out2 = tma_ok(g.out2, g.ldo2, 2, eo);
 
-    auto *kern = gemm_tc_kernel<FP8, LAYOUT, EPI, BN, TO>;
+    auto *kern = gemm_tc_kernel<FP8, LAYOUT, EPI, BN, BOXES, TO>;
     static std::atomic<uint64_t> seen;
     if (first_on_device(seen)) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<BN>::kSmem);
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<BN, BOXES>::kSmem);
         if (e != cudaSuccess) return e;
         done_on_device(seen);
     }
     const int64_t tiles = (int64_t)p.mt * p.nt;
     const int pairs = (int)(tiles < device_sm_count() / 2 ? tiles : device_sm_count() / 2);
-    kern<<<2 * pairs, kThreads, Geo<BN>::kSmem, st>>>(maps, p);
+    kern<<<2 * pairs, kThreads, Geo<BN, BOXES>::kSmem, st>>>(maps, p);
     return cudaGetLastError();
 }
 
@@ -601,13 +644,14 @@ template <bool FP8, int LAYOUT, int EPI, typename TO>
 cudaError_t pick(const GemmArgs &g, cudaStream_t st)
 {
     if constexpr (EPI == kEpiGated || EPI == kEpiGatedBwd) {
-        return go<FP8, LAYOUT, EPI, 256, TO>(g, st);
+        return go<FP8, LAYOUT, EPI, 256, EPI == kEpiGatedBwd ? 2 : 1, TO>(g, st);
     } else {
-        // Whole rounds of tiles over the pairs of SMs decide: a round of 128-column tiles costs a little over half
-        // of one of 256 columns (its products re-read A), but fills a ragged last round better.
+        // Whole rounds of tiles over the pairs of SMs decide: a round of 128-column tiles takes 0.58 of one of 256
+        // columns (6.2 and 10.7 us at K = 2048: its products re-read A), but fills a ragged last round better.
         const int64_t pairs = device_sm_count() / 2, mt = (g.M + 255) / 256;
         const auto rounds = [&](int bn) { return (mt * ((g.N + bn - 1) / bn) + pairs - 1) / pairs; };
-        return 0.56 * rounds(128) < rounds(256) ? go<FP8, LAYOUT, EPI, 128, TO>(g, st) : go<FP8, LAYOUT, EPI, 256, TO>(g, st);
+        if (0.58 * rounds(128) < rounds(256)) return go<FP8, LAYOUT, EPI, 128, 1, TO>(g, st);
+        return go<FP8, LAYOUT, EPI, 256, EPI == kEpiDact ? 2 : kLinearBoxes, TO>(g, st);
     }
 }
 

@@ -24,11 +24,36 @@ __device__ __forceinline__ float logistic(float z)
 constexpr float kGeluA = 1.5957691216057308f;            // 2 sqrt(2 / pi): 0.5 (1 + tanh u) = logistic(2 u)
 constexpr float kGeluB = 1.5957691216057308f * 0.044715f;
 
+// The normal distribution function Phi(z) = erfc(-z / sqrt 2) / 2.  Not PRECISE: the Chebyshev fit of erfc in
+// Press et al., Numerical Recipes, section 6.2 ("erfcc": fractional error below 1.2e-7 everywhere, so that the small
+// tail keeps its digits), one division and one exponential without a branch; erff takes both of its branches in
+// almost every warp.
+template <bool PRECISE>
+__device__ __forceinline__ float normal_cdf(float z)
+{
+    if (PRECISE) return 0.5f * erfcf(z * -0.70710678118654752f);
+    const float x = fabsf(z) * 0.70710678118654752f;
+    float t;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(0.5f, x, 1.f)));
+    float p = 0.17087277f;
+    p = fmaf(p, t, -0.82215223f);
+    p = fmaf(p, t, 1.48851587f);
+    p = fmaf(p, t, -1.13520398f);
+    p = fmaf(p, t, 0.27886807f);
+    p = fmaf(p, t, -0.18628806f);
+    p = fmaf(p, t, 0.09678418f);
+    p = fmaf(p, t, 0.37409196f);
+    p = fmaf(p, t, 1.00002368f);
+    p = fmaf(p, t, -1.26551223f);
+    const float half = 0.5f * t * __expf(fmaf(-x, x, p));  // erfc(x) / 2
+    return z < 0.f ? half : 1.f - half;
+}
+
 template <bool PRECISE, int ACT>
 __device__ __forceinline__ float act_value(float z)
 {
     if (ACT == GDN_ACT_SILU) return z * logistic<PRECISE>(z);
-    if (ACT == GDN_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+    if (ACT == GDN_ACT_GELU) return z * normal_cdf<PRECISE>(z);
     if (ACT == GDN_ACT_GELU_TANH) return z * logistic<PRECISE>(z * (kGeluA + kGeluB * z * z));
     if (ACT == GDN_ACT_RELU) return z < 0.f ? 0.f : z;  // (keeps a NaN)
     if (ACT == GDN_ACT_SIGMOID) return logistic<PRECISE>(z);
@@ -43,7 +68,7 @@ __device__ __forceinline__ void act_both(float z, float &v, float &d)
         v = z * p;
         d = p * (1.f + z * (1.f - p));
     } else if (ACT == GDN_ACT_GELU) {
-        const float c = 0.5f * (1.f + erff(z * 0.70710678118654752f));
+        const float c = normal_cdf<PRECISE>(z);
         const float e = PRECISE ? expf(-0.5f * z * z) : __expf(-0.5f * z * z);
         v = z * c;
         d = c + z * e * 0.3989422804014327f;  // 1 / sqrt(2 pi)
