@@ -5,8 +5,8 @@
 // 128 rows of A and half of B's rows in its shared memory and one M = 256 tcgen05.mma reads both halves,
 // so that every byte staged serves twice the products of a single CTA's tile (a single CTA's 128 x 256
 // instruction with both operands in shared memory takes 161 cycles here for 128 cycles of work; the pair's
-// reads half of B per SM).  Roles per CTA: eight epilogue warps, one thread that issues the TMA loads, one
-// that issues the products (in the pair's first CTA only).  The accumulators are double-buffered in tensor
+// reads half of B per SM).  Roles per CTA: eight epilogue warps (each half of the columns of 32 rows), one
+// that issues the TMA loads, one that issues the products (in the pair's first CTA only).  The accumulators are double-buffered in tensor
 // memory, so a tile's epilogue runs under the next tile's products; a persistent grid walks the tiles in
 // groups of eight row tiles, which keeps one group's operands in L2.
 //
@@ -31,36 +31,32 @@ constexpr unsigned long long kLimitNs = 2000000000ull;
 
 constexpr int kEpiWarps = 8, kThreads = 32 * (kEpiWarps + 2);
 constexpr int kABytes = 128 * 128;       // a CTA's rows of A, 128 bytes of k (or 64 k rows of 2 x 64 m)
-constexpr int kStageBuf = 32 * 128;      // one epilogue box: 32 rows of 128 bytes
 
-// Shared memory of a CTA.  BN = 128: two 128-byte-wide blocks of k per stage, so that eight products and not four
-// follow each wait (16384 x 2048 x 2048: 112 -> 87 us; with BN = 256, whose products take twice as long, it is flat).
-// BOXES: epilogue boxes per warp; with two, the second box of extra values loads, and the first box of results
-// leaves, beside the arithmetic.
-template <int BN, int BOXES> struct Geo {
+// Shared memory of a CTA: operands, and each epilogue warp's column vectors (scales and bias of its half of a tile;
+// the tensors of the epilogue go between registers and global memory).  BN = 128: two
+// 128-byte-wide blocks of k per stage, so that eight products and not four follow each wait (16384 x 2048 x 2048:
+// 112 -> 87 us; with BN = 256, whose products take twice as long, it is flat).
+template <int BN> struct Geo {
     static constexpr int kAtoms = BN == 256 ? 1 : 2;
     static constexpr int kB = BN / 2 * 128;
     static constexpr int kAtom = kABytes + kB;  // 128 bytes of k
     static constexpr int kStage = kAtoms * kAtom;
-    static constexpr int kBoxBytes = kEpiWarps * BOXES * kStageBuf;
-    static constexpr int kBars(int stages) { return 2 * stages + 4 + 2 * kEpiWarps; }
-    static constexpr int kStages = (227 * 1024 - 1024 - kBoxBytes - 512) / kStage;
+    static constexpr int kColBytes = kEpiWarps * 2 * 128 * 4;
+    static constexpr int kStages = (227 * 1024 - 1024 - kColBytes - 256) / kStage;
+    static constexpr int kBars = 2 * kStages + 4;
     static constexpr int kTmem = 2 * BN;  // two accumulators
-    static constexpr int kSmem = 1024 + kStages * kStage + kBoxBytes + kBars(kStages) * 8 + 16;
+    static constexpr int kSmem = 1024 + kStages * kStage + kColBytes + kBars * 8 + 16;
+    static_assert(kStages >= 3 && kSmem <= 227 * 1024, "shared memory budget");
 };
-static_assert(Geo<256, 1>::kStages == 6 && Geo<256, 2>::kStages == 5 && Geo<128, 1>::kStages == 4, "stages");
-static_assert(Geo<256, 1>::kSmem <= 227 * 1024 && Geo<256, 2>::kSmem <= 227 * 1024 && Geo<128, 1>::kSmem <= 227 * 1024,
-              "shared memory budget");
 
 struct TcMaps {
-    CUtensorMap a, b, out, up, extra;
+    CUtensorMap a, b;
 };
 struct TcParams {
     int64_t M, N;            // output rows; output columns (gated: F)
     int kblocks;             // stages of k
     int mt, nt;              // tiles of 256 rows, of BN accumulator columns
-    int tma_out, tma_extra;                   // boxes of them by TMA (else element by element)
-    int vec_w, vec_up, vec_bias, vec_out2;    // 16-byte accesses of them
+    int vec_extra, vec_out, vec_out2;  // what their rows allow: accesses of 32 bytes (2), of 16 (1) or of elements
     const float *x_scale, *w_scale, *bias;
     int act;
     const void *extra;
@@ -148,87 +144,121 @@ __device__ __forceinline__ void pair_commit(uint64_t *bar)
         : "memory");
 }
 
-// ------------------------------------------------------------------ epilogue boxes
-template <typename TO> struct Box {
-    static constexpr int kCols = 128 / (int)sizeof(TO);
-    // byte offset of (row, column) in a 128-byte-swizzled box
-    static __device__ __forceinline__ uint32_t at(int r, int c)
+// ------------------------------------------------------------------ epilogue rows
+// A thread has 16 columns of its row at a time: 32 (fp32: 64) bytes, whole sectors of memory, so they go straight
+// between registers and global memory.  (Boxes in shared memory with TMA stores cost a pipeline stage or two, waits
+// for their reuse, and were slower by 2 to 8 %.)
+// `vec`: 2 where every row allows 32-byte accesses, 1 where it allows 16-byte ones, 0 for single elements.
+__device__ __forceinline__ void load32(const void *p, uint32_t *lo, uint32_t *hi)
+{
+    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(lo[0]), "=r"(lo[1]), "=r"(lo[2]), "=r"(lo[3]), "=r"(hi[0]), "=r"(hi[1]), "=r"(hi[2]), "=r"(hi[3])
+                 : "l"(p)
+                 : "memory");
+}
+__device__ __forceinline__ void store32(void *p, const uint4 &a, const uint4 &b)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x),
+                 "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+}
+template <typename TO> struct Line;
+template <> struct Line<__nv_bfloat16> {
+    uint4 a, b;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p, int vec)
     {
-        const int b = c * (int)sizeof(TO);
-        return (uint32_t)(r * 128 + ((((b >> 4) ^ (r & 7)) << 4) | (b & 15)));
+        if (vec == 2) {
+            load32(p, &a.x, &b.x);
+        } else {
+            a = *(const uint4 *)p;
+            b = *((const uint4 *)p + 1);
+        }
+    }
+    __device__ __forceinline__ void set(int j, __nv_bfloat16 v)  // (j a constant)
+    {
+        uint32_t &w = j < 2 ? a.x : j < 4 ? a.y : j < 6 ? a.z : j < 8 ? a.w : j < 10 ? b.x : j < 12 ? b.y : j < 14 ? b.z : b.w;
+        const uint32_t u = __bfloat16_as_ushort(v);
+        w = j & 1 ? (w & 0xffffu) | (u << 16) : (w & 0xffff0000u) | u;
+    }
+    __device__ __forceinline__ void zero() { a = b = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float *v) const
+    {
+        const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            v[2 * j] = __uint_as_float(u[j] << 16);
+            v[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+        }
     }
 };
-// Rows that TMA cannot address (a pitch or a base off 16 bytes): element by element, 32 columns at a time
-template <typename TO>
-__device__ __forceinline__ void box_in(uint8_t *buf, const void *src, int64_t ld, int64_t row0, int64_t col0, int64_t M, int64_t N, int lane)
-{
-    for (int r = 0; r < 32; ++r)
-        for (int c = lane; c < Box<TO>::kCols; c += 32) {
-            const bool in = row0 + r < M && col0 + c < N;
-            *(TO *)(buf + Box<TO>::at(r, c)) = in ? ((const TO *)src)[(row0 + r) * ld + col0 + c] : from_f<TO>(0.f);
-        }
-    __syncwarp();
-}
-template <typename TO>
-__device__ __forceinline__ void box_out(const uint8_t *buf, void *dst, int64_t ld, int64_t row0, int64_t col0, int64_t M, int64_t N, int lane)
-{
-    __syncwarp();
-    for (int r = 0; r < 32; ++r)
-        for (int c = lane; c < Box<TO>::kCols; c += 32)
-            if (row0 + r < M && col0 + c < N) ((TO *)dst)[(row0 + r) * ld + col0 + c] = *(const TO *)(buf + Box<TO>::at(r, c));
-    __syncwarp();
-}
-__device__ __forceinline__ float lo_bf16(uint32_t u) { return __uint_as_float(u << 16); }
-__device__ __forceinline__ float hi_bf16(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
-// 16 columns of a box row (group g of them), 16 bytes at a time
-__device__ __forceinline__ void row_get(const uint8_t *buf, int r, int g, float *v, __nv_bfloat16)
-{
+template <> struct Line<float> {
+    float v_[16];
+    __device__ __forceinline__ void load(const float *p, int)
+    {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const uint4 u = *(const uint4 *)(buf + r * 128 + (((2 * g + j) ^ (r & 7)) << 4));
-        v[8 * j] = lo_bf16(u.x); v[8 * j + 1] = hi_bf16(u.x);
-        v[8 * j + 2] = lo_bf16(u.y); v[8 * j + 3] = hi_bf16(u.y);
-        v[8 * j + 4] = lo_bf16(u.z); v[8 * j + 5] = hi_bf16(u.z);
-        v[8 * j + 6] = lo_bf16(u.w); v[8 * j + 7] = hi_bf16(u.w);
+        for (int j = 0; j < 4; ++j) *(float4 *)(v_ + 4 * j) = *((const float4 *)p + j);
+    }
+    __device__ __forceinline__ void set(int j, float v) { v_[j] = v; }
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v_[j] = 0.f;
+    }
+    __device__ __forceinline__ void get(float *v) const
+    {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = v_[j];
+    }
+};
+// `p`: column c of a row; columns from N on (and rows that do not exist: `in`) read as zero and are not written
+template <typename TO>
+__device__ __forceinline__ void line_in(Line<TO> &l, const TO *p, bool in, int64_t c, int64_t N, int vec)
+{
+    if (in && vec && c + 16 <= N) {
+        l.load(p, vec);
+    } else {
+        l.zero();
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (in && c + j < N) l.set(j, p[j]);
     }
 }
-__device__ __forceinline__ void row_get(const uint8_t *buf, int r, int g, float *v, float)
+__device__ __forceinline__ void line_put(__nv_bfloat16 *p, const float *v, int vec)
+{
+    const uint4 a = pack8(v), b = pack8(v + 8);
+    if (vec == 2) {
+        store32(p, a, b);
+    } else {
+        *(uint4 *)p = a;
+        *((uint4 *)p + 1) = b;
+    }
+}
+__device__ __forceinline__ void line_put(float *p, const float *v, int)
 {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) *(float4 *)(v + 4 * j) = *(const float4 *)(buf + r * 128 + (((4 * g + j) ^ (r & 7)) << 4));
+    for (int j = 0; j < 4; ++j) *((float4 *)p + j) = *(const float4 *)(v + 4 * j);
 }
-__device__ __forceinline__ void row_put(uint8_t *buf, int r, int g, const float *v, __nv_bfloat16)
+template <typename TO>
+__device__ __forceinline__ void line_out(TO *p, bool in, int64_t c, int64_t N, int vec, const float *v)
 {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) *(uint4 *)(buf + r * 128 + (((2 * g + j) ^ (r & 7)) << 4)) = pack8(v + 8 * j);
-}
-__device__ __forceinline__ void row_put(uint8_t *buf, int r, int g, const float *v, float)
-{
-#pragma unroll
-    for (int j = 0; j < 4; ++j) *(float4 *)(buf + r * 128 + (((4 * g + j) ^ (r & 7)) << 4)) = *(const float4 *)(v + 4 * j);
-}
-// 16 values of a row of global memory from column c on (an output without a box of its own)
-__device__ __forceinline__ void line_out(__nv_bfloat16 *dst, int64_t c, int64_t N, int vec, const float *v)
-{
+    if (!in) return;
     if (vec && c + 16 <= N) {
-        *(uint4 *)dst = pack8(v);
-        *(uint4 *)(dst + 8) = pack8(v + 8);
+        line_put(p, v, vec);
     } else {
 #pragma unroll
         for (int j = 0; j < 16; ++j)
-            if (c + j < N) dst[j] = __float2bfloat16_rn(v[j]);
+            if (c + j < N) p[j] = from_f<TO>(v[j]);
     }
 }
-// 16 per-column values (the same for every row): by 16-byte loads where `vec` and all exist; 0 past the end
-__device__ __forceinline__ void columns(const float *src, int64_t c, int64_t N, int vec, float *v)
+// `count` per-column values from column c on into a warp's shared memory (0 past the end), and 16 of them back
+__device__ __forceinline__ void columns_in(float *dst, const float *src, int64_t c, int64_t N, int count, int lane)
 {
-    if (vec && c + 16 <= N) {
+    for (int i = lane; i < count; i += 32) dst[i] = c + i < N ? __ldg(src + c + i) : 0.f;
+}
+__device__ __forceinline__ void columns(const float *src, float *v)
+{
 #pragma unroll
-        for (int j = 0; j < 4; ++j) *(float4 *)(v + 4 * j) = __ldg((const float4 *)(src + c) + j);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = c + j < N ? __ldg(src + c + j) : 0.f;
-    }
+    for (int j = 0; j < 4; ++j) *(float4 *)(v + 4 * j) = *((const float4 *)src + j);
 }
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float *r)
 {
@@ -261,27 +291,24 @@ __device__ __forceinline__ float column_sums(float *v, int lane)
     return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
 }
 
-constexpr int kLinearBoxes = 1;
-template <int N> struct Count { static constexpr int value = N; };
-
 // LAYOUT 0: A and B K-major; 1: B MN-major; 2: both MN-major
-template <bool FP8, int LAYOUT, int EPI, int BN, int BOXES, typename TO>
+template <bool FP8, int LAYOUT, int EPI, int BN, typename TO>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
 {
-    using G = Geo<BN, BOXES>;
-    constexpr int kAtoms = G::kAtoms;
     constexpr bool kGated = EPI == kEpiGated || EPI == kEpiGatedBwd;
     constexpr bool kExtra = EPI != kEpiGated;
     constexpr bool kPrecise = sizeof(TO) == 4;
     constexpr int kOutN = kGated ? BN / 2 : BN;  // output columns of a tile
     static_assert(!kGated || BN == 256, "a gated tile is 128 gate and 128 up columns");
+    using G = Geo<BN>;
+    constexpr int kAtoms = G::kAtoms;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    uint8_t *boxes = sm + G::kStages * G::kStage;
-    uint64_t *full = (uint64_t *)(boxes + G::kBoxBytes);
-    uint64_t *empty = full + G::kStages, *tfull = empty + G::kStages, *tempty = tfull + 2, *ebar = tempty + 2;
-    uint32_t *tslot = (uint32_t *)(ebar + 2 * kEpiWarps);
+    float *const cols = (float *)(sm + G::kStages * G::kStage);
+    uint64_t *full = (uint64_t *)(sm + G::kStages * G::kStage + G::kColBytes);
+    uint64_t *empty = full + G::kStages, *tfull = empty + G::kStages, *tempty = tfull + 2;
+    uint32_t *tslot = (uint32_t *)(tempty + 2);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_rank();
     const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
@@ -296,7 +323,6 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
             mbar_init(&tfull[i], 1);
             mbar_init(&tempty[i], 2 * kEpiWarps);
         }
-        for (int i = 0; i < 2 * kEpiWarps; ++i) mbar_init(&ebar[i], 1);
         fence_mbar_init();
     }
     if (warp == kEpiWarps + 1) {
@@ -392,177 +418,132 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
         }
     } else {
         // ---------------------------------------------------------------- epilogue
-        constexpr int kCols = Box<TO>::kCols;
-        const int q = warp & 3, half = warp >> 2;
-        constexpr int kChunks = kOutN / kCols / 2;  // boxes' worth of columns of this warp
-        uint8_t *const boxes0 = boxes + warp * BOXES * kStageBuf;
-        uint64_t *const eb = ebar + 2 * warp;
-        uint32_t n = 0, eph = 0;  // (a phase bit per box)
-        // every box but the `pending` latest is free again, for copies by either path
-        auto boxes_free = [&](auto pending) {
-            fence_proxy_async();
-            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(decltype(pending)::value) : "memory");
-            __syncwarp();
-        };
+        constexpr int kGroups = kOutN / 32;           // groups of 16 columns of this warp: half of the tile's
+        const int q = warp & 3, half = warp >> 2;     // its 32 rows, its half
+        const TO *const extra = (const TO *)p.extra;
+        float *const cs = cols + warp * 256;          // scales (gate, up), bias
+        uint32_t n = 0;
         for (int t = pair; t < tiles && ok; t += pairs, ++n) {
             int mi, ni;
             place(t, mi, ni);
             const int64_t row0 = (int64_t)mi * 256 + rank * 128 + q * 32, row = row0 + lane;
+            const int64_t col0 = (int64_t)ni * kOutN + half * (kOutN / 2);
+            const bool in = row < p.M;
             const uint32_t acc = n & 1;
-            const uint32_t tl = tmem + acc * BN + ((uint32_t)(q * 32) << 16);
-            auto col_of = [&](int c) { return (int64_t)ni * kOutN + (half * kChunks + c) * kCols; };
-            auto live = [&](int c) { return col_of(c) < p.N && row0 < p.M; };
-            auto box_of = [&](int c) { return boxes0 + (c % BOXES) * kStageBuf; };
-            // extra values (residual, dy, dh) of chunk c into its box
-            auto fetch = [&](int c) {
-                if (!kExtra || !p.extra || !live(c)) return;
-                if (p.tma_extra) {
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(&eb[c % BOXES], kStageBuf);
-                        tma_load_2d(box_of(c), &maps.extra, (int)col_of(c), (int)row0, &eb[c % BOXES]);
-                    }
-                } else {
-                    box_in<TO>(box_of(c), p.extra, p.ld_extra, row0, col_of(c), p.M, p.N, lane);
-                }
-            };
-            // a finished box to its place: columns col0 ..., of an output with its own map
-            auto store = [&](uint8_t *buf, const CUtensorMap *map, int tma, void *dst, int64_t ld, int64_t col0) {
-                if (tma) {
-                    fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) {
-                        tma_store_2d(map, buf, (int)col0, (int)row0);
-                        tma_store_commit();
-                    }
-                } else {
-                    box_out<TO>(buf, dst, ld, row0, col0, p.M, p.N, lane);
-                }
-            };
-            boxes_free(Count<0>());
-            for (int c = 0; c < BOXES && c < kChunks; ++c) fetch(c);  // under the tile's products
-            const float sx = FP8 && p.x_scale && row < p.M ? p.x_scale[row] : 1.f;
+            const uint32_t tl = tmem + acc * BN + ((uint32_t)(q * 32) << 16) + half * (kOutN / 2);
+            const int64_t left = p.N - col0;  // columns of this warp's half that exist
+            const int groups = row0 >= p.M || left <= 0 ? 0 : left < kGroups * 16 ? (int)((left + 15) / 16) : kGroups;
+            // extra values (residual, dy, dh) and accumulators of the next group load under this group's arithmetic
+            Line<TO> ne;
+            if (kExtra && extra && groups) line_in(ne, extra + row * p.ld_extra + col0, in, col0, p.N, p.vec_extra);
+            const float sx = FP8 && p.x_scale && in ? p.x_scale[row] : 1.f;
+            if (groups && (p.bias || (FP8 && p.w_scale))) {
+                __syncwarp();  // (the last tile's are read)
+                if (FP8 && p.w_scale) columns_in(cs, p.w_scale, col0, p.N, kOutN / 2, lane);
+                if (FP8 && kGated && p.w_scale) columns_in(cs + kOutN / 2, p.w_scale + p.N, col0, p.N, kOutN / 2, lane);
+                if (!kGated && p.bias) columns_in(cs + 128, p.bias, col0, p.N, kOutN / 2, lane);
+                __syncwarp();
+            }
             ok = wait_cluster(&tfull[acc], (n >> 1) & 1);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
+            float nv[16], nu[kGated ? 16 : 1];
+            if (groups) {
+                tmem_ld16(tl, nv);
+                if constexpr (kGated) tmem_ld16(tl + BN / 2, nu);
+            }
+            // (rolled: unrolled over a tile's columns, an activation's code left the instruction cache at every pass)
 #pragma unroll 1
-            for (int c = 0; c < kChunks; ++c) {
-                const int64_t col0 = col_of(c);
-                uint8_t *const buf = box_of(c);
-                if (c >= BOXES) {
-                    boxes_free(Count<BOXES - 1>());
-                    fetch(c);
+            for (int g = 0; g < groups; ++g) {
+                const int64_t cg = col0 + 16 * g;
+                float v[16], u[16], e[16];
+                if (kExtra && extra) {
+                    ne.get(e);
+                    if (g + 1 < groups) line_in(ne, extra + row * p.ld_extra + cg + 16, in, cg + 16, p.N, p.vec_extra);
                 }
-                if (!live(c)) continue;
-                if (kExtra && p.extra && p.tma_extra) {
-                    ok = wait_cta(&eb[c % BOXES], (eph >> (c % BOXES)) & 1);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    eph ^= 1u << (c % BOXES);
-                }
-                // 16 columns at a time, in a loop that stays rolled: unrolled over a box, an activation's code left the
-                // instruction cache at every pass (erf's gradient took 19 K cycles a tile, 2.5 times its arithmetic).
-                // The next accumulators load under this group's arithmetic.
-                constexpr int kGroups = kCols / 16;
-                const int tc = (half * kChunks + c) * kCols;  // accumulator column
-                float nv[16], nu[kGated ? 16 : 1];
-                tmem_ld16(tl + tc, nv);
-                if constexpr (kGated) tmem_ld16(tl + BN / 2 + tc, nu);
-#pragma unroll 1
-                for (int g = 0; g < kGroups; ++g) {
-                    const int64_t cg = col0 + 16 * g;
-                    float v[16], u[16], e[16];
-                    if (kExtra && p.extra) row_get(buf, lane, g, e, TO());
-                    tmem_ld_wait();
-                    pin16(nv);
+                tmem_ld_wait();
+                pin16(nv);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) v[j] = nv[j];
+                for (int j = 0; j < 16; ++j) v[j] = nv[j];
+                if constexpr (kGated) {
+                    pin16(nu);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) u[j] = nu[j];
+                }
+                if (g + 1 < groups) {
+                    tmem_ld16(tl + 16 * (g + 1), nv);
+                    if constexpr (kGated) tmem_ld16(tl + BN / 2 + 16 * (g + 1), nu);
+                }
+                if (FP8 && p.w_scale) {
+                    float ws[16];
+                    columns(cs + 16 * g, ws);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] *= sx * ws[j];
                     if constexpr (kGated) {
-                        pin16(nu);
+                        columns(cs + kOutN / 2 + 16 * g, ws);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) u[j] = nu[j];
-                    }
-                    if (g + 1 < kGroups) {
-                        tmem_ld16(tl + tc + 16 * (g + 1), nv);
-                        if constexpr (kGated) tmem_ld16(tl + BN / 2 + tc + 16 * (g + 1), nu);
-                    }
-                    if (FP8 && p.w_scale) {
-                        float ws[16];
-                        columns(p.w_scale, cg, p.N, p.vec_w, ws);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) v[j] *= sx * ws[j];
-                        if constexpr (kGated) {
-                            columns(p.w_scale + p.N, cg, p.N, p.vec_up, ws);
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) u[j] *= sx * ws[j];
-                        }
-                    }
-                    if (!kGated && p.bias) {
-                        float bs[16];
-                        columns(p.bias, cg, p.N, p.vec_bias, bs);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) v[j] += bs[j];
-                    }
-                    if constexpr (EPI == kEpiLinear) {
-                        if (p.act != GDN_ACT_NONE)
-                            with_act(p.act, [&](auto tag) {
-#pragma unroll
-                                for (int j = 0; j < 16; ++j) v[j] = act_value<kPrecise, decltype(tag)::value>(v[j]);
-                            });
-                        if (p.extra) {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) v[j] += e[j];
-                        }
-                    } else if constexpr (EPI == kEpiDact) {
-                        const bool in = row < p.M;
-                        with_act(p.act, [&](auto tag) {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                float a, d;
-                                act_both<kPrecise, decltype(tag)::value>(v[j], a, d);
-                                v[j] = in ? e[j] * d : 0.f;
-                            }
-                        });
-                    } else if constexpr (EPI == kEpiGated) {
-                        with_act(p.act, [&](auto tag) {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) v[j] = act_value<kPrecise, decltype(tag)::value>(v[j]) * u[j];
-                        });
-                    } else {
-                        float h[16];
-                        with_act(p.act, [&](auto tag) {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                float a, d;
-                                act_both<kPrecise, decltype(tag)::value>(v[j], a, d);
-                                h[j] = a * u[j];
-                                v[j] = e[j] * u[j] * d;
-                                u[j] = e[j] * a;
-                            }
-                        });
-                        row_put(boxes0 + kStageBuf, lane, g, u, TO());  // (one chunk a tile: the second box is free)
-                        if (p.out2 && row < p.M) line_out((__nv_bfloat16 *)p.out2 + row * p.ldo2 + cg, cg, p.N, p.vec_out2, h);
-                    }
-                    row_put(buf, lane, g, v, TO());
-                    if (EPI == kEpiDact && p.colpart) {
-                        const float sum = column_sums(v, lane);
-                        const int64_t cc = cg + (lane >> 1);
-                        if (!(lane & 1) && cc < p.N) p.colpart[(row0 >> 5) * p.N + cc] = sum;
+                        for (int j = 0; j < 16; ++j) u[j] *= sx * ws[j];
                     }
                 }
-                store(buf, &maps.out, p.tma_out, p.out, p.ldo, col0);
-                if constexpr (EPI == kEpiGatedBwd) {
-                    static_assert(kChunks == 1 && BOXES == 2, "boxes of the two halves");
-                    store(boxes0 + kStageBuf, &maps.up, p.tma_out, (TO *)p.out + p.N, p.ldo, col0);
+                if (!kGated && p.bias) {
+                    float bs[16];
+                    columns(cs + 128 + 16 * g, bs);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] += bs[j];
+                }
+                TO *const dst = (TO *)p.out + row * p.ldo + cg;
+                if constexpr (EPI == kEpiLinear) {
+                    if (p.act != GDN_ACT_NONE)
+                        with_act(p.act, [&](auto tag) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) v[j] = act_value<kPrecise, decltype(tag)::value>(v[j]);
+                        });
+                    if (extra) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[j] += e[j];
+                    }
+                } else if constexpr (EPI == kEpiDact) {
+                    with_act(p.act, [&](auto tag) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            float a, d;
+                            act_both<kPrecise, decltype(tag)::value>(v[j], a, d);
+                            v[j] = in ? e[j] * d : 0.f;
+                        }
+                    });
+                } else if constexpr (EPI == kEpiGated) {
+                    with_act(p.act, [&](auto tag) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[j] = act_value<kPrecise, decltype(tag)::value>(v[j]) * u[j];
+                    });
+                } else {
+                    float h[16];
+                    with_act(p.act, [&](auto tag) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            float a, d;
+                            act_both<kPrecise, decltype(tag)::value>(v[j], a, d);
+                            h[j] = a * u[j];
+                            v[j] = e[j] * u[j] * d;
+                            u[j] = e[j] * a;
+                        }
+                    });
+                    line_out(dst + p.N, in, cg, p.N, p.vec_out, u);
+                    if (p.out2) line_out((TO *)p.out2 + row * p.ldo2 + cg, in, cg, p.N, p.vec_out2, h);
+                }
+                line_out(dst, in, cg, p.N, p.vec_out, v);
+                if (EPI == kEpiDact && p.colpart) {
+                    const float sum = column_sums(v, lane);
+                    const int64_t cc = cg + (lane >> 1);
+                    if (!(lane & 1) && cc < p.N) p.colpart[(row0 >> 5) * p.N + cc] = sum;
                 }
             }
-            if (!ok) break;
             // the accumulators are read: hand them back to the issuer
             tc_fence_before();
             __syncwarp();
             if (lane == 0) remote_arrive(leader_addr(&tempty[acc]));
         }
-        if (lane == 0) tma_store_wait0();
     }
     if (!ok) {
         // a wait ran out: give whatever is still in flight a millisecond to land before the memory is let go
@@ -594,10 +575,11 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder()
 
 size_t esz(gdn_dtype t) { return t == GDN_F32 ? 4 : t == GDN_BF16 ? 2 : 1; }
 
-template <bool FP8, int LAYOUT, int EPI, int BN, int BOXES, typename TO>
+template <bool FP8, int LAYOUT, int EPI, int BN, typename TO>
 cudaError_t go(const GemmArgs &g, cudaStream_t st)
 {
     constexpr bool gated = EPI == kEpiGated || EPI == kEpiGatedBwd;
+    using G = Geo<BN>;
     TcMaps maps;
     std::memset(&maps, 0, sizeof(maps));
     const int64_t brows = gated ? 2 * g.N : g.N;
@@ -606,7 +588,7 @@ cudaError_t go(const GemmArgs &g, cudaStream_t st)
     if (!a_ok || !b_ok) return cudaErrorInvalidValue;
     TcParams p{};
     p.M = g.M; p.N = g.N;
-    const int per = Geo<BN, BOXES>::kAtoms * (FP8 ? 128 : 64);
+    const int per = G::kAtoms * (FP8 ? 128 : 64);
     p.kblocks = (int)((g.K + per - 1) / per);
     p.mt = (int)((g.M + 255) / 256);
     p.nt = (int)((g.N + (gated ? BN / 2 : BN) - 1) / (gated ? BN / 2 : BN));
@@ -615,28 +597,24 @@ cudaError_t go(const GemmArgs &g, cudaStream_t st)
     p.out = g.out; p.ldo = g.ldo; p.out2 = g.out2; p.ldo2 = g.ldo2;
     p.colpart = g.colpart;
     const size_t eo = sizeof(TO);
-    p.tma_out = tma_ok(g.out, g.ldo, g.M, eo) && (EPI != kEpiGatedBwd || (g.N * eo) % 16 == 0);
-    if (p.tma_out && !make_operand_map(&maps.out, g.out_dt, g.out, g.N, g.M, g.ldo, 32)) return cudaErrorInvalidValue;
-    if (p.tma_out && EPI == kEpiGatedBwd && !make_operand_map(&maps.up, g.out_dt, (const TO *)g.out + g.N, g.N, g.M, g.ldo, 32))
-        return cudaErrorInvalidValue;
-    p.tma_extra = g.extra && tma_ok(g.extra, g.ld_extra, g.M, eo);
-    if (p.tma_extra && !make_operand_map(&maps.extra, g.out_dt, g.extra, g.N, g.M, g.ld_extra, 32)) return cudaErrorInvalidValue;
-    auto on16 = [](const void *q) { return ((uintptr_t)q & 15) == 0; };
-    p.vec_w = on16(g.w_scale);
-    p.vec_up = g.w_scale && on16(g.w_scale + g.N);
-    p.vec_bias = on16(g.bias);
-    p.vec_out2 = tma_ok(g.out2, g.ldo2, 2, eo);
+    auto allows = [&](const void *q, int64_t ld, size_t also) {
+        const size_t off = (uintptr_t)q | (g.M > 1 ? (size_t)ld * eo : 0) | also;
+        return off % 32 == 0 ? 2 : off % 16 == 0 ? 1 : 0;
+    };
+    p.vec_out = allows(g.out, g.ldo, EPI == kEpiGatedBwd ? g.N * eo : 0);
+    p.vec_extra = allows(g.extra, g.ld_extra, 0);
+    p.vec_out2 = allows(g.out2, g.ldo2, 0);
 
-    auto *kern = gemm_tc_kernel<FP8, LAYOUT, EPI, BN, BOXES, TO>;
+    auto *kern = gemm_tc_kernel<FP8, LAYOUT, EPI, BN, TO>;
     static std::atomic<uint64_t> seen;
     if (first_on_device(seen)) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<BN, BOXES>::kSmem);
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
         if (e != cudaSuccess) return e;
         done_on_device(seen);
     }
     const int64_t tiles = (int64_t)p.mt * p.nt;
     const int pairs = (int)(tiles < device_sm_count() / 2 ? tiles : device_sm_count() / 2);
-    kern<<<2 * pairs, kThreads, Geo<BN, BOXES>::kSmem, st>>>(maps, p);
+    kern<<<2 * pairs, kThreads, G::kSmem, st>>>(maps, p);
     return cudaGetLastError();
 }
 
@@ -644,14 +622,14 @@ template <bool FP8, int LAYOUT, int EPI, typename TO>
 cudaError_t pick(const GemmArgs &g, cudaStream_t st)
 {
     if constexpr (EPI == kEpiGated || EPI == kEpiGatedBwd) {
-        return go<FP8, LAYOUT, EPI, 256, EPI == kEpiGatedBwd ? 2 : 1, TO>(g, st);
+        return go<FP8, LAYOUT, EPI, 256, TO>(g, st);
     } else {
         // Whole rounds of tiles over the pairs of SMs decide: a round of 128-column tiles takes 0.58 of one of 256
         // columns (6.2 and 10.7 us at K = 2048: its products re-read A), but fills a ragged last round better.
         const int64_t pairs = device_sm_count() / 2, mt = (g.M + 255) / 256;
         const auto rounds = [&](int bn) { return (mt * ((g.N + bn - 1) / bn) + pairs - 1) / pairs; };
-        if (0.58 * rounds(128) < rounds(256)) return go<FP8, LAYOUT, EPI, 128, 1, TO>(g, st);
-        return go<FP8, LAYOUT, EPI, 256, EPI == kEpiDact ? 2 : kLinearBoxes, TO>(g, st);
+        if (0.58 * rounds(128) < rounds(256)) return go<FP8, LAYOUT, EPI, 128, TO>(g, st);
+        return go<FP8, LAYOUT, EPI, 256, TO>(g, st);
     }
 }
 
