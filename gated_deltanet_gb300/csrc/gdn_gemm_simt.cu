@@ -60,35 +60,35 @@ __global__ void __launch_bounds__(256) gemm_simt_kernel(GemmArgs g)
         for (int i = 0; i < 4; ++i) {
             const int64_t m = m0 + 4 * ty + i;
             if (m >= g.M) continue;
+            float v[4], d[4];
+            if (EPI == kEpiLinear || EPI == kEpiDact) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (g.bias && n0 + 4 * tx + j < g.N) acc[0][i][j] += g.bias[n0 + 4 * tx + j];
+            }
+#pragma unroll
+            for (int j = 0; j < 4; j += 2) {
+                if (EPI == kEpiLinear || EPI == kEpiGated) act_value<true, ACT>(&acc[0][i][j], v + j);
+                else act_both<true, ACT>(&acc[0][i][j], v + j, d + j);
+            }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int64_t n = n0 + 4 * tx + j;
                 if (n >= g.N) continue;
-                float z = acc[0][i][j];
+                const float u = acc[kB - 1][i][j];
                 if (EPI == kEpiLinear) {
-                    if (g.bias) z += g.bias[n];
-                    z = act_value<true, ACT>(z);
-                    if (extra) z += extra[m * g.ld_extra + n];
-                    out[m * g.ldo + n] = z;
+                    out[m * g.ldo + n] = extra ? v[j] + extra[m * g.ld_extra + n] : v[j];
                 } else if (EPI == kEpiDact) {
-                    if (g.bias) z += g.bias[n];
-                    float v, d;
-                    act_both<true, ACT>(z, v, d);
-                    const float dz = extra[m * g.ld_extra + n] * d;
+                    const float dz = extra[m * g.ld_extra + n] * d[j];
                     out[m * g.ldo + n] = dz;
                     col[j] += dz;
+                } else if (EPI == kEpiGated) {
+                    out[m * g.ldo + n] = v[j] * u;
                 } else {
-                    const float u = acc[kB - 1][i][j];
-                    if (EPI == kEpiGated) {
-                        out[m * g.ldo + n] = act_value<true, ACT>(z) * u;
-                    } else {
-                        float v, d;
-                        act_both<true, ACT>(z, v, d);
-                        const float dh = extra[m * g.ld_extra + n];
-                        out[m * g.ldo + n] = dh * u * d;
-                        out[m * g.ldo + g.N + n] = dh * v;
-                        if (g.out2) ((float *)g.out2)[m * g.ldo2 + n] = v * u;
-                    }
+                    const float dh = extra[m * g.ld_extra + n];
+                    out[m * g.ldo + n] = dh * u * d[j];
+                    out[m * g.ldo + g.N + n] = dh * v[j];
+                    if (g.out2) ((float *)g.out2)[m * g.ldo2 + n] = v[j] * u;
                 }
             }
         }

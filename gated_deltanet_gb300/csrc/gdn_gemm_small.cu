@@ -263,28 +263,33 @@ gemm_small_kernel(const __grid_constant__ SmallMaps maps, const SmallParams p)
                         u[0] += b.x; u[1] += b.y; u[2] += b.z; u[3] += b.w;
                     }
                 }
-                float y[4], y2[4];
+                float y[4], y2[4], a[4], d[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     if (FP8 && p.w_scale) {
                         z[j] *= sx * wg[j];
                         u[j] *= sx * wu[j];
                     }
+                    if (!kGated) z[j] += bias[j];
+                }
+#pragma unroll
+                for (int j = 0; j < 4; j += 2) {
+                    if (EPI == kEpiLinear || EPI == kEpiGated) act_value<kPrecise, ACT>(z + j, a + j);
+                    else act_both<kPrecise, ACT>(z + j, a + j, d + j);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
                     if (EPI == kEpiLinear) {
-                        y[j] = act_value<kPrecise, ACT>(z[j] + bias[j]) + e[j];
+                        y[j] = a[j] + e[j];
                     } else if (EPI == kEpiGated) {
-                        y[j] = act_value<kPrecise, ACT>(z[j]) * u[j];
+                        y[j] = a[j] * u[j];
                     } else if (EPI == kEpiDact) {
-                        float v, d;
-                        act_both<kPrecise, ACT>(z[j] + bias[j], v, d);
-                        y[j] = e[j] * d;
+                        y[j] = e[j] * d[j];
                         col[j] += y[j];
                     } else {
-                        float v, d;
-                        act_both<kPrecise, ACT>(z[j], v, d);
-                        y[j] = e[j] * u[j] * d;
-                        y2[j] = e[j] * v;
-                        z[j] = v * u[j];
+                        y[j] = e[j] * u[j] * d[j];
+                        y2[j] = e[j] * a[j];
+                        z[j] = a[j] * u[j];
                     }
                 }
                 put(out + m * p.ldo + n, y);

@@ -497,7 +497,7 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
                     if (p.act != GDN_ACT_NONE)
                         with_act(p.act, [&](auto tag) {
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) v[j] = act_value<kPrecise, decltype(tag)::value>(v[j]);
+                            for (int j = 0; j < 16; j += 2) act_value<kPrecise, decltype(tag)::value>(v + j, v + j);
                         });
                     if (extra) {
 #pragma unroll
@@ -506,27 +506,35 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
                 } else if constexpr (EPI == kEpiDact) {
                     with_act(p.act, [&](auto tag) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            float a, d;
-                            act_both<kPrecise, decltype(tag)::value>(v[j], a, d);
-                            v[j] = in ? e[j] * d : 0.f;
+                        for (int j = 0; j < 16; j += 2) {
+                            float a[2], d[2];
+                            act_both<kPrecise, decltype(tag)::value>(v + j, a, d);
+                            v[j] = in ? e[j] * d[0] : 0.f;
+                            v[j + 1] = in ? e[j + 1] * d[1] : 0.f;
                         }
                     });
                 } else if constexpr (EPI == kEpiGated) {
                     with_act(p.act, [&](auto tag) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) v[j] = act_value<kPrecise, decltype(tag)::value>(v[j]) * u[j];
+                        for (int j = 0; j < 16; j += 2) {
+                            act_value<kPrecise, decltype(tag)::value>(v + j, v + j);
+                            v[j] *= u[j];
+                            v[j + 1] *= u[j + 1];
+                        }
                     });
                 } else {
                     float h[16];
                     with_act(p.act, [&](auto tag) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            float a, d;
-                            act_both<kPrecise, decltype(tag)::value>(v[j], a, d);
-                            h[j] = a * u[j];
-                            v[j] = e[j] * u[j] * d;
-                            u[j] = e[j] * a;
+                        for (int j = 0; j < 16; j += 2) {
+                            float a[2], d[2];
+                            act_both<kPrecise, decltype(tag)::value>(v + j, a, d);
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                h[j + i] = a[i] * u[j + i];
+                                v[j + i] = e[j + i] * u[j + i] * d[i];
+                                u[j + i] = e[j + i] * a[i];
+                            }
                         }
                     });
                     line_out(dst + p.N, in, cg, p.N, p.vec_out, u);
