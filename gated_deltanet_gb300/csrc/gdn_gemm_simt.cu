@@ -16,6 +16,8 @@ __global__ void __launch_bounds__(256) gemm_simt_kernel(GemmArgs g)
     constexpr int kB = kTwo ? 2 : 1;
     __shared__ float sa[kKt][kT + 4], sb[kB][kKt][kT + 4];
     __shared__ float cs[16][kT];
+    grid_release();
+    grid_wait();
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int64_t m0 = (int64_t)blockIdx.x * kT, n0 = (int64_t)blockIdx.y * kT;  // (x has the larger limit)
     const float *A = (const float *)g.a, *B = (const float *)g.b;
@@ -112,6 +114,8 @@ __global__ void __launch_bounds__(256) gemm_simt_kernel(GemmArgs g)
 __global__ void __launch_bounds__(1024) colsum_finish_kernel(const float *part, int64_t parts, int64_t N, float *out)
 {
     __shared__ float s[32][33];
+    grid_release();
+    grid_wait();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int64_t n = (int64_t)blockIdx.x * 32 + lane;
     float acc = 0.f;
@@ -131,6 +135,8 @@ __global__ void __launch_bounds__(1024) colsum_finish_kernel(const float *part, 
 template <typename T>
 __global__ void __launch_bounds__(128) colsum_rows_kernel(const T *x, int64_t M, int64_t N, int64_t ld, float *part)
 {
+    grid_release();
+    grid_wait();
     const int64_t n = (int64_t)blockIdx.y * 128 + threadIdx.x, p = blockIdx.x;
     if (n >= N) return;
     float acc = 0.f;
@@ -143,30 +149,29 @@ __global__ void __launch_bounds__(128) colsum_rows_kernel(const T *x, int64_t M,
 cudaError_t launch_gemm_simt(const GemmArgs &g, Epi epi, cudaStream_t st)
 {
     if (g.M <= 0 || g.N <= 0) return cudaSuccess;
-    const dim3 grid((unsigned)((g.M + kT - 1) / kT), (unsigned)((g.N + kT - 1) / kT));
+    auto go = [&](auto *kern) {
+        return launch_overlapped(kern, (unsigned)((g.M + kT - 1) / kT), (unsigned)((g.N + kT - 1) / kT), 256, 0, 0, st, g);
+    };
     switch (epi) {
-    case kEpiLinear: gemm_simt_kernel<kEpiLinear><<<grid, 256, 0, st>>>(g); break;
-    case kEpiGated: gemm_simt_kernel<kEpiGated><<<grid, 256, 0, st>>>(g); break;
-    case kEpiDact: gemm_simt_kernel<kEpiDact><<<grid, 256, 0, st>>>(g); break;
-    case kEpiGatedBwd: gemm_simt_kernel<kEpiGatedBwd><<<grid, 256, 0, st>>>(g); break;
+    case kEpiGated: return go(gemm_simt_kernel<kEpiGated>);
+    case kEpiDact: return go(gemm_simt_kernel<kEpiDact>);
+    case kEpiGatedBwd: return go(gemm_simt_kernel<kEpiGatedBwd>);
+    default: return go(gemm_simt_kernel<kEpiLinear>);
     }
-    return cudaGetLastError();
 }
 
 cudaError_t launch_colsum_finish(const float *part, int64_t parts, int64_t N, float *out, cudaStream_t st)
 {
     if (N <= 0) return cudaSuccess;
-    colsum_finish_kernel<<<(unsigned)((N + 31) / 32), 1024, 0, st>>>(part, parts, N, out);
-    return cudaGetLastError();
+    return launch_overlapped(colsum_finish_kernel, (unsigned)((N + 31) / 32), 1, 1024, 0, 0, st, part, parts, N, out);
 }
 
 cudaError_t launch_colsum_rows(const void *x, gdn_dtype dt, int64_t M, int64_t N, int64_t ld, float *part, cudaStream_t st)
 {
     if (M <= 0 || N <= 0) return cudaSuccess;
-    const dim3 grid((unsigned)((M + 31) / 32), (unsigned)((N + 127) / 128));
-    if (dt == GDN_F32) colsum_rows_kernel<<<grid, 128, 0, st>>>((const float *)x, M, N, ld, part);
-    else colsum_rows_kernel<<<grid, 128, 0, st>>>((const __nv_bfloat16 *)x, M, N, ld, part);
-    return cudaGetLastError();
+    const unsigned gx = (unsigned)((M + 31) / 32), gy = (unsigned)((N + 127) / 128);
+    if (dt == GDN_F32) return launch_overlapped(colsum_rows_kernel<float>, gx, gy, 128, 0, 0, st, (const float *)x, M, N, ld, part);
+    return launch_overlapped(colsum_rows_kernel<__nv_bfloat16>, gx, gy, 128, 0, 0, st, (const __nv_bfloat16 *)x, M, N, ld, part);
 }
 
 }  // namespace gdn

@@ -120,6 +120,8 @@ gemm_small_kernel(const __grid_constant__ SmallMaps maps, const SmallParams p)
     tc_fence_after();
     const uint32_t tmem = tslot;
     bool ok = true;
+    grid_release();
+    grid_wait();
 
     if (warp == 4) {
         int s = 0;
@@ -421,18 +423,7 @@ cudaError_t go(const GemmArgs &g, const SmallPlan &pl, cudaStream_t st)
         if (e != cudaSuccess) return e;
         done_on_device(seen);
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(pl.tiles * pl.split));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = pl.smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)pl.split;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, maps, p);
+    return launch_overlapped(kern, (unsigned)(pl.tiles * pl.split), 1, kThreads, pl.smem, pl.split, st, maps, p);
 }
 
 template <bool FP8, bool WT, int EPI, typename TO>

@@ -334,6 +334,8 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *tslot;
+    grid_release();
+    grid_wait();
 
     // tile -> (row tile, column tile): groups of eight row tiles, column tiles within a group one after another
     auto place = [&](int t, int &m, int &n) {
@@ -622,8 +624,7 @@ cudaError_t go(const GemmArgs &g, cudaStream_t st)
     }
     const int64_t tiles = (int64_t)p.mt * p.nt;
     const int pairs = (int)(tiles < device_sm_count() / 2 ? tiles : device_sm_count() / 2);
-    kern<<<2 * pairs, kThreads, G::kSmem, st>>>(maps, p);
-    return cudaGetLastError();
+    return launch_overlapped(kern, 2 * pairs, 1, kThreads, G::kSmem, 0, st, maps, p);
 }
 
 template <bool FP8, int LAYOUT, int EPI, typename TO>
@@ -648,6 +649,8 @@ bool use_small(const GemmArgs &g) { return !g.a_t && g.M <= 128; }
 template <typename T>
 __global__ void __launch_bounds__(256) repack_kernel(const T *src, int64_t ld, int64_t rows, int64_t cols, T *dst, int64_t pitch)
 {
+    grid_release();
+    grid_wait();
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
         for (int64_t c = threadIdx.x; c < cols; c += 256) dst[r * pitch + c] = src[r * ld + c];
 }
@@ -678,9 +681,9 @@ bool tma_ok(const void *p, int64_t ld, int64_t rows, size_t e)
 cudaError_t launch_repack(const void *src, gdn_dtype t, int64_t ld, int64_t rows, int64_t cols, void *dst, int64_t pitch, cudaStream_t st)
 {
     const unsigned grid = (unsigned)(rows < 4096 ? rows : 4096);
-    if (t == GDN_BF16) repack_kernel<<<grid, 256, 0, st>>>((const uint16_t *)src, ld, rows, cols, (uint16_t *)dst, pitch);
-    else repack_kernel<<<grid, 256, 0, st>>>((const uint8_t *)src, ld, rows, cols, (uint8_t *)dst, pitch);
-    return cudaGetLastError();
+    if (t == GDN_BF16)
+        return launch_overlapped(repack_kernel<uint16_t>, grid, 1, 256, 0, 0, st, (const uint16_t *)src, ld, rows, cols, (uint16_t *)dst, pitch);
+    return launch_overlapped(repack_kernel<uint8_t>, grid, 1, 256, 0, 0, st, (const uint8_t *)src, ld, rows, cols, (uint8_t *)dst, pitch);
 }
 
 int64_t gemm_colparts(const GemmArgs &g, Epi epi)

@@ -259,6 +259,32 @@ inline void done_on_device(std::atomic<uint64_t> &seen)
     if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev <= 63) seen.fetch_or(1ull << dev, std::memory_order_relaxed);
 }
 
+// Launches of these operators overlap their neighbours' ends: a kernel may be set up while the one before it in the
+// stream still runs (programmatic stream serialisation), waits for it with grid_wait() before it touches global memory,
+// and lets the next one be set up with grid_release().  A kernel that holds tensor memory releases only once it has it:
+// a successor that got the columns first would wait for a kernel that waits for columns.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kern)(P...), unsigned grid_x, unsigned grid_y, int threads, size_t smem, int cluster, cudaStream_t st,
+                              const A &...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid_x, grid_y);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 0 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // typed loads and stores
 template <typename T> __device__ __forceinline__ float to_f(T v);
 template <> __device__ __forceinline__ float to_f<float>(float v) { return v; }

@@ -199,6 +199,8 @@ template <typename T, typename TO, int VEC, int VPT>
 __global__ void __launch_bounds__(kRowThreads) norm_kernel(NormArgs a, int tpr)
 {
     __shared__ float2 red[2][kRowThreads / 32];
+    grid_release();
+    grid_wait();
     const int t = threadIdx.x & (tpr - 1), rpb = blockDim.x / tpr, nv = a.D / VEC;
     const int64_t step = (int64_t)gridDim.x * rpb;
     const T *x = (const T *)a.x, *r = (const T *)a.r;
@@ -275,6 +277,8 @@ template <typename T, typename TO>
 __global__ void __launch_bounds__(kRowThreads) norm_wide_kernel(NormArgs a)
 {
     __shared__ float2 red[2][kRowThreads / 32];
+    grid_release();
+    grid_wait();
     const T *x = (const T *)a.x, *r = (const T *)a.r;
     int it = 0;
     for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, ++it) {
@@ -313,6 +317,8 @@ template <typename T, int VEC, int VPT>
 __global__ void __launch_bounds__(kRowThreads) norm_bwd_kernel(NormBwdArgs a, int tpr)
 {
     __shared__ float2 red[2][kRowThreads / 32];
+    grid_release();
+    grid_wait();
     extern __shared__ uint4 ahead_slots[];
     const int t = threadIdx.x & (tpr - 1), rpb = blockDim.x / tpr, nv = a.D / VEC;
     const int64_t step = (int64_t)gridDim.x * rpb;
@@ -425,6 +431,8 @@ template <typename T>
 __global__ void __launch_bounds__(kRowThreads) norm_bwd_wide_kernel(NormBwdArgs a)
 {
     __shared__ float2 red[2][kRowThreads / 32];
+    grid_release();
+    grid_wait();
     const T *gy = (const T *)a.dy, *gh = (const T *)a.h, *gd = (const T *)a.dh;
     int it = 0;
     for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, ++it) {
@@ -449,6 +457,8 @@ __global__ void __launch_bounds__(kRowThreads) norm_bwd_wide_kernel(NormBwdArgs 
 template <typename T>
 __global__ void __launch_bounds__(256) norm_dw_wide_kernel(NormBwdArgs a)
 {
+    grid_release();
+    grid_wait();
     const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (c >= a.D) return;
     const T *gy = (const T *)a.dy, *gh = (const T *)a.h;
@@ -509,8 +519,7 @@ cudaError_t launch_rows(F *kern, std::atomic<uint64_t> &seen, const A &a, unsign
         if (e != cudaSuccess) return e;
         done_on_device(seen);
     }
-    kern<<<grid, p.threads, bytes, st>>>(a, p.tpr);
-    return cudaGetLastError();
+    return launch_overlapped(kern, grid, 1, p.threads, bytes, 0, st, a, p.tpr);
 }
 template <typename T, typename TO, int VEC, int VPT>
 cudaError_t norm_rows(const NormArgs &a, const RowPlan &p, unsigned grid, cudaStream_t st)
@@ -534,8 +543,7 @@ cudaError_t norm_go(const NormArgs &a, cudaStream_t st)
     const int sms = device_sm_count();
     if (a.D > kWide) {
         const int64_t most = (int64_t)sms * 4;
-        norm_wide_kernel<T, TO><<<(unsigned)(a.M < most ? a.M : most), kRowThreads, 0, st>>>(a);
-        return cudaGetLastError();
+        return launch_overlapped(norm_wide_kernel<T, TO>, (unsigned)(a.M < most ? a.M : most), 1, kRowThreads, 0, 0, st, a);
     }
     const bool ok = a.D % V == 0 && aligned16(a.x, a.ldx, sizeof(T)) && (!a.r || aligned16(a.r, a.ldr, sizeof(T))) &&
                     ((uintptr_t)a.y & 15) == 0 && ((uintptr_t)a.h & 15) == 0;
@@ -563,9 +571,10 @@ cudaError_t norm_bwd_go(const NormBwdArgs &a, int sms, cudaStream_t st)
     cudaError_t e = cudaSuccess;
     if (norm_bwd_wide(a.D)) {
         const int64_t most = (int64_t)sms * 4;
-        norm_bwd_wide_kernel<T><<<(unsigned)(a.M < most ? a.M : most), kRowThreads, 0, st>>>(a);
+        e = launch_overlapped(norm_bwd_wide_kernel<T>, (unsigned)(a.M < most ? a.M : most), 1, kRowThreads, 0, 0, st, a);
         parts = a.M < kWideParts ? a.M : kWideParts;
-        if (a.dw) norm_dw_wide_kernel<T><<<dim3((unsigned)((a.D + 255) / 256), (unsigned)parts), 256, 0, st>>>(a);
+        if (a.dw && e == cudaSuccess)
+            e = launch_overlapped(norm_dw_wide_kernel<T>, (unsigned)((a.D + 255) / 256), (unsigned)parts, 256, 0, 0, st, a);
     } else {
         const RowPlan p = plan_rows(a.M, a.D, sizeof(T), bwd_vec(a, sizeof(T)), true, sms);
         const unsigned grid = (unsigned)norm_blocks(a.M, p, sms);
@@ -581,7 +590,6 @@ cudaError_t norm_bwd_go(const NormBwdArgs &a, int sms, cudaStream_t st)
             e = norm_bwd_rows<T, V, kMaxGroups>(a, p, grid, st);
         }
     }
-    if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess || !a.dw) return e;
     return launch_colsum_finish(a.part, parts, a.D, a.dw, st);
 }
