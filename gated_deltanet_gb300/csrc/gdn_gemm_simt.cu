@@ -1,113 +1,286 @@
-// Products on the CUDA cores, with the epilogues of the decoder-block operators: fp32 inputs.
+// Products on the CUDA cores, with the epilogues of the decoder-block operators: fp32 inputs.  (The tensor cores
+// truncate their running sums: 2e-6 off at a contraction of 2048, five times fp32's own rounding.)
 //
-// A 64 x 64 tile of the output per CTA of 256 threads, 4 x 4 entries per thread, fp32 sums in the
-// order of k; 16 values of k at a time through shared memory.
+// A CTA of 128 threads owns a tile of 128 x 128 outputs, 16 x 8 entries per thread in packed pairs (one instruction, two
+// fused multiply-adds); 16 values of k at a time through two buffers, the next ones on their way in registers.  Bound: the
+// fp32 pipe, and next to it the 128 bytes a clock that shared memory returns to registers (with 8 x 8 entries per thread
+// that was the bound: 37 of 74 TFLOP/s).  Where such tiles would leave SMs idle: tiles of 64 x 64, 4 x 4 entries per
+// thread, the contraction split over a cluster whose CTAs send their sums to the CTA that finishes the rows.  A thread's
+// columns are two groups half a tile apart, so that a gated tile holds gate and up columns of the same outputs in the same
+// thread.
 #include "gdn_layer.cuh"
 
 namespace gdn {
 namespace {
 
-constexpr int kT = 64, kKt = 16;
+constexpr int kKt = 16, kMaxSplit = 8;
 
-template <int EPI>
-__global__ void __launch_bounds__(256) gemm_simt_kernel(GemmArgs g)
+// four consecutive elements at p, zero from `left` on
+__device__ __forceinline__ float4 load4(const float *p, bool row, int64_t left, bool vec)
 {
-    constexpr bool kTwo = EPI == kEpiGated || EPI == kEpiGatedBwd;
-    constexpr int kB = kTwo ? 2 : 1;
-    __shared__ float sa[kKt][kT + 4], sb[kB][kKt][kT + 4];
-    __shared__ float cs[16][kT];
+    if (row && vec && left >= 4) return *(const float4 *)p;
+    float4 v;
+    v.x = row && left > 0 ? p[0] : 0.f;
+    v.y = row && left > 1 ? p[1] : 0.f;
+    v.z = row && left > 2 ? p[2] : 0.f;
+    v.w = row && left > 3 ? p[3] : 0.f;
+    return v;
+}
+__device__ __forceinline__ uint32_t peer_addr(const float *p, uint32_t cta)
+{
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(cta));
+    return a;
+}
+
+// The two tilings: T x T outputs, RM x CN per thread (rows in groups of RG, columns in two groups)
+template <bool BIG> struct Tiling {
+    static constexpr int T = BIG ? 128 : 64, RM = BIG ? 16 : 4, RG = BIG ? 4 : 2, CN = BIG ? 8 : 4, H = CN / 2;
+    static constexpr int kThreads = (T / RM) * (T / CN);
+    static constexpr int kElems = T * kKt / kThreads;  // of each operand per thread and step
+    static constexpr int kTy = T / RM;
+};
+
+template <int EPI, bool BIG>
+__global__ void __launch_bounds__(Tiling<BIG>::kThreads, 2) gemm_simt_kernel(GemmArgs g, int mtiles, int split, int vec_a, int vec_b)
+{
+    using L = Tiling<BIG>;
+    constexpr bool kGated = EPI == kEpiGated || EPI == kEpiGatedBwd;
+    constexpr int T = L::T, RM = L::RM, RG = L::RG, CN = L::CN, H = L::H, kThreads = L::kThreads, kLd = T + 4;
+    constexpr int kRowStep = T / (RM / RG);          // between a thread's row groups
+    constexpr int kOutN = kGated ? T / 2 : T;        // output columns of a tile
+    __shared__ __align__(16) float sa[2][kKt][kLd], sb[2][kKt][kLd];
+    __shared__ __align__(16) float red[BIG ? 1 : T * T];  // [split][T / split][T]: sums of the rows finished here
+    __shared__ float cs[EPI == kEpiDact ? L::kTy : 1][T];
     grid_release();
     grid_wait();
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    const int64_t m0 = (int64_t)blockIdx.x * kT, n0 = (int64_t)blockIdx.y * kT;  // (x has the larger limit)
+    const int tid = threadIdx.x, tx = (tid >> 5 & 1) * 8 + (tid & 7), ty = (tid >> 6) * 4 + (tid >> 3 & 3);
+    const int rank = blockIdx.x % split;
+    const int64_t tile = blockIdx.x / split;
+    const int64_t m0 = tile % mtiles * T, n0 = tile / mtiles * kOutN;
     const float *A = (const float *)g.a, *B = (const float *)g.b;
-    float acc[kB][4][4] = {};
-    for (int64_t k0 = 0; k0 < g.K; k0 += kKt) {
-        // consecutive threads along the operand's contiguous index
-        for (int i = tid; i < kT * kKt; i += 256) {
-            const int mi = g.a_t ? i & (kT - 1) : i / kKt, ki = g.a_t ? i / kT : i & (kKt - 1);
-            const int64_t m = m0 + mi, k = k0 + ki;
-            sa[ki][mi] = m < g.M && k < g.K ? A[g.a_t ? k * g.lda + m : m * g.lda + k] : 0.f;
-            const int ni = g.b_t ? i & (kT - 1) : i / kKt, kj = g.b_t ? i / kT : i & (kKt - 1);
-            const int64_t n = n0 + ni, kk = k0 + kj;
+
+    // This thread's elements of each operand's next 16 values of k: consecutive along k of one row (K-major), or fours along
+    // the rows at one k
+    constexpr int E = L::kElems, Q = E / 4, kAcross = kThreads / kKt;
+    const int row = tid % T, koff = tid / T * E, kk = tid / kAcross, at = 4 * (tid % kAcross);
+    float4 ra[Q], rb[Q];
+    auto fetch = [&](int64_t k0) {
 #pragma unroll
-            for (int h = 0; h < kB; ++h) {
-                const int64_t row = n + h * g.N;
-                sb[h][kj][ni] = n < g.N && kk < g.K ? B[g.b_t ? kk * g.ldb + row : row * g.ldb + kk] : 0.f;
+        for (int q = 0; q < Q; ++q) {
+            if (g.a_t) {
+                const int64_t m = m0 + q * 4 * kAcross + at;
+                ra[q] = load4(A + (k0 + kk) * g.lda + m, k0 + kk < g.K, g.M - m, vec_a);
+            } else {
+                const int64_t k = k0 + koff + 4 * q;
+                ra[q] = load4(A + (m0 + row) * g.lda + k, m0 + row < g.M, g.K - k, vec_a);
+            }
+            if (g.b_t) {
+                const int64_t n = n0 + q * 4 * kAcross + at;
+                rb[q] = load4(B + (k0 + kk) * g.ldb + n, k0 + kk < g.K, g.N - n, vec_b);
+            } else {
+                const int64_t k = k0 + koff + 4 * q, n = n0 + (kGated ? row % kOutN : row);
+                rb[q] = load4(B + (kGated && row >= kOutN ? g.N + n : n) * g.ldb + k, n < g.N, g.K - k, vec_b);
             }
         }
-        __syncthreads();
+    };
+    auto keep_one = [&](float (*dst)[kLd], const float4 *v, bool along) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            if (along) {
+                *(float4 *)&dst[kk][q * 4 * kAcross + at] = v[q];
+            } else {
+                dst[koff + 4 * q][row] = v[q].x;
+                dst[koff + 4 * q + 1][row] = v[q].y;
+                dst[koff + 4 * q + 2][row] = v[q].z;
+                dst[koff + 4 * q + 3][row] = v[q].w;
+            }
+        }
+    };
+    auto keep = [&](int buf) {
+        keep_one(sa[buf], ra, g.a_t);
+        keep_one(sb[buf], rb, g.b_t);
+    };
+    const int64_t kt = (g.K + kKt - 1) / kKt, kt0 = kt * rank / split, kt1 = kt * (rank + 1) / split;
+    Pair acc[RM][H];
+#pragma unroll
+    for (int i = 0; i < RM; ++i)
+#pragma unroll
+        for (int j = 0; j < H; ++j) acc[i][j].r = 0;
+    if (kt0 < kt1) {
+        fetch(kt0 * kKt);
+        keep(0);
+    }
+    __syncthreads();
+    for (int64_t t = kt0; t < kt1; ++t) {
+        const int buf = (int)(t - kt0) & 1;
+        if (t + 1 < kt1) fetch((t + 1) * kKt);
 #pragma unroll
         for (int k = 0; k < kKt; ++k) {
-            const float4 a = *(const float4 *)&sa[k][4 * ty];
-            const float av[4] = {a.x, a.y, a.z, a.w};
+            float a[RM];
+            Pair b[H];
 #pragma unroll
-            for (int h = 0; h < kB; ++h) {
-                const float4 b = *(const float4 *)&sb[h][k][4 * tx];
-                const float bv[4] = {b.x, b.y, b.z, b.w};
+            for (int i = 0; i < RM; i += RG) {
+                const float *p = &sa[buf][k][i / RG * kRowStep + RG * ty];
+                if constexpr (RG == 4) *(float4 *)(a + i) = *(const float4 *)p;
+                else *(float2 *)(a + i) = *(const float2 *)p;
+            }
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+            for (int h = 0; h < 2; ++h) {
+                const float *p = &sb[buf][k][h * (T / 2) + H * tx];
+                if constexpr (H == 4) *(float4 *)(b + 2 * h) = *(const float4 *)p;
+                else *(float2 *)(b + h) = *(const float2 *)p;
+            }
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[h][i][j] = fmaf(av[i], bv[j], acc[h][i][j]);
+            for (int i = 0; i < RM; ++i) {
+                const Pair aa = pair_of(a[i], a[i]);
+#pragma unroll
+                for (int j = 0; j < H; ++j) acc[i][j] = fma2(aa, b[j], acc[i][j]);
             }
         }
+        if (t + 1 < kt1) keep(buf ^ 1);
         __syncthreads();
     }
+
+    // one pair of neighbouring outputs (m, n), (m, n + 1); returns dz in z (kEpiDact)
     float *out = (float *)g.out;
     const float *extra = (const float *)g.extra;
-    float col[4] = {};
-    with_act(g.act, [&](auto tag) {
+    auto finish = [&](auto tag, int64_t m, int64_t n, float *z, const float *u) {
         constexpr int ACT = decltype(tag)::value;
+        float v[2], d[2];
+        if (!kGated && g.bias) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t m = m0 + 4 * ty + i;
-            if (m >= g.M) continue;
-            float v[4], d[4];
-            if (EPI == kEpiLinear || EPI == kEpiDact) {
+            for (int j = 0; j < 2; ++j)
+                if (n + j < g.N) z[j] += g.bias[n + j];
+        }
+        if constexpr (EPI == kEpiLinear || EPI == kEpiGated) act_value<true, ACT>(z, v);
+        else act_both<true, ACT>(z, v, d);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (g.bias && n0 + 4 * tx + j < g.N) acc[0][i][j] += g.bias[n0 + 4 * tx + j];
+        for (int j = 0; j < 2; ++j) {
+            if (m >= g.M || n + j >= g.N) {
+                z[j] = 0.f;
+                continue;
             }
-#pragma unroll
-            for (int j = 0; j < 4; j += 2) {
-                if (EPI == kEpiLinear || EPI == kEpiGated) act_value<true, ACT>(&acc[0][i][j], v + j);
-                else act_both<true, ACT>(&acc[0][i][j], v + j, d + j);
+            const int64_t c = n + j;
+            if (EPI == kEpiLinear) {
+                out[m * g.ldo + c] = extra ? v[j] + extra[m * g.ld_extra + c] : v[j];
+            } else if (EPI == kEpiDact) {
+                z[j] = extra[m * g.ld_extra + c] * d[j];
+                out[m * g.ldo + c] = z[j];
+            } else if (EPI == kEpiGated) {
+                out[m * g.ldo + c] = v[j] * u[j];
+            } else {
+                const float dh = extra[m * g.ld_extra + c];
+                out[m * g.ldo + c] = dh * u[j] * d[j];
+                out[m * g.ldo + g.N + c] = dh * v[j];
+                if (g.out2) ((float *)g.out2)[m * g.ldo2 + c] = v[j] * u[j];
             }
+        }
+    };
+    auto row_of = [&](int i) { return i / RG * kRowStep + RG * ty + i % RG; };
+    auto col_of = [&](int j) { return (j / H) * (T / 2) + H * tx + j % H; };
+    int groups;  // row groups whose column sums lie in cs
+    if (BIG || split == 1) {
+        groups = L::kTy;
+        float col[CN] = {};
+        with_act(g.act, [&](auto tag) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int64_t n = n0 + 4 * tx + j;
-                if (n >= g.N) continue;
-                const float u = acc[kB - 1][i][j];
-                if (EPI == kEpiLinear) {
-                    out[m * g.ldo + n] = extra ? v[j] + extra[m * g.ld_extra + n] : v[j];
-                } else if (EPI == kEpiDact) {
-                    const float dz = extra[m * g.ld_extra + n] * d[j];
-                    out[m * g.ldo + n] = dz;
-                    col[j] += dz;
-                } else if (EPI == kEpiGated) {
-                    out[m * g.ldo + n] = v[j] * u;
+            for (int i = 0; i < RM; ++i) {
+                const int64_t m = m0 + row_of(i);
+                float z[CN];
+#pragma unroll
+                for (int j = 0; j < H; ++j) unpair(acc[i][j], z[2 * j], z[2 * j + 1]);
+                if constexpr (kGated) {
+#pragma unroll
+                    for (int j = 0; j < H; j += 2) finish(tag, m, n0 + H * tx + j, z + j, z + H + j);
                 } else {
-                    const float dh = extra[m * g.ld_extra + n];
-                    out[m * g.ldo + n] = dh * u * d[j];
-                    out[m * g.ldo + g.N + n] = dh * v[j];
-                    if (g.out2) ((float *)g.out2)[m * g.ldo2 + n] = v[j] * u;
+#pragma unroll
+                    for (int j = 0; j < CN; j += 2) {
+                        finish(tag, m, n0 + col_of(j), z + j, z + j);
+                        if (EPI == kEpiDact) {
+                            col[j] += z[j];
+                            col[j + 1] += z[j + 1];
+                        }
+                    }
                 }
             }
-        }
-    });
-    if (EPI == kEpiDact && g.colpart) {
-        // this tile's column sums over its two groups of 32 rows
+        });
+        if constexpr (EPI == kEpiDact) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) cs[ty][4 * tx + j] = col[j];
-        __syncthreads();
-        if (tid < 2 * kT) {
-            const int half = tid / kT, c = tid % kT;
-            float s = 0.f;
-            for (int i = 0; i < 8; ++i) s += cs[8 * half + i][c];
-            const int64_t p = m0 / 32 + half, n = n0 + c;
-            if (n < g.N && p * 32 < g.M) g.colpart[p * g.N + n] = s;
+            for (int j = 0; j < CN; ++j) cs[ty][col_of(j)] = col[j];
+        }
+    } else {
+        // partial sums to the CTAs that finish their rows, T / split each
+        const int per = T / split;
+        asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < RM; ++i) {
+            const int r = row_of(i);
+#pragma unroll
+            for (int j = 0; j < H; ++j) {
+                float x, y;
+                unpair(acc[i][j], x, y);
+                const uint32_t dst = peer_addr(red + (rank * per + r % per) * T + col_of(2 * j), r / per);
+                asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(dst), "f"(x), "f"(y) : "memory");
+            }
+        }
+        asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
+        constexpr int kPairs = kOutN / 2;
+        groups = kThreads / kPairs;
+        const int c = tid % kPairs * 2, grp = tid / kPairs;
+        float col[2] = {};
+        with_act(g.act, [&](auto tag) {
+            for (int r = grp; r < per; r += kThreads / kPairs) {
+                float z[2] = {}, u[2] = {};
+                for (int s = 0; s < split; ++s) {
+                    const float *p = red + (s * per + r) * T + c;
+                    z[0] += p[0];
+                    z[1] += p[1];
+                    if (kGated) {
+                        u[0] += p[T / 2];
+                        u[1] += p[T / 2 + 1];
+                    }
+                }
+                finish(tag, m0 + rank * per + r, n0 + c, z, u);
+                col[0] += z[0];
+                col[1] += z[1];
+            }
+        });
+        if constexpr (EPI == kEpiDact) {
+            cs[grp][c] = col[0];
+            cs[grp][c + 1] = col[1];
         }
     }
+    if constexpr (EPI == kEpiDact) {
+        if (g.colpart) {
+            __syncthreads();
+            if (tid < T && n0 + tid < g.N) {
+                float sum = 0.f;
+                for (int i = 0; i < groups; ++i) sum += cs[i][tid];
+                g.colpart[(tile % mtiles * split + rank) * g.N + n0 + tid] = sum;
+            }
+        }
+    }
+}
+
+// 128 x 128 tiles where they make work for most SMs, else 64 x 64 with the contraction split for two CTAs on an SM
+struct SimtPlan {
+    bool big;
+    int split, mtiles;
+    int64_t tiles;
+};
+SimtPlan plan_simt(const GemmArgs &g, Epi epi)
+{
+    SimtPlan p;
+    const int64_t sms = device_sm_count(), halves = epi == kEpiGated || epi == kEpiGatedBwd ? 2 : 1;
+    auto tiles = [&](int64_t t) { return ((g.M + t - 1) / t) * ((g.N * halves + t - 1) / t); };
+    p.big = 2 * tiles(128) >= sms;
+    const int64_t t = p.big ? 128 : 64;
+    p.mtiles = (int)((g.M + t - 1) / t);
+    p.tiles = p.mtiles * ((g.N + t / halves - 1) / (t / halves));
+    p.split = 1;
+    while (!p.big && p.split < kMaxSplit && p.tiles * p.split * 2 <= 2 * sms && g.K / (p.split * 2) >= 4 * kKt) p.split *= 2;
+    return p;
 }
 
 // 32 columns per CTA, the parts dealt to 32 warps, whose sums meet in a fixed order
@@ -146,17 +319,27 @@ __global__ void __launch_bounds__(128) colsum_rows_kernel(const T *x, int64_t M,
 
 }  // namespace
 
+int64_t gemm_simt_colparts(const GemmArgs &g, Epi epi)
+{
+    const SimtPlan p = plan_simt(g, epi);
+    return (int64_t)p.mtiles * p.split;
+}
+
 cudaError_t launch_gemm_simt(const GemmArgs &g, Epi epi, cudaStream_t st)
 {
     if (g.M <= 0 || g.N <= 0) return cudaSuccess;
-    auto go = [&](auto *kern) {
-        return launch_overlapped(kern, (unsigned)((g.M + kT - 1) / kT), (unsigned)((g.N + kT - 1) / kT), 256, 0, 0, st, g);
+    const SimtPlan p = plan_simt(g, epi);
+    auto on16 = [](const void *q, int64_t ld) { return ((uintptr_t)q & 15) == 0 && ld % 4 == 0; };
+    auto go = [&](auto *small, auto *big) {
+        return launch_overlapped(p.big ? big : small, (unsigned)(p.tiles * p.split), 1, p.big ? Tiling<true>::kThreads : Tiling<false>::kThreads,
+                                 0, p.split > 1 ? p.split : 0, st, g,
+                                 p.mtiles, p.split, (int)on16(g.a, g.lda), (int)on16(g.b, g.ldb));
     };
     switch (epi) {
-    case kEpiGated: return go(gemm_simt_kernel<kEpiGated>);
-    case kEpiDact: return go(gemm_simt_kernel<kEpiDact>);
-    case kEpiGatedBwd: return go(gemm_simt_kernel<kEpiGatedBwd>);
-    default: return go(gemm_simt_kernel<kEpiLinear>);
+    case kEpiGated: return go(gemm_simt_kernel<kEpiGated, false>, gemm_simt_kernel<kEpiGated, true>);
+    case kEpiDact: return go(gemm_simt_kernel<kEpiDact, false>, gemm_simt_kernel<kEpiDact, true>);
+    case kEpiGatedBwd: return go(gemm_simt_kernel<kEpiGatedBwd, false>, gemm_simt_kernel<kEpiGatedBwd, true>);
+    default: return go(gemm_simt_kernel<kEpiLinear, false>, gemm_simt_kernel<kEpiLinear, true>);
     }
 }
 

@@ -32,25 +32,35 @@ constexpr unsigned long long kLimitNs = 2000000000ull;
 constexpr int kEpiWarps = 8, kThreads = 32 * (kEpiWarps + 2);
 constexpr int kABytes = 128 * 128;       // a CTA's rows of A, 128 bytes of k (or 64 k rows of 2 x 64 m)
 
-// Shared memory of a CTA: operands, and each epilogue warp's column vectors (scales and bias of its half of a tile;
-// the tensors of the epilogue go between registers and global memory).  BN = 128: two
+// What the operands are: bf16, e4m3, or fp32 as three bf16 planes each (x = x0 + x1 + x2, 8 bits of the significand
+// apiece; launch_split).  Of the nine products of planes the six that reach fp32's last bits are taken: x0 w0, and x0 w1,
+// x1 w0, x1 w1, x0 w2, x2 w0, which are 2^-8 of it and less.  The tensor cores truncate their running sums (2e-6 off after
+// 128 additions, five times fp32's own rounding), so x0 w0 is summed over kChain stages at a time only and the epilogue
+// adds those partial sums in registers; the others have an accumulator of their own, whose truncation is 2^-8 as large.
+enum Kind : int { kBf16 = 0, kE4m3 = 1, kF32 = 2 };
+constexpr int kChain = 2;
+
+// Shared memory of a CTA: operands, each epilogue warp's column vectors (scales and bias of its half of a tile; the
+// tensors of the epilogue go between registers and global memory) and its 32 x 16 patch for rows off 16 bytes.  BN = 128: two
 // 128-byte-wide blocks of k per stage, so that eight products and not four follow each wait (16384 x 2048 x 2048:
 // 112 -> 87 us; with BN = 256, whose products take twice as long, it is flat).
-template <int BN> struct Geo {
-    static constexpr int kAtoms = BN == 256 ? 1 : 2;
+template <int KIND, int BN> struct Geo {
+    static constexpr int kAtoms = KIND == kF32 ? 3 : BN == 256 ? 1 : 2;  // (fp32: the planes of one block of k)
+    static constexpr int kPerStage = KIND == kF32 ? 1 : kAtoms;          // blocks of k
     static constexpr int kB = BN / 2 * 128;
     static constexpr int kAtom = kABytes + kB;  // 128 bytes of k
     static constexpr int kStage = kAtoms * kAtom;
-    static constexpr int kColBytes = kEpiWarps * 2 * 128 * 4;
+    static constexpr int kColBytes = kEpiWarps * (2 * 128 + 32 * 17) * 4;
     static constexpr int kStages = (227 * 1024 - 1024 - kColBytes - 256) / kStage;
+    static_assert(kStages == (KIND == kF32 ? 2 : BN == 256 ? 6 : 4) && (KIND != kF32 || BN == 128), "stages");
     static constexpr int kBars = 2 * kStages + 4;
-    static constexpr int kTmem = 2 * BN;  // two accumulators
+    static constexpr int kTmem = (KIND == kF32 ? 4 : 2) * BN;  // two accumulators (fp32: and two for the small products)
     static constexpr int kSmem = 1024 + kStages * kStage + kColBytes + kBars * 8 + 16;
-    static_assert(kStages >= 3 && kSmem <= 227 * 1024, "shared memory budget");
+    static_assert(kSmem <= 227 * 1024, "shared memory budget");
 };
 
 struct TcMaps {
-    CUtensorMap a, b;
+    CUtensorMap a[3], b[3];  // (planes; the first alone unless fp32)
 };
 struct TcParams {
     int64_t M, N;            // output rows; output columns (gated: F)
@@ -210,17 +220,61 @@ template <> struct Line<float> {
         for (int j = 0; j < 16; ++j) v[j] = v_[j];
     }
 };
-// `p`: column c of a row; columns from N on (and rows that do not exist: `in`) read as zero and are not written
-template <typename TO>
-__device__ __forceinline__ void line_in(Line<TO> &l, const TO *p, bool in, int64_t c, int64_t N, int vec)
+// `p`: column c of this lane's row, of the 32 rows from row0 on; columns from N on and rows from M on read as zero and
+// are not written.  Rows off 16 bytes pass through the warp's patch, so that half a warp reads or writes the 16 columns
+// of a row together (lane by lane, every element was a sector of its own: 8071 x 955 outputs with a residual took 117 us).
+constexpr int kPatch = 17;  // floats per row of the patch: lanes that read down a column meet no bank twice
+// (out of line: the fast path's loop has to stay small)
+__device__ __noinline__ void patch_turn(float *v, int lane, float *patch)  // 16 values per lane: by rows of 16 -> by lanes
 {
-    if (in && vec && c + 16 <= N) {
-        l.load(p, vec);
-    } else {
-        l.zero();
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (in && c + j < N) l.set(j, p[j]);
+    for (int i = 0; i < 16; ++i) patch[(2 * i + (lane >> 4)) * kPatch + (lane & 15)] = v[i];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = patch[lane * kPatch + i];
+    __syncwarp();
+}
+template <typename TO>
+__device__ __noinline__ void patch_out(const float *v, TO *first, int64_t ld, int rows, int cols, int lane, float *patch)
+{
+#pragma unroll
+    for (int i = 0; i < 16; ++i) patch[lane * kPatch + i] = v[i];
+    __syncwarp();
+    const int j = lane & 15;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int r = 2 * i + (lane >> 4);
+        if (r < rows && j < cols) first[r * ld + j] = from_f<TO>(patch[r * kPatch + j]);
+    }
+    __syncwarp();
+}
+template <typename TO>
+__device__ __forceinline__ void line_in(Line<TO> &l, const TO *p, int64_t ld, int64_t row0, int lane, int64_t M, int64_t c, int64_t N, int vec)
+{
+    l.zero();
+    if (vec && c + 16 <= N) {
+        if (row0 + lane < M) l.load(p, vec);
+        return;
+    }
+    const TO *first = p - lane * ld + (lane & 15);  // row0's; turned to this lane's row when it is used
+    const bool col = c + (lane & 15) < N;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int r = 2 * i + (lane >> 4);
+        if (col && row0 + r < M) l.set(i, first[r * ld]);
+    }
+}
+template <typename TO>
+__device__ __forceinline__ void line_get(const Line<TO> &l, float *v, int lane, int64_t c, int64_t N, int vec, float *patch)
+{
+    l.get(v);
+    if (!(vec && c + 16 <= N)) {
+        float w[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) w[j] = v[j];
+        patch_turn(w, lane, patch);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = w[j];
     }
 }
 __device__ __forceinline__ void line_put(__nv_bfloat16 *p, const float *v, int vec)
@@ -239,16 +293,17 @@ __device__ __forceinline__ void line_put(float *p, const float *v, int)
     for (int j = 0; j < 4; ++j) *((float4 *)p + j) = *(const float4 *)(v + 4 * j);
 }
 template <typename TO>
-__device__ __forceinline__ void line_out(TO *p, bool in, int64_t c, int64_t N, int vec, const float *v)
+__device__ __forceinline__ void line_out(TO *p, int64_t ld, int64_t row0, int lane, int64_t M, int64_t c, int64_t N, int vec, const float *v,
+                                         float *patch)
 {
-    if (!in) return;
     if (vec && c + 16 <= N) {
-        line_put(p, v, vec);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (c + j < N) p[j] = from_f<TO>(v[j]);
+        if (row0 + lane < M) line_put(p, v, vec);
+        return;
     }
+    float w[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) w[j] = v[j];
+    patch_out<TO>(w, p - lane * ld, ld, (int)(M - row0 < 32 ? M - row0 : 32), (int)(N - c < 16 ? N - c : 16), lane, patch);
 }
 // `count` per-column values from column c on into a warp's shared memory (0 past the end), and 16 of them back
 __device__ __forceinline__ void columns_in(float *dst, const float *src, int64_t c, int64_t N, int count, int lane)
@@ -292,7 +347,7 @@ __device__ __forceinline__ float column_sums(float *v, int lane)
 }
 
 // LAYOUT 0: A and B K-major; 1: B MN-major; 2: both MN-major
-template <bool FP8, int LAYOUT, int EPI, int BN, typename TO>
+template <int KIND, int LAYOUT, int EPI, int BN, typename TO>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
 {
@@ -300,8 +355,8 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
     constexpr bool kExtra = EPI != kEpiGated;
     constexpr bool kPrecise = sizeof(TO) == 4;
     constexpr int kOutN = kGated ? BN / 2 : BN;  // output columns of a tile
-    static_assert(!kGated || BN == 256, "a gated tile is 128 gate and 128 up columns");
-    using G = Geo<BN>;
+    constexpr bool FP8 = KIND == kE4m3, F32 = KIND == kF32;
+    using G = Geo<KIND, BN>;
     constexpr int kAtoms = G::kAtoms;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -361,18 +416,19 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
 #pragma unroll
                     for (int at = 0; at < kAtoms; ++at) {
                         uint8_t *sa = sm + s * G::kStage + at * G::kAtom, *sb = sa + kABytes;
-                        const int k0 = (kb * kAtoms + at) * (FP8 ? 128 : 64);  // (past the end: zeros)
+                        const int k0 = (kb * G::kPerStage + (F32 ? 0 : at)) * (FP8 ? 128 : 64);  // (past the end: zeros)
+                        const CUtensorMap *ma = &maps.a[F32 ? at : 0], *mb = &maps.b[F32 ? at : 0];
                         if (LAYOUT == 2) {
-                            pair_load(sa, &maps.a, m0, k0, bar);
-                            pair_load(sa + 8192, &maps.a, m0 + 64, k0, bar);
+                            pair_load(sa, ma, m0, k0, bar);
+                            pair_load(sa + 8192, ma, m0 + 64, k0, bar);
                         } else {
-                            pair_load(sa, &maps.a, k0, m0, bar);
+                            pair_load(sa, ma, k0, m0, bar);
                         }
                         if (LAYOUT >= 1) {
 #pragma unroll
-                            for (int j = 0; j < BN / 128; ++j) pair_load(sb + 8192 * j, &maps.b, n0 + 64 * j, k0, bar);
+                            for (int j = 0; j < BN / 128; ++j) pair_load(sb + 8192 * j, mb, n0 + 64 * j, k0, bar);
                         } else {
-                            pair_load(sb, &maps.b, k0, n0, bar);
+                            pair_load(sb, mb, k0, n0, bar);
                         }
                     }
                 }
@@ -395,26 +451,48 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
             const uint32_t base = smem_u32(sm);
             const uint64_t da0 = sdesc_sw128(base, LAYOUT == 2 ? 8192 : 16, 1024);
             const uint64_t db0 = sdesc_sw128(base + kABytes, LAYOUT >= 1 ? 8192 : 16, 1024);
-            uint32_t s = 0, ph = 0, n = 0;
-            for (int t = pair; t < tiles && ok; t += pairs, ++n) {
-                const uint32_t acc = n & 1;
-                if (!(ok = __all_sync(0xffffffffu, wait_cluster(&tempty[acc], ((n >> 1) & 1) ^ 1)))) break;
-                tc_fence_after();
-                for (int kb = 0; kb < p.kblocks; ++kb) {
+            uint32_t s = 0, ph = 0, n = 0, parity = 0;
+            for (int t = pair; t < tiles && ok; t += pairs, parity ^= 1) {
+                const uint32_t small = tmem + (2 + parity) * BN;  // (fp32)
+                for (int kb = 0, chain = 0; kb < p.kblocks; ++kb) {
+                    const uint32_t acc = n & 1;
+                    if (chain == 0) {
+                        if (!(ok = __all_sync(0xffffffffu, wait_cluster(&tempty[acc], ((n >> 1) & 1) ^ 1)))) break;
+                        tc_fence_after();
+                    }
                     if (!(ok = __all_sync(0xffffffffu, wait_cluster(&full[s], ph)))) break;
                     tc_fence_after();
                     const uint64_t da = da0 + s * (G::kStage >> 4), db = db0 + s * (G::kStage >> 4);
                     uint64_t *const rel = &empty[s];
                     if (++s == G::kStages) { s = 0; ph ^= 1; }
+                    const bool last = kb + 1 == p.kblocks || (F32 && chain + 1 == kChain);
                     if (elect_one_sync()) {
+                        if constexpr (F32) {
+                            constexpr int pa[5] = {0, 1, 1, 0, 2}, pb[5] = {1, 0, 1, 2, 0};
 #pragma unroll
-                        for (int j = 0; j < 4 * kAtoms; ++j)
-                            pair_mma<FP8>(tmem + acc * BN, da + (j >> 2) * (G::kAtom >> 4) + (j & 3) * sa_step,
-                                          db + (j >> 2) * (G::kAtom >> 4) + (j & 3) * sb_step, id, (kb | j) != 0);
+                            for (int i = 0; i < 5; ++i)
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    pair_mma<false>(small, da + pa[i] * (G::kAtom >> 4) + j * sa_step, db + pb[i] * (G::kAtom >> 4) + j * sb_step, id,
+                                                    (kb | i | j) != 0);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                pair_mma<false>(tmem + acc * BN, da + j * sa_step, db + j * sb_step, id, (chain | j) != 0);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 4 * kAtoms; ++j)
+                                pair_mma<FP8>(tmem + acc * BN, da + (j >> 2) * (G::kAtom >> 4) + (j & 3) * sa_step,
+                                              db + (j >> 2) * (G::kAtom >> 4) + (j & 3) * sb_step, id, (kb | j) != 0);
+                        }
                         pair_commit(rel);
-                        if (kb + 1 == p.kblocks) pair_commit(&tfull[acc]);
+                        if (last) pair_commit(&tfull[acc]);
                     }
                     __syncwarp();
+                    ++chain;
+                    if (last) {
+                        chain = 0;
+                        ++n;
+                    }
                 }
             }
         }
@@ -424,20 +502,20 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
         const int q = warp & 3, half = warp >> 2;     // its 32 rows, its half
         const TO *const extra = (const TO *)p.extra;
         float *const cs = cols + warp * 256;          // scales (gate, up), bias
-        uint32_t n = 0;
-        for (int t = pair; t < tiles && ok; t += pairs, ++n) {
+        float *const patch = cols + kEpiWarps * 256 + warp * 32 * kPatch;
+        uint32_t n = 0, parity = 0;
+        for (int t = pair; t < tiles && ok; t += pairs, parity ^= 1) {
             int mi, ni;
             place(t, mi, ni);
             const int64_t row0 = (int64_t)mi * 256 + rank * 128 + q * 32, row = row0 + lane;
             const int64_t col0 = (int64_t)ni * kOutN + half * (kOutN / 2);
             const bool in = row < p.M;
-            const uint32_t acc = n & 1;
-            const uint32_t tl = tmem + acc * BN + ((uint32_t)(q * 32) << 16) + half * (kOutN / 2);
+            const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + half * (kOutN / 2);
             const int64_t left = p.N - col0;  // columns of this warp's half that exist
             const int groups = row0 >= p.M || left <= 0 ? 0 : left < kGroups * 16 ? (int)((left + 15) / 16) : kGroups;
             // extra values (residual, dy, dh) and accumulators of the next group load under this group's arithmetic
             Line<TO> ne;
-            if (kExtra && extra && groups) line_in(ne, extra + row * p.ld_extra + col0, in, col0, p.N, p.vec_extra);
+            if (kExtra && extra && groups) line_in(ne, extra + row * p.ld_extra + col0, p.ld_extra, row0, lane, p.M, col0, p.N, p.vec_extra);
             const float sx = FP8 && p.x_scale && in ? p.x_scale[row] : 1.f;
             if (groups && (p.bias || (FP8 && p.w_scale))) {
                 __syncwarp();  // (the last tile's are read)
@@ -446,37 +524,9 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
                 if (!kGated && p.bias) columns_in(cs + 128, p.bias, col0, p.N, kOutN / 2, lane);
                 __syncwarp();
             }
-            ok = wait_cluster(&tfull[acc], (n >> 1) & 1);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            tc_fence_after();
-            float nv[16], nu[kGated ? 16 : 1];
-            if (groups) {
-                tmem_ld16(tl, nv);
-                if constexpr (kGated) tmem_ld16(tl + BN / 2, nu);
-            }
-            // (rolled: unrolled over a tile's columns, an activation's code left the instruction cache at every pass)
-#pragma unroll 1
-            for (int g = 0; g < groups; ++g) {
+            // one group of 16 columns: from its sums to its outputs
+            auto finish = [&](int g, float *v, float *u, const float *e) {
                 const int64_t cg = col0 + 16 * g;
-                float v[16], u[16], e[16];
-                if (kExtra && extra) {
-                    ne.get(e);
-                    if (g + 1 < groups) line_in(ne, extra + row * p.ld_extra + cg + 16, in, cg + 16, p.N, p.vec_extra);
-                }
-                tmem_ld_wait();
-                pin16(nv);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] = nv[j];
-                if constexpr (kGated) {
-                    pin16(nu);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) u[j] = nu[j];
-                }
-                if (g + 1 < groups) {
-                    tmem_ld16(tl + 16 * (g + 1), nv);
-                    if constexpr (kGated) tmem_ld16(tl + BN / 2 + 16 * (g + 1), nu);
-                }
                 if (FP8 && p.w_scale) {
                     float ws[16];
                     columns(cs + 16 * g, ws);
@@ -539,20 +589,99 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
                             }
                         }
                     });
-                    line_out(dst + p.N, in, cg, p.N, p.vec_out, u);
-                    if (p.out2) line_out((TO *)p.out2 + row * p.ldo2 + cg, in, cg, p.N, p.vec_out2, h);
+                    line_out(dst + p.N, p.ldo, row0, lane, p.M, cg, p.N, p.vec_out, u, patch);
+                    if (p.out2) line_out((TO *)p.out2 + row * p.ldo2 + cg, p.ldo2, row0, lane, p.M, cg, p.N, p.vec_out2, h, patch);
                 }
-                line_out(dst, in, cg, p.N, p.vec_out, v);
+                line_out(dst, p.ldo, row0, lane, p.M, cg, p.N, p.vec_out, v, patch);
                 if (EPI == kEpiDact && p.colpart) {
                     const float sum = column_sums(v, lane);
                     const int64_t cc = cg + (lane >> 1);
                     if (!(lane & 1) && cc < p.N) p.colpart[(row0 >> 5) * p.N + cc] = sum;
                 }
-            }
+            };
+            auto extra_of = [&](int g, float *e) {
+                if (kExtra && extra) {
+                    const int64_t cg = col0 + 16 * g;
+                    line_get(ne, e, lane, cg, p.N, p.vec_extra, patch);
+                    if (g + 1 < groups) line_in(ne, extra + row * p.ld_extra + cg + 16, p.ld_extra, row0, lane, p.M, cg + 16, p.N, p.vec_extra);
+                }
+            };
+            auto sums_ready = [&] {
+                ok = __all_sync(0xffffffffu, wait_cluster(&tfull[n & 1], (n >> 1) & 1));
+                tc_fence_after();
+                return ok;
+            };
             // the accumulators are read: hand them back to the issuer
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) remote_arrive(leader_addr(&tempty[acc]));
+            auto sums_read = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) remote_arrive(leader_addr(&tempty[n & 1]));
+                ++n;
+            };
+            if constexpr (F32) {
+                float sv[kGroups][16], su[kGated ? kGroups : 1][16];
+                auto add = [&](uint32_t from, bool first) {
+#pragma unroll
+                    for (int g = 0; g < kGroups; ++g) {
+                        if (g >= groups) continue;
+                        float v[16], u[16];
+                        tmem_ld16(from + 16 * g, v);
+                        if constexpr (kGated) tmem_ld16(from + BN / 2 + 16 * g, u);
+                        tmem_ld_wait();
+                        pin16(v);
+                        if constexpr (kGated) pin16(u);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            sv[g][j] = first ? v[j] : sv[g][j] + v[j];
+                            if constexpr (kGated) su[g][j] = first ? u[j] : su[g][j] + u[j];
+                        }
+                    }
+                };
+                for (int kb = 0; kb < p.kblocks; kb += kChain) {
+                    if (!sums_ready()) break;
+                    if (kb == 0) add(lanes + (n & 1) * BN, true);
+                    else add(lanes + (n & 1) * BN, false);
+                    if (kb + kChain >= p.kblocks) add(lanes + (2 + parity) * BN, false);  // the small products
+                    sums_read();
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+                    if (g >= groups) continue;
+                    float e[16];
+                    extra_of(g, e);
+                    finish(g, sv[g], su[kGated ? g : 0], e);
+                }
+            } else {
+                const uint32_t tl = lanes + (n & 1) * BN;
+                if (!sums_ready()) break;
+                float nv[16], nu[kGated ? 16 : 1];
+                if (groups) {
+                    tmem_ld16(tl, nv);
+                    if constexpr (kGated) tmem_ld16(tl + BN / 2, nu);
+                }
+                // (rolled: unrolled over a tile's columns, an activation's code left the instruction cache at every pass)
+#pragma unroll 1
+                for (int g = 0; g < groups; ++g) {
+                    float v[16], u[16], e[16];
+                    extra_of(g, e);
+                    tmem_ld_wait();
+                    pin16(nv);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = nv[j];
+                    if constexpr (kGated) {
+                        pin16(nu);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) u[j] = nu[j];
+                    }
+                    if (g + 1 < groups) {
+                        tmem_ld16(tl + 16 * (g + 1), nv);
+                        if constexpr (kGated) tmem_ld16(tl + BN / 2 + 16 * (g + 1), nu);
+                    }
+                    finish(g, v, u, e);
+                }
+                sums_read();
+            }
         }
     }
     if (!ok) {
@@ -585,20 +714,25 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder()
 
 size_t esz(gdn_dtype t) { return t == GDN_F32 ? 4 : t == GDN_BF16 ? 2 : 1; }
 
-template <bool FP8, int LAYOUT, int EPI, int BN, typename TO>
+template <int KIND, int LAYOUT, int EPI, int BN, typename TO>
 cudaError_t go(const GemmArgs &g, cudaStream_t st)
 {
     constexpr bool gated = EPI == kEpiGated || EPI == kEpiGatedBwd;
-    using G = Geo<BN>;
+    using G = Geo<KIND, BN>;
     TcMaps maps;
     std::memset(&maps, 0, sizeof(maps));
     const int64_t brows = gated ? 2 * g.N : g.N;
-    const bool a_ok = LAYOUT == 2 ? make_operand_map(&maps.a, g.in, g.a, g.M, g.K, g.lda, 64) : make_operand_map(&maps.a, g.in, g.a, g.K, g.M, g.lda, 128);
-    const bool b_ok = LAYOUT >= 1 ? make_operand_map(&maps.b, g.in, g.b, brows, g.K, g.ldb, 64) : make_operand_map(&maps.b, g.in, g.b, g.K, brows, g.ldb, BN / 2);
-    if (!a_ok || !b_ok) return cudaErrorInvalidValue;
+    const gdn_dtype in = KIND == kE4m3 ? GDN_E4M3 : GDN_BF16;
+    for (int i = 0; i < (KIND == kF32 ? 3 : 1); ++i) {
+        const void *a = (const char *)g.a + (KIND == kF32 ? 2 * i * g.a_plane : 0), *b = (const char *)g.b + (KIND == kF32 ? 2 * i * g.b_plane : 0);
+        const bool a_ok = LAYOUT == 2 ? make_operand_map(&maps.a[i], in, a, g.M, g.K, g.lda, 64) : make_operand_map(&maps.a[i], in, a, g.K, g.M, g.lda, 128);
+        const bool b_ok = LAYOUT >= 1 ? make_operand_map(&maps.b[i], in, b, brows, g.K, g.ldb, 64)
+                                      : make_operand_map(&maps.b[i], in, b, g.K, brows, g.ldb, BN / 2);
+        if (!a_ok || !b_ok) return cudaErrorInvalidValue;
+    }
     TcParams p{};
     p.M = g.M; p.N = g.N;
-    const int per = G::kAtoms * (FP8 ? 128 : 64);
+    const int per = G::kPerStage * (KIND == kE4m3 ? 128 : 64);
     p.kblocks = (int)((g.K + per - 1) / per);
     p.mt = (int)((g.M + 255) / 256);
     p.nt = (int)((g.N + (gated ? BN / 2 : BN) - 1) / (gated ? BN / 2 : BN));
@@ -615,7 +749,7 @@ cudaError_t go(const GemmArgs &g, cudaStream_t st)
     p.vec_extra = allows(g.extra, g.ld_extra, 0);
     p.vec_out2 = allows(g.out2, g.ldo2, 0);
 
-    auto *kern = gemm_tc_kernel<FP8, LAYOUT, EPI, BN, TO>;
+    auto *kern = gemm_tc_kernel<KIND, LAYOUT, EPI, BN, TO>;
     static std::atomic<uint64_t> seen;
     if (first_on_device(seen)) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
@@ -627,18 +761,20 @@ cudaError_t go(const GemmArgs &g, cudaStream_t st)
     return launch_overlapped(kern, 2 * pairs, 1, kThreads, G::kSmem, 0, st, maps, p);
 }
 
-template <bool FP8, int LAYOUT, int EPI, typename TO>
+template <int KIND, int LAYOUT, int EPI, typename TO>
 cudaError_t pick(const GemmArgs &g, cudaStream_t st)
 {
-    if constexpr (EPI == kEpiGated || EPI == kEpiGatedBwd) {
-        return go<FP8, LAYOUT, EPI, 256, TO>(g, st);
+    if constexpr (KIND == kF32) {
+        return go<KIND, LAYOUT, EPI, 128, TO>(g, st);
+    } else if constexpr (EPI == kEpiGated || EPI == kEpiGatedBwd) {
+        return go<KIND, LAYOUT, EPI, 256, TO>(g, st);
     } else {
         // Whole rounds of tiles over the pairs of SMs decide: a round of 128-column tiles takes 0.58 of one of 256
         // columns (6.2 and 10.7 us at K = 2048: its products re-read A), but fills a ragged last round better.
         const int64_t pairs = device_sm_count() / 2, mt = (g.M + 255) / 256;
         const auto rounds = [&](int bn) { return (mt * ((g.N + bn - 1) / bn) + pairs - 1) / pairs; };
-        if (0.58 * rounds(128) < rounds(256)) return go<FP8, LAYOUT, EPI, 128, TO>(g, st);
-        return go<FP8, LAYOUT, EPI, 256, TO>(g, st);
+        if (0.58 * rounds(128) < rounds(256)) return go<KIND, LAYOUT, EPI, 128, TO>(g, st);
+        return go<KIND, LAYOUT, EPI, 256, TO>(g, st);
     }
 }
 
@@ -646,13 +782,42 @@ cudaError_t pick(const GemmArgs &g, cudaStream_t st)
 // the weight's, and its contraction the batch.)
 bool use_small(const GemmArgs &g) { return !g.a_t && g.M <= 128; }
 
-template <typename T>
-__global__ void __launch_bounds__(256) repack_kernel(const T *src, int64_t ld, int64_t rows, int64_t cols, T *dst, int64_t pitch)
+// fp32 rows as three planes of bf16: each the rounding of what the ones before leave (exactly x for normal values; an
+// infinity or NaN keeps zeros in the lower planes)
+__global__ void __launch_bounds__(256) split_kernel(const float *src, int64_t ld, int64_t rows, int64_t cols, __nv_bfloat16 *dst, int64_t pitch,
+                                                    int64_t plane)
 {
     grid_release();
     grid_wait();
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-        for (int64_t c = threadIdx.x; c < cols; c += 256) dst[r * pitch + c] = src[r * ld + c];
+        for (int64_t c = (int64_t)threadIdx.x * 2; c < cols; c += 512) {
+            float x[2] = {src[r * ld + c], c + 1 < cols ? src[r * ld + c + 1] : 0.f};
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                const uint32_t w = pack_bf16(x[0], x[1]);
+                *(uint32_t *)(dst + i * plane + r * pitch + c) = w;
+                x[0] = fabsf(x[0]) <= 3.4028234e38f && fabsf(__uint_as_float(w << 16)) <= 3.4028234e38f ? x[0] - __uint_as_float(w << 16) : 0.f;
+                x[1] = fabsf(x[1]) <= 3.4028234e38f && fabsf(__uint_as_float(w & 0xffff0000u)) <= 3.4028234e38f ? x[1] - __uint_as_float(w & 0xffff0000u) : 0.f;
+            }
+        }
+}
+
+// rows into a layout of `pitch` elements (a multiple of 16 bytes): four bytes written at a time
+template <typename T>
+__global__ void __launch_bounds__(256) repack_kernel(const T *src, int64_t ld, int64_t rows, int64_t cols, T *dst, int64_t pitch)
+{
+    constexpr int V = 4 / (int)sizeof(T);
+    grid_release();
+    grid_wait();
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+        for (int64_t c = (int64_t)threadIdx.x * V; c < cols; c += 256 * V) {
+            T v[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[j] = c + j < cols ? src[r * ld + c + j] : T(0);
+            uint32_t w;
+            memcpy(&w, v, 4);
+            *(uint32_t *)(dst + r * pitch + c) = w;
+        }
 }
 
 }  // namespace
@@ -678,6 +843,12 @@ bool tma_ok(const void *p, int64_t ld, int64_t rows, size_t e)
     return ((uintptr_t)p & 15) == 0 && (rows <= 1 || (size_t)ld * e % 16 == 0);
 }
 
+cudaError_t launch_split(const float *src, int64_t ld, int64_t rows, int64_t cols, void *dst, int64_t pitch, int64_t plane, cudaStream_t st)
+{
+    const unsigned grid = (unsigned)(rows < 8192 ? rows : 8192);
+    return launch_overlapped(split_kernel, grid, 1, 256, 0, 0, st, src, ld, rows, cols, (__nv_bfloat16 *)dst, pitch, plane);
+}
+
 cudaError_t launch_repack(const void *src, gdn_dtype t, int64_t ld, int64_t rows, int64_t cols, void *dst, int64_t pitch, cudaStream_t st)
 {
     const unsigned grid = (unsigned)(rows < 4096 ? rows : 4096);
@@ -688,27 +859,37 @@ cudaError_t launch_repack(const void *src, gdn_dtype t, int64_t ld, int64_t rows
 
 int64_t gemm_colparts(const GemmArgs &g, Epi epi)
 {
+    if (g.in == GDN_F32 && !g.a_plane) return gemm_simt_colparts(g, epi);
     return g.in != GDN_F32 && use_small(g) ? gemm_small_colparts(g, epi) : (g.M + 31) / 32;
 }
 
 cudaError_t launch_gemm_tc(const GemmArgs &g, Epi epi, cudaStream_t st)
 {
     if (g.M <= 0 || g.N <= 0) return cudaSuccess;
+    if (g.in == GDN_F32) {
+        switch (epi) {
+        case kEpiGated: return pick<kF32, 0, kEpiGated, float>(g, st);
+        case kEpiGatedBwd: return pick<kF32, 0, kEpiGatedBwd, float>(g, st);
+        case kEpiDact: return pick<kF32, 0, kEpiDact, float>(g, st);
+        default: break;
+        }
+        return g.a_t ? pick<kF32, 2, kEpiLinear, float>(g, st) : g.b_t ? pick<kF32, 1, kEpiLinear, float>(g, st) : pick<kF32, 0, kEpiLinear, float>(g, st);
+    }
     if (use_small(g)) return launch_gemm_small(g, epi, st);
     const bool f32 = g.out_dt == GDN_F32;
     if (g.in == GDN_E4M3) {
-        if (epi == kEpiGated) return pick<true, 0, kEpiGated, __nv_bfloat16>(g, st);
-        return f32 ? pick<true, 0, kEpiLinear, float>(g, st) : pick<true, 0, kEpiLinear, __nv_bfloat16>(g, st);
+        if (epi == kEpiGated) return pick<kE4m3, 0, kEpiGated, __nv_bfloat16>(g, st);
+        return f32 ? pick<kE4m3, 0, kEpiLinear, float>(g, st) : pick<kE4m3, 0, kEpiLinear, __nv_bfloat16>(g, st);
     }
     switch (epi) {
-    case kEpiGated: return pick<false, 0, kEpiGated, __nv_bfloat16>(g, st);
-    case kEpiGatedBwd: return pick<false, 0, kEpiGatedBwd, __nv_bfloat16>(g, st);
-    case kEpiDact: return pick<false, 0, kEpiDact, __nv_bfloat16>(g, st);
+    case kEpiGated: return pick<kBf16, 0, kEpiGated, __nv_bfloat16>(g, st);
+    case kEpiGatedBwd: return pick<kBf16, 0, kEpiGatedBwd, __nv_bfloat16>(g, st);
+    case kEpiDact: return pick<kBf16, 0, kEpiDact, __nv_bfloat16>(g, st);
     default: break;
     }
-    if (g.a_t) return pick<false, 2, kEpiLinear, __nv_bfloat16>(g, st);
-    if (g.b_t) return pick<false, 1, kEpiLinear, __nv_bfloat16>(g, st);
-    return f32 ? pick<false, 0, kEpiLinear, float>(g, st) : pick<false, 0, kEpiLinear, __nv_bfloat16>(g, st);
+    if (g.a_t) return pick<kBf16, 2, kEpiLinear, __nv_bfloat16>(g, st);
+    if (g.b_t) return pick<kBf16, 1, kEpiLinear, __nv_bfloat16>(g, st);
+    return f32 ? pick<kBf16, 0, kEpiLinear, float>(g, st) : pick<kBf16, 0, kEpiLinear, __nv_bfloat16>(g, st);
 }
 
 gdn_status read_tc_status(cudaStream_t st)

@@ -59,32 +59,32 @@ constexpr float kGeluB = 1.5957691216057308f * 0.044715f;
 template <bool PRECISE>
 __device__ __forceinline__ void normal_cdf(const float *z, float *phi, float *bell)
 {
-    if (PRECISE) {
+    if constexpr (PRECISE) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             phi[i] = 0.5f * erfcf(z[i] * -0.70710678118654752f);
             bell[i] = expf(-0.5f * z[i] * z[i]);
         }
-        return;
-    }
-    float x[2], t[2], e[2];
+    } else {
+        float x[2], t[2], e[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        t[i] = fast_rcp(fmaf(fabsf(z[i]), 0.35355339059327376f, 1.f));
-        x[i] = z[i] * 0.84932180028801907f;  // x^2: z^2 / 2 in units of log 2
-    }
-    const Pair tt = pair_of(t[0], t[1]);
-    Pair p = pair_of(0.24651730f, 0.24651730f);
-    constexpr float c[9] = {-1.18611495f, 2.14747446f, -1.63775315f, 0.40232158f, -0.26875686f, 0.13963006f, 0.53970062f, 1.44272920f, -2.82574822f};
+        for (int i = 0; i < 2; ++i) {
+            t[i] = fast_rcp(fmaf(fabsf(z[i]), 0.35355339059327376f, 1.f));
+            x[i] = z[i] * 0.84932180028801907f;  // x^2: z^2 / 2 in units of log 2
+        }
+        const Pair tt = pair_of(t[0], t[1]);
+        Pair p = pair_of(0.24651730f, 0.24651730f);
+        constexpr float c[9] = {-1.18611495f, 2.14747446f, -1.63775315f, 0.40232158f, -0.26875686f, 0.13963006f, 0.53970062f, 1.44272920f, -2.82574822f};
 #pragma unroll
-    for (int k = 0; k < 9; ++k) p = fma2(p, tt, pair_of(c[k], c[k]));
-    p = fma2(pair_of(-x[0], -x[1]), pair_of(x[0], x[1]), p);
-    unpair(p, e[0], e[1]);
+        for (int k = 0; k < 9; ++k) p = fma2(p, tt, pair_of(c[k], c[k]));
+        p = fma2(pair_of(-x[0], -x[1]), pair_of(x[0], x[1]), p);
+        unpair(p, e[0], e[1]);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float half = t[i] * fast_exp2(e[i]);  // erfc(|z| / sqrt 2) / 2
-        phi[i] = z[i] < 0.f ? half : 1.f - half;
-        bell[i] = fast_exp2(-x[i] * x[i]);
+        for (int i = 0; i < 2; ++i) {
+            const float half = t[i] * fast_exp2(e[i]);  // erfc(|z| / sqrt 2) / 2
+            phi[i] = z[i] < 0.f ? half : 1.f - half;
+            bell[i] = fast_exp2(-x[i] * x[i]);
+        }
     }
 }
 
@@ -92,27 +92,27 @@ __device__ __forceinline__ void normal_cdf(const float *z, float *phi, float *be
 template <bool PRECISE, int ACT>
 __device__ __forceinline__ void act_value(const float *z, float *v)
 {
-    if (ACT == GDN_ACT_GELU) {
+    if constexpr (ACT == GDN_ACT_GELU) {
         float phi[2], bell[2];
         normal_cdf<PRECISE>(z, phi, bell);
         v[0] = z[0] * phi[0];
         v[1] = z[1] * phi[1];
-        return;
-    }
+    } else {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        if (ACT == GDN_ACT_SILU) v[i] = z[i] * logistic<PRECISE>(z[i]);
-        else if (ACT == GDN_ACT_GELU_TANH) v[i] = z[i] * logistic<PRECISE>(z[i] * (kGeluA + kGeluB * z[i] * z[i]));
-        else if (ACT == GDN_ACT_RELU) v[i] = z[i] < 0.f ? 0.f : z[i];  // (keeps a NaN)
-        else if (ACT == GDN_ACT_SIGMOID) v[i] = logistic<PRECISE>(z[i]);
-        else v[i] = z[i];
+        for (int i = 0; i < 2; ++i) {
+            if (ACT == GDN_ACT_SILU) v[i] = z[i] * logistic<PRECISE>(z[i]);
+            else if (ACT == GDN_ACT_GELU_TANH) v[i] = z[i] * logistic<PRECISE>(z[i] * (kGeluA + kGeluB * z[i] * z[i]));
+            else if (ACT == GDN_ACT_RELU) v[i] = z[i] < 0.f ? 0.f : z[i];  // (keeps a NaN)
+            else if (ACT == GDN_ACT_SIGMOID) v[i] = logistic<PRECISE>(z[i]);
+            else v[i] = z[i];
+        }
     }
 }
 // values and derivatives
 template <bool PRECISE, int ACT>
 __device__ __forceinline__ void act_both(const float *z, float *v, float *d)
 {
-    if (ACT == GDN_ACT_GELU) {
+    if constexpr (ACT == GDN_ACT_GELU) {
         float phi[2], bell[2];
         normal_cdf<PRECISE>(z, phi, bell);
 #pragma unroll
@@ -120,27 +120,27 @@ __device__ __forceinline__ void act_both(const float *z, float *v, float *d)
             v[i] = z[i] * phi[i];
             d[i] = fmaf(z[i] * 0.3989422804014327f, bell[i], phi[i]);  // 1 / sqrt(2 pi)
         }
-        return;
-    }
+    } else {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        if (ACT == GDN_ACT_SILU) {
-            const float p = logistic<PRECISE>(z[i]);
-            v[i] = z[i] * p;
-            d[i] = fmaf(v[i], 1.f - p, p);
-        } else if (ACT == GDN_ACT_GELU_TANH) {
-            const float z2 = z[i] * z[i], p = logistic<PRECISE>(z[i] * (kGeluA + kGeluB * z2));
-            v[i] = z[i] * p;
-            d[i] = p + v[i] * (1.f - p) * (kGeluA + 3.f * kGeluB * z2);
-        } else if (ACT == GDN_ACT_RELU) {
-            v[i] = z[i] < 0.f ? 0.f : z[i];
-            d[i] = z[i] > 0.f ? 1.f : 0.f;
-        } else if (ACT == GDN_ACT_SIGMOID) {
-            v[i] = logistic<PRECISE>(z[i]);
-            d[i] = v[i] * (1.f - v[i]);
-        } else {
-            v[i] = z[i];
-            d[i] = 1.f;
+        for (int i = 0; i < 2; ++i) {
+            if (ACT == GDN_ACT_SILU) {
+                const float p = logistic<PRECISE>(z[i]);
+                v[i] = z[i] * p;
+                d[i] = fmaf(v[i], 1.f - p, p);
+            } else if (ACT == GDN_ACT_GELU_TANH) {
+                const float z2 = z[i] * z[i], p = logistic<PRECISE>(z[i] * (kGeluA + kGeluB * z2));
+                v[i] = z[i] * p;
+                d[i] = p + v[i] * (1.f - p) * (kGeluA + 3.f * kGeluB * z2);
+            } else if (ACT == GDN_ACT_RELU) {
+                v[i] = z[i] < 0.f ? 0.f : z[i];
+                d[i] = z[i] > 0.f ? 1.f : 0.f;
+            } else if (ACT == GDN_ACT_SIGMOID) {
+                v[i] = logistic<PRECISE>(z[i]);
+                d[i] = v[i] * (1.f - v[i]);
+            } else {
+                v[i] = z[i];
+                d[i] = 1.f;
+            }
         }
     }
 }
@@ -175,6 +175,7 @@ struct GemmArgs {
     const void *a, *b;
     int64_t lda, ldb;
     int a_t, b_t;
+    int64_t a_plane, b_plane;        // fp32 as three bf16 planes, this many elements apart (0: as it is)
     const float *x_scale, *w_scale;  // per row of A and of B, nullable (1)
     const float *bias;               // per column, nullable
     gdn_activation act;
@@ -187,9 +188,12 @@ struct GemmArgs {
     float *colpart;                  // kEpiDact: column sums of groups of rows, [gemm_colparts][N], nullable
 };
 
-// bf16 and e4m3 operands whose rows start on 16-byte boundaries (tma_ok); output types as gdn_linear allows
+// bf16 and e4m3 operands whose rows start on 16-byte boundaries (tma_ok), fp32 ones as planes; output types as
+// gdn_linear allows
 cudaError_t launch_gemm_tc(const GemmArgs &g, Epi epi, cudaStream_t st);
 bool tma_ok(const void *p, int64_t ld, int64_t rows, size_t esz);
+// fp32 rows into three planes of bf16 (`plane` elements apart, `pitch` elements per row)
+cudaError_t launch_split(const float *src, int64_t ld, int64_t rows, int64_t cols, void *dst, int64_t pitch, int64_t plane, cudaStream_t st);
 // copies rows into a layout of `pitch` elements per row
 cudaError_t launch_repack(const void *src, gdn_dtype t, int64_t ld, int64_t rows, int64_t cols, void *dst, int64_t pitch, cudaStream_t st);
 gdn_status read_tc_status(cudaStream_t st);  // synchronises; clears
@@ -203,6 +207,7 @@ int64_t gemm_small_colparts(const GemmArgs &g, Epi epi);
 bool make_operand_map(CUtensorMap *m, gdn_dtype t, const void *base, int64_t cols, int64_t rows, int64_t ld, int box_rows);
 
 cudaError_t launch_gemm_simt(const GemmArgs &g, Epi epi, cudaStream_t st);
+int64_t gemm_simt_colparts(const GemmArgs &g, Epi epi);
 
 // out[n] = sum over `parts` rows of part[.][N] (a fixed order: the same sum every time)
 cudaError_t launch_colsum_finish(const float *part, int64_t parts, int64_t N, float *out, cudaStream_t st);

@@ -86,28 +86,35 @@ struct Carve {  // offsets into a workspace
     }
 };
 
-// fp32 on the CUDA cores, bf16 and e4m3 on the tensor cores
+// fp32 rows to this many go to the CUDA cores as they are; more are worth their splitting into bf16 planes for the
+// tensor cores (at 2048 x 2048, 64 rows: 30 us there, 43 us here; 1024 rows: 389 and 63)
+constexpr int64_t kF32Rows = 64;
+
 cudaError_t launch_product(const GemmArgs &g, Epi epi, cudaStream_t st)
 {
-    return g.in == GDN_F32 ? launch_gemm_simt(g, epi, st) : launch_gemm_tc(g, epi, st);
+    return g.in == GDN_F32 && !g.a_plane ? launch_gemm_simt(g, epi, st) : launch_gemm_tc(g, epi, st);
 }
 
-// An operand of the tensor cores: as it is, or, where its rows do not start on 16-byte boundaries, as a padded
-// copy in the workspace (one more read and write of it; its odd rows could only be loaded element by element)
+// An operand of the tensor cores: as it is, or a copy in the workspace: padded where its rows do not start on 16-byte
+// boundaries (one more read and write of it; its odd rows could only be loaded element by element), in bf16 planes where
+// it is fp32.
 struct Operand {
     const void *p;
-    int64_t ld, rows, cols;
+    int64_t ld, rows, cols, plane;
     bool copy;
     size_t off;
-    void plan(const void *ptr, int64_t stride, int64_t r, int64_t c, gdn_dtype t, Carve &ws)
+    void plan(const void *ptr, int64_t stride, int64_t r, int64_t c, gdn_dtype t, bool planes, Carve &ws)
     {
         p = ptr; ld = stride; rows = r; cols = c;
-        copy = t != GDN_F32 && r > 0 && !tma_ok(ptr, stride, r, esize(t));
         off = 0;
+        plane = 0;
+        copy = planes || (t != GDN_F32 && r > 0 && !tma_ok(ptr, stride, r, esize(t)));
         if (copy) {
-            const int64_t q = 16 / (int64_t)esize(t);
+            const size_t e = planes ? 2 : esize(t);
+            const int64_t q = 16 / (int64_t)e;
             ld = (c + q - 1) / q * q;
-            off = ws.take((size_t)r * ld * esize(t));
+            if (planes) plane = r * ld;
+            off = ws.take((size_t)r * ld * e * (planes ? 3 : 1));
         }
     }
     cudaError_t make(int64_t stride, gdn_dtype t, char *base, cudaStream_t st)
@@ -115,7 +122,8 @@ struct Operand {
         if (!copy) return cudaSuccess;
         const void *src = p;
         p = base + off;
-        return launch_repack(src, t, stride, rows, cols, base + off, ld, st);
+        return plane ? launch_split((const float *)src, stride, rows, cols, base + off, ld, plane, st)
+                     : launch_repack(src, t, stride, rows, cols, base + off, ld, st);
     }
 };
 
@@ -157,18 +165,18 @@ gdn_status check_linear(const gdn_linear_args *a, bool gated, bool backward)
 // A call's workspace: padded copies of operands; backward: dz (its rows padded to 16 bytes) and the column sums
 // of groups of 32 rows
 struct LinearPlan {
-    Operand x, w, dy;
+    Operand x, w, dz;  // dz: dy itself without an activation
     int64_t dz_cols, dz_ld, parts;
     size_t off_dz, off_part, bytes;
-    bool own_dz;
+    bool own_dz, planes;
 };
 GemmArgs forward_product(const gdn_linear_args *a, const LinearPlan &p)
 {
     GemmArgs g{};
     g.M = a->rows; g.N = a->out_features; g.K = a->in_features;
     g.in = a->dtype; g.out_dt = a->out_dtype;
-    g.a = p.x.p; g.lda = p.x.ld;
-    g.b = p.w.p; g.ldb = p.w.ld;
+    g.a = p.x.p; g.lda = p.x.ld; g.a_plane = p.x.plane;
+    g.b = p.w.p; g.ldb = p.w.ld; g.b_plane = p.w.plane;
     g.x_scale = a->x_scale; g.w_scale = a->w_scale;
     g.bias = a->bias;
     g.act = a->act;
@@ -180,21 +188,23 @@ LinearPlan plan_linear(const gdn_linear_args *a, bool gated, bool backward)
     LinearPlan p{};
     Carve c;
     const int64_t wrows = (gated ? 2 : 1) * (int64_t)a->out_features;
-    p.x.plan(a->x, a->ldx, a->rows, a->in_features, a->dtype, c);
-    p.w.plan(a->w, a->ldw, a->rows > 0 ? wrows : 0, a->in_features, a->dtype, c);
+    p.planes = a->dtype == GDN_F32 && a->rows > kF32Rows;
+    p.x.plan(a->x, a->ldx, a->rows, a->in_features, a->dtype, p.planes, c);
+    p.w.plan(a->w, a->ldw, a->rows > 0 ? wrows : 0, a->in_features, a->dtype, p.planes, c);
     if (backward) {
         const int64_t q = 16 / (int64_t)esize(a->dtype);
         p.dz_cols = wrows;
         p.own_dz = gated || a->act != GDN_ACT_NONE;
         p.parts = (a->rows + 31) / 32;
+        const void *dz = a->dy;
+        p.dz_ld = a->ld_dy;
         if (p.own_dz) {
             if (a->dbias && a->rows > 0) p.parts = gemm_colparts(forward_product(a, p), kEpiDact);
+            dz = nullptr;  // (in the workspace)
             p.dz_ld = (p.dz_cols + q - 1) / q * q;
             p.off_dz = c.take((size_t)a->rows * p.dz_ld * esize(a->dtype));
-        } else {
-            p.dy.plan(a->dy, a->ld_dy, a->rows, a->out_features, a->dtype, c);
-            p.dz_ld = p.dy.ld;
         }
+        p.dz.plan(dz, p.dz_ld, a->rows, p.dz_cols, a->dtype, p.planes && (a->dx || a->dw), c);
         p.off_part = c.take(a->dbias ? (size_t)p.parts * a->out_features * sizeof(float) : 0);
     }
     p.bytes = c.at;
@@ -218,7 +228,6 @@ gdn_status run_bwd(const gdn_linear_args *a, bool gated, void *ws, size_t ws_byt
     if (p.x.make(a->ldx, a->dtype, base, st) != cudaSuccess || p.w.make(a->ldw, a->dtype, base, st) != cudaSuccess)
         return GDN_ERR_CUDA;
     float *part = a->dbias ? (float *)(base + p.off_part) : nullptr;
-    const void *dz;
     if (p.own_dz) {
         GemmArgs g = forward_product(a, p);
         g.extra = a->dy; g.ld_extra = a->ld_dy;
@@ -226,23 +235,22 @@ gdn_status run_bwd(const gdn_linear_args *a, bool gated, void *ws, size_t ws_byt
         g.out2 = gated ? a->y : nullptr;
         g.ldo2 = a->ldy;
         g.colpart = part;
-        dz = g.out;
+        p.dz.p = g.out;
         if (launch_product(g, gated ? kEpiGatedBwd : kEpiDact, st) != cudaSuccess) return GDN_ERR_CUDA;
-    } else {
-        if (p.dy.make(a->ld_dy, a->dtype, base, st) != cudaSuccess) return GDN_ERR_CUDA;
-        dz = p.dy.p;
-        if (part && launch_colsum_rows(dz, a->dtype, M, N, p.dz_ld, part, st) != cudaSuccess) return GDN_ERR_CUDA;
+    } else if (part && launch_colsum_rows(a->dy, a->dtype, M, N, a->ld_dy, part, st) != cudaSuccess) {
+        return GDN_ERR_CUDA;
     }
+    if ((a->dx || a->dw) && p.dz.make(p.dz_ld, a->dtype, base, st) != cudaSuccess) return GDN_ERR_CUDA;
     if (part && launch_colsum_finish(part, p.parts, N, a->dbias, st) != cudaSuccess) return GDN_ERR_CUDA;
     GemmArgs g{};
     g.in = a->dtype; g.out_dt = a->dtype;
-    g.a = dz; g.lda = p.dz_ld;
+    g.a = p.dz.p; g.lda = p.dz.ld; g.a_plane = p.dz.plane;
     g.act = GDN_ACT_NONE;
     g.b_t = 1;
     if (a->dx) {  // dx[m][k] = sum_n dz[m][n] w[n][k]
         GemmArgs d = g;
         d.M = M; d.N = K; d.K = p.dz_cols;
-        d.b = p.w.p; d.ldb = p.w.ld;
+        d.b = p.w.p; d.ldb = p.w.ld; d.b_plane = p.w.plane;
         d.out = a->dx; d.ldo = K;
         if (launch_product(d, kEpiLinear, st) != cudaSuccess) return GDN_ERR_CUDA;
     }
@@ -250,7 +258,7 @@ gdn_status run_bwd(const gdn_linear_args *a, bool gated, void *ws, size_t ws_byt
         GemmArgs d = g;
         d.M = p.dz_cols; d.N = K; d.K = M;
         d.a_t = 1;
-        d.b = p.x.p; d.ldb = p.x.ld;
+        d.b = p.x.p; d.ldb = p.x.ld; d.b_plane = p.x.plane;
         d.out = a->dw; d.ldo = K;
         if (launch_product(d, kEpiLinear, st) != cudaSuccess) return GDN_ERR_CUDA;
     }

@@ -474,7 +474,7 @@ bool aligned16(const void *p, int64_t ld, int esz) { return ((uintptr_t)p & 15) 
 // costs a thread about as many instructions as twenty elements do, and with one group a thread the kernels are
 // bound by instructions before they are by memory (16384 rows of 2048 in bf16: norm 33.0 us at 75 % of all issue
 // slots, 28.4 with four groups; backward 67.5 us, 59.0 with four and 53.9 with two, whose weight sums leave registers
-// for more threads), so a thread takes up to four (backward: two) as long as every SM has a thousand threads; few
+// for more threads), so a thread takes up to four (backward: two) as long as every SM has 512 threads; few
 // rows are spread over as many threads as they have groups.
 struct RowPlan {
     int vec, vpt, tpr, threads;
@@ -492,7 +492,7 @@ RowPlan plan_rows(int64_t M, int D, int esz, bool vec_ok, bool backward, int num
     };
     p.vpt = most;
     while (threads_of(p.vpt) > kRowThreads) p.vpt *= vec_ok ? 2 : 4;  // (the backward's most, where it does not hold a row)
-    while (p.vpt > least && threads_of(p.vpt / (vec_ok ? 2 : 4)) <= kRowThreads && M * threads_of(p.vpt) < (int64_t)num_sms * 1024)
+    while (p.vpt > least && threads_of(p.vpt / (vec_ok ? 2 : 4)) <= kRowThreads && M * threads_of(p.vpt) < (int64_t)num_sms * 512)
         p.vpt /= vec_ok ? 2 : 4;
     p.tpr = threads_of(p.vpt);
     // (backward: two rows of 2048 a block, whose dw meet before they are written)
