@@ -1,19 +1,22 @@
-// Products on the CUDA cores, with the epilogues of the decoder-block operators: fp32 inputs.  (The tensor cores
-// truncate their running sums: 2e-6 off at a contraction of 2048, five times fp32's own rounding.)
+// Products of fp32 operands on the CUDA cores, with the epilogues of the decoder-block operators: few rows, which do not
+// repay their splitting into bf16 planes for the tensor cores.
 //
-// A CTA of 128 threads owns a tile of 128 x 128 outputs, 16 x 8 entries per thread in packed pairs (one instruction, two
-// fused multiply-adds); 16 values of k at a time through two buffers, the next ones on their way in registers.  Bound: the
-// fp32 pipe, and next to it the 128 bytes a clock that shared memory returns to registers (with 8 x 8 entries per thread
-// that was the bound: 37 of 74 TFLOP/s).  Where such tiles would leave SMs idle: tiles of 64 x 64, 4 x 4 entries per
-// thread, the contraction split over a cluster whose CTAs send their sums to the CTA that finishes the rows.  A thread's
-// columns are two groups half a tile apart, so that a gated tile holds gate and up columns of the same outputs in the same
-// thread.
+// A CTA of 256 threads owns a tile of 64 x 64 outputs, 4 x 4 entries per thread in packed pairs (one instruction, two fused
+// multiply-adds), 32 values of k at a time through two buffers with the next ones on their way in registers.  The
+// contraction is split over a cluster whose CTAs send their sums to the CTA that finishes the rows, in the order of the
+// contraction, so that every SM has work.  A thread's columns are two groups half a tile apart, so that a gated tile holds
+// gate and up columns of the same outputs in the same thread.  Bound: the latency of the loads (64 x 2048 x 2048: see the
+// tables); shared memory's 128 bytes a clock would be next.
 #include "gdn_layer.cuh"
 
 namespace gdn {
 namespace {
 
-constexpr int kKt = 16, kMaxSplit = 8;
+constexpr int kKt = 32, kMaxSplit = 8;
+constexpr int kThreads = 256, T = 64, RM = 4, RG = 2, CN = 4, H = 2, kTy = 16;  // (rows and columns in two groups of two)
+constexpr int kLd = T + 4, kRowStep = T / 2;
+constexpr int E = T * kKt / kThreads, Q = E / 4;  // elements of each operand per thread and step, in fours
+constexpr int kAcross = kThreads / kKt;
 
 // four consecutive elements at p, zero from `left` on
 __device__ __forceinline__ float4 load4(const float *p, bool row, int64_t left, bool vec)
@@ -33,25 +36,15 @@ __device__ __forceinline__ uint32_t peer_addr(const float *p, uint32_t cta)
     return a;
 }
 
-// The two tilings: T x T outputs, RM x CN per thread (rows in groups of RG, columns in two groups)
-template <bool BIG> struct Tiling {
-    static constexpr int T = BIG ? 128 : 64, RM = BIG ? 16 : 4, RG = BIG ? 4 : 2, CN = BIG ? 8 : 4, H = CN / 2;
-    static constexpr int kThreads = (T / RM) * (T / CN);
-    static constexpr int kElems = T * kKt / kThreads;  // of each operand per thread and step
-    static constexpr int kTy = T / RM;
-};
-
-template <int EPI, bool BIG>
-__global__ void __launch_bounds__(Tiling<BIG>::kThreads, 2) gemm_simt_kernel(GemmArgs g, int mtiles, int split, int vec_a, int vec_b)
+template <int EPI>
+__global__ void __launch_bounds__(kThreads, 2) gemm_simt_kernel(GemmArgs g, int mtiles, int split, int vec_a, int vec_b)
 {
-    using L = Tiling<BIG>;
     constexpr bool kGated = EPI == kEpiGated || EPI == kEpiGatedBwd;
-    constexpr int T = L::T, RM = L::RM, RG = L::RG, CN = L::CN, H = L::H, kThreads = L::kThreads, kLd = T + 4;
-    constexpr int kRowStep = T / (RM / RG);          // between a thread's row groups
     constexpr int kOutN = kGated ? T / 2 : T;        // output columns of a tile
     __shared__ __align__(16) float sa[2][kKt][kLd], sb[2][kKt][kLd];
-    __shared__ __align__(16) float red[BIG ? 1 : T * T];  // [split][T / split][T]: sums of the rows finished here
-    __shared__ float cs[EPI == kEpiDact ? L::kTy : 1][T];
+    __shared__ float cs[EPI == kEpiDact ? kTy : 1][T];
+    float *const red = &sa[0][0][0];  // [split][T / split][T], once the operands are dead: sums of the rows finished here
+    static_assert(sizeof(sa) >= T * T * sizeof(float), "sums fit the operands' place");
     grid_release();
     grid_wait();
     const int tid = threadIdx.x, tx = (tid >> 5 & 1) * 8 + (tid & 7), ty = (tid >> 6) * 4 + (tid >> 3 & 3);
@@ -60,9 +53,8 @@ __global__ void __launch_bounds__(Tiling<BIG>::kThreads, 2) gemm_simt_kernel(Gem
     const int64_t m0 = tile % mtiles * T, n0 = tile / mtiles * kOutN;
     const float *A = (const float *)g.a, *B = (const float *)g.b;
 
-    // This thread's elements of each operand's next 16 values of k: consecutive along k of one row (K-major), or fours along
+    // This thread's elements of each operand's next values of k: consecutive along k of one row (K-major), or fours along
     // the rows at one k
-    constexpr int E = L::kElems, Q = E / 4, kAcross = kThreads / kKt;
     const int row = tid % T, koff = tid / T * E, kk = tid / kAcross, at = 4 * (tid % kAcross);
     float4 ra[Q], rb[Q];
     auto fetch = [&](int64_t k0) {
@@ -122,14 +114,12 @@ __global__ void __launch_bounds__(Tiling<BIG>::kThreads, 2) gemm_simt_kernel(Gem
 #pragma unroll
             for (int i = 0; i < RM; i += RG) {
                 const float *p = &sa[buf][k][i / RG * kRowStep + RG * ty];
-                if constexpr (RG == 4) *(float4 *)(a + i) = *(const float4 *)p;
-                else *(float2 *)(a + i) = *(const float2 *)p;
+                *(float2 *)(a + i) = *(const float2 *)p;
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const float *p = &sb[buf][k][h * (T / 2) + H * tx];
-                if constexpr (H == 4) *(float4 *)(b + 2 * h) = *(const float4 *)p;
-                else *(float2 *)(b + h) = *(const float2 *)p;
+                *(float2 *)(b + h) = *(const float2 *)p;
             }
 #pragma unroll
             for (int i = 0; i < RM; ++i) {
@@ -180,8 +170,8 @@ __global__ void __launch_bounds__(Tiling<BIG>::kThreads, 2) gemm_simt_kernel(Gem
     auto row_of = [&](int i) { return i / RG * kRowStep + RG * ty + i % RG; };
     auto col_of = [&](int j) { return (j / H) * (T / 2) + H * tx + j % H; };
     int groups;  // row groups whose column sums lie in cs
-    if (BIG || split == 1) {
-        groups = L::kTy;
+    if (split == 1) {
+        groups = kTy;
         float col[CN] = {};
         with_act(g.act, [&](auto tag) {
 #pragma unroll
@@ -210,7 +200,7 @@ __global__ void __launch_bounds__(Tiling<BIG>::kThreads, 2) gemm_simt_kernel(Gem
             for (int j = 0; j < CN; ++j) cs[ty][col_of(j)] = col[j];
         }
     } else {
-        // partial sums to the CTAs that finish their rows, T / split each
+        // partial sums to the CTAs that finish their rows, T / split each (whose operands are dead once all are here)
         const int per = T / split;
         asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
 #pragma unroll
@@ -263,23 +253,19 @@ __global__ void __launch_bounds__(Tiling<BIG>::kThreads, 2) gemm_simt_kernel(Gem
     }
 }
 
-// 128 x 128 tiles where they make work for most SMs, else 64 x 64 with the contraction split for two CTAs on an SM
+// tiles, and the contraction split for two CTAs on an SM
 struct SimtPlan {
-    bool big;
     int split, mtiles;
     int64_t tiles;
 };
 SimtPlan plan_simt(const GemmArgs &g, Epi epi)
 {
     SimtPlan p;
-    const int64_t sms = device_sm_count(), halves = epi == kEpiGated || epi == kEpiGatedBwd ? 2 : 1;
-    auto tiles = [&](int64_t t) { return ((g.M + t - 1) / t) * ((g.N * halves + t - 1) / t); };
-    p.big = 2 * tiles(128) >= sms;
-    const int64_t t = p.big ? 128 : 64;
-    p.mtiles = (int)((g.M + t - 1) / t);
-    p.tiles = p.mtiles * ((g.N + t / halves - 1) / (t / halves));
+    const int64_t sms = device_sm_count(), out_n = epi == kEpiGated || epi == kEpiGatedBwd ? T / 2 : T;
+    p.mtiles = (int)((g.M + T - 1) / T);
+    p.tiles = p.mtiles * ((g.N + out_n - 1) / out_n);
     p.split = 1;
-    while (!p.big && p.split < kMaxSplit && p.tiles * p.split * 2 <= 2 * sms && g.K / (p.split * 2) >= 4 * kKt) p.split *= 2;
+    while (p.split < kMaxSplit && p.tiles * p.split * 2 <= 2 * sms && g.K / (p.split * 2) >= 2 * kKt) p.split *= 2;
     return p;
 }
 
@@ -330,16 +316,15 @@ cudaError_t launch_gemm_simt(const GemmArgs &g, Epi epi, cudaStream_t st)
     if (g.M <= 0 || g.N <= 0) return cudaSuccess;
     const SimtPlan p = plan_simt(g, epi);
     auto on16 = [](const void *q, int64_t ld) { return ((uintptr_t)q & 15) == 0 && ld % 4 == 0; };
-    auto go = [&](auto *small, auto *big) {
-        return launch_overlapped(p.big ? big : small, (unsigned)(p.tiles * p.split), 1, p.big ? Tiling<true>::kThreads : Tiling<false>::kThreads,
-                                 0, p.split > 1 ? p.split : 0, st, g,
-                                 p.mtiles, p.split, (int)on16(g.a, g.lda), (int)on16(g.b, g.ldb));
+    auto go = [&](auto *kern) {
+        return launch_overlapped(kern, (unsigned)(p.tiles * p.split), 1, kThreads, 0, p.split > 1 ? p.split : 0, st, g, p.mtiles, p.split,
+                                 (int)on16(g.a, g.lda), (int)on16(g.b, g.ldb));
     };
     switch (epi) {
-    case kEpiGated: return go(gemm_simt_kernel<kEpiGated, false>, gemm_simt_kernel<kEpiGated, true>);
-    case kEpiDact: return go(gemm_simt_kernel<kEpiDact, false>, gemm_simt_kernel<kEpiDact, true>);
-    case kEpiGatedBwd: return go(gemm_simt_kernel<kEpiGatedBwd, false>, gemm_simt_kernel<kEpiGatedBwd, true>);
-    default: return go(gemm_simt_kernel<kEpiLinear, false>, gemm_simt_kernel<kEpiLinear, true>);
+    case kEpiGated: return go(gemm_simt_kernel<kEpiGated>);
+    case kEpiDact: return go(gemm_simt_kernel<kEpiDact>);
+    case kEpiGatedBwd: return go(gemm_simt_kernel<kEpiGatedBwd>);
+    default: return go(gemm_simt_kernel<kEpiLinear>);
     }
 }
 
