@@ -96,9 +96,11 @@ __device__ __forceinline__ uint32_t leader_addr(const void *p)
     asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
     return r;
 }
+// (relaxed: what it announces is that accumulators were read, which the tcgen05 fence before it orders; a release would
+// wait for the epilogue's global stores, 1400 cycles a tile)
 __device__ __forceinline__ void remote_arrive(uint32_t bar)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // a wait for arrivals of both CTAs
 __device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity)
@@ -305,11 +307,21 @@ __device__ __forceinline__ void line_out(TO *p, int64_t ld, int64_t row0, int la
     for (int j = 0; j < 16; ++j) w[j] = v[j];
     patch_out<TO>(w, p - lane * ld, ld, (int)(M - row0 < 32 ? M - row0 : 32), (int)(N - c < 16 ? N - c : 16), lane, patch);
 }
-// `count` per-column values from column c on into a warp's shared memory (0 past the end), and 16 of them back
-__device__ __forceinline__ void columns_in(float *dst, const float *src, int64_t c, int64_t N, int count, int lane)
-{
-    for (int i = lane; i < count; i += 32) dst[i] = c + i < N ? __ldg(src + c + i) : 0.f;
-}
+// Per-column values (scales, bias) of one half of a tile, `COUNT` from column c on: four (two) a lane, on their way in
+// registers while the tile before is finished, then in the warp's shared memory; and 16 of them back.  0 past the end.
+template <int COUNT> struct ColumnsAhead {
+    float v[COUNT / 32];
+    __device__ __forceinline__ void fetch(const float *src, int64_t c, int64_t N, int lane)
+    {
+#pragma unroll
+        for (int i = 0; i < COUNT / 32; ++i) v[i] = c + 32 * i + lane < N ? __ldg(src + c + 32 * i + lane) : 0.f;
+    }
+    __device__ __forceinline__ void keep(float *dst, int lane) const
+    {
+#pragma unroll
+        for (int i = 0; i < COUNT / 32; ++i) dst[32 * i + lane] = v[i];
+    }
+};
 __device__ __forceinline__ void columns(const float *src, float *v)
 {
 #pragma unroll
@@ -503,25 +515,54 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
         const TO *const extra = (const TO *)p.extra;
         float *const cs = cols + warp * 256;          // scales (gate, up), bias
         float *const patch = cols + kEpiWarps * 256 + warp * 32 * kPatch;
+        constexpr int kHalf = kOutN / 2;              // columns of this warp
         uint32_t n = 0, parity = 0;
-        for (int t = pair; t < tiles && ok; t += pairs, parity ^= 1) {
+        int64_t row0 = 0, col0 = 0;                   // of the tile at hand
+        auto to_tile = [&](int t) {
             int mi, ni;
             place(t, mi, ni);
-            const int64_t row0 = (int64_t)mi * 256 + rank * 128 + q * 32, row = row0 + lane;
-            const int64_t col0 = (int64_t)ni * kOutN + half * (kOutN / 2);
-            const bool in = row < p.M;
-            const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + half * (kOutN / 2);
+            row0 = (int64_t)mi * 256 + rank * 128 + q * 32;
+            col0 = (int64_t)ni * kOutN + half * kHalf;
+        };
+        // What a tile's epilogue reads (its column vectors, its first group of residual, dy or dh) is asked for while the
+        // tile before is finished, the other groups' values a group ahead.  (Two groups ahead: registers spill.)
+        Line<TO> ne;
+        ColumnsAhead<kHalf> gate_scale, up_scale, bias_ahead;
+        auto ask_extra = [&](int g) {
+            const int64_t c = col0 + 16 * g;
+            line_in(ne, extra + (row0 + lane) * p.ld_extra + c, p.ld_extra, row0, lane, p.M, c, p.N, p.vec_extra);
+        };
+        auto groups_here = [&] {
             const int64_t left = p.N - col0;  // columns of this warp's half that exist
-            const int groups = row0 >= p.M || left <= 0 ? 0 : left < kGroups * 16 ? (int)((left + 15) / 16) : kGroups;
-            // extra values (residual, dy, dh) and accumulators of the next group load under this group's arithmetic
-            Line<TO> ne;
-            if (kExtra && extra && groups) line_in(ne, extra + row * p.ld_extra + col0, p.ld_extra, row0, lane, p.M, col0, p.N, p.vec_extra);
+            return row0 >= p.M || left <= 0 ? 0 : left < kGroups * 16 ? (int)((left + 15) / 16) : kGroups;
+        };
+        auto ask_tile = [&] {
+            if (FP8 && p.w_scale) gate_scale.fetch(p.w_scale, col0, p.N, lane);
+            if (FP8 && kGated && p.w_scale) up_scale.fetch(p.w_scale + p.N, col0, p.N, lane);
+            if (!kGated && p.bias) bias_ahead.fetch(p.bias, col0, p.N, lane);
+            if (kExtra && extra && groups_here()) {
+                ask_extra(0);
+                // the rest of the row into L2 (16054 x 256 x 8064 with a residual: 190 -> 173 us; flat where the products take longer)
+                if (row0 + lane < p.M)
+                    for (int c = 0; c < kHalf; c += 128 / (int)sizeof(TO))
+                        if (col0 + c < p.N) asm volatile("prefetch.global.L2 [%0];" ::"l"(extra + (row0 + lane) * p.ld_extra + col0 + c));
+            }
+        };
+        if (pair < tiles) {
+            to_tile(pair);
+            ask_tile();
+        }
+        for (int t = pair; t < tiles && ok; t += pairs, parity ^= 1) {
+            const int64_t row = row0 + lane;
+            const bool in = row < p.M;
+            const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + half * kHalf;
+            const int groups = groups_here();
             const float sx = FP8 && p.x_scale && in ? p.x_scale[row] : 1.f;
-            if (groups && (p.bias || (FP8 && p.w_scale))) {
+            if (p.bias || (FP8 && p.w_scale)) {
                 __syncwarp();  // (the last tile's are read)
-                if (FP8 && p.w_scale) columns_in(cs, p.w_scale, col0, p.N, kOutN / 2, lane);
-                if (FP8 && kGated && p.w_scale) columns_in(cs + kOutN / 2, p.w_scale + p.N, col0, p.N, kOutN / 2, lane);
-                if (!kGated && p.bias) columns_in(cs + 128, p.bias, col0, p.N, kOutN / 2, lane);
+                if (FP8 && p.w_scale) gate_scale.keep(cs, lane);
+                if (FP8 && kGated && p.w_scale) up_scale.keep(cs + kHalf, lane);
+                if (!kGated && p.bias) bias_ahead.keep(cs + 128, lane);
                 __syncwarp();
             }
             // one group of 16 columns: from its sums to its outputs
@@ -533,7 +574,7 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
 #pragma unroll
                     for (int j = 0; j < 16; ++j) v[j] *= sx * ws[j];
                     if constexpr (kGated) {
-                        columns(cs + kOutN / 2 + 16 * g, ws);
+                        columns(cs + kHalf + 16 * g, ws);
 #pragma unroll
                         for (int j = 0; j < 16; ++j) u[j] *= sx * ws[j];
                     }
@@ -599,11 +640,17 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
                     if (!(lane & 1) && cc < p.N) p.colpart[(row0 >> 5) * p.N + cc] = sum;
                 }
             };
-            auto extra_of = [&](int g, float *e) {
+            auto extra_of = [&](int g, float *e) {  // (called for g = 0, 1, ...)
                 if (kExtra && extra) {
-                    const int64_t cg = col0 + 16 * g;
-                    line_get(ne, e, lane, cg, p.N, p.vec_extra, patch);
-                    if (g + 1 < groups) line_in(ne, extra + row * p.ld_extra + cg + 16, p.ld_extra, row0, lane, p.M, cg + 16, p.N, p.vec_extra);
+                    line_get(ne, e, lane, col0 + 16 * g, p.N, p.vec_extra, patch);
+                    if (g + 1 < groups) ask_extra(g + 1);
+                }
+            };
+            // the next tile's, once the last group has taken its own
+            auto ask_next = [&] {
+                if (t + pairs < tiles) {
+                    to_tile(t + pairs);
+                    ask_tile();
                 }
             };
             auto sums_ready = [&] {
@@ -652,6 +699,7 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
                     extra_of(g, e);
                     finish(g, sv[g], su[kGated ? g : 0], e);
                 }
+                ask_next();
             } else {
                 const uint32_t tl = lanes + (n & 1) * BN;
                 if (!sums_ready()) break;
@@ -677,10 +725,13 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
                     if (g + 1 < groups) {
                         tmem_ld16(tl + 16 * (g + 1), nv);
                         if constexpr (kGated) tmem_ld16(tl + BN / 2 + 16 * (g + 1), nu);
+                    } else {
+                        sums_read();  // (the last accumulators are in registers)
                     }
                     finish(g, v, u, e);
                 }
-                sums_read();
+                if (!groups) sums_read();
+                ask_next();
             }
         }
     }
