@@ -5,8 +5,8 @@
 // multiply-adds), 32 values of k at a time through two buffers with the next ones on their way in registers.  The
 // contraction is split over a cluster whose CTAs send their sums to the CTA that finishes the rows, in the order of the
 // contraction, so that every SM has work.  A thread's columns are two groups half a tile apart, so that a gated tile holds
-// gate and up columns of the same outputs in the same thread.  Bound: the latency of the loads (64 x 2048 x 2048: see the
-// tables); shared memory's 128 bytes a clock would be next.
+// gate and up columns of the same outputs in the same thread.  Bound: the latency of the loads (64 x 2048 x 2048:
+// 28 us); shared memory's 128 bytes a clock would be next.
 #include "gdn_layer.cuh"
 
 namespace gdn {

@@ -39,6 +39,7 @@ constexpr int kABytes = 128 * 128;       // a CTA's rows of A, 128 bytes of k (o
 // adds those partial sums in registers; the others have an accumulator of their own, whose truncation is 2^-8 as large.
 enum Kind : int { kBf16 = 0, kE4m3 = 1, kF32 = 2 };
 constexpr int kChain = 2;
+constexpr float kF32Max = 3.40282347e38f, kBf16Max = 3.38953139e38f;
 
 // Shared memory of a CTA: operands, each epilogue warp's column vectors (scales and bias of its half of a tile; the
 // tensors of the epilogue go between registers and global memory) and its 32 x 16 patch for rows off 16 bytes.  BN = 128: two
@@ -667,7 +668,10 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
             };
             if constexpr (F32) {
                 float sv[kGroups][16], su[kGated ? kGroups : 1][16];
-                auto add = [&](uint32_t from, bool first) {
+                // (an infinite or NaN leading sum stands: a small product of an infinity with a zero plane would spoil it)
+                auto with_small = [](float sum, float small) { return fabsf(sum) <= kF32Max ? sum + small : sum; };
+                enum Part { kFirst, kNext, kSmall };
+                auto add = [&](uint32_t from, auto part) {
 #pragma unroll
                     for (int g = 0; g < kGroups; ++g) {
                         if (g >= groups) continue;
@@ -679,16 +683,17 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
                         if constexpr (kGated) pin16(u);
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
-                            sv[g][j] = first ? v[j] : sv[g][j] + v[j];
-                            if constexpr (kGated) su[g][j] = first ? u[j] : su[g][j] + u[j];
+                            constexpr Part what = (Part)decltype(part)::value;
+                            sv[g][j] = what == kFirst ? v[j] : what == kNext ? sv[g][j] + v[j] : with_small(sv[g][j], v[j]);
+                            if constexpr (kGated) su[g][j] = what == kFirst ? u[j] : what == kNext ? su[g][j] + u[j] : with_small(su[g][j], u[j]);
                         }
                     }
                 };
                 for (int kb = 0; kb < p.kblocks; kb += kChain) {
                     if (!sums_ready()) break;
-                    if (kb == 0) add(lanes + (n & 1) * BN, true);
-                    else add(lanes + (n & 1) * BN, false);
-                    if (kb + kChain >= p.kblocks) add(lanes + (2 + parity) * BN, false);  // the small products
+                    if (kb == 0) add(lanes + (n & 1) * BN, std::integral_constant<int, kFirst>());
+                    else add(lanes + (n & 1) * BN, std::integral_constant<int, kNext>());
+                    if (kb + kChain >= p.kblocks) add(lanes + (2 + parity) * BN, std::integral_constant<int, kSmall>());
                     sums_read();
                 }
                 if (!ok) break;
@@ -833,8 +838,8 @@ cudaError_t pick(const GemmArgs &g, cudaStream_t st)
 // the weight's, and its contraction the batch.)
 bool use_small(const GemmArgs &g) { return !g.a_t && g.M <= 128; }
 
-// fp32 rows as three planes of bf16: each the rounding of what the ones before leave (exactly x for normal values; an
-// infinity or NaN keeps zeros in the lower planes)
+// fp32 rows as three planes of bf16: each the rounding of what the ones before leave (exactly x for normal values), the
+// first no larger than bf16's largest while x is finite; an infinity or NaN has zeros in the lower planes
 __global__ void __launch_bounds__(256) split_kernel(const float *src, int64_t ld, int64_t rows, int64_t cols, __nv_bfloat16 *dst, int64_t pitch,
                                                     int64_t plane)
 {
@@ -843,12 +848,16 @@ __global__ void __launch_bounds__(256) split_kernel(const float *src, int64_t ld
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
         for (int64_t c = (int64_t)threadIdx.x * 2; c < cols; c += 512) {
             float x[2] = {src[r * ld + c], c + 1 < cols ? src[r * ld + c + 1] : 0.f};
+            const bool finite[2] = {fabsf(x[0]) <= kF32Max, fabsf(x[1]) <= kF32Max};
 #pragma unroll
             for (int i = 0; i < 3; ++i) {
-                const uint32_t w = pack_bf16(x[0], x[1]);
+                float y[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) y[j] = finite[j] ? fminf(fmaxf(x[j], -kBf16Max), kBf16Max) : i ? 0.f : x[j];
+                const uint32_t w = pack_bf16(y[0], y[1]);
                 *(uint32_t *)(dst + i * plane + r * pitch + c) = w;
-                x[0] = fabsf(x[0]) <= 3.4028234e38f && fabsf(__uint_as_float(w << 16)) <= 3.4028234e38f ? x[0] - __uint_as_float(w << 16) : 0.f;
-                x[1] = fabsf(x[1]) <= 3.4028234e38f && fabsf(__uint_as_float(w & 0xffff0000u)) <= 3.4028234e38f ? x[1] - __uint_as_float(w & 0xffff0000u) : 0.f;
+                x[0] -= __uint_as_float(w << 16);
+                x[1] -= __uint_as_float(w & 0xffff0000u);
             }
         }
 }

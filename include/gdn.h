@@ -470,7 +470,10 @@ typedef struct {
  * Linear layer with its epilogue:
  *     y = act(x_scale_m w_scale_n (x w^T) + bias) + residual
  * Products are summed in fp32 and the epilogue runs on those sums; y is
- * rounded once.  bf16 and e4m3 inputs run on the tensor cores.
+ * rounded once.  bf16 and e4m3 inputs run on the tensor cores.  fp32 inputs
+ * run on the CUDA cores up to 64 rows and on the tensor cores above, every
+ * value as the sum of three bf16 values (the last bits of fp32 included);
+ * infinities and NaN come through as a plain fp32 sum has them.
  */
 size_t gdn_linear_workspace_size(const gdn_linear_args *a);
 gdn_status gdn_linear(const gdn_linear_args *a, void *workspace, size_t ws_bytes, gdn_stream_t stream);

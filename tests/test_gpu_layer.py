@@ -340,6 +340,24 @@ def test_infinities_stay_in_their_rows(gdn):
     ref.check(h[good], want, bound)
 
 
+@pytest.mark.parametrize("rows", [10, 70])
+def test_fp32_infinities_and_largest_values(gdn, rows):
+    """An infinity times a weight is an infinity of its sign, and values between bf16's and fp32's largest are finite."""
+    g = gen(27)
+    x, w = randn(g, rows, 200), randn(g, 136, 200) / 8
+    w[:, 9] = 1e-6 * (1 + torch.rand(136, generator=g, device="cuda"))
+    w[:, 5] = torch.where(w[:, 5].abs() < 1e-3, 0.5, w[:, 5])
+    w[17, 5] = 0
+    x[3, 5], x[5, 150], x[7, 9] = -float("inf"), float("nan"), 3.4e38
+    y = gdn.linear(x, w)
+    good = [i for i in range(rows) if i not in (3, 5)]
+    want, bound = ref.linear(x[good], w, None, "none", None, torch.float32)
+    ref.check(y[good], want, bound)
+    assert y[5].isnan().all() and y[3, 17].isnan()
+    rest = torch.arange(136, device="cuda") != 17
+    assert torch.equal(y[3][rest], -float("inf") * w[rest, 5].sign())
+
+
 def test_other_stream_and_graph(gdn):
     g = gen(29)
     M, K, F = 200, 256, 320
