@@ -39,24 +39,26 @@ constexpr int kABytes = 128 * 128;       // a CTA's rows of A, 128 bytes of k (o
 // adds those partial sums in registers; the others have an accumulator of their own, whose truncation is 2^-8 as large.
 enum Kind : int { kBf16 = 0, kE4m3 = 1, kF32 = 2 };
 constexpr int kChain = 2;
+constexpr int kMaxSplit = 4;
 constexpr float kF32Max = 3.40282347e38f, kBf16Max = 3.38953139e38f;
 
 // Shared memory of a CTA: operands, each epilogue warp's column vectors (scales and bias of its half of a tile; the
 // tensors of the epilogue go between registers and global memory) and its 32 x 16 patch for rows off 16 bytes.  BN = 128: two
 // 128-byte-wide blocks of k per stage, so that eight products and not four follow each wait (16384 x 2048 x 2048:
 // 112 -> 87 us; with BN = 256, whose products take twice as long, it is flat).
-template <int KIND, int BN> struct Geo {
+template <int KIND, int BN, bool SPLIT> struct Geo {
     static constexpr int kAtoms = KIND == kF32 ? 3 : BN == 256 ? 1 : 2;  // (fp32: the planes of one block of k)
     static constexpr int kPerStage = KIND == kF32 ? 1 : kAtoms;          // blocks of k
     static constexpr int kB = BN / 2 * 128;
     static constexpr int kAtom = kABytes + kB;  // 128 bytes of k
     static constexpr int kStage = kAtoms * kAtom;
     static constexpr int kColBytes = kEpiWarps * (2 * 128 + 32 * 17) * 4;
-    static constexpr int kStages = (227 * 1024 - 1024 - kColBytes - 256) / kStage;
-    static_assert(kStages == (KIND == kF32 ? 2 : BN == 256 ? 6 : 4) && (KIND != kF32 || BN == 128), "stages");
+    static constexpr int kParts = SPLIT ? kEpiWarps * 3 * 16 * 128 : 0;  // the other CTAs' sums of a split contraction
+    static constexpr int kStages = (227 * 1024 - 1024 - kColBytes - kParts - 256) / kStage;
+    static_assert(kStages == (KIND == kF32 ? 2 : BN == 256 ? 6 : SPLIT ? 3 : 4) && (KIND != kF32 || BN == 128), "stages");
     static constexpr int kBars = 2 * kStages + 4;
     static constexpr int kTmem = (KIND == kF32 ? 4 : 2) * BN;  // two accumulators (fp32: and two for the small products)
-    static constexpr int kSmem = 1024 + kStages * kStage + kColBytes + kBars * 8 + 16;
+    static constexpr int kSmem = 1024 + kStages * kStage + kColBytes + kParts + kBars * 8 + 16;
     static_assert(kSmem <= 227 * 1024, "shared memory budget");
 };
 
@@ -67,6 +69,7 @@ struct TcParams {
     int64_t M, N;            // output rows; output columns (gated: F)
     int kblocks;             // stages of k
     int mt, nt;              // tiles of 256 rows, of BN accumulator columns
+    int split;               // pairs that share a tile's contraction (SPLIT: 2 or 4)
     int vec_extra, vec_out, vec_out2;  // what their rows allow: accesses of 32 bytes (2), of 16 (1) or of elements
     const float *x_scale, *w_scale, *bias;
     int act;
@@ -90,12 +93,16 @@ __device__ __forceinline__ void cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
 }
-// the address, in the first CTA of the pair, of a barrier at the same place
-__device__ __forceinline__ uint32_t leader_addr(const void *p)
+// the address, in CTA `cta` of the cluster, of what is at p here
+__device__ __forceinline__ uint32_t peer_addr(const void *p, uint32_t cta)
 {
     uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(cta));
     return r;
+}
+__device__ __forceinline__ void peer_store(uint32_t addr, float v)
+{
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 // (relaxed: what it announces is that accumulators were read, which the tcgen05 fence before it orders; a release would
 // wait for the epilogue's global stores, 1400 cycles a tile)
@@ -147,13 +154,13 @@ __device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uin
             "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
             "l"(a), "l"(b), "r"(idesc), "r"(acc));
 }
-// arrives on the barrier at the same place in both CTAs once every product issued so far is done
-__device__ __forceinline__ void pair_commit(uint64_t *bar)
+// arrives on the barrier at the same place in both CTAs of the pair from `leader` on once every product issued so far is done
+__device__ __forceinline__ void pair_commit(uint64_t *bar, uint32_t leader)
 {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
             smem_u32(bar)),
-        "h"((uint16_t)3)
+        "h"((uint16_t)(3u << leader))
         : "memory");
 }
 
@@ -360,8 +367,12 @@ __device__ __forceinline__ float column_sums(float *v, int lane)
 }
 
 // LAYOUT 0: A and B K-major; 1: B MN-major; 2: both MN-major
-template <int KIND, int LAYOUT, int EPI, int BN, typename TO>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+//
+// SPLIT: fewer tiles than pairs, so `split` pairs (a cluster) share a tile: each sums its part of the contraction, sends
+// its sums of the columns that another pair finishes to that pair's shared memory (32 rows of a column to a store), and
+// finishes its own share, the parts added in the order of the contraction.
+template <int KIND, int LAYOUT, int EPI, int BN, typename TO, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, 1)
 gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
 {
     constexpr bool kGated = EPI == kEpiGated || EPI == kEpiGatedBwd;
@@ -369,18 +380,22 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
     constexpr bool kPrecise = sizeof(TO) == 4;
     constexpr int kOutN = kGated ? BN / 2 : BN;  // output columns of a tile
     constexpr bool FP8 = KIND == kE4m3, F32 = KIND == kF32;
-    using G = Geo<KIND, BN>;
+    using G = Geo<KIND, BN, SPLIT>;
     constexpr int kAtoms = G::kAtoms;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     float *const cols = (float *)(sm + G::kStages * G::kStage);
-    uint64_t *full = (uint64_t *)(sm + G::kStages * G::kStage + G::kColBytes);
+    float *const parts = (float *)(sm + G::kStages * G::kStage + G::kColBytes);
+    uint64_t *full = (uint64_t *)(sm + G::kStages * G::kStage + G::kColBytes + G::kParts);
     uint64_t *empty = full + G::kStages, *tfull = empty + G::kStages, *tempty = tfull + 2;
     uint32_t *tslot = (uint32_t *)(tempty + 2);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t rank = cluster_rank();
-    const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
+    const uint32_t crank = cluster_rank(), rank = crank & 1, leader = SPLIT ? crank & ~1u : 0;
     const int tiles = p.mt * p.nt;
+    const int pairs = SPLIT ? tiles : gridDim.x >> 1, pair = SPLIT ? blockIdx.x / (2 * p.split) : blockIdx.x >> 1;
+    const int share = SPLIT ? crank >> 1 : 0;  // its part of the contraction: blocks kb0 ..
+    const int kb0 = SPLIT ? p.kblocks * share / p.split : 0;
+    const int kblocks = SPLIT ? p.kblocks * (share + 1) / p.split - kb0 : p.kblocks;
 
     if (tid == 0) {
         for (int s = 0; s < G::kStages; ++s) {
@@ -421,11 +436,11 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
             place(t, mi, ni);
             const int m0 = mi * 256 + (int)rank * 128;
             const int n0 = kGated ? (rank ? (int)p.N : 0) + ni * kOutN : ni * BN + (int)rank * (BN / 2);
-            for (int kb = 0; kb < p.kblocks; ++kb) {
+            for (int kb = kb0; kb < kb0 + kblocks; ++kb) {
                 if (!(ok = __all_sync(0xffffffffu, wait_cta(&empty[s], ph)))) break;
                 if (elect_one_sync()) {
                     if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * G::kStage);
-                    const uint32_t bar = leader_addr(&full[s]);
+                    const uint32_t bar = peer_addr(&full[s], leader);
 #pragma unroll
                     for (int at = 0; at < kAtoms; ++at) {
                         uint8_t *sa = sm + s * G::kStage + at * G::kAtom, *sb = sa + kABytes;
@@ -454,6 +469,7 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
             ok = __all_sync(0xffffffffu, wait_cta(&empty[s], ph));
             if (++s == G::kStages) { s = 0; ph ^= 1; }
         }
+        if (SPLIT) cluster_sync();  // (the exchange of the parts)
     } else if (warp == kEpiWarps + 1) {
         // ---------------------------------------------------------------- products
         if (rank == 0) {
@@ -467,7 +483,7 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
             uint32_t s = 0, ph = 0, n = 0, parity = 0;
             for (int t = pair; t < tiles && ok; t += pairs, parity ^= 1) {
                 const uint32_t small = tmem + (2 + parity) * BN;  // (fp32)
-                for (int kb = 0, chain = 0; kb < p.kblocks; ++kb) {
+                for (int kb = 0, chain = 0; kb < kblocks; ++kb) {
                     const uint32_t acc = n & 1;
                     if (chain == 0) {
                         if (!(ok = __all_sync(0xffffffffu, wait_cluster(&tempty[acc], ((n >> 1) & 1) ^ 1)))) break;
@@ -478,7 +494,7 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
                     const uint64_t da = da0 + s * (G::kStage >> 4), db = db0 + s * (G::kStage >> 4);
                     uint64_t *const rel = &empty[s];
                     if (++s == G::kStages) { s = 0; ph ^= 1; }
-                    const bool last = kb + 1 == p.kblocks || (F32 && chain + 1 == kChain);
+                    const bool last = kb + 1 == kblocks || (F32 && chain + 1 == kChain);
                     if (elect_one_sync()) {
                         if constexpr (F32) {
                             constexpr int pa[5] = {0, 1, 1, 0, 2}, pb[5] = {1, 0, 1, 2, 0};
@@ -497,8 +513,8 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
                                 pair_mma<FP8>(tmem + acc * BN, da + (j >> 2) * (G::kAtom >> 4) + (j & 3) * sa_step,
                                               db + (j >> 2) * (G::kAtom >> 4) + (j & 3) * sb_step, id, (kb | j) != 0);
                         }
-                        pair_commit(rel);
-                        if (last) pair_commit(&tfull[acc]);
+                        pair_commit(rel, leader);
+                        if (last) pair_commit(&tfull[acc], leader);
                     }
                     __syncwarp();
                     ++chain;
@@ -509,6 +525,7 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
                 }
             }
         }
+        if (SPLIT) cluster_sync();
     } else {
         // ---------------------------------------------------------------- epilogue
         constexpr int kGroups = kOutN / 32;           // groups of 16 columns of this warp: half of the tile's
@@ -527,6 +544,8 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
         };
         // What a tile's epilogue reads (its column vectors, its first group of residual, dy or dh) is asked for while the
         // tile before is finished, the other groups' values a group ahead.  (Two groups ahead: registers spill.)
+        // the groups that this pair finishes: all, or its share
+        const int per = SPLIT ? kGroups / p.split : kGroups, g_lo = share * per, g_hi = g_lo + per;
         Line<TO> ne;
         ColumnsAhead<kHalf> gate_scale, up_scale, bias_ahead;
         auto ask_extra = [&](int g) {
@@ -541,12 +560,46 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
             if (FP8 && p.w_scale) gate_scale.fetch(p.w_scale, col0, p.N, lane);
             if (FP8 && kGated && p.w_scale) up_scale.fetch(p.w_scale + p.N, col0, p.N, lane);
             if (!kGated && p.bias) bias_ahead.fetch(p.bias, col0, p.N, lane);
-            if (kExtra && extra && groups_here()) {
-                ask_extra(0);
+            if (kExtra && extra && groups_here() > g_lo) {
+                ask_extra(g_lo);
                 // the rest of the row into L2 (16054 x 256 x 8064 with a residual: 190 -> 173 us; flat where the products take longer)
                 if (row0 + lane < p.M)
                     for (int c = 0; c < kHalf; c += 128 / (int)sizeof(TO))
                         if (col0 + c < p.N) asm volatile("prefetch.global.L2 [%0];" ::"l"(extra + (row0 + lane) * p.ld_extra + col0 + c));
+            }
+        };
+        // where the sums of group g from share `from` lie: the other shares' in their order, a column's 32 rows together
+        constexpr int kVals = kGated ? 32 : 16;
+        auto box = [&](int from, int g) {
+            const int owner = g / per;
+            return parts + (((warp * (p.split - 1) + (from < owner ? from : from - 1)) * per + g - owner * per) * kVals) * 32 + lane;
+        };
+        auto send = [&](int g, const float *v, const float *u) {
+            const uint32_t dst = peer_addr(box(share, g), 2 * (g / per) + rank);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                peer_store(dst + 128 * j, v[j]);
+                if constexpr (kGated) peer_store(dst + 128 * (16 + j), u[j]);
+            }
+        };
+        auto join = [&](int g, float *v, float *u) {
+            float sv[16], su[16];
+            for (int from = 0; from < p.split; ++from) {
+                const float *src = box(from, g);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float a = from == share ? v[j] : src[32 * j];
+                    sv[j] = from ? sv[j] + a : a;
+                    if constexpr (kGated) {
+                        const float b = from == share ? u[j] : src[32 * (16 + j)];
+                        su[j] = from ? su[j] + b : b;
+                    }
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                v[j] = sv[j];
+                if constexpr (kGated) u[j] = su[j];
             }
         };
         if (pair < tiles) {
@@ -641,10 +694,10 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
                     if (!(lane & 1) && cc < p.N) p.colpart[(row0 >> 5) * p.N + cc] = sum;
                 }
             };
-            auto extra_of = [&](int g, float *e) {  // (called for g = 0, 1, ...)
+            auto extra_of = [&](int g, float *e) {  // (called for g = g_lo, g_lo + 1, ...)
                 if (kExtra && extra) {
                     line_get(ne, e, lane, col0 + 16 * g, p.N, p.vec_extra, patch);
-                    if (g + 1 < groups) ask_extra(g + 1);
+                    if (g + 1 < groups && g + 1 < g_hi) ask_extra(g + 1);
                 }
             };
             // the next tile's, once the last group has taken its own
@@ -663,7 +716,7 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
             auto sums_read = [&] {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) remote_arrive(leader_addr(&tempty[n & 1]));
+                if (lane == 0) remote_arrive(peer_addr(&tempty[n & 1], leader));
                 ++n;
             };
             if constexpr (F32) {
@@ -689,22 +742,58 @@ gemm_tc_kernel(const __grid_constant__ TcMaps maps, const TcParams p)
                         }
                     }
                 };
-                for (int kb = 0; kb < p.kblocks; kb += kChain) {
+                for (int kb = 0; kb < kblocks; kb += kChain) {
                     if (!sums_ready()) break;
                     if (kb == 0) add(lanes + (n & 1) * BN, std::integral_constant<int, kFirst>());
                     else add(lanes + (n & 1) * BN, std::integral_constant<int, kNext>());
-                    if (kb + kChain >= p.kblocks) add(lanes + (2 + parity) * BN, std::integral_constant<int, kSmall>());
+                    if (kb + kChain >= kblocks) add(lanes + (2 + parity) * BN, std::integral_constant<int, kSmall>());
                     sums_read();
+                }
+                if constexpr (SPLIT) {
+                    if (ok) {
+#pragma unroll
+                        for (int g = 0; g < kGroups; ++g)
+                            if (g < groups && (g < g_lo || g >= g_hi)) send(g, sv[g], su[kGated ? g : 0]);
+                    }
+                    cluster_sync();
                 }
                 if (!ok) break;
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) {
-                    if (g >= groups) continue;
+                    if (g >= groups || (SPLIT && (g < g_lo || g >= g_hi))) continue;
                     float e[16];
                     extra_of(g, e);
+                    if constexpr (SPLIT) join(g, sv[g], su[kGated ? g : 0]);
                     finish(g, sv[g], su[kGated ? g : 0], e);
                 }
                 ask_next();
+            } else if constexpr (SPLIT) {
+                const uint32_t tl = lanes;
+                float v[16], u[16], e[16];
+                auto sums = [&](int g) {
+                    tmem_ld16(tl + 16 * g, v);
+                    if constexpr (kGated) tmem_ld16(tl + BN / 2 + 16 * g, u);
+                    tmem_ld_wait();
+                    pin16(v);
+                    if constexpr (kGated) pin16(u);
+                };
+                if (sums_ready()) {
+#pragma unroll 1
+                    for (int g = 0; g < groups; ++g) {
+                        if (g >= g_lo && g < g_hi) continue;
+                        sums(g);
+                        send(g, v, u);
+                    }
+                }
+                cluster_sync();
+                if (!ok) break;
+#pragma unroll 1
+                for (int g = g_lo; g < groups && g < g_hi; ++g) {
+                    extra_of(g, e);
+                    sums(g);
+                    join(g, v, u);
+                    finish(g, v, u, e);
+                }
             } else {
                 const uint32_t tl = lanes + (n & 1) * BN;
                 if (!sums_ready()) break;
@@ -770,11 +859,11 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder()
 
 size_t esz(gdn_dtype t) { return t == GDN_F32 ? 4 : t == GDN_BF16 ? 2 : 1; }
 
-template <int KIND, int LAYOUT, int EPI, int BN, typename TO>
-cudaError_t go(const GemmArgs &g, cudaStream_t st)
+template <int KIND, int LAYOUT, int EPI, int BN, typename TO, bool SPLIT = false>
+cudaError_t go(const GemmArgs &g, cudaStream_t st, int split = 1)
 {
     constexpr bool gated = EPI == kEpiGated || EPI == kEpiGatedBwd;
-    using G = Geo<KIND, BN>;
+    using G = Geo<KIND, BN, SPLIT>;
     TcMaps maps;
     std::memset(&maps, 0, sizeof(maps));
     const int64_t brows = gated ? 2 * g.N : g.N;
@@ -796,6 +885,7 @@ cudaError_t go(const GemmArgs &g, cudaStream_t st)
     p.extra = g.extra; p.ld_extra = g.ld_extra;
     p.out = g.out; p.ldo = g.ldo; p.out2 = g.out2; p.ldo2 = g.ldo2;
     p.colpart = g.colpart;
+    p.split = split;
     const size_t eo = sizeof(TO);
     auto allows = [&](const void *q, int64_t ld, size_t also) {
         const size_t off = (uintptr_t)q | (g.M > 1 ? (size_t)ld * eo : 0) | also;
@@ -805,7 +895,7 @@ cudaError_t go(const GemmArgs &g, cudaStream_t st)
     p.vec_extra = allows(g.extra, g.ld_extra, 0);
     p.vec_out2 = allows(g.out2, g.ldo2, 0);
 
-    auto *kern = gemm_tc_kernel<KIND, LAYOUT, EPI, BN, TO>;
+    auto *kern = gemm_tc_kernel<KIND, LAYOUT, EPI, BN, TO, SPLIT>;
     static std::atomic<uint64_t> seen;
     if (first_on_device(seen)) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
@@ -813,22 +903,70 @@ cudaError_t go(const GemmArgs &g, cudaStream_t st)
         done_on_device(seen);
     }
     const int64_t tiles = (int64_t)p.mt * p.nt;
-    const int pairs = (int)(tiles < device_sm_count() / 2 ? tiles : device_sm_count() / 2);
-    return launch_overlapped(kern, 2 * pairs, 1, kThreads, G::kSmem, 0, st, maps, p);
+    const int pairs = SPLIT ? (int)tiles * split : (int)(tiles < device_sm_count() / 2 ? tiles : device_sm_count() / 2);
+    return launch_overlapped(kern, 2 * pairs, 1, kThreads, G::kSmem, 2 * split, st, maps, p);
+}
+
+// (holds no tensor memory: the runtime answers one block per SM for a kernel that does, whatever else it asks for)
+__global__ void __launch_bounds__(kThreads) place_kernel() {}
+
+// clusters of 2 `split` CTAs, one to an SM, that the device runs at once (asked once per device)
+int64_t clusters_at_once(int split)
+{
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices][kMaxSplit + 1];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) dev = 0;
+    int n = known[dev][split].load(std::memory_order_relaxed);
+    if (n) return n;
+    constexpr int room = 200 * 1024;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2u * split;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(2u * split);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = room;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, room) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, place_kernel, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        n = device_sm_count() / (2 * split + 2);
+    }
+    known[dev][split].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// Pairs that share a tile's contraction: as many as there is room for, while each keeps enough of it to repay the
+// exchange of the sums (1.2 us for two, 2.0 us for four): six stages of bf16 or e4m3 (of 0.26 us; 256 x 2048 outputs:
+// K = 1024 6.1 us alone and 6.3 as two, K = 2048 8.2 and 7.5, K = 5504 15.3 and 11.6; 256 x 512 x 8192 20.6, 13.9 as two,
+// 10.1 as four); two of fp32 (six products each; 256 x 1024 x 512: 15.9, 13.7, 12.4 us); two of a gated tile.
+template <int KIND>
+int split_for(const GemmArgs &g, bool gated)
+{
+    const int64_t wide = gated ? 64 : 128, tiles = (g.M + 255) / 256 * ((g.N + wide - 1) / wide);
+    const int per = Geo<KIND, 128, true>::kPerStage * (KIND == kE4m3 ? 128 : 64);
+    const int64_t kb = (g.K + per - 1) / per, least = KIND == kF32 || gated ? 2 : 6;
+    for (int split = gated ? 2 : kMaxSplit; split > 1; split /= 2)
+        if (kb >= split * least && tiles <= clusters_at_once(split)) return split;
+    return 1;
 }
 
 template <int KIND, int LAYOUT, int EPI, typename TO>
 cudaError_t pick(const GemmArgs &g, cudaStream_t st)
 {
+    constexpr bool gated = EPI == kEpiGated || EPI == kEpiGatedBwd;
+    const int split = split_for<KIND>(g, gated);
+    if (split > 1) return go<KIND, LAYOUT, EPI, 128, TO, true>(g, st, split);
     if constexpr (KIND == kF32) {
         return go<KIND, LAYOUT, EPI, 128, TO>(g, st);
-    } else if constexpr (EPI == kEpiGated || EPI == kEpiGatedBwd) {
-        return go<KIND, LAYOUT, EPI, 256, TO>(g, st);
     } else {
         // Whole rounds of tiles over the pairs of SMs decide: a round of 128-column tiles takes 0.58 of one of 256
         // columns (6.2 and 10.7 us at K = 2048: its products re-read A), but fills a ragged last round better.
         const int64_t pairs = device_sm_count() / 2, mt = (g.M + 255) / 256;
-        const auto rounds = [&](int bn) { return (mt * ((g.N + bn - 1) / bn) + pairs - 1) / pairs; };
+        const auto rounds = [&](int64_t bn) { return (mt * ((g.N * (gated ? 2 : 1) + bn - 1) / bn) + pairs - 1) / pairs; };
         if (0.58 * rounds(128) < rounds(256)) return go<KIND, LAYOUT, EPI, 128, TO>(g, st);
         return go<KIND, LAYOUT, EPI, 256, TO>(g, st);
     }

@@ -253,6 +253,46 @@ def test_gated_bwd(gdn, M, F, K, dtype):
     ref.check(y, *ref.gated(x, w, name, dtype), f"{name} y")
 
 
+# contractions long enough, and outputs few enough, for several pairs of SMs to share a tile; the least rows of the tiles
+# of 256; a weight's gradient over many rows
+LONG = [(128, 130, 1600), (129, 72, 1600), (129, 200, 3216), (257, 330, 3200), (520, 129, 6416), (4100, 72, 104)]
+
+
+@pytest.mark.parametrize("M,N,K", LONG)
+@pytest.mark.parametrize("dtype", [BF, F32, E4])
+def test_long_contractions(gdn, M, N, K, dtype):
+    g = gen(M + N + K)
+    x, w, xs, ws = operands(g, M, N, K, dtype)
+    b = randn(g, N)
+    for out in ((F32,) if dtype == F32 else (BF, F32)):
+        r = randn(g, M, N, dtype=out)
+        y = gdn.linear(x, w, b, "gelu", r, x_scale=xs, weight_scale=ws, out_dtype=out)
+        want, bound = ref.linear(x, w, b, "gelu", r, out, xs, ws)
+        ref.check(y, want, bound, f"{out}")
+        assert torch.equal(y, gdn.linear(x, w, b, "gelu", r, x_scale=xs, weight_scale=ws, out_dtype=out))
+    x, w, xs, ws = operands(g, M, 2 * N, K, dtype)
+    h = gdn.gated_linear(x, w, "silu", x_scale=xs, weight_scale=ws)
+    want, bound = ref.gated(x, w, "silu", F32 if dtype == F32 else BF, xs, ws)
+    ref.check(h, want, bound, "gated")
+
+
+@pytest.mark.parametrize("M,N,K", LONG)
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_long_contractions_bwd(gdn, M, N, K, dtype):
+    g = gen(M + N + K)
+    x, w, _, _ = operands(g, M, N, K, dtype)
+    b, dy = randn(g, N), randn(g, M, N, dtype=dtype)
+    want, bound = ref.linear_bwd(dy, x, w, b, "silu", dtype)
+    got = gdn.linear_bwd(dy, x, w, b, "silu")
+    for n, a, e, t in zip(("dx", "dw", "db"), got, want, bound):
+        ref.check(a, e, t, n)
+    assert all(torch.equal(a, c) for a, c in zip(got, gdn.linear_bwd(dy, x, w, b, "silu")))
+    w = operands(g, M, 2 * N, K, dtype)[1]
+    got, (want, bound) = gdn.gated_linear_bwd(dy, x, w, "gelu"), ref.gated_bwd(dy, x, w, "gelu", dtype)
+    for n, a, e, t in zip(("dx", "dw"), got, want, bound):
+        ref.check(a, e, t, f"gated {n}")
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_gradients_against_differences(gdn, dtype):
     """Central differences of the 64-bit forward along random directions."""
