@@ -6,7 +6,7 @@
 // and workspaces come from PyTorch's allocator; the work runs on the current stream of the input's device.
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -96,9 +96,15 @@ Tensor vec(const char *name, const Tensor &t, int64_t n, const Tensor &with, boo
     return t.contiguous();
 }
 
+// (straight to the allocator: by the dispatcher, at::empty, a tensor takes 0.4 us longer, of a call's 4 to 8)
+Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const Tensor &on)
+{
+    return at::detail::empty_cuda(shape, type, on.device(), std::nullopt);
+}
+
 Tensor output(const char *name, const Tensor *given, at::IntArrayRef shape, at::ScalarType type, const Tensor &like)
 {
-    if (!given) return at::empty(shape, like.options().dtype(type).requires_grad(false));
+    if (!given) return fresh(shape, type, like);
     if (given->sizes() != shape || given->scalar_type() != type || given->device() != like.device() || !given->is_contiguous())
         bad_value(std::string(name) + " must be a contiguous tensor of the output's shape, dtype and device");
     return *given;
@@ -130,7 +136,7 @@ void launch(gdn_status (*call)(const Args *, void *, size_t, gdn_stream_t), size
 {
     const size_t need = size(&a);
     if (!need) return checked(call(&a, nullptr, 0, stream_of(on)), what);
-    const Tensor ws = at::empty({(int64_t)need}, on.options().dtype(at::kByte).requires_grad(false));
+    const Tensor ws = fresh({(int64_t)need}, at::kByte, on);
     checked(call(&a, ws.data_ptr(), need, stream_of(on)), what);
 }
 
@@ -226,7 +232,7 @@ PyObject *rms_norm(PyObject *const *p)
     const Tensor y = output("out", tensor("out", p[5], true), x.sizes(), quant ? at::kFloat8_e4m3fn : x.scalar_type(), x);
     a.y = y.data_ptr();
     if (quant) {
-        scale = at::empty(x.sizes().slice(0, x.dim() - 1), x.options().dtype(at::kFloat).requires_grad(false));
+        scale = fresh(x.sizes().slice(0, x.dim() - 1), at::kFloat, x);
         a.out_dtype = GDN_E4M3;
         a.scale = scale.data_ptr<float>();
     }
@@ -246,7 +252,7 @@ PyObject *quantize_rows(PyObject *const *p)
     const Rows xr = rows("x", x, width);
     gdn_norm_args a = norm_args(xr, width);
     const Tensor q = output("out", tensor("out", p[1], true), x.sizes(), at::kFloat8_e4m3fn, x);
-    const Tensor scale = at::empty(x.sizes().slice(0, x.dim() - 1), x.options().dtype(at::kFloat).requires_grad(false));
+    const Tensor scale = fresh(x.sizes().slice(0, x.dim() - 1), at::kFloat, x);
     a.out_dtype = GDN_E4M3;
     a.y = q.data_ptr();
     a.scale = scale.data_ptr<float>();
@@ -281,14 +287,14 @@ PyObject *rms_norm_bwd(PyObject *const *p)
         a.dh = dr.ptr();
         a.ld_dh = dr.ld;
     }
-    const Tensor dx = at::empty(h.sizes(), h.options().requires_grad(false));
+    const Tensor dx = fresh(h.sizes(), h.scalar_type(), h);
     a.dx = dx.data_ptr();
     Tensor wv, dw;
     if (w) {
         wv = vec("weight", *w, width, h, true);
         a.weight = wv.data_ptr();
         a.w_dtype = code_of(wv);
-        dw = at::empty({width}, h.options().dtype(at::kFloat).requires_grad(false));
+        dw = fresh({width}, at::kFloat, h);
         a.dweight = dw.data_ptr<float>();
     }
     launch(gdn_rms_norm_bwd, gdn_rms_norm_bwd_workspace_size, a, h, "gdn_rms_norm_bwd");
@@ -405,11 +411,11 @@ void gradients(Operands &o, const Tensor &dy, const Tensor &x, const Tensor &w, 
     o.a.dy = dyr.ptr();
     o.a.ld_dy = dyr.ld;
     if (need_dx) {
-        dx = at::empty(x.sizes(), x.options().requires_grad(false));
+        dx = fresh(x.sizes(), x.scalar_type(), x);
         o.a.dx = dx.data_ptr();
     }
     if (need_dw) {
-        dw = at::empty(w.sizes(), x.options().requires_grad(false));
+        dw = fresh(w.sizes(), x.scalar_type(), x);
         o.a.dw = dw.data_ptr();
     }
 }
@@ -430,7 +436,7 @@ PyObject *linear_bwd(PyObject *const *p)
     if (b) {
         o.b = vec("bias", *b, o.N, x, false);
         o.a.bias = o.b.data_ptr<float>();
-        db = at::empty({o.N}, x.options().dtype(at::kFloat).requires_grad(false));
+        db = fresh({o.N}, at::kFloat, x);
         o.a.dbias = db.data_ptr<float>();
     }
     launch(gdn_linear_bwd, gdn_linear_bwd_workspace_size, o.a, x, "gdn_linear_bwd");
@@ -450,7 +456,7 @@ PyObject *gated_linear_bwd(PyObject *const *p)
     Tensor dx, dw, y;
     gradients(o, dy, x, w, truth(p[4]), truth(p[5]), dyr, dx, dw);
     if (truth(p[6])) {
-        y = at::empty(like_rows(x, o.N), x.options().requires_grad(false));
+        y = fresh(like_rows(x, o.N), x.scalar_type(), x);
         o.a.y = y.data_ptr();
         o.a.ldy = o.N;
     }
