@@ -974,7 +974,7 @@ cudaError_t pick(const GemmArgs &g, cudaStream_t st)
 
 // Few rows: the weights' reading is the cost, and the pair's tiles would be padding.  (A weight gradient's rows are
 // the weight's, and its contraction the batch.)
-bool use_small(const GemmArgs &g) { return !g.a_t && g.M <= 128; }
+bool use_small(const GemmArgs &g) { return !g.a_t && g.M <= kFewRows; }
 
 // fp32 rows as three planes of bf16: each the rounding of what the ones before leave (exactly x for normal values), the
 // first no larger than bf16's largest while x is finite; an infinity or NaN has zeros in the lower planes
@@ -983,39 +983,53 @@ __global__ void __launch_bounds__(256) split_kernel(const float *src, int64_t ld
 {
     grid_release();
     grid_wait();
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-        for (int64_t c = (int64_t)threadIdx.x * 2; c < cols; c += 512) {
-            float x[2] = {src[r * ld + c], c + 1 < cols ? src[r * ld + c + 1] : 0.f};
-            const bool finite[2] = {fabsf(x[0]) <= kF32Max, fabsf(x[1]) <= kF32Max};
+    constexpr int kPairs = 8;
+    const int64_t per_row = (cols + 64 * kPairs - 1) / (64 * kPairs), warps = (int64_t)gridDim.x * (blockDim.x / 32);
+    for (int64_t u = (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32; u < rows * per_row; u += warps) {
+        const int64_t r = u / per_row, c0 = (u - r * per_row) * (64 * kPairs) + (threadIdx.x & 31) * 2;
+        float x[kPairs][2];
+#pragma unroll
+        for (int k = 0; k < kPairs; ++k)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) x[k][j] = c0 + 64 * k + j < cols ? src[r * ld + c0 + 64 * k + j] : 0.f;
+#pragma unroll
+        for (int k = 0; k < kPairs; ++k) {
+            const int64_t c = c0 + 64 * k;
+            if (c >= cols) break;
+            const bool finite[2] = {fabsf(x[k][0]) <= kF32Max, fabsf(x[k][1]) <= kF32Max};
 #pragma unroll
             for (int i = 0; i < 3; ++i) {
                 float y[2];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) y[j] = finite[j] ? fminf(fmaxf(x[j], -kBf16Max), kBf16Max) : i ? 0.f : x[j];
+                for (int j = 0; j < 2; ++j) y[j] = finite[j] ? fminf(fmaxf(x[k][j], -kBf16Max), kBf16Max) : i ? 0.f : x[k][j];
                 const uint32_t w = pack_bf16(y[0], y[1]);
                 *(uint32_t *)(dst + i * plane + r * pitch + c) = w;
-                x[0] -= __uint_as_float(w << 16);
-                x[1] -= __uint_as_float(w & 0xffff0000u);
+                x[k][0] -= __uint_as_float(w << 16);
+                x[k][1] -= __uint_as_float(w & 0xffff0000u);
             }
         }
+    }
 }
 
-// rows into a layout of `pitch` elements (a multiple of 16 bytes): four bytes written at a time
+// Rows into another layout, element by element: a warp takes 32 x 16 consecutive elements of a row, all on their way at
+// once (a block that walked a row four bytes a thread waited once per step: 16384 x 1001 x 1001 with a residual, four such
+// copies, 108 us; 93 so).
 template <typename T>
-__global__ void __launch_bounds__(256) repack_kernel(const T *src, int64_t ld, int64_t rows, int64_t cols, T *dst, int64_t pitch)
+__global__ void __launch_bounds__(256) copy_rows_kernel(const T *src, int64_t ld, int64_t rows, int64_t cols, T *dst, int64_t ldd)
 {
-    constexpr int V = 4 / (int)sizeof(T);
+    constexpr int kEach = 16;
     grid_release();
     grid_wait();
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-        for (int64_t c = (int64_t)threadIdx.x * V; c < cols; c += 256 * V) {
-            T v[V];
+    const int64_t per_row = (cols + 32 * kEach - 1) / (32 * kEach), warps = (int64_t)gridDim.x * (blockDim.x / 32);
+    for (int64_t u = (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32; u < rows * per_row; u += warps) {
+        const int64_t r = u / per_row, c = (u - r * per_row) * (32 * kEach) + (threadIdx.x & 31);
+        T v[kEach];
 #pragma unroll
-            for (int j = 0; j < V; ++j) v[j] = c + j < cols ? src[r * ld + c + j] : T(0);
-            uint32_t w;
-            memcpy(&w, v, 4);
-            *(uint32_t *)(dst + r * pitch + c) = w;
-        }
+        for (int i = 0; i < kEach; ++i) v[i] = c + 32 * i < cols ? src[r * ld + c + 32 * i] : T(0);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+            if (c + 32 * i < cols) dst[r * ldd + c + 32 * i] = v[i];
+    }
 }
 
 }  // namespace
@@ -1041,18 +1055,26 @@ bool tma_ok(const void *p, int64_t ld, int64_t rows, size_t e)
     return ((uintptr_t)p & 15) == 0 && (rows <= 1 || (size_t)ld * e % 16 == 0);
 }
 
-cudaError_t launch_split(const float *src, int64_t ld, int64_t rows, int64_t cols, void *dst, int64_t pitch, int64_t plane, cudaStream_t st)
+// one warp to 512 elements of a row, as many as run at once
+unsigned blocks_of_rows(int64_t rows, int64_t cols)
 {
-    const unsigned grid = (unsigned)(rows < 8192 ? rows : 8192);
-    return launch_overlapped(split_kernel, grid, 1, 256, 0, 0, st, src, ld, rows, cols, (__nv_bfloat16 *)dst, pitch, plane);
+    const int64_t blocks = (rows * ((cols + 511) / 512) + 7) / 8, most = 8 * device_sm_count();
+    return (unsigned)(blocks < most ? blocks : most);
 }
 
-cudaError_t launch_repack(const void *src, gdn_dtype t, int64_t ld, int64_t rows, int64_t cols, void *dst, int64_t pitch, cudaStream_t st)
+cudaError_t launch_split(const float *src, int64_t ld, int64_t rows, int64_t cols, void *dst, int64_t pitch, int64_t plane, cudaStream_t st)
 {
-    const unsigned grid = (unsigned)(rows < 4096 ? rows : 4096);
+    return launch_overlapped(split_kernel, blocks_of_rows(rows, cols), 1, 256, 0, 0, st, src, ld, rows, cols, (__nv_bfloat16 *)dst, pitch, plane);
+}
+
+cudaError_t launch_copy_rows(const void *src, gdn_dtype t, int64_t ld, int64_t rows, int64_t cols, void *dst, int64_t ldd, cudaStream_t st)
+{
+    const unsigned grid = blocks_of_rows(rows, cols);
+    if (t == GDN_F32)
+        return launch_overlapped(copy_rows_kernel<uint32_t>, grid, 1, 256, 0, 0, st, (const uint32_t *)src, ld, rows, cols, (uint32_t *)dst, ldd);
     if (t == GDN_BF16)
-        return launch_overlapped(repack_kernel<uint16_t>, grid, 1, 256, 0, 0, st, (const uint16_t *)src, ld, rows, cols, (uint16_t *)dst, pitch);
-    return launch_overlapped(repack_kernel<uint8_t>, grid, 1, 256, 0, 0, st, (const uint8_t *)src, ld, rows, cols, (uint8_t *)dst, pitch);
+        return launch_overlapped(copy_rows_kernel<uint16_t>, grid, 1, 256, 0, 0, st, (const uint16_t *)src, ld, rows, cols, (uint16_t *)dst, ldd);
+    return launch_overlapped(copy_rows_kernel<uint8_t>, grid, 1, 256, 0, 0, st, (const uint8_t *)src, ld, rows, cols, (uint8_t *)dst, ldd);
 }
 
 int64_t gemm_colparts(const GemmArgs &g, Epi epi)

@@ -168,6 +168,8 @@ enum Epi : int {
     kEpiGatedBwd = 3,  // out[m, n] = extra up act'(gate), out[m, F + n] = extra act(gate); out2 = act(gate) up
 };
 
+constexpr int64_t kFewRows = 128;  // bf16 and e4m3 rows to this many take the kernel of few rows
+
 // One product with its epilogue.  A(m, k) is at a[m lda + k], or a[k lda + m] when a_t; B(n, k) at
 // b[n ldb + k], or b[k ldb + n] when b_t.  Gated modes: B has 2 N rows, gate rows first.
 struct GemmArgs {
@@ -196,7 +198,7 @@ bool tma_ok(const void *p, int64_t ld, int64_t rows, size_t esz);
 // fp32 rows into three planes of bf16 (`plane` elements apart, `pitch` elements per row)
 cudaError_t launch_split(const float *src, int64_t ld, int64_t rows, int64_t cols, void *dst, int64_t pitch, int64_t plane, cudaStream_t st);
 // copies rows into a layout of `pitch` elements per row
-cudaError_t launch_repack(const void *src, gdn_dtype t, int64_t ld, int64_t rows, int64_t cols, void *dst, int64_t pitch, cudaStream_t st);
+cudaError_t launch_copy_rows(const void *src, gdn_dtype t, int64_t ld, int64_t rows, int64_t cols, void *dst, int64_t ldd, cudaStream_t st);
 gdn_status read_tc_status(cudaStream_t st);  // synchronises; clears
 // the form for few rows (launch_gemm_tc chooses), its status word
 cudaError_t launch_gemm_small(const GemmArgs &g, Epi epi, cudaStream_t st);

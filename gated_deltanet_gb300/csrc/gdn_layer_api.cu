@@ -124,7 +124,27 @@ struct Operand {
         const void *src = p;
         p = base + off;
         return plane ? launch_split((const float *)src, stride, rows, cols, base + off, ld, plane, st)
-                     : launch_repack(src, t, stride, rows, cols, base + off, ld, st);
+                     : launch_copy_rows(src, t, stride, rows, cols, base + off, ld, st);
+    }
+};
+
+// A tensor that the epilogue of a product of many rows reads or writes: as it is, or, where its rows do not start on
+// 16-byte boundaries, by a copy in the workspace that has such rows (element by element the epilogue of 8071 x 571 x 955
+// with a residual took 81 us, with both copies it takes @LOOSE@).
+struct Rows16 {
+    int64_t ld, cols;
+    bool copy;
+    size_t off;
+    void plan(const void *ptr, int64_t stride, int64_t r, int64_t c, gdn_dtype t, bool many, Carve &ws)
+    {
+        ld = stride; cols = c;
+        off = 0;
+        copy = many && ptr && r > 0 && !tma_ok(ptr, stride, r, esize(t));
+        if (copy) {
+            const int64_t q = 16 / (int64_t)esize(t);
+            ld = (c + q - 1) / q * q;
+            off = ws.take((size_t)r * ld * esize(t));
+        }
     }
 };
 
@@ -163,10 +183,11 @@ gdn_status check_linear(const gdn_linear_args *a, bool gated, bool backward)
     return GDN_OK;
 }
 
-// A call's workspace: padded copies of operands; backward: dz (its rows padded to 16 bytes) and the column sums
-// of groups of rows
+// A call's workspace: padded copies of operands and of what the epilogues read and write; backward: dz (its rows padded
+// to 16 bytes) and the column sums of groups of rows
 struct LinearPlan {
     Operand x, w, dz;  // dz: dy itself without an activation
+    Rows16 extra, y, dx, dw;
     int64_t dz_cols, dz_ld, parts;
     size_t off_dz, off_part, bytes;
     bool own_dz, planes;
@@ -184,6 +205,25 @@ GemmArgs forward_product(const gdn_linear_args *a, const LinearPlan &p)
     return g;
 }
 
+// a product whose epilogue's tensors pass by their copies where there are such
+cudaError_t launch_by_rows(GemmArgs g, Epi epi, const Rows16 &extra, const Rows16 &out, char *base, cudaStream_t st)
+{
+    cudaError_t e = cudaSuccess;
+    if (extra.copy) {
+        e = launch_copy_rows(g.extra, g.out_dt, g.ld_extra, g.M, extra.cols, base + extra.off, extra.ld, st);
+        g.extra = base + extra.off;
+        g.ld_extra = extra.ld;
+    }
+    void *const dst = g.out;
+    const int64_t ld = g.ldo;
+    if (out.copy) {
+        g.out = base + out.off;
+        g.ldo = out.ld;
+    }
+    if (e == cudaSuccess) e = launch_product(g, epi, st);
+    return e == cudaSuccess && out.copy ? launch_copy_rows(g.out, g.out_dt, out.ld, g.M, out.cols, dst, ld, st) : e;
+}
+
 LinearPlan plan_linear(const gdn_linear_args *a, bool gated, bool backward)
 {
     LinearPlan p{};
@@ -192,7 +232,11 @@ LinearPlan plan_linear(const gdn_linear_args *a, bool gated, bool backward)
     p.planes = a->dtype == GDN_F32 && a->rows > kF32Rows;
     p.x.plan(a->x, a->ldx, a->rows, a->in_features, a->dtype, p.planes, c);
     p.w.plan(a->w, a->ldw, a->rows > 0 ? wrows : 0, a->in_features, a->dtype, p.planes, c);
-    if (backward) {
+    const bool many = p.planes || (a->dtype != GDN_F32 && a->rows > kFewRows);
+    if (!backward) {
+        p.extra.plan(gated ? nullptr : a->residual, a->ld_residual, a->rows, a->out_features, a->out_dtype, many, c);
+        p.y.plan(a->y, a->ldy, a->rows, a->out_features, a->out_dtype, many, c);
+    } else {
         const int64_t q = 16 / (int64_t)esize(a->dtype);
         p.dz_cols = wrows;
         p.own_dz = gated || a->act != GDN_ACT_NONE;
@@ -204,7 +248,10 @@ LinearPlan plan_linear(const gdn_linear_args *a, bool gated, bool backward)
             dz = nullptr;  // (in the workspace)
             p.dz_ld = (p.dz_cols + q - 1) / q * q;
             p.off_dz = c.take((size_t)a->rows * p.dz_ld * esize(a->dtype));
+            p.extra.plan(a->dy, a->ld_dy, a->rows, a->out_features, a->dtype, many, c);
         }
+        p.dx.plan(a->dx, a->in_features, a->rows, a->in_features, a->dtype, many, c);
+        p.dw.plan(a->rows > 0 ? a->dw : nullptr, a->in_features, wrows, a->in_features, a->dtype, p.planes || a->dtype != GDN_F32, c);
         p.dz.plan(dz, p.dz_ld, a->rows, p.dz_cols, a->dtype, p.planes && (a->dx || a->dw), c);
         p.off_part = c.take(a->dbias ? (size_t)p.parts * a->out_features * sizeof(float) : 0);
     }
@@ -237,7 +284,7 @@ gdn_status run_bwd(const gdn_linear_args *a, bool gated, void *ws, size_t ws_byt
         g.ldo2 = a->ldy;
         g.colpart = part;
         p.dz.p = g.out;
-        if (launch_product(g, gated ? kEpiGatedBwd : kEpiDact, st) != cudaSuccess) return GDN_ERR_CUDA;
+        if (launch_by_rows(g, gated ? kEpiGatedBwd : kEpiDact, p.extra, Rows16{}, base, st) != cudaSuccess) return GDN_ERR_CUDA;
     } else if (part && launch_colsum_rows(a->dy, a->dtype, M, N, a->ld_dy, part, st) != cudaSuccess) {
         return GDN_ERR_CUDA;
     }
@@ -253,7 +300,7 @@ gdn_status run_bwd(const gdn_linear_args *a, bool gated, void *ws, size_t ws_byt
         d.M = M; d.N = K; d.K = p.dz_cols;
         d.b = p.w.p; d.ldb = p.w.ld; d.b_plane = p.w.plane;
         d.out = a->dx; d.ldo = K;
-        if (launch_product(d, kEpiLinear, st) != cudaSuccess) return GDN_ERR_CUDA;
+        if (launch_by_rows(d, kEpiLinear, Rows16{}, p.dx, base, st) != cudaSuccess) return GDN_ERR_CUDA;
     }
     if (a->dw) {  // dw[n][k] = sum_m dz[m][n] x[m][k]
         GemmArgs d = g;
@@ -261,7 +308,7 @@ gdn_status run_bwd(const gdn_linear_args *a, bool gated, void *ws, size_t ws_byt
         d.a_t = 1;
         d.b = p.x.p; d.ldb = p.x.ld; d.b_plane = p.x.plane;
         d.out = a->dw; d.ldo = K;
-        if (launch_product(d, kEpiLinear, st) != cudaSuccess) return GDN_ERR_CUDA;
+        if (launch_by_rows(d, kEpiLinear, Rows16{}, p.dw, base, st) != cudaSuccess) return GDN_ERR_CUDA;
     }
     return GDN_OK;
 }
@@ -279,7 +326,7 @@ gdn_status run_fwd(const gdn_linear_args *a, bool gated, void *ws, size_t ws_byt
     GemmArgs g = forward_product(a, p);
     g.extra = a->residual; g.ld_extra = a->ld_residual;
     g.out = a->y; g.ldo = a->ldy;
-    return launch_product(g, gated ? kEpiGated : kEpiLinear, st) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    return launch_by_rows(g, gated ? kEpiGated : kEpiLinear, p.extra, p.y, base, st) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 size_t linear_workspace(const gdn_linear_args *a, bool gated, bool backward)
