@@ -231,8 +231,10 @@ template <> struct Line<float> {
     }
 };
 // `p`: column c of this lane's row, of the 32 rows from row0 on; columns from N on and rows from M on read as zero and
-// are not written.  Rows off 16 bytes pass through the warp's patch, so that half a warp reads or writes the 16 columns
-// of a row together (lane by lane, every element was a sector of its own: 8071 x 955 outputs with a residual took 117 us).
+// are not written.  A last group that ends before its 16 columns, and rows off 16 bytes (the second half of a gated
+// gradient's rows of odd width; other such tensors come by copies), pass through the warp's patch, so that half a warp
+// reads or writes the 16 columns of a row together (lane by lane, every element was a sector of its own: 117 us for
+// 8071 x 955 outputs with a residual against 81).
 constexpr int kPatch = 17;  // floats per row of the patch: lanes that read down a column meet no bank twice
 // (out of line: the fast path's loop has to stay small)
 __device__ __noinline__ void patch_turn(float *v, int lane, float *patch)  // 16 values per lane: by rows of 16 -> by lanes

@@ -129,8 +129,8 @@ struct Operand {
 };
 
 // A tensor that the epilogue of a product of many rows reads or writes: as it is, or, where its rows do not start on
-// 16-byte boundaries, by a copy in the workspace that has such rows (element by element the epilogue of 8071 x 571 x 955
-// with a residual took 81 us, with both copies it takes @LOOSE@).
+// 16-byte boundaries, by a copy in the workspace that has such rows (8071 x 955 x 571 with a residual: 84 us with an
+// epilogue that goes by elements, 43 with the copies).
 struct Rows16 {
     int64_t ld, cols;
     bool copy;

@@ -370,8 +370,9 @@ gdn_status gdn_chain_states(int ranks, int pairs, int K, int V, const float *sum
  *  - Matrices are row-major with consecutive elements in a row; inputs take a
  *    row stride in elements (at least the row's length), outputs are
  *    contiguous unless they have a stride.  Any length, any alignment to the
- *    element: operands whose rows do not start on 16-byte boundaries are
- *    copied once into the workspace in a padded layout.
+ *    element: matrices whose rows do not start on 16-byte boundaries pass by
+ *    padded copies in the workspace, and fp32 operands of more than 64 rows
+ *    by their bf16 planes (six bytes an element).
  *  - `workspace`: device memory of at least the size that the operator's
  *    _workspace_size call gives for the same arguments, 256-byte aligned, not
  *    used by another call that can run concurrently.  NULL: the
