@@ -350,6 +350,26 @@ def test_products_take_strided_and_unaligned_rows(gdn):
             ref.check(a, e, t)
 
 
+@pytest.mark.parametrize("first", [0, 1])
+def test_offsets_past_32_bits(gdn, first):
+    """Rows of a buffer whose elements lie more than 2^32 apart, on and off 16-byte boundaries."""
+    g = gen(31 + first)
+    room = torch.empty(9 << 29, dtype=BF, device="cuda")
+    ld = room.numel() // 300 // 8 * 8
+    x = room[first:].as_strided((299, 72), (ld, 1), first)
+    x.copy_(randn(g, 299, 72))
+    assert 298 * ld > 1 << 32
+    near, w = x.contiguous(), (randn(g, 144, 72) / 8).to(BF)
+    assert torch.equal(gdn.linear(x, w, None, "silu"), gdn.linear(near, w, None, "silu"))
+    assert torch.equal(gdn.gated_linear(x, w), gdn.gated_linear(near, w))
+    dy = randn(g, 299, 144, dtype=BF)
+    for a, b in zip(gdn.linear_bwd(dy, x, w, None, "silu"), gdn.linear_bwd(dy, near, w, None, "silu")):
+        assert a is b is None or torch.equal(a, b)
+    y, _ = gdn.rms_norm(x, None)
+    want = near.double() * torch.rsqrt(near.double().square().mean(1, keepdim=True) + 1e-6)
+    assert ((y.double() - want).abs() <= want.abs() * (2 ** -8 + 2 ** -18) + 2 ** -133).all()
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_no_rows(gdn, dtype):
     x, w, b = torch.zeros(0, 64, device="cuda", dtype=dtype), torch.ones(32, 64, device="cuda", dtype=dtype), torch.ones(32, device="cuda")
