@@ -7,7 +7,8 @@
 // that finish the rows of x in turn (row t: CTA t mod split), which add them in the order of the
 // contraction; sums are sent and not fetched, so that one meeting of the cluster is enough.  A CTA's shared
 // memory is one queue of 128-byte-wide weight boxes, and two CTAs share an SM: most of what they read is
-// requested at once.
+// requested at once.  Measured: 64 rows of 2048 by 11008 gated bf16 weights (45 MB) 12.6 us from HBM, 8.9 from L2;
+// one row by 2048 x 5504 6.6 us.
 #include <atomic>
 #include <cstring>
 

@@ -1,5 +1,5 @@
-// Products of bf16 and e4m3 operands on the tensor cores, with the epilogues of the decoder-block
-// operators.
+// Products of bf16, e4m3 and (as three bf16 planes) fp32 operands on the tensor cores, with the epilogues of the
+// decoder-block operators.
 //
 // A pair of CTAs (a cluster of two, one per SM) owns a 256 x BN tile of accumulators: each CTA holds
 // 128 rows of A and half of B's rows in its shared memory and one M = 256 tcgen05.mma reads both halves,
@@ -12,6 +12,9 @@
 //
 // Operands are loaded as 128-byte-swizzled boxes, either along k (K-major) or, for the products of the
 // backward passes, along m / n as they lie in memory (MN-major): nothing is transposed.
+//
+// Bound: the tensor pipe (16384 x 2048 x 2048 in bf16: 72.6 us, 1.89 PFLOP/s, the pipe 80 % active; gated 8191 x 2048 x
+// 5504: 89 %; 4096 x 2048 x 2048 in fp32: 158 us, 217 TFLOP/s); with short contractions (K = 256) the epilogue.
 #include <cstring>
 #include <atomic>
 #include <mutex>
