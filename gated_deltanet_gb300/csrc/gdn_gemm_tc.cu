@@ -234,8 +234,8 @@ template <> struct Line<float> {
     }
 };
 // `p`: column c of this lane's row, of the 32 rows from row0 on; columns from N on and rows from M on read as zero and
-// are not written.  A last group that ends before its 16 columns, and rows off 16 bytes (the second half of a gated
-// gradient's rows of odd width; other such tensors come by copies), pass through the warp's patch, so that half a warp
+// are not written.  A last group that ends before its 16 columns, and rows off 16 bytes (of small gated outputs,
+// and the second half of a gated gradient's rows of odd width; other such tensors come by copies), pass through the warp's patch, so that half a warp
 // reads or writes the 16 columns of a row together (lane by lane, every element was a sector of its own: 117 us for
 // 8071 x 955 outputs with a residual against 81).
 constexpr int kPatch = 17;  // floats per row of the patch: lanes that read down a column meet no bank twice

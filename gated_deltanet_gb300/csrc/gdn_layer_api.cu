@@ -235,7 +235,10 @@ LinearPlan plan_linear(const gdn_linear_args *a, bool gated, bool backward)
     const bool many = p.planes || (a->dtype != GDN_F32 && a->rows > kFewRows);
     if (!backward) {
         p.extra.plan(gated ? nullptr : a->residual, a->ld_residual, a->rows, a->out_features, a->out_dtype, many, c);
-        p.y.plan(a->y, a->ldy, a->rows, a->out_features, a->out_dtype, many, c);
+        // (a gated product reads nothing by elements beside it, so that the copy of its output repays its launch only past a
+        // round of tiles: 4000 x 255 x 576 9.3 us without and 10.5 with it, 3001 x 955 x 512 17.9 and 13.4)
+        const bool round = (a->rows + 255) / 256 * ((a->out_features + 127) / 128) > device_sm_count() / 2;
+        p.y.plan(a->y, a->ldy, a->rows, a->out_features, a->out_dtype, many && (!gated || round), c);
     } else {
         const int64_t q = 16 / (int64_t)esize(a->dtype);
         p.dz_cols = wrows;
