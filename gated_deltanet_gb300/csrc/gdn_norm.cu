@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(kRowThreads) norm_bwd_kernel(NormBwdArgs a, in
     }
 }
 
-// Wide rows: dx (and 1 / n of every row), then dw by columns
+// Wide rows: dx and (where dw needs it) 1 / n of every row, either alone where its pointer is null; dw by columns
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads) norm_bwd_wide_kernel(NormBwdArgs a)
 {
@@ -493,7 +493,8 @@ __global__ void __launch_bounds__(kRowThreads) norm_bwd_wide_kernel(NormBwdArgs 
         const float2 s = row_reduce<kSum>(ss, sd, blockDim.x, red[it & 1]);
         const float rn = 1.f / sqrtf(s.x / (float)a.D + a.eps);
         const float k = s.y / (float)a.D * rn * rn;
-        if (threadIdx.x == 0 && a.rstd) a.rstd[row] = rn;  // (only dw needs it)
+        if (threadIdx.x == 0 && a.rstd) a.rstd[row] = rn;
+        if (!a.dx) continue;
         for (int c = threadIdx.x; c < a.D; c += blockDim.x) {
             const float h = to_f(gh[row * a.ld_h + c]);
             float dx = (weight_at(a.w, a.w_dt, c) * to_f(gy[row * a.ld_dy + c]) - h * k) * rn;
@@ -611,6 +612,16 @@ bool bwd_vec(const NormBwdArgs &a, int esz)
 
 constexpr int kWideParts = 64;
 
+// Whether dx lies over rows that the sums of dw read too
+bool dx_over_inputs(const NormBwdArgs &a, size_t esz)
+{
+    const auto over = [&](const void *p, int64_t ld) {
+        const uintptr_t d = (uintptr_t)a.dx, q = (uintptr_t)p;
+        return d < q + ((a.M - 1) * ld + a.D) * esz && q < d + (size_t)a.M * a.D * esz;
+    };
+    return over(a.dy, a.ld_dy) || over(a.h, a.ld_h);
+}
+
 template <typename T>
 cudaError_t norm_bwd_go(const NormBwdArgs &a, int sms, cudaStream_t st)
 {
@@ -618,11 +629,24 @@ cudaError_t norm_bwd_go(const NormBwdArgs &a, int sms, cudaStream_t st)
     int64_t parts;
     cudaError_t e = cudaSuccess;
     if (norm_bwd_wide(a.D)) {
+        // dw reads dy and h once more, with 1 / n of the rows: after the pass that has it and writes dx, but before dx where
+        // dx takes the place of dy (by one more pass over the rows for 1 / n alone)
         const int64_t most = (int64_t)sms * 4;
-        e = launch_overlapped(norm_bwd_wide_kernel<T>, (unsigned)(a.M < most ? a.M : most), 1, kRowThreads, 0, 0, st, a);
+        const bool first = a.dw && dx_over_inputs(a, sizeof(T));
+        NormBwdArgs rows = a;
+        if (first) rows.dx = nullptr;
+        const auto walk = [&] {
+            return launch_overlapped(norm_bwd_wide_kernel<T>, (unsigned)(a.M < most ? a.M : most), 1, kRowThreads, 0, 0, st, rows);
+        };
+        e = walk();
         parts = a.M < kWideParts ? a.M : kWideParts;
         if (a.dw && e == cudaSuccess)
             e = launch_overlapped(norm_dw_wide_kernel<T>, (unsigned)((a.D + 255) / 256), (unsigned)parts, 256, 0, 0, st, a);
+        if (first && e == cudaSuccess) {
+            rows.dx = a.dx;
+            rows.rstd = nullptr;
+            e = walk();
+        }
     } else {
         const RowPlan p = plan_rows(a.M, a.D, sizeof(T), bwd_vec(a, sizeof(T)), true, sms);
         const unsigned grid = (unsigned)norm_blocks(a.M, p, sms);
