@@ -414,7 +414,8 @@ __global__ void __launch_bounds__(kRowThreads) norm_bwd_kernel(NormBwdArgs a, in
         const int64_t cur = row;
         if constexpr (!kTwice) in.next(row, it);
         const float2 s = row_reduce<kSum>(ss, sd, tpr, red[it & 1]);
-        const float rn = 1.f / sqrtf(s.x / (float)a.D + a.eps);
+        // (threads without a row have zeros, which with eps = 0 would give an infinite 1 / n and NaN in dw)
+        const float rn = kTwice || live ? 1.f / sqrtf(s.x / (float)a.D + a.eps) : 0.f;
         const float c = s.y / (float)a.D * rn * rn * rn;  // dx = dh + w dy / n - h c
         T *const dxp = (T *)a.dx + cur * a.D + t;         // (single elements)
 #pragma unroll

@@ -73,3 +73,16 @@ def test_norm_stream_in_the_place_of_x(gdn, lib, D):
                                                ld_residual=D, y=y, h=x))
     assert lib.gdn_rms_norm(a, here()) == 0
     assert torch.equal(y, want[0]) and torch.equal(x, want[1])
+
+
+@pytest.mark.parametrize("M,D", [(1, 5), (3, 101), (3, 104), (9, 33), (5, 512), (130, 257), (2, 513), (3, 9000)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_norm_bwd_without_eps(gdn, M, D, dtype):
+    """eps = 0 with rows that are not zero is an ordinary call, also where the rows do not fill a block."""
+    g = gen(M + D)
+    h, dy, w = randn(g, M, D, dtype=dtype), randn(g, M, D, dtype=dtype), 1 + 0.3 * randn(g, D)
+    dx, dw = gdn.rms_norm_bwd(dy, h, w, None, 0.0)
+    ex, ew = ref.norm_bwd(dy, h, w, None, 0.0)
+    bx, bw = ref.norm_bwd_bound(dy, h, w, None, 0.0, ex, dtype)
+    ref.check(dx, ex, bx, "dx")
+    ref.check(dw, ew, bw, "dw")
