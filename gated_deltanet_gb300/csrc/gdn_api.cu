@@ -408,28 +408,62 @@ gdn_status run(const gdn_shape *s, const void *q, const void *k, const void *v, 
 struct WsEntry {
     void *ptr = nullptr;
     size_t bytes = 0;
+    bool recorded = false;  // a call in a capturing stream was given this buffer: a graph holds its address
 };
 std::mutex g_mu;
 std::map<std::pair<int, cudaStream_t>, WsEntry> g_ws;
 
+bool is_capturing(cudaStream_t stream)
+{
+    cudaStreamCaptureStatus cs;
+    if (cudaStreamIsCapturing(stream, &cs) == cudaSuccess) return cs != cudaStreamCaptureStatusNone;
+    cudaGetLastError();
+    return false;
+}
+
+// Device memory that belongs to no graph, its status word zero, while the stream of the call is being captured
+// (an allocation of that stream would be the graph's own, gone between its launches)
+cudaError_t malloc_beside_capture(void **ptr, size_t bytes)
+{
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    cudaError_t e = cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e != cudaSuccess) return e;
+    cudaStream_t own = nullptr;
+    if ((e = cudaMalloc(ptr, bytes)) == cudaSuccess) {
+        if ((e = cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking)) == cudaSuccess) {
+            e = cudaMemsetAsync(*ptr, 0, kStatusBytes, own);
+            const cudaError_t done = cudaStreamSynchronize(own);
+            if (e == cudaSuccess) e = done;
+            cudaStreamDestroy(own);
+        }
+        if (e != cudaSuccess) cudaFree(*ptr);
+    }
+    if (e != cudaSuccess) *ptr = nullptr;
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    return e;
+}
+
+// A buffer that a captured call was given is never freed (the graph may be replayed whenever its owner likes); it is
+// left behind where the entry grows.
 gdn_status managed_ws(size_t need, cudaStream_t stream, void **out, size_t *out_bytes)
 {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return GDN_ERR_CUDA;
+    const bool capturing = is_capturing(stream);
     std::lock_guard<std::mutex> lock(g_mu);
     WsEntry &w = g_ws[{dev, stream}];
     if (w.bytes < need) {
-        if (w.ptr) cudaFreeAsync(w.ptr, stream);
-        w.ptr = nullptr;
-        w.bytes = 0;
+        if (w.ptr && !w.recorded && !capturing) cudaFreeAsync(w.ptr, stream);
+        w = WsEntry{};
         size_t bytes = align_up(std::max<size_t>(need, 1 << 20), 1 << 20);
-        if (cudaMallocAsync(&w.ptr, bytes, stream) != cudaSuccess) {
+        if ((capturing ? malloc_beside_capture(&w.ptr, bytes) : cudaMallocAsync(&w.ptr, bytes, stream)) != cudaSuccess) {
             cudaGetLastError();
             return GDN_ERR_NOMEM;
         }
-        if (cudaMemsetAsync(w.ptr, 0, kStatusBytes, stream) != cudaSuccess) return GDN_ERR_CUDA;
+        if (!capturing && cudaMemsetAsync(w.ptr, 0, kStatusBytes, stream) != cudaSuccess) return GDN_ERR_CUDA;
         w.bytes = bytes;
     }
+    w.recorded |= capturing;
     *out = w.ptr;
     *out_bytes = w.bytes;
     return GDN_OK;

@@ -199,7 +199,10 @@ gdn_status gdn_chunk_fwd_ws(const gdn_shape *s,
  * chunk_kda_fwd for the per-channel gate) -- the plain entry point -- with
  * default options and a library-managed workspace,
  * cached per (device, stream) and grown stream-ordered (cudaMallocAsync on
- * `stream`) when a call needs more.  Arguments as in gdn_chunk_fwd_ws.
+ * `stream`) when a call needs more; while `stream` is being captured, by
+ * memory beside the graph (cudaMalloc).  A workspace that a captured call
+ * used is never freed: the graph may be replayed at any time that no other
+ * call uses it.  Arguments as in gdn_chunk_fwd_ws.
  */
 gdn_status gdn_chunk_fwd(const gdn_shape *s,
                          const void *q, const void *k, const void *v,
@@ -377,8 +380,12 @@ gdn_status gdn_chain_states(int ranks, int pairs, int K, int V, const float *sum
  *    _workspace_size call gives for the same arguments, 256-byte aligned, not
  *    used by another call that can run concurrently.  NULL: the
  *    library-managed workspace of (device, stream), which is not allowed to
- *    grow while the stream is being captured (GDN_ERR_NOMEM then).  A size of
- *    0 needs none.
+ *    grow while the stream is being captured (GDN_ERR_NOMEM then).  A buffer
+ *    that a captured call used is never freed, also where the workspace grows
+ *    later; replays of the graph use it, so that they must not run
+ *    concurrently with other calls on the library-managed workspace of the
+ *    captured stream, nor with other graphs captured there (a workspace of
+ *    the graph's own avoids that).  A size of 0 needs none.
  *  - A device-side wait that ran out (2 s) is recorded per device; the next
  *    gdn_read_layer_status reads and clears it.
  *  - Zero rows are allowed: outputs without rows are left alone, the

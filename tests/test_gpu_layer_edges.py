@@ -86,3 +86,115 @@ def test_norm_bwd_without_eps(gdn, M, D, dtype):
     bx, bw = ref.norm_bwd_bound(dy, h, w, None, 0.0, ex, dtype)
     ref.check(dx, ex, bx, "dx")
     ref.check(dw, ew, bw, "dw")
+
+
+# ---------------------------------------------------------------- the library-managed workspace
+def product_args(x, w, **kw):
+    code = layer_c.code(x)
+    return layer_c.GdnLinearArgs(**layer_c.pointers(rows=x.shape[0], out_features=w.shape[0], in_features=x.shape[1], dtype=code, out_dtype=code,
+                                                    x=x, ldx=x.shape[1], w=w, ldw=w.shape[1], **kw))
+
+
+def gradient_call(lib, g, M, N, K):
+    """A gelu layer's gradients by the C entry without a workspace, what they write, and the same by the Python call."""
+    x, w, dy = randn(g, M, K, dtype=BF), (randn(g, N, K) / K ** 0.5).to(BF), randn(g, M, N, dtype=BF)
+    out = torch.zeros_like(x), torch.zeros_like(w)
+    a = product_args(x, w, act=2, dy=dy, ld_dy=N, dx=out[0], dw=out[1])
+    assert lib.gdn_linear_bwd_workspace_size(a) > 0
+    return (lambda: lib.gdn_linear_bwd(a, None, 0, here())), out, (dy, x, w, None, "gelu"), a
+
+
+def test_no_workspace_given(gdn, lib):
+    """workspace NULL: every entry that needs one, on a stream that had none."""
+    g = gen(41)
+    x, w, dy = randn(g, 70, 129, dtype=BF), (randn(g, 64, 129) / 11).to(BF), randn(g, 70, 64, dtype=BF)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        y, h = torch.empty(70, 64, dtype=BF, device="cuda"), torch.empty(70, 32, dtype=BF, device="cuda")
+        assert lib.gdn_linear(product_args(x, w, y=y, ldy=64), None, 0, here()) == 0
+        a = product_args(x, w, act=1, y=h, ldy=32)
+        a.out_features = 32
+        assert lib.gdn_gated_linear(a, None, 0, here()) == 0
+        dx, dw = torch.empty_like(x), torch.empty_like(w)
+        assert lib.gdn_linear_bwd(product_args(x, w, act=1, dy=dy, ld_dy=64, dx=dx, dw=dw), None, 0, here()) == 0
+        gx, gw = torch.empty_like(x), torch.empty_like(w)
+        a = product_args(x, w, act=1, dy=dy, ld_dy=64, dx=gx, dw=gw)
+        a.out_features = 32
+        assert lib.gdn_gated_linear_bwd(a, None, 0, here()) == 0
+        nx, nw = torch.empty_like(dy), torch.empty(64, device="cuda")
+        assert lib.gdn_rms_norm_bwd(layer_c.norm_bwd_args(dy, y, torch.ones(64, device="cuda"), None, nx, nw, 1e-5), None, 0, here()) == 0
+    torch.cuda.current_stream().wait_stream(stream)
+    assert torch.equal(y, gdn.linear(x, w)) and torch.equal(h, gdn.gated_linear(x, w))
+    for got, want in (((dx, dw), gdn.linear_bwd(dy, x, w, None, "silu")), ((gx, gw), gdn.gated_linear_bwd(dy[:, :32], x, w)),
+                      ((nx, nw), gdn.rms_norm_bwd(dy, y, torch.ones(64, device="cuda"), None, 1e-5))):
+        assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+def test_graphs_keep_the_library_managed_workspace(gdn, lib):
+    """A captured call's buffer outlives the workspace's growth; growth under capture is refused and enqueues nothing."""
+    g = gen(43)
+    small, out, args, _ = gradient_call(lib, g, 200, 64, 72)
+    large, out2, args2, a2 = gradient_call(lib, g, 3000, 640, 72)
+    assert lib.gdn_linear_bwd_workspace_size(a2) > 2 << 20
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        assert small() == 0
+        stream.synchronize()
+        with torch.cuda.graph(graph, stream=stream):
+            assert small() == 0
+            assert large() == -5
+        assert large() == 0  # the workspace grows
+        for t in out:
+            t.zero_()
+        graph.replay()
+        graph.replay()
+    stream.synchronize()
+    for have, a in ((out, args), (out2, args2)):
+        want = gdn.linear_bwd(*a)
+        assert torch.equal(have[0], want[0]) and torch.equal(have[1], want[1])
+
+
+def test_token_mixer_in_graphs(gdn):
+    """The delta rule and its gradients captured on a stream that had no workspace: replays give what eager calls give, before and after
+    larger calls on that stream and a second graph's capture there."""
+    g = gen(47)
+
+    def inputs(T):
+        q, k, v = (randn(g, 1, T, 2, 128, dtype=BF) for _ in range(3))
+        k = torch.nn.functional.normalize(k.float(), dim=-1).to(BF)
+        gate, beta = -torch.rand(1, T, 2, generator=g, device="cuda") / 10, torch.rand(1, T, 2, generator=g, device="cuda")
+        return q, k, v, gate, beta
+
+    def step(x, do):
+        o, ht = gdn.chunk_gated_delta_rule(*x, output_final_state=True)
+        return o, ht, gdn.chunk_gated_delta_rule_bwd(*x, do)
+
+    x, big = inputs(200), inputs(1500)
+    do, do2 = torch.ones_like(x[2]), torch.ones_like(big[2])
+    want, want2 = step(x, do), step(big, do2)
+    stream, graph, second = torch.cuda.Stream(), torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=stream):
+        got = step(x, do)
+    with torch.cuda.stream(stream):
+        graph.replay()
+        got2 = step(big, do2)
+        graph.replay()
+    stream.synchronize()
+    with torch.cuda.graph(second, stream=stream):
+        again = step(x, do)
+    with torch.cuda.stream(stream):
+        second.replay()
+        graph.replay()
+        assert gdn.read_device_status() == 0
+    stream.synchronize()
+
+    def near(a, b):
+        # (the gradients' sums over tiles are atomic: their order may change)
+        for s, t in zip([*a[:2], *a[2]], [*b[:2], *b[2]]):
+            assert (s is None and t is None) or ((s.float() - t.float()).norm() <= 1e-5 * t.float().norm()).item()
+    near(got, want)
+    near(again, want)
+    near(got2, want2)
