@@ -168,6 +168,12 @@ enum Epi : int {
     kEpiGatedBwd = 3,  // out[m, n] = extra up act'(gate), out[m, F + n] = extra act(gate); out2 = act(gate) up
 };
 
+// How long a device-side wait of the products may last.  The calling thread's switch for testing what happens then
+// (gdn_layer_test_withhold): launches of kernel instances of their own, whose load warps load nothing and whose waits have a
+// limit of 5 ms.  (As run-time arguments of every instance the switch and the limit cost a token's product 0.16 of 7.9 us.)
+constexpr uint64_t kWaitLimitNs = 2000000000ull, kTestWaitLimitNs = 5000000ull;
+bool &withhold_loads();
+
 constexpr int64_t kFewRows = 128;  // bf16 and e4m3 rows to this many take the kernel of few rows
 
 // One product with its epilogue.  A(m, k) is at a[m lda + k], or a[k lda + m] when a_t; B(n, k) at
@@ -199,8 +205,8 @@ bool tma_ok(const void *p, int64_t ld, int64_t rows, size_t esz);
 cudaError_t launch_split(const float *src, int64_t ld, int64_t rows, int64_t cols, void *dst, int64_t pitch, int64_t plane, cudaStream_t st);
 // copies rows into a layout of `pitch` elements per row
 cudaError_t launch_copy_rows(const void *src, gdn_dtype t, int64_t ld, int64_t rows, int64_t cols, void *dst, int64_t ldd, cudaStream_t st);
-gdn_status read_tc_status(cudaStream_t st);  // synchronises; clears
-// the form for few rows (launch_gemm_tc chooses), its status word
+gdn_status read_tc_status(cudaStream_t st);  // its status word: synchronises; clears
+// the form for few rows (launch_gemm_tc chooses), and its status word
 cudaError_t launch_gemm_small(const GemmArgs &g, Epi epi, cudaStream_t st);
 gdn_status read_small_status(cudaStream_t st);
 // rows of partial column sums that a kEpiDact product writes

@@ -339,6 +339,12 @@ size_t linear_workspace(const gdn_linear_args *a, bool gated, bool backward)
 
 }  // namespace
 
+bool &gdn::withhold_loads()
+{
+    static thread_local bool on = false;
+    return on;
+}
+
 extern "C" {
 
 gdn_status gdn_rms_norm(const gdn_norm_args *a, gdn_stream_t stream) { return run_norm(a, true, (cudaStream_t)stream); }
@@ -429,7 +435,10 @@ gdn_status gdn_gated_linear_bwd(const gdn_linear_args *a, void *workspace, size_
 
 gdn_status gdn_read_layer_status(gdn_stream_t stream)
 {
-    return read_tc_status((cudaStream_t)stream);
+    const gdn_status many = read_tc_status((cudaStream_t)stream), few = read_small_status((cudaStream_t)stream);
+    return many != GDN_OK ? many : few;
 }
+
+void gdn_layer_test_withhold(int on) { withhold_loads() = on != 0; }
 
 }  // extern "C"

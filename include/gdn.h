@@ -518,6 +518,14 @@ gdn_status gdn_gated_linear_bwd(const gdn_linear_args *a, void *workspace, size_
  * GDN_ERR_TIMEOUT) and clear it. */
 gdn_status gdn_read_layer_status(gdn_stream_t stream);
 
+/* Testing the timeout path only: while `on` is not 0, gdn_linear calls of the
+ * calling thread launch instances of its kernels that load no operands, so
+ * that the waits for them run out after 5 ms, gdn_read_layer_status reports
+ * GDN_ERR_TIMEOUT and the outputs are undefined.  There are such instances
+ * for bf16 to bf16 and fp32 products in tiles of 128 columns and for bf16
+ * ones of up to 16 rows; other products run as ever. */
+void gdn_layer_test_withhold(int on);
+
 /* Plan summary (host only, no GPU needed) -- what a call would launch: the
  * engine and the in-GPU split (FlashQLA blog, "A balanced solution", the CP
  * enable rule, re-derived for this GPU's SM count). */

@@ -18,6 +18,7 @@ def library():
         f, w = getattr(lib, n), getattr(lib, n + "_workspace_size")
         f.argtypes, f.restype = [t, VP, ctypes.c_size_t, VP], INT
         w.argtypes, w.restype = [t], ctypes.c_size_t
+    lib.gdn_layer_test_withhold.argtypes, lib.gdn_layer_test_withhold.restype = [INT], None
     return lib
 
 

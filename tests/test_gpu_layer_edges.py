@@ -198,3 +198,43 @@ def test_token_mixer_in_graphs(gdn):
     near(got, want)
     near(again, want)
     near(got2, want2)
+
+
+# ---------------------------------------------------------------- waits that run out
+@pytest.fixture
+def withheld(lib):
+    """Calls whose kernels load nothing: their waits run out after 5 ms."""
+    def call(f):
+        lib.gdn_layer_test_withhold(1)
+        try:
+            f()
+        finally:
+            lib.gdn_layer_test_withhold(0)
+        torch.cuda.synchronize()
+    return call
+
+
+# rows, outputs, contraction: few rows with a contraction in one piece and split; many rows in one tile with its contraction split,
+# in one tile without, in several tiles
+@pytest.mark.parametrize("M,N,K", [(3, 40, 64), (16, 200, 2048), (200, 130, 2048), (200, 64, 72), (2000, 640, 200)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_waits_that_run_out(gdn, withheld, M, N, K, dtype):
+    """A timeout is reported once, and the next call on the stream is right."""
+    if dtype == F32 and M <= 64:
+        pytest.skip("nothing waits there")
+    g = gen(M)
+    x, w = randn(g, M, K, dtype=dtype), randn(g, N, K, dtype=dtype)
+    want = gdn.linear(x, w)
+    assert gdn.read_layer_status() == 0
+    withheld(lambda: gdn.linear(x, w))
+    assert gdn.read_layer_status() == -4 and gdn.read_layer_status() == 0
+    assert torch.equal(gdn.linear(x, w), want)
+
+
+def test_one_read_clears_every_kernel_s_status(gdn, withheld):
+    """Timeouts in products of many and of few rows: one read reports and clears both."""
+    w = randn(gen(4), 64, 72, dtype=BF)
+    for order in ((5, 300), (300, 5)):
+        for M in order:
+            withheld(lambda: gdn.linear(randn(gen(M), M, 72, dtype=BF), w))
+        assert gdn.read_layer_status() == -4 and gdn.read_layer_status() == 0
