@@ -136,8 +136,10 @@ __device__ __forceinline__ void act_both(const float *z, float *v, float *d)
                 v[i] = z[i] < 0.f ? 0.f : z[i];
                 d[i] = z[i] > 0.f ? 1.f : 0.f;
             } else if (ACT == GDN_ACT_SIGMOID) {
-                v[i] = logistic<PRECISE>(z[i]);
-                d[i] = v[i] * (1.f - v[i]);
+                // p (1 - p): for z > 0 the difference as exp(-z) p (1 - p itself has lost its digits from z of about 10 on)
+                const float e = PRECISE ? expf(-z[i]) : fast_exp2(-kLog2e * z[i]), p = PRECISE ? 1.f / (1.f + e) : fast_rcp(1.f + e);
+                v[i] = p;
+                d[i] = p * (z[i] > 0.f ? e * p : 1.f - p);
             } else {
                 v[i] = z[i];
                 d[i] = 1.f;

@@ -238,3 +238,28 @@ def test_one_read_clears_every_kernel_s_status(gdn, withheld):
         for M in order:
             withheld(lambda: gdn.linear(randn(gen(M), M, 72, dtype=BF), w))
         assert gdn.read_layer_status() == -4 and gdn.read_layer_status() == 0
+
+
+# ---------------------------------------------------------------- activations far out
+def one_column(z):
+    """x and weight whose product is z itself (one term, a factor of one)."""
+    return z[:, None].contiguous(), torch.ones(1, 1, dtype=z.dtype, device="cuda")
+
+
+@pytest.mark.parametrize("rows", [60, 120, 300])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_sigmoid_slope_keeps_its_digits(gdn, rows, dtype):
+    """The slope of the logistic function falls like exp(-|z|) on both sides and is relative in its error on both.  fp32:
+    the exponential (2 units of 2^-23), 1 + e, the reciprocal, two products: below 2^-20.  bf16: the exponent's rounding, |z| 2^-23, and the
+    approximate exponential and reciprocal beside the rounding of dz."""
+    z = torch.linspace(-70, 70, rows, device="cuda").to(dtype)
+    x, w = one_column(z)
+    dx = gdn.linear_bwd(torch.ones_like(x), x, w, None, "sigmoid")[0][:, 0]
+    want = torch.special.expit(z.double()) * torch.special.expit(-z.double())
+    rel = 2.0 ** -20 if dtype == F32 else ref.HALF[BF] + 2.0 ** -19 + z.double().abs() * 2.0 ** -22
+    ref.check(dx, want, rel * want)
+    both = gdn.gated_linear_bwd(torch.ones_like(x), x, torch.ones(2, 1, dtype=dtype, device="cuda"), "sigmoid")[0][:, 0]
+    p = torch.special.expit(z.double())
+    # z sigmoid'(z) + sigmoid(z): each of the two terms rounded by itself
+    parts = (z.double() * want).abs() + p
+    ref.check(both, z.double() * want + p, (2 * rel + ref.HALF[dtype]) * parts)
