@@ -42,7 +42,6 @@ constexpr int kABytes = 128 * 128;       // a CTA's rows of A, 128 bytes of k (o
 enum Kind : int { kBf16 = 0, kE4m3 = 1, kF32 = 2 };
 constexpr int kChain = 2;
 constexpr int kMaxSplit = 4;
-constexpr float kF32Max = 3.40282347e38f, kBf16Max = 3.38953139e38f;
 
 // Shared memory of a CTA: operands, each epilogue warp's column vectors (scales and bias of its half of a tile; the
 // tensors of the epilogue go between registers and global memory) and its 32 x 16 patch for rows off 16 bytes.  BN = 128: two

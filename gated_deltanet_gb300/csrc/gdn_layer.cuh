@@ -14,6 +14,7 @@ namespace gdn {
 // result is rounded to bf16 (relative step 2^-8) and the fast ones (relative error below 2^-20 for the
 // arguments where the result is not itself lost in that rounding) are enough.
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kF32Max = 3.40282347e38f, kBf16Max = 3.38953139e38f;
 __device__ __forceinline__ float fast_exp2(float x)
 {
     float r;
@@ -131,7 +132,8 @@ __device__ __forceinline__ void act_both(const float *z, float *v, float *d)
             } else if (ACT == GDN_ACT_GELU_TANH) {
                 const float z2 = z[i] * z[i], p = logistic<PRECISE>(z[i] * (kGeluA + kGeluB * z2));
                 v[i] = z[i] * p;
-                d[i] = p + v[i] * (1.f - p) * (kGeluA + 3.f * kGeluB * z2);
+                // (z^2 may pass fp32's range, where p is 0 or 1 and the product with it has to stay 0)
+                d[i] = p + v[i] * (1.f - p) * fminf(kGeluA + 3.f * kGeluB * z2, kF32Max);
             } else if (ACT == GDN_ACT_RELU) {
                 v[i] = z[i] < 0.f ? 0.f : z[i];
                 d[i] = z[i] > 0.f ? 1.f : 0.f;

@@ -263,3 +263,14 @@ def test_sigmoid_slope_keeps_its_digits(gdn, rows, dtype):
     # z sigmoid'(z) + sigmoid(z): each of the two terms rounded by itself
     parts = (z.double() * want).abs() + p
     ref.check(both, z.double() * want + p, (2 * rel + ref.HALF[dtype]) * parts)
+
+
+@pytest.mark.parametrize("rows", [8, 72, 264])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("name", ["silu", "gelu", "gelu_tanh", "relu", "sigmoid"])
+def test_slopes_far_out(gdn, rows, dtype, name):
+    """Arguments whose squares pass fp32's range: the slopes have their limits, 1 or 0."""
+    z = torch.tensor([1e18, 3e19, 1e25, 3e38, -1e18, -3e19, -1e25, -3e38], device="cuda").repeat(rows // 8).to(dtype)
+    x, w = one_column(z)
+    dx = gdn.linear_bwd(torch.ones_like(x), x, w, None, name)[0][:, 0]
+    assert torch.equal(dx, torch.zeros_like(z) if name == "sigmoid" else (z > 0).to(dtype))
