@@ -29,6 +29,9 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return r;
 }
 
+// The scale of a row from max|w h| and 1 / n; NaN for a row that holds an infinity (inf - inf) or a NaN
+__device__ __forceinline__ float row_scale(float most, float rn) { return max_nan(most * rn / kE4m3Max, kScaleMin) + (most - most); }
+
 // VEC elements (16 bytes, or one element) as they are in memory
 template <typename T, int VEC> struct Raw;
 template <> struct Raw<__nv_bfloat16, 8> {
@@ -278,7 +281,7 @@ __global__ void __launch_bounds__(kRowThreads) norm_kernel(NormArgs a, int tpr)
         const float rn = a.normalise ? 1.f / sqrtf(s.x / (float)a.D + a.eps) : 1.f;
         float inv = 1.f;
         if (sizeof(TO) == 1) {
-            const float sc = max_nan(s.y * rn / kE4m3Max, kScaleMin);
+            const float sc = row_scale(s.y, rn);
             inv = 1.f / sc;
             if (t == 0 && cur < a.M) a.scale[cur] = sc;
         }
@@ -339,7 +342,7 @@ __global__ void __launch_bounds__(kRowThreads) norm_wide_kernel(NormArgs a)
         const float rn = a.normalise ? 1.f / sqrtf(s.x / (float)a.D + a.eps) : 1.f;
         float inv = 1.f;
         if (sizeof(TO) == 1) {
-            const float sc = max_nan(s.y * rn / kE4m3Max, kScaleMin);
+            const float sc = row_scale(s.y, rn);
             inv = 1.f / sc;
             if (threadIdx.x == 0) a.scale[row] = sc;
         }

@@ -426,7 +426,7 @@ typedef struct {
 gdn_status gdn_rms_norm(const gdn_norm_args *a, gdn_stream_t stream);
 
 /* One scale per row and e4m3 values of x as it stands: gdn_rms_norm without
- * the norm, residual and weight (x, y, scale of `a`). */
+ * the norm, residual and weight (x, y, scale of `a`; NaN scales as there). */
 gdn_status gdn_quantize_rows(const gdn_norm_args *a, gdn_stream_t stream);
 
 /*

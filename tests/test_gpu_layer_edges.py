@@ -274,3 +274,14 @@ def test_slopes_far_out(gdn, rows, dtype, name):
     x, w = one_column(z)
     dx = gdn.linear_bwd(torch.ones_like(x), x, w, None, name)[0][:, 0]
     assert torch.equal(dx, torch.zeros_like(z) if name == "sigmoid" else (z > 0).to(dtype))
+
+
+@pytest.mark.parametrize("D", [64, 129, 9000])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_quantised_infinities(gdn, D, dtype):
+    """A row that holds an infinity or a NaN has a NaN for its scale, with the norm and without."""
+    x = randn(gen(D), 5, D, dtype=dtype)
+    x[1, 3], x[2, D - 1], x[3, 0] = float("inf"), -float("inf"), float("nan")
+    for q, s in (gdn.quantize_rows(x), gdn.rms_norm_quant(x, None)[:2]):
+        assert s[1:4].isnan().all() and s[[0, 4]].isfinite().all()
+        assert q[[0, 4]].float().isfinite().all()
