@@ -296,11 +296,12 @@ __global__ void __launch_bounds__(128) colsum_rows_kernel(const T *x, int64_t M,
 {
     grid_release();
     grid_wait();
-    const int64_t n = (int64_t)blockIdx.y * 128 + threadIdx.x, p = blockIdx.x;
-    if (n >= N) return;
-    float acc = 0.f;
-    for (int64_t m = p * 32; m < M && m < p * 32 + 32; ++m) acc += to_f(x[m * ld + n]);
-    part[p * N + n] = acc;
+    const int64_t p = blockIdx.x;
+    for (int64_t n = (int64_t)blockIdx.y * 128 + threadIdx.x; n < N; n += (int64_t)gridDim.y * 128) {
+        float acc = 0.f;
+        for (int64_t m = p * 32; m < M && m < p * 32 + 32; ++m) acc += to_f(x[m * ld + n]);
+        part[p * N + n] = acc;
+    }
 }
 
 }  // namespace
@@ -337,7 +338,7 @@ cudaError_t launch_colsum_finish(const float *part, int64_t parts, int64_t N, fl
 cudaError_t launch_colsum_rows(const void *x, gdn_dtype dt, int64_t M, int64_t N, int64_t ld, float *part, cudaStream_t st)
 {
     if (M <= 0 || N <= 0) return cudaSuccess;
-    const unsigned gx = (unsigned)((M + 31) / 32), gy = (unsigned)((N + 127) / 128);
+    const unsigned gx = (unsigned)((M + 31) / 32), gy = (unsigned)((N + 127) / 128 < 65535 ? (N + 127) / 128 : 65535);  // (a grid's most)
     if (dt == GDN_F32) return launch_overlapped(colsum_rows_kernel<float>, gx, gy, 128, 0, 0, st, (const float *)x, M, N, ld, part);
     return launch_overlapped(colsum_rows_kernel<__nv_bfloat16>, gx, gy, 128, 0, 0, st, (const __nv_bfloat16 *)x, M, N, ld, part);
 }

@@ -285,3 +285,12 @@ def test_quantised_infinities(gdn, D, dtype):
     for q, s in (gdn.quantize_rows(x), gdn.rms_norm_quant(x, None)[:2]):
         assert s[1:4].isnan().all() and s[[0, 4]].isfinite().all()
         assert q[[0, 4]].float().isfinite().all()
+
+
+def test_bias_gradient_of_many_columns(gdn):
+    """More columns than a grid has rows of blocks of 128."""
+    N = (1 << 23) + 5
+    g = gen(1)
+    x, w, b, dy = randn(g, 40, 1, dtype=BF), randn(g, N, 1, dtype=BF), randn(g, N), randn(g, 40, N, dtype=BF)
+    db = gdn.linear_bwd(dy, x, w, b, None, need_dx=False, need_dweight=False)[2]
+    ref.check(db, dy.double().sum(0), 40 * ref.SUM * dy.double().abs().sum(0))
