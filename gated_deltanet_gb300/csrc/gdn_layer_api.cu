@@ -148,6 +148,9 @@ struct Rows16 {
     }
 };
 
+// (the coordinates of a tile of 256 rows are 32-bit integers)
+constexpr int64_t kMostRows = INT32_MAX - 255;
+
 gdn_status check_linear(const gdn_linear_args *a, bool gated, bool backward)
 {
     if (!a || a->rows < 0 || a->out_features < 1 || a->in_features < 1) return GDN_ERR_INVALID;
@@ -180,7 +183,7 @@ gdn_status check_linear(const gdn_linear_args *a, bool gated, bool backward)
         if (a->residual && a->rows > 1 && a->ld_residual < N) return GDN_ERR_INVALID;
         if (!on_element(a->y, a->out_dtype) || !on_element(a->residual, a->out_dtype)) return GDN_ERR_INVALID;
     }
-    return GDN_OK;
+    return a->rows <= kMostRows ? GDN_OK : GDN_ERR_UNSUPPORTED;
 }
 
 // A call's workspace: padded copies of operands and of what the epilogues read and write; backward: dz (its rows padded

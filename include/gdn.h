@@ -448,7 +448,7 @@ typedef enum {
 } gdn_activation;
 
 typedef struct {
-    int64_t rows;         /* M */
+    int64_t rows;         /* M, at most 2^31 - 256                                     */
     int out_features;     /* N (gated linear unit: F, the width of one half)           */
     int in_features;      /* K >= 1 */
     gdn_dtype dtype;      /* x and w: GDN_F32, GDN_BF16 or (forward only) GDN_E4M3     */
