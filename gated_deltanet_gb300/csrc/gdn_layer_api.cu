@@ -186,6 +186,43 @@ gdn_status check_linear(const gdn_linear_args *a, bool gated, bool backward)
     return a->rows <= kMostRows ? GDN_OK : GDN_ERR_UNSUPPORTED;
 }
 
+// Rows of `cols` bytes, `ld` bytes apart
+struct Block {
+    uintptr_t at;
+    int64_t rows, cols, ld;
+    Block(const void *p, int64_t r, int64_t c, int64_t stride, size_t e)
+        : at((uintptr_t)p), rows(p ? r : 0), cols(c * (int64_t)e), ld(r > 1 ? stride * (int64_t)e : c * (int64_t)e) {}
+    uintptr_t end() const { return at + (rows - 1) * ld + cols; }
+    // one run of memory against rows: the first row that ends past it starts before its end
+    bool meets(uintptr_t lo, uintptr_t hi) const
+    {
+        const int64_t r = lo < at + cols ? 0 : (int64_t)(lo - at - cols) / ld + 1;
+        return r < rows && at + r * ld < hi;
+    }
+};
+// Whether two blocks share a byte.  (Rows with gaps at different strides on both sides count as apart.)
+bool share(const Block &a, const Block &b)
+{
+    if (a.rows <= 0 || b.rows <= 0 || a.at >= b.end() || b.at >= a.end()) return false;
+    if (a.ld == a.cols) return b.meets(a.at, a.end());
+    if (b.ld == b.cols) return a.meets(b.at, b.end());
+    if (a.ld != b.ld) return false;
+    const Block &lo = a.at <= b.at ? a : b, &hi = a.at <= b.at ? b : a;
+    const int64_t off = (int64_t)(hi.at - lo.at) % lo.ld;  // of hi's rows within lo's
+    return off < lo.cols || off + hi.cols > lo.ld;
+}
+
+// The kernels read operands while they write outputs: y lies over no input but, row for row, the residual.
+bool output_apart(const gdn_linear_args *a, bool gated)
+{
+    const int64_t M = a->rows, N = a->out_features, K = a->in_features, wrows = gated ? 2 * N : N;
+    const size_t e = esize(a->dtype), eo = esize(a->out_dtype);
+    const Block y(a->y, M, N, a->ldy, eo), r(a->residual, M, N, a->ld_residual, eo);
+    const bool same = a->y == a->residual && (M <= 1 || a->ldy == a->ld_residual);
+    return !share(y, Block(a->x, M, K, a->ldx, e)) && !share(y, Block(a->w, wrows, K, a->ldw, e)) && (same || !share(y, r)) &&
+           !share(y, Block(a->bias, 1, N, N, 4)) && !share(y, Block(a->x_scale, 1, M, M, 4)) && !share(y, Block(a->w_scale, 1, wrows, wrows, 4));
+}
+
 // A call's workspace: padded copies of operands and of what the epilogues read and write; backward: dz (its rows padded
 // to 16 bytes) and the column sums of groups of rows
 struct LinearPlan {
@@ -324,6 +361,7 @@ gdn_status run_fwd(const gdn_linear_args *a, bool gated, void *ws, size_t ws_byt
     gdn_status s = check_linear(a, gated, false);
     if (s != GDN_OK) return s;
     if (a->rows == 0) return GDN_OK;
+    if (!output_apart(a, gated)) return GDN_ERR_INVALID;
     LinearPlan p = plan_linear(a, gated, false);
     char *base = nullptr;
     if ((s = take_workspace(p.bytes, ws, ws_bytes, st, &base)) != GDN_OK) return s;

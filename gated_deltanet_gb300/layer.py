@@ -89,7 +89,7 @@ def linear(x, weight, bias=None, activation=None, residual=None, *, x_scale=None
     ``weight_scale`` [N] float32, as :func:`rms_norm_quant` and :func:`quantize_rows` give them); bias [N]
     float32; activation None, "silu", "gelu", "gelu_tanh", "relu" or "sigmoid"; residual [..., N] in the output's
     dtype.  The output is float32 for float32 inputs, else bfloat16 or, with ``out_dtype``, float32.  ``out`` may
-    be ``residual`` itself."""
+    be ``residual`` itself and overlap no other input."""
     f32 = None
     if out_dtype is not None:
         if out_dtype not in (torch.float32, torch.bfloat16):

@@ -376,6 +376,8 @@ gdn_status gdn_chain_states(int ranks, int pairs, int K, int V, const float *sum
  *    element: matrices whose rows do not start on 16-byte boundaries pass by
  *    padded copies in the workspace, and fp32 operands of more than 64 rows
  *    by their bf16 planes (six bytes an element).
+ *  - Outputs lie over no input and no other output, unless said at the field
+ *    (gdn_linear and gdn_gated_linear refuse a y that does, GDN_ERR_INVALID).
  *  - `workspace`: device memory of at least the size that the operator's
  *    _workspace_size call gives for the same arguments, 256-byte aligned, not
  *    used by another call that can run concurrently.  NULL: the

@@ -294,3 +294,33 @@ def test_bias_gradient_of_many_columns(gdn):
     x, w, b, dy = randn(g, 40, 1, dtype=BF), randn(g, N, 1, dtype=BF), randn(g, N), randn(g, 40, N, dtype=BF)
     db = gdn.linear_bwd(dy, x, w, b, None, need_dx=False, need_dweight=False)[2]
     ref.check(db, dy.double().sum(0), 40 * ref.SUM * dy.double().abs().sum(0))
+
+
+# ---------------------------------------------------------------- outputs and operands
+@pytest.mark.parametrize("M", [5, 300])
+def test_outputs_over_operands_are_refused(gdn, M):
+    """A product reads its operands while it writes: y in their place is refused, in the residual's place it is not."""
+    x, w = randn(gen(M), M, 64, dtype=BF), randn(gen(2), 64, 64, dtype=BF)
+    before = x.clone()
+    for f in (lambda: gdn.linear(x, w, out=x), lambda: gdn.gated_linear(x, w.repeat(2, 1), out=x),
+              lambda: gdn.linear(x[:, :64], w, None, None, x, out=x), lambda: gdn.linear(w, w, out=w)):
+        with pytest.raises(gdn.GdnError):
+            f()
+    shifted = torch.empty(M * 64 + 8, dtype=BF, device="cuda")
+    with pytest.raises(gdn.GdnError):
+        gdn.linear(x, w, residual=shifted[8:].view(M, 64), out=shifted[:-8].view(M, 64))
+    assert torch.equal(x, before)
+    stream = before.clone()
+    assert torch.equal(gdn.linear(x, w, residual=stream, out=stream), gdn.linear(x, w, residual=before))
+
+
+@pytest.mark.parametrize("M", [1, 5, 300])
+def test_slices_of_one_buffer(gdn, lib, M):
+    """x, the residual and y as columns side by side in the rows of one buffer share no element: an ordinary call."""
+    g = gen(M)
+    rows, w = randn(g, M, 192, dtype=BF), randn(g, 64, 64, dtype=BF)
+    want = gdn.linear(rows[:, :64], w, residual=rows[:, 64:128])
+    a = layer_c.GdnLinearArgs(**layer_c.pointers(rows=M, out_features=64, in_features=64, dtype=1, out_dtype=1, x=rows, ldx=192, w=w, ldw=64,
+                                                 residual=rows[:, 64:], ld_residual=192, y=rows[:, 128:], ldy=192))
+    assert lib.gdn_linear(a, None, 0, here()) == 0
+    assert torch.equal(rows[:, 128:], want)

@@ -35,3 +35,23 @@ def test_rows_past_32_bits_are_refused(L, call):
         assert getattr(L, call)(ctypes.byref(a), P, 1 << 60, None) == UNSUPPORTED
     if d:
         assert size(ctypes.byref(linear_args(rows=MOST, **d))) >= MOST * 64 * 2
+
+
+@pytest.mark.parametrize("call", ["gdn_linear", "gdn_gated_linear"])
+@pytest.mark.parametrize("kw", [
+    dict(x=P, y=P), dict(x=P, y=P + 64 * 3 + 62), dict(x=P, y=1 << 20, w=(1 << 20) + 32), dict(y=1 << 20, w=(1 << 20) + 4 * 128 - 16),
+    # slices of rows of one buffer that share a column
+    dict(x=P, ldx=200, y=P + 62, ldy=200), dict(x=P + 126, ldx=200, y=P, ldy=200), dict(x=P + 400 * 3, ldx=200, y=P, ldy=200),
+])
+def test_outputs_over_operands_are_refused(L, call, kw):
+    d = dict(x=1 << 24, w=1 << 25, **{k: v for k, v in kw.items() if k not in ("x", "w")})
+    d.update(kw)
+    assert getattr(L, call)(ctypes.byref(linear_args(**d)), P, 1 << 30, None) == INVALID
+
+
+@pytest.mark.parametrize("kw", [dict(residual=P + 16, ld_residual=64), dict(residual=P, ld_residual=72), dict(residual=P + 128, ld_residual=64),
+                                dict(bias=P), dict(bias=P + 4 * 128 - 4)])
+def test_outputs_over_other_inputs_are_refused(L, kw):
+    """y may be the residual, row for row, and lie over no other input."""
+    a = linear_args(x=1 << 24, w=1 << 25, y=P, **kw)
+    assert L.gdn_linear(ctypes.byref(a), P, 1 << 30, None) == INVALID
