@@ -3,8 +3,9 @@
 Each ``csrc/*.cu`` file is compiled to an object in parallel (one -gencode,
 sm_103a only) and linked into ``gated_deltanet_gb300/_lib/libgdn.so``.
 Beside it, ``csrc/layer_binding.cpp`` (the compiled part of the Python binding) becomes ``_lib/_layer.so``
-with the host compiler, against the installed PyTorch's headers.  A rebuild happens only when a source or
-header is newer than what was built.
+with the host compiler, against the installed PyTorch's headers; without PyTorch the library alone is built.  A rebuild
+happens only when a source or header is newer than what was built, and for the binding when PyTorch or Python is
+another than it was built for.
 """
 from __future__ import annotations
 
@@ -12,6 +13,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sys
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -22,6 +24,7 @@ LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libgdn.so")
 BINDING_SRC = os.path.join(CSRC, "layer_binding.cpp")
 BINDING = os.path.join(LIBDIR, "_layer.so")
+BUILT_FOR = os.path.join(LIBDIR, "_layer.built_for")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -35,8 +38,7 @@ def _sources():
 
 
 def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [
-        os.path.join(ROOT, "include", "gdn.h"), os.path.abspath(__file__), BINDING_SRC]
+    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(ROOT, "include", "gdn.h"), os.path.abspath(__file__)]
 
 
 def lib_path() -> str:
@@ -47,11 +49,35 @@ def binding_path() -> str:
     return BINDING
 
 
+def running() -> str | None:
+    """What the binding has to be built for: this PyTorch and this Python; None without PyTorch."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    return f"torch {torch.__version__}, python {sys.version_info[0]}.{sys.version_info[1]}"
+
+
+def built_for() -> str | None:
+    """What the binding was built for; None where none was."""
+    try:
+        with open(BUILT_FOR) as f:
+            return f.read()
+    except FileNotFoundError:
+        return None
+
+
+def _stale(built: str, deps) -> bool:
+    return not os.path.exists(built) or any(os.path.getmtime(p) > os.path.getmtime(built) for p in deps)
+
+
+def _binding_stale() -> bool:
+    now = running()
+    return now is not None and (built_for() != now or _stale(BINDING, _deps() + [BINDING_SRC]))
+
+
 def needs_build() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
-        return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return any(os.path.getmtime(p) > t for p in _deps())
+    return _stale(LIB, _deps()) or _binding_stale()
 
 
 def _compile_binding() -> str:
@@ -83,10 +109,14 @@ def _link_binding(obj: str) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"link of {BINDING} failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    with open(BUILT_FOR + f".tmp{os.getpid()}", "w") as f:
+        f.write(running())
+    os.replace(f.name, BUILT_FOR)
 
 
 def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -> str:
-    if not force and not needs_build():
+    library, binding = force or _stale(LIB, _deps()), running() is not None and (force or _binding_stale())
+    if not library and not binding:
         return LIB
     os.makedirs(OBJ, exist_ok=True)
     os.makedirs(LIBDIR, exist_ok=True)
@@ -103,25 +133,25 @@ def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    srcs = _sources()
+    srcs = _sources() if library else []
     with ThreadPoolExecutor(max_workers=jobs or min(12, len(srcs) + 1)) as ex:
-        binding = ex.submit(_compile_binding)
+        obj = ex.submit(_compile_binding) if binding else None
         results = list(ex.map(compile_one, srcs))
-        binding_obj = binding.result()
     if verbose:
         for _, err in results:
             if err:
                 print(err)
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc()] + ARCH + ["-shared", "-Xlinker", "-soname=libgdn.so", "-o", tmp] + [o for o, _ in results] + ["-lcudart_static"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    _link_binding(binding_obj)
+    if library:
+        tmp = LIB + f".tmp{os.getpid()}"
+        cmd = [nvcc()] + ARCH + ["-shared", "-Xlinker", "-soname=libgdn.so", "-o", tmp] + [o for o, _ in results] + ["-lcudart_static"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, LIB)
+    if binding:  # (last: what fails here does not cost the library)
+        _link_binding(obj.result())
     return LIB
 
 
 if __name__ == "__main__":
-    import sys
     print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))

@@ -19,7 +19,7 @@ import threading
 import torch
 
 from ._binding import GdnError, load_library
-from .build import binding_path
+from . import build
 
 ACTIVATIONS = {None: 0, "none": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3, "relu": 4, "sigmoid": 5}
 
@@ -32,10 +32,11 @@ def _load():
     with _lock:
         if _module is None:
             load_library()
-            p = binding_path()
+            p, how = build.binding_path(), "build it with `python -c 'import __graft_entry__ as g; g.build()'`"
             if not os.path.exists(p):
-                raise ImportError(f"{os.path.basename(p)} not found at {p}; build it with "
-                                  "`python -c 'import __graft_entry__ as g; g.build()'`")
+                raise ImportError(f"{os.path.basename(p)} not found at {p}; {how}")
+            if build.built_for() != build.running():
+                raise ImportError(f"{p} was built for {build.built_for()}, this is {build.running()}; {how}")
             loader = importlib.machinery.ExtensionFileLoader("_layer", p)
             m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_layer", loader))
             loader.exec_module(m)

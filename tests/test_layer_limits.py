@@ -55,3 +55,30 @@ def test_outputs_over_other_inputs_are_refused(L, kw):
     """y may be the residual, row for row, and lie over no other input."""
     a = linear_args(x=1 << 24, w=1 << 25, y=P, **kw)
     assert L.gdn_linear(ctypes.byref(a), P, 1 << 30, None) == INVALID
+
+
+def test_binding_built_for_another_pytorch_is_not_loaded(gdn, monkeypatch):
+    """The compiled binding holds for the PyTorch and Python whose headers it was compiled with: with others it counts as not built,
+    and is refused where nobody built it again."""
+    assert not gdn.build.needs_build()
+    gdn.layer._load()
+    monkeypatch.setattr(gdn.build, "running", lambda: "torch 0.0, python 3.0")
+    assert gdn.build.needs_build()
+    monkeypatch.setattr(gdn.layer, "_module", None)
+    with pytest.raises(ImportError, match="built for torch .* torch 0.0"):
+        gdn.layer._load()
+
+
+def test_library_builds_without_pytorch(gdn, monkeypatch, tmp_path):
+    """Users of the C library alone: without PyTorch no binding is wanted, and one that fails to compile does not cost the library."""
+    monkeypatch.setattr(gdn.build, "running", lambda: None)
+    monkeypatch.setattr(gdn.build, "BINDING", str(tmp_path / "_layer.so"))
+    assert not gdn.build.needs_build()
+    monkeypatch.undo()
+    monkeypatch.setattr(gdn.build, "BINDING", str(tmp_path / "_layer.so"))
+    monkeypatch.setenv("CXX", "false")
+    before = gdn.build.os.path.getmtime(gdn.build.LIB)
+    assert gdn.build.needs_build()
+    with pytest.raises(RuntimeError, match="false"):
+        gdn.build.build()
+    assert gdn.build.os.path.getmtime(gdn.build.LIB) == before
