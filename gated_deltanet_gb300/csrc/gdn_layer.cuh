@@ -11,8 +11,9 @@
 namespace gdn {
 
 // Activations.  `PRECISE` (fp32 outputs) takes the full-accuracy exponential and division; otherwise the
-// result is rounded to bf16 (relative step 2^-8) and the fast ones (relative error below 2^-20 for the
-// arguments where the result is not itself lost in that rounding) are enough.
+// result is rounded to bf16 (relative step 2^-8) and the fast ones are enough: the rounding of the exponent makes exp(-z) off by up to
+// |z| 2^-23 of itself (2^-16.5 at |z| = 90), the approximate exponential and reciprocal by 2^-21.  A logistic function below the
+// smallest normal fp32 number (z < -87.3) is flushed to 0, so that silu is 0 there where it is -1e-36 and less.
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kF32Max = 3.40282347e38f, kBf16Max = 3.38953139e38f;
 __device__ __forceinline__ float fast_exp2(float x)

@@ -324,3 +324,18 @@ def test_slices_of_one_buffer(gdn, lib, M):
                                                  residual=rows[:, 64:], ld_residual=192, y=rows[:, 128:], ldy=192))
     assert lib.gdn_linear(a, None, 0, here()) == 0
     assert torch.equal(rows[:, 128:], want)
+
+
+@pytest.mark.parametrize("rows", [60, 300])
+@pytest.mark.parametrize("name", ["silu", "sigmoid"])
+def test_far_tails_in_bf16(gdn, rows, name):
+    """bf16 outputs of arguments from 16 to 90: the exponent's rounding makes exp(-z) off by |z| 2^-23 of itself, beside the approximate exponential and
+    reciprocal (2^-21) and the output's rounding; a logistic function below the smallest normal fp32 number may be zero."""
+    z = torch.linspace(16, 90, rows // 2, device="cuda")
+    z = torch.cat([z, -z]).to(BF)
+    x, w = one_column(z)
+    y = gdn.linear(x, w, None, name)[:, 0]
+    zd = z.double()
+    want = ref.act(zd, name)
+    lost = 2.0 ** -126 * (zd.abs() if name == "silu" else 1)
+    ref.check(y, want, want.abs() * (ref.HALF[BF] + 2.0 ** -20 + zd.abs() * 2.0 ** -23 * 1.01) + lost)
