@@ -339,3 +339,27 @@ def test_far_tails_in_bf16(gdn, rows, name):
     want = ref.act(zd, name)
     lost = 2.0 ** -126 * (zd.abs() if name == "silu" else 1)
     ref.check(y, want, want.abs() * (ref.HALF[BF] + 2.0 ** -20 + zd.abs() * 2.0 ** -23 * 1.01) + lost)
+
+
+# ---------------------------------------------------------------- fp32 products
+def norm_off(got, want):
+    return float((got.double() - want).norm() / want.norm())
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 72, 48), (64, 129, 2048), (70, 136, 48), (129, 72, 1600), (257, 330, 3200), (520, 129, 6416), (300, 520, 2048)])
+def test_fp32_products_to_the_last_bits(gdn, M, N, K):
+    """The relative 2-norm of the error, which sees every plane of an operand and every product of planes (two planes instead of
+    three: 3.5e-6).  On the tensor cores: sums of 128 in 8 truncated steps, at most 4.3 units of 2^-24 off in the mean; their sum in fp32, sqrt(K / 128)
+    / 2.4 units; the output's rounding; below 4e-7 together.  On the CUDA cores (64 rows and fewer): a sum of K terms of random signs in order, sqrt(K)
+    / 2.4 units, and the rounding."""
+    g = gen(M + K)
+    tol = 4e-7 if M > 64 else 2.0 ** -24 * (1 + K ** 0.5 / 2.4)
+    x, w, dy = randn(g, M, K), randn(g, N, K) / K ** 0.5, randn(g, M, N)
+    assert norm_off(gdn.linear(x, w), x.double() @ w.double().t()) < tol
+    dx, dw, _ = gdn.linear_bwd(dy, x, w)
+    assert norm_off(dx, dy.double() @ w.double()) < (4e-7 if M > 64 else 2.0 ** -24 * (1 + N ** 0.5 / 2.4))
+    assert norm_off(dw, dy.double().t() @ x.double()) < 4e-7
+    w = randn(g, 2 * N, K) / K ** 0.5
+    gate, up = (x.double() @ w.double().t()).split(N, 1)
+    # a product of two such sums
+    assert norm_off(gdn.gated_linear(x, w, None), gate * up) < 2.5 * tol
