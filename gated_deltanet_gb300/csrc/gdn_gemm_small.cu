@@ -323,7 +323,7 @@ gemm_small_kernel(const __grid_constant__ SmallMaps maps, const SmallParams p)
     }
 }
 
-size_t esz(gdn_dtype t) { return t == GDN_F32 ? 4 : t == GDN_BF16 ? 2 : 1; }
+size_t esz(gdn_dtype t) { return t == GDN_BF16 ? 2 : 1; }  // of an operand
 
 constexpr size_t kRoom = 110 * 1024;  // a CTA's shared memory: two on an SM
 

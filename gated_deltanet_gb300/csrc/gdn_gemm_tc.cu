@@ -105,8 +105,12 @@ __device__ __forceinline__ void peer_store(uint32_t addr, float v)
 {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
-// (relaxed: what it announces is that accumulators were read, which the tcgen05 fence before it orders; a release would
-// wait for the epilogue's global stores, 1400 cycles a tile)
+// Relaxed: it hands over tensor memory and nothing else.  The warp's reads of the accumulators are complete (tcgen05.wait::ld)
+// and ordered before the arrival by tcgen05.fence::before_thread_sync (for the whole warp: __syncwarp, then one lane arrives);
+// the issuer's tcgen05.fence::after_thread_sync, behind the wait that saw the arrival, orders its products after it.  Only tcgen05
+// instructions reach tensor memory, and those two fences are what orders them between threads that meet in any way, so no
+// release of ordinary memory is needed: column vectors and patch stay the warp's own.  A release would wait for the
+// epilogue's global stores, 1400 cycles a tile.
 __device__ __forceinline__ void remote_arrive(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -863,7 +867,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder()
     return fn;
 }
 
-size_t esz(gdn_dtype t) { return t == GDN_F32 ? 4 : t == GDN_BF16 ? 2 : 1; }
+size_t esz(gdn_dtype t) { return t == GDN_BF16 ? 2 : 1; }  // of an operand
 
 template <int KIND, int LAYOUT, int EPI, int BN, typename TO, bool SPLIT = false>
 cudaError_t go(const GemmArgs &g, cudaStream_t st, int split = 1)
@@ -989,8 +993,8 @@ cudaError_t pick(const GemmArgs &g, cudaStream_t st)
 // the weight's, and its contraction the batch.)
 bool use_small(const GemmArgs &g) { return !g.a_t && g.M <= kFewRows; }
 
-// fp32 rows as three planes of bf16: each the rounding of what the ones before leave (exactly x for normal values), the
-// first no larger than bf16's largest while x is finite; an infinity or NaN has zeros in the lower planes
+// fp32 rows as three planes of bf16: each the rounding of what the ones before leave (exactly x from 2^-110 on; the planes of
+// smaller values end at bf16's smallest, 2^-133), the first no larger than bf16's largest while x is finite; an infinity or NaN has zeros in the lower planes
 __global__ void __launch_bounds__(256) split_kernel(const float *src, int64_t ld, int64_t rows, int64_t cols, __nv_bfloat16 *dst, int64_t pitch,
                                                     int64_t plane)
 {
@@ -1055,9 +1059,7 @@ bool make_operand_map(CUtensorMap *m, gdn_dtype t, const void *base, int64_t col
     cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     cuuint64_t strides[1] = {rows > 1 ? (cuuint64_t)ld * e : ((cuuint64_t)cols * e + 15) / 16 * 16};
     cuuint32_t box[2] = {(cuuint32_t)(128 / e), (cuuint32_t)box_rows}, es[2] = {1, 1};
-    const CUtensorMapDataType dt = t == GDN_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                                   : t == GDN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                   : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    const CUtensorMapDataType dt = t == GDN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
     return enc(m, dt, 2, const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
