@@ -204,6 +204,7 @@ PyObject *rms_norm(PyObject *const *p)
     const Tensor &x = *tensor("x", p[0]);
     const Tensor *w = tensor("weight", p[1], true), *r = tensor("residual", p[2], true);
     const bool quant = truth(p[4]);
+    if (!r && p[6] != Py_None) bad_value("residual_out goes with a residual");
     cuda("x", x);
     need_real("x", x);
     const int64_t width = width_of("x", x);

@@ -57,8 +57,8 @@ def rms_norm(x, weight=None, residual=None, eps=1e-6, *, out=None, residual_out=
     ``y = weight * h / sqrt(mean(h^2) + eps)`` over the last dimension, in fp32, rounded once.
 
     x, residual [..., D] float32 or bfloat16 (same dtype); weight [D] float32 or bfloat16, or None.
-    Returns ``(y, h)``: both in x's dtype, ``h`` None without a residual.  ``residual_out`` may be
-    ``residual`` itself (the residual stream updated in place)."""
+    Returns ``(y, h)``: both in x's dtype, ``h`` None without a residual.  ``residual_out`` goes
+    with a residual and may be ``residual`` itself (the residual stream updated in place)."""
     y, _, h = (_module or _load()).rms_norm(x, weight, residual, eps, False, out, residual_out)
     return y, h
 

@@ -2,6 +2,7 @@
 import ctypes
 
 import pytest
+import torch
 
 import layer_c
 from test_layer_host import INVALID, UNSUPPORTED, P, linear_args
@@ -82,3 +83,11 @@ def test_library_builds_without_pytorch(gdn, monkeypatch, tmp_path):
     with pytest.raises(RuntimeError, match="false"):
         gdn.build.build()
     assert gdn.build.os.path.getmtime(gdn.build.LIB) == before
+
+
+@pytest.mark.parametrize("name", ["rms_norm", "rms_norm_quant"])
+def test_a_place_for_the_stream_goes_with_a_residual(gdn, name):
+    """Without a residual there is no sum to write: the buffer would be left as it was."""
+    x = torch.zeros(4, 8)
+    with pytest.raises(ValueError, match="residual_out"):
+        getattr(gdn, name)(x, residual_out=torch.zeros(4, 8))
