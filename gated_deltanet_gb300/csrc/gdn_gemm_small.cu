@@ -1,4 +1,5 @@
-// Products of few rows (decode, short batches) on the tensor cores: bound by reading the weights once.
+// Products of few rows (decode, short batches) on the tensor cores: they read the weights once, and are bound by that and by
+// what a launch, a wait for the first weights and a meeting of the cluster take.
 //
 // The roles of the operands are swapped: 128 rows of the weight are the M side of the instruction and up to
 // NT rows of x its N side, so that one token costs an N = 16 instruction and not a padded 128 x 256 tile.  The
@@ -7,8 +8,8 @@
 // that finish the rows of x in turn (row t: CTA t mod split), which add them in the order of the
 // contraction; sums are sent and not fetched, so that one meeting of the cluster is enough.  A CTA's shared
 // memory is one queue of 128-byte-wide weight boxes, and two CTAs share an SM: most of what they read is
-// requested at once.  Measured: 64 rows of 2048 by 11008 gated bf16 weights (45 MB) 12.6 us from HBM, 8.9 from L2;
-// one row by 2048 x 5504 6.6 us.
+// requested at once.  Measured: 64 rows of 2048 by 11008 gated bf16 weights (45 MB) 12.6 us from HBM, 9.1 from L2 (x is
+// staged again for each of its 86 weight tiles: 109 MB through L2); one row by 2048 x 5504 7.2 us from HBM, 5.5 from L2.
 #include <atomic>
 #include <cstring>
 

@@ -1,5 +1,8 @@
 // Internal declarations of the decoder-block operators (norm, linear, gated linear unit): the
 // argument blocks of their kernels and the arithmetic that every engine's epilogue shares.
+//
+// Figures in the comments at these kernels are of calls on the same tensors, twenty in a captured graph, unless they say
+// otherwise: what fits L2 is read from there.
 #pragma once
 
 #include <atomic>
