@@ -267,6 +267,8 @@ cudaError_t launch_norm_bwd(const NormBwdArgs &a, int num_sms, cudaStream_t st);
 // The library-managed workspace of (device, stream), grown to `need` bytes; and whether it holds them already.
 gdn_status managed_workspace(size_t need, cudaStream_t stream, void **out, size_t *out_bytes);
 bool managed_workspace_holds(size_t need, cudaStream_t stream);
+// caller's workspace, or the library's where none is given
+gdn_status take_workspace(size_t need, void *ws, size_t bytes, cudaStream_t st, char **out);
 int device_sm_count();  // of the current device (asked once per device)
 // Whether this is the first call with `seen` on the current device; then the caller sets the kernel's attributes.
 // (Two threads may both see a first call: setting an attribute twice is harmless.)

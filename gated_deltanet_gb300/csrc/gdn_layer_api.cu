@@ -6,13 +6,7 @@
 
 using namespace gdn;
 
-namespace {
-
-size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
-size_t esize(gdn_dtype t) { return t == GDN_F32 ? 4 : t == GDN_BF16 ? 2 : 1; }
-
-// caller's workspace, or the library's where none is given
-gdn_status take_workspace(size_t need, void *ws, size_t bytes, cudaStream_t st, char **out)
+gdn_status gdn::take_workspace(size_t need, void *ws, size_t bytes, cudaStream_t st, char **out)
 {
     *out = nullptr;
     if (need == 0) return GDN_OK;
@@ -34,6 +28,11 @@ gdn_status take_workspace(size_t need, void *ws, size_t bytes, cudaStream_t st, 
     if (s == GDN_OK) *out = (char *)p + 256;
     return s;
 }
+
+namespace {
+
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+size_t esize(gdn_dtype t) { return t == GDN_F32 ? 4 : t == GDN_BF16 ? 2 : 1; }
 
 bool real(gdn_dtype t) { return t == GDN_F32 || t == GDN_BF16; }
 bool on_element(const void *p, gdn_dtype t) { return ((uintptr_t)p & (esize(t) - 1)) == 0; }

@@ -1,0 +1,201 @@
+// Linear attention with a decay for each head on the CUDA cores: every type, any head size up to 256.
+//
+// One CTA per (sequence, value head, 32 columns of c) walks the sequence in chunks of 32 tokens with the state X in registers
+// (its owners add to it) and in shared memory (everyone reads it).  Per chunk, in fp32:
+//   P_ij = cs l^|i-j| (a_i . b_j),  out = os (P c + diag(l^(i+1)) a X),  X <- l^n X + b^T diag(cs l^(n-1-j)) c
+// (against time the powers count from the chunk's other end).  16 x 16 threads hold 2 x 2 outputs each and read operands 16 bytes
+// at a time along the contraction.
+#include "gdn_mix.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kC = 32, kBV = 32, kThreads = 256, kMaxD = 256;
+constexpr int kCS = kBV + 4;
+
+template <typename T>
+__device__ __forceinline__ void load_rows(float *dst, int stride, const T *src, int64_t ld, int rows, int cols, int width)
+{
+    // kC rows of `width` (a multiple of 4) columns, zeros behind `rows` and `cols`
+    for (int i = threadIdx.x; i < kC * width; i += kThreads) {
+        const int r = i / width, c = i - r * width;
+        dst[r * stride + c] = r < rows && c < cols ? to_f<T>(src[(int64_t)r * ld + c]) : 0.f;
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) lin_simt_kernel(const LinArgs args)
+{
+    extern __shared__ float4 lin_smem[];
+    const LinPass &p = args.pass[blockIdx.y];
+    const int nct = (p.dc + kBV - 1) / kBV;
+    if (blockIdx.x >= (int64_t)args.N * args.HV * nct) return;
+    const int ct = (int)(blockIdx.x % nct), hv = (int)(blockIdx.x / nct % args.HV), n = (int)(blockIdx.x / ((int64_t)nct * args.HV));
+    const SeqRange s = seq_range(args.cu, n, args.T);
+    const int da = p.da, w = (da + 3) & ~3, st = w + 4, c0 = ct * kBV, cols = min(kBV, p.dc - c0);
+    float *A = (float *)lin_smem, *B = A + kC * st, *C = B + kC * st, *P = C + kC * kCS, *X = P + kC * kCS;  // X [w][kCS]
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int xq = tid & 7, xr = tid >> 3;  // the state's owner: columns 4 xq .., rows xr + 32 i
+    const float g = args.decay ? args.decay[hv] : 0.f, g2 = g * kRcpLn2;
+    const int64_t xbase = ((int64_t)n * args.HV + hv) * da * p.dc;
+    auto xat = [&](int r, int c) { return xbase + (p.x_t ? (int64_t)(c0 + c) * da + r : (int64_t)r * p.dc + c0 + c); };
+
+    float x[kMaxD / 32][4];
+#pragma unroll
+    for (int i = 0; i < kMaxD / 32; ++i) {
+        const int r = xr + 32 * i;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            x[i][k] = p.x0 && r < da && 4 * xq + k < cols ? p.x0[xat(r, 4 * xq + k)] : 0.f;
+            if (r < w) X[r * kCS + 4 * xq + k] = x[i][k];
+        }
+    }
+    const int chunks = (s.len + kC - 1) / kC;
+    for (int m = 0; m < chunks; ++m) {
+        const int c = p.reverse ? chunks - 1 - m : m;
+        const int64_t t0 = s.bos + (int64_t)c * kC;
+        const int rows = min(kC, s.len - c * kC);
+        const int late = p.reverse && m == 0;  // X0 enters one step later
+        __syncthreads();
+        load_rows<T>(A, st, (const T *)p.a + t0 * p.lda + (int64_t)(hv / p.ra) * da, p.lda, rows, da, w);
+        load_rows<T>(B, st, (const T *)p.b + t0 * p.ldb + (int64_t)(hv / p.rb) * da, p.ldb, rows, da, w);
+        load_rows<T>(C, kCS, (const T *)p.c + t0 * p.ldc + (int64_t)(hv / p.rc) * p.dc + c0, p.ldc, rows, cols, kBV);
+        __syncthreads();
+        float o[2][2] = {};
+        if (p.out) {
+            float z[2][2] = {};
+            for (int k = 0; k < w; k += 4) {
+                float4 u[2], v[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    u[i] = *(const float4 *)&A[(ty + 16 * i) * st + k];
+                    v[i] = *(const float4 *)&B[(tx + 16 * i) * st + k];
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        z[i][j] += u[i].x * v[j].x + u[i].y * v[j].y + u[i].z * v[j].z + u[i].w * v[j].w;
+                        o[i][j] += u[i].x * X[k * kCS + tx + 16 * j] + u[i].y * X[(k + 1) * kCS + tx + 16 * j] +
+                                   u[i].z * X[(k + 2) * kCS + tx + 16 * j] + u[i].w * X[(k + 3) * kCS + tx + 16 * j];
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int r = ty + 16 * i, q = tx + 16 * j, gap = p.reverse ? q - r : r - q;
+                    P[r * kCS + q] = gap >= 0 ? z[i][j] * (p.cs * decay_pow(g2, gap)) : 0.f;
+                    o[i][j] *= decay_pow(g2, p.reverse ? max(rows - r - late, 0) : r + 1);
+                }
+        }
+        __syncthreads();
+        if (p.out) {
+#pragma unroll 4
+            for (int j = 0; j < kC; ++j) {
+                const float u0 = P[ty * kCS + j], u1 = P[(ty + 16) * kCS + j], v0 = C[j * kCS + tx], v1 = C[j * kCS + tx + 16];
+                o[0][0] += u0 * v0;
+                o[0][1] += u0 * v1;
+                o[1][0] += u1 * v0;
+                o[1][1] += u1 * v1;
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int r = ty + 16 * i, q = tx + 16 * j;
+                    if (r < rows && q < cols) {
+                        const int64_t at = ((t0 + r) * args.HV + hv) * p.dc + c0 + q;
+                        if (p.out_f32) ((float *)p.out)[at] = p.os * o[i][j];
+                        else ((T *)p.out)[at] = from_f<T>(p.os * o[i][j]);
+                    }
+                }
+        }
+        const Decayed down(g, rows - late);
+#pragma unroll
+        for (int i = 0; i < kMaxD / 32; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[i][k] = down(x[i][k]);
+        for (int j = 0; j < rows; ++j) {
+            const float f = p.cs * decay_pow(g2, p.reverse ? j : rows - 1 - j);
+            const float4 v = *(const float4 *)&C[j * kCS + 4 * xq];
+#pragma unroll
+            for (int i = 0; i < kMaxD / 32; ++i) {
+                const int r = xr + 32 * i;
+                if (r < w) {
+                    const float b = f * B[j * st + r];
+                    x[i][0] += b * v.x;
+                    x[i][1] += b * v.y;
+                    x[i][2] += b * v.z;
+                    x[i][3] += b * v.w;
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kMaxD / 32; ++i) {
+            const int r = xr + 32 * i;
+            if (r < w) *(float4 *)&X[r * kCS + 4 * xq] = make_float4(x[i][0], x[i][1], x[i][2], x[i][3]);
+        }
+    }
+    if (p.x1) {
+        const Decayed down(g, p.reverse && chunks > 0 ? 1 : 0);
+#pragma unroll
+        for (int i = 0; i < kMaxD / 32; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int r = xr + 32 * i;
+                if (r < da && 4 * xq + k < cols) p.x1[xat(r, 4 * xq + k)] = down(x[i][k]);
+            }
+    }
+}
+
+template <typename T>
+__global__ void lin_heads_kernel(const float *part, const int64_t *cu, int N, int64_t tokens, int H, int r, int D, T *out)
+{
+    // (rows outside every sequence have no parts)
+    const int64_t per = (int64_t)H * D, lo = cu ? clamp64(cu[0], 0, tokens) * per : 0, hi = cu ? clamp64(cu[N], 0, tokens) * per : tokens * per;
+    for (int64_t i = lo + (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < hi; i += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t head = i / D;
+        const float *p = part + (head * r) * D + (i - head * D);
+        float s = p[0];
+        for (int k = 1; k < r; ++k) s += p[(int64_t)k * D];
+        out[i] = from_f<T>(s);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_lin_simt(const LinArgs &a, gdn_dtype dt, cudaStream_t st)
+{
+    int64_t most = 0;
+    size_t smem = 0;
+    for (int i = 0; i < a.passes; ++i) {
+        const LinPass &p = a.pass[i];
+        most = std::max(most, (int64_t)a.N * a.HV * ((p.dc + kBV - 1) / kBV));
+        const size_t w = (p.da + 3) & ~3;
+        smem = std::max(smem, 4 * (2 * kC * (w + 4) + 2 * kC * kCS + w * kCS));
+    }
+    if (most > INT32_MAX) return cudaErrorInvalidConfiguration;
+    auto kern = dt == GDN_F32 ? lin_simt_kernel<float> : lin_simt_kernel<__nv_bfloat16>;
+    static std::atomic<uint64_t> seen[2];
+    if (first_on_device(seen[dt == GDN_F32])) {
+        const int bytes = 4 * (2 * kC * (kMaxD + 4) + 2 * kC * kCS + kMaxD * kCS);
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
+        done_on_device(seen[dt == GDN_F32]);
+    }
+    kern<<<dim3((unsigned)most, a.passes), kThreads, smem, st>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_lin_heads(const float *part, const LinArgs &a, int64_t tokens, int H, int r, int D, void *out, gdn_dtype dt, cudaStream_t st)
+{
+    const int64_t n = tokens * H * D;
+    if (n == 0) return cudaSuccess;
+    const unsigned blocks = (unsigned)std::min<int64_t>((n + 255) / 256, 152 * 16);
+    if (dt == GDN_F32) lin_heads_kernel<float><<<blocks, 256, 0, st>>>(part, a.cu, a.N, tokens, H, r, D, (float *)out);
+    else lin_heads_kernel<__nv_bfloat16><<<blocks, 256, 0, st>>>(part, a.cu, a.N, tokens, H, r, D, (__nv_bfloat16 *)out);
+    return cudaGetLastError();
+}
+
+}  // namespace gdn

@@ -1,0 +1,147 @@
+// Internal declarations of the token mixers beside the gated delta rule: linear attention with a decay for each head, and
+// softmax attention with a sliding window and first tokens that stay visible.
+#pragma once
+
+#include "gdn_layer.cuh"
+
+namespace gdn {
+
+// ---------------------------------------------------------------- sequences
+// Where sequence n stands among `total` tokens: packed by cu (n + 1 offsets) or one of equal length T.  Offsets are clamped to
+// the tensor, so that a malformed table can give wrong results but no access outside.
+struct SeqRange {
+    int64_t bos;
+    int len;
+};
+__host__ __device__ inline int64_t clamp64(int64_t x, int64_t lo, int64_t hi) { return x < lo ? lo : x > hi ? hi : x; }
+__device__ __forceinline__ SeqRange seq_range(const int64_t *cu, int n, int T)
+{
+    if (!cu) return {(int64_t)n * T, T};
+    const int64_t b = clamp64(cu[n], 0, T), e = clamp64(cu[n + 1], b, T);
+    return {b, (int)(e - b)};
+}
+// Tiles of `tile` tokens of all sequences in one grid dimension.  Equal lengths: ceil(T / tile) each.  Packed: sequence n has the
+// slots from floor(cu[n] / tile) + n on, so that no two share one and total / tile + N + 1 slots are enough; some stay empty.
+__host__ __device__ inline int64_t mix_slots(bool packed, int N, int T, int tile)
+{
+    return packed ? (int64_t)T / tile + N + 1 : (int64_t)N * ((T + tile - 1) / tile);
+}
+struct Tile {
+    int n, index;  // sequence, tile within it
+};
+__device__ __forceinline__ Tile tile_of(const int64_t *cu, int N, int T, int tile, int64_t slot)
+{
+    if (!cu) {
+        const int per = (T + tile - 1) / tile;
+        return {(int)(slot / per), (int)(slot % per)};
+    }
+    int lo = 0, hi = N - 1;  // the last n whose first slot is not past this one
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (clamp64(cu[mid], 0, T) / tile + mid <= slot) lo = mid;
+        else hi = mid - 1;
+    }
+    const int64_t i = slot - (clamp64(cu[lo], 0, T) / tile + lo);
+    return {lo, (int)clamp64(i, 0, INT32_MAX / tile - 1)};
+}
+
+// ---------------------------------------------------------------- linear attention
+// One pass of linear attention over every (sequence, value head), in time or against it.  With l = exp(decay), n tokens:
+//   out_i = os (cs sum_{j <= i} l^(i-j) (a_i . b_j) c_j + l^(i+1) a_i X0)
+//   X1    = cs sum_j l^(n-1-j) b_j c_j^T + l^n X0                                X [da][dc]
+// against time: j >= i, l^(j-i), and X0 enters one step later (l^(n-1-i)); X1 = cs sum_j l^j b_j c_j^T + l^(n-1) X0, times l when
+// it is written.  The forward is (q, k, v); with dO the gradients are dq = (dO, v, k) in time and dk = (v, dO, q),
+// dv = (k, q, dO) against it: the state's gradient R_t = l R_{t+1} + scale q_t dO_t^T runs backward.
+struct LinPass {
+    const void *a, *b, *c;   // [tokens][heads][da], [..][da], [..][dc]
+    int64_t lda, ldb, ldc;   // elements from a token to the next
+    int ra, rb, rc;          // value heads that share a head of a, b, c
+    void *out;               // [tokens][HV][dc], the inputs' type or (out_f32) fp32; nullable
+    const float *x0;         // [N][HV][da][dc], or (x_t) [N][HV][dc][da]; nullable (zero)
+    float *x1;               // the same layout, nullable
+    float cs, os;
+    int da, dc, out_f32, x_t, reverse;
+};
+struct LinArgs {
+    LinPass pass[3];
+    int passes;              // 1, or 3 (the gradients)
+    const float *decay;      // [HV], nullable (0)
+    const int64_t *cu;
+    int T, N, HV;            // packed: T = all tokens
+    unsigned *status;
+};
+cudaError_t launch_lin_simt(const LinArgs &a, gdn_dtype dt, cudaStream_t st);
+// out[t][h][d] = sum over the r value heads of head h of part[t][h r + i][d], summed in order
+cudaError_t launch_lin_heads(const float *part, const LinArgs &a, int64_t tokens, int H, int r, int D, void *out, gdn_dtype dt, cudaStream_t st);
+
+struct LinStepArgs {
+    const void *q, *k, *v;
+    int64_t ldq, ldk, ldv;
+    const float *decay, *h0;
+    const int64_t *cu;
+    void *o;
+    float *ht;
+    int T, N, H, HV, K, V;
+    float scale;
+};
+cudaError_t launch_lin_step(const LinStepArgs &a, gdn_dtype dt, cudaStream_t st);
+
+// l^x of a log-decay in base 2 and a count of steps; l^0 = 1 for every decay, minus infinity too
+__device__ __forceinline__ float decay_pow(float g2, int x) { return x == 0 ? 1.f : exp2f(g2 * (float)x); }
+// The state after x steps, l^x X.  Near 1 as X + X (l^x - 1): l^x itself, rounded, would lose the digits of 1 - l^x chunk after chunk.
+struct Decayed {
+    float f;
+    bool near;
+    __device__ __forceinline__ Decayed(float g, int x)
+    {
+        const float d = x == 0 ? 0.f : g * (float)x;
+        near = d > -0.5f;
+        f = near ? expm1f(d) : expf(d);
+    }
+    __device__ __forceinline__ float operator()(float X) const { return fmaf(X, f, near ? X : 0.f); }
+};
+
+// ---------------------------------------------------------------- window attention
+// Query i of a sequence with Lq queries and Lk keys stands at position p = i + Lk - Lq and sees key j when
+// j <= p and (p - j < window or j < sinks).
+struct WinArgs {
+    const void *q, *k, *v;      // [tokens][heads][D]
+    int64_t ldq, ldk, ldv;
+    const int64_t *cu_q, *cu_k;  // both or none
+    int Tq, Tk, N, H, HK, D;
+    int window, sinks;          // clamped to [1, Tk] and [0, Tk]
+    float scale;
+    void *o;                    // [tokens][H][D]
+    float *lse;                 // [B][H][Tq] (packed: [H][Tq]), nullable
+    // gradients
+    const void *dout;
+    int64_t ld_dout;
+    const float *delta;         // rows' sums of dO o, laid out as lse
+    void *dq, *dk, *dv;
+    unsigned *status;
+};
+__host__ __device__ inline int64_t lse_at(const WinArgs &a, int n, int64_t bos, int h)
+{
+    // element of row `bos` (the first of sequence n) and head h
+    return a.cu_q ? (int64_t)h * a.Tq + bos : ((int64_t)n * a.H + h) * a.Tq;
+}
+__device__ __forceinline__ bool win_sees(int p, int j, int window, int sinks) { return j <= p && (p - j < window || j < sinks); }
+cudaError_t launch_win_simt(const WinArgs &a, gdn_dtype dt, cudaStream_t st);
+cudaError_t launch_win_delta(const void *dout, int64_t ld_dout, const void *o, const WinArgs &a, gdn_dtype dt, float *delta, cudaStream_t st);
+cudaError_t launch_win_dq_simt(const WinArgs &a, gdn_dtype dt, cudaStream_t st);
+cudaError_t launch_win_dkv_simt(const WinArgs &a, gdn_dtype dt, cudaStream_t st);
+
+struct WinStepArgs {
+    const void *q;              // [N][T][H][D], token stride ldq
+    int64_t ldq;
+    const void *k, *v;          // [N][S][HK][D] by strides
+    int64_t k_seq, k_tok, k_head, v_seq, v_tok, v_head;
+    const void *lengths;        // [N] int32 or int64
+    int lengths_64;
+    int N, T, S, H, HK, D, window, sinks;
+    float scale;
+    void *o;                    // [N][T][H][D]
+};
+cudaError_t launch_win_step(const WinStepArgs &a, gdn_dtype dt, cudaStream_t st);
+
+}  // namespace gdn

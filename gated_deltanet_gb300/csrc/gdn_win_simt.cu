@@ -1,0 +1,341 @@
+// Attention with a sliding window and sinks on the CUDA cores, forward and gradients: every type, any head size up to 256, any
+// alignment.  (bf16 heads of 64 and 128 on 16-byte boundaries take the tensor cores.)
+//
+// 16 x 16 threads over tiles of TILE queries by TILE keys in fp32, rows ty + 16 r and columns tx + 16 c of the scores per thread,
+// operands read 16 bytes at a time along the contraction.  The forward keeps a running maximum and sum per row (one pass over the
+// keys); the gradients recompute p = exp(scale s - lse).  dK and dV sum over every query head of a key head in the CTA that owns the
+// key tile, in a fixed order and without atomics.
+#include "gdn_mix.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr float kNegInf = -INFINITY;
+
+// TILE rows of D columns as fp32, zeros behind `rows` and D, at a stride of DP + 4
+template <typename T, int TILE, int DP>
+__device__ __forceinline__ void load_tile(float *dst, const T *src, int64_t ld, int rows, int D)
+{
+    for (int i = threadIdx.x; i < TILE * DP; i += kThreads) {
+        const int r = i / DP, c = i % DP;
+        dst[r * (DP + 4) + c] = r < rows && c < D ? to_f<T>(src[(int64_t)r * ld + c]) : 0.f;
+    }
+}
+
+// z[r][c] = sum_k A[ty + 16 r][k] B[tx + 16 c][k]
+template <int RT, int DP>
+__device__ __forceinline__ void dot_tile(float (*z)[RT], const float *A, const float *B, int D)
+{
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < RT; ++j) z[i][j] = 0.f;
+    for (int k = 0; k < D; k += 4) {
+        float4 u[RT], v[RT];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            u[i] = *(const float4 *)&A[(ty + 16 * i) * (DP + 4) + k];
+            v[i] = *(const float4 *)&B[(tx + 16 * i) * (DP + 4) + k];
+        }
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int j = 0; j < RT; ++j) z[i][j] += u[i].x * v[j].x + u[i].y * v[j].y + u[i].z * v[j].z + u[i].w * v[j].w;
+    }
+}
+
+// acc[r][4 m + e] += sum_j P[ty + 16 r][j] V[j][64 m + 4 tx + e]   (P at a stride of TILE + 4)
+template <int RT, int TILE, int DP>
+__device__ __forceinline__ void mul_tile(float (*acc)[DP / 16], const float *P, const float *V)
+{
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    for (int j = 0; j < TILE; j += 4) {
+        float p[RT][4];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) *(float4 *)p[i] = *(const float4 *)&P[(ty + 16 * i) * (TILE + 4) + j];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int m = 0; m < DP / 64; ++m) {
+                const float4 v = *(const float4 *)&V[(j + k) * (DP + 4) + 64 * m + 4 * tx];
+#pragma unroll
+                for (int i = 0; i < RT; ++i) {
+                    acc[i][4 * m] += p[i][k] * v.x;
+                    acc[i][4 * m + 1] += p[i][k] * v.y;
+                    acc[i][4 * m + 2] += p[i][k] * v.z;
+                    acc[i][4 * m + 3] += p[i][k] * v.w;
+                }
+            }
+    }
+}
+
+// rows ty + 16 r of acc to dst (token stride ld)
+template <typename T, int RT, int DP>
+__device__ __forceinline__ void store_tile(T *dst, int64_t ld, const float (*acc)[DP / 16], int rows, int D)
+{
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int e = 0; e < DP / 16; ++e) {
+            const int r = ty + 16 * i, c = 64 * (e >> 2) + 4 * tx + (e & 3);
+            if (r < rows && c < D) dst[(int64_t)r * ld + c] = from_f<T>(acc[i][e]);
+        }
+}
+
+__device__ __forceinline__ float row_max(float x)
+{
+#pragma unroll
+    for (int o = 8; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+}
+__device__ __forceinline__ float row_sum(float x)
+{
+#pragma unroll
+    for (int o = 8; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// The keys that queries at positions p0 .. p1 (inclusive) may see: [0, first) of the sinks, then [lo, hi)
+struct Keys {
+    int first, lo, hi;
+};
+__device__ __forceinline__ Keys keys_of(int p0, int p1, int window, int sinks)
+{
+    Keys k;
+    k.hi = max(p1 + 1, 0);
+    k.lo = min(max(p0 - window + 1, 0), k.hi);
+    k.first = min(sinks, k.lo);
+    return k;
+}
+
+template <typename T, int TILE, int DP>
+__global__ void __launch_bounds__(kThreads) win_fwd_kernel(const WinArgs a)
+{
+    constexpr int RT = TILE / 16;
+    extern __shared__ float4 win_smem[];
+    float *Q = (float *)win_smem, *KV = Q + TILE * (DP + 4), *P = KV + TILE * (DP + 4);
+    const Tile tl = tile_of(a.cu_q, a.N, a.Tq, TILE, blockIdx.x);
+    const SeqRange sq = seq_range(a.cu_q, tl.n, a.Tq), sk = seq_range(a.cu_k, tl.n, a.Tk);
+    const int i0 = tl.index * TILE, rows = min(TILE, sq.len - i0), h = blockIdx.y, hk = h / (a.H / a.HK);
+    if (rows <= 0) return;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, p0 = i0 + sk.len - sq.len;
+    const float c = a.scale * kLog2e;
+    load_tile<T, TILE, DP>(Q, (const T *)a.q + (sq.bos + i0) * a.ldq + (int64_t)h * a.D, a.ldq, rows, a.D);
+
+    float acc[RT][DP / 16] = {}, top[RT], total[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) top[i] = kNegInf, total[i] = 0.f;
+    const Keys ks = keys_of(p0, p0 + rows - 1, a.window, a.sinks);
+    const int nfirst = (ks.first + TILE - 1) / TILE, ntiles = nfirst + (ks.hi - ks.lo + TILE - 1) / TILE;
+    for (int t = 0; t < ntiles; ++t) {
+        const int j0 = t < nfirst ? t * TILE : ks.lo + (t - nfirst) * TILE, end = t < nfirst ? ks.first : ks.hi;
+        const int cols = min(TILE, end - j0);
+        __syncthreads();
+        load_tile<T, TILE, DP>(KV, (const T *)a.k + (sk.bos + j0) * a.ldk + (int64_t)hk * a.D, a.ldk, cols, a.D);
+        __syncthreads();
+        float z[RT][RT];
+        dot_tile<RT, DP>(z, Q, KV, a.D);
+        __syncthreads();
+        load_tile<T, TILE, DP>(KV, (const T *)a.v + (sk.bos + j0) * a.ldv + (int64_t)hk * a.D, a.ldv, cols, a.D);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            const int r = ty + 16 * i;
+            float m = top[i];
+#pragma unroll
+            for (int j = 0; j < RT; ++j) {
+                const int k = tx + 16 * j;
+                z[i][j] = k < cols && win_sees(p0 + r, j0 + k, a.window, a.sinks) ? z[i][j] * c : kNegInf;
+                m = fmaxf(m, z[i][j]);
+            }
+            m = row_max(m);
+            const float base = m == kNegInf ? 0.f : m, fix = exp2f(top[i] - base);
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < RT; ++j) {
+                const float e = exp2f(z[i][j] - base);
+                sum += e;
+                P[r * (TILE + 4) + tx + 16 * j] = e;
+            }
+            total[i] = total[i] * fix + row_sum(sum);
+            top[i] = m;
+#pragma unroll
+            for (int e = 0; e < DP / 16; ++e) acc[i][e] *= fix;
+        }
+        __syncthreads();
+        mul_tile<RT, TILE, DP>(acc, P, KV);
+    }
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+        const float inv = total[i] > 0.f ? 1.f / total[i] : total[i] == 0.f ? 0.f : total[i];  // (a NaN stays)
+#pragma unroll
+        for (int e = 0; e < DP / 16; ++e) acc[i][e] *= inv;
+        if (a.lse && tx == 0 && ty + 16 * i < rows)
+            a.lse[lse_at(a, tl.n, sq.bos, h) + i0 + ty + 16 * i] = total[i] == 0.f ? kNegInf : (top[i] + log2f(total[i])) * 0.69314718055994531f;
+    }
+    store_tile<T, RT, DP>((T *)a.o + ((sq.bos + i0) * a.H + h) * a.D, (int64_t)a.H * a.D, acc, rows, a.D);
+}
+
+// delta = sum over the head of dO o, one warp per (token, head)
+template <typename T>
+__global__ void __launch_bounds__(kThreads) win_delta_kernel(const T *dout, int64_t ld, const T *o, const WinArgs a, float *delta, int64_t rows)
+{
+    const int64_t w = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
+    if (w >= rows) return;
+    const int lane = threadIdx.x & 31, h = (int)(w % a.H);
+    const int64_t t = w / a.H;
+    const T *x = dout + t * ld + (int64_t)h * a.D, *y = o + w * a.D;
+    float s = 0.f;
+    for (int d = lane; d < a.D; d += 32) s = fmaf(to_f<T>(x[d]), to_f<T>(y[d]), s);
+#pragma unroll
+    for (int k = 16; k; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+    const int64_t n = a.cu_q ? 0 : t / a.Tq;
+    if (lane == 0) delta[lse_at(a, (int)n, a.cu_q ? t : 0, h) + (a.cu_q ? 0 : t - n * a.Tq)] = s;
+}
+
+template <typename T, int TILE, int DP>
+__global__ void __launch_bounds__(kThreads) win_dq_kernel(const WinArgs a)
+{
+    constexpr int RT = TILE / 16, ROW = TILE * (DP + 4);
+    extern __shared__ float4 win_smem[];
+    float *Q = (float *)win_smem, *G = Q + ROW, *K = G + ROW, *V = K + ROW, *P = V + ROW;
+    const Tile tl = tile_of(a.cu_q, a.N, a.Tq, TILE, blockIdx.x);
+    const SeqRange sq = seq_range(a.cu_q, tl.n, a.Tq), sk = seq_range(a.cu_k, tl.n, a.Tk);
+    const int i0 = tl.index * TILE, rows = min(TILE, sq.len - i0), h = blockIdx.y, hk = h / (a.H / a.HK);
+    if (rows <= 0) return;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, p0 = i0 + sk.len - sq.len;
+    load_tile<T, TILE, DP>(Q, (const T *)a.q + (sq.bos + i0) * a.ldq + (int64_t)h * a.D, a.ldq, rows, a.D);
+    load_tile<T, TILE, DP>(G, (const T *)a.dout + (sq.bos + i0) * a.ld_dout + (int64_t)h * a.D, a.ld_dout, rows, a.D);
+    float lse[RT], delta[RT], acc[RT][DP / 16] = {};
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+        const int r = ty + 16 * i;
+        const int64_t at = lse_at(a, tl.n, sq.bos, h) + i0 + r;
+        lse[i] = r < rows ? a.lse[at] * kLog2e : 0.f;
+        delta[i] = r < rows ? a.delta[at] : 0.f;
+    }
+    const Keys ks = keys_of(p0, p0 + rows - 1, a.window, a.sinks);
+    const int nfirst = (ks.first + TILE - 1) / TILE, ntiles = nfirst + (ks.hi - ks.lo + TILE - 1) / TILE;
+    for (int t = 0; t < ntiles; ++t) {
+        const int j0 = t < nfirst ? t * TILE : ks.lo + (t - nfirst) * TILE, end = t < nfirst ? ks.first : ks.hi;
+        const int cols = min(TILE, end - j0);
+        __syncthreads();
+        load_tile<T, TILE, DP>(K, (const T *)a.k + (sk.bos + j0) * a.ldk + (int64_t)hk * a.D, a.ldk, cols, a.D);
+        load_tile<T, TILE, DP>(V, (const T *)a.v + (sk.bos + j0) * a.ldv + (int64_t)hk * a.D, a.ldv, cols, a.D);
+        __syncthreads();
+        float z[RT][RT], dp[RT][RT];
+        dot_tile<RT, DP>(z, Q, K, a.D);
+        dot_tile<RT, DP>(dp, G, V, a.D);
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int j = 0; j < RT; ++j) {
+                const int r = ty + 16 * i, k = tx + 16 * j;
+                const bool seen = r < rows && k < cols && win_sees(p0 + r, j0 + k, a.window, a.sinks);
+                P[r * (TILE + 4) + k] = seen ? exp2f(z[i][j] * (a.scale * kLog2e) - lse[i]) * (dp[i][j] - delta[i]) * a.scale : 0.f;
+            }
+        __syncthreads();
+        mul_tile<RT, TILE, DP>(acc, P, K);
+    }
+    store_tile<T, RT, DP>((T *)a.dq + ((sq.bos + i0) * a.H + h) * a.D, (int64_t)a.H * a.D, acc, rows, a.D);
+}
+
+template <typename T, int TILE, int DP>
+__global__ void __launch_bounds__(kThreads) win_dkv_kernel(const WinArgs a)
+{
+    constexpr int RT = TILE / 16, ROW = TILE * (DP + 4);
+    extern __shared__ float4 win_smem[];
+    float *K = (float *)win_smem, *V = K + ROW, *Q = V + ROW, *G = Q + ROW, *P = G + ROW, *Z = P + TILE * (TILE + 4);
+    const Tile tl = tile_of(a.cu_k, a.N, a.Tk, TILE, blockIdx.x);
+    const SeqRange sq = seq_range(a.cu_q, tl.n, a.Tq), sk = seq_range(a.cu_k, tl.n, a.Tk);
+    const int j0 = tl.index * TILE, cols = min(TILE, sk.len - j0), hk = blockIdx.y, G_ = a.H / a.HK;
+    if (cols <= 0) return;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, off = sk.len - sq.len;
+    load_tile<T, TILE, DP>(K, (const T *)a.k + (sk.bos + j0) * a.ldk + (int64_t)hk * a.D, a.ldk, cols, a.D);
+    load_tile<T, TILE, DP>(V, (const T *)a.v + (sk.bos + j0) * a.ldv + (int64_t)hk * a.D, a.ldv, cols, a.D);
+    float dk[RT][DP / 16] = {}, dv[RT][DP / 16] = {};
+    // queries from the first that reaches key j0 to the last that sees any key of the tile
+    const int begin = max(0, j0 - off);
+    const int end = j0 < a.sinks ? sq.len : (int)min((int64_t)sq.len, (int64_t)j0 + cols - 1 + a.window - off);
+    for (int g = 0; g < G_; ++g) {
+        const int h = hk * G_ + g;
+        for (int i0 = begin; i0 < end; i0 += TILE) {
+            const int rows = min(TILE, end - i0);
+            __syncthreads();
+            load_tile<T, TILE, DP>(Q, (const T *)a.q + (sq.bos + i0) * a.ldq + (int64_t)h * a.D, a.ldq, rows, a.D);
+            load_tile<T, TILE, DP>(G, (const T *)a.dout + (sq.bos + i0) * a.ld_dout + (int64_t)h * a.D, a.ld_dout, rows, a.D);
+            __syncthreads();
+            float z[RT][RT], dp[RT][RT];  // [key][query]
+            dot_tile<RT, DP>(z, K, Q, a.D);
+            dot_tile<RT, DP>(dp, V, G, a.D);
+#pragma unroll
+            for (int j = 0; j < RT; ++j) {
+                const int i = tx + 16 * j;
+                const int64_t at = lse_at(a, tl.n, sq.bos, h) + i0 + i;
+                const float lse = i < rows ? a.lse[at] * kLog2e : 0.f, delta = i < rows ? a.delta[at] : 0.f;
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    const int k = ty + 16 * r;
+                    const bool seen = i < rows && k < cols && win_sees(i0 + i + off, j0 + k, a.window, a.sinks);
+                    const float p = seen ? exp2f(z[r][j] * (a.scale * kLog2e) - lse) : 0.f;
+                    P[k * (TILE + 4) + i] = p;
+                    Z[k * (TILE + 4) + i] = seen ? p * (dp[r][j] - delta) * a.scale : 0.f;
+                }
+            }
+            __syncthreads();
+            mul_tile<RT, TILE, DP>(dv, P, G);
+            mul_tile<RT, TILE, DP>(dk, Z, Q);
+        }
+    }
+    store_tile<T, RT, DP>((T *)a.dk + ((sk.bos + j0) * a.HK + hk) * a.D, (int64_t)a.HK * a.D, dk, cols, a.D);
+    store_tile<T, RT, DP>((T *)a.dv + ((sk.bos + j0) * a.HK + hk) * a.D, (int64_t)a.HK * a.D, dv, cols, a.D);
+}
+
+enum Which { kFwd, kDq, kDkv };
+
+template <typename T, int TILE, int DP>
+cudaError_t launch_tiles(const WinArgs &a, Which what, cudaStream_t st)
+{
+    auto kern = what == kFwd ? win_fwd_kernel<T, TILE, DP> : what == kDq ? win_dq_kernel<T, TILE, DP> : win_dkv_kernel<T, TILE, DP>;
+    const size_t row = TILE * (DP + 4) * 4, p = TILE * (TILE + 4) * 4;
+    const size_t smem = what == kFwd ? 2 * row + p : what == kDq ? 4 * row + p : 4 * row + 2 * p;
+    static std::atomic<uint64_t> seen[3];
+    if (first_on_device(seen[what])) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        done_on_device(seen[what]);
+    }
+    const int64_t tiles = what == kDkv ? mix_slots(a.cu_k, a.N, a.Tk, TILE) : mix_slots(a.cu_q, a.N, a.Tq, TILE);
+    if (tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
+    if (tiles == 0) return cudaSuccess;
+    kern<<<dim3((unsigned)tiles, what == kDkv ? a.HK : a.H), kThreads, smem, st>>>(a);
+    return cudaGetLastError();
+}
+template <typename T>
+cudaError_t launch_typed(const WinArgs &a, Which what, cudaStream_t st)
+{
+    return a.D <= 64 ? launch_tiles<T, 64, 64>(a, what, st) : a.D <= 128 ? launch_tiles<T, 64, 128>(a, what, st) : launch_tiles<T, 32, 256>(a, what, st);
+}
+cudaError_t launch_any(const WinArgs &a, gdn_dtype dt, Which what, cudaStream_t st)
+{
+    return dt == GDN_F32 ? launch_typed<float>(a, what, st) : launch_typed<__nv_bfloat16>(a, what, st);
+}
+
+}  // namespace
+
+cudaError_t launch_win_simt(const WinArgs &a, gdn_dtype dt, cudaStream_t st) { return launch_any(a, dt, kFwd, st); }
+cudaError_t launch_win_dq_simt(const WinArgs &a, gdn_dtype dt, cudaStream_t st) { return launch_any(a, dt, kDq, st); }
+cudaError_t launch_win_dkv_simt(const WinArgs &a, gdn_dtype dt, cudaStream_t st) { return launch_any(a, dt, kDkv, st); }
+
+cudaError_t launch_win_delta(const void *dout, int64_t ld, const void *o, const WinArgs &a, gdn_dtype dt, float *delta, cudaStream_t st)
+{
+    const int64_t rows = (a.cu_q ? (int64_t)a.Tq : (int64_t)a.N * a.Tq) * a.H, blocks = (rows * 32 + kThreads - 1) / kThreads;
+    if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+    if (dt == GDN_F32) win_delta_kernel<float><<<(unsigned)blocks, kThreads, 0, st>>>((const float *)dout, ld, (const float *)o, a, delta, rows);
+    else win_delta_kernel<__nv_bfloat16><<<(unsigned)blocks, kThreads, 0, st>>>((const __nv_bfloat16 *)dout, ld, (const __nv_bfloat16 *)o, a, delta, rows);
+    return cudaGetLastError();
+}
+
+}  // namespace gdn

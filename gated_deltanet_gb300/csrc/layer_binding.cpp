@@ -1,5 +1,6 @@
 // Python binding of the decoder-block operators (gdn_rms_norm, gdn_linear, gdn_gated_linear and their
-// gradients): checks and marshals PyTorch tensors.
+// gradients) and of the token mixers beside the gated delta rule (gdn_linear_attn, gdn_window_attn, theirs):
+// checks and marshals PyTorch tensors.
 //
 // The calls of a decoding step run for a few microseconds on the GPU, and marshalling twenty fields from Python
 // cost more than that (10 to 19 us a call through ctypes), so this part of the binding is compiled.  Outputs
@@ -12,6 +13,8 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <array>
+#include <cmath>
 #include <string>
 
 #include "../../include/gdn.h"
@@ -465,6 +468,282 @@ PyObject *gated_linear_bwd(PyObject *const *p)
     return tuple_of(dx, dw, y);
 }
 
+// ---------------------------------------------------------------- token mixers
+// A tensor [B, T, heads, size] whose tokens are evenly spaced with consecutive heads and elements (a slice of a fused
+// projection), else a contiguous copy; ld: elements from a token to the next.
+struct Tokens {
+    Tensor t;
+    int64_t ld = 0;
+    void *ptr() const { return t.data_ptr(); }
+};
+Tokens tokens(const Tensor &t)
+{
+    const int64_t B = t.size(0), T = t.size(1), h = t.size(2), d = t.size(3);
+    if (t.is_contiguous()) return {t, h * d};
+    const int64_t ld = T > 1 ? t.stride(1) : B > 1 ? t.stride(0) : h * d;
+    if ((d == 1 || t.stride(3) == 1) && (h == 1 || t.stride(2) == d) && ld >= h * d && (B == 1 || t.stride(0) == T * ld)) return {t, ld};
+    return {t.contiguous(), h * d};
+}
+
+void four(const char *name, const Tensor &t, const Tensor *with = nullptr)
+{
+    cuda(name, t, with);
+    if (with && t.scalar_type() != with->scalar_type()) bad_type(std::string(name) + " and q must share a dtype");
+    if (t.dim() != 4) bad_value(std::string(name) + " must have four dimensions, got shape " + shape_of(t));
+    if (t.size(0) > INT32_MAX || t.size(1) > INT32_MAX || t.size(2) > INT32_MAX || t.size(3) > INT32_MAX) bad_value(std::string(name) + " is too large");
+}
+void same_shape(const char *name, const Tensor &t, at::IntArrayRef shape)
+{
+    if (t.sizes() != shape) bad_value(std::string(name) + " has an unexpected shape " + shape_of(t));
+}
+
+// [N + 1] offsets of packed sequences
+Tensor offsets(const char *name, const Tensor &t, const Tensor &with, int64_t batch)
+{
+    cuda(name, t, &with);
+    if (t.scalar_type() != at::kLong) bad_type(std::string(name) + " must be int64");
+    if (t.dim() != 1 || t.size(0) < 1) bad_value(std::string(name) + " must be [N + 1]");
+    if (t.size(0) - 1 > INT32_MAX) bad_value(std::string(name) + " is too long");
+    if (batch != 1) bad_value("packed input has a batch of 1");
+    return t.contiguous();
+}
+
+struct Linear {
+    gdn_linear_attn_args a{};
+    Tokens q, k, v;
+    Tensor decay, h0, cu;
+};
+// (a state [N, HV, K, V]; `out`: to be written, so as it is)
+Tensor state(const char *name, const Tensor &t, const Tensor &with, at::IntArrayRef shape, bool out = false)
+{
+    cuda(name, t, &with);
+    if (t.scalar_type() != at::kFloat) bad_type(std::string(name) + " must be float32");
+    if (t.sizes() != shape) bad_value(std::string(name) + " must be [N, HV, K, V], got shape " + shape_of(t));
+    if (out && !t.is_contiguous()) bad_value(std::string(name) + " must be contiguous");
+    return t.contiguous();
+}
+std::array<int64_t, 4> state_shape(const gdn_linear_attn_args &a) { return {a.num_seqs, a.HV, a.K, a.V}; }
+
+void linear_inputs(Linear &l, const Tensor &q, const Tensor &k, const Tensor &v, const Tensor *decay, PyObject *scale, const Tensor *h0, const Tensor *cu)
+{
+    four("q", q);
+    need_real("q", q);
+    four("k", k, &q);
+    four("v", v, &q);
+    same_shape("k", k, q.sizes());
+    if (v.size(0) != q.size(0) || v.size(1) != q.size(1)) bad_value("v must have q's batch and tokens, got shape " + shape_of(v));
+    if (q.size(2) < 1 || v.size(2) < 1 || v.size(2) % q.size(2)) bad_value("the heads of v must be a multiple of those of q");
+    if (q.size(3) < 1 || v.size(3) < 1) bad_value("heads must have at least one element");
+    gdn_linear_attn_args &a = l.a;
+    a.B = (int)q.size(0); a.T = (int)q.size(1); a.H = (int)q.size(2); a.K = (int)q.size(3);
+    a.HV = (int)v.size(2); a.V = (int)v.size(3);
+    a.dtype = code_of(q);
+    l.q = tokens(q); l.k = tokens(k); l.v = tokens(v);
+    a.q = l.q.ptr(); a.k = l.k.ptr(); a.v = l.v.ptr();
+    a.ldq = l.q.ld; a.ldk = l.k.ld; a.ldv = l.v.ld;
+    a.num_seqs = a.B;
+    if (cu) {
+        l.cu = offsets("cu_seqlens", *cu, q, q.size(0));
+        a.cu_seqlens = l.cu.data_ptr<int64_t>();
+        a.num_seqs = (int)(l.cu.size(0) - 1);
+    }
+    if (decay) {
+        l.decay = vec("decay", *decay, a.HV, q, false);
+        a.decay = l.decay.data_ptr<float>();
+    }
+    a.scale = scale == Py_None ? 1.f / std::sqrt((float)a.K) : (float)number(scale);
+    if (h0) {
+        l.h0 = state("initial_state", *h0, q, state_shape(a));
+        a.h0 = l.h0.data_ptr<float>();
+    }
+}
+
+// (q, k, v, decay, scale, initial_state, output_final_state, cu_seqlens, out, final_state, recurrent) -> (o, ht)
+PyObject *linear_attn(PyObject *const *p)
+{
+    const Tensor &q = *tensor("q", p[0]), &k = *tensor("k", p[1]), &v = *tensor("v", p[2]);
+    const Tensor *decay = tensor("decay", p[3], true), *h0 = tensor("initial_state", p[5], true), *cu = tensor("cu_seqlens", p[7], true);
+    const Tensor *out = tensor("out", p[8], true), *fin = tensor("final_state", p[9], true);
+    const bool want = truth(p[6]), recurrent = truth(p[10]);
+    if (fin && !want) bad_value("final_state goes with output_final_state");
+    cuda("q", q);
+    const c10::cuda::CUDAGuard guard(q.device());
+    Linear l;
+    linear_inputs(l, q, k, v, decay, p[4], h0, cu);
+    const Tensor o = output("out", out, v.sizes(), v.scalar_type(), q);
+    l.a.o = o.data_ptr();
+    Tensor ht;
+    if (want) {
+        ht = fin ? state("final_state", *fin, q, state_shape(l.a), true) : fresh(state_shape(l.a), at::kFloat, q);
+        l.a.ht = ht.data_ptr<float>();
+    }
+    if (recurrent) checked(gdn_linear_attn_recurrent(&l.a, stream_of(q)), "gdn_linear_attn_recurrent");
+    else launch(gdn_linear_attn, gdn_linear_attn_workspace_size, l.a, q, "gdn_linear_attn");
+    return tuple_of(o, ht);
+}
+
+// (q, k, v, decay, do, scale, initial_state, dht, cu_seqlens) -> (dq, dk, dv, dh0)
+PyObject *linear_attn_bwd(PyObject *const *p)
+{
+    const Tensor &q = *tensor("q", p[0]), &k = *tensor("k", p[1]), &v = *tensor("v", p[2]), &dout = *tensor("do", p[4]);
+    const Tensor *decay = tensor("decay", p[3], true), *h0 = tensor("initial_state", p[6], true), *dht = tensor("dht", p[7], true);
+    cuda("q", q);
+    const c10::cuda::CUDAGuard guard(q.device());
+    Linear l;
+    linear_inputs(l, q, k, v, decay, p[5], h0, tensor("cu_seqlens", p[8], true));
+    four("do", dout, &q);
+    same_shape("do", dout, v.sizes());
+    const Tokens d = tokens(dout);
+    l.a.dout = d.ptr();
+    l.a.ld_dout = d.ld;
+    Tensor dhtv, dh0;
+    if (dht) {
+        dhtv = state("dht", *dht, q, state_shape(l.a));
+        l.a.dht = dhtv.data_ptr<float>();
+    }
+    const Tensor dq = fresh(q.sizes(), q.scalar_type(), q), dk = fresh(k.sizes(), q.scalar_type(), q), dv = fresh(v.sizes(), q.scalar_type(), q);
+    l.a.dq = dq.data_ptr(); l.a.dk = dk.data_ptr(); l.a.dv = dv.data_ptr();
+    if (h0) {
+        dh0 = fresh(state_shape(l.a), at::kFloat, q);
+        l.a.dh0 = dh0.data_ptr<float>();
+    }
+    launch(gdn_linear_attn_bwd, gdn_linear_attn_bwd_workspace_size, l.a, q, "gdn_linear_attn_bwd");
+    return tuple_of(dq, dk, dv, dh0);
+}
+
+struct Window {
+    gdn_window_attn_args a{};
+    Tokens q, k, v;
+    Tensor cu_q, cu_k;
+};
+// window and sinks as the C entries take them (nothing is longer than 2^31 - 1 tokens)
+int count(const char *name, PyObject *o, int64_t least)
+{
+    const int64_t n = integer(o);
+    if (n < least) bad_value(std::string(name) + " must be at least " + std::to_string(least));
+    return (int)std::min<int64_t>(n, INT32_MAX);
+}
+void window_inputs(Window &w, const Tensor &q, const Tensor &k, const Tensor &v, PyObject *window, PyObject *sinks, PyObject *scale, const Tensor *cu,
+                   const Tensor *cu_k)
+{
+    four("q", q);
+    need_real("q", q);
+    four("k", k, &q);
+    four("v", v, &q);
+    same_shape("v", v, k.sizes());
+    if (k.size(0) != q.size(0) || k.size(3) != q.size(3)) bad_value("k must have q's batch and head size, got shape " + shape_of(k));
+    if (q.size(2) < 1 || k.size(2) < 1 || q.size(2) % k.size(2)) bad_value("the heads of q must be a multiple of those of k");
+    if (q.size(3) < 1) bad_value("heads must have at least one element");
+    if (cu_k && !cu) bad_value("cu_seqlens_k goes with cu_seqlens");
+    if (cu && !cu_k && k.size(1) != q.size(1)) bad_value("keys of other lengths than the queries need cu_seqlens_k");
+    gdn_window_attn_args &a = w.a;
+    a.B = (int)q.size(0); a.Tq = (int)q.size(1); a.Tk = (int)k.size(1); a.H = (int)q.size(2); a.HK = (int)k.size(2); a.D = (int)q.size(3);
+    a.dtype = code_of(q);
+    a.window = count("window", window, 1);
+    a.sinks = count("sinks", sinks, 0);
+    a.scale = scale == Py_None ? 1.f / std::sqrt((float)a.D) : (float)number(scale);
+    w.q = tokens(q); w.k = tokens(k); w.v = tokens(v);
+    a.q = w.q.ptr(); a.k = w.k.ptr(); a.v = w.v.ptr();
+    a.ldq = w.q.ld; a.ldk = w.k.ld; a.ldv = w.v.ld;
+    a.num_seqs = a.B;
+    if (cu) {
+        w.cu_q = offsets("cu_seqlens", *cu, q, q.size(0));
+        w.cu_k = cu_k ? offsets("cu_seqlens_k", *cu_k, q, q.size(0)) : w.cu_q;
+        if (w.cu_k.size(0) != w.cu_q.size(0)) bad_value("cu_seqlens and cu_seqlens_k must have one length");
+        a.cu_seqlens_q = w.cu_q.data_ptr<int64_t>();
+        a.cu_seqlens_k = w.cu_k.data_ptr<int64_t>();
+        a.num_seqs = (int)(w.cu_q.size(0) - 1);
+    }
+}
+
+// (q, k, v, window, sinks, scale, cu_seqlens, cu_seqlens_k, return_lse, out) -> (o, lse)
+PyObject *window_attn(PyObject *const *p)
+{
+    const Tensor &q = *tensor("q", p[0]), &k = *tensor("k", p[1]), &v = *tensor("v", p[2]);
+    cuda("q", q);
+    const c10::cuda::CUDAGuard guard(q.device());
+    Window w;
+    window_inputs(w, q, k, v, p[3], p[4], p[5], tensor("cu_seqlens", p[6], true), tensor("cu_seqlens_k", p[7], true));
+    const Tensor o = output("out", tensor("out", p[9], true), q.sizes(), q.scalar_type(), q);
+    w.a.o = o.data_ptr();
+    Tensor lse;
+    if (truth(p[8])) {
+        lse = fresh({q.size(0), q.size(2), q.size(1)}, at::kFloat, q);
+        w.a.lse = lse.data_ptr<float>();
+    }
+    launch(gdn_window_attn, gdn_window_attn_workspace_size, w.a, q, "gdn_window_attn");
+    return tuple_of(o, lse);
+}
+
+// (do, q, k, v, o, lse, window, sinks, scale, cu_seqlens, cu_seqlens_k) -> (dq, dk, dv)
+PyObject *window_attn_bwd(PyObject *const *p)
+{
+    const Tensor &dout = *tensor("do", p[0]), &q = *tensor("q", p[1]), &k = *tensor("k", p[2]), &v = *tensor("v", p[3]), &o = *tensor("o", p[4]),
+                 &lse = *tensor("lse", p[5]);
+    cuda("q", q);
+    const c10::cuda::CUDAGuard guard(q.device());
+    Window w;
+    window_inputs(w, q, k, v, p[6], p[7], p[8], tensor("cu_seqlens", p[9], true), tensor("cu_seqlens_k", p[10], true));
+    four("do", dout, &q);
+    four("o", o, &q);
+    same_shape("do", dout, q.sizes());
+    same_shape("o", o, q.sizes());
+    cuda("lse", lse, &q);
+    if (lse.scalar_type() != at::kFloat) bad_type("lse must be float32");
+    const int64_t stats[] = {q.size(0), q.size(2), q.size(1)};
+    same_shape("lse", lse, stats);
+    const Tokens d = tokens(dout);
+    const Tensor oc = o.contiguous(), lc = lse.contiguous();
+    w.a.dout = d.ptr();
+    w.a.ld_dout = d.ld;
+    w.a.o = oc.data_ptr();
+    w.a.lse = lc.data_ptr<float>();
+    const Tensor dq = fresh(q.sizes(), q.scalar_type(), q), dk = fresh(k.sizes(), q.scalar_type(), q), dv = fresh(v.sizes(), q.scalar_type(), q);
+    w.a.dq = dq.data_ptr(); w.a.dk = dk.data_ptr(); w.a.dv = dv.data_ptr();
+    launch(gdn_window_attn_bwd, gdn_window_attn_bwd_workspace_size, w.a, q, "gdn_window_attn_bwd");
+    return tuple_of(dq, dk, dv);
+}
+
+// (q, k_cache, v_cache, lengths, window, sinks, scale, out) -> o
+PyObject *window_attn_decode(PyObject *const *p)
+{
+    const Tensor &q = *tensor("q", p[0]), &k = *tensor("k_cache", p[1]), &v = *tensor("v_cache", p[2]), &len = *tensor("lengths", p[3]);
+    cuda("q", q);
+    const c10::cuda::CUDAGuard guard(q.device());
+    four("q", q);
+    need_real("q", q);
+    four("k_cache", k, &q);
+    four("v_cache", v, &q);
+    same_shape("v_cache", v, k.sizes());
+    if (k.size(0) != q.size(0) || k.size(3) != q.size(3)) bad_value("k_cache must have q's batch and head size, got shape " + shape_of(k));
+    if (q.size(2) < 1 || k.size(2) < 1 || q.size(2) % k.size(2)) bad_value("the heads of q must be a multiple of those of k_cache");
+    if (q.size(3) < 1) bad_value("heads must have at least one element");
+    // a cache is never copied: a call reads a window of it
+    for (const auto &c : {std::make_pair("k_cache", &k), std::make_pair("v_cache", &v)})
+        if (c.second->size(3) > 1 && c.second->stride(3) != 1) bad_value(std::string(c.first) + " must have consecutive elements in a head");
+    cuda("lengths", len, &q);
+    if (len.scalar_type() != at::kInt && len.scalar_type() != at::kLong) bad_type("lengths must be int32 or int64");
+    if (len.dim() != 1 || len.size(0) != q.size(0)) bad_value("lengths must be [B], got shape " + shape_of(len));
+    const Tensor lc = len.contiguous();
+    const Tokens qt = tokens(q);
+    gdn_window_decode_args a{};
+    a.N = (int)q.size(0); a.T = (int)q.size(1); a.S = (int)k.size(1); a.H = (int)q.size(2); a.HK = (int)k.size(2); a.D = (int)q.size(3);
+    a.dtype = code_of(q);
+    a.window = count("window", p[4], 1);
+    a.sinks = count("sinks", p[5], 0);
+    a.scale = p[6] == Py_None ? 1.f / std::sqrt((float)a.D) : (float)number(p[6]);
+    a.q = qt.ptr(); a.ldq = qt.ld;
+    a.k = k.data_ptr(); a.v = v.data_ptr();
+    a.k_seq = k.stride(0); a.k_tok = k.stride(1); a.k_head = k.stride(2);
+    a.v_seq = v.stride(0); a.v_tok = v.stride(1); a.v_head = v.stride(2);
+    a.lengths = lc.data_ptr();
+    a.lengths_64 = lc.scalar_type() == at::kLong;
+    const Tensor o = output("out", tensor("out", p[7], true), q.sizes(), q.scalar_type(), q);
+    a.o = o.data_ptr();
+    launch(gdn_window_attn_decode, gdn_window_attn_decode_workspace_size, a, q, "gdn_window_attn_decode");
+    return wrap(o);
+}
+
 // (device index) -> status code
 PyObject *read_status(PyObject *const *p)
 {
@@ -513,6 +792,11 @@ PyMethodDef methods[] = {
     method<linear_bwd, 7>("linear_bwd"),
     method<gated_linear, 6>("gated_linear"),
     method<gated_linear_bwd, 7>("gated_linear_bwd"),
+    method<linear_attn, 11>("linear_attn"),
+    method<linear_attn_bwd, 9>("linear_attn_bwd"),
+    method<window_attn, 10>("window_attn"),
+    method<window_attn_bwd, 11>("window_attn_bwd"),
+    method<window_attn_decode, 8>("window_attn_decode"),
     method<read_status, 1>("read_status"),
     method<row_view, 2>("row_view"),
     method<set_error, 1>("set_error"),

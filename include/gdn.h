@@ -528,6 +528,139 @@ gdn_status gdn_read_layer_status(gdn_stream_t stream);
  * ones of up to 16 rows; other products run as ever. */
 void gdn_layer_test_withhold(int on);
 
+/* ------------------------------------------------------------------------
+ * Token mixers beside the gated delta rule: linear attention with a decay for
+ * each head, and softmax attention with a sliding window and a few first
+ * tokens that stay visible (sinks); their forms for single tokens and their
+ * gradients.  (No counterpart in the pages.)
+ *
+ *  - Layouts are the delta rule's: [B][T][heads][size], heads that share a
+ *    key head are neighbours (value head h reads key head h / (HV / H), query
+ *    head h key head h / (H / HK)), packed input by cu_seqlens (B = 1, T all
+ *    tokens).  Inputs take the distance from a token to the next in elements
+ *    (a slice of a fused projection): heads and elements of a token are
+ *    consecutive, the batch is T tokens apart.  Outputs are contiguous and
+ *    lie over no input, unless said at the field.
+ *  - Any alignment to the element.  bf16 heads of 64 or 128 (linear attention:
+ *    K = V) on 16-byte boundaries run on the tensor cores, everything else on
+ *    the CUDA cores.  Head sizes up to 256.
+ *  - Offsets in cu_seqlens are clamped to the tensor; tokens outside every
+ *    sequence are neither read nor written.
+ *  - Workspaces as for the decoder-block operators above (and
+ *    gdn_read_layer_status for device-side waits that ran out).
+ *  - Inputs are finite: a NaN or an infinity reaches, besides the outputs that
+ *    depend on it, others of the same sequence and tile of tokens (a product
+ *    with a weight of zero is NaN); it reaches no other sequence.
+ */
+typedef struct {
+    int B, T, H, HV, K, V;  /* packed: B = 1, T all tokens; K, V <= 256                  */
+    int num_seqs;           /* N: B, or len(cu_seqlens) - 1                              */
+    gdn_dtype dtype;        /* q, k, v, o, dout, dq, dk, dv: GDN_F32 or GDN_BF16         */
+    float scale;
+    const void *q, *k, *v;  /* [B][T][H][K], [B][T][H][K], [B][T][HV][V]                 */
+    int64_t ldq, ldk, ldv;  /* elements from a token to the next                         */
+    const float *decay;     /* [HV], natural logarithm (<= 0); nullable (no decay)       */
+    const float *h0;        /* [N][HV][K][V], nullable (zero)                            */
+    const int64_t *cu_seqlens;
+    void *o;                /* [B][T][HV][V]                                             */
+    float *ht;              /* [N][HV][K][V], nullable.  gdn_linear_attn_recurrent: may
+                               be h0 itself (the state updated in place)                 */
+    const void *dout;       /* backward: [B][T][HV][V]                                   */
+    int64_t ld_dout;
+    const float *dht;       /* backward: [N][HV][K][V], nullable (zero)                  */
+    void *dq, *dk, *dv;     /* backward: as q, k, v, contiguous                          */
+    float *dh0;             /* backward: [N][HV][K][V], nullable                         */
+} gdn_linear_attn_args;
+
+/*
+ * Linear attention with a decay for each value head:
+ *     S_t = exp(decay) S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t,
+ *     S_0 = h0,  ht = S_T
+ * in chunks of tokens: within a chunk the decayed products of q and k, between
+ * chunks the state, in fp32.  On the tensor cores the decayed products and the
+ * state are rounded to bf16 as operands of the output (not of the state).
+ * The decay is a constant of the layer: no gradient is computed for it.
+ */
+size_t gdn_linear_attn_workspace_size(const gdn_linear_attn_args *a);
+gdn_status gdn_linear_attn(const gdn_linear_attn_args *a, void *workspace, size_t ws_bytes, gdn_stream_t stream);
+
+/* The same token by token, for decoding and short continuations (fp32
+ * throughout; suited to a few tokens per sequence). */
+gdn_status gdn_linear_attn_recurrent(const gdn_linear_attn_args *a, gdn_stream_t stream);
+
+/*
+ * Gradients of gdn_linear_attn from its inputs, dout and dht.  With
+ * R_t = exp(decay) R_{t+1} + scale q_t dout_t^T, dht joining at the last token:
+ *     dq_t = scale S_t dout_t,  dk_t = R_t v_t,  dv_t = R_t^T k_t,
+ *     dh0 = exp(decay) R_1
+ * (key heads that several value heads share: the sum of theirs, in fp32, in a
+ * fixed order).
+ */
+size_t gdn_linear_attn_bwd_workspace_size(const gdn_linear_attn_args *a);
+gdn_status gdn_linear_attn_bwd(const gdn_linear_attn_args *a, void *workspace, size_t ws_bytes, gdn_stream_t stream);
+
+typedef struct {
+    int B, Tq, Tk, H, HK, D;  /* packed: B = 1, Tq and Tk all tokens; D <= 256           */
+    int num_seqs;
+    gdn_dtype dtype;          /* q, k, v, o and the gradients: GDN_F32 or GDN_BF16       */
+    int window;               /* >= 1: keys a query sees, its own among them             */
+    int sinks;                /* >= 0: first keys of the sequence that stay visible      */
+    float scale;
+    const void *q, *k, *v;    /* [B][Tq][H][D], [B][Tk][HK][D] twice                     */
+    int64_t ldq, ldk, ldv;
+    const int64_t *cu_seqlens_q, *cu_seqlens_k; /* [N + 1] both, or none                 */
+    void *o;                  /* [B][Tq][H][D] (backward: an input, contiguous)          */
+    float *lse;               /* [B][H][Tq], nullable (backward: an input)               */
+    const void *dout;         /* backward: [B][Tq][H][D]                                 */
+    int64_t ld_dout;
+    void *dq, *dk, *dv;       /* backward: as q, k, v, contiguous                        */
+} gdn_window_attn_args;
+
+/*
+ * Causal softmax attention with a sliding window and sinks.  Query i of a
+ * sequence of Lq queries and Lk keys stands at p = i + Lk - Lq and sees key j
+ * when j <= p and (p - j < window or j < sinks):
+ *     o_i = sum_j softmax_j(scale q_i . k_j) v_j
+ *     lse_i = log sum_j exp(scale q_i . k_j)
+ * A row that sees nothing (p < 0) gives zeros and lse = -infinity.  Scores,
+ * statistics and sums in fp32; on the tensor cores the weights exp(..) are
+ * rounded to bf16 as operands.
+ */
+size_t gdn_window_attn_workspace_size(const gdn_window_attn_args *a);
+gdn_status gdn_window_attn(const gdn_window_attn_args *a, void *workspace, size_t ws_bytes, gdn_stream_t stream);
+
+/*
+ * Gradients of gdn_window_attn from its inputs, o, lse and dout: with
+ * p = exp(scale s - lse), delta = dout . o and dz = p (dout v^T - delta) scale,
+ *     dq = dz k,  dk = dz^T q,  dv = p^T dout
+ * (summed over the query heads of a key head in fp32, in a fixed order).
+ */
+size_t gdn_window_attn_bwd_workspace_size(const gdn_window_attn_args *a);
+gdn_status gdn_window_attn_bwd(const gdn_window_attn_args *a, void *workspace, size_t ws_bytes, gdn_stream_t stream);
+
+typedef struct {
+    int N, T, S, H, HK, D;    /* sequences, new tokens each, cache slots each            */
+    gdn_dtype dtype;
+    int window, sinks;        /* as gdn_window_attn_args                                 */
+    float scale;
+    const void *q;            /* [N][T][H][D]                                            */
+    int64_t ldq;
+    const void *k, *v;        /* [N][S][HK][D], any strides, consecutive elements        */
+    int64_t k_seq, k_tok, k_head, v_seq, v_tok, v_head; /* strides in elements           */
+    const void *lengths;      /* [N]: slots filled, the new tokens among them            */
+    int lengths_64;           /* lengths are int64 (else int32)                          */
+    void *o;                  /* [N][T][H][D]                                            */
+} gdn_window_decode_args;
+
+/*
+ * gdn_window_attn for a few new tokens over a cache: new token t of sequence n
+ * stands at position lengths[n] - T + t.  Slots from lengths[n] on and slots
+ * outside the window and the sinks are not read.  Lengths are clamped to
+ * [0, S]; a row that sees nothing gives zeros.
+ */
+size_t gdn_window_attn_decode_workspace_size(const gdn_window_decode_args *a);
+gdn_status gdn_window_attn_decode(const gdn_window_decode_args *a, void *workspace, size_t ws_bytes, gdn_stream_t stream);
+
 /* Plan summary (host only, no GPU needed) -- what a call would launch: the
  * engine and the in-GPU split (FlashQLA blog, "A balanced solution", the CP
  * enable rule, re-derived for this GPU's SM count). */
