@@ -2,7 +2,7 @@
 // each call.
 #include <cmath>
 
-#include "gdn_layer.cuh"
+#include "gdn_mix.cuh"
 
 using namespace gdn;
 
@@ -475,8 +475,12 @@ gdn_status gdn_gated_linear_bwd(const gdn_linear_args *a, void *workspace, size_
 
 gdn_status gdn_read_layer_status(gdn_stream_t stream)
 {
-    const gdn_status many = read_tc_status((cudaStream_t)stream), few = read_small_status((cudaStream_t)stream);
-    return many != GDN_OK ? many : few;
+    // (each reads and clears its own)
+    const gdn_status all[] = {read_tc_status((cudaStream_t)stream), read_small_status((cudaStream_t)stream), read_lin_status((cudaStream_t)stream),
+                              read_win_status((cudaStream_t)stream)};
+    for (const gdn_status s : all)
+        if (s != GDN_OK) return s;
+    return GDN_OK;
 }
 
 void gdn_layer_test_withhold(int on) { withhold_loads() = on != 0; }

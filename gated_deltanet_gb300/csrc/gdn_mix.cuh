@@ -41,8 +41,8 @@ __device__ __forceinline__ Tile tile_of(const int64_t *cu, int N, int T, int til
         if (clamp64(cu[mid], 0, T) / tile + mid <= slot) lo = mid;
         else hi = mid - 1;
     }
-    const int64_t i = slot - (clamp64(cu[lo], 0, T) / tile + lo);
-    return {lo, (int)clamp64(i, 0, INT32_MAX / tile - 1)};
+    const int64_t i = slot - (clamp64(cu[lo], 0, T) / tile + lo), past = INT32_MAX / tile - 1;
+    return {lo, (int)(i < 0 || i > past ? past : i)};  // (slots in front of the first sequence are empty too)
 }
 
 // ---------------------------------------------------------------- linear attention
@@ -71,6 +71,19 @@ struct LinArgs {
     unsigned *status;
 };
 cudaError_t launch_lin_simt(const LinArgs &a, gdn_dtype dt, cudaStream_t st);
+// bf16, all sizes 64 or all 128, rows on 16-byte boundaries: on the tensor cores.  A plan splits sequences into segments where there
+// are few; then `bytes` of workspace.
+struct LinPlan {
+    size_t bytes;
+    int64_t slots;           // (sequence, segment) pairs
+    int tokens;              // of a segment
+};
+bool lin_tc_ok(const LinArgs &a, int64_t tokens);
+LinPlan lin_tc_plan(const LinArgs &a, int D);
+cudaError_t launch_lin_tc(const LinArgs &a, void *ws, int64_t tokens, cudaStream_t st);
+gdn_status read_lin_status(cudaStream_t st);
+// a TMA map over bf16 [tokens][heads][D], `ld` elements from a token to the next: boxes of 64 elements x 1 head x box_rows tokens
+bool heads_map(CUtensorMap *m, const void *base, int D, int heads, int64_t tokens, int64_t ld, int box_rows);
 // out[t][h][d] = sum over the r value heads of head h of part[t][h r + i][d], summed in order
 cudaError_t launch_lin_heads(const float *part, const LinArgs &a, int64_t tokens, int H, int r, int D, void *out, gdn_dtype dt, cudaStream_t st);
 
@@ -127,6 +140,10 @@ __host__ __device__ inline int64_t lse_at(const WinArgs &a, int n, int64_t bos, 
 }
 __device__ __forceinline__ bool win_sees(int p, int j, int window, int sinks) { return j <= p && (p - j < window || j < sinks); }
 cudaError_t launch_win_simt(const WinArgs &a, gdn_dtype dt, cudaStream_t st);
+// bf16 heads of 64 or 128, rows on 16-byte boundaries, a positive scale: on the tensor cores (tq, tk: all tokens)
+bool win_tc_ok(const WinArgs &a, int64_t tq, int64_t tk);
+cudaError_t launch_win_tc(const WinArgs &a, int64_t tq, int64_t tk, cudaStream_t st);
+gdn_status read_win_status(cudaStream_t st);
 cudaError_t launch_win_delta(const void *dout, int64_t ld_dout, const void *o, const WinArgs &a, gdn_dtype dt, float *delta, cudaStream_t st);
 cudaError_t launch_win_dq_simt(const WinArgs &a, gdn_dtype dt, cudaStream_t st);
 cudaError_t launch_win_dkv_simt(const WinArgs &a, gdn_dtype dt, cudaStream_t st);

@@ -41,7 +41,7 @@ gdn_status check_lin(const gdn_linear_attn_args *a, bool backward, bool recurren
     if (a->K > kMaxHead || a->V > kMaxHead) return GDN_ERR_UNSUPPORTED;
     if (a->cu_seqlens ? a->B != 1 : a->num_seqs != a->B) return GDN_ERR_INVALID;
     const int64_t tokens = (int64_t)a->B * a->T, qk = (int64_t)a->H * a->K, vo = (int64_t)a->HV * a->V;
-    if (qk > INT32_MAX || vo > INT32_MAX || (int64_t)a->num_seqs * a->HV > INT32_MAX / 8) return GDN_ERR_UNSUPPORTED;
+    if (qk > INT32_MAX || vo > INT32_MAX || a->T > INT32_MAX / 2 || (int64_t)a->num_seqs * a->HV > INT32_MAX / 8) return GDN_ERR_UNSUPPORTED;
     const size_t e = esize(a->dtype);
     if (tokens > 0 && (!a->q || !a->k || !a->v)) return GDN_ERR_INVALID;
     if (tokens > 1 && (a->ldq < qk || a->ldk < qk || a->ldv < vo)) return GDN_ERR_INVALID;
@@ -93,6 +93,12 @@ LinArgs lin_backward(const gdn_linear_attn_args *a, float *part)
     l.pass[1] = {a->v, a->dout, a->q, a->ldv, a->ld_dout, a->ldq, 1, 1, r, part ? (void *)(part + n) : a->dk, a->dht, nullptr, a->scale, 1.f, a->V, a->K, part != nullptr, 1, 1};
     l.pass[2] = {a->k, a->q, a->dout, a->ldk, a->ldq, a->ld_dout, r, r, 1, a->dv, a->dht, a->dh0, a->scale, 1.f, a->K, a->V, 0, 0, 1};
     return l;
+}
+bool lin_on_tc(const gdn_linear_attn_args *a, const LinArgs &l) { return a->dtype == GDN_BF16 && lin_tc_ok(l, (int64_t)a->B * a->T); }
+size_t lin_split_bytes(const gdn_linear_attn_args *a, const LinArgs &l) { return lin_on_tc(a, l) ? up256(lin_tc_plan(l, a->K).bytes) : 0; }
+cudaError_t run_lin(const gdn_linear_attn_args *a, const LinArgs &l, void *ws, cudaStream_t st)
+{
+    return lin_on_tc(a, l) ? launch_lin_tc(l, ws, (int64_t)a->B * a->T, st) : launch_lin_simt(l, a->dtype, st);
 }
 size_t lin_part_bytes(const gdn_linear_attn_args *a)
 {
@@ -177,15 +183,17 @@ extern "C" {
 
 size_t gdn_linear_attn_workspace_size(const gdn_linear_attn_args *a)
 {
-    (void)a;
-    return 0;
+    return check_lin(a, false, false) == GDN_OK && a->num_seqs > 0 ? lin_split_bytes(a, lin_forward(a)) : 0;
 }
 
-gdn_status gdn_linear_attn(const gdn_linear_attn_args *a, void *, size_t, gdn_stream_t stream)
+gdn_status gdn_linear_attn(const gdn_linear_attn_args *a, void *ws, size_t ws_bytes, gdn_stream_t stream)
 {
-    const gdn_status s = check_lin(a, false, false);
+    gdn_status s = check_lin(a, false, false);
     if (s != GDN_OK || a->num_seqs == 0) return s;
-    return of(launch_lin_simt(lin_forward(a), a->dtype, stream));
+    const LinArgs l = lin_forward(a);
+    char *base = nullptr;
+    if ((s = take_workspace(lin_split_bytes(a, l), ws, ws_bytes, stream, &base)) != GDN_OK) return s;
+    return of(run_lin(a, l, base, stream));
 }
 
 gdn_status gdn_linear_attn_recurrent(const gdn_linear_attn_args *a, gdn_stream_t stream)
@@ -204,7 +212,9 @@ gdn_status gdn_linear_attn_recurrent(const gdn_linear_attn_args *a, gdn_stream_t
 
 size_t gdn_linear_attn_bwd_workspace_size(const gdn_linear_attn_args *a)
 {
-    return check_lin(a, true, false) == GDN_OK ? lin_part_bytes(a) : 0;
+    if (check_lin(a, true, false) != GDN_OK || a->num_seqs == 0) return 0;
+    const size_t parts = lin_part_bytes(a);
+    return parts + lin_split_bytes(a, lin_backward(a, parts ? (float *)256 : nullptr));  // (parts are aligned wherever they lie)
 }
 
 gdn_status gdn_linear_attn_bwd(const gdn_linear_attn_args *a, void *ws, size_t ws_bytes, gdn_stream_t stream)
@@ -212,10 +222,11 @@ gdn_status gdn_linear_attn_bwd(const gdn_linear_attn_args *a, void *ws, size_t w
     gdn_status s = check_lin(a, true, false);
     if (s != GDN_OK || a->num_seqs == 0) return s;
     char *base = nullptr;
-    if ((s = take_workspace(lin_part_bytes(a), ws, ws_bytes, stream, &base)) != GDN_OK) return s;
-    float *part = (float *)base;
+    if ((s = take_workspace(gdn_linear_attn_bwd_workspace_size(a), ws, ws_bytes, stream, &base)) != GDN_OK) return s;
+    const size_t parts = lin_part_bytes(a);
+    float *const part = parts ? (float *)base : nullptr;
     const LinArgs l = lin_backward(a, part);
-    cudaError_t e = launch_lin_simt(l, a->dtype, stream);
+    cudaError_t e = run_lin(a, l, base + parts, stream);
     if (part && e == cudaSuccess) {
         const int64_t tokens = (int64_t)a->B * a->T;
         const int r = a->HV / a->H;
@@ -235,7 +246,10 @@ gdn_status gdn_window_attn(const gdn_window_attn_args *a, void *, size_t, gdn_st
 {
     const gdn_status s = check_win(a, false);
     if (s != GDN_OK || a->num_seqs == 0 || a->Tq == 0) return s;
-    return of(launch_win_simt(win_args(a), a->dtype, stream));
+    const WinArgs w = win_args(a);
+    const int64_t tq = (int64_t)a->B * a->Tq, tk = (int64_t)a->B * a->Tk;
+    if (tq == 0) return GDN_OK;
+    return of(a->dtype == GDN_BF16 && win_tc_ok(w, tq, tk) ? launch_win_tc(w, tq, tk, stream) : launch_win_simt(w, a->dtype, stream));
 }
 
 size_t gdn_window_attn_bwd_workspace_size(const gdn_window_attn_args *a)

@@ -334,34 +334,35 @@ def test_window_step_strided(gdn, dtype):
 
 
 # ---------------------------------------------------------------- together
-def test_untouched_rows(gdn):
+@pytest.mark.parametrize("at", [30, 1000])
+def test_untouched_rows(gdn, at):
     """Tokens in front of the first sequence and behind the last stay as they were (outputs given by the caller) and reach nothing, whatever they hold."""
     g = gen(40)
-    T, H, D = 500, 2, 128
-    cu = torch.tensor([30, 200, 333], device="cuda")
+    T, H, D = 470 + at, 2, 128
+    cu = torch.tensor([at, 170 + at, 303 + at], device="cuda")
     q, k, v = (randn(g, 1, T, H, D, dtype=BF) for _ in range(3))
     for t in (q, k, v):
-        t[:, :30], t[:, 333:] = torch.nan, torch.inf
-    cut = [t[:, 30:333].contiguous() for t in (q, k, v)]
+        t[:, :at], t[:, at + 303:] = torch.nan, torch.inf
+    cut = [t[:, at:at + 303].contiguous() for t in (q, k, v)]
     decay = torch.tensor([-0.1, -0.01], device="cuda")
     out = torch.full_like(q, 7.0)
     gdn.chunk_linear_attention(q, k, v, decay, cu_seqlens=cu, out=out)
-    want, _ = gdn.chunk_linear_attention(*cut, decay, cu_seqlens=cu - 30)
-    assert torch.equal(out[:, 30:333], want) and (out[:, :30] == 7).all() and (out[:, 333:] == 7).all()
+    want, _ = gdn.chunk_linear_attention(*cut, decay, cu_seqlens=cu - at)
+    assert torch.equal(out[:, at:at + 303], want) and (out[:, :at] == 7).all() and (out[:, at + 303:] == 7).all()
     out.fill_(7.0)
     gdn.window_attention(q, k, v, 50, 3, cu_seqlens=cu, out=out)
-    want = gdn.window_attention(*cut, 50, 3, cu_seqlens=cu - 30)
-    assert torch.equal(out[:, 30:333], want) and (out[:, :30] == 7).all() and (out[:, 333:] == 7).all()
+    want = gdn.window_attention(*cut, 50, 3, cu_seqlens=cu - at)
+    assert torch.equal(out[:, at:at + 303], want) and (out[:, :at] == 7).all() and (out[:, at + 303:] == 7).all()
     o, lse = gdn.window_attention(q, k, v, 50, 3, cu_seqlens=cu, return_lse=True)
     do = torch.randn_like(q)
     got = gdn.window_attention_bwd(do, q, k, v, o, lse, 50, 3, cu_seqlens=cu)
-    want = gdn.window_attention_bwd(do[:, 30:333].contiguous(), *cut, o[:, 30:333].contiguous(), lse[:, :, 30:333].contiguous(), 50, 3, cu_seqlens=cu - 30)
+    want = gdn.window_attention_bwd(do[:, at:at + 303].contiguous(), *cut, o[:, at:at + 303].contiguous(), lse[:, :, at:at + 303].contiguous(), 50, 3, cu_seqlens=cu - at)
     for a, b in zip(got, want):
-        assert torch.equal(a[:, 30:333], b)
+        assert torch.equal(a[:, at:at + 303], b)
     got = gdn.chunk_linear_attention_bwd(q, k, v, decay, do, cu_seqlens=cu)
-    want = gdn.chunk_linear_attention_bwd(*cut, decay, do[:, 30:333].contiguous(), cu_seqlens=cu - 30)
+    want = gdn.chunk_linear_attention_bwd(*cut, decay, do[:, at:at + 303].contiguous(), cu_seqlens=cu - at)
     for a, b in zip(got[:3], want[:3]):
-        assert torch.equal(a[:, 30:333], b)
+        assert torch.equal(a[:, at:at + 303], b)
 
 
 def test_neighbours_stay_apart(gdn):
