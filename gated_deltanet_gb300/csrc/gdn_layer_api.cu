@@ -477,7 +477,7 @@ gdn_status gdn_read_layer_status(gdn_stream_t stream)
 {
     // (each reads and clears its own)
     const gdn_status all[] = {read_tc_status((cudaStream_t)stream), read_small_status((cudaStream_t)stream), read_lin_status((cudaStream_t)stream),
-                              read_win_status((cudaStream_t)stream)};
+                              read_win_status((cudaStream_t)stream), read_win_bwd_status((cudaStream_t)stream)};
     for (const gdn_status s : all)
         if (s != GDN_OK) return s;
     return GDN_OK;

@@ -144,6 +144,10 @@ cudaError_t launch_win_simt(const WinArgs &a, gdn_dtype dt, cudaStream_t st);
 bool win_tc_ok(const WinArgs &a, int64_t tq, int64_t tk);
 cudaError_t launch_win_tc(const WinArgs &a, int64_t tq, int64_t tk, cudaStream_t st);
 gdn_status read_win_status(cudaStream_t st);
+bool win_bwd_tc_ok(const WinArgs &a, int64_t tq, int64_t tk);
+size_t win_bwd_tc_bytes(const WinArgs &a);  // of workspace, beside delta (which the call fills)
+cudaError_t launch_win_bwd_tc(const WinArgs &a, int64_t tq, int64_t tk, float *delta, void *ws, cudaStream_t st);
+gdn_status read_win_bwd_status(cudaStream_t st);
 cudaError_t launch_win_delta(const void *dout, int64_t ld_dout, const void *o, const WinArgs &a, gdn_dtype dt, float *delta, cudaStream_t st);
 cudaError_t launch_win_dq_simt(const WinArgs &a, gdn_dtype dt, cudaStream_t st);
 cudaError_t launch_win_dkv_simt(const WinArgs &a, gdn_dtype dt, cudaStream_t st);

@@ -152,6 +152,12 @@ WinArgs win_args(const gdn_window_attn_args *a)
     return w;
 }
 
+size_t win_delta_bytes(const gdn_window_attn_args *a) { return up256((size_t)a->B * a->Tq * a->H * sizeof(float)); }
+bool win_bwd_on_tc(const gdn_window_attn_args *a)
+{
+    return a->dtype == GDN_BF16 && win_bwd_tc_ok(win_args(a), (int64_t)a->B * a->Tq, (int64_t)a->B * a->Tk);
+}
+
 gdn_status check_step(const gdn_window_decode_args *a)
 {
     if (!a || a->N < 0 || a->T < 0 || a->S < 0 || a->H < 1 || a->HK < 1 || a->H % a->HK || a->D < 1) return GDN_ERR_INVALID;
@@ -254,7 +260,8 @@ gdn_status gdn_window_attn(const gdn_window_attn_args *a, void *, size_t, gdn_st
 
 size_t gdn_window_attn_bwd_workspace_size(const gdn_window_attn_args *a)
 {
-    return check_win(a, true) == GDN_OK ? up256((size_t)a->B * a->Tq * a->H * sizeof(float)) : 0;
+    if (check_win(a, true) != GDN_OK || a->num_seqs == 0) return 0;
+    return win_delta_bytes(a) + (win_bwd_on_tc(a) ? win_bwd_tc_bytes(win_args(a)) : 0);
 }
 
 gdn_status gdn_window_attn_bwd(const gdn_window_attn_args *a, void *ws, size_t ws_bytes, gdn_stream_t stream)
@@ -262,13 +269,16 @@ gdn_status gdn_window_attn_bwd(const gdn_window_attn_args *a, void *ws, size_t w
     gdn_status s = check_win(a, true);
     if (s != GDN_OK || a->num_seqs == 0) return s;
     char *base = nullptr;
-    if ((s = take_workspace(up256((size_t)a->B * a->Tq * a->H * sizeof(float)), ws, ws_bytes, stream, &base)) != GDN_OK) return s;
+    if ((s = take_workspace(gdn_window_attn_bwd_workspace_size(a), ws, ws_bytes, stream, &base)) != GDN_OK) return s;
     WinArgs w = win_args(a);
-    w.delta = (const float *)base;
+    float *const delta = (float *)base;
+    w.delta = delta;
+    const int64_t tq = (int64_t)a->B * a->Tq, tk = (int64_t)a->B * a->Tk;
+    if (win_bwd_on_tc(a)) return of(launch_win_bwd_tc(w, tq, tk, delta, base + win_delta_bytes(a), stream));
     cudaError_t e = cudaSuccess;
-    if (a->Tq > 0) e = launch_win_delta(a->dout, a->ld_dout, a->o, w, a->dtype, (float *)base, stream);
-    if (e == cudaSuccess && a->Tq > 0) e = launch_win_dq_simt(w, a->dtype, stream);
-    if (e == cudaSuccess && a->Tk > 0) e = launch_win_dkv_simt(w, a->dtype, stream);
+    if (tq > 0) e = launch_win_delta(a->dout, a->ld_dout, a->o, w, a->dtype, delta, stream);
+    if (e == cudaSuccess && tq > 0) e = launch_win_dq_simt(w, a->dtype, stream);
+    if (e == cudaSuccess && tk > 0) e = launch_win_dkv_simt(w, a->dtype, stream);
     return of(e);
 }
 

@@ -1,0 +1,684 @@
+// Gradients of attention with a sliding window and sinks on the tensor cores: bf16, heads of 64 or 128, rows on 16-byte boundaries.
+//
+//   P = exp2(c S - lse'),  dP = dO V^T,  Z = P (dP - delta):   dQ = scale Z K,  dK = scale Z^T Q,  dV = P^T dO
+// with c = scale log2 e, lse' in base 2, delta = the row's dO . o.  Two kernels, each with the gradients it owns in tensor memory and
+// the scores taken again (seven products of a tile of pairs in place of five, but no atomics: sums have a fixed order, and no fp32
+// gradient passes through memory):
+//   win_dq_kernel   128 queries of a head against the tiles of 128 keys that they see; also takes delta
+//   win_dkv_kernel  128 keys of a key head against the tiles of 128 queries of its heads that see them, scores transposed (a lane is
+//                   a key), so that P^T and Z^T are left operands in tensor memory as they come
+// Sinks are seen by every query behind them.  Where the window does not reach, the queries of a tile of sinks are dealt out to CTAs of
+// their own (kSinkRun queries each) whose fp32 parts win_sinks_kernel adds to the tile's in order: one CTA for all of them would walk
+// the whole sequence while the others see a window.
+//
+// Warps: 0-3 and 4-7 two groups of 128 lanes, each on half of a tile's columns, 8 loads, 9 products.
+#include "gdn_mix.cuh"
+#include "gdn_ptx.cuh"
+
+namespace gdn {
+namespace {
+
+using namespace ptx;
+
+constexpr int kTile = 128, kThreads = 320, kBox = kTile * 128;
+constexpr uint32_t kTmem = 512;
+
+__device__ unsigned g_win_bwd_status;
+
+template <int D, int RING>
+struct Geo {
+    static constexpr int kBoxes = D / 64, kUnit = kBoxes * kBox, kRing = RING;
+    static constexpr int kA = 0, kB = kUnit, kRingAt = 2 * kUnit, kStats = kRingAt + RING * kUnit, kBars = kStats + 2048, kSmem = kBars + 256 + 1024;
+};
+constexpr int ring_of_dq(int D) { return D == 128 ? 4 : 8; }
+enum Bar { kIn, kSF, kPF = kSF + 2, kPB, kZB, kDone, kLanded, kFull, kMostRing = 8, kEmpty = kFull + kMostRing, kNumBars = kEmpty + kMostRing };
+
+struct Maps {
+    CUtensorMap q, k, v, dout, dq, dk, dv;
+};
+
+__device__ __forceinline__ void init_bars(uint64_t *bar, int ring)
+{
+    mbar_init(&bar[kIn], 1);
+    mbar_init(&bar[kSF], 1);
+    mbar_init(&bar[kSF + 1], 1);
+    mbar_init(&bar[kPF], 1);
+    mbar_init(&bar[kPB], 8);
+    mbar_init(&bar[kZB], 8);
+    mbar_init(&bar[kDone], 1);
+    mbar_init(&bar[kLanded], 1);
+    for (int i = 0; i < ring; ++i) {
+        mbar_init(&bar[kFull + i], 1);
+        mbar_init(&bar[kEmpty + i], 1);
+    }
+    fence_mbar_init();
+}
+// rows from `rows` on of a tile of BOXES boxes, by one warp
+template <int BOXES>
+__device__ __forceinline__ void zero_rows(uint8_t *tile, int rows)
+{
+#pragma unroll
+    for (int b = 0; b < BOXES; ++b)
+        for (int e = rows * 8 + (threadIdx.x & 31); e < kTile * 8; e += 32) *(uint4 *)(tile + b * kBox + e * 16) = make_uint4(0, 0, 0, 0);
+}
+// D(128 x 128) = A(128 x D) B(128 x D)^T, both rows of d in shared memory
+template <int D>
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b)
+{
+    const uint64_t da = sdesc_sw128(a, 16, 1024), db = sdesc_sw128(b, 16, 1024);
+    constexpr uint32_t id = idesc_bf16_f32(128, 128, 0, 0);
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+        const uint32_t o = ((ks >> 2) * kBox + (ks & 3) * 32) >> 4;
+        mma_ss(d, da + o, db + o, id, ks > 0);
+    }
+}
+// D(128 x D) (+)= A(128 x 128) B(128 x D): A bf16 in tensor memory, the halves of its columns at a and a + 64, B's rows in shared memory
+template <int D>
+__device__ __forceinline__ void mma_sum(uint32_t d, uint32_t a, uint32_t b, bool fresh)
+{
+    const uint64_t db = sdesc_sw128(b, kBox, 1024);
+    constexpr uint32_t id = idesc_bf16_f32(128, D, 0, 1);
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) mma_ts(d, a + (ks >> 2) * 64 + (ks & 3) * 8, db + ks * 128, id, !fresh || ks > 0);
+}
+// a tile of rows in shared memory to [tokens][heads][D]: by TMA where it is whole, else by the group's 128 threads
+template <int D>
+__device__ __forceinline__ void store_rows(const CUtensorMap *map, void *out, uint8_t *tile, int64_t t0, int rows, int heads, int h, int r)
+{
+    if (rows == kTile) {
+        if (r == 0) {
+#pragma unroll
+            for (int b = 0; b < D / 64; ++b) tma_store_3d(map, tile + b * kBox, b * 64, h, (int)t0);
+            tma_store_commit();
+            tma_store_wait0();
+        }
+    } else {
+        for (int k = r; k < rows * (D / 8); k += 128) {
+            const int row = k / (D / 8), e = k % (D / 8) * 8;
+            *(uint4 *)((__nv_bfloat16 *)out + ((t0 + row) * heads + h) * D + e) = *(const uint4 *)(tile + (e >> 6) * kBox + sw128(row, e & 63));
+        }
+    }
+}
+
+// ---------------------------------------------------------------- dQ (lane = query)
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) win_dq_kernel(const __grid_constant__ Maps maps, const WinArgs a, float *delta, uint64_t limit, int withhold)
+{
+    using G = Geo<D, ring_of_dq(D)>;
+    constexpr uint32_t kS = 0, kP = 256, kQ = 384;  // S: two buffers (Z in their place), dP, dQ
+    extern __shared__ uint8_t win_bwd_smem[];
+    uint8_t *sm = (uint8_t *)(((uintptr_t)win_bwd_smem + 1023) & ~(uintptr_t)1023);
+    const Tile tl = tile_of(a.cu_q, a.N, a.Tq, kTile, blockIdx.x);
+    const SeqRange sq = seq_range(a.cu_q, tl.n, a.Tq), sk = seq_range(a.cu_k, tl.n, a.Tk);
+    const int i0 = tl.index * kTile, rows = min(kTile, sq.len - i0), h = blockIdx.y, hk = h / (a.H / a.HK);
+    if (rows <= 0) return;
+    const int p0 = i0 + sk.len - sq.len;
+    const int hi = min(max(p0 + rows, 0), sk.len), lo = hi == 0 ? 0 : min(max(p0 - a.window + 1, 0), hi);
+    const int first = min(a.sinks, lo), nfirst = (first + kTile - 1) / kTile, nt = nfirst + (hi - lo + kTile - 1) / kTile;
+    auto key0 = [&](int t) { return t < nfirst ? t * kTile : lo + (t - nfirst) * kTile; };
+    auto columns = [&](int t) { return min(kTile, (t < nfirst ? first : hi) - key0(t)); };
+    auto ragged = [&](int t) { return key0(t) + kTile > sk.len; };
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint64_t *bar = (uint64_t *)(sm + G::kBars);
+    uint32_t *tslot = (uint32_t *)(bar + kNumBars);
+    if (tid == 0) init_bars(bar, G::kRing);
+    if (warp == 8) tmem_alloc(tslot, kTmem);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tslot, base = smem_u32(sm);
+    unsigned *const status = &g_win_bwd_status;
+    auto wait = [&](int b, uint32_t parity) { return mbar_wait(&bar[b], parity, status, kStatusTimeout, limit); };
+    auto all = [&](bool ok) { return __all_sync(0xffffffffu, ok); };
+    auto full = [&](int i) { return all(wait(kFull + i % G::kRing, (i / G::kRing) & 1)); };  // unit 2 t: K, 2 t + 1: V
+    auto unit = [&](int i) { return G::kRingAt + (i % G::kRing) * G::kUnit; };
+
+    if (warp == 8) {
+        // ---------------------------------------------------------------- loads
+        bool ok = !withhold;
+        if (ok && elect_one_sync()) {
+            mbar_arrive_expect_tx(&bar[kIn], 2 * G::kUnit);
+#pragma unroll
+            for (int b = 0; b < G::kBoxes; ++b) {
+                tma_load_3d(sm + G::kA + b * kBox, &maps.q, b * 64, h, (int)(sq.bos + i0), &bar[kIn]);
+                tma_load_3d(sm + G::kB + b * kBox, &maps.dout, b * 64, h, (int)(sq.bos + i0), &bar[kIn]);
+            }
+        }
+        __syncwarp();
+        int i = 0, mended = 0;
+        for (; i < 2 * nt && ok; ++i) {
+            const int s = i % G::kRing, t = i >> 1;
+            if (i >= G::kRing && !(ok = all(wait(kEmpty + s, (i / G::kRing - 1) & 1)))) break;
+            // K's rows behind the end are the next sequence's, and 0 x NaN is NaN: they are zeroed before the tile counts as full
+            const bool mend = !(i & 1) && ragged(t);
+            uint64_t *const landing = &bar[mend ? (int)kLanded : kFull + s];
+            if (elect_one_sync()) {
+                mbar_arrive_expect_tx(landing, G::kUnit);
+#pragma unroll
+                for (int b = 0; b < G::kBoxes; ++b)
+                    tma_load_3d(sm + unit(i) + b * kBox, i & 1 ? &maps.v : &maps.k, b * 64, hk, (int)(sk.bos + key0(t)), landing);
+            }
+            __syncwarp();
+            if (mend) {
+                if (!(ok = all(wait(kLanded, mended++ & 1)))) break;
+                zero_rows<G::kBoxes>(sm + unit(i), sk.len - key0(t));
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[kFull + s]);
+            }
+        }
+        if (!withhold) wait(kIn, 0);
+        for (int k = max(0, i - G::kRing); k < i; ++k) wait(kFull + k % G::kRing, (k / G::kRing) & 1);  // (no copy outlives the CTA)
+    } else if (warp == 9) {
+        // ---------------------------------------------------------------- products: S(t+1), dQ(t), dP(t+1)
+        auto scores = [&](int t) {
+            tc_fence_after();
+            if (elect_one_sync()) {
+                mma_rows<D>(tmem + kS + (t & 1) * 128, base + G::kA, base + unit(2 * t));
+                mma_commit(&bar[kSF + (t & 1)]);  // (two: the groups may not have seen the last one's)
+            }
+            __syncwarp();
+        };
+        auto slopes = [&](int t) {
+            tc_fence_after();
+            if (elect_one_sync()) {
+                mma_rows<D>(tmem + kP, base + G::kB, base + unit(2 * t + 1));
+                mma_commit(&bar[kPF]);
+                mma_commit(&bar[kEmpty + (2 * t + 1) % G::kRing]);
+            }
+            __syncwarp();
+        };
+        bool ok = all(wait(kIn, 0));
+        if (ok && nt > 0 && (ok = full(0))) {
+            scores(0);
+            if ((ok = full(1))) slopes(0);
+        }
+        for (int t = 0; t < nt && ok; ++t) {
+            if (t + 1 < nt) {
+                if (!(ok = full(2 * t + 2))) break;
+                scores(t + 1);
+            }
+            if (!(ok = all(wait(kZB, t & 1)))) break;
+            tc_fence_after();
+            if (elect_one_sync()) {
+                mma_sum<D>(tmem + kQ, tmem + kS + (t & 1) * 128, base + unit(2 * t), t == 0);
+                mma_commit(&bar[kEmpty + (2 * t) % G::kRing]);
+            }
+            __syncwarp();
+            if (t + 1 < nt) {
+                if (!(ok = full(2 * t + 3))) break;
+                slopes(t + 1);
+            }
+        }
+        if (elect_one_sync()) mma_commit(&bar[kDone]);
+        __syncwarp();
+        wait(kDone, 0);
+    } else {
+        const int x = warp >> 2, r = tid & 127, p = p0 + r;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const float c = a.scale * kLog2e;
+        float *part = (float *)(sm + G::kStats);
+        const int64_t at = lse_at(a, tl.n, sq.bos, h) + i0 + r;
+        float lse = r < rows ? a.lse[at] * kLog2e : INFINITY;
+        if (lse == -INFINITY) lse = INFINITY;  // a row that sees nothing: weights of zero
+        // delta: each group half of the row, from dO in shared memory and o
+        float d = 0.f;
+        bool ok = wait(kIn, 0);
+        if (ok && r < rows) {
+            const __nv_bfloat16 *o = (const __nv_bfloat16 *)a.o + ((sq.bos + i0 + r) * a.H + h) * D + x * (D / 2);
+#pragma unroll
+            for (int e = 0; e < D / 2; e += 8) {
+                const uint4 u = *(const uint4 *)(o + e);
+                const int col = x * (D / 2) + e;
+                const uint4 g = *(const uint4 *)(sm + G::kB + (col >> 6) * kBox + sw128(r, col & 63));
+                const uint32_t *pu = (const uint32_t *)&u, *pg = (const uint32_t *)&g;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    d = fmaf(__uint_as_float(pu[k] << 16), __uint_as_float(pg[k] << 16), d);
+                    d = fmaf(__uint_as_float(pu[k] & 0xffff0000u), __uint_as_float(pg[k] & 0xffff0000u), d);
+                }
+            }
+        }
+        part[x * 128 + r] = d;
+        ok = bar_all(1, 256, ok);
+        d = part[r] + part[128 + r];
+        if (x == 0 && r < rows) delta[at] = d;
+        for (int t = 0; t < nt && ok; ++t) {
+            const int j0 = key0(t) + 64 * x, cols = columns(t) - 64 * x;
+            const uint32_t ts = tmem + lanes + kS + (t & 1) * 128 + 64 * x, tp = tmem + lanes + kP + 64 * x;
+            if (!(ok = all(wait(kSF + (t & 1), (t >> 1) & 1)))) break;
+            tc_fence_after();
+            float s[64];
+            tmem_ld32(ts, (uint32_t *)s);
+            tmem_ld32(ts + 32, (uint32_t *)s + 32);
+            tmem_ld_wait();
+            const Pair cc = pair_of(c, c), minus = pair_of(-lse, -lse);
+#pragma unroll
+            for (int j = 0; j < 64; j += 2) {
+                unpair(fma2(pair_of(s[j], s[j + 1]), cc, minus), s[j], s[j + 1]);
+                s[j] = ex2(s[j]);
+                s[j + 1] = ex2(s[j + 1]);
+            }
+            const bool whole = cols >= 64 && j0 + 63 <= p0 && (p0 + rows - 1 - j0 < a.window || j0 + 64 <= a.sinks);
+            if (!whole) {
+                const int end = min(cols, p - j0 + 1), begin = p - a.window + 1 - j0, sink = a.sinks - j0;
+#pragma unroll
+                for (int j = 0; j < 64; ++j)
+                    if (j >= end || (j < begin && j >= sink)) s[j] = 0.f;
+            }
+            if (!(ok = all(wait(kPF, t & 1)))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                float g[32];
+                uint32_t w[16];
+                tmem_ld32(tp + 32 * q, (uint32_t *)g);
+                tmem_ld_wait();
+                if (!whole) {  // (dP is not finite where a key outside the sequence is not)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) g[j] = s[32 * q + j] == 0.f ? 0.f : g[j];
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j) w[j] = pack_bf16(s[32 * q + 2 * j] * (g[2 * j] - d), s[32 * q + 2 * j + 1] * (g[2 * j + 1] - d));
+                tmem_st16(ts + 16 * q, w);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[kZB]);
+        }
+        ok = bar_all(1, 256, wait(kDone, 0) && ok);
+        if (ok) {
+            tc_fence_after();
+            uint8_t *tile = sm + G::kA;  // (the last scores are taken)
+#pragma unroll
+            for (int q = 0; q < D / 64; ++q) {
+                const int col = x * (D / 2) + 32 * q;
+                float o[32];
+                if (nt > 0) {
+                    tmem_ld32(tmem + lanes + kQ + col, (uint32_t *)o);
+                    tmem_ld_wait();
+                }
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] = nt > 0 ? o[j] * a.scale : 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) *(uint4 *)(tile + (col >> 6) * kBox + sw128(r, (col & 63) + 8 * j)) = pack8(o + 8 * j);
+            }
+            fence_proxy_async();
+            bar_sync(1, 256);
+            if (x == 0) store_rows<D>(&maps.dq, a.dq, tile, sq.bos + i0, rows, a.H, h, r);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmem);
+    }
+}
+
+// ---------------------------------------------------------------- dK, dV (lane = key)
+constexpr int kSinkRun = 1024;   // queries of a CTA that sums for a tile of sinks where the window does not reach
+constexpr int kMostSinkTiles = 4;  // (more tiles of sinks share the work among them)
+
+struct Sinks {
+    float *own, *run;  // fp32 parts [N][HK][tiles][2][128][D] of the tiles' own CTAs and [slots][HK][tiles][2][128][D] of the runs
+    int tiles;         // tiles of sinks whose far queries are dealt out; 0: none
+    int64_t slots;
+};
+
+// the last query (exclusive) that sees a key of j0 .. j0 + cols - 1 through the window
+__device__ __forceinline__ int window_end(const WinArgs &a, int j0, int cols, int off, int Lq)
+{
+    return (int)clamp64((int64_t)j0 + cols - 1 + a.window - off, 0, Lq);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) win_dkv_kernel(const __grid_constant__ Maps maps, const WinArgs a, const Sinks sinks, int64_t key_tiles,
+                                                              uint64_t limit, int withhold)
+{
+    using G = Geo<D, 4>;
+    constexpr uint32_t kS = 0, kP = 128, kV = 256, kK = 384;  // S^T (P^T in its place), dP^T (Z^T), dV, dK
+    extern __shared__ uint8_t win_bwd_smem[];
+    uint8_t *sm = (uint8_t *)(((uintptr_t)win_bwd_smem + 1023) & ~(uintptr_t)1023);
+    const int hk = blockIdx.y, per = a.H / a.HK;
+    // a tile of keys, or a run of queries against a tile of sinks
+    const bool run = blockIdx.x >= key_tiles;
+    const int64_t item = run ? blockIdx.x - key_tiles : blockIdx.x;
+    const Tile tl = run ? tile_of(a.cu_q, a.N, a.Tq, kSinkRun, item / sinks.tiles) : tile_of(a.cu_k, a.N, a.Tk, kTile, item);
+    const SeqRange sq = seq_range(a.cu_q, tl.n, a.Tq), sk = seq_range(a.cu_k, tl.n, a.Tk);
+    const int st = run ? (int)(item % sinks.tiles) : tl.index;
+    const int j0 = st * kTile, cols = min(kTile, sk.len - j0), off = sk.len - sq.len;
+    if (cols <= 0) return;
+    int begin = max(0, j0 - off), end = window_end(a, j0, cols, off, sq.len);
+    const bool dealt = !run && st < sinks.tiles;  // its fp32 part is joined with the runs'
+    if (run) {
+        begin = max(max(begin, end), tl.index * kSinkRun);
+        end = (int)min((int64_t)sq.len, (int64_t)(tl.index + 1) * kSinkRun);
+        if (begin >= end) return;
+    } else if (!dealt && j0 < a.sinks) {
+        end = sq.len;
+    }
+    const int tiles = begin < end ? (end - begin + kTile - 1) / kTile : 0, nt = tiles * per;
+    float *const part = run ? sinks.run + (((item / sinks.tiles) * a.HK + hk) * sinks.tiles + st) * 2 * kTile * D
+                      : dealt ? sinks.own + (((int64_t)tl.n * a.HK + hk) * sinks.tiles + st) * 2 * kTile * D : nullptr;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint64_t *bar = (uint64_t *)(sm + G::kBars);
+    uint32_t *tslot = (uint32_t *)(bar + kNumBars);
+    if (tid == 0) init_bars(bar, G::kRing);
+    if (warp == 8) tmem_alloc(tslot, kTmem);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tslot, base = smem_u32(sm);
+    unsigned *const status = &g_win_bwd_status;
+    auto wait = [&](int b, uint32_t parity) { return mbar_wait(&bar[b], parity, status, kStatusTimeout, limit); };
+    auto all = [&](bool ok) { return __all_sync(0xffffffffu, ok); };
+    auto full = [&](int i) { return all(wait(kFull + i % G::kRing, (i / G::kRing) & 1)); };  // unit 2 t: Q, 2 t + 1: dO
+    auto unit = [&](int i) { return G::kRingAt + (i % G::kRing) * G::kUnit; };
+    auto query0 = [&](int t) { return begin + (t % tiles) * kTile; };
+    auto head = [&](int t) { return hk * per + t / tiles; };
+    auto ragged = [&](int t) { return query0(t) + kTile > sq.len; };
+
+    if (warp == 8) {
+        // ---------------------------------------------------------------- loads
+        bool ok = !withhold;
+        if (ok && elect_one_sync()) {
+            mbar_arrive_expect_tx(&bar[kIn], 2 * G::kUnit);
+#pragma unroll
+            for (int b = 0; b < G::kBoxes; ++b) {
+                tma_load_3d(sm + G::kA + b * kBox, &maps.k, b * 64, hk, (int)(sk.bos + j0), &bar[kIn]);
+                tma_load_3d(sm + G::kB + b * kBox, &maps.v, b * 64, hk, (int)(sk.bos + j0), &bar[kIn]);
+            }
+        }
+        __syncwarp();
+        int i = 0, mended = 0;
+        for (; i < 2 * nt && ok; ++i) {
+            const int s = i % G::kRing, t = i >> 1;
+            if (i >= G::kRing && !(ok = all(wait(kEmpty + s, (i / G::kRing - 1) & 1)))) break;
+            // rows behind the end are the next sequence's, and 0 x NaN is NaN: they are zeroed before the tile counts as full
+            const bool mend = ragged(t);
+            uint64_t *const landing = &bar[mend ? (int)kLanded : kFull + s];
+            if (elect_one_sync()) {
+                mbar_arrive_expect_tx(landing, G::kUnit);
+#pragma unroll
+                for (int b = 0; b < G::kBoxes; ++b)
+                    tma_load_3d(sm + unit(i) + b * kBox, i & 1 ? &maps.dout : &maps.q, b * 64, head(t), (int)(sq.bos + query0(t)), landing);
+            }
+            __syncwarp();
+            if (mend) {
+                if (!(ok = all(wait(kLanded, mended++ & 1)))) break;
+                zero_rows<G::kBoxes>(sm + unit(i), sq.len - query0(t));
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[kFull + s]);
+            }
+        }
+        if (!withhold) wait(kIn, 0);
+        for (int k = max(0, i - G::kRing); k < i; ++k) wait(kFull + k % G::kRing, (k / G::kRing) & 1);  // (no copy outlives the CTA)
+    } else if (warp == 9) {
+        // ---------------------------------------------------------------- products: dV(t), S(t+1), dK(t), dP(t+1)
+        auto scores = [&](int t) {
+            tc_fence_after();
+            if (elect_one_sync()) {
+                mma_rows<D>(tmem + kS, base + G::kA, base + unit(2 * t));
+                mma_commit(&bar[kSF]);
+            }
+            __syncwarp();
+        };
+        auto slopes = [&](int t) {
+            tc_fence_after();
+            if (elect_one_sync()) {
+                mma_rows<D>(tmem + kP, base + G::kB, base + unit(2 * t + 1));
+                mma_commit(&bar[kPF]);
+            }
+            __syncwarp();
+        };
+        bool ok = all(wait(kIn, 0));
+        if (ok && nt > 0 && (ok = full(0))) {
+            scores(0);
+            if ((ok = full(1))) slopes(0);
+        }
+        for (int t = 0; t < nt && ok; ++t) {
+            if (!(ok = all(wait(kPB, t & 1)))) break;
+            tc_fence_after();
+            if (elect_one_sync()) {
+                mma_sum<D>(tmem + kV, tmem + kS, base + unit(2 * t + 1), t == 0);
+                mma_commit(&bar[kEmpty + (2 * t + 1) % G::kRing]);
+            }
+            __syncwarp();
+            if (t + 1 < nt) {
+                if (!(ok = full(2 * t + 2))) break;
+                scores(t + 1);
+            }
+            if (!(ok = all(wait(kZB, t & 1)))) break;
+            tc_fence_after();
+            if (elect_one_sync()) {
+                mma_sum<D>(tmem + kK, tmem + kP, base + unit(2 * t), t == 0);
+                mma_commit(&bar[kEmpty + (2 * t) % G::kRing]);
+            }
+            __syncwarp();
+            if (t + 1 < nt) {
+                if (!(ok = full(2 * t + 3))) break;
+                slopes(t + 1);
+            }
+        }
+        if (elect_one_sync()) mma_commit(&bar[kDone]);
+        __syncwarp();
+        wait(kDone, 0);
+    } else {
+        const int x = warp >> 2, r = tid & 127, j = j0 + r;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lanes + kS + 64 * x, tp = tmem + lanes + kP + 64 * x;
+        const float c = a.scale * kLog2e;
+        float *const stats = (float *)(sm + G::kStats) + x * 256;  // [tile parity][lse, delta][64 queries of this group]
+        // this thread's number of tile t: lse (of the first 64 threads) or delta of one of the group's queries
+        auto stat = [&](int t) {
+            const int i = query0(t) + 64 * x + (r & 63);
+            if (i >= end) return r < 64 ? INFINITY : 0.f;  // weights of zero
+            const int64_t at = lse_at(a, tl.n, sq.bos, head(t)) + i;
+            if (r >= 64) return a.delta[at];
+            const float l = a.lse[at] * kLog2e;
+            return l == -INFINITY ? INFINITY : l;
+        };
+        float next = nt > 0 ? stat(0) : 0.f;
+        bool ok = true;
+        for (int t = 0; t < nt; ++t) {
+            const int i0 = query0(t) + 64 * x, q0 = i0 + off, rows = min(end - i0, 64);  // (the group's 64 queries)
+            float *const ls = stats + (t & 1) * 128, *const dl = ls + 64;
+            ls[r] = next;
+            if (t + 1 < nt) next = stat(t + 1);
+            if (!(ok = bar_all(1 + x, 128, ok && wait(kSF, t & 1)))) break;  // (the group leaves together)
+            tc_fence_after();
+            float s[64];
+            tmem_ld32(ts, (uint32_t *)s);
+            tmem_ld32(ts + 32, (uint32_t *)s + 32);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 64; k += 4) {
+                const float4 l = *(const float4 *)(ls + k);
+                s[k] = ex2(fmaf(s[k], c, -l.x));
+                s[k + 1] = ex2(fmaf(s[k + 1], c, -l.y));
+                s[k + 2] = ex2(fmaf(s[k + 2], c, -l.z));
+                s[k + 3] = ex2(fmaf(s[k + 3], c, -l.w));
+            }
+            if (!(rows == 64 && j0 + kTile - 1 <= q0 && (q0 + 63 - j0 < a.window || j0 + kTile <= a.sinks))) {
+                const int first = j - q0, last = j < a.sinks ? rows : (int)min((int64_t)rows, (int64_t)j + a.window - q0);
+#pragma unroll
+                for (int k = 0; k < 64; ++k)
+                    if (k < first || k >= last) s[k] = 0.f;
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                uint32_t w[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) w[k] = pack_bf16(s[32 * q + 2 * k], s[32 * q + 2 * k + 1]);
+                tmem_st16(ts + 16 * q, w);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[kPB]);
+            ok = all(wait(kPF, t & 1));
+            tc_fence_after();
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                float g[32];
+                uint32_t w[16];
+                tmem_ld32(tp + 32 * q, (uint32_t *)g);
+                tmem_ld_wait();
+#pragma unroll
+                for (int k = 0; k < 32; k += 4) {
+                    const float4 d = *(const float4 *)(dl + 32 * q + k);
+                    const float *u = s + 32 * q + k;
+                    w[k / 2] = pack_bf16(u[0] * (g[k] - d.x), u[1] * (g[k + 1] - d.y));
+                    w[k / 2 + 1] = pack_bf16(u[2] * (g[k + 2] - d.z), u[3] * (g[k + 3] - d.w));
+                }
+                tmem_st16(tp + 16 * q, w);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[kZB]);
+        }
+        // ---------------------------------------------------------------- dV by the first group, dK by the second
+        ok = bar_all(1 + x, 128, wait(kDone, 0) && ok);
+        if (ok) {
+            tc_fence_after();
+            const float f = x == 0 ? 1.f : a.scale;
+            uint8_t *tile = sm + (x == 0 ? G::kB : G::kA);  // (V's and K's last products are taken)
+#pragma unroll
+            for (int q = 0; q < D / 32; ++q) {
+                float o[32];
+                if (nt > 0) {
+                    tmem_ld32(tmem + lanes + (x == 0 ? kV : kK) + 32 * q, (uint32_t *)o);
+                    tmem_ld_wait();
+                }
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] = nt > 0 ? o[k] * f : 0.f;
+                if (part) {
+                    float *dst = part + ((int64_t)(1 - x) * kTile + r) * D + 32 * q;  // dK, then dV
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4) *(float4 *)(dst + k) = *(const float4 *)&o[k];
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) *(uint4 *)(tile + (q >> 1) * kBox + sw128(r, 32 * (q & 1) + 8 * k)) = pack8(o + 8 * k);
+                }
+            }
+            if (!part) {
+                fence_proxy_async();
+                bar_sync(1 + x, 128);
+                store_rows<D>(x == 0 ? &maps.dv : &maps.dk, x == 0 ? a.dv : a.dk, tile, sk.bos + j0, cols, a.HK, hk, r);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmem);
+    }
+}
+
+// dK and dV of the tiles of sinks: their own part and the runs', in order
+template <int D>
+__global__ void __launch_bounds__(256) win_sinks_kernel(const WinArgs a, const Sinks s)
+{
+    const int which = blockIdx.z, st = blockIdx.y % s.tiles, hk = blockIdx.y / s.tiles;
+    const int n = blockIdx.x / (kTile * D / 1024), e = (blockIdx.x % (kTile * D / 1024)) * 1024 + threadIdx.x * 4;
+    const SeqRange sq = seq_range(a.cu_q, n, a.Tq), sk = seq_range(a.cu_k, n, a.Tk);
+    const int j0 = st * kTile, cols = min(kTile, sk.len - j0), r = e / D;
+    if (r >= cols) return;
+    const int off = sk.len - sq.len;
+    const int from = max(max(0, j0 - off), window_end(a, j0, cols, off, sq.len));  // the first query of a run
+    const int64_t slot0 = a.cu_q ? clamp64(a.cu_q[n], 0, a.Tq) / kSinkRun + n : (int64_t)n * ((a.Tq + kSinkRun - 1) / kSinkRun);
+    float4 x = *(const float4 *)(s.own + ((((int64_t)n * a.HK + hk) * s.tiles + st) * 2 + which) * kTile * D + e);
+    for (int i = from / kSinkRun; from < sq.len && i * kSinkRun < sq.len; ++i) {
+        const float4 y = *(const float4 *)(s.run + ((((slot0 + i) * a.HK + hk) * s.tiles + st) * 2 + which) * kTile * D + e);
+        x.x += y.x;
+        x.y += y.y;
+        x.z += y.z;
+        x.w += y.w;
+    }
+    __nv_bfloat16 *dst = (__nv_bfloat16 *)(which ? a.dv : a.dk) + ((sk.bos + j0 + r) * a.HK + hk) * D + e % D;
+    *(uint2 *)dst = make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
+}
+
+Sinks plan_sinks(const WinArgs &a, int D, size_t *bytes)
+{
+    Sinks s{};
+    const int tiles = (a.sinks + kTile - 1) / kTile;
+    *bytes = 0;
+    if (a.window >= a.Tk || tiles > kMostSinkTiles || tiles == 0) return s;
+    s.tiles = tiles;
+    s.slots = mix_slots(a.cu_q != nullptr, a.N, a.Tq, kSinkRun);
+    *bytes = ((size_t)a.N + s.slots) * a.HK * tiles * 2 * kTile * D * sizeof(float);
+    return s;
+}
+
+template <int D>
+cudaError_t launch(const WinArgs &a, int64_t tq, int64_t tk, float *delta, void *ws, cudaStream_t st)
+{
+    Maps maps;
+    if (!heads_map(&maps.q, a.q, D, a.H, tq, a.ldq, kTile) || !heads_map(&maps.k, a.k, D, a.HK, tk, a.ldk, kTile) ||
+        !heads_map(&maps.v, a.v, D, a.HK, tk, a.ldv, kTile) || !heads_map(&maps.dout, a.dout, D, a.H, tq, a.ld_dout, kTile) ||
+        !heads_map(&maps.dq, a.dq, D, a.H, tq, (int64_t)a.H * D, kTile) || !heads_map(&maps.dk, a.dk, D, a.HK, tk, (int64_t)a.HK * D, kTile) ||
+        !heads_map(&maps.dv, a.dv, D, a.HK, tk, (int64_t)a.HK * D, kTile))
+        return cudaErrorInvalidValue;
+    constexpr int smem_q = Geo<D, ring_of_dq(D)>::kSmem, smem_k = Geo<D, 4>::kSmem;
+    static std::atomic<uint64_t> seen;
+    if (first_on_device(seen)) {
+        cudaError_t e = cudaFuncSetAttribute(win_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_q);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(win_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_k);
+        if (e != cudaSuccess) return e;
+        done_on_device(seen);
+    }
+    size_t bytes;
+    Sinks s = plan_sinks(a, D, &bytes);
+    s.own = (float *)ws;
+    s.run = s.own + (int64_t)a.N * a.HK * s.tiles * 2 * kTile * D;
+    const int64_t qt = mix_slots(a.cu_q != nullptr, a.N, a.Tq, kTile), kt = mix_slots(a.cu_k != nullptr, a.N, a.Tk, kTile);
+    const int64_t ctas = kt + s.slots * s.tiles;
+    if (qt > INT32_MAX || ctas > INT32_MAX || (int64_t)a.N * kTile * D / 1024 > INT32_MAX) return cudaErrorInvalidConfiguration;
+    const int withhold = withhold_loads();
+    const uint64_t limit = withhold ? kTestWaitLimitNs : kWaitLimitNs;
+    win_dq_kernel<D><<<dim3((unsigned)qt, a.H), kThreads, smem_q, st>>>(maps, a, delta, limit, withhold);
+    win_dkv_kernel<D><<<dim3((unsigned)ctas, a.HK), kThreads, smem_k, st>>>(maps, a, s, kt, limit, withhold);
+    if (s.tiles > 0) win_sinks_kernel<D><<<dim3((unsigned)(a.N * (kTile * D / 1024)), a.HK * s.tiles, 2), 256, 0, st>>>(a, s);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+bool win_bwd_tc_ok(const WinArgs &a, int64_t tq, int64_t tk)
+{
+    return win_tc_ok(a, tq, tk) && tma_ok(a.dout, a.ld_dout, tq, 2) && !(((uintptr_t)a.dq | (uintptr_t)a.dk | (uintptr_t)a.dv) & 15) &&
+           a.HK * kMostSinkTiles <= 65535;
+}
+
+size_t win_bwd_tc_bytes(const WinArgs &a)
+{
+    size_t bytes;
+    plan_sinks(a, a.D, &bytes);
+    return bytes;
+}
+
+cudaError_t launch_win_bwd_tc(const WinArgs &a, int64_t tq, int64_t tk, float *delta, void *ws, cudaStream_t st)
+{
+    return a.D == 64 ? launch<64>(a, tq, tk, delta, ws, st) : launch<128>(a, tq, tk, delta, ws, st);
+}
+
+gdn_status read_win_bwd_status(cudaStream_t st)
+{
+    unsigned word = 0, zero = 0;
+    if (cudaMemcpyFromSymbolAsync(&word, g_win_bwd_status, sizeof(word), 0, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+        cudaMemcpyToSymbolAsync(g_win_bwd_status, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, st) != cudaSuccess ||
+        cudaStreamSynchronize(st) != cudaSuccess)
+        return GDN_ERR_CUDA;
+    return word & kStatusTimeout ? GDN_ERR_TIMEOUT : GDN_OK;
+}
+
+}  // namespace gdn

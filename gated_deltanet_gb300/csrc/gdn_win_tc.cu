@@ -32,7 +32,7 @@ struct Geo {
     static constexpr int kRing = D == 128 ? 5 : 8;  // K and V tiles in flight
     static constexpr int kQ = 0, kKV = 2 * kUnit, kBars = kKV + kRing * kUnit, kSmem = kBars + 256 + 1024;
 };
-enum Bar { kQF, kSF, kPB = kSF + 2, kDone = kPB + 2, kFix = kDone + 2, kFin, kFull, kMostRing = 8, kEmpty = kFull + kMostRing, kNumBars = kEmpty + kMostRing };
+enum Bar { kQF, kSF, kPB = kSF + 2, kDone = kPB + 2, kLanded = kDone + 2, kFin, kFull, kMostRing = 8, kEmpty = kFull + kMostRing, kNumBars = kEmpty + kMostRing };
 
 struct Maps {
     CUtensorMap q, k, v, o;
@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kThreads, 1) win_tc_kernel(const __grid_consta
             mbar_init(&bar[kPB + x], 4);
             mbar_init(&bar[kDone + x], 1);
         }
-        mbar_init(&bar[kFix], 1);
+        mbar_init(&bar[kLanded], 1);
         mbar_init(&bar[kFin], 1);
         for (int i = 0; i < G::kRing; ++i) {
             mbar_init(&bar[kFull + i], 1);
@@ -116,32 +116,30 @@ __global__ void __launch_bounds__(kThreads, 1) win_tc_kernel(const __grid_consta
                     tma_load_3d(sm + G::kQ + x * G::kUnit + b * kBox, &maps.q, b * 64, x ? B.h : A.h, (int)(sq.bos + (x ? B.i0 : A.i0)), &bar[kQF]);
         }
         __syncwarp();
-        int i = 0;
+        int i = 0, mended = 0;
         for (; i < 2 * nt && ok; ++i) {
             const int s = i % G::kRing;
             if (i >= G::kRing && !(ok = all(wait(kEmpty + s, (i / G::kRing - 1) & 1)))) break;
+            // V's rows behind the end are the next sequence's, and 0 x NaN is NaN: they are zeroed before the tile counts as full
+            const bool mend = (i & 1) && ragged(i >> 1);
+            uint64_t *const landing = &bar[mend ? (int)kLanded : kFull + s];
             if (elect_one_sync()) {
-                mbar_arrive_expect_tx(&bar[kFull + s], G::kUnit);
+                mbar_arrive_expect_tx(landing, G::kUnit);
 #pragma unroll
                 for (int b = 0; b < G::kBoxes; ++b)
-                    tma_load_3d(sm + G::kKV + s * G::kUnit + b * kBox, i & 1 ? &maps.v : &maps.k, b * 64, hk, (int)(sk.bos + key0(i >> 1)), &bar[kFull + s]);
+                    tma_load_3d(sm + G::kKV + s * G::kUnit + b * kBox, i & 1 ? &maps.v : &maps.k, b * 64, hk, (int)(sk.bos + key0(i >> 1)), landing);
             }
             __syncwarp();
-        }
-        // The rows behind the end.  Only the last tile holds such, and the sinks' where a sequence has less than a tile of keys: by
-        // then every load has been issued.
-        static_assert(G::kRing >= 4, "");
-        for (int t = 0; t < nt && ok; ++t) {
-            if (!ragged(t)) continue;
-            if (!(ok = full(2 * t + 1))) break;
-            const int rows = sk.len - key0(t);
-            uint8_t *v = sm + G::kKV + ((2 * t + 1) % G::kRing) * G::kUnit;
+            if (mend) {
+                if (!(ok = all(wait(kLanded, mended++ & 1)))) break;
+                uint8_t *v = sm + G::kKV + s * G::kUnit;
 #pragma unroll
-            for (int b = 0; b < G::kBoxes; ++b)
-                for (int e = rows * 8 + lane; e < kTile * 8; e += 32) *(uint4 *)(v + b * kBox + e * 16) = make_uint4(0, 0, 0, 0);
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[kFix]);
+                for (int b = 0; b < G::kBoxes; ++b)
+                    for (int e = (sk.len - key0(i >> 1)) * 8 + lane; e < kTile * 8; e += 32) *(uint4 *)(v + b * kBox + e * 16) = make_uint4(0, 0, 0, 0);
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[kFull + s]);
+            }
         }
         if (!withhold) wait(kQF, 0);
         for (int k = max(0, i - G::kRing); k < i; ++k) wait(kFull + k % G::kRing, (k / G::kRing) & 1);  // (no copy outlives the CTA)
@@ -164,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1) win_tc_kernel(const __grid_consta
             for (int ks = 0; ks < kTile / 16; ++ks) mma_ts(tmem + kO + 128 * x, tmem + kS + 128 * x + ks * 8, dv + ks * 128, idO, !fresh || ks > 0);
         };
         bool ok = all(wait(kQF, 0));
-        int done[2] = {0, 0}, fixes = 0, late = -1;  // late: the tile whose PV_B is still to come
+        int done[2] = {0, 0}, late = -1;  // late: the tile whose PV_B is still to come
         auto second = [&]() {  // PV_B(late)
             ok = all(wait(kPB + 1, done[1] & 1));
             if (!ok) return;
@@ -192,7 +190,6 @@ __global__ void __launch_bounds__(kThreads, 1) win_tc_kernel(const __grid_consta
             }
             __syncwarp();
             if (!(ok = full(2 * t + 1))) break;
-            if (ragged(t) && !(ok = all(wait(kFix, fixes++ & 1)))) break;
             if (needA) {
                 if (!(ok = all(wait(kPB, done[0] & 1)))) break;
                 tc_fence_after();
