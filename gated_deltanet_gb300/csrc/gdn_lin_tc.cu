@@ -2,14 +2,26 @@
 //
 // One CTA per (sequence or segment of one, value head, 64 columns of c) walks chunks of 128 tokens; the state X (D x 64, fp32)
 // stays in tensor memory.  Per chunk of n tokens, forward in time, every product a tcgen05 MMA with M = 128:
-//   Z  = a b^T                       (128 x 128)     Z_ij -> cs l^(i-j) Z_ij for j <= i, rounded to bf16 where it lies
-//   O1 = a X,  O2 = Z c              (128 x 64)      out_i = os (l^(i+1) O1_i + O2_i)
-//   X <- l^n X + b^T C               (D x 64)        C_j = cs l^(n-1-j) c_j as the sum of two bf16 values
-// X enters O1 rounded to bf16; the state itself takes C as hi + lo (16 bits of it; one bf16 alone would put 2^-9 into a state that
-// is returned in fp32), and b and c as they are.  Against time the same with the powers counted from the chunk's other end.
+//   Z = a b^T                   (128 x 128)   Z_ij <- cs l^(i-j) Z_ij for j <= i, rounded to bf16 where it lies
+//   O1 = a X,  O2 = Z c         (128 x 64)    out_i = os (l^(i+1) O1_i + O2_i)
+//   X <- l^n X + b^T C          (D x 64)      C_j = cs l^(n-1-j) c_j as the sum of two bf16 values
+// Against time the same with the powers counted from the chunk's other end.
+// X enters O1 rounded to bf16.  X itself takes C as hi + lo, 16 bits of it (one bf16 alone would put 2^-9 into a state that is returned
+// in fp32; the two leave it 2.4e-6 in the 2-norm), and b and c as they are.
 //
-// Warps: 0 loads (TMA, two stages of a, b and c's columns), 1 issues the products, 4-7 turn Z, 8-11 round and decay X, 12-15 write
-// out, 16-19 scale c.  The chain from chunk to chunk is X's: product, read, round, decay, write back.
+// Bound by shared memory: it gives the products about 80 bytes a cycle, so that one of 128 x 128 x 16 with both operands there takes
+// 104 cycles (64 for the arithmetic), 128 x 64 x 16 takes 76, with its left operand in tensor memory 46, and it serves the copies and
+// the warps beside them.  A chunk's products are 2640 cycles alone and about 3700 so; a chunk takes 4100.  Hence: hi and lo lie next to
+// each other and go in as one right operand of 128 columns (X is the sum of two accumulators); outputs go from registers to memory.
+// A whole head to a CTA has the cheaper products (N = 128, X transposed, C in tensor memory) but half the CTAs and most of its
+// CUDA-core work on the chain from chunk to chunk: 138 us at 4 x 4096 tokens of 16 heads of 128 where this takes 76; C in three parts
+// (24 bits) 102.
+//
+// Warps: 0 loads (TMA: two stages of a and b, three of c, which is done with later; zeroes the rows behind a sequence's end, which are
+// the next one's: 0 x NaN is NaN), 1 issues the products, 4-7 turn Z, 8-15 round and decay X, 16-19 write out, 20-27 scale and split c.
+// One warp of a role polls a barrier and the others wait for it at a named one, which takes no instructions (polled by every waiting
+// warp, 10 000 of a chunk's 24 500 instructions were polls).  Order of the products: X(m+1), O1(m), Z(m+1), O2(m); X is read, rounded
+// and decayed, and c split, while the last three run.
 #include <cudaTypedefs.h>
 
 #include "gdn_mix.cuh"
@@ -20,22 +32,22 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kC = 128, kCols = 64, kThreads = 640, kStages = 2, kBox = kC * 128;
-constexpr uint32_t kZ = 0, kO1 = 256, kO2 = 320, kX = 384, kTmem = 512;  // tensor-memory columns (Z: two buffers)
+constexpr int kC = 128, kCols = 64, kThreads = 896, kStages = 2, kStagesC = 3, kBox = kC * 128;
+// tensor-memory columns: Z (two buffers), the outputs, the state's two accumulators
+constexpr uint32_t kZ = 0, kO1 = 256, kO2 = 320, kX = 384, kTmem = 512;
 
 __device__ unsigned g_lin_status;
 
 template <int D>
 struct Geo {
     static constexpr int kBoxes = D / 64;
-    static constexpr int kA = 0, kB = kBoxes * kBox, kCc = 2 * kBoxes * kBox, kStage = (2 * kBoxes + 1) * kBox;
-    static constexpr int kXs = kStages * kStage, kHi = kXs + kBox, kLo = kHi + kBox, kOut = kLo + kBox, kTab = kOut + kBox, kBars = kTab + 1024;
-    static constexpr int kSmem = kBars + 256 + 1024;
+    static constexpr int kA = 0, kB = kBoxes * kBox, kStage = 2 * kBoxes * kBox;  // a and b; c in a ring of its own
+    static constexpr int kCs = kStages * kStage, kXs = kCs + kStagesC * kBox, kParts = kXs + kBox, kBars = kParts + 2 * kBox, kSmem = kBars + 256 + 1024;
 };
-enum Bar { kFull, kEmpty = kFull + kStages, kZF = kEmpty + kStages, kZB = kZF + 2, kXB = kZB + 2, kCB, kXF, kOF, kOE, kFix, kFin, kNumBars };
+enum Bar { kFull, kEmpty = kFull + kStages, kFullC = kEmpty + kStages, kEmptyC = kFullC + kStagesC, kZF = kEmptyC + kStagesC, kZB = kZF + 2, kLanded = kZB + 2, kXB, kCB, kXF, kO1F, kOF, kOE, kFin, kNumBars };
 
 struct Maps {
-    CUtensorMap a[3], b[3], c[3], out[3];
+    CUtensorMap a[3], b[3], c[3];
 };
 
 struct Split {
@@ -63,6 +75,8 @@ struct Part {
     __device__ int rows(int c) const { return min(kC, s.len - c * kC); }
 };
 
+__device__ __forceinline__ float low_bf16(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high_bf16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 // STATE: only what the segment adds to the state, from zero
 template <int D, bool STATE>
 __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_constant__ Maps maps, const LinArgs args, const Split split, uint64_t limit, int withhold)
@@ -70,10 +84,13 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     using G = Geo<D>;
     constexpr int nct = D / kCols;
     extern __shared__ uint8_t lin_tc_smem[];
-    uint8_t *sm = (uint8_t *)(((uintptr_t)lin_tc_smem + 1023) & ~(uintptr_t)1023);
-    const LinPass &p = args.pass[blockIdx.y];
-    const int ct = (int)(blockIdx.x % nct), hv = (int)(blockIdx.x / nct % args.HV), c0 = ct * kCols;
-    const int64_t slot = blockIdx.x / ((unsigned)nct * args.HV);
+    uint8_t *const sm = lin_tc_smem + (-smem_u32(lin_tc_smem) & 1023u);
+    // (the column halves and the passes of a head next to each other: they read the same tensors)
+    const int c0 = (int)(blockIdx.x % nct) * kCols, pi = (int)(blockIdx.x / nct % args.passes);
+    const LinPass &p = args.pass[pi];
+    const unsigned rest = blockIdx.x / (nct * args.passes);
+    const int hv = (int)(rest % args.HV);
+    const int64_t slot = rest / args.HV;
     int n;
     const Part part(args, split, slot, n);
     const bool rev = p.reverse;
@@ -83,7 +100,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     const float g = args.decay ? args.decay[hv] : 0.f, g2 = g * kRcpLn2;
     const int64_t xbase = ((int64_t)n * args.HV + hv) * D * D;
     auto xat = [&](int r, int c) { return xbase + (p.x_t ? (int64_t)(c0 + c) * D + r : (int64_t)r * D + c0 + c); };
-    float *const mine = split.states ? split.states + (((int64_t)blockIdx.y * split.slots + slot) * args.HV + hv) * D * D + c0 : nullptr;
+    float *const mine = split.states ? split.states + (((int64_t)pi * split.slots + slot) * args.HV + hv) * D * D + c0 : nullptr;
 
     if (nm <= 0) {
         // nothing to walk: a sequence without tokens hands its state on
@@ -95,26 +112,26 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
 
     uint64_t *bar = (uint64_t *)(sm + G::kBars);
     uint32_t *tslot = (uint32_t *)(bar + kNumBars);
-    float *tab = (float *)(sm + G::kTab);
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&bar[kFull + i], 1);
             mbar_init(&bar[kEmpty + i], 1);
             mbar_init(&bar[kZF + i], 1);
             mbar_init(&bar[kZB + i], 4);
         }
-        mbar_init(&bar[kXB], 4);
-        mbar_init(&bar[kCB], 4);
+        for (int i = 0; i < kStagesC; ++i) {
+            mbar_init(&bar[kFullC + i], 1);
+            mbar_init(&bar[kEmptyC + i], 1);
+        }
+        mbar_init(&bar[kLanded], 1);
+        mbar_init(&bar[kXB], 8);
+        mbar_init(&bar[kCB], 8);
         mbar_init(&bar[kXF], 1);
+        mbar_init(&bar[kO1F], 1);
         mbar_init(&bar[kOF], 1);
         mbar_init(&bar[kOE], 4);
-        mbar_init(&bar[kFix], 4);
         mbar_init(&bar[kFin], 1);
         fence_mbar_init();
-    }
-    if (tid < 256) {  // tab[127 + i - j]: cs l^|i - j| on the side that counts, else 0
-        const int d = rev ? 127 - tid : tid - 127;
-        tab[tid] = d >= 0 ? p.cs * decay_pow(g2, d) : 0.f;
     }
     if (warp == 3) tmem_alloc(tslot, kTmem);
     tc_fence_before();
@@ -125,35 +142,60 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     unsigned *const status = &g_lin_status;
     auto wait = [&](int b, uint32_t parity) { return mbar_wait(&bar[b], parity, status, kStatusTimeout, limit); };
     auto all = [&](bool ok) { return __all_sync(0xffffffffu, ok); };
-    // the sequence's last chunk, where it is not full: its place here (or none)
-    const int ragged = part.s.len % kC == 0 ? -1 : rev ? (part.m0 == 0 ? 0 : -1) : (last_seg ? nm - 1 : -1);
-    auto loaded = [&](int m) { return wait(kFull + m % kStages, (m / kStages) & 1) && (m != ragged || wait(kFix, 0)); };
+    auto loaded = [&](int m) { return all(wait(kFull + m % kStages, (m / kStages) & 1)); };    // a and b
+    auto loaded_c = [&](int m) { return all(wait(kFullC + m % kStagesC, (m / kStagesC) & 1)); };
 
     if (warp == 0) {
         // ---------------------------------------------------------------- loads
+        // (a and b are done with earlier than c, by most of a chunk's time)
         bool ok = !withhold;
         int m = 0;
         for (; m < nm && ok; ++m) {
-            const int s = m % kStages;
+            const int s = m % kStages, c = part.chunk(m, rev), rows = part.rows(c), t0 = (int)(part.s.bos + (int64_t)c * kC);
+            uint8_t *const st = sm + s * G::kStage;
+            auto zero_tail = [&](uint8_t *at, int boxes) {
+                for (int b = 0; b < boxes; ++b)
+                    for (int e = rows * 8 + lane; e < kC * 8; e += 32) *(uint4 *)(at + b * kBox + e * 16) = make_uint4(0, 0, 0, 0);
+                fence_proxy_async();
+                __syncwarp();
+            };
             if (m >= kStages && !(ok = all(wait(kEmpty + s, (m / kStages - 1) & 1)))) break;
+            uint64_t *landing = &bar[rows < kC ? (int)kLanded : kFull + s];
             if (elect_one_sync()) {
-                uint8_t *st = sm + s * G::kStage;
-                const int t0 = (int)(part.s.bos + (int64_t)part.chunk(m, rev) * kC);
-                mbar_arrive_expect_tx(&bar[kFull + s], STATE ? (G::kBoxes + 1) * kBox : G::kStage);
+                mbar_arrive_expect_tx(landing, (STATE ? 1 : 2) * G::kBoxes * kBox);
 #pragma unroll
                 for (int i = 0; i < G::kBoxes; ++i) {
-                    tma_load_3d(st + G::kB + i * kBox, &maps.b[blockIdx.y], i * 64, hv / p.rb, t0, &bar[kFull + s]);
-                    if (!STATE) tma_load_3d(st + G::kA + i * kBox, &maps.a[blockIdx.y], i * 64, hv / p.ra, t0, &bar[kFull + s]);
+                    tma_load_3d(st + G::kB + i * kBox, &maps.b[pi], i * 64, hv / p.rb, t0, landing);
+                    if (!STATE) tma_load_3d(st + G::kA + i * kBox, &maps.a[pi], i * 64, hv / p.ra, t0, landing);
                 }
-                tma_load_3d(st + G::kCc, &maps.c[blockIdx.y], c0, hv / p.rc, t0, &bar[kFull + s]);
             }
             __syncwarp();
+            if (rows < kC) {  // (one chunk of a sequence at most)
+                if (!(ok = all(wait(kLanded, 0)))) break;
+                zero_tail(st + G::kB, G::kBoxes);
+                if (lane == 0) mbar_arrive(&bar[kFull + s]);
+            }
+            const int sc = m % kStagesC;
+            if (m >= kStagesC && !(ok = all(wait(kEmptyC + sc, (m / kStagesC - 1) & 1)))) break;
+            landing = &bar[rows < kC ? (int)kLanded : kFullC + sc];
+            if (elect_one_sync()) {
+                mbar_arrive_expect_tx(landing, kBox);
+                tma_load_3d(sm + G::kCs + sc * kBox, &maps.c[pi], c0, hv / p.rc, t0, landing);
+            }
+            __syncwarp();
+            if (rows < kC) {
+                if (!(ok = all(wait(kLanded, 1)))) break;
+                zero_tail(sm + G::kCs + sc * kBox, 1);
+                if (lane == 0) mbar_arrive(&bar[kFullC + sc]);
+            }
         }
-        for (int i = max(0, m - kStages); i < m; ++i) wait(kFull + i % kStages, (i / kStages) & 1);  // (no copy outlives the CTA)
+        // no copy outlives the CTA
+        for (int i = max(0, m - kStages); i < m; ++i) wait(kFull + i % kStages, (i / kStages) & 1);
+        for (int i = max(0, m - kStagesC); i < m; ++i) wait(kFullC + i % kStagesC, (i / kStagesC) & 1);
     } else if (warp == 1) {
         // ---------------------------------------------------------------- products
-        const uint32_t idZ = idesc_bf16_f32(128, 128, 0, 0), idMN = idesc_bf16_f32(128, kCols, 0, 1), idX = idesc_bf16_f32(128, kCols, 1, 1);
-        const uint64_t dX = sdesc_sw128(base + G::kXs, kBox, 1024), dHi = sdesc_sw128(base + G::kHi, kBox, 1024), dLo = sdesc_sw128(base + G::kLo, kBox, 1024);
+        const uint32_t idZ = idesc_bf16_f32(128, 128, 0, 0), idO = idesc_bf16_f32(128, kCols, 0, 1), idX = idesc_bf16_f32(128, 2 * kCols, 1, 1);
+        const uint64_t dX = sdesc_sw128(base + G::kXs, kBox, 1024), dC = sdesc_sw128(base + G::kParts, kBox, 1024);
         auto scores = [&](int m) {
             const uint32_t st = base + (m % kStages) * G::kStage, z = tmem + kZ + (m & 1) * 128;
             const uint64_t da = sdesc_sw128(st + G::kA, 16, 1024), db = sdesc_sw128(st + G::kB, 16, 1024);
@@ -168,48 +210,46 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
             }
             __syncwarp();
         };
-        bool ok = all(loaded(0));
+        bool ok = loaded(0);
         if (!STATE && ok) scores(0);
         for (int m = 0; m < nm && ok; ++m) {
             const uint32_t st = base + (m % kStages) * G::kStage;
-            if (!(ok = all(wait(kXB, m & 1)))) break;
-            if (!STATE) {
-                if (m > 0 && !(ok = all(wait(kOE, (m - 1) & 1)))) break;
-                const uint64_t da = sdesc_sw128(st + G::kA, 16, 1024);
-                tc_fence_after();
-                if (elect_one_sync()) {
-#pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) mma_ss(tmem + kO1, da + (((ks >> 2) * kBox + (ks & 3) * 32) >> 4), dX + ks * 128, idMN, ks > 0);
-                }
-                __syncwarp();
-            } else if (!(ok = all(loaded(m)))) {
-                break;
-            }
-            if (!(ok = all(wait(kCB, m & 1)))) break;
+            if (STATE && !(ok = loaded(m))) break;
+            if (!(ok = all(wait(kXB, m & 1) && wait(kCB, m & 1)))) break;
             tc_fence_after();
             if (elect_one_sync()) {
                 const uint64_t db = sdesc_sw128(st + G::kB, kBox, 1024);
 #pragma unroll
-                for (int ks = 0; ks < kC / 16; ++ks) mma_ss(tmem + kX, db + ks * 128, dHi + ks * 128, idX, 1u);
-#pragma unroll
-                for (int ks = 0; ks < kC / 16; ++ks) mma_ss(tmem + kX, db + ks * 128, dLo + ks * 128, idX, 1u);
+                for (int ks = 0; ks < kC / 16; ++ks) mma_ss(tmem + kX, db + ks * 128, dC + ks * 128, idX, 1u);
                 mma_commit(&bar[kXF]);
-                if (STATE) mma_commit(&bar[kEmpty + m % kStages]);
+                if (STATE) {
+                    mma_commit(&bar[kEmpty + m % kStages]);
+                    mma_commit(&bar[kEmptyC + m % kStagesC]);
+                }
             }
             __syncwarp();
             if (!STATE) {
-                if (m + 1 < nm) {
-                    if (!(ok = all(loaded(m + 1)))) break;
-                    scores(m + 1);
-                }
-                if (!(ok = all(wait(kZB + (m & 1), (m >> 1) & 1)))) break;
-                const uint64_t dc = sdesc_sw128(st + G::kCc, kBox, 1024);
+                if (m > 0 && !(ok = all(wait(kOE, (m - 1) & 1)))) break;  // the last outputs have been read
+                const uint64_t da = sdesc_sw128(st + G::kA, 16, 1024), dc = sdesc_sw128(base + G::kCs + m % kStagesC * kBox, kBox, 1024);
                 tc_fence_after();
                 if (elect_one_sync()) {
 #pragma unroll
-                    for (int ks = 0; ks < kC / 16; ++ks) mma_ts(tmem + kO2, tmem + kZ + (m & 1) * 128 + ks * 8, dc + ks * 128, idMN, ks > 0);
-                    mma_commit(&bar[kOF]);
+                    for (int ks = 0; ks < D / 16; ++ks) mma_ss(tmem + kO1, da + (((ks >> 2) * kBox + (ks & 3) * 32) >> 4), dX + ks * 128, idO, ks > 0);
+                    mma_commit(&bar[kO1F]);
                     mma_commit(&bar[kEmpty + m % kStages]);
+                }
+                __syncwarp();
+                if (m + 1 < nm) {
+                    if (!(ok = loaded(m + 1))) break;
+                    scores(m + 1);
+                }
+                if (!(ok = all(wait(kZB + (m & 1), (m >> 1) & 1)) && loaded_c(m))) break;
+                tc_fence_after();
+                if (elect_one_sync()) {
+#pragma unroll
+                    for (int ks = 0; ks < kC / 16; ++ks) mma_ts(tmem + kO2, tmem + kZ + (m & 1) * 128 + ks * 8, dc + ks * 128, idO, ks > 0);
+                    mma_commit(&bar[kOF]);
+                    mma_commit(&bar[kEmptyC + m % kStagesC]);
                 }
                 __syncwarp();
             }
@@ -220,20 +260,63 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     } else if (warp >= 4 && warp < 8) {
         // ---------------------------------------------------------------- Z (thread = row)
         if (!STATE) {
-            const int i = tid - 128;
+            const int i = tid - 128, w = warp - 4;
+            const float l1 = decay_pow(g2, 1), l2 = decay_pow(g2, 2);
             for (int m = 0; m < nm; ++m) {
-                if (!all(wait(kZF + (m & 1), (m >> 1) & 1))) break;
+                if (!bar_all(1, 128, w != 0 || wait(kZF + (m & 1), (m >> 1) & 1))) break;
                 tc_fence_after();
                 const uint32_t z = tmem + lanes + kZ + (m & 1) * 128;
-#pragma unroll
+#pragma unroll 1
                 for (int q = 0; q < 4; ++q) {
-                    uint32_t v[32], w[16];
-                    tmem_ld32(z + 32 * q, v);
-                    tmem_ld_wait();
-                    const float *f = tab + 127 + i - 32 * q;
+                    uint32_t v[32], u[16];
+                    if (rev ? q < w : q > w) {  // (all of it on the side that does not count)
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) w[j] = pack_bf16(__uint_as_float(v[2 * j]) * f[-2 * j], __uint_as_float(v[2 * j + 1]) * f[-2 * j - 1]);
-                    tmem_st16(z + 16 * q, w);  // (over columns that are read already)
+                        for (int j = 0; j < 16; ++j) u[j] = 0u;
+                    } else {
+                        tmem_ld32(z + 32 * q, v);
+                        tmem_ld_wait();
+                        float *const x = (float *)v;
+                        // cs l^|i - j| from the column next to the row's own side on, one more l at every step (no table in shared
+                        // memory, which the products keep busy)
+                        if (q == w) {
+                            float f = 0.f;
+                            if (rev) {
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) {
+                                    f = j == lane ? p.cs : f * l1;
+                                    x[j] = j < lane ? 0.f : x[j] * f;
+                                }
+                            } else {
+#pragma unroll
+                                for (int j = 31; j >= 0; --j) {
+                                    f = j == lane ? p.cs : f * l1;
+                                    x[j] = j > lane ? 0.f : x[j] * f;
+                                }
+                            }
+                        } else {
+                            float f = p.cs * decay_pow(g2, rev ? 32 * q - i : i - 32 * q - 31), f1 = f * l1;
+                            if (rev) {
+#pragma unroll
+                                for (int j = 0; j < 32; j += 2) {
+                                    x[j] *= f;
+                                    x[j + 1] *= f1;
+                                    f *= l2;
+                                    f1 *= l2;
+                                }
+                            } else {
+#pragma unroll
+                                for (int j = 31; j > 0; j -= 2) {
+                                    x[j] *= f;
+                                    x[j - 1] *= f1;
+                                    f *= l2;
+                                    f1 *= l2;
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) u[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
+                    }
+                    tmem_st16(z + 16 * q, u);  // (over columns that are read already)
                 }
                 tmem_st_wait();
                 tc_fence_before();
@@ -241,87 +324,93 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
                 if (lane == 0) mbar_arrive(&bar[kZB + (m & 1)]);
             }
         }
-    } else if (warp >= 8 && warp < 12) {
-        // ---------------------------------------------------------------- the state (thread = row of X)
-        const int r = tid - 256;
-        const uint32_t xt = tmem + lanes + kX;
-        float x[kCols];
-        if (r < D) {
-            if (!STATE && mine) {
+    } else if (warp >= 8 && warp < 16) {
+        // ---------------------------------------------------------------- the state (thread = 32 columns of a row of X)
+        const int r = tid & 127, c1 = warp >= 12 ? 32 : 0;
+        const bool real = r < D;
+        const uint32_t xt = tmem + lanes + kX + c1;
+        float x[32];
 #pragma unroll
-                for (int c = 0; c < kCols; c += 4) *(float4 *)&x[c] = *(const float4 *)(mine + (int64_t)r * D + c);
-            } else if (!STATE && p.x0) {
+        for (int c = 0; c < 32; ++c) x[c] = 0.f;
+        if (!STATE && real) {
+            if (mine) {
 #pragma unroll
-                for (int c = 0; c < kCols; ++c) x[c] = p.x0[xat(r, c)];
-            } else {
+                for (int c = 0; c < 32; c += 4) *(float4 *)&x[c] = *(const float4 *)(mine + (int64_t)r * D + c1 + c);
+            } else if (p.x0) {
 #pragma unroll
-                for (int c = 0; c < kCols; ++c) x[c] = 0.f;
+                for (int c = 0; c < 32; ++c) x[c] = p.x0[xat(r, c1 + c)];
             }
-        } else {
-#pragma unroll
-            for (int c = 0; c < kCols; ++c) x[c] = 0.f;
         }
+        // the sum of the two accumulators
         auto read = [&]() {
+            float y[32];
             tc_fence_after();
             tmem_ld32(xt, (uint32_t *)x);
-            tmem_ld32(xt + 32, (uint32_t *)x + 32);
+            tmem_ld32(xt + kCols, (uint32_t *)y);
             tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[k] += y[k];
         };
         bool ok = true;
         for (int m = 0; m < nm; ++m) {
-            const int c = part.chunk(m, rev);
-            const Decayed down(g, part.rows(c) - (rev && part.m0 + m == 0));
+            const int rows = part.rows(part.chunk(m, rev)), late = rev && part.m0 + m == 0;
+            const Decayed down(g, rows - late);
             if (m > 0) {
-                if (!(ok = all(wait(kXF, (m - 1) & 1)))) break;
+                if (!(ok = bar_all(2, 256, warp != 8 || wait(kXF, (m - 1) & 1)))) break;
                 read();
             }
-            if (!STATE && r < D) {
+            const uint32_t none[32] = {};
+            tmem_st32(xt + kCols, none);
 #pragma unroll
-                for (int i = 0; i < kCols / 8; ++i) *(uint4 *)(sm + G::kXs + sw128(r, 8 * i)) = pack8(x + 8 * i);
+            for (int q = 0; q < 2; ++q) {
+                float y[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) y[k] = down(x[16 * q + k]);
+                tmem_st16(xt + 16 * q, (const uint32_t *)y);
             }
+            if (!STATE) {
+                if (m > 0 && !(ok = bar_all(2, 256, warp != 8 || wait(kO1F, (m - 1) & 1)))) break;  // the last copy has been read
+                if (real) {
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) x[i] = down(x[i]);
-            tmem_st32(xt, (const uint32_t *)x);
-            tmem_st32(xt + 32, (const uint32_t *)x + 32);
+                    for (int i = 0; i < 32; i += 8) *(uint4 *)(sm + G::kXs + sw128(r, c1 + i)) = pack8(x + i);
+                }
+                fence_proxy_async();
+            }
             tmem_st_wait();
             tc_fence_before();
-            fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[kXB]);
         }
-        if (ok && (STATE || (p.x1 && last_seg)) && all(wait(kXF, (nm - 1) & 1))) {
+        if (ok && (STATE || (p.x1 && last_seg)) && bar_all(2, 256, warp != 8 || wait(kXF, (nm - 1) & 1))) {
             read();
             const Decayed down(g, rev && !STATE ? 1 : 0);
-            if (r < D) {
+            if (real) {
                 if (STATE) {
 #pragma unroll
-                    for (int c = 0; c < kCols; c += 4) *(float4 *)(mine + (int64_t)r * D + c) = *(const float4 *)&x[c];
+                    for (int c = 0; c < 32; c += 4) *(float4 *)(mine + (int64_t)r * D + c1 + c) = *(const float4 *)&x[c];
                 } else {
 #pragma unroll
-                    for (int c = 0; c < kCols; ++c) p.x1[xat(r, c)] = down(x[c]);
+                    for (int c = 0; c < 32; ++c) p.x1[xat(r, c1 + c)] = down(x[c]);
                 }
             }
         }
-    } else if (warp >= 12 && warp < 16) {
+    } else if (warp >= 16 && warp < 20) {
         // ---------------------------------------------------------------- outputs (thread = row)
         if (!STATE) {
-            const int i = tid - 384;
-            const uint32_t o1 = tmem + lanes + kO1, o2 = tmem + lanes + kO2;
-            uint8_t *const tile = sm + G::kOut;
+            const int i = tid & 127;
+            const bool wide = ((uintptr_t)p.out & 31) == 0;
             for (int m = 0; m < nm; ++m) {
-                const int c = part.chunk(m, rev), rows = part.rows(c);
-                const int late = rev && part.m0 + m == 0;
+                const int c = part.chunk(m, rev), rows = part.rows(c), late = rev && part.m0 + m == 0;
                 const float f = p.os * decay_pow(g2, rev ? max(rows - i - late, 0) : i + 1);
-                const int64_t t0 = part.s.bos + (int64_t)c * kC;
-                const bool ok = wait(kOF, m & 1);
-                if (tid == 384) tma_store_wait_read0();
-                if (!bar_all(1, 128, ok)) break;  // (together: the others would wait for a warp that gave up)
+                const uint32_t o1 = tmem + lanes + kO1, o2 = tmem + lanes + kO2;
+                const int64_t at = ((part.s.bos + (int64_t)c * kC + i) * args.HV + hv) * D + c0;
+                if (!bar_all(3, 128, warp != 16 || wait(kOF, m & 1))) break;
                 tc_fence_after();
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    float u[32], w[32];
-                    tmem_ld32(o1 + 32 * q, (uint32_t *)u);
-                    tmem_ld32(o2 + 32 * q, (uint32_t *)w);
+                    float u[32], v[32];
+                    tmem_ld32(o2 + 32 * q, (uint32_t *)u);
+                    tmem_ld32(o1 + 32 * q, (uint32_t *)v);
                     tmem_ld_wait();
                     if (q == 1) {
                         tc_fence_before();
@@ -329,72 +418,59 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
                         if (lane == 0) mbar_arrive(&bar[kOE]);
                     }
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) u[k] = fmaf(f, u[k], p.os * w[k]);
-                    if (p.out_f32) {
-                        if (i < rows) {
-                            float *dst = (float *)p.out + ((t0 + i) * args.HV + hv) * D + c0 + 32 * q;
+                    for (int k = 0; k < 32; ++k) u[k] = fmaf(f, v[k], p.os * u[k]);
+                    if (i < rows) {
+                        if (p.out_f32) {
+                            float *dst = (float *)p.out + at + 32 * q;
 #pragma unroll
                             for (int k = 0; k < 32; k += 4) *(float4 *)(dst + k) = *(const float4 *)&u[k];
-                        }
-                    } else {
+                        } else {
+                            __nv_bfloat16 *dst = (__nv_bfloat16 *)p.out + at + 32 * q;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) *(uint4 *)(tile + sw128(i, 32 * q + 8 * k)) = pack8(u + 8 * k);
-                    }
-                }
-                if (!p.out_f32) {
-                    if (rows == kC) fence_proxy_async();
-                    bar_sync(1, 128);
-                    if (rows == kC) {
-                        if (tid == 384) {
-                            tma_store_3d(&maps.out[blockIdx.y], tile, c0, hv, (int)t0);
-                            tma_store_commit();
+                            for (int k = 0; k < 32; k += 16) {
+                                const uint4 y = pack8(u + k), z = pack8(u + k + 8);
+                                if (wide) {  // (a whole sector by one thread)
+                                    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst + k), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w),
+                                                 "r"(z.x), "r"(z.y), "r"(z.z), "r"(z.w)
+                                                 : "memory");
+                                } else {
+                                    *(uint4 *)(dst + k) = y;
+                                    *(uint4 *)(dst + k + 8) = z;
+                                }
+                            }
                         }
-                    } else {
-                        for (int k = i; k < rows * 8; k += 128)
-                            *(uint4 *)((__nv_bfloat16 *)p.out + ((t0 + (k >> 3)) * args.HV + hv) * D + c0 + 8 * (k & 7)) =
-                                *(const uint4 *)(tile + sw128(k >> 3, 8 * (k & 7)));
                     }
+                    __syncwarp();
                 }
             }
-            if (tid == 384) tma_store_wait0();
         }
-    } else if (warp >= 16) {
-        // ---------------------------------------------------------------- C: c's rows scaled (thread = row)
-        const int j = tid - 512;
+    } else if (warp >= 20) {
+        // ---------------------------------------------------------------- C in two parts (thread = 32 columns of a row)
+        const int j = tid & 127, i0 = warp >= 24 ? 4 : 0;
         for (int m = 0; m < nm; ++m) {
             const int rows = part.rows(part.chunk(m, rev));
-            uint8_t *const stage = sm + (m % kStages) * G::kStage, *const src = stage + G::kCc;
-            if (!all(wait(kFull + m % kStages, (m / kStages) & 1))) break;
-            if (m == ragged) {  // the rows behind the end are the next sequence's, and 0 x NaN is NaN
-                if (j >= rows) {
-#pragma unroll
-                    for (int b = 0; b <= G::kBoxes; ++b)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) *(uint4 *)(stage + G::kB + b * kBox + j * 128 + i * 16) = make_uint4(0, 0, 0, 0);
-                }
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[kFix]);
-            }
             const float f = j < rows ? p.cs * decay_pow(g2, rev ? j : rows - 1 - j) : 0.f;
-            uint4 hi[8], lo[8];
+            const uint8_t *const src = sm + G::kCs + m % kStagesC * kBox;
+            uint8_t *const dst = sm + G::kParts;
+            if (!bar_all(4, 256, warp != 20 || loaded_c(m))) break;
+            uint4 hi[4], lo[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint4 raw = *(const uint4 *)(src + sw128(j, 8 * i));
+            for (int i = 0; i < 4; ++i) {
+                const uint4 raw = *(const uint4 *)(src + sw128(j, 8 * (i0 + i)));
                 const uint32_t *w = (const uint32_t *)&raw;
                 uint32_t *ph = (uint32_t *)&hi[i], *pl = (uint32_t *)&lo[i];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const float u = f * __uint_as_float(w[k] << 16), v = f * __uint_as_float(w[k] & 0xffff0000u);
+                    const float u = f * low_bf16(w[k]), v = f * high_bf16(w[k]);
                     ph[k] = pack_bf16(u, v);
-                    pl[k] = pack_bf16(u - __uint_as_float(ph[k] << 16), v - __uint_as_float(ph[k] & 0xffff0000u));
+                    pl[k] = pack_bf16(u - low_bf16(ph[k]), v - high_bf16(ph[k]));
                 }
             }
-            if (m > 0 && !all(wait(kXF, (m - 1) & 1))) break;  // the products have read the last chunk's
+            if (m > 0 && !bar_all(4, 256, warp != 20 || wait(kXF, (m - 1) & 1))) break;  // the products have read the last chunk's
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                *(uint4 *)(sm + G::kHi + sw128(j, 8 * i)) = hi[i];
-                *(uint4 *)(sm + G::kLo + sw128(j, 8 * i)) = lo[i];
+            for (int i = 0; i < 4; ++i) {
+                *(uint4 *)(dst + sw128(j, 8 * (i0 + i))) = hi[i];
+                *(uint4 *)(dst + kBox + sw128(j, 8 * (i0 + i))) = lo[i];
             }
             fence_proxy_async();
             __syncwarp();
@@ -455,7 +531,6 @@ cudaError_t launch(const LinArgs &a, void *ws, int64_t tokens, cudaStream_t st)
         if (!heads_map(&maps.a[i], p.a, D, a.HV / p.ra, tokens, p.lda, kC) || !heads_map(&maps.b[i], p.b, D, a.HV / p.rb, tokens, p.ldb, kC) ||
             !heads_map(&maps.c[i], p.c, D, a.HV / p.rc, tokens, p.ldc, kC))
             return cudaErrorInvalidValue;
-        if (!p.out_f32 && !heads_map(&maps.out[i], p.out, D, a.HV, tokens, (int64_t)a.HV * D, kC)) return cudaErrorInvalidValue;
     }
     const LinPlan plan = lin_tc_plan(a, D);
     Split split{};
@@ -469,9 +544,9 @@ cudaError_t launch(const LinArgs &a, void *ws, int64_t tokens, cudaStream_t st)
         if (e != cudaSuccess) return e;
         done_on_device(seen);
     }
-    const int64_t ctas = plan.slots * a.HV * (D / kCols), elements = (int64_t)a.N * a.HV * D * D;
+    const int64_t ctas = plan.slots * a.HV * (D / kCols) * a.passes, elements = (int64_t)a.N * a.HV * D * D;
     if (ctas > INT32_MAX || elements / 256 > INT32_MAX) return cudaErrorInvalidConfiguration;
-    const dim3 grid((unsigned)ctas, a.passes);
+    const unsigned grid = (unsigned)ctas;
     const int withhold = withhold_loads();
     const uint64_t limit = withhold ? kTestWaitLimitNs : kWaitLimitNs;
     if (split.states) {

@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kThreads, 1) win_dq_kernel(const __grid_consta
     using G = Geo<D, ring_of_dq(D)>;
     constexpr uint32_t kS = 0, kP = 256, kQ = 384;  // S: two buffers (Z in their place), dP, dQ
     extern __shared__ uint8_t win_bwd_smem[];
-    uint8_t *sm = (uint8_t *)(((uintptr_t)win_bwd_smem + 1023) & ~(uintptr_t)1023);
+    uint8_t *const sm = win_bwd_smem + (-smem_u32(win_bwd_smem) & 1023u);  // (an offset: a cast would lose that it is shared memory)
     const Tile tl = tile_of(a.cu_q, a.N, a.Tq, kTile, blockIdx.x);
     const SeqRange sq = seq_range(a.cu_q, tl.n, a.Tq), sk = seq_range(a.cu_k, tl.n, a.Tk);
     const int i0 = tl.index * kTile, rows = min(kTile, sq.len - i0), h = blockIdx.y, hk = h / (a.H / a.HK);
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1) win_dkv_kernel(const __grid_const
     using G = Geo<D, 4>;
     constexpr uint32_t kS = 0, kP = 128, kV = 256, kK = 384;  // S^T (P^T in its place), dP^T (Z^T), dV, dK
     extern __shared__ uint8_t win_bwd_smem[];
-    uint8_t *sm = (uint8_t *)(((uintptr_t)win_bwd_smem + 1023) & ~(uintptr_t)1023);
+    uint8_t *const sm = win_bwd_smem + (-smem_u32(win_bwd_smem) & 1023u);  // (an offset: a cast would lose that it is shared memory)
     const int hk = blockIdx.y, per = a.H / a.HK;
     // a tile of keys, or a run of queries against a tile of sinks
     const bool run = blockIdx.x >= key_tiles;

@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kThreads, 1) win_tc_kernel(const __grid_consta
 {
     using G = Geo<D>;
     extern __shared__ uint8_t win_tc_smem[];
-    uint8_t *sm = (uint8_t *)(((uintptr_t)win_tc_smem + 1023) & ~(uintptr_t)1023);
+    uint8_t *const sm = win_tc_smem + (-smem_u32(win_tc_smem) & 1023u);  // (an offset: a cast would lose that it is shared memory)
     const Tile tl = tile_of(a.cu_q, a.N, a.Tq, by_heads ? kTile : 2 * kTile, blockIdx.x);
     const SeqRange sq = seq_range(a.cu_q, tl.n, a.Tq), sk = seq_range(a.cu_k, tl.n, a.Tk);
     const int h0 = by_heads ? 2 * blockIdx.y : blockIdx.y, hk = h0 / (a.H / a.HK), off = sk.len - sq.len;
