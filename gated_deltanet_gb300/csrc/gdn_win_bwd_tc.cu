@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1) win_dq_kernel(const __grid_consta
         if (lse == -INFINITY) lse = INFINITY;  // a row that sees nothing: weights of zero
         // delta: each group half of the row, from dO in shared memory and o
         float d = 0.f;
-        bool ok = wait(kIn, 0);
+        bool ok = bar_all(1, 256, warp != 0 || wait(kIn, 0));
         if (ok && r < rows) {
             const __nv_bfloat16 *o = (const __nv_bfloat16 *)a.o + ((sq.bos + i0 + r) * a.H + h) * D + x * (D / 2);
 #pragma unroll
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) win_dq_kernel(const __grid_consta
         for (int t = 0; t < nt && ok; ++t) {
             const int j0 = key0(t) + 64 * x, cols = columns(t) - 64 * x;
             const uint32_t ts = tmem + lanes + kS + (t & 1) * 128 + 64 * x, tp = tmem + lanes + kP + 64 * x;
-            if (!(ok = all(wait(kSF + (t & 1), (t >> 1) & 1)))) break;
+            if (!(ok = bar_all(1, 256, warp != 0 || wait(kSF + (t & 1), (t >> 1) & 1)))) break;
             tc_fence_after();
             float s[64];
             tmem_ld32(ts, (uint32_t *)s);
@@ -266,9 +266,9 @@ __global__ void __launch_bounds__(kThreads, 1) win_dq_kernel(const __grid_consta
                 const int end = min(cols, p - j0 + 1), begin = p - a.window + 1 - j0, sink = a.sinks - j0;
 #pragma unroll
                 for (int j = 0; j < 64; ++j)
-                    if (j >= end || (j < begin && j >= sink)) s[j] = 0.f;
+                    s[j] = (int)(j < end) & ((int)(j >= begin) | (int)(j < sink)) ? s[j] : 0.f;
             }
-            if (!(ok = all(wait(kPF, t & 1)))) break;
+            if (!(ok = bar_all(1, 256, warp != 0 || wait(kPF, t & 1)))) break;
             tc_fence_after();
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1) win_dq_kernel(const __grid_consta
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[kZB]);
         }
-        ok = bar_all(1, 256, wait(kDone, 0) && ok);
+        ok = bar_all(1, 256, (warp != 0 || wait(kDone, 0)) && ok);
         if (ok) {
             tc_fence_after();
             uint8_t *tile = sm + G::kA;  // (the last scores are taken)
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1) win_dkv_kernel(const __grid_const
             float *const ls = stats + (t & 1) * 128, *const dl = ls + 64;
             ls[r] = next;
             if (t + 1 < nt) next = stat(t + 1);
-            if (!(ok = bar_all(1 + x, 128, ok && wait(kSF, t & 1)))) break;  // (the group leaves together)
+            if (!(ok = bar_all(1 + x, 128, (warp & 3) || wait(kSF, t & 1)))) break;  // (the group leaves together)
             tc_fence_after();
             float s[64];
             tmem_ld32(ts, (uint32_t *)s);
@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1) win_dkv_kernel(const __grid_const
                 const int first = j - q0, last = j < a.sinks ? rows : (int)min((int64_t)rows, (int64_t)j + a.window - q0);
 #pragma unroll
                 for (int k = 0; k < 64; ++k)
-                    if (k < first || k >= last) s[k] = 0.f;
+                    s[k] = (int)(k >= first) & (int)(k < last) ? s[k] : 0.f;
             }
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1) win_dkv_kernel(const __grid_const
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[kPB]);
-            ok = all(wait(kPF, t & 1));
+            if (!(ok = bar_all(1 + x, 128, (warp & 3) || wait(kPF, t & 1)))) break;
             tc_fence_after();
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) win_dkv_kernel(const __grid_const
             if (lane == 0) mbar_arrive(&bar[kZB]);
         }
         // ---------------------------------------------------------------- dV by the first group, dK by the second
-        ok = bar_all(1 + x, 128, wait(kDone, 0) && ok);
+        ok = bar_all(1 + x, 128, ((warp & 3) || wait(kDone, 0)) && ok);
         if (ok) {
             tc_fence_after();
             const float f = x == 0 ? 1.f : a.scale;

@@ -8,8 +8,9 @@
 // passes the old by more than 8 (P then stays below 2^8, in fp32's and bf16's range; the rounding of P is relative), so that most
 // tiles leave O alone.
 //
-// Warps: 0-3 and 4-7 softmax of A and B (thread = row) and their outputs, 8 loads (a ring of K and V tiles) and zeroes the
-// V rows behind a sequence's end (they are the next sequence's, and 0 x NaN is NaN), 9 products.
+// Warps: 0-7 and 8-15 softmax of A and B and their outputs (two threads to a row: with one a tile's softmax took 3800 cycles, one warp to
+// a scheduler and side having nothing to hide its latencies behind), 16 loads (a ring of K and V tiles) and zeroes the V rows behind a
+// sequence's end (they are the next sequence's, and 0 x NaN is NaN), 17 products.
 // The products are issued S_A(t), PV_B(t-1), S_B(t), PV_A(t): S(t) is complete only when PV(t-1) is, which is why a softmax that sees
 // its scores may also touch its O.
 #include "gdn_mix.cuh"
@@ -20,7 +21,7 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kTile = 128, kThreads = 320, kBox = kTile * 128;
+constexpr int kTile = 128, kThreads = 640, kBox = kTile * 128;
 constexpr uint32_t kS = 0, kO = 256, kTmem = 512;  // + 128 for tile B
 constexpr float kRaise = 8.f;
 
@@ -29,8 +30,8 @@ __device__ unsigned g_win_status;
 template <int D>
 struct Geo {
     static constexpr int kBoxes = D / 64, kUnit = kBoxes * kBox;
-    static constexpr int kRing = D == 128 ? 5 : 8;  // K and V tiles in flight
-    static constexpr int kQ = 0, kKV = 2 * kUnit, kBars = kKV + kRing * kUnit, kSmem = kBars + 256 + 1024;
+    static constexpr int kRing = D == 128 ? 4 : 8;  // K and V tiles in flight
+    static constexpr int kQ = 0, kKV = 2 * kUnit, kRed = kKV + kRing * kUnit, kBars = kRed + 2048, kSmem = kBars + 256 + 1024;
 };
 enum Bar { kQF, kSF, kPB = kSF + 2, kDone = kPB + 2, kLanded = kDone + 2, kFin, kFull, kMostRing = 8, kEmpty = kFull + kMostRing, kNumBars = kEmpty + kMostRing };
 
@@ -45,7 +46,8 @@ struct Side {
     __device__ bool needs(int j0, int sinks) const { return rows > 0 && j0 < hi && (j0 + kTile > lo || j0 < sinks); }
     __device__ bool whole(int j0, int cols, int window, int sinks) const
     {
-        return cols == kTile && j0 + kTile - 1 <= p0 && (p0 + rows - 1 - j0 < window || j0 + kTile <= sinks);
+        // of the 64 keys from j0 on
+        return cols >= 64 && j0 + 63 <= p0 && (p0 + rows - 1 - j0 < window || j0 + 64 <= sinks);
     }
 };
 
@@ -83,7 +85,7 @@ __global__ void __launch_bounds__(kThreads, 1) win_tc_kernel(const __grid_consta
         mbar_init(&bar[kQF], 1);
         for (int x = 0; x < 2; ++x) {
             mbar_init(&bar[kSF + x], 1);
-            mbar_init(&bar[kPB + x], 4);
+            mbar_init(&bar[kPB + x], 8);
             mbar_init(&bar[kDone + x], 1);
         }
         mbar_init(&bar[kLanded], 1);
@@ -94,7 +96,7 @@ __global__ void __launch_bounds__(kThreads, 1) win_tc_kernel(const __grid_consta
         }
         fence_mbar_init();
     }
-    if (warp == 8) tmem_alloc(tslot, kTmem);
+    if (warp == 16) tmem_alloc(tslot, kTmem);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -105,7 +107,7 @@ __global__ void __launch_bounds__(kThreads, 1) win_tc_kernel(const __grid_consta
     // unit i of the ring: K of tile i / 2, or its V
     auto full = [&](int i) { return all(wait(kFull + i % G::kRing, (i / G::kRing) & 1)); };
 
-    if (warp == 8) {
+    if (warp == 16) {
         // ---------------------------------------------------------------- loads
         bool ok = !withhold;
         if (ok && elect_one_sync()) {
@@ -143,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1) win_tc_kernel(const __grid_consta
         }
         if (!withhold) wait(kQF, 0);
         for (int k = max(0, i - G::kRing); k < i; ++k) wait(kFull + k % G::kRing, (k / G::kRing) & 1);  // (no copy outlives the CTA)
-    } else if (warp == 9) {
+    } else if (warp == 17) {
         // ---------------------------------------------------------------- products
         const uint32_t idS = idesc_bf16_f32(128, 128, 0, 0), idO = idesc_bf16_f32(128, D, 0, 1);
         auto unit = [&](int i) { return base + G::kKV + (i % G::kRing) * G::kUnit; };
@@ -159,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1) win_tc_kernel(const __grid_consta
         auto output = [&](int x, int t, bool fresh) {
             const uint64_t dv = sdesc_sw128(unit(2 * t + 1), kBox, 1024);
 #pragma unroll
-            for (int ks = 0; ks < kTile / 16; ++ks) mma_ts(tmem + kO + 128 * x, tmem + kS + 128 * x + ks * 8, dv + ks * 128, idO, !fresh || ks > 0);
+            for (int ks = 0; ks < kTile / 16; ++ks) mma_ts(tmem + kO + 128 * x, tmem + kS + 128 * x + (ks >> 2) * 64 + (ks & 3) * 8, dv + ks * 128, idO, !fresh || ks > 0);
         };
         bool ok = all(wait(kQF, 0));
         int done[2] = {0, 0}, late = -1;  // late: the tile whose PV_B is still to come
@@ -212,52 +214,64 @@ __global__ void __launch_bounds__(kThreads, 1) win_tc_kernel(const __grid_consta
         }
         __syncwarp();
         wait(kFin, 0);
-    } else {
-        // ---------------------------------------------------------------- softmax (thread = row)
-        const int x = warp >> 2, r = tid & 127;
+    } else if (warp < 16) {
+        // ---------------------------------------------------------------- softmax (thread = half a row: 64 of a tile's keys)
+        const int x = warp >> 3, half = warp >> 2 & 1, r = tid & 127, bar_id = 1 + x;
+        const bool leads = (warp & 7) == 0;  // (one warp of a side polls, the others meet it: polls take instructions from those who work)
         const Side s = side_of(x);
-        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16, ts = tmem + lanes + kS + 128 * x, to = tmem + lanes + kO + 128 * x;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16, ts = tmem + lanes + kS + 128 * x, to = tmem + lanes + kO + 128 * x + half * (D / 2);
         const float c = a.scale * kLog2e;
         const int p = s.p0 + r;
+        float *const red = (float *)(sm + G::kRed) + x * 256;  // [half][row]: the halves' maxima, last their sums
         float m = -INFINITY, l = 0.f;
         int done = 0;
         bool ok = true;
-        for (int t = 0; t < nt && ok; ++t) {
-            const int j0 = key0(t), cols = columns(t);
-            if (!s.needs(j0, a.sinks)) continue;
-            if (!(ok = all(wait(kSF + x, done & 1)))) break;
+        for (int t = 0; t < nt; ++t) {
+            const int j0 = key0(t) + 64 * half, cols = columns(t) - 64 * half;
+            if (!s.needs(key0(t), a.sinks)) continue;
+            if (!(ok = bar_all(bar_id, 256, !leads || wait(kSF + x, done & 1)))) break;
             tc_fence_after();
-            float z[128];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, (uint32_t *)z + 32 * q);
+            float z[64];
+            tmem_ld32(ts + 64 * half, (uint32_t *)z);
+            tmem_ld32(ts + 64 * half + 32, (uint32_t *)z + 32);
             tmem_ld_wait();
             if (!s.whole(j0, cols, a.window, a.sinks)) {
-                const int end = min(cols, p - j0 + 1), begin = p - a.window + 1 - j0, sink = a.sinks - j0;
+                const int end = min(cols, p - j0 + 1), begin = p - a.window + 1 - j0, sink = max(a.sinks - j0, 0);
+                if (__any_sync(0xffffffffu, end < 64)) {
 #pragma unroll
-                for (int j = 0; j < 128; ++j)
-                    if (j >= end || (j < begin && j >= sink)) z[j] = -INFINITY;
+                    for (int j = 0; j < 64; ++j) z[j] = j < end ? z[j] : -INFINITY;
+                }
+                if (__any_sync(0xffffffffu, sink < begin)) {
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) z[j] = (int)(j >= begin) | (int)(j < sink) ? z[j] : -INFINITY;
+                }
             }
             float top[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 top[q] = z[q];
 #pragma unroll
-                for (int j = 4 + q; j < 128; j += 4) top[q] = fmaxf(top[q], z[j]);
+                for (int j = 4 + q; j < 64; j += 4) top[q] = fmaxf(top[q], z[j]);
             }
-            const float mx = c * fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-            if (__any_sync(0xffffffffu, mx > m + kRaise)) {
+            float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+            mx *= c;
+            if (bar_any(bar_id, 256, mx > m + kRaise)) {
+                red[half * 128 + r] = mx;
+                bar_sync(bar_id, 256);
+                mx = fmaxf(mx, red[(half ^ 1) * 128 + r]);
+                bar_sync(bar_id, 256);  // (the place is written again)
                 const float raised = fmaxf(m, mx), f = m == -INFINITY ? 0.f : ex2(m - raised);
                 l *= f;
                 m = raised;
                 if (done > 0) {
-#pragma unroll
+#pragma unroll 1
                     for (int q = 0; q < D / 32; ++q) {
-                        float o[32];
-                        tmem_ld32(to + 32 * q, (uint32_t *)o);
+                        float o[16];
+                        tmem_ld16(to + 16 * q, (uint32_t *)o);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] *= f;
-                        tmem_st32(to + 32 * q, (const uint32_t *)o);
+                        for (int j = 0; j < 16; ++j) o[j] *= f;
+                        tmem_st16(to + 16 * q, (const uint32_t *)o);
                     }
                 }
             }
@@ -265,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1) win_tc_kernel(const __grid_consta
             const Pair cc = pair_of(c, c), minus = pair_of(-mm, -mm), one = pair_of(1.f, 1.f);
             Pair sum[2] = {pair_of(0.f, 0.f), pair_of(0.f, 0.f)};
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < 2; ++q) {
                 uint32_t w[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
@@ -276,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1) win_tc_kernel(const __grid_consta
                     sum[j & 1] = fma2(pair_of(u, v), one, sum[j & 1]);
                     w[j] = pack_bf16(u, v);
                 }
-                tmem_st16(ts + 16 * q, w);
+                tmem_st16(ts + 64 * half + 16 * q, w);  // (in the place of this half's scores)
             }
             tmem_st_wait();
             tc_fence_before();
@@ -288,14 +302,18 @@ __global__ void __launch_bounds__(kThreads, 1) win_tc_kernel(const __grid_consta
             l += (u[0] + u[1]) + (u[2] + u[3]);
             ++done;
         }
-        // ---------------------------------------------------------------- outputs
-        ok = bar_all(1 + x, 128, wait(kDone + x, 0) && ok);
+        // ---------------------------------------------------------------- outputs (thread = half a row)
+        ok = bar_all(bar_id, 256, (!leads || wait(kDone + x, 0)) && ok);
         if (ok && s.rows > 0) {
             tc_fence_after();
+            red[half * 128 + r] = l;
+            bar_sync(bar_id, 256);
+            l += red[(half ^ 1) * 128 + r];
             const float inv = l == 0.f ? 0.f : 1.f / l;
             uint8_t *tile = sm + G::kQ + x * G::kUnit;  // (the last scores are taken)
 #pragma unroll
-            for (int q = 0; q < D / 32; ++q) {
+            for (int q = 0; q < D / 64; ++q) {
+                const int col = half * (D / 2) + 32 * q;
                 float o[32];
                 if (done > 0) {
                     tmem_ld32(to + 32 * q, (uint32_t *)o);
@@ -304,22 +322,22 @@ __global__ void __launch_bounds__(kThreads, 1) win_tc_kernel(const __grid_consta
 #pragma unroll
                 for (int j = 0; j < 32; ++j) o[j] = done > 0 && l != 0.f ? o[j] * inv : 0.f;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) *(uint4 *)(tile + (q >> 1) * kBox + sw128(r, 32 * (q & 1) + 8 * j)) = pack8(o + 8 * j);
+                for (int j = 0; j < 4; ++j) *(uint4 *)(tile + (col >> 6) * kBox + sw128(r, (col & 63) + 8 * j)) = pack8(o + 8 * j);
             }
-            if (a.lse && r < s.rows)
+            if (half == 0 && a.lse && r < s.rows)
                 a.lse[lse_at(a, tl.n, sq.bos, s.h) + s.i0 + r] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
             fence_proxy_async();
-            bar_sync(1 + x, 128);
+            bar_sync(bar_id, 256);
             const int64_t t0 = sq.bos + s.i0;
             if (s.rows == kTile) {
-                if (r == 0) {
+                if (half == 0 && r == 0) {
 #pragma unroll
                     for (int b = 0; b < G::kBoxes; ++b) tma_store_3d(&maps.o, tile + b * kBox, b * 64, s.h, (int)t0);
                     tma_store_commit();
                     tma_store_wait0();
                 }
             } else {
-                for (int k = r; k < s.rows * (D / 8); k += 128) {
+                for (int k = half * 128 + r; k < s.rows * (D / 8); k += 256) {
                     const int row = k / (D / 8), e = k % (D / 8) * 8;
                     *(uint4 *)((__nv_bfloat16 *)a.o + ((t0 + row) * a.H + s.h) * D + e) = *(const uint4 *)(tile + (e >> 6) * kBox + sw128(row, e & 63));
                 }
@@ -328,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) win_tc_kernel(const __grid_consta
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == 16) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmem);
     }
