@@ -133,6 +133,11 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
         mbar_init(&bar[kFin], 1);
         fence_mbar_init();
     }
+    if (tid == 32) {
+        prefetch_map(&maps.b[pi]);
+        prefetch_map(&maps.a[pi]);
+        prefetch_map(&maps.c[pi]);
+    }
     if (warp == 3) tmem_alloc(tslot, kTmem);
     tc_fence_before();
     __syncthreads();

@@ -32,8 +32,8 @@ struct Tile {
 __device__ __forceinline__ Tile tile_of(const int64_t *cu, int N, int T, int tile, int64_t slot)
 {
     if (!cu) {
-        const int per = (T + tile - 1) / tile;
-        return {(int)(slot / per), (int)(slot % per)};
+        const unsigned per = (unsigned)(T + tile - 1) / tile, n = (unsigned)slot / per;  // (slots of equal lengths are grid indices: 31 bits)
+        return {(int)n, (int)((unsigned)slot - n * per)};
     }
     int lo = 0, hi = N - 1;  // the last n whose first slot is not past this one
     while (lo < hi) {

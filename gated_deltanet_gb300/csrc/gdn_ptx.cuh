@@ -159,6 +159,8 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void 
                  "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(src))
                  : "memory");
 }
+// the map itself is on its way to the copy unit's cache before the first copy asks for it
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) { asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory"); }
 // true on one lane of a converged warp
 __device__ __forceinline__ bool elect_one_sync()
 {

@@ -113,6 +113,13 @@ __global__ void __launch_bounds__(kThreads, 1) win_dq_kernel(const __grid_consta
     const SeqRange sq = seq_range(a.cu_q, tl.n, a.Tq), sk = seq_range(a.cu_k, tl.n, a.Tk);
     const int i0 = tl.index * kTile, rows = min(kTile, sq.len - i0), h = blockIdx.y, hk = h / (a.H / a.HK);
     if (rows <= 0) return;
+    // o for delta, asked for first: half of its row by each thread of the two groups
+    uint4 row[D / 16];
+    if (threadIdx.x < 256 && (threadIdx.x & 127) < rows) {
+        const uint4 *o = (const uint4 *)((const __nv_bfloat16 *)a.o + ((sq.bos + i0 + (threadIdx.x & 127)) * a.H + h) * D + (threadIdx.x >> 7) * (D / 2));
+#pragma unroll
+        for (int e = 0; e < D / 16; ++e) row[e] = o[e];
+    }
     const int p0 = i0 + sk.len - sq.len;
     const int hi = min(max(p0 + rows, 0), sk.len), lo = hi == 0 ? 0 : min(max(p0 - a.window + 1, 0), hi);
     const int first = min(a.sinks, lo), nfirst = (first + kTile - 1) / kTile, nt = nfirst + (hi - lo + kTile - 1) / kTile;
@@ -124,6 +131,12 @@ __global__ void __launch_bounds__(kThreads, 1) win_dq_kernel(const __grid_consta
     uint64_t *bar = (uint64_t *)(sm + G::kBars);
     uint32_t *tslot = (uint32_t *)(bar + kNumBars);
     if (tid == 0) init_bars(bar, G::kRing);
+    if (tid == 32) {
+        prefetch_map(&maps.q);
+        prefetch_map(&maps.dout);
+        prefetch_map(&maps.k);
+        prefetch_map(&maps.v);
+    }
     if (warp == 8) tmem_alloc(tslot, kTmem);
     tc_fence_before();
     __syncthreads();
@@ -227,10 +240,9 @@ __global__ void __launch_bounds__(kThreads, 1) win_dq_kernel(const __grid_consta
         float d = 0.f;
         bool ok = bar_all(1, 256, warp != 0 || wait(kIn, 0));
         if (ok && r < rows) {
-            const __nv_bfloat16 *o = (const __nv_bfloat16 *)a.o + ((sq.bos + i0 + r) * a.H + h) * D + x * (D / 2);
 #pragma unroll
             for (int e = 0; e < D / 2; e += 8) {
-                const uint4 u = *(const uint4 *)(o + e);
+                const uint4 u = row[e / 8];
                 const int col = x * (D / 2) + e;
                 const uint4 g = *(const uint4 *)(sm + G::kB + (col >> 6) * kBox + sw128(r, col & 63));
                 const uint32_t *pu = (const uint32_t *)&u, *pg = (const uint32_t *)&g;
@@ -369,6 +381,12 @@ __global__ void __launch_bounds__(kThreads, 1) win_dkv_kernel(const __grid_const
     uint64_t *bar = (uint64_t *)(sm + G::kBars);
     uint32_t *tslot = (uint32_t *)(bar + kNumBars);
     if (tid == 0) init_bars(bar, G::kRing);
+    if (tid == 32) {
+        prefetch_map(&maps.q);
+        prefetch_map(&maps.dout);
+        prefetch_map(&maps.k);
+        prefetch_map(&maps.v);
+    }
     if (warp == 8) tmem_alloc(tslot, kTmem);
     tc_fence_before();
     __syncthreads();

@@ -33,7 +33,7 @@ struct Geo {
     static constexpr int kRing = D == 128 ? 4 : 8;  // K and V tiles in flight
     static constexpr int kQ = 0, kKV = 2 * kUnit, kRed = kKV + kRing * kUnit, kBars = kRed + 2048, kSmem = kBars + 256 + 1024;
 };
-enum Bar { kQF, kSF, kPB = kSF + 2, kDone = kPB + 2, kLanded = kDone + 2, kFin, kFull, kMostRing = 8, kEmpty = kFull + kMostRing, kNumBars = kEmpty + kMostRing };
+enum Bar { kQF, kSF = kQF + 2, kPB = kSF + 2, kDone = kPB + 2, kLanded = kDone + 2, kFin, kFull, kMostRing = 8, kEmpty = kFull + kMostRing, kNumBars = kEmpty + kMostRing };
 
 struct Maps {
     CUtensorMap q, k, v, o;
@@ -82,8 +82,8 @@ __global__ void __launch_bounds__(kThreads, 1) win_tc_kernel(const __grid_consta
     uint64_t *bar = (uint64_t *)(sm + G::kBars);
     uint32_t *tslot = (uint32_t *)(bar + kNumBars);
     if (tid == 0) {
-        mbar_init(&bar[kQF], 1);
         for (int x = 0; x < 2; ++x) {
+            mbar_init(&bar[kQF + x], 1);
             mbar_init(&bar[kSF + x], 1);
             mbar_init(&bar[kPB + x], 8);
             mbar_init(&bar[kDone + x], 1);
@@ -95,6 +95,11 @@ __global__ void __launch_bounds__(kThreads, 1) win_tc_kernel(const __grid_consta
             mbar_init(&bar[kEmpty + i], 1);
         }
         fence_mbar_init();
+    }
+    if (tid == 32) {
+        prefetch_map(&maps.q);
+        prefetch_map(&maps.k);
+        prefetch_map(&maps.v);
     }
     if (warp == 16) tmem_alloc(tslot, kTmem);
     tc_fence_before();
@@ -110,14 +115,18 @@ __global__ void __launch_bounds__(kThreads, 1) win_tc_kernel(const __grid_consta
     if (warp == 16) {
         // ---------------------------------------------------------------- loads
         bool ok = !withhold;
-        if (ok && elect_one_sync()) {
-            mbar_arrive_expect_tx(&bar[kQF], (B.rows > 0 ? 2 : 1) * G::kUnit);
-            for (int x = 0; x < (B.rows > 0 ? 2 : 1); ++x)
+        auto queries = [&](int x) {
+            if (elect_one_sync()) {
+                mbar_arrive_expect_tx(&bar[kQF + x], G::kUnit);
 #pragma unroll
                 for (int b = 0; b < G::kBoxes; ++b)
-                    tma_load_3d(sm + G::kQ + x * G::kUnit + b * kBox, &maps.q, b * 64, x ? B.h : A.h, (int)(sq.bos + (x ? B.i0 : A.i0)), &bar[kQF]);
-        }
-        __syncwarp();
+                    tma_load_3d(sm + G::kQ + x * G::kUnit + b * kBox, &maps.q, b * 64, x ? B.h : A.h, (int)(sq.bos + (x ? B.i0 : A.i0)), &bar[kQF + x]);
+            }
+            __syncwarp();
+        };
+        const bool both = ok && B.rows > 0;
+        if (ok) queries(0);
+        if (both && nt == 0) queries(1);
         int i = 0, mended = 0;
         for (; i < 2 * nt && ok; ++i) {
             const int s = i % G::kRing;
@@ -132,6 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1) win_tc_kernel(const __grid_consta
                     tma_load_3d(sm + G::kKV + s * G::kUnit + b * kBox, i & 1 ? &maps.v : &maps.k, b * 64, hk, (int)(sk.bos + key0(i >> 1)), landing);
             }
             __syncwarp();
+            if (both && i == 0) queries(1);  // (behind what the first scores wait for)
             if (mend) {
                 if (!(ok = all(wait(kLanded, mended++ & 1)))) break;
                 uint8_t *v = sm + G::kKV + s * G::kUnit;
@@ -144,6 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1) win_tc_kernel(const __grid_consta
             }
         }
         if (!withhold) wait(kQF, 0);
+        if (both) wait(kQF + 1, 0);
         for (int k = max(0, i - G::kRing); k < i; ++k) wait(kFull + k % G::kRing, (k / G::kRing) & 1);  // (no copy outlives the CTA)
     } else if (warp == 17) {
         // ---------------------------------------------------------------- products
@@ -186,6 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1) win_tc_kernel(const __grid_consta
             __syncwarp();
             if (late >= 0) second();
             if (!ok) break;
+            if (t == 0 && B.rows > 0 && !(ok = all(wait(kQF + 1, 0)))) break;
             if (elect_one_sync()) {
                 if (needB) scores(1, t);
                 mma_commit(&bar[kEmpty + (2 * t) % G::kRing]);
