@@ -149,18 +149,48 @@ __global__ void __launch_bounds__(kThreads) lin_simt_kernel(const LinArgs args)
     }
 }
 
-template <typename T>
-__global__ void lin_heads_kernel(const float *part, const int64_t *cu, int N, int64_t tokens, int H, int r, int D, T *out)
+// dq and dk (blockIdx.y) of shared heads, W elements to a thread
+template <typename T, int W>
+__global__ void lin_heads_kernel(const float *part, const int64_t *cu, int N, int64_t tokens, int H, int r, int D, T *dq, T *dk)
 {
     // (rows outside every sequence have no parts)
     const int64_t per = (int64_t)H * D, lo = cu ? clamp64(cu[0], 0, tokens) * per : 0, hi = cu ? clamp64(cu[N], 0, tokens) * per : tokens * per;
-    for (int64_t i = lo + (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < hi; i += (int64_t)gridDim.x * blockDim.x) {
+    T *const out = blockIdx.y ? dk : dq;
+    part += blockIdx.y * tokens * per * r;
+    for (int64_t i = lo + W * ((int64_t)blockIdx.x * blockDim.x + threadIdx.x); i < hi; i += W * (int64_t)gridDim.x * blockDim.x) {
         const int64_t head = i / D;
         const float *p = part + (head * r) * D + (i - head * D);
-        float s = p[0];
-        for (int k = 1; k < r; ++k) s += p[(int64_t)k * D];
-        out[i] = from_f<T>(s);
+        float s[W];
+#pragma unroll
+        for (int e = 0; e < W; ++e) s[e] = 0.f;
+        for (int k = 0; k < r; ++k) {
+            float x[W];
+            if constexpr (W == 4) *(float4 *)x = *(const float4 *)(p + (int64_t)k * D);
+            else x[0] = p[(int64_t)k * D];
+#pragma unroll
+            for (int e = 0; e < W; ++e) s[e] += x[e];
+        }
+        if constexpr (W == 4 && sizeof(T) == 2) {
+            __nv_bfloat162 y[2] = {__floats2bfloat162_rn(s[0], s[1]), __floats2bfloat162_rn(s[2], s[3])};
+            *(uint2 *)(out + i) = *(const uint2 *)y;
+        } else if constexpr (W == 4) {
+            *(float4 *)(out + i) = make_float4(s[0], s[1], s[2], s[3]);
+        } else {
+            out[i] = from_f<T>(s[0]);
+        }
     }
+}
+
+template <typename T>
+cudaError_t heads(const float *part, const LinArgs &a, int64_t tokens, int H, int r, int D, void *dq, void *dk, cudaStream_t st)
+{
+    const int64_t n = tokens * H * D;
+    if (n == 0) return cudaSuccess;
+    const bool four = D % 4 == 0 && !(((uintptr_t)dq | (uintptr_t)dk) & 15);
+    const unsigned blocks = (unsigned)std::min<int64_t>((n + 1023) / 1024, 152 * 8);
+    auto kern = four ? lin_heads_kernel<T, 4> : lin_heads_kernel<T, 1>;
+    kern<<<dim3(blocks, 2), 256, 0, st>>>(part, a.cu, a.N, tokens, H, r, D, (T *)dq, (T *)dk);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -188,14 +218,9 @@ cudaError_t launch_lin_simt(const LinArgs &a, gdn_dtype dt, cudaStream_t st)
     return cudaGetLastError();
 }
 
-cudaError_t launch_lin_heads(const float *part, const LinArgs &a, int64_t tokens, int H, int r, int D, void *out, gdn_dtype dt, cudaStream_t st)
+cudaError_t launch_lin_heads(const float *part, const LinArgs &a, int64_t tokens, int H, int r, int D, void *dq, void *dk, gdn_dtype dt, cudaStream_t st)
 {
-    const int64_t n = tokens * H * D;
-    if (n == 0) return cudaSuccess;
-    const unsigned blocks = (unsigned)std::min<int64_t>((n + 255) / 256, 152 * 16);
-    if (dt == GDN_F32) lin_heads_kernel<float><<<blocks, 256, 0, st>>>(part, a.cu, a.N, tokens, H, r, D, (float *)out);
-    else lin_heads_kernel<__nv_bfloat16><<<blocks, 256, 0, st>>>(part, a.cu, a.N, tokens, H, r, D, (__nv_bfloat16 *)out);
-    return cudaGetLastError();
+    return dt == GDN_F32 ? heads<float>(part, a, tokens, H, r, D, dq, dk, st) : heads<__nv_bfloat16>(part, a, tokens, H, r, D, dq, dk, st);
 }
 
 }  // namespace gdn

@@ -67,6 +67,7 @@ struct Part {
         s = seq_range(a.cu, n, a.T);
         seg = t.index;
         chunks = (s.len + kC - 1) / kC;
+        // (packed sequences of at most a segment's length stay whole)
         const int per = sp.states ? sp.tokens / kC : chunks;
         m0 = (int)min((int64_t)seg * per, (int64_t)chunks);
         nm = min(per, chunks - m0);
@@ -100,7 +101,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     const float g = args.decay ? args.decay[hv] : 0.f, g2 = g * kRcpLn2;
     const int64_t xbase = ((int64_t)n * args.HV + hv) * D * D;
     auto xat = [&](int r, int c) { return xbase + (p.x_t ? (int64_t)(c0 + c) * D + r : (int64_t)r * D + c0 + c); };
-    float *const mine = split.states ? split.states + (((int64_t)pi * split.slots + slot) * args.HV + hv) * D * D + c0 : nullptr;
+    float *const mine = split.states && part.nm < part.chunks ? split.states + (((int64_t)pi * split.slots + slot) * args.HV + hv) * D * D + c0 : nullptr;
 
     if (nm <= 0) {
         // nothing to walk: a sequence without tokens hands its state on
@@ -490,28 +491,40 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     }
 }
 
-// What the segments add to the state -> the state that enters each (in place), one thread per element
+// What the segments add to the state -> the state that enters each (in place): four elements to a thread, a block of 1024 to a (sequence,
+// head) pair's piece.  Eight segments are asked for at once (one after the other, 19 segments took 64 us).
 template <int D>
-__global__ void lin_join_kernel(const LinArgs args, const Split split)
+__global__ void __launch_bounds__(256) lin_join_kernel(const LinArgs args, const Split split)
 {
+    constexpr int kPieces = D * D / 1024;
     const LinPass &p = args.pass[blockIdx.y];
-    const int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    const int64_t pair = e / (D * D);
-    const int at = (int)(e % (D * D)), n = (int)(pair / args.HV), hv = (int)(pair % args.HV);
-    if (n >= args.N) return;
+    const int pair = (int)(blockIdx.x / kPieces), at = (int)(blockIdx.x % kPieces) * 1024 + 4 * threadIdx.x;
+    const int n = pair / args.HV, hv = pair - n * args.HV;
     const SeqRange s = seq_range(args.cu, n, args.T);
+    const int segs = (s.len + split.tokens - 1) / split.tokens;
+    if (segs <= 1) return;  // (whole)
     const int64_t slot0 = args.cu ? clamp64(args.cu[n], 0, args.T) / split.tokens + n : (int64_t)n * ((args.T + split.tokens - 1) / split.tokens);
     const float g = args.decay ? args.decay[hv] : 0.f;
-    const int segs = (s.len + split.tokens - 1) / split.tokens;
     // tokens of a segment in the order of processing: against time the first has the sequence's odd end
     const int odd = (s.len + kC - 1) / kC * kC - s.len;
-    float x = p.x0 ? p.x0[pair * D * D + (p.x_t ? (at % D) * D + at / D : at)] : 0.f;
+    float x[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = p.x0 ? p.x0[(int64_t)pair * D * D + (p.x_t ? ((at + e) % D) * D + at / D : at + e)] : 0.f;
+    const int64_t step = (int64_t)args.HV * D * D;
     float *buf = split.states + (((int64_t)blockIdx.y * split.slots + slot0) * args.HV + hv) * D * D + at;
     const Decayed first(g, split.tokens - (p.reverse ? odd + 1 : 0)), rest(g, split.tokens);
-    for (int i = 0; i < segs; ++i, buf += (int64_t)args.HV * D * D) {
-        const float add = i + 1 < segs ? *buf : 0.f;
-        *buf = x;
-        x = (i == 0 ? first(x) : rest(x)) + add;
+    for (int i = 0; i < segs; i += 8) {
+        float4 add[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) add[k] = i + k + 1 < segs ? *(const float4 *)(buf + (i + k) * step) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (i + k < segs) {
+                *(float4 *)(buf + (i + k) * step) = make_float4(x[0], x[1], x[2], x[3]);
+                const float *y = (const float *)&add[k];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = (i + k == 0 ? first(x[e]) : rest(x[e])) + y[e];
+            }
     }
 }
 
@@ -550,13 +563,13 @@ cudaError_t launch(const LinArgs &a, void *ws, int64_t tokens, cudaStream_t st)
         done_on_device(seen);
     }
     const int64_t ctas = plan.slots * a.HV * (D / kCols) * a.passes, elements = (int64_t)a.N * a.HV * D * D;
-    if (ctas > INT32_MAX || elements / 256 > INT32_MAX) return cudaErrorInvalidConfiguration;
+    if (ctas > INT32_MAX || elements / 1024 > INT32_MAX) return cudaErrorInvalidConfiguration;
     const unsigned grid = (unsigned)ctas;
     const int withhold = withhold_loads();
     const uint64_t limit = withhold ? kTestWaitLimitNs : kWaitLimitNs;
     if (split.states) {
         lin_tc_kernel<D, true><<<grid, kThreads, Geo<D>::kSmem, st>>>(maps, a, split, limit, withhold);
-        lin_join_kernel<D><<<dim3((unsigned)((elements + 255) / 256), a.passes), 256, 0, st>>>(a, split);
+        lin_join_kernel<D><<<dim3((unsigned)(elements / 1024), a.passes), 256, 0, st>>>(a, split);
     }
     lin_tc_kernel<D, false><<<grid, kThreads, Geo<D>::kSmem, st>>>(maps, a, split, limit, withhold);
     return cudaGetLastError();
@@ -577,10 +590,11 @@ bool heads_map(CUtensorMap *m, const void *base, int D, int heads, int64_t token
 
 LinPlan lin_tc_plan(const LinArgs &a, int D)
 {
-    // A split walks its chunks twice (the second time with outputs), so it pays only where (sequence, head) pairs leave SMs
-    // idle: the time of a plan is taken as rounds of CTAs times chunks of a segment, a chunk of the first walk as 0.6 of one.
-    const int64_t total = a.cu ? (a.T + kC - 1) / kC : (int64_t)a.N * ((a.T + kC - 1) / kC);  // chunks, and per sequence (packed: on average)
-    const int64_t each = std::max<int64_t>(1, (total + a.N - 1) / a.N), ctas = (int64_t)a.N * a.HV * (D / kCols) * a.passes, sms = device_sm_count();
+    // A split walks its chunks twice (the second time with outputs), so it pays only where (sequence, head) pairs leave SMs idle: the
+    // time of a plan is taken as rounds of CTAs times chunks of a segment, a walk without outputs as 0.6 of one with them (measured: 80 us
+    // and 122 at 65536 tokens of 8 heads) and the further launches as 8 chunks.  The lengths of packed sequences are not known here: the
+    // segment is what one sequence of all tokens would be cut into, so that one that holds up the others is cut and the others stay whole.
+    const int64_t each = std::max(1, (a.T + kC - 1) / kC), ctas = (int64_t)(a.cu ? 1 : a.N) * a.HV * (D / kCols) * a.passes, sms = device_sm_count();
     int64_t best = 1;
     double least = 1e30;
     for (int64_t s = 1; s <= std::min<int64_t>(64, (each + 3) / 4); ++s) {

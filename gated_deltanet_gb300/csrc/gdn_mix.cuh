@@ -84,8 +84,8 @@ cudaError_t launch_lin_tc(const LinArgs &a, void *ws, int64_t tokens, cudaStream
 gdn_status read_lin_status(cudaStream_t st);
 // a TMA map over bf16 [tokens][heads][D], `ld` elements from a token to the next: boxes of 64 elements x 1 head x box_rows tokens
 bool heads_map(CUtensorMap *m, const void *base, int D, int heads, int64_t tokens, int64_t ld, int box_rows);
-// out[t][h][d] = sum over the r value heads of head h of part[t][h r + i][d], summed in order
-cudaError_t launch_lin_heads(const float *part, const LinArgs &a, int64_t tokens, int H, int r, int D, void *out, gdn_dtype dt, cudaStream_t st);
+// dq and dk of heads that r value heads share: out[t][h][d] = sum over i of part[t][h r + i][d], in order (`part`: dq's, then dk's)
+cudaError_t launch_lin_heads(const float *part, const LinArgs &a, int64_t tokens, int H, int r, int D, void *dq, void *dk, gdn_dtype dt, cudaStream_t st);
 
 struct LinStepArgs {
     const void *q, *k, *v;

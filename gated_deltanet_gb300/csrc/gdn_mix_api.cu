@@ -236,8 +236,7 @@ gdn_status gdn_linear_attn_bwd(const gdn_linear_attn_args *a, void *ws, size_t w
     if (part && e == cudaSuccess) {
         const int64_t tokens = (int64_t)a->B * a->T;
         const int r = a->HV / a->H;
-        e = launch_lin_heads(part, l, tokens, a->H, r, a->K, a->dq, a->dtype, stream);
-        if (e == cudaSuccess) e = launch_lin_heads(part + tokens * a->HV * a->K, l, tokens, a->H, r, a->K, a->dk, a->dtype, stream);
+        e = launch_lin_heads(part, l, tokens, a->H, r, a->K, a->dq, a->dk, a->dtype, stream);
     }
     return of(e);
 }
