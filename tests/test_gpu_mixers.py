@@ -1,10 +1,14 @@
 """Linear attention with a decay per head and attention with a sliding window and sinks on the GPU against their 64-bit forms
 (``mixer_reference``), element by element within bounds that count roundings, at the sizes where kernels go wrong: one token, tiles that
 end inside, sequences of any length next to each other, empty ones, shared heads, strided and unaligned inputs, rows that see nothing."""
+import ctypes
+
 import pytest
 import torch
 
+import layer_c
 import mixer_reference as ref
+import test_mixers_host as host
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
@@ -442,3 +446,199 @@ def test_empty(gdn):
     dq, dk, dv = gdn.window_attention_bwd(z, z, k, k, z, lse, 3)
     assert dq.numel() == 0 and not dk.any() and not dv.any()
     assert gdn.window_attention_decode(z, k, k, torch.tensor([9, 3], device="cuda"), 3).shape == z.shape
+
+
+# ---------------------------------------------------------------- one sequence that holds up the others
+@pytest.mark.parametrize("H,HV,D", [(1, 1, 128), (1, 2, 128), (2, 2, 64)])
+def test_linear_packed_split(gdn, H, HV, D):
+    """Of a packed batch only the sequences longer than a segment are split; the others, short and empty ones, keep their places."""
+    lens = [0, 3, 9000, 1, 0, 200, 5000, 129]
+    q, k, v, decay, h0, cu, g = linear_inputs((1, lens, H, HV, D, D), BF, True, 6)
+    decay = -torch.linspace(2e-4, 2e-2, HV, device="cuda")
+    o, ht = gdn.chunk_linear_attention(q, k, v, decay, initial_state=h0, output_final_state=True, cu_seqlens=cu)
+    do, dht = randn(g, *v.shape, dtype=BF), randn(g, *h0.shape)
+    got = gdn.chunk_linear_attention_bwd(q, k, v, decay, do, None, h0, dht, cu)
+    o2, ht2 = gdn.fused_recurrent_linear_attention(q.float(), k.float(), v.float(), decay, initial_state=h0, output_final_state=True, cu_seqlens=cu)
+    want = gdn.chunk_linear_attention_bwd(q.float(), k.float(), v.float(), decay, do.float(), None, h0, dht, cu)
+    at = 0
+    for n, length in enumerate(lens):
+        piece = slice(at, at + length)
+        at += length
+        ref.check_norm(ht[n], ht2[n].double(), 2e-5, "state")
+        ref.check_norm(got[3][n], want[3][n].double(), 2e-5, "dh0")
+        if length:
+            ref.check_norm(o[:, piece], o2[:, piece].double(), 2.0 ** -8, "o")
+            for name, a, b in zip(("dq", "dk", "dv"), got, want):
+                ref.check_norm(a[:, piece], b[:, piece].double(), 2.0 ** -8, name)
+
+
+@pytest.mark.parametrize("window,sinks", [(100, 600), (2 ** 31 - 1, 2 ** 31 - 1), (2000, 0), (1, 1499)])
+def test_window_many_sinks(gdn, window, sinks):
+    """More sinks than are dealt out to CTAs of their own, and windows longer than the sequence."""
+    q, k, v, _, _, _, _, g = window_inputs((1, 1500, None, 2, 1, 64, 1, 0), BF, 3)
+    o, lse = gdn.window_attention(q, k, v, window, sinks, return_lse=True)
+    eo, el, bo, bl = ref.window(q, k, v, window, sinks, 0.125)
+    ref.check(o, eo, bo, "o")
+    ref.check(lse, el, bl, "lse")
+    check_window_bwd(gdn, q, k, v, randn(g, *q.shape, dtype=BF), window, sinks, 0.125, None, None)
+
+
+def test_tables_are_clamped(gdn):
+    """Offsets outside the tensor are taken as its ends."""
+    g = gen(43)
+    q, k, v, do = (randn(g, 1, 300, 2, 128, dtype=BF) for _ in range(4))
+    decay, wild, cu = torch.tensor([-0.1, -0.01], device="cuda"), torch.tensor([-3, 170, 2 ** 40], device="cuda"), torch.tensor([0, 170, 300], device="cuda")
+
+    def everything(cu):
+        o, lse = gdn.window_attention(q, k, v, 60, 3, cu_seqlens=cu, return_lse=True)
+        return [o, lse, *gdn.window_attention_bwd(do, q, k, v, o, lse, 60, 3, cu_seqlens=cu),
+                *gdn.chunk_linear_attention(q, k, v, decay, output_final_state=True, cu_seqlens=cu),
+                *gdn.fused_recurrent_linear_attention(q, k, v, decay, output_final_state=True, cu_seqlens=cu),
+                *gdn.chunk_linear_attention_bwd(q, k, v, decay, do, cu_seqlens=cu)[:3]]
+
+    for a, b in zip(everything(wild), everything(cu)):
+        assert torch.equal(a, b)
+    lens = torch.tensor([2 ** 40, -7], device="cuda")
+    two = [t.view(2, 150, 2, 128) for t in (k, v)]
+    got = gdn.window_attention_decode(q[:, :2].view(2, 1, 2, 128), *two, lens, 60, 3)
+    assert torch.equal(got, gdn.window_attention_decode(q[:, :2].view(2, 1, 2, 128), *two, torch.tensor([150, 0], device="cuda"), 60, 3))
+
+
+def test_offsets_past_32_bits(gdn):
+    """2^24 + 1000 tokens of 128: the last rows, whose elements lie behind the 2^31st, against the plain forms of the last 700 tokens
+    (what lies further back is outside the window, or has decayed by e^-150 and more)."""
+    T, D, last, skip = 2 ** 24 + 1000, 128, 700, 300
+    q, k, v, do = (torch.empty(1, T, 1, D, device="cuda", dtype=BF).normal_(generator=gen(44 + i)) for i in range(4))
+    cut = [t[:, -last:].contiguous() for t in (q, k, v, do)]
+    o, lse = gdn.window_attention(q, k, v, 64, 0, return_lse=True)
+    eo, el, bo, bl = ref.window(*cut[:3], 64, 0, D ** -0.5)
+    ref.check(o[:, -last + skip:], eo[:, skip:], bo[:, skip:], "o")
+    ref.check(lse[..., -last + skip:], el[..., skip:], bl[..., skip:], "lse")
+    got = gdn.window_attention_bwd(do, q, k, v, o, lse, 64, 0)
+    want, bound = ref.window_bwd(cut[3], *cut[:3], o[:, -last:], 64, 0, D ** -0.5)
+    for name, a, b, e in zip(("dq", "dk", "dv"), got, want, bound):
+        ref.check(a[:, -last + skip:], b[:, skip:], e[:, skip:], name)
+    del got, o, lse
+    decay = torch.tensor([-0.5], device="cuda")
+    o, ht = gdn.chunk_linear_attention(q, k, v, decay, output_final_state=True)
+    eo, eh, so, sh = ref.linear(*cut[:3], decay, D ** -0.5, None, None)
+    n = D + 2 * last + 16
+    ref.check(o[:, -last + skip:], eo[:, skip:], ref.linear_bound(eo, so, n, BF)[:, skip:], "o")
+    ref.check(ht, eh, ref.state_bound(sh, n, BF), "state")
+    got = gdn.chunk_linear_attention_bwd(q, k, v, decay, do)
+    want, size = ref.linear_bwd(*cut[:3], decay, cut[3], D ** -0.5, None, None, None)
+    for name, a, b, s in zip(("dq", "dk", "dv"), got, want, size):
+        ref.check(a[:, -last + skip:], b[:, skip:], ref.linear_bound(b, s, n + D, BF)[:, skip:], name)
+    del got, o
+    # one sequence's cache of as many slots: its newest and its first
+    lens = torch.tensor([T], device="cuda")
+    near = [torch.cat([t[:, :4], t[:, -64:]], 1) for t in (k, v)]
+    got = gdn.window_attention_decode(q[:, -1:], k, v, lens, 64, 4)
+    eo, bo = ref.window_step(q[:, -1:], *near, [68], 64, 4, D ** -0.5)
+    ref.check(got, eo, bo, "o")
+
+
+# ---------------------------------------------------------------- calls of the C entries, at once, and cut short
+def linear_call(lib, q, k, v, decay, do=None, stream=0):
+    """(run, outputs): gdn_linear_attn, or its gradients, with the library's own workspace."""
+    B, T, H, D = q.shape
+    HV = v.shape[2]
+    out = [torch.empty_like(v)] if do is None else [torch.empty_like(t) for t in (q, k, v)]
+    named = dict(o=out[0]) if do is None else dict(zip(("dq", "dk", "dv"), out), dout=do)
+    a = host.GdnLinearAttnArgs(**layer_c.pointers(B=B, T=T, H=H, HV=HV, K=D, V=D, num_seqs=B, dtype=1, scale=0.1, q=q, k=k, v=v, ldq=H * D, ldk=H * D,
+                                                  ldv=HV * D, decay=decay, ld_dout=HV * D, **named))
+    f = lib.gdn_linear_attn if do is None else lib.gdn_linear_attn_bwd
+    return lambda kept=(q, k, v, decay, do): f(ctypes.byref(a), None, 0, stream), out  # (the block holds addresses alone)
+
+
+def window_call(lib, q, k, v, o, lse, do=None, stream=0):
+    B, T, H, D = q.shape
+    HK = k.shape[2]
+    grads = [] if do is None else [torch.empty_like(t) for t in (q, k, v)]
+    a = host.GdnWindowAttnArgs(**layer_c.pointers(B=B, Tq=T, Tk=T, H=H, HK=HK, D=D, num_seqs=B, dtype=1, window=200, sinks=4, scale=0.1, q=q, k=k, v=v, ldq=H * D,
+                                                  ldk=HK * D, ldv=HK * D, o=o, lse=lse, ld_dout=H * D, dout=do, **dict(zip(("dq", "dk", "dv"), grads))))
+    f = lib.gdn_window_attn if do is None else lib.gdn_window_attn_bwd
+    return lambda kept=(q, k, v, o, lse, do): f(ctypes.byref(a), None, 0, stream), grads or [o, lse]
+
+
+L = host.L
+
+
+def calls_and_results(gdn, lib, seed, stream=0):
+    """Calls that take workspaces of the library's, in the order of a training step, their outputs, and what the binding gives."""
+    g = gen(seed)
+    q, k = (randn(g, 1, 3000, 1, 128, dtype=BF) for _ in range(2))
+    v, do = (randn(g, 1, 3000, 2, 128, dtype=BF) for _ in range(2))
+    decay = torch.tensor([-0.1, -1e-3], device="cuda")
+    o, lse = torch.empty_like(v), torch.empty(1, 2, 3000, device="cuda")
+    calls = [linear_call(lib, q, k, v, decay, None, stream), linear_call(lib, q, k, v, decay, do, stream), window_call(lib, v, q, k, o, lse, None, stream),
+             window_call(lib, v, q, k, o, lse, do, stream)]
+    w, l = gdn.window_attention(v, q, k, 200, 4, 0.1, return_lse=True)
+    want = [[gdn.chunk_linear_attention(q, k, v, decay, 0.1)[0]], gdn.chunk_linear_attention_bwd(q, k, v, decay, do, 0.1)[:3], [w, l],
+            gdn.window_attention_bwd(do, v, q, k, w, l, 200, 4, 0.1)]
+    return calls, want
+
+
+def test_library_workspace(gdn, L):
+    """Without a workspace of the caller's, on two streams at once: as with one each."""
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    both = [calls_and_results(gdn, L, 50 + i, s.cuda_stream) for i, s in enumerate(streams)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for steps in zip(*(calls for calls, _ in both)):
+            for run, _ in steps:
+                assert run() == 0
+    torch.cuda.synchronize()
+    for calls, want in both:
+        for (_, out), w in zip(calls, want):
+            for a, b in zip(out, w):
+                assert torch.equal(a, b)
+
+
+def test_two_graphs_at_once(gdn):
+    """Two captured runs, with the binding's workspaces, replayed on two streams at once."""
+    g = gen(45)
+    runs = []
+    for _ in range(2):
+        q, k = (randn(g, 1, 3000, 1, 128, dtype=BF) for _ in range(2))
+        v, do = (randn(g, 1, 3000, 2, 128, dtype=BF) for _ in range(2))
+        decay = torch.tensor([-0.1, -1e-3], device="cuda")
+
+        def run(q=q, k=k, v=v, do=do, decay=decay):
+            o, ht = gdn.chunk_linear_attention(q, k, v, decay, output_final_state=True)
+            w, lse = gdn.window_attention(v, q, k, 200, 4, return_lse=True)
+            return [o, ht, w, lse, *gdn.chunk_linear_attention_bwd(q, k, v, decay, do)[:3], *gdn.window_attention_bwd(do, v, q, k, w, lse, 200, 4)]
+        want = run()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = run()
+        runs.append((graph, got, want, torch.cuda.Stream(), run))  # (run: a graph does not keep the tensors that were there before it)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for graph, _, _, stream, _ in runs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, got, want, _, _ in runs:
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
+def test_waits_that_run_out(gdn, L):
+    """Calls whose kernels load nothing, so that their waits run out after 5 ms: reported once, and the next call is right."""
+    L.gdn_layer_test_withhold.argtypes, L.gdn_layer_test_withhold.restype = [ctypes.c_int], None
+    calls, want = calls_and_results(gdn, L, 52)
+    torch.cuda.synchronize()
+    assert gdn.read_layer_status() == 0
+    for (run, out), w in zip(calls, want):
+        L.gdn_layer_test_withhold(1)
+        try:
+            assert run() == 0
+        finally:
+            L.gdn_layer_test_withhold(0)
+        torch.cuda.synchronize()
+        assert gdn.read_layer_status() == -4 and gdn.read_layer_status() == 0
+        assert run() == 0
+        torch.cuda.synchronize()
+        for a, b in zip(out, w):
+            assert torch.equal(a, b)
