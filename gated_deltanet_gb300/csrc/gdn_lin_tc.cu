@@ -76,8 +76,6 @@ struct Part {
     __device__ int rows(int c) const { return min(kC, s.len - c * kC); }
 };
 
-__device__ __forceinline__ float low_bf16(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float high_bf16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 // STATE: only what the segment adds to the state, from zero
 template <int D, bool STATE>
 __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_constant__ Maps maps, const LinArgs args, const Split split, uint64_t limit, int withhold)

@@ -11,6 +11,13 @@
 // their own (kSinkRun queries each) whose fp32 parts win_sinks_kernel adds to the tile's in order: one CTA for all of them would walk
 // the whole sequence while the others see a window.
 //
+// 4 x 4096 tokens, 16 heads over 4 of 128, window 1024: dQ 212 us, dK and dV 270, 137 GFLOP of scores each way.
+//  - dQ: one CTA per SM walks tiles of queries (a CTA to each: 245 us; starting one and filling its pipeline took 12000 cycles, the walk 24000).
+//    Q and dO are left operands in tensor memory: 128 x 128 x 16 then takes 67 cycles, with both operands in shared memory 104, which is bound by
+//    its 80 bytes a cycle.  A tile of keys takes 2480 cycles: its products 1610 alone, the copies of K and V take shared memory from them.
+//  - dK, dV: no room for K and V beside four accumulators; a tile of queries takes 3000 cycles, its products 2740.
+//  - Four groups of 128 lanes in place of two: no faster (the exponentials are 1024 cycles of a tile's either way), and 96 registers spill.
+//
 // Warps: 0-3 and 4-7 two groups of 128 lanes, each on half of a tile's columns, 8 loads, 9 products.
 #include "gdn_mix.cuh"
 #include "gdn_ptx.cuh"
@@ -20,31 +27,34 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kTile = 128, kThreads = 320, kBox = kTile * 128;
+constexpr int kTile = 128, kBox = kTile * 128;
+constexpr int kGroups = 2, kCols = kTile / kGroups, kLanes = 128 * kGroups, kLoads = 4 * kGroups, kProducts = kLoads + 1, kThreads = kLanes + 64;
 constexpr uint32_t kTmem = 512;
 
 __device__ unsigned g_win_bwd_status;
 
-template <int D, int RING>
+template <int D>
 struct Geo {
-    static constexpr int kBoxes = D / 64, kUnit = kBoxes * kBox, kRing = RING;
-    static constexpr int kA = 0, kB = kUnit, kRingAt = 2 * kUnit, kStats = kRingAt + RING * kUnit, kBars = kStats + 2048, kSmem = kBars + 256 + 1024;
+    static constexpr int kBoxes = D / 64, kUnit = kBoxes * kBox, kRing = D == 128 ? 5 : 8;
+    static constexpr int kA = 0, kB = kUnit, kRingAt = 2 * kUnit, kStats = kRingAt + kRing * kUnit, kBars = kStats + 1024, kItems = kBars + 256, kSmem = kItems + 128 + 1024;
 };
-constexpr int ring_of_dq(int D) { return D == 128 ? 4 : 8; }
-enum Bar { kIn, kSF, kPF = kSF + 2, kPB, kZB, kDone, kLanded, kFull, kMostRing = 8, kEmpty = kFull + kMostRing, kNumBars = kEmpty + kMostRing };
+enum Bar { kIn, kAB, kTaken, kSF, kSR, kPF, kPB, kZB, kDone, kFin, kLanded, kFull, kMostRing = 8, kEmpty = kFull + kMostRing, kNumBars = kEmpty + kMostRing };
 
 struct Maps {
-    CUtensorMap q, k, v, dout, dq, dk, dv;
+    CUtensorMap q, k, v, o, dout, dq, dk, dv;
 };
 
 __device__ __forceinline__ void init_bars(uint64_t *bar, int ring)
 {
     mbar_init(&bar[kIn], 1);
+    mbar_init(&bar[kAB], 4 * kGroups);
+    mbar_init(&bar[kTaken], 1);
+    mbar_init(&bar[kFin], 1);
     mbar_init(&bar[kSF], 1);
-    mbar_init(&bar[kSF + 1], 1);
+    mbar_init(&bar[kSR], 4 * kGroups);
     mbar_init(&bar[kPF], 1);
-    mbar_init(&bar[kPB], 8);
-    mbar_init(&bar[kZB], 8);
+    mbar_init(&bar[kPB], 4 * kGroups);
+    mbar_init(&bar[kZB], 4 * kGroups);
     mbar_init(&bar[kDone], 1);
     mbar_init(&bar[kLanded], 1);
     for (int i = 0; i < ring; ++i) {
@@ -73,60 +83,74 @@ __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b)
         mma_ss(d, da + o, db + o, id, ks > 0);
     }
 }
-// D(128 x D) (+)= A(128 x 128) B(128 x D): A bf16 in tensor memory, the halves of its columns at a and a + 64, B's rows in shared memory
+// The same with A's rows in tensor memory
+template <int D>
+__device__ __forceinline__ void mma_kept(uint32_t d, uint32_t a, uint32_t b)
+{
+    const uint64_t db = sdesc_sw128(b, 16, 1024);
+    constexpr uint32_t id = idesc_bf16_f32(128, 128, 0, 0);
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) mma_ts(d, a + ks * 8, db + (((ks >> 2) * kBox + (ks & 3) * 32) >> 4), id, ks > 0);
+}
+// D(128 x D) (+)= A(128 x 128) B(128 x D): A bf16 in tensor memory, each group's columns in the place of its scores, B's rows in shared memory
 template <int D>
 __device__ __forceinline__ void mma_sum(uint32_t d, uint32_t a, uint32_t b, bool fresh)
 {
     const uint64_t db = sdesc_sw128(b, kBox, 1024);
     constexpr uint32_t id = idesc_bf16_f32(128, D, 0, 1);
 #pragma unroll
-    for (int ks = 0; ks < 8; ++ks) mma_ts(d, a + (ks >> 2) * 64 + (ks & 3) * 8, db + ks * 128, id, !fresh || ks > 0);
+    for (int ks = 0; ks < 8; ++ks) mma_ts(d, a + ks / (kCols / 16) * kCols + ks % (kCols / 16) * 8, db + ks * 128, id, !fresh || ks > 0);
 }
-// a tile of rows in shared memory to [tokens][heads][D]: by TMA where it is whole, else by the group's 128 threads
-template <int D>
-__device__ __forceinline__ void store_rows(const CUtensorMap *map, void *out, uint8_t *tile, int64_t t0, int rows, int heads, int h, int r)
+// the first rows of a tile in shared memory to [tokens][heads][D], by THREADS threads (r: which)
+template <int D, int THREADS>
+__device__ __forceinline__ void copy_rows(void *out, const uint8_t *tile, int64_t t0, int rows, int heads, int h, int r)
 {
-    if (rows == kTile) {
-        if (r == 0) {
-#pragma unroll
-            for (int b = 0; b < D / 64; ++b) tma_store_3d(map, tile + b * kBox, b * 64, h, (int)t0);
-            tma_store_commit();
-            tma_store_wait0();
-        }
-    } else {
-        for (int k = r; k < rows * (D / 8); k += 128) {
-            const int row = k / (D / 8), e = k % (D / 8) * 8;
-            *(uint4 *)((__nv_bfloat16 *)out + ((t0 + row) * heads + h) * D + e) = *(const uint4 *)(tile + (e >> 6) * kBox + sw128(row, e & 63));
-        }
+    for (int k = r; k < rows * (D / 8); k += THREADS) {
+        const int row = k / (D / 8), e = k % (D / 8) * 8;
+        *(uint4 *)((__nv_bfloat16 *)out + ((t0 + row) * heads + h) * D + e) = *(const uint4 *)(tile + (e >> 6) * kBox + sw128(row, e & 63));
     }
 }
 
 // ---------------------------------------------------------------- dQ (lane = query)
+// A tile of queries of a head, and the tiles of keys that it sees: those of the sinks in front of its window, then the window's
+struct Queries {
+    int64_t at;            // of its first row in lse and delta
+    int t0, rows, h, p0;   // first token, rows (0: no more tiles), head, position of the first row
+    int k0, klen, hk;      // the sequence's first key and length, key head
+    int lo, hi, first, nfirst, nt;
+    __device__ __forceinline__ void set(const WinArgs &a, unsigned item)
+    {
+        h = (int)(item % (unsigned)a.H);
+        hk = h / (a.H / a.HK);
+        const Tile tl = tile_of(a.cu_q, a.N, a.Tq, kTile, item / (unsigned)a.H);
+        const SeqRange sq = seq_range(a.cu_q, tl.n, a.Tq), sk = seq_range(a.cu_k, tl.n, a.Tk);
+        const int i0 = tl.index * kTile;
+        at = lse_at(a, tl.n, sq.bos, h) + i0;
+        t0 = (int)(sq.bos + i0);
+        rows = max(min(kTile, sq.len - i0), 0);
+        p0 = i0 + sk.len - sq.len;
+        k0 = (int)sk.bos;
+        klen = sk.len;
+        hi = min(max(p0 + rows, 0), klen);
+        lo = hi == 0 ? 0 : min(max(p0 - a.window + 1, 0), hi);
+        first = min(a.sinks, lo);
+        nfirst = (first + kTile - 1) / kTile;
+        nt = nfirst + (hi - lo + kTile - 1) / kTile;
+    }
+    __device__ __forceinline__ int key0(int t) const { return t < nfirst ? t * kTile : lo + (t - nfirst) * kTile; }
+    __device__ __forceinline__ int columns(int t) const { return min(kTile, (t < nfirst ? first : hi) - key0(t)); }
+    __device__ __forceinline__ bool ragged(int t) const { return key0(t) + kTile > klen; }
+};
+static_assert(sizeof(Queries) <= 64);
+
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) win_dq_kernel(const __grid_constant__ Maps maps, const WinArgs a, float *delta, uint64_t limit, int withhold)
+__global__ void __launch_bounds__(kThreads, 1) win_dq_kernel(const __grid_constant__ Maps maps, const WinArgs a, unsigned items, float *delta, uint64_t limit,
+                                                             int withhold)
 {
-    using G = Geo<D, ring_of_dq(D)>;
-    constexpr uint32_t kS = 0, kP = 256, kQ = 384;  // S: two buffers (Z in their place), dP, dQ
+    using G = Geo<D>;
+    constexpr uint32_t kS = 0, kP = 128, kQ = 256, kAQ = 384, kAG = 448;  // S, dP (Z in its place), dQ; Q and dO as left operands
     extern __shared__ uint8_t win_bwd_smem[];
     uint8_t *const sm = win_bwd_smem + (-smem_u32(win_bwd_smem) & 1023u);  // (an offset: a cast would lose that it is shared memory)
-    const Tile tl = tile_of(a.cu_q, a.N, a.Tq, kTile, blockIdx.x);
-    const SeqRange sq = seq_range(a.cu_q, tl.n, a.Tq), sk = seq_range(a.cu_k, tl.n, a.Tk);
-    const int i0 = tl.index * kTile, rows = min(kTile, sq.len - i0), h = blockIdx.y, hk = h / (a.H / a.HK);
-    if (rows <= 0) return;
-    // o for delta, asked for first: half of its row by each thread of the two groups
-    uint4 row[D / 16];
-    if (threadIdx.x < 256 && (threadIdx.x & 127) < rows) {
-        const uint4 *o = (const uint4 *)((const __nv_bfloat16 *)a.o + ((sq.bos + i0 + (threadIdx.x & 127)) * a.H + h) * D + (threadIdx.x >> 7) * (D / 2));
-#pragma unroll
-        for (int e = 0; e < D / 16; ++e) row[e] = o[e];
-    }
-    const int p0 = i0 + sk.len - sq.len;
-    const int hi = min(max(p0 + rows, 0), sk.len), lo = hi == 0 ? 0 : min(max(p0 - a.window + 1, 0), hi);
-    const int first = min(a.sinks, lo), nfirst = (first + kTile - 1) / kTile, nt = nfirst + (hi - lo + kTile - 1) / kTile;
-    auto key0 = [&](int t) { return t < nfirst ? t * kTile : lo + (t - nfirst) * kTile; };
-    auto columns = [&](int t) { return min(kTile, (t < nfirst ? first : hi) - key0(t)); };
-    auto ragged = [&](int t) { return key0(t) + kTile > sk.len; };
-
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint64_t *bar = (uint64_t *)(sm + G::kBars);
     uint32_t *tslot = (uint32_t *)(bar + kNumBars);
@@ -137,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1) win_dq_kernel(const __grid_consta
         prefetch_map(&maps.k);
         prefetch_map(&maps.v);
     }
-    if (warp == 8) tmem_alloc(tslot, kTmem);
+    if (warp == kLoads) tmem_alloc(tslot, kTmem);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -145,169 +169,249 @@ __global__ void __launch_bounds__(kThreads, 1) win_dq_kernel(const __grid_consta
     unsigned *const status = &g_win_bwd_status;
     auto wait = [&](int b, uint32_t parity) { return mbar_wait(&bar[b], parity, status, kStatusTimeout, limit); };
     auto all = [&](bool ok) { return __all_sync(0xffffffffu, ok); };
-    auto full = [&](int i) { return all(wait(kFull + i % G::kRing, (i / G::kRing) & 1)); };  // unit 2 t: K, 2 t + 1: V
+    auto full = [&](int i) { return all(wait(kFull + i % G::kRing, (i / G::kRing) & 1)); };  // a tile of queries: O, K and V of each tile of keys, a place for dQ
     auto unit = [&](int i) { return G::kRingAt + (i % G::kRing) * G::kUnit; };
 
-    if (warp == 8) {
+    // n counts this CTA's tiles of queries, i and first_unit the units, from and t the tiles of keys of all of them.  The loading warp finds
+    // the tiles and hands them on with kIn, a tile without rows behind the last.
+    Queries *const handed = (Queries *)(sm + G::kItems);
+    bool ok = true;
+    int n = 0, from = 0, first_unit = 0;
+    Queries it;
+    if (warp == kLoads) {
         // ---------------------------------------------------------------- loads
-        bool ok = !withhold;
-        if (ok && elect_one_sync()) {
-            mbar_arrive_expect_tx(&bar[kIn], 2 * G::kUnit);
-#pragma unroll
-            for (int b = 0; b < G::kBoxes; ++b) {
-                tma_load_3d(sm + G::kA + b * kBox, &maps.q, b * 64, h, (int)(sq.bos + i0), &bar[kIn]);
-                tma_load_3d(sm + G::kB + b * kBox, &maps.dout, b * 64, h, (int)(sq.bos + i0), &bar[kIn]);
-            }
-        }
-        __syncwarp();
+        ok = !withhold;
         int i = 0, mended = 0;
-        for (; i < 2 * nt && ok; ++i) {
-            const int s = i % G::kRing, t = i >> 1;
-            if (i >= G::kRing && !(ok = all(wait(kEmpty + s, (i / G::kRing - 1) & 1)))) break;
-            // K's rows behind the end are the next sequence's, and 0 x NaN is NaN: they are zeroed before the tile counts as full
-            const bool mend = !(i & 1) && ragged(t);
-            uint64_t *const landing = &bar[mend ? (int)kLanded : kFull + s];
+        for (unsigned item = blockIdx.x; ok; item += gridDim.x) {
+            it.rows = 0;
+            if (item < items) {
+                it.set(a, item);
+                if (it.rows == 0) continue;
+            }
+            if (n > 0 && !(ok = all(wait(kTaken, (n - 1) & 1)))) break;
             if (elect_one_sync()) {
-                mbar_arrive_expect_tx(landing, G::kUnit);
+                handed[n & 1] = it;
+                if (it.rows == 0) {
+                    mbar_arrive(&bar[kIn]);
+                } else {
+                    mbar_arrive_expect_tx(&bar[kIn], 2 * G::kUnit);
 #pragma unroll
-                for (int b = 0; b < G::kBoxes; ++b)
-                    tma_load_3d(sm + unit(i) + b * kBox, i & 1 ? &maps.v : &maps.k, b * 64, hk, (int)(sk.bos + key0(t)), landing);
+                    for (int b = 0; b < G::kBoxes; ++b) {
+                        tma_load_3d(sm + G::kA + b * kBox, &maps.q, b * 64, it.h, it.t0, &bar[kIn]);
+                        tma_load_3d(sm + G::kB + b * kBox, &maps.dout, b * 64, it.h, it.t0, &bar[kIn]);
+                    }
+                }
             }
             __syncwarp();
-            if (mend) {
-                if (!(ok = all(wait(kLanded, mended++ & 1)))) break;
-                zero_rows<G::kBoxes>(sm + unit(i), sk.len - key0(t));
-                fence_proxy_async();
+            ++n;
+            if (it.rows == 0) break;
+            for (int u = -1; u <= 2 * it.nt; ++u, ++i) {
+                const int s = i % G::kRing, t = u >> 1;
+                if (i >= G::kRing && !(ok = all(wait(kEmpty + s, (i / G::kRing - 1) & 1)))) break;
+                if (u == 2 * it.nt) {  // (given to dQ as it is)
+                    if (lane == 0) mbar_arrive(&bar[kFull + s]);
+                    continue;
+                }
+                // K's rows behind the end are the next sequence's, and 0 x NaN is NaN: they are zeroed before the tile counts as full
+                const bool mend = u >= 0 && !(u & 1) && it.ragged(t);
+                uint64_t *const landing = &bar[mend ? (int)kLanded : kFull + s];
+                if (elect_one_sync()) {
+                    mbar_arrive_expect_tx(landing, G::kUnit);
+#pragma unroll
+                    for (int b = 0; b < G::kBoxes; ++b) {
+                        if (u < 0) tma_load_3d(sm + unit(i) + b * kBox, &maps.o, b * 64, it.h, it.t0, landing);
+                        else tma_load_3d(sm + unit(i) + b * kBox, u & 1 ? &maps.v : &maps.k, b * 64, it.hk, it.k0 + it.key0(t), landing);
+                    }
+                }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[kFull + s]);
+                if (mend) {
+                    if (!(ok = all(wait(kLanded, mended++ & 1)))) break;
+                    zero_rows<G::kBoxes>(sm + unit(i), it.klen - it.key0(t));
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar[kFull + s]);
+                }
             }
         }
-        if (!withhold) wait(kIn, 0);
-        for (int k = max(0, i - G::kRing); k < i; ++k) wait(kFull + k % G::kRing, (k / G::kRing) & 1);  // (no copy outlives the CTA)
-    } else if (warp == 9) {
+        // no copy outlives the CTA
+        if (n > 0) wait(kIn, (n - 1) & 1);
+        for (int k = max(0, i - G::kRing); k < i; ++k) wait(kFull + k % G::kRing, (k / G::kRing) & 1);
+    } else if (warp == kProducts) {
         // ---------------------------------------------------------------- products: S(t+1), dQ(t), dP(t+1)
+        auto key = [&](int t) { return first_unit + 1 + 2 * (t - from); };  // the unit of tile t's K; its V is the next
         auto scores = [&](int t) {
             tc_fence_after();
             if (elect_one_sync()) {
-                mma_rows<D>(tmem + kS + (t & 1) * 128, base + G::kA, base + unit(2 * t));
-                mma_commit(&bar[kSF + (t & 1)]);  // (two: the groups may not have seen the last one's)
+                mma_kept<D>(tmem + kS, tmem + kAQ, base + unit(key(t)));
+                mma_commit(&bar[kSF]);
             }
             __syncwarp();
         };
         auto slopes = [&](int t) {
             tc_fence_after();
             if (elect_one_sync()) {
-                mma_rows<D>(tmem + kP, base + G::kB, base + unit(2 * t + 1));
+                mma_kept<D>(tmem + kP, tmem + kAG, base + unit(key(t) + 1));
                 mma_commit(&bar[kPF]);
-                mma_commit(&bar[kEmpty + (2 * t + 1) % G::kRing]);
+                mma_commit(&bar[kEmpty + (key(t) + 1) % G::kRing]);
             }
             __syncwarp();
         };
-        bool ok = all(wait(kIn, 0));
-        if (ok && nt > 0 && (ok = full(0))) {
-            scores(0);
-            if ((ok = full(1))) slopes(0);
-        }
-        for (int t = 0; t < nt && ok; ++t) {
-            if (t + 1 < nt) {
-                if (!(ok = full(2 * t + 2))) break;
-                scores(t + 1);
+        for (;; ++n) {
+            // (the groups have taken all of the last tile of queries' scores)
+            if (!(ok = all(wait(kAB, n & 1)))) break;
+            it = handed[n & 1];
+            if (it.rows == 0) break;
+            const int end = from + it.nt;
+            if (it.nt > 0) {
+                if (!(ok = full(key(from)))) break;
+                scores(from);
+                if (!(ok = full(key(from) + 1))) break;
+                slopes(from);
             }
-            if (!(ok = all(wait(kZB, t & 1)))) break;
-            tc_fence_after();
-            if (elect_one_sync()) {
-                mma_sum<D>(tmem + kQ, tmem + kS + (t & 1) * 128, base + unit(2 * t), t == 0);
-                mma_commit(&bar[kEmpty + (2 * t) % G::kRing]);
+            for (int t = from; t < end; ++t) {
+                if (t + 1 < end) {
+                    if (!(ok = all(wait(kSR, t & 1)) && full(key(t + 1)))) break;
+                    scores(t + 1);
+                }
+                if (!(ok = all(wait(kZB, t & 1)))) break;
+                tc_fence_after();
+                if (elect_one_sync()) {
+                    mma_sum<D>(tmem + kQ, tmem + kP, base + unit(key(t)), t == from);
+                    mma_commit(&bar[kEmpty + key(t) % G::kRing]);
+                }
+                __syncwarp();
+                if (t + 1 < end) {
+                    if (!(ok = full(key(t + 1) + 1))) break;
+                    slopes(t + 1);
+                }
             }
+            if (!ok) break;
+            if (elect_one_sync()) mma_commit(&bar[kDone]);
             __syncwarp();
-            if (t + 1 < nt) {
-                if (!(ok = full(2 * t + 3))) break;
-                slopes(t + 1);
-            }
+            first_unit += 2 + 2 * it.nt;
+            from = end;
         }
-        if (elect_one_sync()) mma_commit(&bar[kDone]);
+        if (elect_one_sync()) mma_commit(&bar[kFin]);  // every product has ended before the tensor memory goes
         __syncwarp();
-        wait(kDone, 0);
+        wait(kFin, 0);
     } else {
-        const int x = warp >> 2, r = tid & 127, p = p0 + r;
+        const int x = warp >> 2, r = tid & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lanes + kS + kCols * x, tp = tmem + lanes + kP + kCols * x;
         const float c = a.scale * kLog2e;
-        float *part = (float *)(sm + G::kStats);
-        const int64_t at = lse_at(a, tl.n, sq.bos, h) + i0 + r;
-        float lse = r < rows ? a.lse[at] * kLog2e : INFINITY;
-        if (lse == -INFINITY) lse = INFINITY;  // a row that sees nothing: weights of zero
-        // delta: each group half of the row, from dO in shared memory and o
-        float d = 0.f;
-        bool ok = bar_all(1, 256, warp != 0 || wait(kIn, 0));
-        if (ok && r < rows) {
+        float *const part = (float *)(sm + G::kStats);
+        bool stored = false;  // (thread 0: a store is on its way from a unit's place)
+        int place = 0;
+        // the next tile of queries: Q by one group, dO by the other, to tensor memory; delta by the other, which has the row of dO (what stands
+        // behind the last row is not taken).  Before any product of the tile: they leave little of shared memory to others.
+        auto take = [&]() {
+            if (!(ok = bar_all(1, kLanes, warp != 0 || wait(kIn, n & 1)))) return;
+            it = handed[n & 1];
+            if (it.rows > 0) {
+                if (!(ok = bar_all(1, kLanes, warp != 0 || wait(kFull + first_unit % G::kRing, (first_unit / G::kRing) & 1)))) return;
+                const uint8_t *src = sm + (x == 0 ? G::kA : G::kB);
+                uint32_t w[D / 2];
 #pragma unroll
-            for (int e = 0; e < D / 2; e += 8) {
-                const uint4 u = row[e / 8];
-                const int col = x * (D / 2) + e;
-                const uint4 g = *(const uint4 *)(sm + G::kB + (col >> 6) * kBox + sw128(r, col & 63));
-                const uint32_t *pu = (const uint32_t *)&u, *pg = (const uint32_t *)&g;
+                for (int col = 0; col < D; col += 8) *(uint4 *)&w[col / 2] = *(const uint4 *)(src + (col >> 6) * kBox + sw128(r, col & 63));
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    d = fmaf(__uint_as_float(pu[k] << 16), __uint_as_float(pg[k] << 16), d);
-                    d = fmaf(__uint_as_float(pu[k] & 0xffff0000u), __uint_as_float(pg[k] & 0xffff0000u), d);
+                for (int col = 0; col < D; col += 32) tmem_st16(tmem + lanes + (x == 0 ? kAQ : kAG) + col / 2, w + col / 2);
+                if (x != 0) {
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int col = 0; col < D; col += 8) {
+                        const uint4 u = *(const uint4 *)(sm + unit(first_unit) + (col >> 6) * kBox + sw128(r, col & 63));
+                        const uint32_t *pu = (const uint32_t *)&u, *pg = w + col / 2;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) sum[k] = fmaf(high_bf16(pu[k]), high_bf16(pg[k]), fmaf(low_bf16(pu[k]), low_bf16(pg[k]), sum[k]));
+                    }
+                    part[r] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 }
+                tmem_st_wait();
             }
-        }
-        part[x * 128 + r] = d;
-        ok = bar_all(1, 256, ok);
-        d = part[r] + part[128 + r];
-        if (x == 0 && r < rows) delta[at] = d;
-        for (int t = 0; t < nt && ok; ++t) {
-            const int j0 = key0(t) + 64 * x, cols = columns(t) - 64 * x;
-            const uint32_t ts = tmem + lanes + kS + (t & 1) * 128 + 64 * x, tp = tmem + lanes + kP + 64 * x;
-            if (!(ok = bar_all(1, 256, warp != 0 || wait(kSF + (t & 1), (t >> 1) & 1)))) break;
-            tc_fence_after();
-            float s[64];
-            tmem_ld32(ts, (uint32_t *)s);
-            tmem_ld32(ts + 32, (uint32_t *)s + 32);
-            tmem_ld_wait();
-            const Pair cc = pair_of(c, c), minus = pair_of(-lse, -lse);
-#pragma unroll
-            for (int j = 0; j < 64; j += 2) {
-                unpair(fma2(pair_of(s[j], s[j + 1]), cc, minus), s[j], s[j + 1]);
-                s[j] = ex2(s[j]);
-                s[j + 1] = ex2(s[j + 1]);
-            }
-            const bool whole = cols >= 64 && j0 + 63 <= p0 && (p0 + rows - 1 - j0 < a.window || j0 + 64 <= a.sinks);
-            if (!whole) {
-                const int end = min(cols, p - j0 + 1), begin = p - a.window + 1 - j0, sink = a.sinks - j0;
-#pragma unroll
-                for (int j = 0; j < 64; ++j)
-                    s[j] = (int)(j < end) & ((int)(j >= begin) | (int)(j < sink)) ? s[j] : 0.f;
-            }
-            if (!(ok = bar_all(1, 256, warp != 0 || wait(kPF, t & 1)))) break;
-            tc_fence_after();
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                float g[32];
-                uint32_t w[16];
-                tmem_ld32(tp + 32 * q, (uint32_t *)g);
-                tmem_ld_wait();
-                if (!whole) {  // (dP is not finite where a key outside the sequence is not)
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) g[j] = s[32 * q + j] == 0.f ? 0.f : g[j];
-                }
-#pragma unroll
-                for (int j = 0; j < 16; ++j) w[j] = pack_bf16(s[32 * q + 2 * j] * (g[2 * j] - d), s[32 * q + 2 * j + 1] * (g[2 * j + 1] - d));
-                tmem_st16(ts + 16 * q, w);
-            }
-            tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[kZB]);
-        }
-        ok = bar_all(1, 256, (warp != 0 || wait(kDone, 0)) && ok);
-        if (ok) {
-            tc_fence_after();
-            uint8_t *tile = sm + G::kA;  // (the last scores are taken)
+            if (lane == 0) mbar_arrive(&bar[kAB]);
+        };
+        take();
+        while (ok && it.rows > 0) {
+            const int p = it.p0 + r;
+            float lse = r < it.rows ? a.lse[it.at + r] : INFINITY;
+            bar_sync(1, kLanes);
+            if (tid == 0) {  // (the next tile of queries may be loaded, and another unit in O's place and in the last dQ's)
+                mbar_arrive(&bar[kTaken]);
+                mbar_arrive(&bar[kEmpty + first_unit % G::kRing]);
+                if (stored) {
+                    tma_store_wait_read0();
+                    mbar_arrive(&bar[kEmpty + place]);
+                    stored = false;
+                }
+            }
+            const float d = part[r];
+            if (x == 0 && r < it.rows) delta[it.at + r] = d;
+            lse = lse == -INFINITY ? INFINITY : lse * kLog2e;  // (a row that sees nothing: weights of zero)
+            for (int t = 0; t < it.nt; ++t) {
+                const int j0 = it.key0(t) + kCols * x, cols = it.columns(t) - kCols * x;
+                if (!(ok = bar_all(1, kLanes, warp != 0 || wait(kSF, (from + t) & 1)))) break;
+                tc_fence_after();
+                float s[kCols];
 #pragma unroll
-            for (int q = 0; q < D / 64; ++q) {
-                const int col = x * (D / 2) + 32 * q;
+                for (int q = 0; q < kCols; q += 32) tmem_ld32(ts + q, (uint32_t *)s + q);
+                tmem_ld_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[kSR]);  // (the next tile's scores may come)
+                const Pair cc = pair_of(c, c), minus = pair_of(-lse, -lse);
+#pragma unroll
+                for (int j = 0; j < kCols; j += 2) {
+                    unpair(fma2(pair_of(s[j], s[j + 1]), cc, minus), s[j], s[j + 1]);
+                    s[j] = ex2(s[j]);
+                    s[j + 1] = ex2(s[j + 1]);
+                }
+                if (!(cols >= kCols && j0 + kCols - 1 <= it.p0 && (it.p0 + it.rows - 1 - j0 < a.window || j0 + kCols <= a.sinks))) {
+                    const int end = min(cols, p - j0 + 1), begin = p - a.window + 1 - j0, sink = max(a.sinks - j0, 0);
+                    if (__any_sync(0xffffffffu, end < kCols)) {
+#pragma unroll
+                        for (int j = 0; j < kCols; ++j) s[j] = j < end ? s[j] : 0.f;
+                    }
+                    if (__any_sync(0xffffffffu, sink < begin)) {
+#pragma unroll
+                        for (int j = 0; j < kCols; ++j) s[j] = (int)(j >= begin) | (int)(j < sink) ? s[j] : 0.f;
+                    }
+                }
+                if (!(ok = bar_all(1, kLanes, warp != 0 || wait(kPF, (from + t) & 1)))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int q = 0; q < kCols; q += 32) {
+                    float g[32];
+                    uint32_t w[16];
+                    tmem_ld32(tp + q, (uint32_t *)g);
+                    tmem_ld_wait();
+                    if (it.ragged(t)) {  // (dP is not finite where a key outside the sequence is not)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) g[j] = s[q + j] == 0.f ? 0.f : g[j];
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) w[j] = pack_bf16(s[q + 2 * j] * (g[2 * j] - d), s[q + 2 * j + 1] * (g[2 * j + 1] - d));
+                    tmem_st16(tp + q / 2, w);  // (over columns that are read already)
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[kZB]);
+            }
+            from += it.nt;
+            first_unit += 2 + 2 * it.nt;
+            if (!ok || !(ok = bar_all(1, kLanes, warp != 0 || (wait(kDone, n & 1) && wait(kFull + (first_unit - 1) % G::kRing, ((first_unit - 1) / G::kRing) & 1)))))
+                break;
+            ++n;
+            tc_fence_after();
+            // the products go on with the next tile of queries while this one's gradient is stored
+            const int t0 = it.t0, rows = it.rows, h = it.h, nt = it.nt;
+            take();
+            uint8_t *const tile = sm + unit(first_unit - 1);
+#pragma unroll
+            for (int q = 0; q < D / kGroups; q += 32) {
+                const int col = x * (D / kGroups) + q;
                 float o[32];
                 if (nt > 0) {
                     tmem_ld32(tmem + lanes + kQ + col, (uint32_t *)o);
@@ -316,16 +420,29 @@ __global__ void __launch_bounds__(kThreads, 1) win_dq_kernel(const __grid_consta
 #pragma unroll
                 for (int j = 0; j < 32; ++j) o[j] = nt > 0 ? o[j] * a.scale : 0.f;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) *(uint4 *)(tile + (col >> 6) * kBox + sw128(r, (col & 63) + 8 * j)) = pack8(o + 8 * j);
+                for (int j = 0; j < 32; j += 8) *(uint4 *)(tile + (col >> 6) * kBox + sw128(r, (col & 63) + j)) = pack8(o + j);
             }
             fence_proxy_async();
-            bar_sync(1, 256);
-            if (x == 0) store_rows<D>(&maps.dq, a.dq, tile, sq.bos + i0, rows, a.H, h, r);
+            bar_sync(1, kLanes);
+            place = (first_unit - 1) % G::kRing;
+            if (rows == kTile) {
+                if (tid == 0) {
+#pragma unroll
+                    for (int b = 0; b < G::kBoxes; ++b) tma_store_3d(&maps.dq, tile + b * kBox, b * 64, h, t0);
+                    tma_store_commit();
+                    stored = true;
+                }
+            } else {
+                copy_rows<D, kLanes>(a.dq, tile, t0, rows, a.H, h, tid);
+                bar_sync(1, kLanes);
+                if (tid == 0) mbar_arrive(&bar[kEmpty + place]);
+            }
         }
+        if (tid == 0) tma_store_wait0();
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == kLoads) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmem);
     }
@@ -351,7 +468,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1) win_dkv_kernel(const __grid_constant__ Maps maps, const WinArgs a, const Sinks sinks, int64_t key_tiles,
                                                               uint64_t limit, int withhold)
 {
-    using G = Geo<D, 4>;
+    using G = Geo<D>;
     constexpr uint32_t kS = 0, kP = 128, kV = 256, kK = 384;  // S^T (P^T in its place), dP^T (Z^T), dV, dK
     extern __shared__ uint8_t win_bwd_smem[];
     uint8_t *const sm = win_bwd_smem + (-smem_u32(win_bwd_smem) & 1023u);  // (an offset: a cast would lose that it is shared memory)
@@ -387,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1) win_dkv_kernel(const __grid_const
         prefetch_map(&maps.k);
         prefetch_map(&maps.v);
     }
-    if (warp == 8) tmem_alloc(tslot, kTmem);
+    if (warp == kLoads) tmem_alloc(tslot, kTmem);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -401,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1) win_dkv_kernel(const __grid_const
     auto head = [&](int t) { return hk * per + t / tiles; };
     auto ragged = [&](int t) { return query0(t) + kTile > sq.len; };
 
-    if (warp == 8) {
+    if (warp == kLoads) {
         // ---------------------------------------------------------------- loads
         bool ok = !withhold;
         if (ok && elect_one_sync()) {
@@ -437,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1) win_dkv_kernel(const __grid_const
         }
         if (!withhold) wait(kIn, 0);
         for (int k = max(0, i - G::kRing); k < i; ++k) wait(kFull + k % G::kRing, (k / G::kRing) & 1);  // (no copy outlives the CTA)
-    } else if (warp == 9) {
+    } else if (warp == kProducts) {
         // ---------------------------------------------------------------- products: dV(t), S(t+1), dK(t), dP(t+1)
         auto scores = [&](int t) {
             tc_fence_after();
@@ -490,51 +607,59 @@ __global__ void __launch_bounds__(kThreads, 1) win_dkv_kernel(const __grid_const
     } else {
         const int x = warp >> 2, r = tid & 127, j = j0 + r;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + lanes + kS + 64 * x, tp = tmem + lanes + kP + 64 * x;
+        const uint32_t ts = tmem + lanes + kS + kCols * x, tp = tmem + lanes + kP + kCols * x;
         const float c = a.scale * kLog2e;
-        float *const stats = (float *)(sm + G::kStats) + x * 256;  // [tile parity][lse, delta][64 queries of this group]
-        // this thread's number of tile t: lse (of the first 64 threads) or delta of one of the group's queries
+        float *const stats = (float *)(sm + G::kStats) + x * 2 * kCols;  // [lse, delta][the group's queries]
+        // this thread's number of tile t: lse (the first half of a group) or delta (the second) of one of the group's queries
         auto stat = [&](int t) {
-            const int i = query0(t) + 64 * x + (r & 63);
-            if (i >= end) return r < 64 ? INFINITY : 0.f;  // weights of zero
+            const int i = query0(t) + kCols * x + (r & (kCols - 1));
+            if (i >= end) return r < kCols ? INFINITY : 0.f;  // weights of zero
             const int64_t at = lse_at(a, tl.n, sq.bos, head(t)) + i;
-            if (r >= 64) return a.delta[at];
+            if (r >= kCols) return a.delta[at];
             const float l = a.lse[at] * kLog2e;
             return l == -INFINITY ? INFINITY : l;
         };
         float next = nt > 0 ? stat(0) : 0.f;
         bool ok = true;
         for (int t = 0; t < nt; ++t) {
-            const int i0 = query0(t) + 64 * x, q0 = i0 + off, rows = min(end - i0, 64);  // (the group's 64 queries)
-            float *const ls = stats + (t & 1) * 128, *const dl = ls + 64;
-            ls[r] = next;
+            const int i0 = query0(t) + kCols * x, q0 = i0 + off, rows = min(end - i0, kCols);  // (the group's queries)
+            float *const ls = stats, *const dl = ls + kCols;
+            // (each is read between one of the two barriers and the other)
+            const float now = next;
+            if (r < kCols) ls[r] = now;
             if (t + 1 < nt) next = stat(t + 1);
             if (!(ok = bar_all(1 + x, 128, (warp & 3) || wait(kSF, t & 1)))) break;  // (the group leaves together)
+            if (r >= kCols) ls[r] = now;
             tc_fence_after();
-            float s[64];
-            tmem_ld32(ts, (uint32_t *)s);
-            tmem_ld32(ts + 32, (uint32_t *)s + 32);
+            float s[kCols];
+#pragma unroll
+            for (int q = 0; q < kCols; q += 32) tmem_ld32(ts + q, (uint32_t *)s + q);
             tmem_ld_wait();
 #pragma unroll
-            for (int k = 0; k < 64; k += 4) {
+            for (int k = 0; k < kCols; k += 4) {
                 const float4 l = *(const float4 *)(ls + k);
                 s[k] = ex2(fmaf(s[k], c, -l.x));
                 s[k + 1] = ex2(fmaf(s[k + 1], c, -l.y));
                 s[k + 2] = ex2(fmaf(s[k + 2], c, -l.z));
                 s[k + 3] = ex2(fmaf(s[k + 3], c, -l.w));
             }
-            if (!(rows == 64 && j0 + kTile - 1 <= q0 && (q0 + 63 - j0 < a.window || j0 + kTile <= a.sinks))) {
+            if (!(rows == kCols && j0 + kTile - 1 <= q0 && (q0 + kCols - 1 - j0 < a.window || j0 + kTile <= a.sinks))) {
                 const int first = j - q0, last = j < a.sinks ? rows : (int)min((int64_t)rows, (int64_t)j + a.window - q0);
+                if (__any_sync(0xffffffffu, first > 0)) {
 #pragma unroll
-                for (int k = 0; k < 64; ++k)
-                    s[k] = (int)(k >= first) & (int)(k < last) ? s[k] : 0.f;
+                    for (int k = 0; k < kCols; ++k) s[k] = k >= first ? s[k] : 0.f;
+                }
+                if (__any_sync(0xffffffffu, last < kCols)) {
+#pragma unroll
+                    for (int k = 0; k < kCols; ++k) s[k] = k < last ? s[k] : 0.f;
+                }
             }
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
+            for (int q = 0; q < kCols; q += 32) {
                 uint32_t w[16];
 #pragma unroll
-                for (int k = 0; k < 16; ++k) w[k] = pack_bf16(s[32 * q + 2 * k], s[32 * q + 2 * k + 1]);
-                tmem_st16(ts + 16 * q, w);
+                for (int k = 0; k < 16; ++k) w[k] = pack_bf16(s[q + 2 * k], s[q + 2 * k + 1]);
+                tmem_st16(ts + q / 2, w);
             }
             tmem_st_wait();
             tc_fence_before();
@@ -543,19 +668,19 @@ __global__ void __launch_bounds__(kThreads, 1) win_dkv_kernel(const __grid_const
             if (!(ok = bar_all(1 + x, 128, (warp & 3) || wait(kPF, t & 1)))) break;
             tc_fence_after();
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
+            for (int q = 0; q < kCols; q += 32) {
                 float g[32];
                 uint32_t w[16];
-                tmem_ld32(tp + 32 * q, (uint32_t *)g);
+                tmem_ld32(tp + q, (uint32_t *)g);
                 tmem_ld_wait();
 #pragma unroll
                 for (int k = 0; k < 32; k += 4) {
-                    const float4 d = *(const float4 *)(dl + 32 * q + k);
-                    const float *u = s + 32 * q + k;
+                    const float4 d = *(const float4 *)(dl + q + k);
+                    const float *u = s + q + k;
                     w[k / 2] = pack_bf16(u[0] * (g[k] - d.x), u[1] * (g[k + 1] - d.y));
                     w[k / 2 + 1] = pack_bf16(u[2] * (g[k + 2] - d.z), u[3] * (g[k + 3] - d.w));
                 }
-                tmem_st16(tp + 16 * q, w);
+                tmem_st16(tp + q / 2, w);
             }
             tmem_st_wait();
             tc_fence_before();
@@ -563,39 +688,47 @@ __global__ void __launch_bounds__(kThreads, 1) win_dkv_kernel(const __grid_const
             if (lane == 0) mbar_arrive(&bar[kZB]);
         }
         // ---------------------------------------------------------------- dV by the first group, dK by the second
+        const bool key = x != 0;
         ok = bar_all(1 + x, 128, ((warp & 3) || wait(kDone, 0)) && ok);
         if (ok) {
             tc_fence_after();
-            const float f = x == 0 ? 1.f : a.scale;
-            uint8_t *tile = sm + (x == 0 ? G::kB : G::kA);  // (V's and K's last products are taken)
+            const float f = key ? a.scale : 1.f;
+            uint8_t *tile = sm + (key ? G::kA : G::kB);  // (K's and V's last products are taken)
 #pragma unroll
-            for (int q = 0; q < D / 32; ++q) {
+            for (int col = 0; col < D; col += 32) {
                 float o[32];
                 if (nt > 0) {
-                    tmem_ld32(tmem + lanes + (x == 0 ? kV : kK) + 32 * q, (uint32_t *)o);
+                    tmem_ld32(tmem + lanes + (key ? kK : kV) + col, (uint32_t *)o);
                     tmem_ld_wait();
                 }
 #pragma unroll
                 for (int k = 0; k < 32; ++k) o[k] = nt > 0 ? o[k] * f : 0.f;
                 if (part) {
-                    float *dst = part + ((int64_t)(1 - x) * kTile + r) * D + 32 * q;  // dK, then dV
+                    float *dst = part + ((int64_t)(1 - key) * kTile + r) * D + col;  // dK, then dV
 #pragma unroll
                     for (int k = 0; k < 32; k += 4) *(float4 *)(dst + k) = *(const float4 *)&o[k];
                 } else {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) *(uint4 *)(tile + (q >> 1) * kBox + sw128(r, 32 * (q & 1) + 8 * k)) = pack8(o + 8 * k);
+                    for (int k = 0; k < 4; ++k) *(uint4 *)(tile + (col >> 6) * kBox + sw128(r, (col & 63) + 8 * k)) = pack8(o + 8 * k);
                 }
             }
             if (!part) {
                 fence_proxy_async();
                 bar_sync(1 + x, 128);
-                store_rows<D>(x == 0 ? &maps.dv : &maps.dk, x == 0 ? a.dv : a.dk, tile, sk.bos + j0, cols, a.HK, hk, r);
+                if (cols < kTile) {
+                    copy_rows<D, 128>(key ? a.dk : a.dv, tile, sk.bos + j0, cols, a.HK, hk, r);
+                } else if (r == 0) {
+#pragma unroll
+                    for (int b = 0; b < G::kBoxes; ++b) tma_store_3d(key ? &maps.dk : &maps.dv, tile + b * kBox, b * 64, hk, (int)(sk.bos + j0));
+                    tma_store_commit();
+                    tma_store_wait0();
+                }
             }
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == kLoads) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmem);
     }
@@ -643,14 +776,15 @@ cudaError_t launch(const WinArgs &a, int64_t tq, int64_t tk, float *delta, void 
     Maps maps;
     if (!heads_map(&maps.q, a.q, D, a.H, tq, a.ldq, kTile) || !heads_map(&maps.k, a.k, D, a.HK, tk, a.ldk, kTile) ||
         !heads_map(&maps.v, a.v, D, a.HK, tk, a.ldv, kTile) || !heads_map(&maps.dout, a.dout, D, a.H, tq, a.ld_dout, kTile) ||
-        !heads_map(&maps.dq, a.dq, D, a.H, tq, (int64_t)a.H * D, kTile) || !heads_map(&maps.dk, a.dk, D, a.HK, tk, (int64_t)a.HK * D, kTile) ||
+        !heads_map(&maps.o, a.o, D, a.H, tq, (int64_t)a.H * D, kTile) || !heads_map(&maps.dq, a.dq, D, a.H, tq, (int64_t)a.H * D, kTile) ||
+        !heads_map(&maps.dk, a.dk, D, a.HK, tk, (int64_t)a.HK * D, kTile) ||
         !heads_map(&maps.dv, a.dv, D, a.HK, tk, (int64_t)a.HK * D, kTile))
         return cudaErrorInvalidValue;
-    constexpr int smem_q = Geo<D, ring_of_dq(D)>::kSmem, smem_k = Geo<D, 4>::kSmem;
+    constexpr int smem = Geo<D>::kSmem;
     static std::atomic<uint64_t> seen;
     if (first_on_device(seen)) {
-        cudaError_t e = cudaFuncSetAttribute(win_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_q);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(win_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_k);
+        cudaError_t e = cudaFuncSetAttribute(win_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(win_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         done_on_device(seen);
     }
@@ -660,11 +794,11 @@ cudaError_t launch(const WinArgs &a, int64_t tq, int64_t tk, float *delta, void 
     s.run = s.own + (int64_t)a.N * a.HK * s.tiles * 2 * kTile * D;
     const int64_t qt = mix_slots(a.cu_q != nullptr, a.N, a.Tq, kTile), kt = mix_slots(a.cu_k != nullptr, a.N, a.Tk, kTile);
     const int64_t ctas = kt + s.slots * s.tiles;
-    if (qt > INT32_MAX || ctas > INT32_MAX || (int64_t)a.N * kTile * D / 1024 > INT32_MAX) return cudaErrorInvalidConfiguration;
+    if (qt * a.H > INT32_MAX || ctas > INT32_MAX || (int64_t)a.N * kTile * D / 1024 > INT32_MAX) return cudaErrorInvalidConfiguration;
     const int withhold = withhold_loads();
     const uint64_t limit = withhold ? kTestWaitLimitNs : kWaitLimitNs;
-    win_dq_kernel<D><<<dim3((unsigned)qt, a.H), kThreads, smem_q, st>>>(maps, a, delta, limit, withhold);
-    win_dkv_kernel<D><<<dim3((unsigned)ctas, a.HK), kThreads, smem_k, st>>>(maps, a, s, kt, limit, withhold);
+    win_dq_kernel<D><<<(unsigned)std::min<int64_t>(qt * a.H, device_sm_count()), kThreads, smem, st>>>(maps, a, (unsigned)(qt * a.H), delta, limit, withhold);
+    win_dkv_kernel<D><<<dim3((unsigned)ctas, a.HK), kThreads, smem, st>>>(maps, a, s, kt, limit, withhold);
     if (s.tiles > 0) win_sinks_kernel<D><<<dim3((unsigned)(a.N * (kTile * D / 1024)), a.HK * s.tiles, 2), 256, 0, st>>>(a, s);
     return cudaGetLastError();
 }
