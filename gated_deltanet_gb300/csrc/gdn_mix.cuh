@@ -138,6 +138,73 @@ __host__ __device__ inline int64_t lse_at(const WinArgs &a, int n, int64_t bos, 
     // element of row `bos` (the first of sequence n) and head h
     return a.cu_q ? (int64_t)h * a.Tq + bos : ((int64_t)n * a.H + h) * a.Tq;
 }
+// Keys that are sinks are seen by every query behind them.  Where the window does not reach, the queries of a tile of sinks are dealt out
+// to CTAs of their own, `run` queries each, whose fp32 parts of dK and dV a join adds to the tile's in order: one CTA for all of them would
+// walk the whole sequence while the others see a window.
+struct WinSinks {
+    float *own, *parts;  // [N][HK][tiles][2][tile][D] of the tiles' own CTAs, [slots][HK][tiles][2][tile][D] of the runs
+    int tiles;           // tiles of sinks whose far queries are dealt out; 0: none
+    int64_t slots;       // runs of all sequences
+};
+inline WinSinks win_sinks_plan(const WinArgs &a, int tile, int run, int most, void *ws, size_t *bytes)
+{
+    WinSinks s{};
+    const int tiles = (a.sinks + tile - 1) / tile;
+    *bytes = 0;
+    if (a.window >= a.Tk || tiles > most || tiles == 0) return s;
+    s.tiles = tiles;
+    s.slots = mix_slots(a.cu_q != nullptr, a.N, a.Tq, run);
+    const int64_t each = (int64_t)a.HK * tiles * 2 * tile * a.D;
+    s.own = (float *)ws;
+    s.parts = s.own + a.N * each;
+    *bytes = (size_t)(a.N + s.slots) * each * sizeof(float);
+    return s;
+}
+// What a CTA of dK and dV sums: a tile of keys against queries begin .. end of each head
+struct WinKeyTile {
+    SeqRange sq, sk;
+    int n, j0, cols, off, begin, end;
+    float *part;  // fp32 [2][tile][D] (dK, dV) in place of the gradients; null: these
+    __device__ __forceinline__ WinKeyTile(const WinArgs &a, const WinSinks &s, int64_t key_tiles, int tile, int run, int64_t item, int hk)
+    {
+        const bool far = item >= key_tiles;  // a run of queries against a tile of sinks
+        if (far) item -= key_tiles;
+        const Tile tl = far ? tile_of(a.cu_q, a.N, a.Tq, run, item / s.tiles) : tile_of(a.cu_k, a.N, a.Tk, tile, item);
+        n = tl.n;
+        sq = seq_range(a.cu_q, n, a.Tq);
+        sk = seq_range(a.cu_k, n, a.Tk);
+        const int st = far ? (int)(item % s.tiles) : tl.index;
+        j0 = st * tile;
+        cols = min(tile, sk.len - j0);
+        off = sk.len - sq.len;
+        begin = max(0, j0 - off);
+        end = (int)clamp64((int64_t)j0 + cols - 1 + a.window - off, 0, sq.len);  // the last (exclusive) that sees a key through the window
+        const bool dealt = !far && st < s.tiles;
+        if (far) {
+            begin = max(max(begin, end), tl.index * run);
+            end = (int)min((int64_t)sq.len, (int64_t)(tl.index + 1) * run);
+            if (begin >= end) cols = 0;  // (nothing to do)
+        } else if (!dealt && j0 < a.sinks) {
+            end = sq.len;
+        }
+        const int64_t size = (int64_t)2 * tile * a.D;
+        part = far ? s.parts + ((item / s.tiles * a.HK + hk) * s.tiles + st) * size : dealt ? s.own + (((int64_t)n * a.HK + hk) * s.tiles + st) * size : nullptr;
+    }
+};
+__device__ __forceinline__ float added(float x, float y) { return x + y; }
+__device__ __forceinline__ float4 added(float4 x, float4 y) { return make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w); }
+// what stands at `at` in the parts [2][tile][D] of a tile of sinks, added up in order (F: one element, or four)
+template <typename F>
+__device__ __forceinline__ F win_sinks_sum(const WinArgs &a, const WinSinks &s, int tile, int run, int n, int hk, int st, int64_t at)
+{
+    const SeqRange sq = seq_range(a.cu_q, n, a.Tq), sk = seq_range(a.cu_k, n, a.Tk);
+    const int j0 = st * tile, cols = min(tile, sk.len - j0), off = sk.len - sq.len;
+    const int from = max(max(0, j0 - off), (int)clamp64((int64_t)j0 + cols - 1 + a.window - off, 0, sq.len));  // the first query of a run
+    const int64_t slot0 = a.cu_q ? clamp64(a.cu_q[n], 0, a.Tq) / run + n : (int64_t)n * ((a.Tq + run - 1) / run), size = (int64_t)2 * tile * a.D;
+    F x = *(const F *)(s.own + (((int64_t)n * a.HK + hk) * s.tiles + st) * size + at);
+    for (int i = from / run; from < sq.len && i * run < sq.len; ++i) x = added(x, *(const F *)(s.parts + (((slot0 + i) * a.HK + hk) * s.tiles + st) * size + at));
+    return x;
+}
 __device__ __forceinline__ bool win_sees(int p, int j, int window, int sinks) { return j <= p && (p - j < window || j < sinks); }
 cudaError_t launch_win_simt(const WinArgs &a, gdn_dtype dt, cudaStream_t st);
 // bf16 heads of 64 or 128, rows on 16-byte boundaries, a positive scale: on the tensor cores (tq, tk: all tokens)
@@ -150,7 +217,8 @@ cudaError_t launch_win_bwd_tc(const WinArgs &a, int64_t tq, int64_t tk, float *d
 gdn_status read_win_bwd_status(cudaStream_t st);
 cudaError_t launch_win_delta(const void *dout, int64_t ld_dout, const void *o, const WinArgs &a, gdn_dtype dt, float *delta, cudaStream_t st);
 cudaError_t launch_win_dq_simt(const WinArgs &a, gdn_dtype dt, cudaStream_t st);
-cudaError_t launch_win_dkv_simt(const WinArgs &a, gdn_dtype dt, cudaStream_t st);
+size_t win_dkv_simt_bytes(const WinArgs &a);  // of workspace, beside delta
+cudaError_t launch_win_dkv_simt(const WinArgs &a, gdn_dtype dt, void *ws, cudaStream_t st);
 
 struct WinStepArgs {
     const void *q;              // [N][T][H][D], token stride ldq

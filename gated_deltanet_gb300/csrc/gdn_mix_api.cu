@@ -260,7 +260,7 @@ gdn_status gdn_window_attn(const gdn_window_attn_args *a, void *, size_t, gdn_st
 size_t gdn_window_attn_bwd_workspace_size(const gdn_window_attn_args *a)
 {
     if (check_win(a, true) != GDN_OK || a->num_seqs == 0) return 0;
-    return win_delta_bytes(a) + (win_bwd_on_tc(a) ? win_bwd_tc_bytes(win_args(a)) : 0);
+    return win_delta_bytes(a) + (win_bwd_on_tc(a) ? win_bwd_tc_bytes(win_args(a)) : win_dkv_simt_bytes(win_args(a)));
 }
 
 gdn_status gdn_window_attn_bwd(const gdn_window_attn_args *a, void *ws, size_t ws_bytes, gdn_stream_t stream)
@@ -277,7 +277,7 @@ gdn_status gdn_window_attn_bwd(const gdn_window_attn_args *a, void *ws, size_t w
     cudaError_t e = cudaSuccess;
     if (tq > 0) e = launch_win_delta(a->dout, a->ld_dout, a->o, w, a->dtype, delta, stream);
     if (e == cudaSuccess && tq > 0) e = launch_win_dq_simt(w, a->dtype, stream);
-    if (e == cudaSuccess && tk > 0) e = launch_win_dkv_simt(w, a->dtype, stream);
+    if (e == cudaSuccess && tk > 0) e = launch_win_dkv_simt(w, a->dtype, base + win_delta_bytes(a), stream);
     return of(e);
 }
 

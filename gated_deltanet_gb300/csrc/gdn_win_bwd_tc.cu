@@ -7,9 +7,7 @@
 //   win_dq_kernel   128 queries of a head against the tiles of 128 keys that they see; also takes delta
 //   win_dkv_kernel  128 keys of a key head against the tiles of 128 queries of its heads that see them, scores transposed (a lane is
 //                   a key), so that P^T and Z^T are left operands in tensor memory as they come
-// Sinks are seen by every query behind them.  Where the window does not reach, the queries of a tile of sinks are dealt out to CTAs of
-// their own (kSinkRun queries each) whose fp32 parts win_sinks_kernel adds to the tile's in order: one CTA for all of them would walk
-// the whole sequence while the others see a window.
+// The far queries of sinks are dealt out to CTAs of their own, whose parts win_sinks_kernel adds up (WinSinks).
 //
 // 4 x 4096 tokens, 16 heads over 4 of 128, window 1024: dQ 212 us, dK and dV 270, 137 GFLOP of scores each way.
 //  - dQ: one CTA per SM walks tiles of queries (a CTA to each: 245 us; starting one and filling its pipeline took 12000 cycles, the walk 24000).
@@ -452,20 +450,8 @@ __global__ void __launch_bounds__(kThreads, 1) win_dq_kernel(const __grid_consta
 constexpr int kSinkRun = 1024;   // queries of a CTA that sums for a tile of sinks where the window does not reach
 constexpr int kMostSinkTiles = 4;  // (more tiles of sinks share the work among them)
 
-struct Sinks {
-    float *own, *run;  // fp32 parts [N][HK][tiles][2][128][D] of the tiles' own CTAs and [slots][HK][tiles][2][128][D] of the runs
-    int tiles;         // tiles of sinks whose far queries are dealt out; 0: none
-    int64_t slots;
-};
-
-// the last query (exclusive) that sees a key of j0 .. j0 + cols - 1 through the window
-__device__ __forceinline__ int window_end(const WinArgs &a, int j0, int cols, int off, int Lq)
-{
-    return (int)clamp64((int64_t)j0 + cols - 1 + a.window - off, 0, Lq);
-}
-
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) win_dkv_kernel(const __grid_constant__ Maps maps, const WinArgs a, const Sinks sinks, int64_t key_tiles,
+__global__ void __launch_bounds__(kThreads, 1) win_dkv_kernel(const __grid_constant__ Maps maps, const WinArgs a, const WinSinks sinks, int64_t key_tiles,
                                                               uint64_t limit, int withhold)
 {
     using G = Geo<D>;
@@ -473,26 +459,12 @@ __global__ void __launch_bounds__(kThreads, 1) win_dkv_kernel(const __grid_const
     extern __shared__ uint8_t win_bwd_smem[];
     uint8_t *const sm = win_bwd_smem + (-smem_u32(win_bwd_smem) & 1023u);  // (an offset: a cast would lose that it is shared memory)
     const int hk = blockIdx.y, per = a.H / a.HK;
-    // a tile of keys, or a run of queries against a tile of sinks
-    const bool run = blockIdx.x >= key_tiles;
-    const int64_t item = run ? blockIdx.x - key_tiles : blockIdx.x;
-    const Tile tl = run ? tile_of(a.cu_q, a.N, a.Tq, kSinkRun, item / sinks.tiles) : tile_of(a.cu_k, a.N, a.Tk, kTile, item);
-    const SeqRange sq = seq_range(a.cu_q, tl.n, a.Tq), sk = seq_range(a.cu_k, tl.n, a.Tk);
-    const int st = run ? (int)(item % sinks.tiles) : tl.index;
-    const int j0 = st * kTile, cols = min(kTile, sk.len - j0), off = sk.len - sq.len;
-    if (cols <= 0) return;
-    int begin = max(0, j0 - off), end = window_end(a, j0, cols, off, sq.len);
-    const bool dealt = !run && st < sinks.tiles;  // its fp32 part is joined with the runs'
-    if (run) {
-        begin = max(max(begin, end), tl.index * kSinkRun);
-        end = (int)min((int64_t)sq.len, (int64_t)(tl.index + 1) * kSinkRun);
-        if (begin >= end) return;
-    } else if (!dealt && j0 < a.sinks) {
-        end = sq.len;
-    }
+    const WinKeyTile kt(a, sinks, key_tiles, kTile, kSinkRun, blockIdx.x, hk);
+    if (kt.cols <= 0) return;
+    const SeqRange sq = kt.sq, sk = kt.sk;
+    const int n = kt.n, j0 = kt.j0, cols = kt.cols, off = kt.off, begin = kt.begin, end = kt.end;
+    float *const part = kt.part;
     const int tiles = begin < end ? (end - begin + kTile - 1) / kTile : 0, nt = tiles * per;
-    float *const part = run ? sinks.run + (((item / sinks.tiles) * a.HK + hk) * sinks.tiles + st) * 2 * kTile * D
-                      : dealt ? sinks.own + (((int64_t)tl.n * a.HK + hk) * sinks.tiles + st) * 2 * kTile * D : nullptr;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint64_t *bar = (uint64_t *)(sm + G::kBars);
@@ -614,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1) win_dkv_kernel(const __grid_const
         auto stat = [&](int t) {
             const int i = query0(t) + kCols * x + (r & (kCols - 1));
             if (i >= end) return r < kCols ? INFINITY : 0.f;  // weights of zero
-            const int64_t at = lse_at(a, tl.n, sq.bos, head(t)) + i;
+            const int64_t at = lse_at(a, n, sq.bos, head(t)) + i;
             if (r >= kCols) return a.delta[at];
             const float l = a.lse[at] * kLog2e;
             return l == -INFINITY ? INFINITY : l;
@@ -736,38 +708,15 @@ __global__ void __launch_bounds__(kThreads, 1) win_dkv_kernel(const __grid_const
 
 // dK and dV of the tiles of sinks: their own part and the runs', in order
 template <int D>
-__global__ void __launch_bounds__(256) win_sinks_kernel(const WinArgs a, const Sinks s)
+__global__ void __launch_bounds__(256) win_sinks_kernel(const WinArgs a, const WinSinks s)
 {
     const int which = blockIdx.z, st = blockIdx.y % s.tiles, hk = blockIdx.y / s.tiles;
-    const int n = blockIdx.x / (kTile * D / 1024), e = (blockIdx.x % (kTile * D / 1024)) * 1024 + threadIdx.x * 4;
-    const SeqRange sq = seq_range(a.cu_q, n, a.Tq), sk = seq_range(a.cu_k, n, a.Tk);
-    const int j0 = st * kTile, cols = min(kTile, sk.len - j0), r = e / D;
-    if (r >= cols) return;
-    const int off = sk.len - sq.len;
-    const int from = max(max(0, j0 - off), window_end(a, j0, cols, off, sq.len));  // the first query of a run
-    const int64_t slot0 = a.cu_q ? clamp64(a.cu_q[n], 0, a.Tq) / kSinkRun + n : (int64_t)n * ((a.Tq + kSinkRun - 1) / kSinkRun);
-    float4 x = *(const float4 *)(s.own + ((((int64_t)n * a.HK + hk) * s.tiles + st) * 2 + which) * kTile * D + e);
-    for (int i = from / kSinkRun; from < sq.len && i * kSinkRun < sq.len; ++i) {
-        const float4 y = *(const float4 *)(s.run + ((((slot0 + i) * a.HK + hk) * s.tiles + st) * 2 + which) * kTile * D + e);
-        x.x += y.x;
-        x.y += y.y;
-        x.z += y.z;
-        x.w += y.w;
-    }
-    __nv_bfloat16 *dst = (__nv_bfloat16 *)(which ? a.dv : a.dk) + ((sk.bos + j0 + r) * a.HK + hk) * D + e % D;
+    const int n = blockIdx.x / (kTile * D / 1024), e = (blockIdx.x % (kTile * D / 1024)) * 1024 + threadIdx.x * 4, r = st * kTile + e / D;
+    const SeqRange sk = seq_range(a.cu_k, n, a.Tk);
+    if (r >= sk.len) return;
+    const float4 x = win_sinks_sum<float4>(a, s, kTile, kSinkRun, n, hk, st, (int64_t)which * kTile * D + e);
+    __nv_bfloat16 *dst = (__nv_bfloat16 *)(which ? a.dv : a.dk) + ((sk.bos + r) * a.HK + hk) * D + e % D;
     *(uint2 *)dst = make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
-}
-
-Sinks plan_sinks(const WinArgs &a, int D, size_t *bytes)
-{
-    Sinks s{};
-    const int tiles = (a.sinks + kTile - 1) / kTile;
-    *bytes = 0;
-    if (a.window >= a.Tk || tiles > kMostSinkTiles || tiles == 0) return s;
-    s.tiles = tiles;
-    s.slots = mix_slots(a.cu_q != nullptr, a.N, a.Tq, kSinkRun);
-    *bytes = ((size_t)a.N + s.slots) * a.HK * tiles * 2 * kTile * D * sizeof(float);
-    return s;
 }
 
 template <int D>
@@ -789,9 +738,7 @@ cudaError_t launch(const WinArgs &a, int64_t tq, int64_t tk, float *delta, void 
         done_on_device(seen);
     }
     size_t bytes;
-    Sinks s = plan_sinks(a, D, &bytes);
-    s.own = (float *)ws;
-    s.run = s.own + (int64_t)a.N * a.HK * s.tiles * 2 * kTile * D;
+    const WinSinks s = win_sinks_plan(a, kTile, kSinkRun, kMostSinkTiles, ws, &bytes);
     const int64_t qt = mix_slots(a.cu_q != nullptr, a.N, a.Tq, kTile), kt = mix_slots(a.cu_k != nullptr, a.N, a.Tk, kTile);
     const int64_t ctas = kt + s.slots * s.tiles;
     if (qt * a.H > INT32_MAX || ctas > INT32_MAX || (int64_t)a.N * kTile * D / 1024 > INT32_MAX) return cudaErrorInvalidConfiguration;
@@ -814,7 +761,7 @@ bool win_bwd_tc_ok(const WinArgs &a, int64_t tq, int64_t tk)
 size_t win_bwd_tc_bytes(const WinArgs &a)
 {
     size_t bytes;
-    plan_sinks(a, a.D, &bytes);
+    win_sinks_plan(a, kTile, kSinkRun, kMostSinkTiles, nullptr, &bytes);
     return bytes;
 }
 

@@ -12,6 +12,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr float kNegInf = -INFINITY;
+constexpr int kSinkRun = 256, kMostSinks = 512;  // queries of a run, and sinks up to which they are dealt out (WinSinks)
 
 // TILE rows of D columns as fp32, zeros behind `rows` and D, at a stride of DP + 4
 template <typename T, int TILE, int DP>
@@ -243,22 +244,20 @@ __global__ void __launch_bounds__(kThreads) win_dq_kernel(const WinArgs a)
 }
 
 template <typename T, int TILE, int DP>
-__global__ void __launch_bounds__(kThreads) win_dkv_kernel(const WinArgs a)
+__global__ void __launch_bounds__(kThreads) win_dkv_kernel(const WinArgs a, const WinSinks sinks, int64_t key_tiles)
 {
     constexpr int RT = TILE / 16, ROW = TILE * (DP + 4);
     extern __shared__ float4 win_smem[];
     float *K = (float *)win_smem, *V = K + ROW, *Q = V + ROW, *G = Q + ROW, *P = G + ROW, *Z = P + TILE * (TILE + 4);
-    const Tile tl = tile_of(a.cu_k, a.N, a.Tk, TILE, blockIdx.x);
-    const SeqRange sq = seq_range(a.cu_q, tl.n, a.Tq), sk = seq_range(a.cu_k, tl.n, a.Tk);
-    const int j0 = tl.index * TILE, cols = min(TILE, sk.len - j0), hk = blockIdx.y, G_ = a.H / a.HK;
-    if (cols <= 0) return;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, off = sk.len - sq.len;
+    const int hk = blockIdx.y, G_ = a.H / a.HK;
+    const WinKeyTile kt(a, sinks, key_tiles, TILE, kSinkRun, blockIdx.x, hk);
+    if (kt.cols <= 0) return;
+    const SeqRange sq = kt.sq, sk = kt.sk;
+    const int n = kt.n, j0 = kt.j0, cols = kt.cols, off = kt.off, begin = kt.begin, end = kt.end;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     load_tile<T, TILE, DP>(K, (const T *)a.k + (sk.bos + j0) * a.ldk + (int64_t)hk * a.D, a.ldk, cols, a.D);
     load_tile<T, TILE, DP>(V, (const T *)a.v + (sk.bos + j0) * a.ldv + (int64_t)hk * a.D, a.ldv, cols, a.D);
     float dk[RT][DP / 16] = {}, dv[RT][DP / 16] = {};
-    // queries from the first that reaches key j0 to the last that sees any key of the tile
-    const int begin = max(0, j0 - off);
-    const int end = j0 < a.sinks ? sq.len : (int)min((int64_t)sq.len, (int64_t)j0 + cols - 1 + a.window - off);
     for (int g = 0; g < G_; ++g) {
         const int h = hk * G_ + g;
         for (int i0 = begin; i0 < end; i0 += TILE) {
@@ -273,7 +272,7 @@ __global__ void __launch_bounds__(kThreads) win_dkv_kernel(const WinArgs a)
 #pragma unroll
             for (int j = 0; j < RT; ++j) {
                 const int i = tx + 16 * j;
-                const int64_t at = lse_at(a, tl.n, sq.bos, h) + i0 + i;
+                const int64_t at = lse_at(a, n, sq.bos, h) + i0 + i;
                 const float lse = i < rows ? a.lse[at] * kLog2e : 0.f, delta = i < rows ? a.delta[at] : 0.f;
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
@@ -289,45 +288,101 @@ __global__ void __launch_bounds__(kThreads) win_dkv_kernel(const WinArgs a)
             mul_tile<RT, TILE, DP>(dk, Z, Q);
         }
     }
+    if (kt.part) {
+        store_tile<float, RT, DP>(kt.part, a.D, dk, cols, a.D);
+        store_tile<float, RT, DP>(kt.part + TILE * a.D, a.D, dv, cols, a.D);
+        return;
+    }
     store_tile<T, RT, DP>((T *)a.dk + ((sk.bos + j0) * a.HK + hk) * a.D, (int64_t)a.HK * a.D, dk, cols, a.D);
     store_tile<T, RT, DP>((T *)a.dv + ((sk.bos + j0) * a.HK + hk) * a.D, (int64_t)a.HK * a.D, dv, cols, a.D);
 }
 
-enum Which { kFwd, kDq, kDkv };
-
-template <typename T, int TILE, int DP>
-cudaError_t launch_tiles(const WinArgs &a, Which what, cudaStream_t st)
+// dK and dV of the tiles of sinks: their own part and the runs', in order
+template <typename T, int TILE>
+__global__ void __launch_bounds__(kThreads) win_sinks_kernel(const WinArgs a, const WinSinks s, int64_t count)
 {
-    auto kern = what == kFwd ? win_fwd_kernel<T, TILE, DP> : what == kDq ? win_dq_kernel<T, TILE, DP> : win_dkv_kernel<T, TILE, DP>;
-    const size_t row = TILE * (DP + 4) * 4, p = TILE * (TILE + 4) * 4;
-    const size_t smem = what == kFwd ? 2 * row + p : what == kDq ? 4 * row + p : 4 * row + 2 * p;
-    static std::atomic<uint64_t> seen[3];
-    if (first_on_device(seen[what])) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-        done_on_device(seen[what]);
-    }
-    const int64_t tiles = what == kDkv ? mix_slots(a.cu_k, a.N, a.Tk, TILE) : mix_slots(a.cu_q, a.N, a.Tq, TILE);
+    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (i >= count) return;
+    const int size = 2 * TILE * a.D, at = (int)(i % size), which = at / (TILE * a.D), e = at % (TILE * a.D), r0 = e / a.D;
+    const int64_t tile = i / size;
+    const int st = (int)(tile % s.tiles), hk = (int)(tile / s.tiles % a.HK), n = (int)(tile / s.tiles / a.HK), r = st * TILE + r0;
+    const SeqRange sk = seq_range(a.cu_k, n, a.Tk);
+    if (r >= sk.len) return;
+    ((T *)(which ? a.dv : a.dk))[((sk.bos + r) * a.HK + hk) * a.D + e % a.D] = from_f<T>(win_sinks_sum<float>(a, s, TILE, kSinkRun, n, hk, st, at));
+}
+
+template <typename K>
+cudaError_t prepare(K kern, size_t smem, std::atomic<uint64_t> &seen)
+{
+    if (!first_on_device(seen)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess) done_on_device(seen);
+    return e;
+}
+// the forward or dQ: a CTA to a tile of queries of a head
+template <typename T, int TILE, int DP>
+cudaError_t launch_rows(const WinArgs &a, bool dq, cudaStream_t st)
+{
+    auto kern = dq ? win_dq_kernel<T, TILE, DP> : win_fwd_kernel<T, TILE, DP>;
+    const size_t smem = (dq ? 4 : 2) * TILE * (DP + 4) * 4 + TILE * (TILE + 4) * 4;
+    static std::atomic<uint64_t> seen[2];
+    const cudaError_t e = prepare(kern, smem, seen[dq]);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = mix_slots(a.cu_q != nullptr, a.N, a.Tq, TILE);
     if (tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
     if (tiles == 0) return cudaSuccess;
-    kern<<<dim3((unsigned)tiles, what == kDkv ? a.HK : a.H), kThreads, smem, st>>>(a);
+    kern<<<dim3((unsigned)tiles, a.H), kThreads, smem, st>>>(a);
     return cudaGetLastError();
 }
-template <typename T>
-cudaError_t launch_typed(const WinArgs &a, Which what, cudaStream_t st)
+template <typename T, int TILE, int DP>
+cudaError_t launch_keys(const WinArgs &a, void *ws, cudaStream_t st)
 {
-    return a.D <= 64 ? launch_tiles<T, 64, 64>(a, what, st) : a.D <= 128 ? launch_tiles<T, 64, 128>(a, what, st) : launch_tiles<T, 32, 256>(a, what, st);
+    auto kern = win_dkv_kernel<T, TILE, DP>;
+    const size_t smem = 4 * TILE * (DP + 4) * 4 + 2 * TILE * (TILE + 4) * 4;
+    static std::atomic<uint64_t> seen;
+    const cudaError_t e = prepare(kern, smem, seen);
+    if (e != cudaSuccess) return e;
+    size_t bytes;
+    const WinSinks s = win_sinks_plan(a, TILE, kSinkRun, kMostSinks / TILE, ws, &bytes);
+    const int64_t tiles = mix_slots(a.cu_k != nullptr, a.N, a.Tk, TILE), ctas = tiles + s.slots * s.tiles;
+    const int64_t count = (int64_t)a.N * a.HK * s.tiles * 2 * TILE * a.D, blocks = (count + kThreads - 1) / kThreads;
+    if (ctas > INT32_MAX || blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+    if (tiles == 0) return cudaSuccess;
+    kern<<<dim3((unsigned)ctas, a.HK), kThreads, smem, st>>>(a, s, tiles);
+    if (s.tiles > 0) win_sinks_kernel<T, TILE><<<(unsigned)blocks, kThreads, 0, st>>>(a, s, count);
+    return cudaGetLastError();
 }
-cudaError_t launch_any(const WinArgs &a, gdn_dtype dt, Which what, cudaStream_t st)
+int tile_of_size(int D) { return D <= 128 ? 64 : 32; }
+template <typename T>
+cudaError_t launch_rows_of(const WinArgs &a, bool dq, cudaStream_t st)
 {
-    return dt == GDN_F32 ? launch_typed<float>(a, what, st) : launch_typed<__nv_bfloat16>(a, what, st);
+    return a.D <= 64 ? launch_rows<T, 64, 64>(a, dq, st) : a.D <= 128 ? launch_rows<T, 64, 128>(a, dq, st) : launch_rows<T, 32, 256>(a, dq, st);
+}
+template <typename T>
+cudaError_t launch_keys_of(const WinArgs &a, void *ws, cudaStream_t st)
+{
+    return a.D <= 64 ? launch_keys<T, 64, 64>(a, ws, st) : a.D <= 128 ? launch_keys<T, 64, 128>(a, ws, st) : launch_keys<T, 32, 256>(a, ws, st);
+}
+cudaError_t launch_any(const WinArgs &a, gdn_dtype dt, bool dq, cudaStream_t st)
+{
+    return dt == GDN_F32 ? launch_rows_of<float>(a, dq, st) : launch_rows_of<__nv_bfloat16>(a, dq, st);
 }
 
 }  // namespace
 
-cudaError_t launch_win_simt(const WinArgs &a, gdn_dtype dt, cudaStream_t st) { return launch_any(a, dt, kFwd, st); }
-cudaError_t launch_win_dq_simt(const WinArgs &a, gdn_dtype dt, cudaStream_t st) { return launch_any(a, dt, kDq, st); }
-cudaError_t launch_win_dkv_simt(const WinArgs &a, gdn_dtype dt, cudaStream_t st) { return launch_any(a, dt, kDkv, st); }
+cudaError_t launch_win_simt(const WinArgs &a, gdn_dtype dt, cudaStream_t st) { return launch_any(a, dt, false, st); }
+cudaError_t launch_win_dq_simt(const WinArgs &a, gdn_dtype dt, cudaStream_t st) { return launch_any(a, dt, true, st); }
+cudaError_t launch_win_dkv_simt(const WinArgs &a, gdn_dtype dt, void *ws, cudaStream_t st)
+{
+    return dt == GDN_F32 ? launch_keys_of<float>(a, ws, st) : launch_keys_of<__nv_bfloat16>(a, ws, st);
+}
+size_t win_dkv_simt_bytes(const WinArgs &a)
+{
+    size_t bytes;
+    const int tile = tile_of_size(a.D);
+    win_sinks_plan(a, tile, kSinkRun, kMostSinks / tile, nullptr, &bytes);
+    return bytes;
+}
 
 cudaError_t launch_win_delta(const void *dout, int64_t ld, const void *o, const WinArgs &a, gdn_dtype dt, float *delta, cudaStream_t st)
 {
