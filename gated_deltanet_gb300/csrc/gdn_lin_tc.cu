@@ -586,6 +586,18 @@ bool heads_map(CUtensorMap *m, const void *base, int D, int heads, int64_t token
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool strided_map(CUtensorMap *m, const void *base, int D, int heads, int T, int batch, int64_t head, int64_t tok, int64_t seq, int box_rows)
+{
+    const auto enc = encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)T, (cuuint64_t)batch};
+    auto bytes = [&](int64_t stride, int64_t size) { return (cuuint64_t)(size > 1 ? stride : D) * 2; };  // (of one there is no next)
+    const cuuint64_t strides[3] = {bytes(head, heads), bytes(tok, T), bytes(seq, batch)};
+    const cuuint32_t box[4] = {64, 1, (cuuint32_t)box_rows, 1}, es[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 LinPlan lin_tc_plan(const LinArgs &a, int D)
 {
     // A split walks its chunks twice (the second time with outputs), so it pays only where (sequence, head) pairs leave SMs idle: the

@@ -84,6 +84,8 @@ cudaError_t launch_lin_tc(const LinArgs &a, void *ws, int64_t tokens, cudaStream
 gdn_status read_lin_status(cudaStream_t st);
 // a TMA map over bf16 [tokens][heads][D], `ld` elements from a token to the next: boxes of 64 elements x 1 head x box_rows tokens
 bool heads_map(CUtensorMap *m, const void *base, int D, int heads, int64_t tokens, int64_t ld, int box_rows);
+// the same over [batch][T][heads][D] by strides (multiples of 8 elements): boxes of a sequence's tokens, zeros behind its end
+bool strided_map(CUtensorMap *m, const void *base, int D, int heads, int T, int batch, int64_t head, int64_t tok, int64_t seq, int box_rows);
 // dq and dk of heads that r value heads share: out[t][h][d] = sum over i of part[t][h r + i][d], in order (`part`: dq's, then dk's)
 cudaError_t launch_lin_heads(const float *part, const LinArgs &a, int64_t tokens, int H, int r, int D, void *dq, void *dk, gdn_dtype dt, cudaStream_t st);
 
@@ -126,6 +128,7 @@ struct WinArgs {
     float scale;
     void *o;                    // [tokens][H][D]
     float *lse;                 // [B][H][Tq] (packed: [H][Tq]), nullable
+    int64_t o_seq, o_tok, o_head;  // o's strides in elements (gradients: as the caller has it)
     // gradients
     const void *dout;
     int64_t ld_dout;
@@ -215,7 +218,7 @@ bool win_bwd_tc_ok(const WinArgs &a, int64_t tq, int64_t tk);
 size_t win_bwd_tc_bytes(const WinArgs &a);  // of workspace, beside delta (which the call fills)
 cudaError_t launch_win_bwd_tc(const WinArgs &a, int64_t tq, int64_t tk, float *delta, void *ws, cudaStream_t st);
 gdn_status read_win_bwd_status(cudaStream_t st);
-cudaError_t launch_win_delta(const void *dout, int64_t ld_dout, const void *o, const WinArgs &a, gdn_dtype dt, float *delta, cudaStream_t st);
+cudaError_t launch_win_delta(const WinArgs &a, gdn_dtype dt, float *delta, cudaStream_t st);
 cudaError_t launch_win_dq_simt(const WinArgs &a, gdn_dtype dt, cudaStream_t st);
 size_t win_dkv_simt_bytes(const WinArgs &a);  // of workspace, beside delta
 cudaError_t launch_win_dkv_simt(const WinArgs &a, gdn_dtype dt, void *ws, cudaStream_t st);

@@ -130,8 +130,11 @@ gdn_status check_win(const gdn_window_attn_args *a, bool backward)
     if (tk > 0 && (!a->dk || !a->dv)) return GDN_ERR_INVALID;
     if (tq > 1 && a->ld_dout < wq) return GDN_ERR_INVALID;
     if (!on(a->dout, e) || !on(a->dq, e) || !on(a->dk, e) || !on(a->dv, e)) return GDN_ERR_INVALID;
+    if (a->o_seq < 0 || a->o_tok < 0 || a->o_head < 0) return GDN_ERR_INVALID;
+    const bool strided = a->o_seq || a->o_tok || a->o_head;
+    const Span kept = strided ? Span(a->o, tq > 0, (a->B - 1) * a->o_seq + (a->Tq - 1) * a->o_tok + (a->H - 1) * a->o_head + a->D, 1, e) : o;
     const Span out[] = {Span(a->dq, tq, wq, wq, e), Span(a->dk, tk, wk, wk, e), Span(a->dv, tk, wk, wk, e)};
-    const Span in[] = {q, k, v, cq, ck, o, lse, Span(a->dout, tq, wq, a->ld_dout, e)};
+    const Span in[] = {q, k, v, cq, ck, kept, lse, Span(a->dout, tq, wq, a->ld_dout, e)};
     return apart(out, in) ? GDN_OK : GDN_ERR_INVALID;
 }
 WinArgs win_args(const gdn_window_attn_args *a)
@@ -147,6 +150,10 @@ WinArgs win_args(const gdn_window_attn_args *a)
     w.scale = a->scale;
     w.o = a->o;
     w.lse = a->lse;
+    const bool strided = a->o_seq || a->o_tok || a->o_head;
+    w.o_head = strided ? a->o_head : a->D;
+    w.o_tok = strided ? a->o_tok : (int64_t)a->H * a->D;
+    w.o_seq = strided ? a->o_seq : a->Tq * ((int64_t)a->H * a->D);
     w.dout = a->dout; w.ld_dout = a->ld_dout;
     w.dq = a->dq; w.dk = a->dk; w.dv = a->dv;
     return w;
@@ -275,7 +282,7 @@ gdn_status gdn_window_attn_bwd(const gdn_window_attn_args *a, void *ws, size_t w
     const int64_t tq = (int64_t)a->B * a->Tq, tk = (int64_t)a->B * a->Tk;
     if (win_bwd_on_tc(a)) return of(launch_win_bwd_tc(w, tq, tk, delta, base + win_delta_bytes(a), stream));
     cudaError_t e = cudaSuccess;
-    if (tq > 0) e = launch_win_delta(a->dout, a->ld_dout, a->o, w, a->dtype, delta, stream);
+    if (tq > 0) e = launch_win_delta(w, a->dtype, delta, stream);
     if (e == cudaSuccess && tq > 0) e = launch_win_dq_simt(w, a->dtype, stream);
     if (e == cudaSuccess && tk > 0) e = launch_win_dkv_simt(w, a->dtype, base + win_delta_bytes(a), stream);
     return of(e);

@@ -116,6 +116,7 @@ struct Queries {
     int t0, rows, h, p0;   // first token, rows (0: no more tiles), head, position of the first row
     int k0, klen, hk;      // the sequence's first key and length, key head
     int lo, hi, first, nfirst, nt;
+    int b, tb;             // batch and its token, as O is asked for
     __device__ __forceinline__ void set(const WinArgs &a, unsigned item)
     {
         h = (int)(item % (unsigned)a.H);
@@ -125,6 +126,8 @@ struct Queries {
         const int i0 = tl.index * kTile;
         at = lse_at(a, tl.n, sq.bos, h) + i0;
         t0 = (int)(sq.bos + i0);
+        b = a.cu_q ? 0 : tl.n;
+        tb = t0 - b * a.Tq;
         rows = max(min(kTile, sq.len - i0), 0);
         p0 = i0 + sk.len - sq.len;
         k0 = (int)sk.bos;
@@ -217,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1) win_dq_kernel(const __grid_consta
                     mbar_arrive_expect_tx(landing, G::kUnit);
 #pragma unroll
                     for (int b = 0; b < G::kBoxes; ++b) {
-                        if (u < 0) tma_load_3d(sm + unit(i) + b * kBox, &maps.o, b * 64, it.h, it.t0, landing);
+                        if (u < 0) tma_load_4d(sm + unit(i) + b * kBox, &maps.o, b * 64, it.h, it.tb, it.b, landing);
                         else tma_load_3d(sm + unit(i) + b * kBox, u & 1 ? &maps.v : &maps.k, b * 64, it.hk, it.k0 + it.key0(t), landing);
                     }
                 }
@@ -725,7 +728,7 @@ cudaError_t launch(const WinArgs &a, int64_t tq, int64_t tk, float *delta, void 
     Maps maps;
     if (!heads_map(&maps.q, a.q, D, a.H, tq, a.ldq, kTile) || !heads_map(&maps.k, a.k, D, a.HK, tk, a.ldk, kTile) ||
         !heads_map(&maps.v, a.v, D, a.HK, tk, a.ldv, kTile) || !heads_map(&maps.dout, a.dout, D, a.H, tq, a.ld_dout, kTile) ||
-        !heads_map(&maps.o, a.o, D, a.H, tq, (int64_t)a.H * D, kTile) || !heads_map(&maps.dq, a.dq, D, a.H, tq, (int64_t)a.H * D, kTile) ||
+        !strided_map(&maps.o, a.o, D, a.H, a.Tq, a.cu_q ? 1 : a.N, a.o_head, a.o_tok, a.o_seq, kTile) || !heads_map(&maps.dq, a.dq, D, a.H, tq, (int64_t)a.H * D, kTile) ||
         !heads_map(&maps.dk, a.dk, D, a.HK, tk, (int64_t)a.HK * D, kTile) ||
         !heads_map(&maps.dv, a.dv, D, a.HK, tk, (int64_t)a.HK * D, kTile))
         return cudaErrorInvalidValue;
@@ -754,6 +757,9 @@ cudaError_t launch(const WinArgs &a, int64_t tq, int64_t tk, float *delta, void 
 
 bool win_bwd_tc_ok(const WinArgs &a, int64_t tq, int64_t tk)
 {
+    const int64_t strides[] = {a.H > 1 ? a.o_head : 8, a.Tq > 1 ? a.o_tok : 8, !a.cu_q && a.N > 1 ? a.o_seq : 8};
+    for (int64_t s : strides)
+        if (s < 8 || s % 8 || s >= (int64_t)1 << 38) return false;
     return win_tc_ok(a, tq, tk) && tma_ok(a.dout, a.ld_dout, tq, 2) && !(((uintptr_t)a.dq | (uintptr_t)a.dk | (uintptr_t)a.dv) & 15) &&
            a.HK * kMostSinkTiles <= 65535;
 }

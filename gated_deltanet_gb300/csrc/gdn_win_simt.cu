@@ -181,19 +181,19 @@ __global__ void __launch_bounds__(kThreads) win_fwd_kernel(const WinArgs a)
 
 // delta = sum over the head of dO o, one warp per (token, head)
 template <typename T>
-__global__ void __launch_bounds__(kThreads) win_delta_kernel(const T *dout, int64_t ld, const T *o, const WinArgs a, float *delta, int64_t rows)
+__global__ void __launch_bounds__(kThreads) win_delta_kernel(const WinArgs a, float *delta, int64_t rows)
 {
     const int64_t w = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
     if (w >= rows) return;
     const int lane = threadIdx.x & 31, h = (int)(w % a.H);
     const int64_t t = w / a.H;
-    const T *x = dout + t * ld + (int64_t)h * a.D, *y = o + w * a.D;
+    const int64_t n = a.cu_q ? 0 : t / a.Tq, i = t - n * a.Tq;
+    const T *x = (const T *)a.dout + t * a.ld_dout + (int64_t)h * a.D, *y = (const T *)a.o + n * a.o_seq + i * a.o_tok + h * a.o_head;
     float s = 0.f;
     for (int d = lane; d < a.D; d += 32) s = fmaf(to_f<T>(x[d]), to_f<T>(y[d]), s);
 #pragma unroll
     for (int k = 16; k; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-    const int64_t n = a.cu_q ? 0 : t / a.Tq;
-    if (lane == 0) delta[lse_at(a, (int)n, a.cu_q ? t : 0, h) + (a.cu_q ? 0 : t - n * a.Tq)] = s;
+    if (lane == 0) delta[lse_at(a, (int)n, 0, h) + i] = s;
 }
 
 template <typename T, int TILE, int DP>
@@ -384,12 +384,12 @@ size_t win_dkv_simt_bytes(const WinArgs &a)
     return bytes;
 }
 
-cudaError_t launch_win_delta(const void *dout, int64_t ld, const void *o, const WinArgs &a, gdn_dtype dt, float *delta, cudaStream_t st)
+cudaError_t launch_win_delta(const WinArgs &a, gdn_dtype dt, float *delta, cudaStream_t st)
 {
     const int64_t rows = (a.cu_q ? (int64_t)a.Tq : (int64_t)a.N * a.Tq) * a.H, blocks = (rows * 32 + kThreads - 1) / kThreads;
     if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-    if (dt == GDN_F32) win_delta_kernel<float><<<(unsigned)blocks, kThreads, 0, st>>>((const float *)dout, ld, (const float *)o, a, delta, rows);
-    else win_delta_kernel<__nv_bfloat16><<<(unsigned)blocks, kThreads, 0, st>>>((const __nv_bfloat16 *)dout, ld, (const __nv_bfloat16 *)o, a, delta, rows);
+    if (dt == GDN_F32) win_delta_kernel<float><<<(unsigned)blocks, kThreads, 0, st>>>(a, delta, rows);
+    else win_delta_kernel<__nv_bfloat16><<<(unsigned)blocks, kThreads, 0, st>>>(a, delta, rows);
     return cudaGetLastError();
 }
 

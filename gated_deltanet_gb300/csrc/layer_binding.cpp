@@ -693,10 +693,14 @@ PyObject *window_attn_bwd(PyObject *const *p)
     const int64_t stats[] = {q.size(0), q.size(2), q.size(1)};
     same_shape("lse", lse, stats);
     const Tokens d = tokens(dout);
-    const Tensor oc = o.contiguous(), lc = lse.contiguous();
+    // o as it lies where the copies can ask for it so, each head's elements together and 16 bytes apart
+    bool there = o.size(3) == 1 || o.stride(3) == 1;
+    for (int i = 0; i < 3; ++i) there = there && (o.size(i) <= 1 || (o.stride(i) > 0 && o.stride(i) * o.element_size() % 16 == 0));
+    const Tensor oc = there ? o : o.contiguous(), lc = lse.contiguous();
     w.a.dout = d.ptr();
     w.a.ld_dout = d.ld;
     w.a.o = oc.data_ptr();
+    w.a.o_seq = oc.stride(0); w.a.o_tok = oc.stride(1); w.a.o_head = oc.stride(2);
     w.a.lse = lc.data_ptr<float>();
     const Tensor dq = fresh(q.sizes(), q.scalar_type(), q), dk = fresh(k.sizes(), q.scalar_type(), q), dv = fresh(v.sizes(), q.scalar_type(), q);
     w.a.dq = dq.data_ptr(); w.a.dk = dk.data_ptr(); w.a.dv = dv.data_ptr();

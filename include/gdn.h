@@ -609,11 +609,13 @@ typedef struct {
     const void *q, *k, *v;    /* [B][Tq][H][D], [B][Tk][HK][D] twice                     */
     int64_t ldq, ldk, ldv;
     const int64_t *cu_seqlens_q, *cu_seqlens_k; /* [N + 1] both, or none                 */
-    void *o;                  /* [B][Tq][H][D] (backward: an input, contiguous)          */
+    void *o;                  /* [B][Tq][H][D] (backward: an input)                      */
     float *lse;               /* [B][H][Tq], nullable (backward: an input)               */
     const void *dout;         /* backward: [B][Tq][H][D]                                 */
     int64_t ld_dout;
     void *dq, *dk, *dv;       /* backward: as q, k, v, contiguous                        */
+    int64_t o_seq, o_tok, o_head; /* backward: o's strides in elements (consecutive in a
+                                 head), as [B][H][Tq][D] has them; all zero: contiguous  */
 } gdn_window_attn_args;
 
 /*

@@ -538,6 +538,27 @@ def test_offsets_past_32_bits(gdn):
     ref.check(got, eo, bo, "o")
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_window_bwd_o_by_strides(gdn, dtype):
+    """The forward's output as it lies: heads in front of tokens, a slice, elements apart, one value for all heads."""
+    for B, cu in ((2, None), (1, offsets([130, 0, 70]))):
+        q, k, v, w, sinks, _, _, g = window_inputs((B, 200, None, 4, 2, 64, 40, 3), dtype, 4)
+        do = randn(g, *q.shape, dtype=dtype)
+        o, lse = gdn.window_attention(q, k, v, w, sinks, cu_seqlens=cu, return_lse=True)
+        want = gdn.window_attention_bwd(do, q, k, v, o, lse, w, sinks, cu_seqlens=cu)
+        wide = torch.zeros(B, 200, 4, 72, device="cuda", dtype=dtype)
+        odd = torch.zeros(B, 200, 4, 65, device="cuda", dtype=dtype)
+        wide[..., :64], odd[..., 1:] = o, o
+        for p in (o.transpose(1, 2).contiguous().transpose(1, 2), o.permute(1, 0, 2, 3).contiguous().permute(1, 0, 2, 3), wide[..., :64], odd[..., 1:],
+                  o.transpose(2, 3).contiguous().transpose(2, 3)):
+            for a, b in zip(gdn.window_attention_bwd(do, q, k, v, p, lse, w, sinks, cu_seqlens=cu), want):
+                assert torch.equal(a, b)
+        one = o[:, :, :1].expand(-1, -1, 4, -1)
+        for a, b in zip(gdn.window_attention_bwd(do, q, k, v, one, lse, w, sinks, cu_seqlens=cu),
+                        gdn.window_attention_bwd(do, q, k, v, one.contiguous(), lse, w, sinks, cu_seqlens=cu)):
+            assert torch.equal(a, b)
+
+
 # ---------------------------------------------------------------- calls of the C entries, at once, and cut short
 def linear_call(lib, q, k, v, decay, do=None, stream=0):
     """(run, outputs): gdn_linear_attn, or its gradients, with the library's own workspace."""

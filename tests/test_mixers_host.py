@@ -21,7 +21,8 @@ class GdnLinearAttnArgs(ctypes.Structure):
 class GdnWindowAttnArgs(ctypes.Structure):
     _fields_ = [(n, INT) for n in ("B", "Tq", "Tk", "H", "HK", "D", "num_seqs", "dtype", "window", "sinks")] + [("scale", F)] + [
         (n, VP) for n in ("q", "k", "v")] + [(n, I64) for n in ("ldq", "ldk", "ldv")] + [
-        (n, VP) for n in ("cu_seqlens_q", "cu_seqlens_k", "o", "lse", "dout")] + [("ld_dout", I64)] + [(n, VP) for n in ("dq", "dk", "dv")]
+        (n, VP) for n in ("cu_seqlens_q", "cu_seqlens_k", "o", "lse", "dout")] + [("ld_dout", I64)] + [(n, VP) for n in ("dq", "dk", "dv")] + [
+        (n, I64) for n in ("o_seq", "o_tok", "o_head")]
 
 
 class GdnWindowDecodeArgs(ctypes.Structure):
@@ -108,7 +109,7 @@ def test_window_refuses(L, kw):
 
 
 @pytest.mark.parametrize("kw", WINDOW_BAD + [dict(lse=None), dict(dout=None), dict(dq=None), dict(dk=None), dict(dv=None), dict(ld_dout=255), dict(dq=at(5)), dict(dk=at(6)),
-                                             dict(dv=at(3)), dict(dq=at(4))])
+                                             dict(dv=at(3)), dict(dq=at(4)), dict(o_tok=-64), dict(o_seq=1 << 29, o_tok=64, o_head=512)])
 def test_window_bwd_refuses(L, kw):
     a = window_args(**kw)
     assert L.gdn_window_attn_bwd(ctypes.byref(a), None, 0, None) == INVALID
