@@ -352,16 +352,28 @@ cudaError_t launch_keys(const WinArgs &a, void *ws, cudaStream_t st)
     if (s.tiles > 0) win_sinks_kernel<T, TILE><<<(unsigned)blocks, kThreads, 0, st>>>(a, s, count);
     return cudaGetLastError();
 }
-int tile_of_size(int D) { return D <= 128 ? 64 : 32; }
+// Tiles of 64 (each key and query is read half as often), or of 32 where 64 would leave SMs without a tile, and for heads whose tiles of 64
+// do not fit.  fp32, window 100, gradients of 2048 tokens, 4 heads over 2 of 64 (128 tiles of queries, 64 of keys): 182 us with 64, 145 with
+// 32; 300 tokens of 2 heads of 40: 90 and 70; 2 x 2048 tokens, 4 heads of 64, window 256 (256 tiles): 258 and 272.
+int tile_for(int D, bool packed, int N, int T, int heads)
+{
+    return D > 128 || mix_slots(packed, N, T, 64) * heads < device_sm_count() ? 32 : 64;
+}
+int row_tile(const WinArgs &a) { return tile_for(a.D, a.cu_q != nullptr, a.N, a.Tq, a.H); }
+int key_tile(const WinArgs &a) { return tile_for(a.D, a.cu_k != nullptr, a.N, a.Tk, a.HK); }
 template <typename T>
 cudaError_t launch_rows_of(const WinArgs &a, bool dq, cudaStream_t st)
 {
-    return a.D <= 64 ? launch_rows<T, 64, 64>(a, dq, st) : a.D <= 128 ? launch_rows<T, 64, 128>(a, dq, st) : launch_rows<T, 32, 256>(a, dq, st);
+    if (a.D > 128) return launch_rows<T, 32, 256>(a, dq, st);
+    if (row_tile(a) == 32) return a.D <= 64 ? launch_rows<T, 32, 64>(a, dq, st) : launch_rows<T, 32, 128>(a, dq, st);
+    return a.D <= 64 ? launch_rows<T, 64, 64>(a, dq, st) : launch_rows<T, 64, 128>(a, dq, st);
 }
 template <typename T>
 cudaError_t launch_keys_of(const WinArgs &a, void *ws, cudaStream_t st)
 {
-    return a.D <= 64 ? launch_keys<T, 64, 64>(a, ws, st) : a.D <= 128 ? launch_keys<T, 64, 128>(a, ws, st) : launch_keys<T, 32, 256>(a, ws, st);
+    if (a.D > 128) return launch_keys<T, 32, 256>(a, ws, st);
+    if (key_tile(a) == 32) return a.D <= 64 ? launch_keys<T, 32, 64>(a, ws, st) : launch_keys<T, 32, 128>(a, ws, st);
+    return a.D <= 64 ? launch_keys<T, 64, 64>(a, ws, st) : launch_keys<T, 64, 128>(a, ws, st);
 }
 cudaError_t launch_any(const WinArgs &a, gdn_dtype dt, bool dq, cudaStream_t st)
 {
@@ -379,7 +391,7 @@ cudaError_t launch_win_dkv_simt(const WinArgs &a, gdn_dtype dt, void *ws, cudaSt
 size_t win_dkv_simt_bytes(const WinArgs &a)
 {
     size_t bytes;
-    const int tile = tile_of_size(a.D);
+    const int tile = key_tile(a);
     win_sinks_plan(a, tile, kSinkRun, kMostSinks / tile, nullptr, &bytes);
     return bytes;
 }
