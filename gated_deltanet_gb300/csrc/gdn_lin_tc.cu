@@ -50,25 +50,32 @@ struct Maps {
     CUtensorMap a[3], b[3], c[3];
 };
 
+constexpr float kAgain = 1.6f, kLaunches = 8.f;  // a split's walk in walks, its further launches in chunks (lin_tc_plan)
+constexpr size_t kChosenBytes = 256;
+inline bool several(const LinArgs &a) { return a.cu && a.N > 1; }
+
 struct Split {
     float *states;  // [passes][slots][HV][D][D]: what a segment adds to the state, then the state that enters it; null: one segment each
     int tokens;     // of a segment (a multiple of kC)
     int64_t slots;
+    const int *chosen;  // packed: a multiple of `tokens` that lin_choose_kernel took, and whether a sequence is longer; nullable
+    __device__ int segment() const { return chosen ? *chosen : tokens; }
+    __device__ bool none() const { return chosen && !chosen[1]; }  // no sequence is cut
 };
 
 // A CTA's part of a sequence, in the order of processing
 struct Part {
     SeqRange s;
     int chunks, m0, nm, seg;  // of the sequence; the first one's place, how many; which segment
-    __device__ Part(const LinArgs &a, const Split &sp, int64_t slot, int &n)
+    __device__ Part(const LinArgs &a, bool split, int tokens, int64_t slot, int &n)
     {
-        const Tile t = sp.states ? tile_of(a.cu, a.N, a.T, sp.tokens, slot) : Tile{(int)slot, 0};
+        const Tile t = split ? tile_of(a.cu, a.N, a.T, tokens, slot) : Tile{(int)slot, 0};
         n = t.n;
         s = seq_range(a.cu, n, a.T);
         seg = t.index;
         chunks = (s.len + kC - 1) / kC;
         // (packed sequences of at most a segment's length stay whole)
-        const int per = sp.states ? sp.tokens / kC : chunks;
+        const int per = split ? tokens / kC : chunks;
         m0 = (int)min((int64_t)seg * per, (int64_t)chunks);
         nm = min(per, chunks - m0);
     }
@@ -90,8 +97,9 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     const unsigned rest = blockIdx.x / (nct * args.passes);
     const int hv = (int)(rest % args.HV);
     const int64_t slot = rest / args.HV;
+    if (STATE && split.none()) return;
     int n;
-    const Part part(args, split, slot, n);
+    const Part part(args, split.states, split.segment(), slot, n);
     const bool rev = p.reverse;
     const bool last_seg = part.m0 + part.nm == part.chunks;
     const int nm = part.nm;
@@ -494,14 +502,15 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
 template <int D>
 __global__ void __launch_bounds__(256) lin_join_kernel(const LinArgs args, const Split split)
 {
+    if (split.none()) return;
     constexpr int kPieces = D * D / 1024;
     const LinPass &p = args.pass[blockIdx.y];
     const int pair = (int)(blockIdx.x / kPieces), at = (int)(blockIdx.x % kPieces) * 1024 + 4 * threadIdx.x;
     const int n = pair / args.HV, hv = pair - n * args.HV;
     const SeqRange s = seq_range(args.cu, n, args.T);
-    const int segs = (s.len + split.tokens - 1) / split.tokens;
+    const int tokens = split.segment(), segs = (s.len + tokens - 1) / tokens;
     if (segs <= 1) return;  // (whole)
-    const int64_t slot0 = args.cu ? clamp64(args.cu[n], 0, args.T) / split.tokens + n : (int64_t)n * ((args.T + split.tokens - 1) / split.tokens);
+    const int64_t slot0 = args.cu ? clamp64(args.cu[n], 0, args.T) / tokens + n : (int64_t)n * ((args.T + tokens - 1) / tokens);
     const float g = args.decay ? args.decay[hv] : 0.f;
     // tokens of a segment in the order of processing: against time the first has the sequence's odd end
     const int odd = (s.len + kC - 1) / kC * kC - s.len;
@@ -510,7 +519,7 @@ __global__ void __launch_bounds__(256) lin_join_kernel(const LinArgs args, const
     for (int e = 0; e < 4; ++e) x[e] = p.x0 ? p.x0[(int64_t)pair * D * D + (p.x_t ? ((at + e) % D) * D + at / D : at + e)] : 0.f;
     const int64_t step = (int64_t)args.HV * D * D;
     float *buf = split.states + (((int64_t)blockIdx.y * split.slots + slot0) * args.HV + hv) * D * D + at;
-    const Decayed first(g, split.tokens - (p.reverse ? odd + 1 : 0)), rest(g, split.tokens);
+    const Decayed first(g, tokens - (p.reverse ? odd + 1 : 0)), rest(g, tokens);
     for (int i = 0; i < segs; i += 8) {
         float4 add[8];
 #pragma unroll
@@ -523,6 +532,46 @@ __global__ void __launch_bounds__(256) lin_join_kernel(const LinArgs args, const
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[e] = (i + k == 0 ? first(x[e]) : rest(x[e])) + y[e];
             }
+    }
+}
+
+// The segment of a packed batch, from its lengths: a multiple of the plan's, or none.  A warp takes one: the longest piece, or the SMs' share of
+// all pieces and half a piece for the ragged end, in chunks, as in lin_tc_plan.  (In place of the
+// plan's own segment, which fits one sequence of all tokens: 30 random cuts of 32768 tokens, 8 heads of 128, 172 -> 121 us, gradients 424 -> 295;
+// one call more to wait for where little is to choose: two sequences of 8191 tokens 51 -> 57.)
+__device__ constexpr int kMultiples[16] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32, 40, 48, 0};
+__global__ void __launch_bounds__(512) lin_choose_kernel(const LinArgs args, int tokens, float share, int *chosen)
+{
+    __shared__ float time[16];
+    __shared__ int cuts[16];
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t per = kMultiples[w] ? (int64_t)kMultiples[w] * (tokens / kC) : INT32_MAX;
+    float work = 0.f;
+    int longest = 0;
+    bool twice = false;
+    for (int n = lane; n < args.N; n += 32) {
+        const int chunks = (seq_range(args.cu, n, args.T).len + kC - 1) / kC;
+        if (chunks == 0) continue;
+        const bool cut = chunks > per;
+        work += cut ? kAgain * (float)(chunks + 2 * ((chunks + per - 1) / per)) : (float)(chunks + 2);
+        longest = max(longest, (int)min((int64_t)chunks, per));
+        twice |= cut;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        work += __shfl_xor_sync(0xffffffffu, work, o);
+        longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+    }
+    twice = __any_sync(0xffffffffu, twice);
+    if (lane == 0) cuts[w] = twice, time[w] = fmaxf((twice ? kAgain : 1.f) * (float)(longest + 2), work * share + 0.5f * (float)longest) + (twice ? kLaunches : 0.f);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        int best = 15;  // (none, where another is not faster)
+        for (int i = 0; i < 15; ++i)
+            if (time[i] < time[best]) best = i;
+        const int64_t seg = kMultiples[best] ? (int64_t)kMultiples[best] * tokens : INT32_MAX / kC * kC;
+        chosen[1] = cuts[best];
+        *chosen = (int)min(seg, (int64_t)(args.T + kC - 1) / kC * kC);  // (a sequence of all tokens is not longer)
     }
 }
 
@@ -553,6 +602,8 @@ cudaError_t launch(const LinArgs &a, void *ws, int64_t tokens, cudaStream_t st)
     split.slots = plan.slots;
     split.tokens = plan.tokens;
     split.states = plan.bytes ? (float *)ws : nullptr;
+    int *const chosen = split.states && several(a) ? (int *)((char *)ws + plan.bytes - kChosenBytes) : nullptr;
+    split.chosen = chosen;
     static std::atomic<uint64_t> seen;
     if (first_on_device(seen)) {
         cudaError_t e = cudaFuncSetAttribute(lin_tc_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<D>::kSmem);
@@ -565,6 +616,7 @@ cudaError_t launch(const LinArgs &a, void *ws, int64_t tokens, cudaStream_t st)
     const unsigned grid = (unsigned)ctas;
     const int withhold = withhold_loads();
     const uint64_t limit = withhold ? kTestWaitLimitNs : kWaitLimitNs;
+    if (chosen) lin_choose_kernel<<<1, 512, 0, st>>>(a, plan.tokens, (float)(a.HV * (D / kCols) * a.passes) / (float)device_sm_count(), chosen);
     if (split.states) {
         lin_tc_kernel<D, true><<<grid, kThreads, Geo<D>::kSmem, st>>>(maps, a, split, limit, withhold);
         lin_join_kernel<D><<<dim3((unsigned)(elements / 1024), a.passes), 256, 0, st>>>(a, split);
@@ -601,15 +653,15 @@ bool strided_map(CUtensorMap *m, const void *base, int D, int heads, int T, int 
 LinPlan lin_tc_plan(const LinArgs &a, int D)
 {
     // A split walks its chunks twice (the second time with outputs), so it pays only where (sequence, head) pairs leave SMs idle: the
-    // time of a plan is taken as rounds of CTAs times chunks of a segment, a walk without outputs as 0.6 of one with them (measured: 80 us
-    // and 122 at 65536 tokens of 8 heads) and the further launches as 8 chunks.  The lengths of packed sequences are not known here: the
-    // segment is what one sequence of all tokens would be cut into, so that one that holds up the others is cut and the others stay whole.
+    // time of a plan is taken as rounds of CTAs times chunks of a segment and two more to begin and end one, a walk without outputs as 0.6 of
+    // one with them (measured: 80 us and 122 at 65536 tokens of 8 heads) and the further launches as 8 chunks.  The lengths of packed
+    // sequences are not known here: the segment is what one sequence of all tokens would be cut into, and lin_choose_kernel takes a multiple of it.
     const int64_t each = std::max(1, (a.T + kC - 1) / kC), ctas = (int64_t)(a.cu ? 1 : a.N) * a.HV * (D / kCols) * a.passes, sms = device_sm_count();
     int64_t best = 1;
     double least = 1e30;
     for (int64_t s = 1; s <= std::min<int64_t>(64, (each + 3) / 4); ++s) {
         const int64_t per = (each + s - 1) / s;
-        const double t = (double)((ctas * s + sms - 1) / sms) * (double)per * (s > 1 ? 1.6 : 1.0) + (s > 1 ? 8.0 : 0.0);
+        const double t = (double)((ctas * s + sms - 1) / sms) * (double)(per + 2) * (s > 1 ? (double)kAgain : 1.0) + (s > 1 ? (double)kLaunches : 0.0);
         if (t < least) least = t, best = s;
     }
     LinPlan p{};
@@ -619,7 +671,7 @@ LinPlan lin_tc_plan(const LinArgs &a, int D)
     }
     p.tokens = (int)((each + best - 1) / best) * kC;
     p.slots = mix_slots(a.cu != nullptr, a.N, a.T, p.tokens);
-    p.bytes = (size_t)a.passes * p.slots * a.HV * D * D * sizeof(float);
+    p.bytes = (size_t)a.passes * p.slots * a.HV * D * D * sizeof(float) + (several(a) ? kChosenBytes : 0);
     return p;
 }
 
