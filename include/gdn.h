@@ -525,7 +525,8 @@ gdn_status gdn_read_layer_status(gdn_stream_t stream);
  * that the waits for them run out after 5 ms, gdn_read_layer_status reports
  * GDN_ERR_TIMEOUT and the outputs are undefined.  There are such instances
  * for bf16 to bf16 and fp32 products in tiles of 128 columns and for bf16
- * ones of up to 16 rows; other products run as ever. */
+ * ones of up to 16 rows; other products run as ever.  The token mixers'
+ * tensor-core kernels below load nothing either. */
 void gdn_layer_test_withhold(int on);
 
 /* ------------------------------------------------------------------------
