@@ -23,46 +23,65 @@ __device__ __forceinline__ void load_rows(float *dst, int stride, const T *src, 
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) lin_simt_kernel(const LinArgs args)
+struct Split {
+    float *states;  // [passes][slots][HV][da][dc]: what a segment adds to the state, then the state that enters it; null: one segment each
+    int tokens;     // of a segment (a multiple of kC)
+    int64_t slots;
+    size_t pass;    // elements of a pass
+};
+
+// W: a, b columns at most.  STATE: only what a segment adds to the state, from zero.
+template <typename T, int W, bool STATE>
+__global__ void __launch_bounds__(kThreads) lin_simt_kernel(const LinArgs args, const Split split)
 {
     extern __shared__ float4 lin_smem[];
     const LinPass &p = args.pass[blockIdx.y];
     const int nct = (p.dc + kBV - 1) / kBV;
-    if (blockIdx.x >= (int64_t)args.N * args.HV * nct) return;
-    const int ct = (int)(blockIdx.x % nct), hv = (int)(blockIdx.x / nct % args.HV), n = (int)(blockIdx.x / ((int64_t)nct * args.HV));
+    if (blockIdx.x >= split.slots * args.HV * nct) return;
+    const int ct = (int)(blockIdx.x % nct), hv = (int)(blockIdx.x / nct % args.HV);
+    const int64_t slot = blockIdx.x / ((int64_t)nct * args.HV);
+    const Tile tl = split.states ? tile_of(args.cu, args.N, args.T, split.tokens, slot) : Tile{(int)slot, 0};
+    const int n = tl.n;
     const SeqRange s = seq_range(args.cu, n, args.T);
+    // the segment, in the order of processing
+    const int chunks = (s.len + kC - 1) / kC, per = split.states ? split.tokens / kC : chunks;
+    const int m0 = (int)min((int64_t)tl.index * per, (int64_t)chunks), m1 = (int)min((int64_t)m0 + per, (int64_t)chunks);
+    const bool last = m1 == chunks, cut = chunks > per;
+    if (STATE ? !cut || last : tl.index > 0 && m0 >= m1) return;
     const int da = p.da, w = (da + 3) & ~3, st = w + 4, c0 = ct * kBV, cols = min(kBV, p.dc - c0);
     float *A = (float *)lin_smem, *B = A + kC * st, *C = B + kC * st, *P = C + kC * kCS, *X = P + kC * kCS;  // X [w][kCS]
+    __shared__ float pw[kC + 1];  // l^i
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int xq = tid & 7, xr = tid >> 3;  // the state's owner: columns 4 xq .., rows xr + 32 i
-    const float g = args.decay ? args.decay[hv] : 0.f, g2 = g * kRcpLn2;
+    const float g = args.decay ? args.decay[hv] : 0.f;
+    if (tid <= kC) pw[tid] = decay_pow(g * kRcpLn2, tid);
     const int64_t xbase = ((int64_t)n * args.HV + hv) * da * p.dc;
     auto xat = [&](int r, int c) { return xbase + (p.x_t ? (int64_t)(c0 + c) * da + r : (int64_t)r * p.dc + c0 + c); };
+    float *const mine = cut ? split.states + blockIdx.y * split.pass + (slot * args.HV + hv) * da * p.dc + c0 : nullptr;
 
-    float x[kMaxD / 32][4];
+    float x[W / 32][4];
 #pragma unroll
-    for (int i = 0; i < kMaxD / 32; ++i) {
+    for (int i = 0; i < W / 32; ++i) {
         const int r = xr + 32 * i;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            x[i][k] = p.x0 && r < da && 4 * xq + k < cols ? p.x0[xat(r, 4 * xq + k)] : 0.f;
+            x[i][k] = STATE || r >= da || 4 * xq + k >= cols ? 0.f : mine ? mine[(int64_t)r * p.dc + 4 * xq + k] : p.x0 ? p.x0[xat(r, 4 * xq + k)] : 0.f;
             if (r < w) X[r * kCS + 4 * xq + k] = x[i][k];
         }
     }
-    const int chunks = (s.len + kC - 1) / kC;
-    for (int m = 0; m < chunks; ++m) {
+    const bool out = !STATE && p.out;
+    for (int m = m0; m < m1; ++m) {
         const int c = p.reverse ? chunks - 1 - m : m;
         const int64_t t0 = s.bos + (int64_t)c * kC;
         const int rows = min(kC, s.len - c * kC);
         const int late = p.reverse && m == 0;  // X0 enters one step later
         __syncthreads();
-        load_rows<T>(A, st, (const T *)p.a + t0 * p.lda + (int64_t)(hv / p.ra) * da, p.lda, rows, da, w);
+        if (!STATE) load_rows<T>(A, st, (const T *)p.a + t0 * p.lda + (int64_t)(hv / p.ra) * da, p.lda, rows, da, w);
         load_rows<T>(B, st, (const T *)p.b + t0 * p.ldb + (int64_t)(hv / p.rb) * da, p.ldb, rows, da, w);
         load_rows<T>(C, kCS, (const T *)p.c + t0 * p.ldc + (int64_t)(hv / p.rc) * p.dc + c0, p.ldc, rows, cols, kBV);
         __syncthreads();
         float o[2][2] = {};
-        if (p.out) {
+        if (out) {
             float z[2][2] = {};
             for (int k = 0; k < w; k += 4) {
                 float4 u[2], v[2];
@@ -85,12 +104,12 @@ __global__ void __launch_bounds__(kThreads) lin_simt_kernel(const LinArgs args)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const int r = ty + 16 * i, q = tx + 16 * j, gap = p.reverse ? q - r : r - q;
-                    P[r * kCS + q] = gap >= 0 ? z[i][j] * (p.cs * decay_pow(g2, gap)) : 0.f;
-                    o[i][j] *= decay_pow(g2, p.reverse ? max(rows - r - late, 0) : r + 1);
+                    P[r * kCS + q] = gap >= 0 ? z[i][j] * (p.cs * pw[gap]) : 0.f;
+                    o[i][j] *= pw[p.reverse ? max(rows - r - late, 0) : r + 1];
                 }
         }
-        __syncthreads();
-        if (p.out) {
+        if (!STATE) __syncthreads();
+        if (out) {
 #pragma unroll 4
             for (int j = 0; j < kC; ++j) {
                 const float u0 = P[ty * kCS + j], u1 = P[(ty + 16) * kCS + j], v0 = C[j * kCS + tx], v1 = C[j * kCS + tx + 16];
@@ -113,14 +132,14 @@ __global__ void __launch_bounds__(kThreads) lin_simt_kernel(const LinArgs args)
         }
         const Decayed down(g, rows - late);
 #pragma unroll
-        for (int i = 0; i < kMaxD / 32; ++i)
+        for (int i = 0; i < W / 32; ++i)
 #pragma unroll
             for (int k = 0; k < 4; ++k) x[i][k] = down(x[i][k]);
         for (int j = 0; j < rows; ++j) {
-            const float f = p.cs * decay_pow(g2, p.reverse ? j : rows - 1 - j);
+            const float f = p.cs * pw[p.reverse ? j : rows - 1 - j];
             const float4 v = *(const float4 *)&C[j * kCS + 4 * xq];
 #pragma unroll
-            for (int i = 0; i < kMaxD / 32; ++i) {
+            for (int i = 0; i < W / 32; ++i) {
                 const int r = xr + 32 * i;
                 if (r < w) {
                     const float b = f * B[j * st + r];
@@ -132,20 +151,54 @@ __global__ void __launch_bounds__(kThreads) lin_simt_kernel(const LinArgs args)
             }
         }
 #pragma unroll
-        for (int i = 0; i < kMaxD / 32; ++i) {
+        for (int i = 0; i < W / 32; ++i) {
             const int r = xr + 32 * i;
-            if (r < w) *(float4 *)&X[r * kCS + 4 * xq] = make_float4(x[i][0], x[i][1], x[i][2], x[i][3]);
+            if (!STATE && r < w) *(float4 *)&X[r * kCS + 4 * xq] = make_float4(x[i][0], x[i][1], x[i][2], x[i][3]);
         }
     }
-    if (p.x1) {
+    if (STATE) {
+#pragma unroll
+        for (int i = 0; i < W / 32; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int r = xr + 32 * i;
+                if (r < da && 4 * xq + k < cols) mine[(int64_t)r * p.dc + 4 * xq + k] = x[i][k];
+            }
+    } else if (p.x1 && last) {
         const Decayed down(g, p.reverse && chunks > 0 ? 1 : 0);
 #pragma unroll
-        for (int i = 0; i < kMaxD / 32; ++i)
+        for (int i = 0; i < W / 32; ++i)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int r = xr + 32 * i;
                 if (r < da && 4 * xq + k < cols) p.x1[xat(r, 4 * xq + k)] = down(x[i][k]);
             }
+    }
+}
+
+// What the segments add to the state -> the state that enters each (in place), an element to a thread
+__global__ void __launch_bounds__(kThreads) lin_join_kernel(const LinArgs args, const Split split)
+{
+    const LinPass &p = args.pass[blockIdx.y];
+    const int size = p.da * p.dc;
+    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x, pair = i / size;
+    if (pair >= (int64_t)args.N * args.HV) return;
+    const int at = (int)(i - pair * size), n = (int)(pair / args.HV), hv = (int)(pair - (int64_t)n * args.HV);
+    const SeqRange s = seq_range(args.cu, n, args.T);
+    const int segs = (s.len + split.tokens - 1) / split.tokens;
+    if (segs <= 1) return;  // (whole)
+    const int64_t slot0 = args.cu ? clamp64(args.cu[n], 0, args.T) / split.tokens + n : (int64_t)n * ((args.T + split.tokens - 1) / split.tokens);
+    const float g = args.decay ? args.decay[hv] : 0.f;
+    // tokens of a segment in the order of processing: against time the first has the sequence's odd end, and X0 enters one step later
+    const int odd = (s.len + kC - 1) / kC * kC - s.len;
+    const Decayed first(g, split.tokens - (p.reverse ? odd + 1 : 0)), rest(g, split.tokens);
+    float x = p.x0 ? p.x0[pair * size + (p.x_t ? at % p.dc * p.da + at / p.dc : at)] : 0.f;
+    float *buf = split.states + blockIdx.y * split.pass + (slot0 * args.HV + hv) * size + at;
+    for (int k = 0; k < segs; ++k) {
+        float *const here = buf + k * (int64_t)args.HV * size;
+        const float add = k + 1 < segs ? *here : 0.f;
+        *here = x;
+        x = (k == 0 ? first(x) : rest(x)) + add;
     }
 }
 
@@ -195,27 +248,76 @@ cudaError_t heads(const float *part, const LinArgs &a, int64_t tokens, int H, in
 
 }  // namespace
 
-cudaError_t launch_lin_simt(const LinArgs &a, gdn_dtype dt, cudaStream_t st)
+LinPlan lin_simt_plan(const LinArgs &a)
 {
-    int64_t most = 0;
+    // A split walks twice (the second time with outputs), so only as many segments as bring four CTAs to an SM, of four chunks at least.  The
+    // lengths of packed sequences are not known here: the segment is what one sequence of all tokens is cut into, shorter ones stay whole.
+    // fp32: @B
+    int64_t ctas = 0, size = 0;
+    for (int i = 0; i < a.passes; ++i) {
+        ctas += (int64_t)(a.cu ? 1 : a.N) * a.HV * ((a.pass[i].dc + kBV - 1) / kBV);
+        size = std::max(size, (int64_t)a.pass[i].da * a.pass[i].dc);
+    }
+    const int64_t each = (a.T + kC - 1) / kC, segs = std::min<int64_t>(4 * device_sm_count() / std::max<int64_t>(ctas, 1), each / 4);
+    LinPlan p{};
+    p.slots = a.N;
+    if (segs < 2) return p;
+    p.tokens = (int)((each + segs - 1) / segs) * kC;
+    p.slots = mix_slots(a.cu != nullptr, a.N, a.T, p.tokens);
+    p.bytes = (size_t)a.passes * p.slots * a.HV * size * sizeof(float);
+    return p;
+}
+
+namespace {
+
+template <typename T, int W>
+cudaError_t launch(const LinArgs &a, void *ws, cudaStream_t st)
+{
+    const LinPlan plan = lin_simt_plan(a);
+    int64_t most = 0, joined = 0;
     size_t smem = 0;
+    Split split{};
+    split.states = plan.bytes ? (float *)ws : nullptr;
+    split.tokens = plan.tokens;
+    split.slots = plan.slots;
+    split.pass = plan.bytes / sizeof(float) / a.passes;
     for (int i = 0; i < a.passes; ++i) {
         const LinPass &p = a.pass[i];
-        most = std::max(most, (int64_t)a.N * a.HV * ((p.dc + kBV - 1) / kBV));
+        most = std::max(most, plan.slots * a.HV * ((p.dc + kBV - 1) / kBV));
+        joined = std::max(joined, ((int64_t)a.N * a.HV * p.da * p.dc + kThreads - 1) / kThreads);
         const size_t w = (p.da + 3) & ~3;
         smem = std::max(smem, 4 * (2 * kC * (w + 4) + 2 * kC * kCS + w * kCS));
     }
-    if (most > INT32_MAX) return cudaErrorInvalidConfiguration;
-    auto kern = dt == GDN_F32 ? lin_simt_kernel<float> : lin_simt_kernel<__nv_bfloat16>;
-    static std::atomic<uint64_t> seen[2];
-    if (first_on_device(seen[dt == GDN_F32])) {
-        const int bytes = 4 * (2 * kC * (kMaxD + 4) + 2 * kC * kCS + kMaxD * kCS);
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (most > INT32_MAX || joined > INT32_MAX) return cudaErrorInvalidConfiguration;
+    static std::atomic<uint64_t> seen;
+    if (first_on_device(seen)) {
+        const int bytes = 4 * (2 * kC * (W + 4) + 2 * kC * kCS + W * kCS);
+        cudaError_t e = cudaFuncSetAttribute(lin_simt_kernel<T, W, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(lin_simt_kernel<T, W, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
-        done_on_device(seen[dt == GDN_F32]);
+        done_on_device(seen);
     }
-    kern<<<dim3((unsigned)most, a.passes), kThreads, smem, st>>>(a);
+    const dim3 grid((unsigned)most, a.passes);
+    if (split.states) {
+        lin_simt_kernel<T, W, true><<<grid, kThreads, smem, st>>>(a, split);
+        lin_join_kernel<<<dim3((unsigned)joined, a.passes), kThreads, 0, st>>>(a, split);
+    }
+    lin_simt_kernel<T, W, false><<<grid, kThreads, smem, st>>>(a, split);
     return cudaGetLastError();
+}
+template <typename T>
+cudaError_t launch_of(const LinArgs &a, void *ws, cudaStream_t st)
+{
+    int da = 0;
+    for (int i = 0; i < a.passes; ++i) da = std::max(da, a.pass[i].da);
+    return da <= 64 ? launch<T, 64>(a, ws, st) : da <= 128 ? launch<T, 128>(a, ws, st) : launch<T, kMaxD>(a, ws, st);
+}
+
+}  // namespace
+
+cudaError_t launch_lin_simt(const LinArgs &a, gdn_dtype dt, void *ws, cudaStream_t st)
+{
+    return dt == GDN_F32 ? launch_of<float>(a, ws, st) : launch_of<__nv_bfloat16>(a, ws, st);
 }
 
 cudaError_t launch_lin_heads(const float *part, const LinArgs &a, int64_t tokens, int H, int r, int D, void *dq, void *dk, gdn_dtype dt, cudaStream_t st)

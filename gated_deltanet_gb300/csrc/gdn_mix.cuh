@@ -70,7 +70,6 @@ struct LinArgs {
     int T, N, HV;            // packed: T = all tokens
     unsigned *status;
 };
-cudaError_t launch_lin_simt(const LinArgs &a, gdn_dtype dt, cudaStream_t st);
 // bf16, all sizes 64 or all 128, rows on 16-byte boundaries: on the tensor cores.  A plan splits sequences into segments where there
 // are few; then `bytes` of workspace.
 struct LinPlan {
@@ -78,6 +77,8 @@ struct LinPlan {
     int64_t slots;           // (sequence, segment) pairs
     int tokens;              // of a segment
 };
+LinPlan lin_simt_plan(const LinArgs &a);
+cudaError_t launch_lin_simt(const LinArgs &a, gdn_dtype dt, void *ws, cudaStream_t st);
 bool lin_tc_ok(const LinArgs &a, int64_t tokens);
 LinPlan lin_tc_plan(const LinArgs &a, int D);
 cudaError_t launch_lin_tc(const LinArgs &a, void *ws, int64_t tokens, cudaStream_t st);

@@ -95,10 +95,10 @@ LinArgs lin_backward(const gdn_linear_attn_args *a, float *part)
     return l;
 }
 bool lin_on_tc(const gdn_linear_attn_args *a, const LinArgs &l) { return a->dtype == GDN_BF16 && lin_tc_ok(l, (int64_t)a->B * a->T); }
-size_t lin_split_bytes(const gdn_linear_attn_args *a, const LinArgs &l) { return lin_on_tc(a, l) ? up256(lin_tc_plan(l, a->K).bytes) : 0; }
+size_t lin_split_bytes(const gdn_linear_attn_args *a, const LinArgs &l) { return up256(lin_on_tc(a, l) ? lin_tc_plan(l, a->K).bytes : lin_simt_plan(l).bytes); }
 cudaError_t run_lin(const gdn_linear_attn_args *a, const LinArgs &l, void *ws, cudaStream_t st)
 {
-    return lin_on_tc(a, l) ? launch_lin_tc(l, ws, (int64_t)a->B * a->T, st) : launch_lin_simt(l, a->dtype, st);
+    return lin_on_tc(a, l) ? launch_lin_tc(l, ws, (int64_t)a->B * a->T, st) : launch_lin_simt(l, a->dtype, ws, st);
 }
 size_t lin_part_bytes(const gdn_linear_attn_args *a)
 {
