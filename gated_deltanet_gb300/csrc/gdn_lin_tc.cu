@@ -14,7 +14,7 @@
 // the warps beside them.  A chunk's products are 2640 cycles alone and about 3700 so; a chunk takes 4100.  Hence: hi and lo lie next to
 // each other and go in as one right operand of 128 columns (X is the sum of two accumulators); outputs go from registers to memory.
 // A whole head to a CTA has the cheaper products (N = 128, X transposed, C in tensor memory) but half the CTAs and most of its
-// CUDA-core work on the chain from chunk to chunk: 138 us at 4 x 4096 tokens of 16 heads of 128 where this takes 76; C in three parts
+// CUDA-core work on the chain from chunk to chunk: 138 us at 4 x 4096 tokens of 16 heads of 128 where this takes 80; C in three parts
 // (24 bits) 102.
 //
 // Warps: 0 loads (TMA: two stages of a and b, three of c, which is done with later; zeroes the rows behind a sequence's end, which are

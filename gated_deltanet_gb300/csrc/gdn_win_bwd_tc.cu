@@ -9,8 +9,8 @@
 //                   a key), so that P^T and Z^T are left operands in tensor memory as they come
 // The far queries of sinks are dealt out to CTAs of their own, whose parts win_sinks_kernel adds up (WinSinks).
 //
-// 4 x 4096 tokens, 16 heads over 4 of 128, window 1024: dQ 212 us, dK and dV 270, 137 GFLOP of scores each way.
-//  - dQ: one CTA per SM walks tiles of queries (a CTA to each: 245 us; starting one and filling its pipeline took 12000 cycles, the walk 24000).
+// 4 x 4096 tokens, 16 heads over 4 of 128, window 1024: 445 us: dQ 188, dK and dV 254 (680 TFLOP/s by the floor's five products).
+//  - dQ: one CTA per SM walks tiles of queries (a CTA to each: 245 us at the time; starting one and filling its pipeline took 12000 cycles, the walk 24000).
 //    Q and dO are left operands in tensor memory: 128 x 128 x 16 then takes 67 cycles, with both operands in shared memory 104, which is bound by
 //    its 80 bytes a cycle.  A tile of keys takes 2480 cycles: its products 1610 alone, the copies of K and V take shared memory from them.
 //  - dK, dV: no room for K and V beside four accumulators; a tile of queries takes 3000 cycles, its products 2740.

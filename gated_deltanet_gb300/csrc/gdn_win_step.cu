@@ -7,7 +7,9 @@
 //   step_mma_kernel   bf16 heads of 64 and 128 on 16-byte boundaries, R = 16: each of four warps walks its own tiles of 16 keys, which
 //                     arrive by cp.async (16 bytes a lane) some tiles ahead, S = Q K^T and O += P V by mma.sync (a tile of 128 queries
 //                     for tcgen05 would be mostly empty; the keys' bytes bound the call all the same)
-//   step_any_kernel   everything else, R = 8: tiles of 32 keys through shared memory, fp32 on the CUDA cores
+//   step_any_kernel   everything else, R = 8: tiles of 32 keys through shared memory, fp32 on the CUDA cores, which bound it
+// 64 sequences, window 4096, 16 heads over 4: bf16 heads of 128 103 us, 5.2 TB/s; of 96 440; fp32 of 128 615 (read element by element 830, 876).
+// One sequence, window 1024: 9.8 us, launch and latency.
 #include "gdn_mix.cuh"
 #include "gdn_ptx.cuh"
 
@@ -267,7 +269,20 @@ __global__ void __launch_bounds__(kThreads) step_mma_kernel(const WinStepArgs a)
 // ---------------------------------------------------------------- any type and size, on the CUDA cores
 constexpr int kAnyRows = 8, kAnyKeys = 32;
 
-template <typename T, int DP>
+// E elements of 16 bytes as fp32
+template <typename T>
+__device__ __forceinline__ void spread(float *dst, uint4 x)
+{
+    if constexpr (sizeof(T) == 4) {
+        *(uint4 *)dst = x;
+    } else {
+        *(float4 *)dst = make_float4(low_bf16(x.x), high_bf16(x.x), low_bf16(x.y), high_bf16(x.y));
+        *(float4 *)(dst + 4) = make_float4(low_bf16(x.z), high_bf16(x.z), low_bf16(x.w), high_bf16(x.w));
+    }
+}
+
+// WIDE: the cache's rows are on 16 bytes and a multiple of them long
+template <typename T, int DP, bool WIDE>
 __global__ void __launch_bounds__(kThreads) step_any_kernel(const WinStepArgs a)
 {
     constexpr int kStride = DP + 4, kCols = (DP + kThreads - 1) / kThreads;
@@ -292,13 +307,35 @@ __global__ void __launch_bounds__(kThreads) step_any_kernel(const WinStepArgs a)
     for (int t = t0; t < t1; ++t) {
         const int keys = min(kAnyKeys, it.count - t * kAnyKeys);
         __syncthreads();
+        if constexpr (WIDE) {  // (all of a thread's loads in flight: element by element a tile waited four times)
+            constexpr int E = 16 / sizeof(T), kPer = DP / E, kAll = kAnyKeys * kPer / kThreads, kBatch = kAll < 8 ? kAll : 8;
+#pragma unroll 1
+            for (int b = 0; b < kAll; b += kBatch) {
+                uint4 k[kBatch], v[kBatch];
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    const int i = tid + (b + u) * kThreads, r = i / kPer, d = i % kPer * E;
+                    const bool in = r < keys && d < a.D;
+                    const int64_t j = it.key(t * kAnyKeys + (in ? r : 0));
+                    k[u] = in ? *(const uint4 *)(Kg + j * a.k_tok + d) : make_uint4(0, 0, 0, 0);
+                    v[u] = in ? *(const uint4 *)(Vg + j * a.v_tok + d) : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    const int i = tid + (b + u) * kThreads, r = i / kPer, d = i % kPer * E;
+                    spread<T>(K + r * kStride + d, k[u]);
+                    spread<T>(V + r * kStride + d, v[u]);
+                }
+            }
+        } else {
 #pragma unroll 8
-        for (int i = tid; i < kAnyKeys * DP; i += kThreads) {
-            const int r = i / DP, d = i % DP;
-            const bool in = r < keys && d < a.D;
-            const int64_t j = it.key(t * kAnyKeys + (in ? r : 0));
-            K[r * kStride + d] = in ? to_f<T>(Kg[j * a.k_tok + d]) : 0.f;
-            V[r * kStride + d] = in ? to_f<T>(Vg[j * a.v_tok + d]) : 0.f;
+            for (int i = tid; i < kAnyKeys * DP; i += kThreads) {
+                const int r = i / DP, d = i % DP;
+                const bool in = r < keys && d < a.D;
+                const int64_t j = it.key(t * kAnyKeys + (in ? r : 0));
+                K[r * kStride + d] = in ? to_f<T>(Kg[j * a.k_tok + d]) : 0.f;
+                V[r * kStride + d] = in ? to_f<T>(Vg[j * a.v_tok + d]) : 0.f;
+            }
         }
         __syncthreads();
         {  // rows warp and warp + 4, key lane
@@ -396,9 +433,13 @@ cudaError_t launch(K kern, const WinStepArgs &a, int R, int keys_each, size_t sm
 template <typename T, int DP>
 cudaError_t launch_any(const WinStepArgs &a, cudaStream_t st)
 {
-    static std::atomic<uint64_t> seen;
+    constexpr int E = 16 / sizeof(T);
+    static std::atomic<uint64_t> seen[2];
     const size_t smem = 4 * ((2 * kAnyKeys + 2 * kAnyRows) * (DP + 4) + kAnyRows * kAnyKeys + 3 * kAnyRows);
-    return launch(step_any_kernel<T, DP>, a, kAnyRows, kAnyKeys, smem, seen, st);
+    const int64_t strides = a.k_seq | a.k_tok | a.k_head | a.v_seq | a.v_tok | a.v_head;
+    const bool wide = strides % E == 0 && a.D % E == 0 && !(((uintptr_t)a.k | (uintptr_t)a.v) & 15);
+    return wide ? launch(step_any_kernel<T, DP, true>, a, kAnyRows, kAnyKeys, smem, seen[1], st)
+                : launch(step_any_kernel<T, DP, false>, a, kAnyRows, kAnyKeys, smem, seen[0], st);
 }
 template <typename T>
 cudaError_t launch_any(const WinStepArgs &a, cudaStream_t st)

@@ -13,6 +13,8 @@
 // sequence's end (they are the next sequence's, and 0 x NaN is NaN), 17 products.
 // The products are issued S_A(t), PV_B(t-1), S_B(t), PV_A(t): S(t) is complete only when PV(t-1) is, which is why a softmax that sees
 // its scores may also touch its O.
+// 4 x 4096 tokens, 16 heads over 4 of 128, window 1024: 145 us, 830 TFLOP/s.  S with both operands in shared memory takes 104 cycles a product
+// where the arithmetic takes 64, which with P V (67 of 64), the copies and a CTA's start and end is what bounds it.
 #include "gdn_mix.cuh"
 #include "gdn_ptx.cuh"
 
