@@ -87,7 +87,10 @@ def _window(p, s, cache):
         o, s.lse = gdn.window_attention(s.qh, s.kh, s.v, p.window, p.sinks, return_lse=True)
         room = torch.zeros(B, ROOM, *s.v.shape[2:], dtype=s.v.dtype, device=s.v.device)
         return o, SimpleNamespace(k=torch.cat([s.kh, room], 1), v=torch.cat([s.v, room], 1),
-                                  lengths=torch.full((B,), T, dtype=torch.int32, device=s.v.device))
+                                  lengths=torch.full((B,), T, dtype=torch.int32, device=s.v.device), room=ROOM)
+    if T > cache.room:
+        raise ValueError(f"the cache has room for {cache.room} more tokens, not {T}")
+    cache.room -= T
     rows, at = torch.arange(B, device=s.v.device)[:, None], cache.lengths[:, None] + torch.arange(T, device=s.v.device)
     cache.k[rows, at], cache.v[rows, at] = s.kh, s.v
     cache.lengths += T

@@ -102,6 +102,8 @@ def test_stack_forward_and_decode(block):
         parts.append(got)
     assert rel(torch.cat(parts, 1), want) < bound
     assert rel(torch.cat(parts, 1)[:, 120:], want[:, 120:]) < bound
+    with pytest.raises(ValueError, match="room"):  # (the window layer's cache is full)
+        block.forward(layers[1], torch.zeros(2, block.ROOM - 29, 256, dtype=x.dtype, device="cuda"), states[1])
 
 
 def test_stack_gradients_against_differences(block):
