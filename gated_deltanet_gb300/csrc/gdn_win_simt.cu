@@ -353,20 +353,23 @@ cudaError_t launch_keys(const WinArgs &a, void *ws, cudaStream_t st)
     if (s.tiles > 0) win_sinks_kernel<T, TILE><<<(unsigned)blocks, kThreads, 0, st>>>(a, s, count);
     return cudaGetLastError();
 }
-// Tiles of 64 (each key and query is read half as often), or of 32 where 64 would leave SMs without a tile, and for heads whose tiles of 64
-// do not fit.  fp32, window 100, gradients of 2048 tokens, 4 heads over 2 of 64 (128 tiles of queries, 64 of keys): 182 us with 64, 145 with
-// 32; 300 tokens of 2 heads of 40: 90 and 70; 2 x 2048 tokens, 4 heads of 64, window 256 (256 tiles): 258 and 272.
-int tile_for(int D, bool packed, int N, int T, int heads)
+// Tiles of 64 (each key and query is read half as often), or of 32 where 64 would leave SMs without a tile, where much of a tile of 64 lies
+// outside the window, and for heads whose tiles of 64 do not fit.  fp32, 64 and 32:
+//   gradients, window 100, 2048 tokens of 4 heads over 2 of 64 (128 tiles of queries, 64 of keys): 182 us, 145; 300 tokens of 2 heads of 40: 90, 70
+//   11502 tokens of 8 heads over 4 of 64: window 35 219, 176, gradients 766, 621; window 128 283, 252, gradients 887, 842
+//   2 x 2048 tokens, 4 heads of 64, window 256: 94, 104, gradients 258, 272
+//   8 heads of 128, window 128, 4 x 2048 tokens: 346, 412, gradients 1532, 1251
+int tile_for(const WinArgs &a, const int64_t *cu, int T, int heads, bool forward)
 {
-    return D > 128 || mix_slots(packed, N, T, 64) * heads < device_sm_count() ? 32 : 64;
+    const bool narrow = a.window <= 128 && (!forward || a.D <= 64);
+    return a.D > 128 || narrow || mix_slots(cu != nullptr, a.N, T, 64) * heads < device_sm_count() ? 32 : 64;
 }
-int row_tile(const WinArgs &a) { return tile_for(a.D, a.cu_q != nullptr, a.N, a.Tq, a.H); }
-int key_tile(const WinArgs &a) { return tile_for(a.D, a.cu_k != nullptr, a.N, a.Tk, a.HK); }
+int key_tile(const WinArgs &a) { return tile_for(a, a.cu_k, a.Tk, a.HK, false); }
 template <typename T>
 cudaError_t launch_rows_of(const WinArgs &a, bool dq, cudaStream_t st)
 {
     if (a.D > 128) return launch_rows<T, 32, 256>(a, dq, st);
-    if (row_tile(a) == 32) return a.D <= 64 ? launch_rows<T, 32, 64>(a, dq, st) : launch_rows<T, 32, 128>(a, dq, st);
+    if (tile_for(a, a.cu_q, a.Tq, a.H, !dq) == 32) return a.D <= 64 ? launch_rows<T, 32, 64>(a, dq, st) : launch_rows<T, 32, 128>(a, dq, st);
     return a.D <= 64 ? launch_rows<T, 64, 64>(a, dq, st) : launch_rows<T, 64, 128>(a, dq, st);
 }
 template <typename T>
