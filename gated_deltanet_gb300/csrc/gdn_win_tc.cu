@@ -126,9 +126,9 @@ __global__ void __launch_bounds__(kThreads, 1) win_tc_kernel(const __grid_consta
             }
             __syncwarp();
         };
-        const bool both = ok && B.rows > 0;
+        // (without keys nothing waits for B's queries: they would land on its outputs)
+        const bool both = ok && B.rows > 0 && nt > 0;
         if (ok) queries(0);
-        if (both && nt == 0) queries(1);
         int i = 0, mended = 0;
         for (; i < 2 * nt && ok; ++i) {
             const int s = i % G::kRing;

@@ -302,6 +302,30 @@ def test_window_large_scores(gdn, dtype):
     check_window_bwd(gdn, q, k, v, randn(g, 1, T, 1, D, dtype=dtype), 250, 4, D ** -0.5, None, None)
 
 
+@pytest.mark.parametrize("H,HK", [(4, 2), (3, 3)])  # (a CTA's two tiles: two heads, neighbouring rows)
+@pytest.mark.parametrize("D", [64, 128])
+def test_window_tiles_without_keys(gdn, H, HK, D):
+    """Tiles of queries that see no key at all write zeros over the place where their queries land: many of them, while copies on
+    another stream slow the loads down."""
+    g = gen(27)
+    B, Tq, Tk = 4, 2300, 40
+    q, k, v = randn(g, B, Tq, H, D, dtype=BF), randn(g, B, Tk, HK, D, dtype=BF), randn(g, B, Tk, HK, D, dtype=BF)
+    cu, cu_k = offsets([700, 3, 1597]), offsets([0, 0, 37])
+    side, src = torch.cuda.Stream(), torch.empty(2 ** 27, device="cuda", dtype=torch.uint8)
+    dst = torch.empty_like(src)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        with torch.cuda.stream(side):
+            dst.copy_(src)
+        o, lse = gdn.window_attention(q, k, v, 50, 3, return_lse=True)
+        assert not o[:, :Tq - Tk].any() and (lse[..., :Tq - Tk] == -torch.inf).all()
+        assert torch.isfinite(lse[..., Tq - Tk:]).all()
+        o, lse = gdn.window_attention(q[:1], k[:1, :37], v[:1, :37], 50, 3, cu_seqlens=cu, cu_seqlens_k=cu_k, return_lse=True)
+        assert not o[:, :Tq - 37].any() and (lse[..., :Tq - 37] == -torch.inf).all()
+        assert torch.isfinite(lse[..., Tq - 37:]).all()
+    side.synchronize()
+
+
 # (N, T, S, H, HK, D, window, sinks, lengths)
 STEP = [
     (1, 1, 64, 4, 1, 128, 16, 2, [40]), (3, 1, 300, 8, 2, 128, 100, 4, [300, 1, 0]), (2, 1, 1000, 2, 2, 64, 2000, 0, [999, 513]),
