@@ -25,9 +25,9 @@ __device__ __forceinline__ void load_rows(float *dst, int stride, const T *src, 
 }
 
 struct Split {
-    float *states;  // [passes][slots][HV][da][dc]: what a segment adds to the state, then the state that enters it; null: one segment each
+    float *held;    // [passes][states][HV][da][dc]: what a segment adds to the state, then the state that enters it; null: one segment each
     int tokens;     // of a segment (a multiple of kC)
-    int64_t slots;
+    int64_t slots, states;
     size_t pass;    // elements of a pass
 };
 
@@ -38,14 +38,14 @@ __global__ void __launch_bounds__(kThreads) lin_simt_kernel(const LinArgs args, 
     extern __shared__ float4 lin_smem[];
     const LinPass &p = args.pass[blockIdx.y];
     const int nct = (p.dc + kBV - 1) / kBV;
-    if (blockIdx.x >= split.slots * args.HV * nct) return;
+    if (blockIdx.x >= (STATE ? split.states : split.slots) * args.HV * nct) return;
     const int ct = (int)(blockIdx.x % nct), hv = (int)(blockIdx.x / nct % args.HV);
     const int64_t slot = blockIdx.x / ((int64_t)nct * args.HV);
-    const Tile tl = split.states ? tile_of(args.cu, args.N, args.T, split.tokens, slot) : Tile{(int)slot, 0};
+    const Tile tl = !split.held ? Tile{(int)slot, 0} : STATE ? cut_of(args.cu, args.N, args.T, split.tokens, slot) : tile_of(args.cu, args.N, args.T, split.tokens, slot);
     const int n = tl.n;
     const SeqRange s = seq_range(args.cu, n, args.T);
     // the segment, in the order of processing
-    const int chunks = (s.len + kC - 1) / kC, per = split.states ? split.tokens / kC : chunks;
+    const int chunks = (s.len + kC - 1) / kC, per = split.held ? split.tokens / kC : chunks;
     const int m0 = (int)min((int64_t)tl.index * per, (int64_t)chunks), m1 = (int)min((int64_t)m0 + per, (int64_t)chunks);
     const bool last = m1 == chunks, cut = chunks > per;
     if (STATE ? !cut || last : tl.index > 0 && m0 >= m1) return;
@@ -58,7 +58,8 @@ __global__ void __launch_bounds__(kThreads) lin_simt_kernel(const LinArgs args, 
     if (tid <= kC) pw[tid] = decay_pow(g * kRcpLn2, tid);
     const int64_t xbase = ((int64_t)n * args.HV + hv) * da * p.dc;
     auto xat = [&](int r, int c) { return xbase + (p.x_t ? (int64_t)(c0 + c) * da + r : (int64_t)r * p.dc + c0 + c); };
-    float *const mine = cut ? split.states + blockIdx.y * split.pass + (slot * args.HV + hv) * da * p.dc + c0 : nullptr;
+    const int64_t at = cut ? cut_state0(args.cu, n, args.T, split.tokens) + tl.index : 0;
+    float *const mine = cut ? split.held + blockIdx.y * split.pass + (at * args.HV + hv) * da * p.dc + c0 : nullptr;
 
     float x[W / 32][4];
 #pragma unroll
@@ -182,19 +183,21 @@ __global__ void __launch_bounds__(kThreads) lin_join_kernel(const LinArgs args, 
 {
     const LinPass &p = args.pass[blockIdx.y];
     const int size = p.da * p.dc;
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x, pair = i / size;
-    if (pair >= (int64_t)args.N * args.HV) return;
-    const int at = (int)(i - pair * size), n = (int)(pair / args.HV), hv = (int)(pair - (int64_t)n * args.HV);
+    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x, which = i / size, place = which / args.HV;
+    if (place >= long_places(args.cu != nullptr, args.N, args.T, split.tokens)) return;
+    const int at = (int)(i - which * size), hv = (int)(which - place * args.HV);
+    auto first_at = [&](int n) { return long_place(args.cu, n, args.T, split.tokens); };
+    const int n = args.cu ? last_from(args.N, place, first_at) : (int)place;
     const SeqRange s = seq_range(args.cu, n, args.T);
     const int segs = (s.len + split.tokens - 1) / split.tokens;
-    if (segs <= 1) return;  // (whole)
-    const int64_t slot0 = args.cu ? clamp64(args.cu[n], 0, args.T) / split.tokens + n : (int64_t)n * ((args.T + split.tokens - 1) / split.tokens);
+    if (segs <= 1 || first_at(n) != place) return;  // (whole)
+    const int64_t slot0 = cut_state0(args.cu, n, args.T, split.tokens), pair = (int64_t)n * args.HV + hv;
     const float g = args.decay ? args.decay[hv] : 0.f;
     // tokens of a segment in the order of processing: against time the first has the sequence's odd end, and X0 enters one step later
     const int odd = (s.len + kC - 1) / kC * kC - s.len;
     const Decayed first(g, split.tokens - (p.reverse ? odd + 1 : 0)), rest(g, split.tokens);
     float x = p.x0 ? p.x0[pair * size + (p.x_t ? at % p.dc * p.da + at / p.dc : at)] : 0.f;
-    float *buf = split.states + blockIdx.y * split.pass + (slot0 * args.HV + hv) * size + at;
+    float *buf = split.held + blockIdx.y * split.pass + (slot0 * args.HV + hv) * size + at;
     for (int k = 0; k < segs; ++k) {
         float *const here = buf + k * (int64_t)args.HV * size;
         const float add = k + 1 < segs ? *here : 0.f;
@@ -266,7 +269,9 @@ LinPlan lin_simt_plan(const LinArgs &a)
     if (segs < 3) return p;
     p.tokens = (int)((each + segs - 1) / segs) * kC;
     p.slots = mix_slots(a.cu != nullptr, a.N, a.T, p.tokens);
-    p.bytes = (size_t)a.passes * p.slots * a.HV * size * sizeof(float);
+    p.states = cut_states(a.cu != nullptr, a.N, a.T, p.tokens);
+    p.places = long_places(a.cu != nullptr, a.N, a.T, p.tokens);
+    p.bytes = (size_t)a.passes * p.states * a.HV * size * sizeof(float);
     return p;
 }
 
@@ -276,21 +281,23 @@ template <typename T, int W>
 cudaError_t launch(const LinArgs &a, void *ws, cudaStream_t st)
 {
     const LinPlan plan = lin_simt_plan(a);
-    int64_t most = 0, joined = 0;
+    int64_t most = 0, summed = 0, joined = 0;
     size_t smem = 0;
     Split split{};
-    split.states = plan.bytes ? (float *)ws : nullptr;
+    split.held = plan.bytes ? (float *)ws : nullptr;
     split.tokens = plan.tokens;
     split.slots = plan.slots;
+    split.states = plan.states;
     split.pass = plan.bytes / sizeof(float) / a.passes;
     for (int i = 0; i < a.passes; ++i) {
         const LinPass &p = a.pass[i];
         most = std::max(most, plan.slots * a.HV * ((p.dc + kBV - 1) / kBV));
-        joined = std::max(joined, ((int64_t)a.N * a.HV * p.da * p.dc + kThreads - 1) / kThreads);
+        summed = std::max(summed, plan.states * a.HV * ((p.dc + kBV - 1) / kBV));
+        joined = std::max(joined, (plan.places * a.HV * p.da * p.dc + kThreads - 1) / kThreads);
         const size_t w = (p.da + 3) & ~3;
         smem = std::max(smem, 4 * (2 * kC * (w + 4) + 2 * kC * kCS + w * kCS));
     }
-    if (most > INT32_MAX || joined > INT32_MAX) return cudaErrorInvalidConfiguration;
+    if (most > INT32_MAX || summed > INT32_MAX || joined > INT32_MAX) return cudaErrorInvalidConfiguration;
     static std::atomic<uint64_t> seen;
     if (first_on_device(seen)) {
         const int bytes = 4 * (2 * kC * (W + 4) + 2 * kC * kCS + W * kCS);
@@ -299,12 +306,11 @@ cudaError_t launch(const LinArgs &a, void *ws, cudaStream_t st)
         if (e != cudaSuccess) return e;
         done_on_device(seen);
     }
-    const dim3 grid((unsigned)most, a.passes);
-    if (split.states) {
-        lin_simt_kernel<T, W, true><<<grid, kThreads, smem, st>>>(a, split);
+    if (split.held) {
+        lin_simt_kernel<T, W, true><<<dim3((unsigned)summed, a.passes), kThreads, smem, st>>>(a, split);
         lin_join_kernel<<<dim3((unsigned)joined, a.passes), kThreads, 0, st>>>(a, split);
     }
-    lin_simt_kernel<T, W, false><<<grid, kThreads, smem, st>>>(a, split);
+    lin_simt_kernel<T, W, false><<<dim3((unsigned)most, a.passes), kThreads, smem, st>>>(a, split);
     return cudaGetLastError();
 }
 template <typename T>

@@ -55,9 +55,9 @@ constexpr size_t kChosenBytes = 256;
 inline bool several(const LinArgs &a) { return a.cu && a.N > 1; }
 
 struct Split {
-    float *states;  // [passes][slots][HV][D][D]: what a segment adds to the state, then the state that enters it; null: one segment each
+    float *held;    // [passes][states][HV][D][D]: what a segment adds to the state, then the state that enters it; null: one segment each
     int tokens;     // of a segment (a multiple of kC)
-    int64_t slots;
+    int64_t states;
     const int *chosen;  // packed: a multiple of `tokens` that lin_choose_kernel took, and whether a sequence is longer; nullable
     __device__ int segment() const { return chosen ? *chosen : tokens; }
     __device__ bool none() const { return chosen && !chosen[1]; }  // no sequence is cut
@@ -67,9 +67,10 @@ struct Split {
 struct Part {
     SeqRange s;
     int chunks, m0, nm, seg;  // of the sequence; the first one's place, how many; which segment
-    __device__ Part(const LinArgs &a, bool split, int tokens, int64_t slot, int &n)
+    // (held: slots are those of the segments' states)
+    __device__ Part(const LinArgs &a, bool split, bool held, int tokens, int64_t slot, int &n)
     {
-        const Tile t = split ? tile_of(a.cu, a.N, a.T, tokens, slot) : Tile{(int)slot, 0};
+        const Tile t = !split ? Tile{(int)slot, 0} : held ? cut_of(a.cu, a.N, a.T, tokens, slot) : tile_of(a.cu, a.N, a.T, tokens, slot);
         n = t.n;
         s = seq_range(a.cu, n, a.T);
         seg = t.index;
@@ -99,7 +100,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     const int64_t slot = rest / args.HV;
     if (STATE && split.none()) return;
     int n;
-    const Part part(args, split.states, split.segment(), slot, n);
+    const Part part(args, split.held, STATE, split.segment(), slot, n);
     const bool rev = p.reverse;
     const bool last_seg = part.m0 + part.nm == part.chunks;
     const int nm = part.nm;
@@ -107,7 +108,8 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     const float g = args.decay ? args.decay[hv] : 0.f, g2 = g * kRcpLn2;
     const int64_t xbase = ((int64_t)n * args.HV + hv) * D * D;
     auto xat = [&](int r, int c) { return xbase + (p.x_t ? (int64_t)(c0 + c) * D + r : (int64_t)r * D + c0 + c); };
-    float *const mine = split.states && part.nm < part.chunks ? split.states + (((int64_t)pi * split.slots + slot) * args.HV + hv) * D * D + c0 : nullptr;
+    const int64_t at = split.held && part.nm < part.chunks ? (int64_t)pi * split.states + cut_state0(args.cu, n, args.T, split.segment()) + part.seg : 0;
+    float *const mine = split.held && part.nm < part.chunks ? split.held + (at * args.HV + hv) * D * D + c0 : nullptr;
 
     if (nm <= 0) {
         // nothing to walk: a sequence without tokens hands its state on
@@ -497,28 +499,30 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     }
 }
 
-// What the segments add to the state -> the state that enters each (in place): four elements to a thread, a block of 1024 to a (sequence,
-// head) pair's piece.  Eight segments are asked for at once (one after the other, 19 segments took 64 us).
+// What the segments add to the state -> the state that enters each (in place): four elements to a thread, a block of 1024 to a piece of a (cut
+// sequence, head) pair.  Eight segments are asked for at once (one after the other, 19 segments took 64 us).
 template <int D>
 __global__ void __launch_bounds__(256) lin_join_kernel(const LinArgs args, const Split split)
 {
     if (split.none()) return;
     constexpr int kPieces = D * D / 1024;
     const LinPass &p = args.pass[blockIdx.y];
-    const int pair = (int)(blockIdx.x / kPieces), at = (int)(blockIdx.x % kPieces) * 1024 + 4 * threadIdx.x;
-    const int n = pair / args.HV, hv = pair - n * args.HV;
+    const int which = (int)(blockIdx.x / kPieces), at = (int)(blockIdx.x % kPieces) * 1024 + 4 * threadIdx.x, tokens = split.segment();
+    const int place = which / args.HV, hv = which - place * args.HV;
+    auto first_at = [&](int n) { return long_place(args.cu, n, args.T, tokens); };
+    const int n = args.cu ? last_from(args.N, place, first_at) : place;
     const SeqRange s = seq_range(args.cu, n, args.T);
-    const int tokens = split.segment(), segs = (s.len + tokens - 1) / tokens;
-    if (segs <= 1) return;  // (whole)
-    const int64_t slot0 = args.cu ? clamp64(args.cu[n], 0, args.T) / tokens + n : (int64_t)n * ((args.T + tokens - 1) / tokens);
+    const int segs = (s.len + tokens - 1) / tokens;
+    if (segs <= 1 || first_at(n) != place) return;  // (whole)
+    const int64_t slot0 = cut_state0(args.cu, n, args.T, tokens), pair = (int64_t)n * args.HV + hv;
     const float g = args.decay ? args.decay[hv] : 0.f;
     // tokens of a segment in the order of processing: against time the first has the sequence's odd end
     const int odd = (s.len + kC - 1) / kC * kC - s.len;
     float x[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = p.x0 ? p.x0[(int64_t)pair * D * D + (p.x_t ? ((at + e) % D) * D + at / D : at + e)] : 0.f;
+    for (int e = 0; e < 4; ++e) x[e] = p.x0 ? p.x0[pair * D * D + (p.x_t ? ((at + e) % D) * D + at / D : at + e)] : 0.f;
     const int64_t step = (int64_t)args.HV * D * D;
-    float *buf = split.states + (((int64_t)blockIdx.y * split.slots + slot0) * args.HV + hv) * D * D + at;
+    float *buf = split.held + (((int64_t)blockIdx.y * split.states + slot0) * args.HV + hv) * D * D + at;
     const Decayed first(g, tokens - (p.reverse ? odd + 1 : 0)), rest(g, tokens);
     for (int i = 0; i < segs; i += 8) {
         float4 add[8];
@@ -599,10 +603,10 @@ cudaError_t launch(const LinArgs &a, void *ws, int64_t tokens, cudaStream_t st)
     }
     const LinPlan plan = lin_tc_plan(a, D);
     Split split{};
-    split.slots = plan.slots;
+    split.states = plan.states;
     split.tokens = plan.tokens;
-    split.states = plan.bytes ? (float *)ws : nullptr;
-    int *const chosen = split.states && several(a) ? (int *)((char *)ws + plan.bytes - kChosenBytes) : nullptr;
+    split.held = plan.bytes ? (float *)ws : nullptr;
+    int *const chosen = split.held && several(a) ? (int *)((char *)ws + plan.bytes - kChosenBytes) : nullptr;
     split.chosen = chosen;
     static std::atomic<uint64_t> seen;
     if (first_on_device(seen)) {
@@ -611,17 +615,16 @@ cudaError_t launch(const LinArgs &a, void *ws, int64_t tokens, cudaStream_t st)
         if (e != cudaSuccess) return e;
         done_on_device(seen);
     }
-    const int64_t ctas = plan.slots * a.HV * (D / kCols) * a.passes, elements = (int64_t)a.N * a.HV * D * D;
-    if (ctas > INT32_MAX || elements / 1024 > INT32_MAX) return cudaErrorInvalidConfiguration;
-    const unsigned grid = (unsigned)ctas;
+    const int64_t each = (int64_t)a.HV * (D / kCols) * a.passes, joined = plan.places * a.HV * D * D / 1024;
+    if (plan.slots * each > INT32_MAX || plan.states * each > INT32_MAX || joined > INT32_MAX) return cudaErrorInvalidConfiguration;
     const int withhold = withhold_loads();
     const uint64_t limit = withhold ? kTestWaitLimitNs : kWaitLimitNs;
-    if (chosen) lin_choose_kernel<<<1, 512, 0, st>>>(a, plan.tokens, (float)(a.HV * (D / kCols) * a.passes) / (float)device_sm_count(), chosen);
-    if (split.states) {
-        lin_tc_kernel<D, true><<<grid, kThreads, Geo<D>::kSmem, st>>>(maps, a, split, limit, withhold);
-        lin_join_kernel<D><<<dim3((unsigned)(elements / 1024), a.passes), 256, 0, st>>>(a, split);
+    if (chosen) lin_choose_kernel<<<1, 512, 0, st>>>(a, plan.tokens, (float)each / (float)device_sm_count(), chosen);
+    if (split.held) {
+        lin_tc_kernel<D, true><<<(unsigned)(plan.states * each), kThreads, Geo<D>::kSmem, st>>>(maps, a, split, limit, withhold);
+        lin_join_kernel<D><<<dim3((unsigned)joined, a.passes), 256, 0, st>>>(a, split);
     }
-    lin_tc_kernel<D, false><<<grid, kThreads, Geo<D>::kSmem, st>>>(maps, a, split, limit, withhold);
+    lin_tc_kernel<D, false><<<(unsigned)(plan.slots * each), kThreads, Geo<D>::kSmem, st>>>(maps, a, split, limit, withhold);
     return cudaGetLastError();
 }
 
@@ -671,7 +674,9 @@ LinPlan lin_tc_plan(const LinArgs &a, int D)
     }
     p.tokens = (int)((each + best - 1) / best) * kC;
     p.slots = mix_slots(a.cu != nullptr, a.N, a.T, p.tokens);
-    p.bytes = (size_t)a.passes * p.slots * a.HV * D * D * sizeof(float) + (several(a) ? kChosenBytes : 0);
+    p.states = cut_states(a.cu != nullptr, a.N, a.T, p.tokens);
+    p.places = long_places(a.cu != nullptr, a.N, a.T, p.tokens);
+    p.bytes = (size_t)a.passes * p.states * a.HV * D * D * sizeof(float) + (several(a) ? kChosenBytes : 0);
     return p;
 }
 

@@ -29,20 +29,63 @@ __host__ __device__ inline int64_t mix_slots(bool packed, int N, int T, int tile
 struct Tile {
     int n, index;  // sequence, tile within it
 };
+// the last n below N with start(n) <= at, or 0 (start does not fall)
+template <typename F>
+__device__ __forceinline__ int last_from(int N, int64_t at, F start)
+{
+    int lo = 0, hi = N - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (start(mid) <= at) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+// tile i of sequence n; i outside what a sequence can have: one that is behind every end
+__device__ __forceinline__ Tile tile_at(int n, int64_t i, int tile)
+{
+    const int64_t past = max(INT32_MAX / tile - 1, 1);
+    return {n, (int)(i < 0 || i > past ? past : i)};
+}
 __device__ __forceinline__ Tile tile_of(const int64_t *cu, int N, int T, int tile, int64_t slot)
 {
     if (!cu) {
         const unsigned per = (unsigned)(T + tile - 1) / tile, n = (unsigned)slot / per;  // (slots of equal lengths are grid indices: 31 bits)
         return {(int)n, (int)((unsigned)slot - n * per)};
     }
-    int lo = 0, hi = N - 1;  // the last n whose first slot is not past this one
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (clamp64(cu[mid], 0, T) / tile + mid <= slot) lo = mid;
-        else hi = mid - 1;
-    }
-    const int64_t i = slot - (clamp64(cu[lo], 0, T) / tile + lo), past = INT32_MAX / tile - 1;
-    return {lo, (int)(i < 0 || i > past ? past : i)};  // (slots in front of the first sequence are empty too)
+    auto first = [&](int n) { return clamp64(cu[n], 0, T) / tile + n; };
+    const int n = last_from(N, slot, first);
+    return tile_at(n, slot - first(n), tile);  // (slots in front of the first sequence are empty too)
+}
+// Places for the sequences of `least` tokens or more alone: sequence n has min(n, floor(cu[n] / least)), so that no two of them share one and
+// floor(T / least) are enough whatever N is.  (Shorter ones' places are others' or nobody's.)  Equal lengths: n.
+__host__ __device__ inline int64_t long_places(bool packed, int N, int T, int least)
+{
+    return !packed ? (T >= least ? N : 0) : T / least < N ? T / least : N;
+}
+__device__ __forceinline__ int64_t long_place(const int64_t *cu, int n, int T, int least)
+{
+    if (!cu) return n;
+    const int64_t at = clamp64(cu[n], 0, T) / least;
+    return at < n ? at : n;
+}
+// The sequences that are cut, those longer than `tokens`, hold their segments' states one behind the other: sequence n from
+// floor(cu[n] / tokens) + its place on (a sequence of more than `tokens` has at most floor(len / tokens) + 1 segments).
+__host__ __device__ inline int64_t cut_states(bool packed, int N, int T, int tokens)
+{
+    return packed ? T / tokens + long_places(packed, N, T, tokens) : (int64_t)N * ((T + tokens - 1) / tokens);
+}
+__device__ __forceinline__ int64_t cut_state0(const int64_t *cu, int n, int T, int tokens)
+{
+    return cu ? clamp64(cu[n], 0, T) / tokens + long_place(cu, n, T, tokens) : (int64_t)n * ((T + tokens - 1) / tokens);
+}
+// The segment whose state is the at-th (of a sequence that is not cut, or behind its end, where there is none)
+__device__ __forceinline__ Tile cut_of(const int64_t *cu, int N, int T, int tokens, int64_t at)
+{
+    if (!cu) return tile_of(cu, N, T, tokens, at);
+    auto first = [&](int n) { return cut_state0(cu, n, T, tokens); };
+    const int n = last_from(N, at, first);
+    return tile_at(n, at - first(n), tokens);
 }
 
 // ---------------------------------------------------------------- linear attention
@@ -74,7 +117,8 @@ struct LinArgs {
 // are few; then `bytes` of workspace.
 struct LinPlan {
     size_t bytes;
-    int64_t slots;           // (sequence, segment) pairs
+    int64_t slots;           // (sequence, segment) pairs, some of them empty
+    int64_t states, places;  // segments' states held, and sequences that are cut, at most
     int tokens;              // of a segment
 };
 LinPlan lin_simt_plan(const LinArgs &a);

@@ -496,6 +496,21 @@ def test_linear_packed_split(gdn, H, HV, D):
                 ref.check_norm(a[:, piece], b[:, piece].double(), 2.0 ** -8, name)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("long", [[], [1900], [1500, 0, 700, 2600]])
+def test_linear_many_sequences(gdn, dtype, long):
+    """Hundreds of short and empty sequences, and between them none, one or a few that are longer than a segment."""
+    short = [int(x) for x in torch.randint(0, 40, (300,), generator=torch.Generator().manual_seed(len(long)))]
+    at = {40 + 80 * i: x for i, x in enumerate(long)}
+    lens = [at.get(i, x) for i, x in enumerate(short)]
+    case = (1, lens, 1, 2, 64, 64)
+    q, k, v, decay, h0, cu, g = linear_inputs(case, dtype, True, 7)
+    got = gdn.chunk_linear_attention(q, k, v, decay, initial_state=h0, output_final_state=True, cu_seqlens=cu)
+    check_linear(got, q, k, v, decay, 0.125, h0, cu, longest(case))
+    do, dht = randn(g, *v.shape, dtype=dtype), randn(g, *h0.shape)
+    check_linear_bwd(gdn, q, k, v, decay, do, 0.125, h0, dht, cu, longest(case))
+
+
 @pytest.mark.parametrize("window,sinks", [(100, 600), (2 ** 31 - 1, 2 ** 31 - 1), (2000, 0), (1, 1499)])
 def test_window_many_sinks(gdn, window, sinks):
     """More sinks than are dealt out to CTAs of their own, and windows longer than the sequence."""

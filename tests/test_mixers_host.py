@@ -161,6 +161,25 @@ def test_workspaces(L):
     assert L.gdn_window_attn_bwd(ctypes.byref(w), at(30), need - 1, None) == WORKSPACE
 
 
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("backward", [False, True])
+@pytest.mark.parametrize("heads", [1, 32])
+def test_linear_workspace_of_many_sequences(L, dtype, backward, heads):
+    """States are held for the segments of sequences that are cut: of T tokens, whatever the lengths, at most twice as many as one sequence of
+    all tokens has."""
+    size = L.gdn_linear_attn_bwd_workspace_size if backward else L.gdn_linear_attn_workspace_size
+
+    def need(n):
+        return size(ctypes.byref(linear_args(B=1, T=65536, H=heads, HV=heads, K=128, V=128, num_seqs=n, dtype=dtype, cu_seqlens=at(20000), ldq=heads * 128,
+                                             ldk=heads * 128, ldv=heads * 128, ld_dout=heads * 128,
+                                             **{k: at(1000 * i) for i, k in enumerate(("q", "k", "v", "o", "dout", "dq", "dk", "dv", "h0", "ht", "dht", "dh0", "decay"))})))
+
+    one = need(1)
+    assert one > 0 or heads > 1  # (many heads fill the GPU with whole sequences)
+    for n in (1024, 4096, 65536):
+        assert (need(n) > 0) == (one > 0) and need(n) <= 2 * one + 256
+
+
 def test_binding_refuses_host_tensors(gdn):
     t, s, n = torch.zeros(1, 4, 2, 64), torch.zeros(1, 2, 64, 64), torch.zeros(1, dtype=torch.int32)
     for call in (lambda: gdn.chunk_linear_attention(t, t, t), lambda: gdn.fused_recurrent_linear_attention(t, t, t, initial_state=s),
