@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(256) lin_join_kernel(const LinArgs args, const
     const int which = (int)(blockIdx.x / kPieces), at = (int)(blockIdx.x % kPieces) * 1024 + 4 * threadIdx.x, tokens = split.segment();
     const int place = which / args.HV, hv = which - place * args.HV;
     auto first_at = [&](int n) { return long_place(args.cu, n, args.T, tokens); };
-    const int n = args.cu ? last_from(args.N, place, first_at) : place;
+    const int n = args.cu ? last_from_warp(args.N, place, first_at) : place;
     const SeqRange s = seq_range(args.cu, n, args.T);
     const int segs = (s.len + tokens - 1) / tokens;
     if (segs <= 1 || first_at(n) != place) return;  // (whole)

@@ -41,6 +41,22 @@ __device__ __forceinline__ int last_from(int N, int64_t at, F start)
     }
     return lo;
 }
+// The same by a whole warp, 32 of them at a time: where every warp of many CTAs looks a sequence up (each step of the other waits for memory:
+// the join of the sinks' gradients of 200 sequences took 130 us more with it)
+template <typename F>
+__device__ __forceinline__ int last_from_warp(int N, int64_t at, F start)
+{
+    const int lane = threadIdx.x & 31;
+    int lo = 0;
+    for (int left = N; left > 1;) {
+        const int step = (left + 31) / 32, i = lane * step;
+        const unsigned below = __ballot_sync(0xffffffffu, i == 0 || (i < left && start(lo + i) <= at));
+        const int k = 31 - __clz(below);
+        lo += k * step;
+        left = min(step, left - k * step);
+    }
+    return lo;
+}
 // tile i of sequence n; i outside what a sequence can have: one that is behind every end
 __device__ __forceinline__ Tile tile_at(int n, int64_t i, int tile)
 {
@@ -53,7 +69,7 @@ __device__ __forceinline__ Tile tile_of(const int64_t *cu, int N, int T, int til
         const unsigned per = (unsigned)(T + tile - 1) / tile, n = (unsigned)slot / per;  // (slots of equal lengths are grid indices: 31 bits)
         return {(int)n, (int)((unsigned)slot - n * per)};
     }
-    auto first = [&](int n) { return clamp64(cu[n], 0, T) / tile + n; };
+    auto first = [&](int n) { return (int64_t)((unsigned)clamp64(cu[n], 0, T) / (unsigned)tile) + n; };
     const int n = last_from(N, slot, first);
     return tile_at(n, slot - first(n), tile);  // (slots in front of the first sequence are empty too)
 }
@@ -66,8 +82,7 @@ __host__ __device__ inline int64_t long_places(bool packed, int N, int T, int le
 __device__ __forceinline__ int64_t long_place(const int64_t *cu, int n, int T, int least)
 {
     if (!cu) return n;
-    const int64_t at = clamp64(cu[n], 0, T) / least;
-    return at < n ? at : n;
+    return min((int)((unsigned)clamp64(cu[n], 0, T) / (unsigned)least), n);
 }
 // The sequences that are cut, those longer than `tokens`, hold their segments' states one behind the other: sequence n from
 // floor(cu[n] / tokens) + its place on (a sequence of more than `tokens` has at most floor(len / tokens) + 1 segments).
@@ -77,7 +92,7 @@ __host__ __device__ inline int64_t cut_states(bool packed, int N, int T, int tok
 }
 __device__ __forceinline__ int64_t cut_state0(const int64_t *cu, int n, int T, int tokens)
 {
-    return cu ? clamp64(cu[n], 0, T) / tokens + long_place(cu, n, T, tokens) : (int64_t)n * ((T + tokens - 1) / tokens);
+    return cu ? (int64_t)((unsigned)clamp64(cu[n], 0, T) / (unsigned)tokens) + long_place(cu, n, T, tokens) : (int64_t)n * ((T + tokens - 1) / tokens);
 }
 // The segment whose state is the at-th (of a sequence that is not cut, or behind its end, where there is none)
 __device__ __forceinline__ Tile cut_of(const int64_t *cu, int N, int T, int tokens, int64_t at)
@@ -188,11 +203,23 @@ __host__ __device__ inline int64_t lse_at(const WinArgs &a, int n, int64_t bos, 
 }
 // Keys that are sinks are seen by every query behind them.  Where the window does not reach, the queries of a tile of sinks are dealt out
 // to CTAs of their own, `run` queries each, whose fp32 parts of dK and dV a join adds to the tile's in order: one CTA for all of them would
-// walk the whole sequence while the others see a window.
+// walk the whole sequence while the others see a window.  Sequences of fewer than `least` keys, whose sinks have few far queries, stay with their
+// tiles' CTAs and have no place here, so that the parts are at most 2 + sinks / run times what dK and dV would take in fp32, however many sequences
+// there are.  Few: none behind the tiles of sinks, or half a run where key tiles fill the GPU four times over and a CTA's longer walk costs less
+// than the parts' way through memory (bf16, 8 heads over 4 of 128, 4 sinks, dealt out and not: 200 x 300 tokens, window 128 661 us and 501; one
+// sequence of 1660, window 1024 103 and 123).
 struct WinSinks {
-    float *own, *parts;  // [N][HK][tiles][2][tile][D] of the tiles' own CTAs, [slots][HK][tiles][2][tile][D] of the runs
-    int tiles;           // tiles of sinks whose far queries are dealt out; 0: none
-    int64_t slots;       // runs of all sequences
+    float *own, *parts;     // [places][HK][tiles][2][tile][D] of the tiles' own CTAs, [slots][HK][tiles][2][tile][D] of the runs
+    int tiles;              // tiles of sinks whose far queries are dealt out; 0: none
+    int least;
+    int64_t places, slots;  // of sequences that are dealt out, of their runs
+    __device__ __forceinline__ bool deals(const SeqRange &sq, const SeqRange &sk) const { return tiles > 0 && sq.len > 0 && sk.len >= least; }
+    __device__ __forceinline__ int64_t place(const WinArgs &a, int n) const { return long_place(a.cu_k, n, a.Tk, least); }
+    // the first run of a sequence that is dealt out
+    __device__ __forceinline__ int64_t slot0(const WinArgs &a, int n, int run) const
+    {
+        return a.cu_q ? (int64_t)((unsigned)clamp64(a.cu_q[n], 0, a.Tq) / (unsigned)run) + place(a, n) : (int64_t)n * ((a.Tq + run - 1) / run);
+    }
 };
 inline WinSinks win_sinks_plan(const WinArgs &a, int tile, int run, int most, void *ws, size_t *bytes)
 {
@@ -200,12 +227,17 @@ inline WinSinks win_sinks_plan(const WinArgs &a, int tile, int run, int most, vo
     const int tiles = (a.sinks + tile - 1) / tile;
     *bytes = 0;
     if (a.window >= a.Tk || tiles > most || tiles == 0) return s;
+    const bool packed = a.cu_q != nullptr;
+    const bool full = (packed ? 1 : (int64_t)a.N) * a.Tk / tile * a.HK >= 4 * (int64_t)device_sm_count();
+    s.least = a.window + tiles * tile + (full ? run / 2 : 0);
+    s.places = long_places(packed, a.N, a.Tk, s.least);
+    if (s.places == 0) return s;
     s.tiles = tiles;
-    s.slots = mix_slots(a.cu_q != nullptr, a.N, a.Tq, run);
+    s.slots = packed ? a.Tq / run + s.places : (int64_t)a.N * ((a.Tq + run - 1) / run);
     const int64_t each = (int64_t)a.HK * tiles * 2 * tile * a.D;
     s.own = (float *)ws;
-    s.parts = s.own + a.N * each;
-    *bytes = (size_t)(a.N + s.slots) * each * sizeof(float);
+    s.parts = s.own + s.places * each;
+    *bytes = (size_t)(s.places + s.slots) * each * sizeof(float);
     return s;
 }
 // What a CTA of dK and dV sums: a tile of keys against queries begin .. end of each head
@@ -217,7 +249,15 @@ struct WinKeyTile {
     {
         const bool far = item >= key_tiles;  // a run of queries against a tile of sinks
         if (far) item -= key_tiles;
-        const Tile tl = far ? tile_of(a.cu_q, a.N, a.Tq, run, item / s.tiles) : tile_of(a.cu_k, a.N, a.Tk, tile, item);
+        const int64_t slot = far ? item / s.tiles : 0;
+        Tile tl;
+        if (far && a.cu_q) {
+            auto first = [&](int n) { return s.slot0(a, n, run); };
+            const int last = last_from_warp(a.N, slot, first);
+            tl = tile_at(last, slot - first(last), run);
+        } else {
+            tl = far ? tile_of(nullptr, a.N, a.Tq, run, slot) : tile_of(a.cu_k, a.N, a.Tk, tile, item);
+        }
         n = tl.n;
         sq = seq_range(a.cu_q, n, a.Tq);
         sk = seq_range(a.cu_k, n, a.Tk);
@@ -227,20 +267,27 @@ struct WinKeyTile {
         off = sk.len - sq.len;
         begin = max(0, j0 - off);
         end = (int)clamp64((int64_t)j0 + cols - 1 + a.window - off, 0, sq.len);  // the last (exclusive) that sees a key through the window
-        const bool dealt = !far && st < s.tiles;
+        const bool dealt = !far && st < s.tiles && s.deals(sq, sk);
         if (far) {
             begin = max(max(begin, end), tl.index * run);
             end = (int)min((int64_t)sq.len, (int64_t)(tl.index + 1) * run);
-            if (begin >= end) cols = 0;  // (nothing to do)
+            if (begin >= end || !s.deals(sq, sk)) cols = 0;  // (nothing to do)
         } else if (!dealt && j0 < a.sinks) {
             end = sq.len;
         }
         const int64_t size = (int64_t)2 * tile * a.D;
-        part = far ? s.parts + ((item / s.tiles * a.HK + hk) * s.tiles + st) * size : dealt ? s.own + (((int64_t)n * a.HK + hk) * s.tiles + st) * size : nullptr;
+        part = far ? s.parts + ((slot * a.HK + hk) * s.tiles + st) * size : dealt ? s.own + ((s.place(a, n) * a.HK + hk) * s.tiles + st) * size : nullptr;
     }
 };
 __device__ __forceinline__ float added(float x, float y) { return x + y; }
 __device__ __forceinline__ float4 added(float4 x, float4 y) { return make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w); }
+// The sequence that is dealt out at a place, or -1 (by whole warps)
+__device__ __forceinline__ int win_sinks_at(const WinArgs &a, const WinSinks &s, int64_t place)
+{
+    auto first = [&](int n) { return s.place(a, n); };
+    const int n = a.cu_q ? last_from_warp(a.N, place, first) : (int)place;
+    return first(n) == place && s.deals(seq_range(a.cu_q, n, a.Tq), seq_range(a.cu_k, n, a.Tk)) ? n : -1;
+}
 // what stands at `at` in the parts [2][tile][D] of a tile of sinks, added up in order (F: one element, or four)
 template <typename F>
 __device__ __forceinline__ F win_sinks_sum(const WinArgs &a, const WinSinks &s, int tile, int run, int n, int hk, int st, int64_t at)
@@ -248,8 +295,8 @@ __device__ __forceinline__ F win_sinks_sum(const WinArgs &a, const WinSinks &s, 
     const SeqRange sq = seq_range(a.cu_q, n, a.Tq), sk = seq_range(a.cu_k, n, a.Tk);
     const int j0 = st * tile, cols = min(tile, sk.len - j0), off = sk.len - sq.len;
     const int from = max(max(0, j0 - off), (int)clamp64((int64_t)j0 + cols - 1 + a.window - off, 0, sq.len));  // the first query of a run
-    const int64_t slot0 = a.cu_q ? clamp64(a.cu_q[n], 0, a.Tq) / run + n : (int64_t)n * ((a.Tq + run - 1) / run), size = (int64_t)2 * tile * a.D;
-    F x = *(const F *)(s.own + (((int64_t)n * a.HK + hk) * s.tiles + st) * size + at);
+    const int64_t slot0 = s.slot0(a, n, run), size = (int64_t)2 * tile * a.D;
+    F x = *(const F *)(s.own + ((s.place(a, n) * a.HK + hk) * s.tiles + st) * size + at);
     for (int i = from / run; from < sq.len && i * run < sq.len; ++i) x = added(x, *(const F *)(s.parts + (((slot0 + i) * a.HK + hk) * s.tiles + st) * size + at));
     return x;
 }

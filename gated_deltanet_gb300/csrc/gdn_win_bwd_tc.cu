@@ -714,7 +714,8 @@ template <int D>
 __global__ void __launch_bounds__(256) win_sinks_kernel(const WinArgs a, const WinSinks s)
 {
     const int which = blockIdx.z, st = blockIdx.y % s.tiles, hk = blockIdx.y / s.tiles;
-    const int n = blockIdx.x / (kTile * D / 1024), e = (blockIdx.x % (kTile * D / 1024)) * 1024 + threadIdx.x * 4, r = st * kTile + e / D;
+    const int n = win_sinks_at(a, s, blockIdx.x / (kTile * D / 1024)), e = (blockIdx.x % (kTile * D / 1024)) * 1024 + threadIdx.x * 4, r = st * kTile + e / D;
+    if (n < 0) return;
     const SeqRange sk = seq_range(a.cu_k, n, a.Tk);
     if (r >= sk.len) return;
     const float4 x = win_sinks_sum<float4>(a, s, kTile, kSinkRun, n, hk, st, (int64_t)which * kTile * D + e);
@@ -744,12 +745,12 @@ cudaError_t launch(const WinArgs &a, int64_t tq, int64_t tk, float *delta, void 
     const WinSinks s = win_sinks_plan(a, kTile, kSinkRun, kMostSinkTiles, ws, &bytes);
     const int64_t qt = mix_slots(a.cu_q != nullptr, a.N, a.Tq, kTile), kt = mix_slots(a.cu_k != nullptr, a.N, a.Tk, kTile);
     const int64_t ctas = kt + s.slots * s.tiles;
-    if (qt * a.H > INT32_MAX || ctas > INT32_MAX || (int64_t)a.N * kTile * D / 1024 > INT32_MAX) return cudaErrorInvalidConfiguration;
+    if (qt * a.H > INT32_MAX || ctas > INT32_MAX || s.places * kTile * D / 1024 > INT32_MAX) return cudaErrorInvalidConfiguration;
     const int withhold = withhold_loads();
     const uint64_t limit = withhold ? kTestWaitLimitNs : kWaitLimitNs;
     win_dq_kernel<D><<<(unsigned)std::min<int64_t>(qt * a.H, device_sm_count()), kThreads, smem, st>>>(maps, a, (unsigned)(qt * a.H), delta, limit, withhold);
     win_dkv_kernel<D><<<dim3((unsigned)ctas, a.HK), kThreads, smem, st>>>(maps, a, s, kt, limit, withhold);
-    if (s.tiles > 0) win_sinks_kernel<D><<<dim3((unsigned)(a.N * (kTile * D / 1024)), a.HK * s.tiles, 2), 256, 0, st>>>(a, s);
+    if (s.tiles > 0) win_sinks_kernel<D><<<dim3((unsigned)(s.places * (kTile * D / 1024)), a.HK * s.tiles, 2), 256, 0, st>>>(a, s);
     return cudaGetLastError();
 }
 

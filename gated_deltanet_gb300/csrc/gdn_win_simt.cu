@@ -303,10 +303,11 @@ template <typename T, int TILE>
 __global__ void __launch_bounds__(kThreads) win_sinks_kernel(const WinArgs a, const WinSinks s, int64_t count)
 {
     const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (i >= count) return;
+    if (i >= count) return;  // (a warp has one tile: they are multiples of 64)
     const int size = 2 * TILE * a.D, at = (int)(i % size), which = at / (TILE * a.D), e = at % (TILE * a.D), r0 = e / a.D;
     const int64_t tile = i / size;
-    const int st = (int)(tile % s.tiles), hk = (int)(tile / s.tiles % a.HK), n = (int)(tile / s.tiles / a.HK), r = st * TILE + r0;
+    const int st = (int)(tile % s.tiles), hk = (int)(tile / s.tiles % a.HK), n = win_sinks_at(a, s, tile / s.tiles / a.HK), r = st * TILE + r0;
+    if (n < 0) return;
     const SeqRange sk = seq_range(a.cu_k, n, a.Tk);
     if (r >= sk.len) return;
     ((T *)(which ? a.dv : a.dk))[((sk.bos + r) * a.HK + hk) * a.D + e % a.D] = from_f<T>(win_sinks_sum<float>(a, s, TILE, kSinkRun, n, hk, st, at));
@@ -346,7 +347,7 @@ cudaError_t launch_keys(const WinArgs &a, void *ws, cudaStream_t st)
     size_t bytes;
     const WinSinks s = win_sinks_plan(a, TILE, kSinkRun, kMostSinks / TILE, ws, &bytes);
     const int64_t tiles = mix_slots(a.cu_k != nullptr, a.N, a.Tk, TILE), ctas = tiles + s.slots * s.tiles;
-    const int64_t count = (int64_t)a.N * a.HK * s.tiles * 2 * TILE * a.D, blocks = (count + kThreads - 1) / kThreads;
+    const int64_t count = s.places * a.HK * s.tiles * 2 * TILE * a.D, blocks = (count + kThreads - 1) / kThreads;
     if (ctas > INT32_MAX || blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
     if (tiles == 0) return cudaSuccess;
     kern<<<dim3((unsigned)ctas, a.HK), kThreads, smem, st>>>(a, s, tiles);

@@ -253,6 +253,36 @@ def test_window_bwd(gdn, case, dtype):
     check_window_bwd(gdn, q, k, v, randn(g, *q.shape, dtype=dtype), w, sinks, q.shape[3] ** -0.5, cu, cu_k)
 
 
+@pytest.mark.parametrize("case", [
+    # several runs of far queries to a tile of sinks, one tile of them and more
+    (2, 2600, None, 2, 1, 128, 100, 4), (1, 3000, None, 2, 2, 64, 100, 300), (1, 2500, None, 2, 1, 128, 1, 512), (2, 1200, 2300, 2, 1, 64, 333, 130),
+    # sequences of several runs next to short and empty ones, keys packed otherwise than queries
+    (1, [1100, 2300, 0, 40, 1500], None, 2, 1, 128, 100, 4), (1, [1100, 40, 2300, 5], [1500, 900, 1200, 0], 2, 1, 64, 60, 130), (1, [3, 0, 1500, 7], [900, 1300, 2600, 2], 1, 1, 128, 90, 2),
+    # lengths next to those from which on sinks are dealt out: window, sinks in tiles of 32, 64 or 128, in large batches half a run of 256 or 1024
+    (1, [131, 132, 133, 163, 164, 165, 227, 228, 229, 357], None, 2, 1, 64, 100, 4), (1, [259, 260, 261, 291, 292, 293, 355, 356, 357, 500], None, 1, 1, 128, 100, 130),
+    (1, [740, 739, 741, 260, 259, 261, 291, 292, 293, 60] * 5, None, 4, 4, 64, 100, 4),
+], ids=str)
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_window_bwd_far_queries(gdn, case, dtype):
+    q, k, v, w, sinks, cu, cu_k, g = window_inputs(case, dtype, 5)
+    check_window_bwd(gdn, q, k, v, randn(g, *q.shape, dtype=dtype), w, sinks, q.shape[3] ** -0.5, cu, cu_k)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("long", [[], [1900], [1300, 0, 300, 2200]])
+def test_window_many_sequences(gdn, dtype, long):
+    """Hundreds of short and empty sequences, and between them none, one or a few that are longer than the window and the sinks."""
+    short = [int(x) for x in torch.randint(0, 40, (200,), generator=torch.Generator().manual_seed(len(long)))]
+    at = {20 + 50 * i: x for i, x in enumerate(long)}
+    lens = [at.get(i, x) for i, x in enumerate(short)]
+    q, k, v, w, sinks, cu, _, g = window_inputs((1, lens, None, 2, 1, 64, 50, 3), dtype, 6)
+    o, lse = gdn.window_attention(q, k, v, w, sinks, cu_seqlens=cu, return_lse=True)
+    eo, el, bo, bl = ref.window(q, k, v, w, sinks, 0.125, cu)
+    ref.check(o, eo, bo, "o")
+    ref.check(lse, el, bl, "lse")
+    check_window_bwd(gdn, q, k, v, randn(g, *q.shape, dtype=dtype), w, sinks, 0.125, cu, None)
+
+
 def test_window_bwd_against_differences(gdn):
     """fp32: the slope of sum(o do) along a direction.  Step 2^-7: the second-order term is below 1e-3 of the gradients' size, the
     sums' rounding over the step too."""

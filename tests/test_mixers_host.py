@@ -180,6 +180,23 @@ def test_linear_workspace_of_many_sequences(L, dtype, backward, heads):
         assert (need(n) > 0) == (one > 0) and need(n) <= 2 * one + 256
 
 
+@pytest.mark.parametrize("dtype,most", [(0, 4), (1, 2.5)])
+@pytest.mark.parametrize("window", [1, 128, 1024])
+@pytest.mark.parametrize("sinks", [4, 300, 512])
+def test_window_workspace_of_many_sequences(L, dtype, most, window, sinks):
+    """fp32 parts of the sinks' gradients: of T tokens, whatever the lengths, two for each long sequence's sinks and one for each run of its queries
+    (256 on the CUDA cores, 1024 on the tensor cores), to 512 sinks at most: 2 + 512 / 256 or 2 + 512 / 1024 times dK and dV in fp32."""
+    T, heads, D = 65536, 16, 128
+
+    def need(n):
+        return L.gdn_window_attn_bwd_workspace_size(ctypes.byref(window_args(
+            B=1, Tq=T, Tk=T, H=heads, HK=heads, D=D, num_seqs=n, dtype=dtype, window=window, sinks=sinks, cu_seqlens_q=at(200), cu_seqlens_k=at(201), ldq=heads * D,
+            ldk=heads * D, ldv=heads * D, ld_dout=heads * D, **{k: at(10 * i) for i, k in enumerate(("q", "k", "v", "o", "lse", "dout", "dq", "dk", "dv"))})))
+
+    for n in (1, 1024, 4096, 65536):
+        assert 0 < need(n) <= T * heads * 4 + most * 2 * T * heads * D * 4
+
+
 def test_binding_refuses_host_tensors(gdn):
     t, s, n = torch.zeros(1, 4, 2, 64), torch.zeros(1, 2, 64, 64), torch.zeros(1, dtype=torch.int32)
     for call in (lambda: gdn.chunk_linear_attention(t, t, t), lambda: gdn.fused_recurrent_linear_attention(t, t, t, initial_state=s),
