@@ -29,6 +29,9 @@ struct Split {
     int tokens;     // of a segment (a multiple of kC)
     int64_t slots, states;
     size_t pass;    // elements of a pass
+    const int *chosen;  // several packed sequences: the segment that lin_choose_kernel took (`tokens` at least), and whether a sequence is longer
+    __device__ int segment() const { return chosen ? *chosen : tokens; }
+    __device__ bool none() const { return chosen && !chosen[1]; }  // no sequence is cut
 };
 
 // W: a, b columns at most.  STATE: only what a segment adds to the state, from zero.
@@ -38,14 +41,15 @@ __global__ void __launch_bounds__(kThreads) lin_simt_kernel(const LinArgs args, 
     extern __shared__ float4 lin_smem[];
     const LinPass &p = args.pass[blockIdx.y];
     const int nct = (p.dc + kBV - 1) / kBV;
-    if (blockIdx.x >= (STATE ? split.states : split.slots) * args.HV * nct) return;
+    if (blockIdx.x >= (STATE ? split.states : split.slots) * args.HV * nct || (STATE && split.none())) return;
     const int ct = (int)(blockIdx.x % nct), hv = (int)(blockIdx.x / nct % args.HV);
     const int64_t slot = blockIdx.x / ((int64_t)nct * args.HV);
-    const Tile tl = !split.held ? Tile{(int)slot, 0} : STATE ? cut_of(args.cu, args.N, args.T, split.tokens, slot) : tile_of(args.cu, args.N, args.T, split.tokens, slot);
+    const int tokens = split.segment();
+    const Tile tl = !split.held ? Tile{(int)slot, 0} : STATE ? cut_of(args.cu, args.N, args.T, tokens, slot) : tile_of(args.cu, args.N, args.T, tokens, slot);
     const int n = tl.n;
     const SeqRange s = seq_range(args.cu, n, args.T);
     // the segment, in the order of processing
-    const int chunks = (s.len + kC - 1) / kC, per = split.held ? split.tokens / kC : chunks;
+    const int chunks = (s.len + kC - 1) / kC, per = split.held ? tokens / kC : chunks;
     const int m0 = (int)min((int64_t)tl.index * per, (int64_t)chunks), m1 = (int)min((int64_t)m0 + per, (int64_t)chunks);
     const bool last = m1 == chunks, cut = chunks > per;
     if (STATE ? !cut || last : tl.index > 0 && m0 >= m1) return;
@@ -58,7 +62,7 @@ __global__ void __launch_bounds__(kThreads) lin_simt_kernel(const LinArgs args, 
     if (tid <= kC) pw[tid] = decay_pow(g * kRcpLn2, tid);
     const int64_t xbase = ((int64_t)n * args.HV + hv) * da * p.dc;
     auto xat = [&](int r, int c) { return xbase + (p.x_t ? (int64_t)(c0 + c) * da + r : (int64_t)r * p.dc + c0 + c); };
-    const int64_t at = cut ? cut_state0(args.cu, n, args.T, split.tokens) + tl.index : 0;
+    const int64_t at = cut ? cut_state0(args.cu, n, args.T, tokens) + tl.index : 0;
     float *const mine = cut ? split.held + blockIdx.y * split.pass + (at * args.HV + hv) * da * p.dc + c0 : nullptr;
 
     float x[W / 32][4];
@@ -181,21 +185,22 @@ __global__ void __launch_bounds__(kThreads) lin_simt_kernel(const LinArgs args, 
 // What the segments add to the state -> the state that enters each (in place), an element to a thread
 __global__ void __launch_bounds__(kThreads) lin_join_kernel(const LinArgs args, const Split split)
 {
+    if (split.none()) return;
     const LinPass &p = args.pass[blockIdx.y];
-    const int size = p.da * p.dc;
+    const int size = p.da * p.dc, tokens = split.segment();
     const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x, which = i / size, place = which / args.HV;
-    if (place >= long_places(args.cu != nullptr, args.N, args.T, split.tokens)) return;
+    if (place >= long_places(args.cu != nullptr, args.N, args.T, tokens)) return;
     const int at = (int)(i - which * size), hv = (int)(which - place * args.HV);
-    auto first_at = [&](int n) { return long_place(args.cu, n, args.T, split.tokens); };
+    auto first_at = [&](int n) { return long_place(args.cu, n, args.T, tokens); };
     const int n = args.cu ? last_from(args.N, place, first_at) : (int)place;
     const SeqRange s = seq_range(args.cu, n, args.T);
-    const int segs = (s.len + split.tokens - 1) / split.tokens;
+    const int segs = (s.len + tokens - 1) / tokens;
     if (segs <= 1 || first_at(n) != place) return;  // (whole)
-    const int64_t slot0 = cut_state0(args.cu, n, args.T, split.tokens), pair = (int64_t)n * args.HV + hv;
+    const int64_t slot0 = cut_state0(args.cu, n, args.T, tokens), pair = (int64_t)n * args.HV + hv;
     const float g = args.decay ? args.decay[hv] : 0.f;
     // tokens of a segment in the order of processing: against time the first has the sequence's odd end, and X0 enters one step later
     const int odd = (s.len + kC - 1) / kC * kC - s.len;
-    const Decayed first(g, split.tokens - (p.reverse ? odd + 1 : 0)), rest(g, split.tokens);
+    const Decayed first(g, tokens - (p.reverse ? odd + 1 : 0)), rest(g, tokens);
     float x = p.x0 ? p.x0[pair * size + (p.x_t ? at % p.dc * p.da + at / p.dc : at)] : 0.f;
     float *buf = split.held + blockIdx.y * split.pass + (slot0 * args.HV + hv) * size + at;
     for (int k = 0; k < segs; ++k) {
@@ -203,6 +208,39 @@ __global__ void __launch_bounds__(kThreads) lin_join_kernel(const LinArgs args, 
         const float add = k + 1 < segs ? *here : 0.f;
         *here = x;
         x = (k == 0 ? first(x) : rest(x)) + add;
+    }
+}
+
+// The segment of several packed sequences, from their lengths: lin_simt_plan's rule with the longest one's chunks, and as many sequences as that
+// makes of all chunks, in the place of one sequence of all tokens
+__global__ void __launch_bounds__(kThreads) lin_choose_kernel(const LinArgs args, int tokens, int64_t ctas, int64_t room, int *chosen)
+{
+    __shared__ long long all[kThreads / 32];
+    __shared__ int most[kThreads / 32];
+    long long sum = 0;
+    int longest = 0;
+    for (int n = threadIdx.x; n < args.N; n += kThreads) {
+        const int chunks = (seq_range(args.cu, n, args.T).len + kC - 1) / kC;
+        sum += chunks;
+        longest = max(longest, chunks);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+    }
+    if ((threadIdx.x & 31) == 0) all[threadIdx.x >> 5] = sum, most[threadIdx.x >> 5] = longest;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < kThreads / 32; ++w) {
+            sum += all[w];
+            longest = max(longest, most[w]);
+        }
+        const int64_t segs = min(room * longest / max(ctas * (int64_t)sum, (int64_t)1), (int64_t)longest / 4);
+        // (not shorter than the plan's, whose grid and states it goes by)
+        const int each = max(segs < 3 ? longest : (int)((longest + segs - 1) / segs), tokens / kC);
+        chosen[0] = each * kC;
+        chosen[1] = longest > each;
     }
 }
 
@@ -250,20 +288,31 @@ cudaError_t heads(const float *part, const LinArgs &a, int64_t tokens, int H, in
     return cudaGetLastError();
 }
 
+// CTAs that walk a sequence, or a segment of one
+int64_t ctas_of(const LinArgs &a)
+{
+    int64_t ctas = 0;
+    for (int i = 0; i < a.passes; ++i) ctas += (int64_t)a.HV * ((a.pass[i].dc + kBV - 1) / kBV);
+    return ctas;
+}
+// the segments that each of n sequences of `chunks` chunks is cut into (lin_simt_plan); fewer than three: none
+int64_t segments(const LinArgs &a, int64_t n, int64_t chunks) { return std::min<int64_t>(4 * device_sm_count() / std::max<int64_t>(n * ctas_of(a), 1), chunks / 4); }
+// whether several packed sequences' segment is chosen on the device: where as many of one length would not be cut
+bool chooses(const LinArgs &a) { return a.cu && a.N > 1 && segments(a, a.N, (a.T + kC - 1) / kC / a.N) < 3; }
+
 }  // namespace
 
 LinPlan lin_simt_plan(const LinArgs &a)
 {
     // A split walks twice (the second time with outputs), so only as many segments as bring four CTAs to an SM, of four chunks at least, and
     // none where that is two.  The lengths of packed sequences are not known here: the segment is what one sequence of all tokens is cut into,
-    // shorter ones stay whole.  fp32, whole and cut: 2048 tokens of 8 heads of 64 608 us and 100, gradients 553 and 182; 4 x 2048 of 8 heads of
-    // 128 (four segments) 907 and 735; 4 x 4096 of 16 heads of 128 (two) 2181 and 2835; 300 tokens of 4 heads of 32, gradients (two) 64 and 70.
-    int64_t ctas = 0, size = 0;
-    for (int i = 0; i < a.passes; ++i) {
-        ctas += (int64_t)(a.cu ? 1 : a.N) * a.HV * ((a.pass[i].dc + kBV - 1) / kBV);
-        size = std::max(size, (int64_t)a.pass[i].da * a.pass[i].dc);
-    }
-    const int64_t each = (a.T + kC - 1) / kC, segs = std::min<int64_t>(4 * device_sm_count() / std::max<int64_t>(ctas, 1), each / 4);
+    // shorter ones stay whole.  Where as many sequences of one length would not be cut, lin_choose_kernel takes a longer segment, or none (8 x 8192
+    // tokens of 8 heads of 128, packed: 6007 us by the plan's segment, 4365; the call costs 6).  fp32, whole and cut: 2048 tokens of 8 heads of 64
+    // 608 us and 100, gradients 553 and 182; 4 x 2048 of 8 heads of 128 (four segments) 907 and 735; 4 x 4096 of 16 heads of 128 (two) 2181 and
+    // 2835; 300 tokens of 4 heads of 32, gradients (two) 64 and 70.
+    int64_t size = 0;
+    for (int i = 0; i < a.passes; ++i) size = std::max(size, (int64_t)a.pass[i].da * a.pass[i].dc);
+    const int64_t each = (a.T + kC - 1) / kC, segs = segments(a, a.cu ? 1 : a.N, each);
     LinPlan p{};
     p.slots = a.N;
     if (segs < 3) return p;
@@ -272,6 +321,7 @@ LinPlan lin_simt_plan(const LinArgs &a)
     p.states = cut_states(a.cu != nullptr, a.N, a.T, p.tokens);
     p.places = long_places(a.cu != nullptr, a.N, a.T, p.tokens);
     p.bytes = (size_t)a.passes * p.states * a.HV * size * sizeof(float);
+    p.bytes = ((p.bytes + 255) & ~(size_t)255) + (chooses(a) ? kChosenBytes : 0);
     return p;
 }
 
@@ -288,7 +338,12 @@ cudaError_t launch(const LinArgs &a, void *ws, cudaStream_t st)
     split.tokens = plan.tokens;
     split.slots = plan.slots;
     split.states = plan.states;
-    split.pass = plan.bytes / sizeof(float) / a.passes;
+    size_t held = plan.bytes;
+    if (plan.bytes && chooses(a)) {
+        held -= kChosenBytes;
+        split.chosen = (const int *)((const char *)ws + held);
+    }
+    split.pass = held / sizeof(float) / a.passes;
     for (int i = 0; i < a.passes; ++i) {
         const LinPass &p = a.pass[i];
         most = std::max(most, plan.slots * a.HV * ((p.dc + kBV - 1) / kBV));
@@ -306,6 +361,7 @@ cudaError_t launch(const LinArgs &a, void *ws, cudaStream_t st)
         if (e != cudaSuccess) return e;
         done_on_device(seen);
     }
+    if (split.chosen) lin_choose_kernel<<<1, kThreads, 0, st>>>(a, plan.tokens, ctas_of(a), 4 * device_sm_count(), const_cast<int *>(split.chosen));
     if (split.held) {
         lin_simt_kernel<T, W, true><<<dim3((unsigned)summed, a.passes), kThreads, smem, st>>>(a, split);
         lin_join_kernel<<<dim3((unsigned)joined, a.passes), kThreads, 0, st>>>(a, split);

@@ -51,7 +51,7 @@ struct Maps {
 };
 
 constexpr float kAgain = 1.6f, kLaunches = 8.f;  // a split's walk in walks, its further launches in chunks (lin_tc_plan)
-constexpr size_t kChosenBytes = 256;
+
 inline bool several(const LinArgs &a) { return a.cu && a.N > 1; }
 
 struct Split {

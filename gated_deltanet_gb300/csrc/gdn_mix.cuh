@@ -131,11 +131,12 @@ struct LinArgs {
 // bf16, all sizes 64 or all 128, rows on 16-byte boundaries: on the tensor cores.  A plan splits sequences into segments where there
 // are few; then `bytes` of workspace.
 struct LinPlan {
-    size_t bytes;
+    size_t bytes;            // of workspace, the last kChosenBytes of them for packed sequences' segment where that is chosen on the device
     int64_t slots;           // (sequence, segment) pairs, some of them empty
     int64_t states, places;  // segments' states held, and sequences that are cut, at most
     int tokens;              // of a segment
 };
+constexpr size_t kChosenBytes = 256;
 LinPlan lin_simt_plan(const LinArgs &a);
 cudaError_t launch_lin_simt(const LinArgs &a, gdn_dtype dt, void *ws, cudaStream_t st);
 bool lin_tc_ok(const LinArgs &a, int64_t tokens);

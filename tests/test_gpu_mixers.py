@@ -541,6 +541,18 @@ def test_linear_many_sequences(gdn, dtype, long):
     check_linear_bwd(gdn, q, k, v, decay, do, 0.125, h0, dht, cu, longest(case))
 
 
+@pytest.mark.parametrize("lens", [[2000, 1700, 3, 0, 1500], [900] * 8, [70] * 8], ids=str)
+def test_linear_packed_rule(gdn, lens):
+    """fp32, heads enough that several packed sequences' segment is chosen from their lengths: longer than what one sequence of all tokens would be
+    cut into (the forward of the first), none (its gradients, equal lengths)."""
+    case = (1, lens, 2, 24, 64, 64)
+    q, k, v, decay, h0, cu, g = linear_inputs(case, F32, True, 8)
+    got = gdn.chunk_linear_attention(q, k, v, decay, initial_state=h0, output_final_state=True, cu_seqlens=cu)
+    check_linear(got, q, k, v, decay, 0.125, h0, cu, longest(case))
+    do, dht = randn(g, *v.shape), randn(g, *h0.shape)
+    check_linear_bwd(gdn, q, k, v, decay, do, 0.125, h0, dht, cu, longest(case))
+
+
 @pytest.mark.parametrize("window,sinks", [(100, 600), (2 ** 31 - 1, 2 ** 31 - 1), (2000, 0), (1, 1499)])
 def test_window_many_sinks(gdn, window, sinks):
     """More sinks than are dealt out to CTAs of their own, and windows longer than the sequence."""
