@@ -1,23 +1,28 @@
 // Linear attention with a decay for each head on the tensor cores: bf16, heads of 64 or 128 (K = V), rows on 16-byte boundaries.
 //
 // One CTA per (sequence or segment of one, value head, 64 columns of c) walks chunks of 128 tokens; the state X (D x 64, fp32)
-// stays in tensor memory.  Per chunk of n tokens, forward in time, every product a tcgen05 MMA with M = 128:
+// stays in tensor memory, or in registers.  Per chunk of n tokens, forward in time, every product a tcgen05 MMA with M = 128:
 //   Z = a b^T                   (128 x 128)   Z_ij <- cs l^(i-j) Z_ij for j <= i, rounded to bf16 where it lies
 //   O1 = a X,  O2 = Z c         (128 x 64)    out_i = os (l^(i+1) O1_i + O2_i)
-//   X <- l^n X + b^T C          (D x 64)      C_j = cs l^(n-1-j) c_j as the sum of two bf16 values
+//   X <- l^n X + b^T C          (D x 64)      C_j = cs l^(n-1-j) c_j as the sum of two or three bf16 values
 // Against time the same with the powers counted from the chunk's other end.
-// X enters O1 rounded to bf16.  X itself takes C as hi + lo, 16 bits of it (one bf16 alone would put 2^-9 into a state that is returned
-// in fp32; the two leave it 2.4e-6 in the 2-norm), and b and c as they are.
+// X enters O1 rounded to bf16, and b and c go in as they are.  C:
+//  - Where a pass returns X (RETURNED; fp32) C goes into it as three bf16 values, 24 bits, and X is summed in registers: the accumulators begin at
+//    zero in each chunk, because the tensor cores cut off what a small product has below a large sum, chunk after chunk.  X is then off by 1e-7
+//    to 3e-7 of its 2-norm, as plain fp32 sums are.
+//  - Where only outputs in bf16 (or the fp32 parts of bf16 gradients) see X, C goes in as hi + lo, 16 bits of it, and X is the accumulators' sum, which
+//    leaves X 2.4e-6 of its 2-norm off, 2^-10 of the rounding with which it enters O1.
 //
 // Bound by shared memory: it gives the products about 80 bytes a cycle, so that one of 128 x 128 x 16 with both operands there takes
 // 104 cycles (64 for the arithmetic), 128 x 64 x 16 takes 76, with its left operand in tensor memory 46, and it serves the copies and
 // the warps beside them.  A chunk's products are 2640 cycles alone and about 3700 so; a chunk takes 4100.  Hence: hi and lo lie next to
 // each other and go in as one right operand of 128 columns (X is the sum of two accumulators); outputs go from registers to memory.
+// The third part is 608 cycles of products more and takes one of c's three stages.
+// 4 x 4096 tokens of 16 heads of 128 80 us, 94 with the states returned (92 with X in the accumulators, whose sums leave slow decays 1.3e-6 off).
 // A whole head to a CTA has the cheaper products (N = 128, X transposed, C in tensor memory) but half the CTAs and most of its
-// CUDA-core work on the chain from chunk to chunk: 138 us at 4 x 4096 tokens of 16 heads of 128 where this takes 80; C in three parts
-// (24 bits) 102.
+// CUDA-core work on the chain from chunk to chunk: 138 us where this took 80.
 //
-// Warps: 0 loads (TMA: two stages of a and b, three of c, which is done with later; zeroes the rows behind a sequence's end, which are
+// Warps: 0 loads (TMA: two stages of a and b, three (two) of c, which is done with later; zeroes the rows behind a sequence's end, which are
 // the next one's: 0 x NaN is NaN), 1 issues the products, 4-7 turn Z, 8-15 round and decay X, 16-19 write out, 20-27 scale and split c.
 // One warp of a role polls a barrier and the others wait for it at a named one, which takes no instructions (polled by every waiting
 // warp, 10 000 of a chunk's 24 500 instructions were polls).  Order of the products: X(m+1), O1(m), Z(m+1), O2(m); X is read, rounded
@@ -84,8 +89,8 @@ struct Part {
     __device__ int rows(int c) const { return min(kC, s.len - c * kC); }
 };
 
-// STATE: only what the segment adds to the state, from zero
-template <int D, bool STATE>
+// STATE: only what the segment adds to the state, from zero.  RETURNED: a pass returns its state (x1)
+template <int D, bool STATE, bool RETURNED>
 __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_constant__ Maps maps, const LinArgs args, const Split split, uint64_t limit, int withhold)
 {
     using G = Geo<D>;
@@ -156,8 +161,20 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     unsigned *const status = &g_lin_status;
     auto wait = [&](int b, uint32_t parity) { return mbar_wait(&bar[b], parity, status, kStatusTimeout, limit); };
     auto all = [&](bool ok) { return __all_sync(0xffffffffu, ok); };
+    // what goes into a state that is returned takes C's third part, which has the last of c's stages
+    const bool third = RETURNED && p.x1 && (STATE || last_seg);
+    const int ring = third ? kStagesC - 1 : kStagesC;
+    constexpr int kThird = G::kCs + (kStagesC - 1) * kBox;
     auto loaded = [&](int m) { return all(wait(kFull + m % kStages, (m / kStages) & 1)); };    // a and b
-    auto loaded_c = [&](int m) { return all(wait(kFullC + m % kStagesC, (m / kStagesC) & 1)); };
+    // c's stage of a chunk, and how often it has come round
+    struct {
+        int s = 0, round = 0;
+        __device__ __forceinline__ void next(int ring)
+        {
+            if (++s == ring) s = 0, ++round;
+        }
+    } at_c;
+    auto loaded_c = [&]() { return all(wait(kFullC + at_c.s, at_c.round & 1)); };
 
     if (warp == 0) {
         // ---------------------------------------------------------------- loads
@@ -189,8 +206,9 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
                 zero_tail(st + G::kB, G::kBoxes);
                 if (lane == 0) mbar_arrive(&bar[kFull + s]);
             }
-            const int sc = m % kStagesC;
-            if (m >= kStagesC && !(ok = all(wait(kEmptyC + sc, (m / kStagesC - 1) & 1)))) break;
+            const int sc = at_c.s;
+            if (at_c.round > 0 && !(ok = all(wait(kEmptyC + sc, (at_c.round - 1) & 1)))) break;
+            at_c.next(ring);
             landing = &bar[rows < kC ? (int)kLanded : kFullC + sc];
             if (elect_one_sync()) {
                 mbar_arrive_expect_tx(landing, kBox);
@@ -205,11 +223,11 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
         }
         // no copy outlives the CTA
         for (int i = max(0, m - kStages); i < m; ++i) wait(kFull + i % kStages, (i / kStages) & 1);
-        for (int i = max(0, m - kStagesC); i < m; ++i) wait(kFullC + i % kStagesC, (i / kStagesC) & 1);
+        for (int i = max(0, m - ring); i < m; ++i) wait(kFullC + i % ring, (i / ring) & 1);
     } else if (warp == 1) {
         // ---------------------------------------------------------------- products
-        const uint32_t idZ = idesc_bf16_f32(128, 128, 0, 0), idO = idesc_bf16_f32(128, kCols, 0, 1), idX = idesc_bf16_f32(128, 2 * kCols, 1, 1);
-        const uint64_t dX = sdesc_sw128(base + G::kXs, kBox, 1024), dC = sdesc_sw128(base + G::kParts, kBox, 1024);
+        const uint32_t idZ = idesc_bf16_f32(128, 128, 0, 0), idO = idesc_bf16_f32(128, kCols, 0, 1), idX = idesc_bf16_f32(128, 2 * kCols, 1, 1), idX3 = idesc_bf16_f32(128, kCols, 1, 1);
+        const uint64_t dX = sdesc_sw128(base + G::kXs, kBox, 1024), dC = sdesc_sw128(base + G::kParts, kBox, 1024), dC3 = sdesc_sw128(base + kThird, kBox, 1024);
         auto scores = [&](int m) {
             const uint32_t st = base + (m % kStages) * G::kStage, z = tmem + kZ + (m & 1) * 128;
             const uint64_t da = sdesc_sw128(st + G::kA, 16, 1024), db = sdesc_sw128(st + G::kB, 16, 1024);
@@ -226,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
         };
         bool ok = loaded(0);
         if (!STATE && ok) scores(0);
-        for (int m = 0; m < nm && ok; ++m) {
+        for (int m = 0; m < nm && ok; ++m, at_c.next(ring)) {
             const uint32_t st = base + (m % kStages) * G::kStage;
             if (STATE && !(ok = loaded(m))) break;
             if (!(ok = all(wait(kXB, m & 1) && wait(kCB, m & 1)))) break;
@@ -234,17 +252,21 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
             if (elect_one_sync()) {
                 const uint64_t db = sdesc_sw128(st + G::kB, kBox, 1024);
 #pragma unroll
-                for (int ks = 0; ks < kC / 16; ++ks) mma_ss(tmem + kX, db + ks * 128, dC + ks * 128, idX, 1u);
+                for (int ks = 0; ks < kC / 16; ++ks) mma_ss(tmem + kX, db + ks * 128, dC + ks * 128, idX, !RETURNED || ks > 0);
+                if (third) {
+#pragma unroll
+                    for (int ks = 0; ks < kC / 16; ++ks) mma_ss(tmem + kX + kCols, db + ks * 128, dC3 + ks * 128, idX3, 1u);
+                }
                 mma_commit(&bar[kXF]);
                 if (STATE) {
                     mma_commit(&bar[kEmpty + m % kStages]);
-                    mma_commit(&bar[kEmptyC + m % kStagesC]);
+                    mma_commit(&bar[kEmptyC + at_c.s]);
                 }
             }
             __syncwarp();
             if (!STATE) {
                 if (m > 0 && !(ok = all(wait(kOE, (m - 1) & 1)))) break;  // the last outputs have been read
-                const uint64_t da = sdesc_sw128(st + G::kA, 16, 1024), dc = sdesc_sw128(base + G::kCs + m % kStagesC * kBox, kBox, 1024);
+                const uint64_t da = sdesc_sw128(st + G::kA, 16, 1024), dc = sdesc_sw128(base + G::kCs + at_c.s * kBox, kBox, 1024);
                 tc_fence_after();
                 if (elect_one_sync()) {
 #pragma unroll
@@ -257,13 +279,13 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
                     if (!(ok = loaded(m + 1))) break;
                     scores(m + 1);
                 }
-                if (!(ok = all(wait(kZB + (m & 1), (m >> 1) & 1)) && loaded_c(m))) break;
+                if (!(ok = all(wait(kZB + (m & 1), (m >> 1) & 1)) && loaded_c())) break;
                 tc_fence_after();
                 if (elect_one_sync()) {
 #pragma unroll
                     for (int ks = 0; ks < kC / 16; ++ks) mma_ts(tmem + kO2, tmem + kZ + (m & 1) * 128 + ks * 8, dc + ks * 128, idO, ks > 0);
                     mma_commit(&bar[kOF]);
-                    mma_commit(&bar[kEmptyC + m % kStagesC]);
+                    mma_commit(&bar[kEmptyC + at_c.s]);
                 }
                 __syncwarp();
             }
@@ -355,15 +377,27 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
                 for (int c = 0; c < 32; ++c) x[c] = p.x0[xat(r, c1 + c)];
             }
         }
-        // the sum of the two accumulators
+        // the sum of the two accumulators; RETURNED: beside what the registers hold of the state
         auto read = [&]() {
-            float y[32];
             tc_fence_after();
-            tmem_ld32(xt, (uint32_t *)x);
-            tmem_ld32(xt + kCols, (uint32_t *)y);
-            tmem_ld_wait();
+            if constexpr (RETURNED) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) x[k] += y[k];
+                for (int q = 0; q < 32; q += 16) {
+                    float y[16], z[16];
+                    tmem_ld16(xt + q, (uint32_t *)y);
+                    tmem_ld16(xt + kCols + q, (uint32_t *)z);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) x[q + k] += y[k] + z[k];
+                }
+            } else {
+                float y[32];
+                tmem_ld32(xt, (uint32_t *)x);
+                tmem_ld32(xt + kCols, (uint32_t *)y);
+                tmem_ld_wait();
+#pragma unroll
+                for (int k = 0; k < 32; ++k) x[k] += y[k];
+            }
         };
         bool ok = true;
         for (int m = 0; m < nm; ++m) {
@@ -373,14 +407,16 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
                 if (!(ok = bar_all(2, 256, warp != 8 || wait(kXF, (m - 1) & 1)))) break;
                 read();
             }
-            const uint32_t none[32] = {};
-            tmem_st32(xt + kCols, none);
+            if constexpr (!RETURNED) {
+                const uint32_t none[32] = {};
+                tmem_st32(xt + kCols, none);
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                float y[16];
+                for (int q = 0; q < 2; ++q) {
+                    float y[16];
 #pragma unroll
-                for (int k = 0; k < 16; ++k) y[k] = down(x[16 * q + k]);
-                tmem_st16(xt + 16 * q, (const uint32_t *)y);
+                    for (int k = 0; k < 16; ++k) y[k] = down(x[16 * q + k]);
+                    tmem_st16(xt + 16 * q, (const uint32_t *)y);
+                }
             }
             if (!STATE) {
                 if (m > 0 && !(ok = bar_all(2, 256, warp != 8 || wait(kO1F, (m - 1) & 1)))) break;  // the last copy has been read
@@ -390,10 +426,14 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
                 }
                 fence_proxy_async();
             }
-            tmem_st_wait();
+            if constexpr (!RETURNED) tmem_st_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[kXB]);
+            if constexpr (RETURNED) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) x[k] = down(x[k]);
+            }
         }
         if (ok && (STATE || (p.x1 && last_seg)) && bar_all(2, 256, warp != 8 || wait(kXF, (nm - 1) & 1))) {
             read();
@@ -459,14 +499,14 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
             }
         }
     } else if (warp >= 20) {
-        // ---------------------------------------------------------------- C in two parts (thread = 32 columns of a row)
+        // ---------------------------------------------------------------- C in parts (thread = 32 columns of a row)
         const int j = tid & 127, i0 = warp >= 24 ? 4 : 0;
-        for (int m = 0; m < nm; ++m) {
+        for (int m = 0; m < nm; ++m, at_c.next(ring)) {
             const int rows = part.rows(part.chunk(m, rev));
             const float f = j < rows ? p.cs * decay_pow(g2, rev ? j : rows - 1 - j) : 0.f;
-            const uint8_t *const src = sm + G::kCs + m % kStagesC * kBox;
+            const uint8_t *const src = sm + G::kCs + at_c.s * kBox;
             uint8_t *const dst = sm + G::kParts;
-            if (!bar_all(4, 256, warp != 20 || loaded_c(m))) break;
+            if (!bar_all(4, 256, warp != 20 || loaded_c())) break;
             uint4 hi[4], lo[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -485,6 +525,18 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
             for (int i = 0; i < 4; ++i) {
                 *(uint4 *)(dst + sw128(j, 8 * (i0 + i))) = hi[i];
                 *(uint4 *)(dst + kBox + sw128(j, 8 * (i0 + i))) = lo[i];
+            }
+            if (third) {  // (what the two leave, from c again: it stays until the products have been issued)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint4 raw = *(const uint4 *)(src + sw128(j, 8 * (i0 + i)));
+                    const uint32_t *w = (const uint32_t *)&raw, *ph = (const uint32_t *)&hi[i], *pl = (const uint32_t *)&lo[i];
+                    uint32_t left[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        left[k] = pack_bf16(f * low_bf16(w[k]) - low_bf16(ph[k]) - low_bf16(pl[k]), f * high_bf16(w[k]) - high_bf16(ph[k]) - high_bf16(pl[k]));
+                    *(uint4 *)(sm + kThird + sw128(j, 8 * (i0 + i))) = make_uint4(left[0], left[1], left[2], left[3]);
+                }
             }
             fence_proxy_async();
             __syncwarp();
@@ -610,21 +662,25 @@ cudaError_t launch(const LinArgs &a, void *ws, int64_t tokens, cudaStream_t st)
     split.chosen = chosen;
     static std::atomic<uint64_t> seen;
     if (first_on_device(seen)) {
-        cudaError_t e = cudaFuncSetAttribute(lin_tc_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<D>::kSmem);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(lin_tc_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<D>::kSmem);
-        if (e != cudaSuccess) return e;
+        for (auto kern : {lin_tc_kernel<D, false, false>, lin_tc_kernel<D, true, false>, lin_tc_kernel<D, false, true>, lin_tc_kernel<D, true, true>}) {
+            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<D>::kSmem);
+            if (e != cudaSuccess) return e;
+        }
         done_on_device(seen);
     }
+    bool returned = false;
+    for (int i = 0; i < a.passes; ++i) returned = returned || a.pass[i].x1;
+    auto sums = returned ? lin_tc_kernel<D, true, true> : lin_tc_kernel<D, true, false>, walk = returned ? lin_tc_kernel<D, false, true> : lin_tc_kernel<D, false, false>;
     const int64_t each = (int64_t)a.HV * (D / kCols) * a.passes, joined = plan.places * a.HV * D * D / 1024;
     if (plan.slots * each > INT32_MAX || plan.states * each > INT32_MAX || joined > INT32_MAX) return cudaErrorInvalidConfiguration;
     const int withhold = withhold_loads();
     const uint64_t limit = withhold ? kTestWaitLimitNs : kWaitLimitNs;
     if (chosen) lin_choose_kernel<<<1, 512, 0, st>>>(a, plan.tokens, (float)each / (float)device_sm_count(), chosen);
     if (split.held) {
-        lin_tc_kernel<D, true><<<(unsigned)(plan.states * each), kThreads, Geo<D>::kSmem, st>>>(maps, a, split, limit, withhold);
+        sums<<<(unsigned)(plan.states * each), kThreads, Geo<D>::kSmem, st>>>(maps, a, split, limit, withhold);
         lin_join_kernel<D><<<dim3((unsigned)joined, a.passes), 256, 0, st>>>(a, split);
     }
-    lin_tc_kernel<D, false><<<(unsigned)(plan.slots * each), kThreads, Geo<D>::kSmem, st>>>(maps, a, split, limit, withhold);
+    walk<<<(unsigned)(plan.slots * each), kThreads, Geo<D>::kSmem, st>>>(maps, a, split, limit, withhold);
     return cudaGetLastError();
 }
 

@@ -25,7 +25,8 @@ def chunk_linear_attention(q, k, v, decay=None, scale=None, initial_state=None, 
     q, k [B, T, H, K]; v [B, T, HV, V] (float32 or bfloat16, same dtype, HV a multiple of H); decay [HV] float32, the natural
     logarithm of what a token leaves of the state (None: 0, nothing decays), a constant of the layer; scale defaults to
     ``K ** -0.5``; initial_state [N, HV, K, V] float32 or None; cu_seqlens [N + 1] for packed input (B == 1).  Returns
-    ``(o, final_state)``, the state float32 and None unless requested.  ``out`` and ``final_state`` overlap no input."""
+    ``(o, final_state)``, the state None unless requested, float32 and summed as such (for bfloat16 heads of 64 and 128 the call then
+    takes about a sixth longer).  ``out`` and ``final_state`` overlap no input."""
     return _m().linear_attn(q, k, v, decay, scale, initial_state, output_final_state, cu_seqlens, out, final_state, False)
 
 

@@ -579,7 +579,11 @@ typedef struct {
  *     S_0 = h0,  ht = S_T
  * in chunks of tokens: within a chunk the decayed products of q and k, between
  * chunks the state, in fp32.  On the tensor cores the decayed products and the
- * state are rounded to bf16 as operands of the output (not of the state).
+ * state are rounded to bf16 as operands of the output; what is added to the
+ * state (exp(decay (n - 1 - j)) v_j, k_j as it is) is split into bf16 parts: into
+ * three where ht is asked for, which is then good to fp32 (3e-7 of its 2-norm),
+ * into two (16 bits) where o alone takes the state.  So o may differ by its
+ * rounding between a call with ht and one without.
  * The decay is a constant of the layer: no gradient is computed for it.
  */
 size_t gdn_linear_attn_workspace_size(const gdn_linear_attn_args *a);
@@ -595,7 +599,8 @@ gdn_status gdn_linear_attn_recurrent(const gdn_linear_attn_args *a, gdn_stream_t
  *     dq_t = scale S_t dout_t,  dk_t = R_t v_t,  dv_t = R_t^T k_t,
  *     dh0 = exp(decay) R_1
  * (key heads that several value heads share: the sum of theirs, in fp32, in a
- * fixed order).
+ * fixed order).  On the tensor cores R is split as the state is, for dh0 into
+ * three parts.
  */
 size_t gdn_linear_attn_bwd_workspace_size(const gdn_linear_attn_args *a);
 gdn_status gdn_linear_attn_bwd(const gdn_linear_attn_args *a, void *workspace, size_t ws_bytes, gdn_stream_t stream);

@@ -170,6 +170,21 @@ def test_linear_long(gdn):
             ref.check_norm(a, b.double(), 2e-5 if name == "dh0" else 2.0 ** -8, name)
 
 
+@pytest.mark.parametrize("case", [(2, 4096, 2, 2, 128, 128), (1, 5000, 1, 2, 64, 64), (1, [700, 0, 3000, 129], 2, 2, 128, 128), (4, 127, 1, 1, 128, 128)], ids=str)
+@pytest.mark.parametrize("slow", [False, True])
+def test_linear_state_is_fp32(gdn, case, slow):
+    """Final states and the initial state's gradient are returned in fp32 and are as good from bf16 inputs on the tensor cores: their 2-norm is off by
+    what fp32 products may be (4e-7) and two units of the decays' exponentials (2^-22)."""
+    q, k, v, decay, h0, cu, g = linear_inputs(case, BF, True, 9)
+    if slow:
+        decay = -torch.linspace(1e-5, 1e-3, v.shape[2], device="cuda")
+    _, ht = gdn.chunk_linear_attention(q, k, v, decay, initial_state=h0, output_final_state=True, cu_seqlens=cu)
+    do, dht = randn(g, *v.shape, dtype=BF), randn(g, *h0.shape)
+    dh0 = gdn.chunk_linear_attention_bwd(q, k, v, decay, do, None, h0, dht, cu)[3]
+    ref.check_norm(ht, ref.linear(q, k, v, decay, q.shape[3] ** -0.5, h0, cu)[1], 4e-7 + 2.0 ** -22, "state")
+    ref.check_norm(dh0, ref.linear_bwd(q, k, v, decay, do, q.shape[3] ** -0.5, h0, dht, cu)[0][3], 4e-7 + 2.0 ** -22, "dh0")
+
+
 @pytest.mark.parametrize("T", [1, 3])
 def test_linear_state_in_place(gdn, T):
     q, k, v, decay, h0, _, _ = linear_inputs((3, T, 2, 4, 128, 128), BF, True, 6)
@@ -389,6 +404,25 @@ def test_window_step_strided(gdn, dtype):
                  (randn(g, N, S, HK, D + 3, dtype=dtype)[..., 3:], randn(g, N, S, HK, D + 1, dtype=dtype)[..., 1:])):
         eo, bo = ref.window_step(q, k, v, [S, 0], 60, 2, 0.1)
         ref.check(gdn.window_attention_decode(q, k, v, lens, 60, 2, 0.1), eo, bo)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_window_step_in_turn(gdn, dtype):
+    """A cache of window + sinks slots whose window is overwritten in turn, called with a window of all slots: as over all tokens."""
+    g = gen(33)
+    N, T, H, HK, D, w, sinks = 2, 75, 4, 2, 64, 24, 3
+    q, k, v = randn(g, N, T, H, D, dtype=dtype), randn(g, N, T, HK, D, dtype=dtype), randn(g, N, T, HK, D, dtype=dtype)
+    eo, _, bo, _ = ref.window(q, k, v, w, sinks, D ** -0.5)
+    kept = [torch.full((N, w + sinks, HK, D), torch.nan, device="cuda", dtype=dtype) for _ in range(2)]
+    for t in range(T):
+        at = t if t < w + sinks else sinks + (t - sinks) % w
+        kept[0][:, at], kept[1][:, at] = k[:, t], v[:, t]
+        lens = torch.full((N,), min(t + 1, w + sinks), dtype=torch.int32, device="cuda")
+        if t < w + sinks:  # (until it is full slots are positions)
+            got = gdn.window_attention_decode(q[:, t:t + 1], *kept, lens, w, sinks)
+        else:
+            got = gdn.window_attention_decode(q[:, t:t + 1], *kept, lens, w + sinks)
+        ref.check(got, eo[:, t:t + 1], bo[:, t:t + 1], t)
 
 
 # ---------------------------------------------------------------- together
