@@ -5,7 +5,8 @@
 //   P_ij = cs l^|i-j| (a_i . b_j),  out = os (P c + diag(l^(i+1)) a X),  X <- l^n X + b^T diag(cs l^(n-1-j)) c
 // (against time the powers count from the chunk's other end).  16 x 16 threads hold 2 x 2 outputs each and read operands 16 bytes
 // at a time along the contraction.  Bound by a chunk's chain (loads, three products, 8 to 12 us) where CTAs are few, for which sequences are
-// cut into segments (lin_simt_plan), else by reads of shared memory: 4 x 4096 tokens of 16 heads of 128 in fp32 2.2 ms, 15 TFLOP/s.
+// cut into segments (lin_simt_plan), else by reads of shared memory: 4 x 4096 tokens of 16 heads of 128 in fp32 2.2 ms, 7.8 TFLOP/s by the
+// operator's 4 K V a token and head, 12.7 by what is done here (every 32 columns take a chunk's P again).
 #include "gdn_mix.cuh"
 
 namespace gdn {

@@ -1,12 +1,13 @@
 // Linear attention with a decay for each head, token by token (decoding, short continuations):
 //   S <- l S + k_t v_t^T,  o_t = scale S^T q_t
 //
-// Bound by the state's traffic, 8 K V bytes per (sequence, value head) for a token or a few.  One CTA of 256 threads holds
+// It has the state's traffic, 8 K V bytes per (sequence, value head), for a token or a few.  One CTA of 256 threads holds
 // 64 columns of the state in registers for all tokens of its sequence: thread (row group y, column quad x) has rows y + 16 i and
 // four columns, so that a row is read as 256 consecutive bytes and all of a thread's loads (8 of 16 bytes at K = 128) are in
 // flight together.  Per token the read-out is a sum over the thread's rows, a shuffle between the warp's two row groups and a sum
 // over eight warps in shared memory.  ht may be h0 itself: every element is read and written by the same thread.
-// 64 sequences, 16 heads of 128 x 128: 27.8 us, 4.9 TB/s; one sequence of 8 heads 5.5.
+// 64 sequences, 16 heads of 128 x 128: 27.7 us, 4.9 TB/s, of which DRAM sees two thirds in the launch and is 46 % busy: bound by three CTAs an
+// SM (74 registers) that load, compute and store with nothing to cover one's stores by the next one's loads.  One sequence of 8 heads: 5.7.
 #include "gdn_mix.cuh"
 
 namespace gdn {

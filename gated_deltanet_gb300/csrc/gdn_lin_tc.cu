@@ -11,7 +11,7 @@
 //    zero in each chunk, because the tensor cores cut off what a small product has below a large sum, chunk after chunk.  X is then off by 1e-7
 //    to 3e-7 of its 2-norm, as plain fp32 sums are.
 //  - Where only outputs in bf16 (or the fp32 parts of bf16 gradients) see X, C goes in as hi + lo, 16 bits of it, and X is the accumulators' sum, which
-//    leaves X 2.4e-6 of its 2-norm off, 2^-10 of the rounding with which it enters O1.
+//    leaves X 2.4e-6 of its 2-norm off, a 700th of the rounding with which it enters O1.
 //
 // Bound by shared memory: it gives the products about 80 bytes a cycle, so that one of 128 x 128 x 16 with both operands there takes
 // 104 cycles (64 for the arithmetic), 128 x 64 x 16 takes 76, with its left operand in tensor memory 46, and it serves the copies and

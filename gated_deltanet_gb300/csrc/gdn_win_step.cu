@@ -7,9 +7,10 @@
 //   step_mma_kernel   bf16 heads of 64 and 128 on 16-byte boundaries, R = 16: each of four warps walks its own tiles of 16 keys, which
 //                     arrive by cp.async (16 bytes a lane) some tiles ahead, S = Q K^T and O += P V by mma.sync (a tile of 128 queries
 //                     for tcgen05 would be mostly empty; the keys' bytes bound the call all the same)
-//   step_any_kernel   everything else, R = 8: tiles of 32 keys through shared memory, fp32 on the CUDA cores, which bound it
-// 64 sequences, window 4096, 16 heads over 4: bf16 heads of 128 103 us, 5.2 TB/s; of 96 440; fp32 of 128 615 (read element by element 830, 876).
-// One sequence, window 1024: 9.8 us, launch and latency.
+//   step_any_kernel   everything else, R = 8: tiles of 32 keys through shared memory, fp32 on the CUDA cores.  Bound by a tile's chain (loads,
+//                     barrier, products, barrier; no tile is loaded ahead): the arithmetic of fp32 heads of 128 below is 30 us of 593
+// 64 sequences, window 4096, 16 heads over 4: bf16 heads of 128 103 us, 5.2 TB/s; of 64 79; of 96 443; fp32 of 128 593 (read element by element
+// 830, 876).  One sequence, window 1024: 10.2 us, launch and latency.
 #include "gdn_mix.cuh"
 #include "gdn_ptx.cuh"
 

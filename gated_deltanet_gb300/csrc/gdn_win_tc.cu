@@ -6,15 +6,15 @@
 //   S = Q K^T,  P = exp2(c S - m) (bf16, in S's place),  O += P V            c = scale log2 e
 // in one pass over the keys.  m is a row's maximum as it was last raised: O and the sum are brought to a new one only when a score
 // passes the old by more than 8 (P then stays below 2^8, in fp32's and bf16's range; the rounding of P is relative), so that most
-// tiles leave O alone.
+// tiles leave O alone (the one-pass softmax of Milakov and Gimelshein, 2018, in the later published form that puts small raises off).
 //
 // Warps: 0-7 and 8-15 softmax of A and B and their outputs (two threads to a row: with one a tile's softmax took 3800 cycles, one warp to
 // a scheduler and side having nothing to hide its latencies behind), 16 loads (a ring of K and V tiles) and zeroes the V rows behind a
 // sequence's end (they are the next sequence's, and 0 x NaN is NaN), 17 products.
 // The products are issued S_A(t), PV_B(t-1), S_B(t), PV_A(t): S(t) is complete only when PV(t-1) is, which is why a softmax that sees
 // its scores may also touch its O.
-// 4 x 4096 tokens, 16 heads over 4 of 128, window 1024: 145 us, 830 TFLOP/s.  S with both operands in shared memory takes 104 cycles a product
-// where the arithmetic takes 64, which with P V (67 of 64), the copies and a CTA's start and end is what bounds it.
+// 4 x 4096 tokens, 16 heads over 4 of 128, window 1024: 146 us, 822 TFLOP/s; of 64 138.  S with both operands in shared memory takes 104 cycles a
+// product where the arithmetic takes 64, with P V (67 of 64) 84 us of the 146; the rest are a CTA's start and end and the softmax between its nine tiles.
 #include "gdn_mix.cuh"
 #include "gdn_ptx.cuh"
 

@@ -6,7 +6,9 @@ Layouts are the delta rule's: CUDA tensors [B, T, heads, size] in float32 or bfl
 ``cu_seqlens`` (int64, on the device) for packed input.  The work runs on the current stream and gradients are explicit calls.
 Slices of a fused projection (consecutive heads, any distance between tokens) are taken as they are, other strides are made
 contiguous first.  Outputs and temporary buffers come from PyTorch's allocator, so the calls can be captured into a CUDA graph.
-bfloat16 heads of 64 and 128 run on the tensor cores, everything else (to 256) on the CUDA cores.
+bfloat16 heads of 64 and 128 run on the tensor cores, everything else (to 256) on the CUDA cores.  Inputs are finite: a NaN or an
+infinity reaches, besides what depends on it, other tokens of its sequence nearby (hidden behind a mask it does too), but no other
+sequence.  Outputs of packed input hold nothing where no sequence has tokens.
 """
 from __future__ import annotations
 
@@ -59,7 +61,9 @@ def window_attention(q, k, v, window, sinks=0, scale=None, cu_seqlens=None, cu_s
 def window_attention_decode(q, k_cache, v_cache, lengths, window, sinks=0, scale=None, *, out=None):
     """:func:`window_attention` of a few new tokens over a cache: q [B, T, H, D] (T = 1 when decoding), k_cache and v_cache
     [B, S, HK, D] at any strides between slots, heads and sequences, lengths [B] (int32 or int64, on the device): the slots filled,
-    the T new tokens' among them.  Slots from lengths on and those that no new token sees are not read."""
+    the T new tokens' among them.  Slots from lengths on and those that no new token sees are not read.  Slots are positions; a cache of
+    ``window + sinks`` slots whose window is overwritten in turn serves single tokens once it is full, with a window of all its slots
+    (the softmax does not depend on their order)."""
     return _m().window_attn_decode(q, k_cache, v_cache, lengths, window, sinks, scale, out)
 
 
